@@ -409,6 +409,137 @@ int kda_debug_checks(void);
 /* A static, human-readable name for a status code (never NULL). */
 const char *kda_status_string(kda_status_t status);
 
+/* ------------------------------------------------------------------------------------------
+ * The other layers of a stack that serves KDA: linear attention with a decay for each head, and
+ * softmax attention over a paged key-value cache.  The pages interleave KDA layers with full
+ * attention and keep both kinds of state under one paged manager ("はじめての自然言語処理 --
+ * Kimi K3", the infrastructure paragraph on inference); these calls follow the conventions at the
+ * top of this file, with dimension structs of their own.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Dimensions of the linear-attention calls.  batch, seqlen, num_seqs, heads, dk, dv and dtype as
+ * in kda_dims_t; q and k have qk_heads heads, a divisor of `heads`: head h reads q and k of head
+ * h / (heads / qk_heads). */
+typedef struct {
+    int32_t batch;
+    int32_t seqlen;
+    int32_t num_seqs;
+    int32_t heads;
+    int32_t qk_heads;
+    int32_t dk;
+    int32_t dv;
+    kda_dtype_t dtype;
+} kda_lin_dims_t;
+
+/* kda_lin_chunk_fwd -- linear attention with a decay for each head, chunkwise, for prompts and
+ * for resuming from a cached state.
+ *
+ * Operation: for every sequence n and head h, from initial_state[n,h] (zeros when NULL),
+ *   S_t = exp(g_t + head_g) S_{t-1} + k_t v_t^T,     o_t = S_t^T q_t,
+ * writing o_t to `out` and the state after the last token to final_state[n,h] (skipped when NULL).
+ * No scale is applied to q.
+ *   q, k     : [batch, seqlen, qk_heads, dk]  dtype
+ *   v, out   : [batch, seqlen, heads, dv]     dtype (out is written)
+ *   g        : fp32 [batch, seqlen, heads] log decay of each token, or NULL (zeros)
+ *   head_g   : fp32 [heads] log decay of each head, or NULL (zeros); both may be given
+ *              The log decays are <= 0, of any magnitude; -infinity forgets everything before
+ *              the token.  (A positive sum g + head_g is outside the precondition.)
+ *   initial_state, final_state : fp32 [num_seqs, heads, dk, dv]; the same pointer is allowed,
+ *              partial overlap is not.
+ *   cu_seqlens : as in kda_chunk_fwd (NULL for dense batches; clamped on the device).
+ *   workspace  : device memory of kda_lin_chunk_fwd_workspace_bytes(dims) bytes, 16-byte aligned
+ *              (NULL when that is 0).  Its contents on entry do not matter; calls that overlap in
+ *              time need workspaces of their own.  It holds the states of the parts that a
+ *              sequence is cut into when there are fewer (sequence, head) pairs than SMs.
+ * v and the states may take any magnitude their formats hold.  Tokens of other sequences (and
+ * what lies behind the last) never reach a sequence's results, NaN and infinities included; a
+ * NaN or infinity of a sequence's own token may reach its outputs from the start of that token's
+ * chunk (at most 64 tokens, counted from the sequence's start) on, and its state.
+ * Returns KDA_OK or an error found on the host before any launch: KDA_ERR_NULL, KDA_ERR_SHAPE,
+ * KDA_ERR_UNSUPPORTED, KDA_ERR_ALIGN, KDA_ERR_WORKSPACE.  seqlen = 0 is valid (final_state becomes
+ * a copy of the initial state, or zeros). */
+kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const void *v,
+                               const float *g, const float *head_g,
+                               const float *initial_state, const int32_t *cu_seqlens,
+                               void *out, float *final_state,
+                               void *workspace, size_t workspace_bytes,
+                               const kda_lin_dims_t *dims, cudaStream_t stream);
+
+/* Bytes of workspace kda_lin_chunk_fwd needs for `dims` (0: none; host arithmetic only). */
+size_t kda_lin_chunk_fwd_workspace_bytes(const kda_lin_dims_t *dims);
+
+/* kda_lin_recurrent_step -- one decode token per row of the same operation, state in place.
+ *   q, k    : [N, qk_heads, dk] dtype;  v, out : [N, heads, dv] dtype
+ *   g       : fp32 [N, heads] or NULL;  head_g : fp32 [heads] or NULL
+ *   state   : fp32 [num_seqs, heads, dk, dv], read and written in place
+ *   state_indices : as in kda_recurrent_step (rows with a slot outside the pool are skipped; two
+ *             rows must not name the same slot)
+ * dims: batch = N rows (0 is valid), seqlen = 1, num_seqs = pool slots.  Errors as in
+ * kda_recurrent_step. */
+kda_status_t kda_lin_recurrent_step(const void *q, const void *k, const void *v,
+                                    const float *g, const float *head_g, float *state,
+                                    const int32_t *state_indices, void *out,
+                                    const kda_lin_dims_t *dims, cudaStream_t stream);
+
+/* Dimensions of the paged-cache calls.
+ *   rows       : sequences N
+ *   heads      : query heads, a multiple of kv_heads: query head h reads key/value head
+ *                h / (heads / kv_heads)  (ignored by kda_paged_append)
+ *   head_dim   : 64 or 128
+ *   pages, page_size : the pool: K and V caches are [pages, page_size, kv_heads, head_dim]
+ *   max_pages  : width of the block table */
+typedef struct {
+    int32_t rows;
+    int32_t heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t pages;
+    int32_t page_size;
+    int32_t max_pages;
+    kda_dtype_t dtype;
+} kda_paged_dims_t;
+
+/* kda_paged_append -- writes new tokens' keys and values into a paged cache.
+ *
+ * Token u of row n (u = 0, 1, ...) goes to position p = positions[n] + u of that row: to offset
+ * p % page_size of page block_table[n, p / page_size].
+ *   k, v        : [tokens, kv_heads, head_dim] dtype
+ *   k_cache, v_cache : [pages, page_size, kv_heads, head_dim] dtype, written in place
+ *   block_table : int32 [rows, max_pages]
+ *   positions   : int32 [rows], the position of each row's first new token
+ *   cu_seqlens  : int32 [rows + 1], row n's tokens are [cu[n], cu[n+1]) (clamped on the device to
+ *                 [0, tokens]), or NULL: one token per row (then tokens = rows)
+ * Tokens at a position outside [0, max_pages * page_size), or whose page is outside the pool, are
+ * skipped.  Two tokens must not name the same place.  Errors as in the other calls. */
+kda_status_t kda_paged_append(const void *k, const void *v, void *k_cache, void *v_cache,
+                              const int32_t *block_table, const int32_t *positions,
+                              const int32_t *cu_seqlens, int64_t tokens,
+                              const kda_paged_dims_t *dims, cudaStream_t stream);
+
+/* kda_paged_attention -- softmax attention of one new token per row over its cached tokens.
+ *
+ * Per row n and query head h, with len = seq_lens[n] clamped to [0, max_pages * page_size]:
+ *   s_t = scale * q . K_t (t < len),  out = sum_t e^(s_t - m) V_t / sum_t e^(s_t - m),
+ *   lse = m + ln sum_t e^(s_t - m),   m = max_t s_t.
+ * A row without tokens gets out = 0 and lse = -infinity.  Cached tokens whose page lies outside
+ * the pool are left out of the sums.  What the cache holds at or past a row's length never
+ * reaches its results, NaN and infinities included.
+ *   q, out      : [rows, heads, head_dim] dtype (out is written)
+ *   seq_lens    : int32 [rows];  block_table : int32 [rows, max_pages]
+ *   scale       : finite, else KDA_ERR_SHAPE
+ *   lse         : fp32 [rows, heads], or NULL
+ *   workspace   : device memory of kda_paged_attention_workspace_bytes(dims) bytes, 16-byte
+ *                 aligned (NULL when that is 0), contents on entry of no matter; one per
+ *                 call in flight.  It holds the parts of rows that are split over their length.
+ * Results do not depend on timing (parts are joined in the order of the tokens). */
+kda_status_t kda_paged_attention(const void *q, const void *k_cache, const void *v_cache,
+                                 const int32_t *block_table, const int32_t *seq_lens, float scale,
+                                 void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                 const kda_paged_dims_t *dims, cudaStream_t stream);
+
+/* Bytes of workspace kda_paged_attention needs for `dims` (host arithmetic only). */
+size_t kda_paged_attention_workspace_bytes(const kda_paged_dims_t *dims);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,83 @@
+// Internal declarations of the linear-attention and paged-cache calls.
+#pragma once
+
+#include "kda_internal.h"
+
+namespace kda {
+
+// SMs of the GPU this library is written for: how far work is split is chosen against it, on the
+// host, without asking the device (so that workspace sizes are plain arithmetic).
+constexpr int kSms = 152;
+
+// Log decays are taken in log2 units from here up: a decay of 2^-1e5 is zero in every format, and
+// sums of 64 of them stay exact in the two-float form the kernels use.
+constexpr double kMinLog2Decay = -1e5;
+
+struct LinArgs {
+    const void *q, *k, *v;
+    const float *g;           // [tokens, H] or nullptr
+    const float *head_g;      // [H] or nullptr
+    const float *s0;          // [N, H, dk, dv] or nullptr
+    const int32_t *cu;        // [N + 1] or nullptr (dense)
+    void *out;
+    float *sT;                // [N, H, dk, dv] or nullptr
+    int64_t seqlen;           // tokens per dense row, or total packed tokens
+    int32_t num_seqs, heads, qk_heads, dk, dv;
+};
+
+struct LinStepArgs {
+    const void *q, *k, *v;
+    const float *g, *head_g;
+    float *state;
+    const int32_t *idx;
+    void *out;
+    int32_t rows, slots, heads, qk_heads;
+};
+
+// Token range of sequence n, clamped so that malformed offsets never index outside the tensors.
+__device__ __forceinline__ void lin_range(const LinArgs &a, int n, int64_t &bos, int64_t &eos) {
+    if (a.cu == nullptr) {
+        bos = (int64_t)n * a.seqlen;
+        eos = bos + a.seqlen;
+    } else {
+        int64_t b = __ldg(a.cu + n), e = __ldg(a.cu + n + 1);
+        b = b < 0 ? 0 : (b > a.seqlen ? a.seqlen : b);
+        e = e < b ? b : (e > a.seqlen ? a.seqlen : e);
+        bos = b;
+        eos = e;
+    }
+}
+
+// A token's log decay in log2 units, fp64 (NaN passes through).
+__device__ __forceinline__ double lin_log2_decay(const LinArgs &a, int64_t tok, int h) {
+    double x = 0.0;
+    if (a.g) x += (double)a.g[tok * a.heads + h];
+    if (a.head_g) x += (double)__ldg(a.head_g + h);
+    x *= 1.4426950408889634074;
+    return x < kMinLog2Decay ? kMinLog2Decay : x;
+}
+
+struct PagedArgs {
+    const void *q, *k_cache, *v_cache;
+    const int32_t *table, *lens;
+    void *out;
+    float *lse;
+    float scale;
+    int32_t rows, heads, kv_heads, pages, page_size, max_pages;
+};
+
+struct AppendArgs {
+    const void *k, *v;
+    void *k_cache, *v_cache;
+    const int32_t *table, *positions, *cu;
+    int64_t tokens;
+    int32_t rows, pages, page_size, max_pages;
+    int32_t row_vecs;         // 16-byte vectors of one token's keys (kv_heads * head_dim * size / 16)
+};
+
+cudaError_t launch_lin_chunk_simt(const LinArgs &a, kda_dtype_t dt, cudaStream_t st);
+cudaError_t launch_lin_step(const LinStepArgs &a, int dk, int dv, kda_dtype_t dt, cudaStream_t st);
+cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st);
+cudaError_t launch_paged_attention(const PagedArgs &a, int d, kda_dtype_t dt, void *workspace, cudaStream_t st);
+
+}  // namespace kda

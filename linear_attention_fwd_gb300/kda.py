@@ -29,13 +29,29 @@ EXPORTED = ("kda_chunk_fwd", "kda_chunk_fwd_with", "kda_chunk_fwd_bounded", "kda
             "kda_recurrent_steps", "kda_device_status", "kda_chunk_fwd_ws",
             "kda_chunk_fwd_workspace_bytes", "kda_chunk_fwd_noalloc", "kda_debug_checks",
             "kda_chunk_fwd_qknorm", "kda_recurrent_step_qknorm", "kda_recurrent_steps_qknorm",
-            "kda_status_string")
+            "kda_status_string",
+            "kda_lin_chunk_fwd", "kda_lin_chunk_fwd_workspace_bytes", "kda_lin_recurrent_step",
+            "kda_paged_append", "kda_paged_attention", "kda_paged_attention_workspace_bytes")
 
 
 class KdaDims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32),
                 ("num_seqs", ctypes.c_int32), ("heads", ctypes.c_int32),
                 ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class KdaLinDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32),
+                ("num_seqs", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("qk_heads", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class KdaPagedDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 class KdaError(RuntimeError):
@@ -92,6 +108,19 @@ def lib() -> ctypes.CDLL:
         L.kda_device_status.argtypes = [vp]
         L.kda_debug_checks.restype = ctypes.c_int
         L.kda_debug_checks.argtypes = []
+        lp, pp = ctypes.POINTER(KdaLinDims), ctypes.POINTER(KdaPagedDims)
+        L.kda_lin_chunk_fwd.restype = ctypes.c_int
+        L.kda_lin_chunk_fwd.argtypes = [vp] * 10 + [ctypes.c_size_t, lp, vp]
+        L.kda_lin_chunk_fwd_workspace_bytes.restype = ctypes.c_size_t
+        L.kda_lin_chunk_fwd_workspace_bytes.argtypes = [lp]
+        L.kda_lin_recurrent_step.restype = ctypes.c_int
+        L.kda_lin_recurrent_step.argtypes = [vp] * 8 + [lp, vp]
+        L.kda_paged_append.restype = ctypes.c_int
+        L.kda_paged_append.argtypes = [vp] * 7 + [ctypes.c_int64, pp, vp]
+        L.kda_paged_attention.restype = ctypes.c_int
+        L.kda_paged_attention.argtypes = [vp] * 5 + [ctypes.c_float] + [vp] * 3 + [ctypes.c_size_t, pp, vp]
+        L.kda_paged_attention_workspace_bytes.restype = ctypes.c_size_t
+        L.kda_paged_attention_workspace_bytes.argtypes = [pp]
         L.kda_status_string.restype = ctypes.c_char_p
         L.kda_status_string.argtypes = [ctypes.c_int]
         _lib = L
@@ -453,3 +482,230 @@ def kda_chunk_fwd_gated(q, k, v, g, beta, gate, norm_weight=None, eps: float = 1
     if st != KDA_OK:
         raise KdaError(st, "kda_chunk_fwd_gated")
     return out, final_state
+
+
+# ---------------------------------------------------------------------------------------------
+# Linear attention with a decay for each head, and attention over a paged key-value cache.
+
+
+def _need(name, t, dev, dtype, shape):
+    """One required tensor: its device, type, layout and shape."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _on_current_device(dev):
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device, got {dev}")
+
+
+def _allocate(stream, *want):
+    """New tensors (shape, dtype, device), made for use on `stream`: memory that the allocator hands
+    out for another stream may still be in use there."""
+    if stream is None:
+        return [torch.empty(s, dtype=t, device=d) for s, t, d in want]
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return [torch.empty(s, dtype=t, device=d) for s, t, d in want]
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def kda_lin_chunk_fwd_workspace_bytes(q, v, cu_seqlens=None) -> int:
+    """Bytes of device workspace kda_lin_chunk_fwd needs for these shapes."""
+    B, T, H, dv = v.shape
+    n = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    dims = KdaLinDims(B, T, n, H, q.shape[2], q.shape[3], dv, _dtype_code(q.dtype))
+    return int(lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(dims)))
+
+
+def kda_lin_chunk_fwd(q, k, v, g=None, head_g=None, initial_state=None, cu_seqlens=None, *, out=None,
+                      final_state=None, output_final_state: bool = True, workspace=None, stream=None):
+    """Linear attention with a decay for each head, chunkwise (prompts, resume):
+    S_t = exp(g_t + head_g) S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.
+
+    q, k: [B, T, Hk, dk]; v: [B, T, H, dv] with Hk a divisor of H (all fp32 or all bf16); g: fp32
+    [B, T, H] log decay of each token or None; head_g: fp32 [H] log decay of each head or None;
+    initial_state: fp32 [N, H, dk, dv] or None; cu_seqlens: int32 [N+1] (packed, B == 1) or None.
+    workspace: uint8 tensor of kda_lin_chunk_fwd_workspace_bytes bytes (allocated here when None).
+    Returns (out [B, T, H, dv], final_state fp32 [N, H, dk, dv] or None).
+    """
+    dev, dt = q.device, q.dtype
+    _on_current_device(dev)
+    code = _dtype_code(dt)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [B, T, Hk, dk] and v [B, T, H, dv]")
+    B, T, Hk, dk = q.shape
+    H, dv = v.shape[2:]
+    _need("q", q, dev, dt, q.shape)
+    _need("k", k, dev, dt, q.shape)
+    _need("v", v, dev, dt, (B, T, H, dv))
+    if g is not None:
+        _need("g", g, dev, torch.float32, (B, T, H))
+    if head_g is not None:
+        _need("head_g", head_g, dev, torch.float32, (H,))
+    N = B
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
+        N = cu_seqlens.numel() - 1
+        _need("cu_seqlens", cu_seqlens, dev, torch.int32, (N + 1,))
+    if initial_state is not None:
+        _need("initial_state", initial_state, dev, torch.float32, (N, H, dk, dv))
+    dims = KdaLinDims(B, T, N, H, Hk, dk, dv, code)
+    if out is None:
+        out, = _allocate(stream, ((B, T, H, dv), dt, dev))
+    else:
+        _need("out", out, dev, dt, (B, T, H, dv))
+    if final_state is not None:
+        _need("final_state", final_state, dev, torch.float32, (N, H, dk, dv))
+    elif output_final_state:
+        final_state, = _allocate(stream, ((N, H, dk, dv), torch.float32, dev))
+    L = lib()
+    dp = ctypes.byref(dims)
+    if workspace is None:
+        bytes_ = L.kda_lin_chunk_fwd_workspace_bytes(dp)
+        if bytes_:
+            workspace, = _allocate(stream, ((bytes_,), torch.uint8, dev))
+    else:
+        _need("workspace", workspace, dev, torch.uint8, workspace.shape)
+    st = L.kda_lin_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(g), _addr(head_g),
+                             _addr(initial_state), _addr(cu_seqlens), out.data_ptr(),
+                             _addr(final_state), _addr(workspace),
+                             0 if workspace is None else workspace.numel(), dp, _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_lin_chunk_fwd")
+    return out, final_state
+
+
+def kda_lin_recurrent_step(q, k, v, g, head_g, state, state_indices=None, *, out=None, stream=None):
+    """One token per row of the same operation; ``state`` is updated in place.
+
+    q, k: [N, Hk, dk]; v: [N, H, dv]; g: fp32 [N, H] or None; head_g: fp32 [H] or None; state: fp32
+    [P, H, dk, dv]; state_indices: int32 [N] (rows outside the pool are skipped: their outputs are
+    not written) or None.  Returns out [N, H, dv].
+    """
+    dev, dt = q.device, q.dtype
+    _on_current_device(dev)
+    code = _dtype_code(dt)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q must be [N, Hk, dk] and v [N, H, dv]")
+    N, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    _need("q", q, dev, dt, q.shape)
+    _need("k", k, dev, dt, q.shape)
+    _need("v", v, dev, dt, (N, H, dv))
+    if g is not None:
+        _need("g", g, dev, torch.float32, (N, H))
+    if head_g is not None:
+        _need("head_g", head_g, dev, torch.float32, (H,))
+    _need("state", state, dev, torch.float32, (state.shape[0], H, dk, dv))
+    if state_indices is not None:
+        _need("state_indices", state_indices, dev, torch.int32, (N,))
+    dims = KdaLinDims(N, 1, state.shape[0], H, Hk, dk, dv, code)
+    if out is None:
+        out, = _allocate(stream, ((N, H, dv), dt, dev))
+    else:
+        _need("out", out, dev, dt, (N, H, dv))
+    st = lib().kda_lin_recurrent_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(g), _addr(head_g),
+                                      state.data_ptr(), _addr(state_indices), out.data_ptr(),
+                                      ctypes.byref(dims), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_lin_recurrent_step")
+    return out
+
+
+def _paged_dims(rows, heads, k_cache, v_cache, block_table, dev, dt):
+    if k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("caches must be [pages, page_size, Hkv, d] and block_table [N, max_pages]")
+    pages, page_size, Hkv, d = k_cache.shape
+    _need("k_cache", k_cache, dev, dt, k_cache.shape)
+    _need("v_cache", v_cache, dev, dt, k_cache.shape)
+    _need("block_table", block_table, dev, torch.int32, (rows, block_table.shape[1]))
+    return KdaPagedDims(rows, heads, Hkv, d, pages, page_size, block_table.shape[1], _dtype_code(dt))
+
+
+def kda_paged_append(k, v, k_cache, v_cache, block_table, positions, cu_seqlens=None, *, stream=None):
+    """Write new tokens' keys and values into a paged cache, in place.
+
+    k, v: [tokens, Hkv, d]; k_cache, v_cache: [pages, page_size, Hkv, d]; block_table: int32
+    [N, max_pages]; positions: int32 [N], where each row's first new token goes; cu_seqlens: int32
+    [N+1] (row n's tokens are cu[n] .. cu[n+1]) or None (one token per row).  Tokens at a position
+    past the table or on a page outside the pool are skipped.
+    """
+    dev, dt = k.device, k.dtype
+    _on_current_device(dev)
+    _dtype_code(dt)
+    N = positions.numel()
+    dims = _paged_dims(N, 1, k_cache, v_cache, block_table, dev, dt)
+    tokens = k.shape[0]
+    _need("k", k, dev, dt, (tokens, dims.kv_heads, dims.head_dim))
+    _need("v", v, dev, dt, (tokens, dims.kv_heads, dims.head_dim))
+    _need("positions", positions, dev, torch.int32, (N,))
+    if cu_seqlens is not None:
+        _need("cu_seqlens", cu_seqlens, dev, torch.int32, (N + 1,))
+    st = lib().kda_paged_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                block_table.data_ptr(), positions.data_ptr(), _addr(cu_seqlens), tokens,
+                                ctypes.byref(dims), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_paged_append")
+
+
+def kda_paged_attention_workspace_bytes(q, k_cache, block_table) -> int:
+    """Bytes of device workspace kda_paged_attention needs for these shapes."""
+    pages, page_size, Hkv, d = k_cache.shape
+    dims = KdaPagedDims(q.shape[0], q.shape[1], Hkv, d, pages, page_size, block_table.shape[1],
+                        _dtype_code(q.dtype))
+    return int(lib().kda_paged_attention_workspace_bytes(ctypes.byref(dims)))
+
+
+def kda_paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, *, out=None, lse=None,
+                        output_lse: bool = True, workspace=None, stream=None):
+    """Softmax attention of one new token per row over its cached tokens.
+
+    q: [N, Hq, d]; k_cache, v_cache: [pages, page_size, Hkv, d] with Hkv a divisor of Hq;
+    block_table: int32 [N, max_pages]; seq_lens: int32 [N]; scale: multiplies q . k.
+    workspace: uint8 tensor of kda_paged_attention_workspace_bytes bytes (allocated here when None).
+    Returns (out [N, Hq, d], lse fp32 [N, Hq] or None); a row without tokens gets 0 and -infinity.
+    """
+    dev, dt = q.device, q.dtype
+    _on_current_device(dev)
+    _dtype_code(dt)
+    if q.dim() != 3:
+        raise ValueError("q must be [N, Hq, d]")
+    N, Hq, d = q.shape
+    dims = _paged_dims(N, Hq, k_cache, v_cache, block_table, dev, dt)
+    _need("q", q, dev, dt, (N, Hq, dims.head_dim))
+    _need("seq_lens", seq_lens, dev, torch.int32, (N,))
+    if out is None:
+        out, = _allocate(stream, ((N, Hq, d), dt, dev))
+    else:
+        _need("out", out, dev, dt, (N, Hq, d))
+    if lse is not None:
+        _need("lse", lse, dev, torch.float32, (N, Hq))
+    elif output_lse:
+        lse, = _allocate(stream, ((N, Hq), torch.float32, dev))
+    L = lib()
+    dp = ctypes.byref(dims)
+    if workspace is None:
+        bytes_ = L.kda_paged_attention_workspace_bytes(dp)
+        if bytes_:
+            workspace, = _allocate(stream, ((bytes_,), torch.uint8, dev))
+    else:
+        _need("workspace", workspace, dev, torch.uint8, workspace.shape)
+    st = L.kda_paged_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                               block_table.data_ptr(), seq_lens.data_ptr(), scale, out.data_ptr(),
+                               _addr(lse), _addr(workspace),
+                               0 if workspace is None else workspace.numel(), dp, _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_paged_attention")
+    return out, lse

@@ -78,6 +78,7 @@ struct AppendArgs {
 cudaError_t launch_lin_chunk_simt(const LinArgs &a, kda_dtype_t dt, cudaStream_t st);
 cudaError_t launch_lin_step(const LinStepArgs &a, int dk, int dv, kda_dtype_t dt, cudaStream_t st);
 cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st);
+size_t paged_attention_workspace_bytes(int64_t rows, int heads, int kv_heads, int64_t max_tokens, int d, kda_dtype_t dt);
 cudaError_t launch_paged_attention(const PagedArgs &a, int d, kda_dtype_t dt, void *workspace, cudaStream_t st);
 
 }  // namespace kda

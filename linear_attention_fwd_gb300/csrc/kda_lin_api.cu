@@ -21,8 +21,8 @@ kda_status_t check_paged_dims(const kda_paged_dims_t *d) {
     if (d == nullptr) return KDA_ERR_NULL;
     if (!dtype_ok(d->dtype) || !head_size_ok(d->head_dim)) return KDA_ERR_UNSUPPORTED;
     if (d->rows < 0 || d->kv_heads <= 0 || d->pages <= 0 || d->page_size <= 0 || d->max_pages <= 0) return KDA_ERR_SHAPE;
-    // positions within a row are 32-bit
-    if ((int64_t)d->max_pages * d->page_size > 0x7fffffffLL) return KDA_ERR_SHAPE;
+    // a position within a row, and with the sign bit a token's place in the pool, are 32-bit
+    if ((int64_t)d->max_pages * d->page_size > 0x7fffffffLL - 64 || (int64_t)d->pages * d->page_size > 0xffffffffLL) return KDA_ERR_SHAPE;
     return KDA_OK;
 }
 
@@ -112,8 +112,9 @@ extern "C" kda_status_t kda_paged_append(const void *k, const void *v, void *k_c
 }
 
 extern "C" size_t kda_paged_attention_workspace_bytes(const kda_paged_dims_t *d) {
-    (void)d;
-    return 0;
+    if (check_paged_dims(d) != KDA_OK || d->heads <= 0 || d->heads % d->kv_heads != 0) return 0;
+    return kda::paged_attention_workspace_bytes(d->rows, d->heads, d->kv_heads, (int64_t)d->max_pages * d->page_size,
+                                                d->head_dim, d->dtype);
 }
 
 extern "C" kda_status_t kda_paged_attention(const void *q, const void *k_cache, const void *v_cache,

@@ -75,7 +75,11 @@ struct AppendArgs {
     int32_t row_vecs;         // 16-byte vectors of one token's keys (kv_heads * head_dim * size / 16)
 };
 
-cudaError_t launch_lin_chunk_simt(const LinArgs &a, kda_dtype_t dt, cudaStream_t st);
+cudaError_t launch_lin_chunk_simt(const LinArgs &a, cudaStream_t st);   // fp32
+// bf16: `parts` CTAs per (sequence, head); with more than one, workspace of lin_workspace_bytes.
+cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, int parts, cudaStream_t st);
+// Waits for `st`, then reads and clears the count of expired bounded waits of that kernel.
+cudaError_t take_lin_expiries(cudaStream_t st, unsigned int *count);
 cudaError_t launch_lin_step(const LinStepArgs &a, int dk, int dv, kda_dtype_t dt, cudaStream_t st);
 cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st);
 size_t paged_attention_workspace_bytes(int64_t rows, int heads, int kv_heads, int64_t max_tokens, int d, kda_dtype_t dt);

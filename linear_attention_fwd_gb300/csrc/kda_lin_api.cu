@@ -28,9 +28,21 @@ kda_status_t check_paged_dims(const kda_paged_dims_t *d) {
 
 }  // namespace
 
+// CTAs per (sequence, head) of the tensor-core kernel: as many as fill the SMs, at most 16, each of
+// at least 8 chunks of 64 tokens on average.
+static int lin_parts(const kda_lin_dims_t *d) {
+    if (d->dtype != KDA_BF16) return 1;
+    const int64_t units = (int64_t)d->num_seqs * d->heads, chunks = (int64_t)d->batch * d->seqlen / d->num_seqs / 64;
+    int64_t parts = kda::kSms / units;
+    if (parts > 16) parts = 16;
+    if (parts > chunks / 8) parts = chunks / 8;
+    return parts < 1 ? 1 : (int)parts;
+}
+
 extern "C" size_t kda_lin_chunk_fwd_workspace_bytes(const kda_lin_dims_t *d) {
-    (void)d;
-    return 0;
+    if (check_lin_dims(d) != KDA_OK || d->batch <= 0 || d->seqlen <= 0) return 0;
+    // the parts' states, then their decays; all but the last part's
+    return (size_t)(lin_parts(d) - 1) * d->num_seqs * d->heads * ((size_t)d->dk * d->dv * 4 + 8);
 }
 
 extern "C" kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const float *g,
@@ -70,7 +82,11 @@ extern "C" kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const vo
     }
     const kda::LinArgs a{q, k, v, g, head_g, initial_state, cu_seqlens, out, final_state,
                          (int64_t)d->seqlen, d->num_seqs, d->heads, d->qk_heads, d->dk, d->dv};
-    return kda::launch_lin_chunk_simt(a, d->dtype, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    // in place, a unit's last part would write the state that its other parts start from
+    const int parts = initial_state && initial_state == final_state ? 1 : lin_parts(d);
+    const cudaError_t e = d->dtype == KDA_BF16 ? kda::launch_lin_chunk_tc(a, workspace, parts, stream)
+                                               : kda::launch_lin_chunk_simt(a, stream);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 extern "C" kda_status_t kda_lin_recurrent_step(const void *q, const void *k, const void *v, const float *g,

@@ -1,4 +1,4 @@
-// Linear attention with a decay for each head, chunkwise, in fp32 arithmetic.
+// Linear attention with a decay for each head, chunkwise, for fp32 inputs (fp32 arithmetic).
 //
 // Chunks of C = 32 tokens, G_i = sum of the log decays of the chunk's tokens 0..i, S the state
 // before the chunk:
@@ -17,16 +17,7 @@ namespace {
 
 constexpr int C = 32, CB = 32, kThreads = 256;
 
-template <typename T> __device__ __forceinline__ float4 load4(const T *p);
-template <> __device__ __forceinline__ float4 load4<float>(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x));
-    const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y));
-    return make_float4(x.x, x.y, y.x, y.y);
-}
-
-template <typename T, int DK>
+template <int DK>
 __global__ void __launch_bounds__(kThreads) kda_lin_chunk_simt_kernel(LinArgs a) {
     constexpr int LD = DK + 4;                 // row pitch of Q and K: 16-byte reads of 8 rows hit 8 bank groups
     extern __shared__ __align__(16) float smem[];
@@ -40,8 +31,8 @@ __global__ void __launch_bounds__(kThreads) kda_lin_chunk_simt_kernel(LinArgs a)
     const int n = unit / a.heads, h = unit - n * a.heads, hk = h / (a.heads / a.qk_heads);
     int64_t bos, eos;
     lin_range(a, n, bos, eos);
-    const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k), *v = static_cast<const T *>(a.v);
-    T *out = static_cast<T *>(a.out);
+    const float *q = static_cast<const float *>(a.q), *k = static_cast<const float *>(a.k), *v = static_cast<const float *>(a.v);
+    float *out = static_cast<float *>(a.out);
 
     // this thread's part of S: RT rows from r0, 4 columns from cc
     constexpr int RT = DK / 32;
@@ -61,8 +52,8 @@ __global__ void __launch_bounds__(kThreads) kda_lin_chunk_simt_kernel(LinArgs a)
             float4 qv = make_float4(0.f, 0.f, 0.f, 0.f), kv = qv;
             if (r < nr) {
                 const int64_t at = ((t0 + r) * a.qk_heads + hk) * DK + c;
-                qv = load4(q + at);
-                kv = load4(k + at);
+                qv = *reinterpret_cast<const float4 *>(q + at);
+                kv = *reinterpret_cast<const float4 *>(k + at);
             }
             *reinterpret_cast<float4 *>(&sQ[r][c]) = qv;
             *reinterpret_cast<float4 *>(&sK[r][c]) = kv;
@@ -70,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) kda_lin_chunk_simt_kernel(LinArgs a)
         {
             const int r = t / 8, c = 4 * (t % 8);
             *reinterpret_cast<float4 *>(&sV[r][c]) =
-                r < nr ? load4(v + ((t0 + r) * a.heads + h) * a.dv + c0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                r < nr ? *reinterpret_cast<const float4 *>(v + ((t0 + r) * a.heads + h) * a.dv + c0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         if (t < 32) {
             double G = t < nr ? lin_log2_decay(a, t0 + t, h) : 0.0;
@@ -144,9 +135,8 @@ __global__ void __launch_bounds__(kThreads) kda_lin_chunk_simt_kernel(LinArgs a)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 if (2 * ty + e < nr) {
-                    T *o = out + ((t0 + 2 * ty + e) * a.heads + h) * a.dv + c0 + 2 * tx;
-                    o[0] = from_f<T>(acc[e][0]);
-                    o[1] = from_f<T>(acc[e][1]);
+                    *reinterpret_cast<float2 *>(out + ((t0 + 2 * ty + e) * a.heads + h) * a.dv + c0 + 2 * tx) =
+                        make_float2(acc[e][0], acc[e][1]);
                 }
         }
         __syncthreads();   // sS is read
@@ -174,22 +164,21 @@ __global__ void __launch_bounds__(kThreads) kda_lin_chunk_simt_kernel(LinArgs a)
         for (int m = 0; m < RT; ++m) *reinterpret_cast<float4 *>(a.sT + sbase + (int64_t)(r0 + m) * a.dv) = s[m];
 }
 
-template <typename T, int DK>
+template <int DK>
 cudaError_t launch_t(const LinArgs &a, cudaStream_t st) {
     constexpr int smem = (2 * C * (DK + 4) + (C + DK) * CB) * 4;
-    const cudaError_t e = cudaFuncSetAttribute(kda_lin_chunk_simt_kernel<T, DK>,
+    const cudaError_t e = cudaFuncSetAttribute(kda_lin_chunk_simt_kernel<DK>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = (int64_t)a.num_seqs * a.heads * (a.dv / CB);
-    kda_lin_chunk_simt_kernel<T, DK><<<(unsigned)grid, kThreads, smem, st>>>(a);
+    kda_lin_chunk_simt_kernel<DK><<<(unsigned)grid, kThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_lin_chunk_simt(const LinArgs &a, kda_dtype_t dt, cudaStream_t st) {
-    if (dt == KDA_F32) return a.dk == 128 ? launch_t<float, 128>(a, st) : launch_t<float, 64>(a, st);
-    return a.dk == 128 ? launch_t<__nv_bfloat16, 128>(a, st) : launch_t<__nv_bfloat16, 64>(a, st);
+cudaError_t launch_lin_chunk_simt(const LinArgs &a, cudaStream_t st) {
+    return a.dk == 128 ? launch_t<128>(a, st) : launch_t<64>(a, st);
 }
 
 }  // namespace kda

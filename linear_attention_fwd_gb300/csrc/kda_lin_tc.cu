@@ -1,0 +1,537 @@
+// Linear attention with a decay for each head, chunkwise, on the sm_103a tensor cores
+// (tcgen05 + TMEM + TMA).  bf16 inputs and outputs, fp32 state, computed at d_k = d_v = 128 (a
+// 64-wide head reads its missing channels as zeros).
+//
+// Chunks of C = 64 tokens; G_i = sum of the chunk's log decays up to token i, S the state before
+// the chunk, all products transposed so that the state's value channels are TMEM lanes:
+//   (1) S^T <- e^{G_63} S^T + V^T K',   K'_j = e^{G_63 - G_j} k_j
+//   (2) O_I^T = S^T Q^T                 (scaled by e^{G_i} per token in fp32 when it is read)
+//   (3) O_J^T = V^T P^T,                P_ij = (q_i . k_j) e^{G_i - G_j}, j <= i
+// Every exponent is <= 0.  The sums G are fp64, kept as two floats, so that a difference is exact
+// to fp32 whatever the sums' magnitude.
+//
+// Precision.  The tensor cores multiply bf16 exactly and add in fp32.  q, k and v enter as they
+// are; what is computed enters as a sum of bf16 terms, each the rounding of what the ones before it
+// left: K' as three (2^-24 of each product: the state is an fp32 result), S and P as two (2^-16:
+// they end in bf16 outputs, whose own rounding is 2^-8).  bf16 has fp32's range, so no scale is
+// carried.
+//
+// Roles (18 warps).  Everything meets at mbarriers; no CTA-wide barrier inside the loop.
+//   warps 0-7    S: state from TMEM after (1) of the chunk before, its bf16 terms and the scaled
+//                state back to TMEM (64 key channels per thread)
+//   warps 8-11   O: the chunk's two output products from TMEM to global memory
+//   warps 12-15  K', then P (mma.sync, the scores' fragments are the rows to scale and store)
+//   warp 16      TMA of the tiles, three chunks ahead, and the decay sums
+//   warp 17      issues the tensor-core products
+// Per chunk the tensor pipe runs (1) 12 x M128 N128 K16, (2) 16 x M128 N64 K16, (3) 8 x M128 N64
+// K16; (2) and (3) cover the S warps' turn-around, (1) the O warps'.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "kda_lin.h"
+#include "tc_ptx.cuh"
+
+namespace kda {
+
+// Count of bounded device waits that gave up since the host last read it.
+__device__ unsigned int g_kda_lin_timeouts = 0;
+
+namespace {
+
+using namespace ptx;
+
+constexpr int C = 64, D = 128, NT = 18 * 32;
+constexpr int kStages = 3, kGRing = 4;
+constexpr uint32_t kWaitPolls = 1u << 20;   // about a second, then the CTA gives up
+
+// shared memory, byte offsets from a 1024-aligned base
+constexpr uint32_t STAGE = 3 * 16384;                       // Q, K, V tiles [64][128] bf16, 128-byte swizzle
+constexpr uint32_t OFF_KP = kStages * STAGE;                // K': three terms [64][128] bf16, same layout
+constexpr uint32_t OFF_P = OFF_KP + 3 * 16384;              // P: two terms [64 i][64 j] bf16
+constexpr uint32_t OFF_G = OFF_P + 2 * 8192;                // decay vectors, kGRing slots
+constexpr uint32_t G_SLOT = 4 * 64 * 4 + 16;                //   G hi, G lo, e^{G_63 - G}, e^G; e^{G_63}
+constexpr uint32_t OFF_BAR = OFF_G + kGRing * G_SLOT;
+enum Bar { kFull = 0, kEmpty = 3, kG = 6, kKp = 10, kP = 11, kReady = 12, kDone = 13, kOFull = 14, kOEmpty = 15, kBars = 16 };
+constexpr uint32_t OFF_TM = OFF_BAR + kBars * 8;
+constexpr uint32_t SMEM_BYTES = OFF_TM + 16 + 1024;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+static_assert(OFF_BAR % 8 == 0 && G_SLOT % 16 == 0, "alignment");
+
+// tensor memory columns (lane = value channel)
+constexpr uint32_t TM_S = 0;        // S^T fp32, scaled for the running chunk   128
+constexpr uint32_t TM_S16 = 128;    // S^T as two bf16 terms, two buffers       2 x (64 + 64)
+constexpr uint32_t TM_OI = 384;     // (2)                                      64
+constexpr uint32_t TM_OJ = 448;     // (3)                                      64
+constexpr uint32_t TM_COLS = 512;
+
+constexpr uint32_t IDESC_KV = idesc_bf16_f32(128, 128) | (1u << 15) | (1u << 16);   // A (V) and B (K') MN-major
+constexpr uint32_t IDESC_SQ = idesc_bf16_f32(128, 64);                              // A in TMEM, B (Q) K-major
+constexpr uint32_t IDESC_VP = idesc_bf16_f32(128, 64) | (1u << 15);                 // A (V) MN-major, B (P) K-major
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Byte offset of element (row, col) in a 128-byte-swizzled tile of 64 rows, 64-column halves 8 KB apart.
+__device__ __forceinline__ uint32_t sw(int row, int col) {
+    return (uint32_t)((col >> 6) * 8192 + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4) + ((col & 7) << 1));
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// x as a bf16 pair and the rest it leaves
+__device__ __forceinline__ uint32_t take_bf16(float2 &x) {
+    const uint32_t h = pack_bf16(x.x, x.y);
+    x = __ffma2_rn(unpack_bf16(h), make_float2(-1.f, -1.f), x);
+    return h;
+}
+
+// One CTA per (sequence, head) unit and part of its chunks: part p of P is chunks
+// [p nc / P, (p + 1) nc / P).  kFull: the whole forward of the part; its state at the start is
+// composed from the initial state and the states that the parts before it reach from zero
+// (`locals`, with their total log2 decays).  Otherwise only that state: the part's from zero.
+template <bool kFullPass>
+__global__ void __launch_bounds__(NT, 1)
+kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                        const __grid_constant__ CUtensorMap tmv, const LinArgs a, const int P,
+                        float *locals, double *decays) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int s_fail;
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int H = a.heads;
+    const int64_t units = (int64_t)a.num_seqs * H;
+    const int p = (int)(blockIdx.x / units);
+    const int64_t unit = blockIdx.x % units;
+    const int n = (int)(unit / H), h = (int)(unit % H), hk = h / (H / a.qk_heads);
+    int64_t bos, eos;
+    lin_range(a, n, bos, eos);
+    const int nc = (int)((eos - bos + C - 1) / C);
+    const int c_lo = (int)((int64_t)p * nc / P), c_hi = (int)((int64_t)(p + 1) * nc / P);
+    const int chunks = c_hi - c_lo;
+    const int64_t first = bos + (int64_t)c_lo * C;     // the part's first token
+    const bool last_part = p == P - 1;
+    if (chunks == 0 && !(kFullPass ? last_part && a.sT : true)) return;
+
+    auto bar = [&](int b) { return sb + OFF_BAR + 8 * b; };
+    if (tid == 0) {
+        s_fail = 0;
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(bar(kFull + s), 1);
+            mbar_init(bar(kEmpty + s), 1);
+        }
+        for (int s = 0; s < kGRing; ++s) mbar_init(bar(kG + s), 32);
+        mbar_init(bar(kKp), 128);
+        mbar_init(bar(kP), 128);
+        mbar_init(bar(kReady), 256);
+        mbar_init(bar(kDone), 1);
+        mbar_init(bar(kOFull), 1);
+        mbar_init(bar(kOEmpty), 128);
+        fence_mbar_init();
+    }
+    if (warp == 17) {
+        tmem_alloc(sb + OFF_TM, TM_COLS);
+        tmem_relinquish();
+    }
+    if (kFullPass && warp >= 12 && warp < 16)   // P's blocks above the diagonal stay zero
+        for (int x = tid - 384; x < 1024; x += 128) *reinterpret_cast<uint4 *>(sm + OFF_P + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + OFF_TM);
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int jl = 32 * (warp & 3) + lane;             // value channel of this thread's TMEM lane
+    auto gslot = [&](int k) { return reinterpret_cast<float *>(sm + OFF_G + (k % kGRing) * G_SLOT); };
+    auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity & 1u, kWaitPolls); };
+    bool ok = true;
+
+    if (warp < 8) {
+        // ---- S: this thread's 64 key channels from i0, 32 at a time
+        const int i0 = 64 * (warp >> 2);
+        const int64_t sstep = (int64_t)a.dk * a.dv;
+        for (int k = 0; k <= chunks; ++k) {
+            float dec = 1.f;
+            if (k > 0) ok = wait(kDone, k - 1);
+            if (ok && k < chunks) {
+                ok = wait(kG + k % kGRing, k / kGRing);
+                dec = gslot(k)[256];
+            }
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int ib = i0 + 32 * b;
+                float v[32];
+                if (k > 0) {
+                    tmem_ld32(trow + TM_S + ib, v);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[c] = 0.f;
+                    if (kFullPass && jl < a.dv && ib < a.dk) {
+                        const int64_t at = (int64_t)ib * a.dv + jl;
+                        if (a.s0)
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) v[c] = a.s0[unit * sstep + at + (int64_t)c * a.dv];
+                        for (int e = 0; e < p; ++e) {
+                            const float f = exp2f((float)decays[e * units + unit]);
+                            const float *l = locals + (e * units + unit) * sstep + at;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) v[c] = fmaf(f, v[c], __ldcg(l + (int64_t)c * a.dv));
+                        }
+                    }
+                }
+                if (k == chunks) {   // the part's last state
+                    float *to = kFullPass ? (last_part ? a.sT : nullptr) : locals;
+                    if (to && jl < a.dv && ib < a.dk) {
+                        to += (kFullPass ? unit : p * units + unit) * sstep + (int64_t)ib * a.dv + jl;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) to[(int64_t)c * a.dv] = v[c];
+                    }
+                    continue;
+                }
+                if (kFullPass) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        float2 x = make_float2(v[2 * c], v[2 * c + 1]);
+                        hi[c] = take_bf16(x);
+                        lo[c] = pack_bf16(x.x, x.y);
+                    }
+                    const uint32_t t16 = trow + TM_S16 + 128 * (k & 1) + ib / 2;
+                    tmem_st16u(t16, hi);
+                    tmem_st16u(t16 + 64, lo);
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] *= dec;
+                tmem_st32(trow + TM_S + ib, v);
+            }
+            if (k < chunks) {
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(kReady));
+            }
+        }
+    } else if (warp < 12) {
+        // ---- O: tokens as columns, this thread's value channel; lanes 2c and 2c + 1 exchange halves so
+        // that each stores channel pairs of every other token
+        if (kFullPass) {
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
+            const int odd = lane & 1;
+            for (int k = 0; k < chunks; ++k) {
+                ok = wait(kOFull, k) && wait(kG + k % kGRing, k / kGRing);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float *eg = gslot(k) + 192;
+                const int64_t t0 = first + (int64_t)k * C;
+                const int nr = eos - t0 < C ? (int)(eos - t0) : C;
+                __nv_bfloat16 *o = out + ((t0 + odd) * H + h) * a.dv + (jl & ~1);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    float v[32], w[32];
+                    tmem_ld32x2(trow + TM_OI + 32 * b, trow + TM_OJ + 32 * b, v, w);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 e4 = *reinterpret_cast<const float4 *>(eg + 32 * b + c);
+                        v[c] = fmaf(e4.x, v[c], w[c]);
+                        v[c + 1] = fmaf(e4.y, v[c + 1], w[c + 1]);
+                        v[c + 2] = fmaf(e4.z, v[c + 2], w[c + 2]);
+                        v[c + 3] = fmaf(e4.w, v[c + 3], w[c + 3]);
+                    }
+                    if (b == 1) {
+                        tc_fence_before();
+                        mbar_arrive(bar(kOEmpty));
+                    }
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
+                        const uint32_t x = odd ? pack_bf16(got, v[c + 1]) : pack_bf16(v[c], got);
+                        const int tok = 32 * b + c;
+                        if (tok + odd < nr && jl < a.dv) *reinterpret_cast<uint32_t *>(o + (int64_t)tok * H * a.dv) = x;
+                    }
+                }
+            }
+        }
+    } else if (warp < 16) {
+        // ---- K' and P
+        const int t = tid - 384, I = warp - 12;        // P: rows 16 I ..
+        const int g = lane >> 2, t4 = lane & 3;
+        for (int k = 0; k < chunks; ++k) {
+            const int s = k % kStages;
+            const uint32_t st = s * STAGE;
+            const int64_t left = eos - (first + (int64_t)k * C);
+            const int nr = left < C ? (int)left : C;
+            ok = wait(kFull + s, k / kStages) && wait(kG + k % kGRing, k / kGRing) && (k == 0 || wait(kDone, k - 1));
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            const float *gv = gslot(k);
+#pragma unroll 2
+            for (int e = 0; e < 8; ++e) {   // 16-byte pieces lie at the same offsets in K and K'
+                const int x = t + 128 * e, r = (x >> 3) & 63;
+                const uint4 u = *reinterpret_cast<const uint4 *>(sm + st + 16384 + 16 * x);
+                const float w = gv[128 + r];
+                const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+                uint32_t o0[4], o1[4], o2[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float2 y = __fmul2_rn(unpack_bf16(r < nr ? uw[c] : 0u), make_float2(w, w));
+                    o0[c] = take_bf16(y);
+                    o1[c] = take_bf16(y);
+                    o2[c] = pack_bf16(y.x, y.y);
+                }
+                uint4 *to = reinterpret_cast<uint4 *>(sm + OFF_KP + 16 * x);
+                to[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+                to[1024] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+                to[2048] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+                // rows past the sequence belong to another one: their values never enter a product
+                if (r >= nr) *reinterpret_cast<uint4 *>(sm + st + 32768 + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_async_smem();
+            mbar_arrive(bar(kKp));
+            if (!kFullPass) continue;
+
+            uint32_t qa[8][4];
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                ldsm_x4(sb + st + sw(16 * I + (lane & 15), 16 * kk + ((lane >> 4) << 3)), qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3]);
+            const int r0 = 16 * I + g;
+            const float gh0 = gv[r0], gh1 = gv[r0 + 8], gl0 = gv[64 + r0], gl1 = gv[64 + r0 + 8];
+            ok = k == 0 || wait(kOFull, k - 1);   // the previous chunk's P is consumed
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            for (int J = 0; J <= I; ++J) {
+                float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    uint32_t b0, b1, b2, b3;
+                    ldsm_x4(sb + st + 16384 + sw(16 * J + (lane & 7) + ((lane >> 4) << 3), 16 * kk + (((lane >> 3) & 1) << 3)), b0, b1, b2, b3);
+                    mma_16816(acc[0], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b0, b1);
+                    mma_16816(acc[1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b2, b3);
+                }
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const int j = 16 * J + 8 * nt + 2 * t4;
+                    const float2 hj = *reinterpret_cast<const float2 *>(gv + j), lj = *reinterpret_cast<const float2 *>(gv + 64 + j);
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const int i = r0 + 8 * hh;
+                        const float gh = hh ? gh1 : gh0, gl = hh ? gl1 : gl0;
+                        float2 x;
+                        x.x = j <= i && j < nr ? acc[nt][2 * hh] * ex2((gh - hj.x) + (gl - lj.x)) : 0.f;
+                        x.y = j + 1 <= i && j + 1 < nr ? acc[nt][2 * hh + 1] * ex2((gh - hj.y) + (gl - lj.y)) : 0.f;
+                        const uint32_t at = OFF_P + sw(i, j);
+                        *reinterpret_cast<uint32_t *>(sm + at) = take_bf16(x);
+                        *reinterpret_cast<uint32_t *>(sm + at + 8192) = pack_bf16(x.x, x.y);
+                    }
+                }
+            }
+            fence_async_smem();
+            mbar_arrive(bar(kP));
+        }
+    } else if (warp == 16) {
+        // ---- tiles by TMA, and the decay sums: lane l holds tokens 2l and 2l + 1
+        double total = 0.0;
+        auto load_g = [&](int k, double &x, double &y) {
+            const int64_t t = first + (int64_t)k * C + 2 * lane;
+            x = t < eos ? lin_log2_decay(a, t, h) : 0.0;
+            y = t + 1 < eos ? lin_log2_decay(a, t + 1, h) : 0.0;
+        };
+        double gx = 0.0, gy = 0.0;
+        if (chunks > 0) load_g(0, gx, gy);
+        for (int k = 0; k < chunks; ++k) {
+            const int s = k % kStages;
+            ok = k < kStages || wait(kEmpty + s, k / kStages - 1);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                const uint32_t st = sb + s * STAGE, b = bar(kFull + s);
+                const int tok = (int)(first + (int64_t)k * C);
+                mbar_arrive_expect_tx(b, kFullPass ? 3 * 16384 : 2 * 16384);
+                tma_load_3d(st + 16384, &tmk, b, 0, hk, tok);
+                tma_load_3d(st + 24576, &tmk, b, 64, hk, tok);
+                tma_load_3d(st + 32768, &tmv, b, 0, h, tok);
+                tma_load_3d(st + 40960, &tmv, b, 64, h, tok);
+                if (kFullPass) {
+                    tma_load_3d(st, &tmq, b, 0, hk, tok);
+                    tma_load_3d(st + 8192, &tmq, b, 64, hk, tok);
+                }
+            }
+            __syncwarp();
+            const double x = gx, y = gy;
+            if (k + 1 < chunks) load_g(k + 1, gx, gy);
+            double G1 = x + y;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double z = __shfl_up_sync(0xffffffffu, G1, o);
+                if (lane >= o) G1 += z;
+            }
+            const double G0 = __shfl_up_sync(0xffffffffu, G1, 1);
+            const double Ga = (lane ? G0 : 0.0) + x;
+            const double last = __shfl_sync(0xffffffffu, G1, 31);
+            float *gv = gslot(k);
+            const float2 hi = make_float2((float)Ga, (float)G1);
+            reinterpret_cast<float2 *>(gv)[lane] = hi;
+            reinterpret_cast<float2 *>(gv + 64)[lane] = make_float2((float)(Ga - (double)hi.x), (float)(G1 - (double)hi.y));
+            reinterpret_cast<float2 *>(gv + 128)[lane] = make_float2(exp2f((float)(last - Ga)), exp2f((float)(last - G1)));
+            reinterpret_cast<float2 *>(gv + 192)[lane] = make_float2(exp2f(hi.x), exp2f(hi.y));
+            if (lane == 0) gv[256] = exp2f((float)last);
+            total += last;
+            mbar_arrive(bar(kG + k % kGRing));
+        }
+        if (!kFullPass && lane == 0) decays[p * units + unit] = total;
+    } else if (lane == 0) {
+        // ---- tensor-core products
+        const uint64_t dsm = sdesc_sw128(sb);
+        const uint64_t kpd = sdesc_sw128_mn(sb + OFF_KP, 8192, 1024);
+        for (int k = 0; k < chunks; ++k) {
+            const int s = k % kStages;
+            const uint32_t st = s * STAGE;
+            const uint64_t vd = sdesc_sw128_mn(sb + st + 32768, 8192, 1024);
+            ok = wait(kFull + s, k / kStages) && wait(kReady, k) && wait(kKp, k);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16_ss(tmem + TM_S, vd + ((2048 * kk) >> 4), kpd + ((16384 * e + 2048 * kk) >> 4), IDESC_KV, 1);
+            mma_commit(bar(kDone));
+            if (kFullPass) {
+                ok = k == 0 || wait(kOEmpty, k - 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_f16_ts(tmem + TM_OI, tmem + TM_S16 + 128 * (k & 1) + 64 * e + 8 * kk,
+                                   dsm + ((st + (kk >> 2) * 8192 + (kk & 3) * 32) >> 4), IDESC_SQ, e + kk > 0);
+                ok = wait(kP, k);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16_ss(tmem + TM_OJ, vd + ((2048 * kk) >> 4), dsm + ((OFF_P + 8192 * e + 32 * kk) >> 4), IDESC_VP, e + kk > 0);
+                mma_commit(bar(kOFull));
+            }
+            mma_commit(bar(kEmpty + s));
+        }
+        // nothing arrives at a barrier after the CTA has ended
+        for (int k = chunks > kStages ? chunks - kStages : 0; ok && k < chunks; ++k) ok = wait(kEmpty + k % kStages, k / kStages);
+    }
+    __syncwarp();
+    if (!ok) s_fail = 1;
+    tc_fence_before();
+    __syncthreads();
+    if (s_fail) {
+        // A bounded wait expired.  What is in flight lands first (each barrier it completes is given
+        // a few milliseconds for both parities), then the part's results are marked.
+        if (tid == 0) {
+            for (int b = 0; b < kBars; ++b) {
+                mbar_wait(bar(b), 0, 1u << 12);
+                mbar_wait(bar(b), 1, 1u << 12);
+            }
+            atomicAdd(&g_kda_lin_timeouts, 1u);
+        }
+        const float nan = __int_as_float(0x7fc00000);
+        float *to = kFullPass ? (last_part ? a.sT : nullptr) : locals;
+        if (to) {
+            to += (kFullPass ? unit : p * units + unit) * (int64_t)a.dk * a.dv;
+            for (int x = tid; x < a.dk * a.dv; x += NT) to[x] = nan;
+        }
+        if (kFullPass) {
+            const int64_t t1 = bos + (int64_t)c_hi * C < eos ? bos + (int64_t)c_hi * C : eos;
+            for (int64_t x = tid; x < (t1 - first) * a.dv; x += NT)
+                static_cast<__nv_bfloat16 *>(a.out)[((first + x / a.dv) * H + h) * a.dv + x % a.dv] = __float2bfloat16(nan);
+        } else if (tid == 0) {
+            decays[p * units + unit] = 0.0;
+        }
+        __syncthreads();
+    }
+    if (warp == 17) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, TM_COLS);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p)
+                   : nullptr;
+    }();
+    return fn;
+}
+
+// [tokens][H][d] bf16 as (d, H, tokens), 64 x 1 x 64 boxes, 128-byte swizzle.  The second box of a
+// 64-wide head lies past the first dimension and lands as zeros, as do tokens past the end.
+bool make_map(CUtensorMap *m, const void *ptr, int64_t tokens, int H, int d) {
+    auto enc = encode_fn();
+    if (enc == nullptr) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2};
+    cuuint32_t box[3] = {64, 1, 64};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t take_lin_expiries(cudaStream_t st, unsigned int *count) {
+    static const unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(count, g_kda_lin_timeouts, sizeof(unsigned int), 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess)
+        e = cudaMemcpyToSymbolAsync(g_kda_lin_timeouts, &zero, sizeof(unsigned int), 0, cudaMemcpyHostToDevice, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    return e;
+}
+
+cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, int parts, cudaStream_t st) {
+    const int64_t tokens = a.cu ? a.seqlen : (int64_t)a.num_seqs * a.seqlen;
+    const int64_t units = (int64_t)a.num_seqs * a.heads;
+    CUtensorMap mq, mk, mv;
+    if (!make_map(&mq, a.q, tokens, a.qk_heads, a.dk) || !make_map(&mk, a.k, tokens, a.qk_heads, a.dk) ||
+        !make_map(&mv, a.v, tokens, a.heads, a.dv))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(kda_lin_chunk_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    float *locals = static_cast<float *>(workspace);
+    double *decays = reinterpret_cast<double *>(locals + (int64_t)(parts - 1) * units * a.dk * a.dv);
+    if (parts > 1) {
+        e = cudaFuncSetAttribute(kda_lin_chunk_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        // parts 0 .. parts - 2 of `parts`: the last one's state from zero is not needed
+        kda_lin_chunk_tc_kernel<false><<<(unsigned)(units * (parts - 1)), NT, SMEM_BYTES, st>>>(mq, mk, mv, a, parts, locals, decays);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    kda_lin_chunk_tc_kernel<true><<<(unsigned)(units * parts), NT, SMEM_BYTES, st>>>(mq, mk, mv, a, parts, locals, decays);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

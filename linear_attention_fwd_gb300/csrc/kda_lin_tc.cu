@@ -4,27 +4,30 @@
 //
 // Chunks of C = 64 tokens; G_i = sum of the chunk's log decays up to token i, S the state before
 // the chunk, all products transposed so that the state's value channels are TMEM lanes:
-//   (1) S^T <- e^{G_63} S^T + V^T K',   K'_j = e^{G_63 - G_j} k_j
+//   (1) dS^T  = V^T K',                 K'_j = e^{G_63 - G_j} k_j,     then S <- e^{G_63} S + dS
 //   (2) O_I^T = S^T Q^T                 (scaled by e^{G_i} per token in fp32 when it is read)
 //   (3) O_J^T = V^T P^T,                P_ij = (q_i . k_j) e^{G_i - G_j}, j <= i
-// Every exponent is <= 0.  The sums G are fp64, kept as two floats, so that a difference is exact
-// to fp32 whatever the sums' magnitude.
+// Every exponent is <= 0.  The sums G are kept as two floats, so that a difference is exact to fp32
+// whatever the sums' magnitude.
 //
 // Precision.  The tensor cores multiply bf16 exactly and add in fp32.  q, k and v enter as they
 // are; what is computed enters as a sum of bf16 terms, each the rounding of what the ones before it
 // left: K' as three (2^-24 of each product: the state is an fp32 result), S and P as two (2^-16:
 // they end in bf16 outputs, whose own rounding is 2^-8).  bf16 has fp32's range, so no scale is
-// carried.
+// carried.  The state itself stays in registers and takes each chunk's dS by an fp32 fused
+// multiply-add: the tensor cores truncate their sums, which over many chunks would pile up.
 //
-// Roles (18 warps).  Everything meets at mbarriers; no CTA-wide barrier inside the loop.
-//   warps 0-7    S: state from TMEM after (1) of the chunk before, its bf16 terms and the scaled
-//                state back to TMEM (64 key channels per thread)
-//   warps 8-11   O: the chunk's two output products from TMEM to global memory
-//   warps 12-15  K', then P (mma.sync, the scores' fragments are the rows to scale and store)
+// Roles (20 warps, registers shared out by setmaxnreg).  Everything meets at mbarriers; there is no
+// CTA-wide barrier inside the loop.
+//   warps 0-7    S: the state (64 key channels of one value channel per thread); its bf16 terms to
+//                TMEM
+//   warps 8-11   half of K', then the previous chunk's outputs from TMEM to global memory
+//   warps 12-15  half of K', then P (scores by mma.sync, decays and bf16 terms on the fragments)
 //   warp 16      TMA of the tiles, three chunks ahead, and the decay sums
 //   warp 17      issues the tensor-core products
 // Per chunk the tensor pipe runs (1) 12 x M128 N128 K16, (2) 16 x M128 N64 K16, (3) 8 x M128 N64
-// K16; (2) and (3) cover the S warps' turn-around, (1) the O warps'.
+// K16, in this order: K' of the next chunk is made during (2) and (3), and the S warps have the
+// whole of (1) to turn dS of the chunk before into the operand of (2).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -40,7 +43,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int C = 64, D = 128, NT = 18 * 32;
+constexpr int C = 64, NT = 20 * 32;
 constexpr int kStages = 3, kGRing = 4;
 constexpr uint32_t kWaitPolls = 1u << 20;   // about a second, then the CTA gives up
 
@@ -51,15 +54,19 @@ constexpr uint32_t OFF_P = OFF_KP + 3 * 16384;              // P: two terms [64 
 constexpr uint32_t OFF_G = OFF_P + 2 * 8192;                // decay vectors, kGRing slots
 constexpr uint32_t G_SLOT = 4 * 64 * 4 + 16;                //   G hi, G lo, e^{G_63 - G}, e^G; e^{G_63}
 constexpr uint32_t OFF_BAR = OFF_G + kGRing * G_SLOT;
-enum Bar { kFull = 0, kEmpty = 3, kG = 6, kKp = 10, kP = 11, kReady = 12, kDone = 13, kOFull = 14, kOEmpty = 15, kBars = 16 };
-constexpr uint32_t OFF_TM = OFF_BAR + kBars * 8;
+// A wait names a phase by its parity, so no barrier may complete a phase before every waiter has
+// passed the one before.  That holds because each phase needs, directly or through others, an
+// arrival that its slowest waiter makes after that pass; the products (1) run ahead of the S warps
+// and so have a barrier for each of dS's buffers.
+enum Bar { kFull = 0, kEmpty = 3, kG = 6, kKp = 10, kP = 11, kReady = 12, kOFull = 13, kOEmpty = 14, kDone = 15, kBars = 17 };
+constexpr uint32_t OFF_TM = OFF_BAR + kBars * 8 + 8;
 constexpr uint32_t SMEM_BYTES = OFF_TM + 16 + 1024;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 static_assert(OFF_BAR % 8 == 0 && G_SLOT % 16 == 0, "alignment");
 
 // tensor memory columns (lane = value channel)
-constexpr uint32_t TM_S = 0;        // S^T fp32, scaled for the running chunk   128
-constexpr uint32_t TM_S16 = 128;    // S^T as two bf16 terms, two buffers       2 x (64 + 64)
+constexpr uint32_t TM_DS = 0;       // (1), two buffers                         2 x 128
+constexpr uint32_t TM_S16 = 256;    // S^T as two bf16 terms                    64 + 64
 constexpr uint32_t TM_OI = 384;     // (2)                                      64
 constexpr uint32_t TM_OJ = 448;     // (3)                                      64
 constexpr uint32_t TM_COLS = 512;
@@ -81,6 +88,16 @@ __device__ __forceinline__ uint32_t sw(int row, int col) {
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// (h, l) + (x, y) as two floats: the sum of the large parts is split exactly, the small parts are added
+__device__ __forceinline__ void add2f(float &h, float &l, float x, float y) {
+    const float s = h + x, b = s - h;
+    l += y + ((h - (s - b)) + (x - b));
+    h = s;
 }
 
 // x as a bf16 pair and the rest it leaves
@@ -126,10 +143,11 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
             mbar_init(bar(kEmpty + s), 1);
         }
         for (int s = 0; s < kGRing; ++s) mbar_init(bar(kG + s), 32);
-        mbar_init(bar(kKp), 128);
+        mbar_init(bar(kKp), 256);
         mbar_init(bar(kP), 128);
         mbar_init(bar(kReady), 256);
         mbar_init(bar(kDone), 1);
+        mbar_init(bar(kDone + 1), 1);
         mbar_init(bar(kOFull), 1);
         mbar_init(bar(kOEmpty), 128);
         fence_mbar_init();
@@ -149,294 +167,333 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
     const int jl = 32 * (warp & 3) + lane;             // value channel of this thread's TMEM lane
     auto gslot = [&](int k) { return reinterpret_cast<float *>(sm + OFF_G + (k % kGRing) * G_SLOT); };
     auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity & 1u, kWaitPolls); };
+    auto done = [&](int k) { return wait(kDone + (k & 1), k >> 1); };
     bool ok = true;
 
     if (warp < 8) {
-        // ---- S: this thread's 64 key channels from i0, 32 at a time
+        // ---- S
+        regs_inc<128>();
         const int i0 = 64 * (warp >> 2);
         const int64_t sstep = (int64_t)a.dk * a.dv;
-        for (int k = 0; k <= chunks; ++k) {
-            float dec = 1.f;
-            if (k > 0) ok = wait(kDone, k - 1);
-            if (ok && k < chunks) {
-                ok = wait(kG + k % kGRing, k / kGRing);
-                dec = gslot(k)[256];
-            }
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
+        const bool mine = jl < a.dv && i0 < a.dk;
+        const int64_t at = (int64_t)i0 * a.dv + jl;
+        float v[64];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int ib = i0 + 32 * b;
-                float v[32];
-                if (k > 0) {
-                    tmem_ld32(trow + TM_S + ib, v);
-                } else {
+        for (int c = 0; c < 64; ++c) v[c] = 0.f;
+        if (kFullPass && mine) {
+            if (a.s0)
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] = 0.f;
-                    if (kFullPass && jl < a.dv && ib < a.dk) {
-                        const int64_t at = (int64_t)ib * a.dv + jl;
-                        if (a.s0)
+                for (int c = 0; c < 64; ++c) v[c] = a.s0[unit * sstep + at + (int64_t)c * a.dv];
+            for (int e = 0; e < p; ++e) {
+                const float f = exp2f((float)decays[e * units + unit]);
+                const float *l = locals + (e * units + unit) * sstep + at;
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) v[c] = a.s0[unit * sstep + at + (int64_t)c * a.dv];
-                        for (int e = 0; e < p; ++e) {
-                            const float f = exp2f((float)decays[e * units + unit]);
-                            const float *l = locals + (e * units + unit) * sstep + at;
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) v[c] = fmaf(f, v[c], __ldcg(l + (int64_t)c * a.dv));
-                        }
-                    }
-                }
-                if (k == chunks) {   // the part's last state
-                    float *to = kFullPass ? (last_part ? a.sT : nullptr) : locals;
-                    if (to && jl < a.dv && ib < a.dk) {
-                        to += (kFullPass ? unit : p * units + unit) * sstep + (int64_t)ib * a.dv + jl;
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) to[(int64_t)c * a.dv] = v[c];
-                    }
-                    continue;
-                }
-                if (kFullPass) {
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        float2 x = make_float2(v[2 * c], v[2 * c + 1]);
-                        hi[c] = take_bf16(x);
-                        lo[c] = pack_bf16(x.x, x.y);
-                    }
-                    const uint32_t t16 = trow + TM_S16 + 128 * (k & 1) + ib / 2;
-                    tmem_st16u(t16, hi);
-                    tmem_st16u(t16 + 64, lo);
-                }
-#pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] *= dec;
-                tmem_st32(trow + TM_S + ib, v);
-            }
-            if (k < chunks) {
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(bar(kReady));
+                for (int c = 0; c < 64; ++c) v[c] = fmaf(f, v[c], __ldcg(l + (int64_t)c * a.dv));
             }
         }
-    } else if (warp < 12) {
-        // ---- O: tokens as columns, this thread's value channel; lanes 2c and 2c + 1 exchange halves so
-        // that each stores channel pairs of every other token
-        if (kFullPass) {
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
-            const int odd = lane & 1;
-            for (int k = 0; k < chunks; ++k) {
-                ok = wait(kOFull, k) && wait(kG + k % kGRing, k / kGRing);
+        for (int k = 0; k <= chunks; ++k) {
+            if (k > 0) {
+                ok = done(k - 1) && wait(kG + (k - 1) % kGRing, (k - 1) / kGRing);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const float *eg = gslot(k) + 192;
-                const int64_t t0 = first + (int64_t)k * C;
-                const int nr = eos - t0 < C ? (int)(eos - t0) : C;
-                __nv_bfloat16 *o = out + ((t0 + odd) * H + h) * a.dv + (jl & ~1);
+                const float dec = gslot(k - 1)[256];
+                const float2 d2 = make_float2(dec, dec);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    float v[32], w[32];
-                    tmem_ld32x2(trow + TM_OI + 32 * b, trow + TM_OJ + 32 * b, v, w);
-#pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const float4 e4 = *reinterpret_cast<const float4 *>(eg + 32 * b + c);
-                        v[c] = fmaf(e4.x, v[c], w[c]);
-                        v[c + 1] = fmaf(e4.y, v[c + 1], w[c + 1]);
-                        v[c + 2] = fmaf(e4.z, v[c + 2], w[c + 2]);
-                        v[c + 3] = fmaf(e4.w, v[c + 3], w[c + 3]);
-                    }
-                    if (b == 1) {
-                        tc_fence_before();
-                        mbar_arrive(bar(kOEmpty));
-                    }
+                    float w[32];
+                    tmem_ld32(trow + TM_DS + 128 * ((k - 1) & 1) + i0 + 32 * b, w);
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
-                        const uint32_t x = odd ? pack_bf16(got, v[c + 1]) : pack_bf16(v[c], got);
-                        const int tok = 32 * b + c;
-                        if (tok + odd < nr && jl < a.dv) *reinterpret_cast<uint32_t *>(o + (int64_t)tok * H * a.dv) = x;
+                        const float2 x = __ffma2_rn(d2, make_float2(v[32 * b + c], v[32 * b + c + 1]), make_float2(w[c], w[c + 1]));
+                        v[32 * b + c] = x.x;
+                        v[32 * b + c + 1] = x.y;
                     }
                 }
             }
+            if (k == chunks) break;
+            if (kFullPass) {
+                ok = k == 0 || wait(kOFull, k - 1);   // the chunk before has read its operand
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        float2 x = make_float2(v[16 * b + 2 * c], v[16 * b + 2 * c + 1]);
+                        hi[c] = take_bf16(x);
+                        lo[c] = pack_bf16(x.x, x.y);
+                    }
+                    tmem_st8u(trow + TM_S16 + i0 / 2 + 8 * b, hi);
+                    tmem_st8u(trow + TM_S16 + 64 + i0 / 2 + 8 * b, lo);
+                }
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            mbar_arrive(bar(kReady));
+        }
+        float *to = kFullPass ? (last_part ? a.sT : nullptr) : locals;
+        if (ok && to && mine) {
+            to += (kFullPass ? unit : p * units + unit) * sstep + at;
+#pragma unroll
+            for (int c = 0; c < 64; ++c) to[(int64_t)c * a.dv] = v[c];
         }
     } else if (warp < 16) {
-        // ---- K' and P
-        const int t = tid - 384, I = warp - 12;        // P: rows 16 I ..
-        const int g = lane >> 2, t4 = lane & 3;
-        for (int k = 0; k < chunks; ++k) {
-            const int s = k % kStages;
-            const uint32_t st = s * STAGE;
-            const int64_t left = eos - (first + (int64_t)k * C);
-            const int nr = left < C ? (int)left : C;
-            ok = wait(kFull + s, k / kStages) && wait(kG + k % kGRing, k / kGRing) && (k == 0 || wait(kDone, k - 1));
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
+        // ---- K' (each of the two halves of these warps half of it), then the halves' own work
+        regs_dec<88>();
+        const int half = (warp - 8) >> 2, t = tid & 127;
+        // O: tokens as columns, this thread's value channel.  Lanes 2c and 2c + 1 exchange halves so that
+        // each stores channel pairs of every other token.
+        const int odd = lane & 1;
+        const uint32_t sel = odd ? 0x3276u : 0x5410u;
+        const int64_t two = 2 * (int64_t)H * a.dv;   // two tokens
+        // P: 20 blocks of 16 x 8 on or below the diagonal, five a warp, two of them on it: three of row
+        // block I from c0, then two
+        const int w4 = warp & 3, g = lane >> 2, t4 = lane & 3;
+        const int Ia = w4 < 2 ? 3 : 2, ca = w4 & 1 ? 3 : 0;
+        const int Ib = w4 == 0 ? 0 : (w4 == 2 ? 3 : 1), cb = w4 == 1 ? 2 : (w4 == 2 ? 6 : 0);
+        for (int k = 0; k <= chunks; ++k) {
+            const uint32_t st = (k % kStages) * STAGE;
             const float *gv = gslot(k);
-#pragma unroll 2
-            for (int e = 0; e < 8; ++e) {   // 16-byte pieces lie at the same offsets in K and K'
-                const int x = t + 128 * e, r = (x >> 3) & 63;
-                const uint4 u = *reinterpret_cast<const uint4 *>(sm + st + 16384 + 16 * x);
-                const float w = gv[128 + r];
-                const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
-                uint32_t o0[4], o1[4], o2[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float2 y = __fmul2_rn(unpack_bf16(r < nr ? uw[c] : 0u), make_float2(w, w));
-                    o0[c] = take_bf16(y);
-                    o1[c] = take_bf16(y);
-                    o2[c] = pack_bf16(y.x, y.y);
+            if (k < chunks) {
+                const int64_t left = eos - (first + (int64_t)k * C);
+                const int nr = left < C ? (int)left : C;
+                // the tile and its decays landed, K' of the chunk before consumed
+                ok = wait(kFull + k % kStages, k / kStages) && wait(kG + k % kGRing, k / kGRing) && (k == 0 || done(k - 1));
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
                 }
-                uint4 *to = reinterpret_cast<uint4 *>(sm + OFF_KP + 16 * x);
-                to[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-                to[1024] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-                to[2048] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
-                // rows past the sequence belong to another one: their values never enter a product
-                if (r >= nr) *reinterpret_cast<uint4 *>(sm + st + 32768 + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_async_smem();
-            mbar_arrive(bar(kKp));
-            if (!kFullPass) continue;
-
-            uint32_t qa[8][4];
+#pragma unroll 2
+                for (int e = 0; e < 4; ++e) {   // 16-byte pieces lie at the same offsets in K and K'
+                    const int x = 512 * half + t + 128 * e, r = (x >> 3) & 63;
+                    const uint4 u = *reinterpret_cast<const uint4 *>(sm + st + 16384 + 16 * x);
+                    const float w = gv[128 + r];
+                    const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+                    uint32_t o0[4], o1[4], o2[4];
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                ldsm_x4(sb + st + sw(16 * I + (lane & 15), 16 * kk + ((lane >> 4) << 3)), qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3]);
-            const int r0 = 16 * I + g;
-            const float gh0 = gv[r0], gh1 = gv[r0 + 8], gl0 = gv[64 + r0], gl1 = gv[64 + r0 + 8];
-            ok = k == 0 || wait(kOFull, k - 1);   // the previous chunk's P is consumed
+                    for (int c = 0; c < 4; ++c) {
+                        float2 y = __fmul2_rn(unpack_bf16(r < nr ? uw[c] : 0u), make_float2(w, w));
+                        o0[c] = take_bf16(y);
+                        o1[c] = take_bf16(y);
+                        o2[c] = pack_bf16(y.x, y.y);
+                    }
+                    uint4 *to = reinterpret_cast<uint4 *>(sm + OFF_KP + 16 * x);
+                    to[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+                    to[1024] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+                    to[2048] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+                    // rows past the sequence belong to another one: their values never enter a product
+                    if (r >= nr) *reinterpret_cast<uint4 *>(sm + st + 32768 + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_async_smem();
+                mbar_arrive(bar(kKp));
+            }
+            if (!kFullPass || k == (half ? chunks : 0)) continue;
+            ok = k == 0 || wait(kOFull, k - 1);   // the previous chunk's outputs are there, its P is consumed
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
             }
-            for (int J = 0; J <= I; ++J) {
-                float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            if (half == 0) {
+                tc_fence_after();
+                const float *eg = gslot(k - 1) + 192;
+                const int64_t t0 = first + (int64_t)(k - 1) * C;
+                const int nr = eos - t0 < C ? (int)(eos - t0) : C;
+                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + ((t0 + odd) * H + h) * a.dv + (jl & ~1);
+                int rows = jl < a.dv ? nr - odd : 0;   // token c + odd is stored where c < rows
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    float v[16], w[16];
+                    tmem_ld16x2(trow + TM_OI + 16 * b, trow + TM_OJ + 16 * b, v, w);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    uint32_t b0, b1, b2, b3;
-                    ldsm_x4(sb + st + 16384 + sw(16 * J + (lane & 7) + ((lane >> 4) << 3), 16 * kk + (((lane >> 3) & 1) << 3)), b0, b1, b2, b3);
-                    mma_16816(acc[0], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b0, b1);
-                    mma_16816(acc[1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b2, b3);
+                    for (int c = 0; c < 16; c += 2) {
+                        const float2 e2 = *reinterpret_cast<const float2 *>(eg + 16 * b + c);
+                        const float2 y = __ffma2_rn(e2, make_float2(v[c], v[c + 1]), make_float2(w[c], w[c + 1]));
+                        const uint32_t x = pack_bf16(y.x, y.y);
+                        const uint32_t z = __byte_perm(x, __shfl_xor_sync(0xffffffffu, x, 1), sel);
+                        if (c < rows) *reinterpret_cast<uint32_t *>(o) = z;
+                        o += two;
+                    }
+                    rows -= 16;
                 }
+                tc_fence_before();
+                mbar_arrive(bar(kOEmpty));
+            } else {
+                const int64_t left = eos - (first + (int64_t)k * C);
+                const int nr = left < C ? (int)left : C;
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part) {
+                    const int I = part ? Ib : Ia, c0 = part ? cb : ca;
+                    float acc[3][4];
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const int j = 16 * J + 8 * nt + 2 * t4;
-                    const float2 hj = *reinterpret_cast<const float2 *>(gv + j), lj = *reinterpret_cast<const float2 *>(gv + 64 + j);
+                    for (int b = 0; b < 3; ++b)
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const int i = r0 + 8 * hh;
-                        const float gh = hh ? gh1 : gh0, gl = hh ? gl1 : gl0;
-                        float2 x;
-                        x.x = j <= i && j < nr ? acc[nt][2 * hh] * ex2((gh - hj.x) + (gl - lj.x)) : 0.f;
-                        x.y = j + 1 <= i && j + 1 < nr ? acc[nt][2 * hh + 1] * ex2((gh - hj.y) + (gl - lj.y)) : 0.f;
-                        const uint32_t at = OFF_P + sw(i, j);
-                        *reinterpret_cast<uint32_t *>(sm + at) = take_bf16(x);
-                        *reinterpret_cast<uint32_t *>(sm + at + 8192) = pack_bf16(x.x, x.y);
+                        for (int e = 0; e < 4; ++e) acc[b][e] = 0.f;
+                    const uint32_t qrow = sb + st + (16 * I + (lane & 15)) * 128, krow = sb + st + 16384 + (8 * c0 + (lane & 7)) * 128;
+#pragma unroll 1
+                    for (int kk = 0; kk < 4; ++kk) {   // 32 channels: 16-byte pieces 4 kk .. 4 kk + 3 of a row's halves
+                        const uint32_t hf = (kk >> 1) * 8192, pc = 4 * (kk & 1);
+                        uint32_t q0[4], q1[4];
+                        ldsm_x4(qrow + hf + (((pc + (lane >> 4)) ^ (lane & 7)) << 4), q0[0], q0[1], q0[2], q0[3]);
+                        ldsm_x4(qrow + hf + (((pc + 2 + (lane >> 4)) ^ (lane & 7)) << 4), q1[0], q1[1], q1[2], q1[3]);
+                        const uint32_t ka = krow + hf + (((pc + (lane >> 3)) ^ (lane & 7)) << 4);
+#pragma unroll
+                        for (int b = 0; b < 3; ++b) {
+                            if (b == 2 && part) continue;
+                            uint32_t b0, b1, b2, b3;
+                            ldsm_x4(ka + 1024 * b, b0, b1, b2, b3);
+                            mma_16816(acc[b], q0[0], q0[1], q0[2], q0[3], b0, b1);
+                            mma_16816(acc[b], q1[0], q1[1], q1[2], q1[3], b2, b3);
+                        }
+                    }
+                    const int i = 16 * I + g;
+                    const int m0 = i < nr ? i : nr - 1, m1 = i + 8 < nr ? i + 8 : nr - 1;   // the last key of each row
+                    const float2 gh0 = make_float2(gv[i], gv[i]), gh1 = make_float2(gv[i + 8], gv[i + 8]);
+                    const float2 gl0 = make_float2(gv[64 + i], gv[64 + i]), gl1 = make_float2(gv[72 + i], gv[72 + i]);
+                    const float2 neg = make_float2(-1.f, -1.f);
+#pragma unroll
+                    for (int b = 0; b < 3; ++b) {
+                        if (b == 2 && part) continue;
+                        const int j = 8 * (c0 + b) + 2 * t4;
+                        const float2 hj = *reinterpret_cast<const float2 *>(gv + j), lj = *reinterpret_cast<const float2 *>(gv + 64 + j);
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            const float2 d = __fadd2_rn(__ffma2_rn(hj, neg, hh ? gh1 : gh0), __ffma2_rn(lj, neg, hh ? gl1 : gl0));
+                            float2 x = __fmul2_rn(make_float2(acc[b][2 * hh], acc[b][2 * hh + 1]), make_float2(ex2(d.x), ex2(d.y)));
+                            const int m = hh ? m1 : m0;
+                            x = make_float2(j <= m ? x.x : 0.f, j < m ? x.y : 0.f);
+                            const uint32_t at = OFF_P + sw(i + 8 * hh, j);
+                            *reinterpret_cast<uint32_t *>(sm + at) = take_bf16(x);
+                            *reinterpret_cast<uint32_t *>(sm + at + 8192) = pack_bf16(x.x, x.y);
+                        }
                     }
                 }
+                fence_async_smem();
+                mbar_arrive(bar(kP));
             }
-            fence_async_smem();
-            mbar_arrive(bar(kP));
         }
-    } else if (warp == 16) {
-        // ---- tiles by TMA, and the decay sums: lane l holds tokens 2l and 2l + 1
-        double total = 0.0;
-        auto load_g = [&](int k, double &x, double &y) {
-            const int64_t t = first + (int64_t)k * C + 2 * lane;
-            x = t < eos ? lin_log2_decay(a, t, h) : 0.0;
-            y = t + 1 < eos ? lin_log2_decay(a, t + 1, h) : 0.0;
-        };
-        double gx = 0.0, gy = 0.0;
-        if (chunks > 0) load_g(0, gx, gy);
-        for (int k = 0; k < chunks; ++k) {
-            const int s = k % kStages;
-            ok = k < kStages || wait(kEmpty + s, k / kStages - 1);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            if (lane == 0) {
-                const uint32_t st = sb + s * STAGE, b = bar(kFull + s);
-                const int tok = (int)(first + (int64_t)k * C);
-                mbar_arrive_expect_tx(b, kFullPass ? 3 * 16384 : 2 * 16384);
-                tma_load_3d(st + 16384, &tmk, b, 0, hk, tok);
-                tma_load_3d(st + 24576, &tmk, b, 64, hk, tok);
-                tma_load_3d(st + 32768, &tmv, b, 0, h, tok);
-                tma_load_3d(st + 40960, &tmv, b, 64, h, tok);
-                if (kFullPass) {
-                    tma_load_3d(st, &tmq, b, 0, hk, tok);
-                    tma_load_3d(st + 8192, &tmq, b, 64, hk, tok);
+    } else {
+        regs_dec<48>();
+        if (warp == 16) {
+            // ---- tiles by TMA, and the decay sums: lane l holds tokens 2l and 2l + 1
+            float th = 0.f, tl = 0.f;   // the part's sum
+            const float hg = a.head_g ? __ldg(a.head_g + h) : 0.f;
+            const float *gp = a.g ? a.g + (first + 2 * lane) * H + h : nullptr;
+            float gx = 0.f, gy = 0.f;
+            auto load_g = [&](int k) {
+                const int64_t t = first + (int64_t)k * C + 2 * lane;
+                gx = gp && t < eos ? __ldg(gp + (int64_t)k * C * H) : 0.f;
+                gy = gp && t + 1 < eos ? __ldg(gp + (int64_t)k * C * H + H) : 0.f;
+            };
+            // g + hg in log2 units as two floats (below -1e5 it is that: the decay is zero)
+            auto log2_decay = [&](float x, bool in, float &hi, float &lo) {
+                constexpr float kL = 1.44269502e+00f, kLl = 1.92596299e-08f;   // log2 e = kL + kLl
+                const float s = x + hg, b = s - x, e = (x - (s - b)) + (hg - b);
+                hi = s * kL;
+                lo = fmaf(s, kL, -hi) + fmaf(s, kLl, e * kL);
+                if (s < -6.9e4f) {
+                    hi = -1e5f;
+                    lo = 0.f;
                 }
+                if (!in) hi = lo = 0.f;
+            };
+            if (chunks > 0) load_g(0);
+            for (int k = 0; k < chunks; ++k) {
+                const int s = k % kStages;
+                ok = k < kStages || wait(kEmpty + s, k / kStages - 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const uint32_t st = sb + s * STAGE, b = bar(kFull + s);
+                    const int tok = (int)(first + (int64_t)k * C);
+                    mbar_arrive_expect_tx(b, kFullPass ? 3 * 16384 : 2 * 16384);
+                    tma_load_3d(st + 16384, &tmk, b, 0, hk, tok);
+                    tma_load_3d(st + 24576, &tmk, b, 64, hk, tok);
+                    tma_load_3d(st + 32768, &tmv, b, 0, h, tok);
+                    tma_load_3d(st + 40960, &tmv, b, 64, h, tok);
+                    if (kFullPass) {
+                        tma_load_3d(st, &tmq, b, 0, hk, tok);
+                        tma_load_3d(st + 8192, &tmq, b, 64, hk, tok);
+                    }
+                }
+                __syncwarp();
+                const int64_t t = first + (int64_t)k * C + 2 * lane;
+                float xh, xl, yh, yl;
+                log2_decay(gx, t < eos, xh, xl);
+                log2_decay(gy, t + 1 < eos, yh, yl);
+                if (k + 1 < chunks) load_g(k + 1);
+                float bh = xh, bl = xl;            // sums up to the lane's second token
+                add2f(bh, bl, yh, yl);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float ph = __shfl_up_sync(0xffffffffu, bh, o), pl = __shfl_up_sync(0xffffffffu, bl, o);
+                    if (lane >= o) add2f(bh, bl, ph, pl);
+                }
+                float ah = __shfl_up_sync(0xffffffffu, bh, 1), al = __shfl_up_sync(0xffffffffu, bl, 1);
+                if (lane == 0) ah = al = 0.f;
+                add2f(ah, al, xh, xl);             // and up to its first
+                const float eh = __shfl_sync(0xffffffffu, bh, 31), el = __shfl_sync(0xffffffffu, bl, 31);
+                float *gv = gslot(k);
+                reinterpret_cast<float2 *>(gv)[lane] = make_float2(ah, bh);
+                reinterpret_cast<float2 *>(gv + 64)[lane] = make_float2(al, bl);
+                reinterpret_cast<float2 *>(gv + 128)[lane] = make_float2(exp2f((eh - ah) + (el - al)), exp2f((eh - bh) + (el - bl)));
+                reinterpret_cast<float2 *>(gv + 192)[lane] = make_float2(exp2f(ah + al), exp2f(bh + bl));
+                if (lane == 0) gv[256] = exp2f(eh + el);
+                if (!kFullPass) add2f(th, tl, eh, el);
+                mbar_arrive(bar(kG + k % kGRing));
             }
-            __syncwarp();
-            const double x = gx, y = gy;
-            if (k + 1 < chunks) load_g(k + 1, gx, gy);
-            double G1 = x + y;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double z = __shfl_up_sync(0xffffffffu, G1, o);
-                if (lane >= o) G1 += z;
-            }
-            const double G0 = __shfl_up_sync(0xffffffffu, G1, 1);
-            const double Ga = (lane ? G0 : 0.0) + x;
-            const double last = __shfl_sync(0xffffffffu, G1, 31);
-            float *gv = gslot(k);
-            const float2 hi = make_float2((float)Ga, (float)G1);
-            reinterpret_cast<float2 *>(gv)[lane] = hi;
-            reinterpret_cast<float2 *>(gv + 64)[lane] = make_float2((float)(Ga - (double)hi.x), (float)(G1 - (double)hi.y));
-            reinterpret_cast<float2 *>(gv + 128)[lane] = make_float2(exp2f((float)(last - Ga)), exp2f((float)(last - G1)));
-            reinterpret_cast<float2 *>(gv + 192)[lane] = make_float2(exp2f(hi.x), exp2f(hi.y));
-            if (lane == 0) gv[256] = exp2f((float)last);
-            total += last;
-            mbar_arrive(bar(kG + k % kGRing));
-        }
-        if (!kFullPass && lane == 0) decays[p * units + unit] = total;
-    } else if (lane == 0) {
-        // ---- tensor-core products
-        const uint64_t dsm = sdesc_sw128(sb);
-        const uint64_t kpd = sdesc_sw128_mn(sb + OFF_KP, 8192, 1024);
-        for (int k = 0; k < chunks; ++k) {
-            const int s = k % kStages;
-            const uint32_t st = s * STAGE;
-            const uint64_t vd = sdesc_sw128_mn(sb + st + 32768, 8192, 1024);
-            ok = wait(kFull + s, k / kStages) && wait(kReady, k) && wait(kKp, k);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int e = 0; e < 3; ++e)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_f16_ss(tmem + TM_S, vd + ((2048 * kk) >> 4), kpd + ((16384 * e + 2048 * kk) >> 4), IDESC_KV, 1);
-            mma_commit(bar(kDone));
-            if (kFullPass) {
-                ok = k == 0 || wait(kOEmpty, k - 1);
+            if (!kFullPass && lane == 0) decays[p * units + unit] = (double)th + (double)tl;
+        } else if (warp == 17 && lane == 0) {
+            // ---- tensor-core products
+            const uint64_t dsm = sdesc_sw128(sb);
+            const uint64_t kpd = sdesc_sw128_mn(sb + OFF_KP, 8192, 1024);
+            for (int k = 0; k < chunks; ++k) {
+                const int s = k % kStages;
+                const uint32_t st = s * STAGE;
+                const uint64_t vd = sdesc_sw128_mn(sb + st + 32768, 8192, 1024);
+                // dS of two chunks ago was taken before the S warps got ready for the chunk before
+                ok = wait(kFull + s, k / kStages) && wait(kKp, k) && (kFullPass || wait(kReady, k));
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_f16_ts(tmem + TM_OI, tmem + TM_S16 + 128 * (k & 1) + 64 * e + 8 * kk,
-                                   dsm + ((st + (kk >> 2) * 8192 + (kk & 3) * 32) >> 4), IDESC_SQ, e + kk > 0);
-                ok = wait(kP, k);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int e = 2; e >= 0; --e)   // the smallest terms first
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f16_ss(tmem + TM_OJ, vd + ((2048 * kk) >> 4), dsm + ((OFF_P + 8192 * e + 32 * kk) >> 4), IDESC_VP, e + kk > 0);
-                mma_commit(bar(kOFull));
+                        mma_f16_ss(tmem + TM_DS + 128 * (k & 1), vd + ((2048 * kk) >> 4), kpd + ((16384 * e + 2048 * kk) >> 4), IDESC_KV,
+                                   e < 2 || kk > 0);
+                mma_commit(bar(kDone + (k & 1)));
+                if (kFullPass) {
+                    ok = wait(kReady, k) && (k == 0 || wait(kOEmpty, k - 1));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_f16_ts(tmem + TM_OI, tmem + TM_S16 + 64 * e + 8 * kk,
+                                       dsm + ((st + (kk >> 2) * 8192 + (kk & 3) * 32) >> 4), IDESC_SQ, e + kk > 0);
+                    ok = wait(kP, k);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16_ss(tmem + TM_OJ, vd + ((2048 * kk) >> 4), dsm + ((OFF_P + 8192 * e + 32 * kk) >> 4), IDESC_VP, e + kk > 0);
+                    mma_commit(bar(kOFull));
+                }
+                mma_commit(bar(kEmpty + s));
             }
-            mma_commit(bar(kEmpty + s));
+            // nothing arrives at a barrier after the CTA has ended
+            for (int k = chunks > kStages ? chunks - kStages : 0; ok && k < chunks; ++k) ok = wait(kEmpty + k % kStages, k / kStages);
         }
-        // nothing arrives at a barrier after the CTA has ended
-        for (int k = chunks > kStages ? chunks - kStages : 0; ok && k < chunks; ++k) ok = wait(kEmpty + k % kStages, k / kStages);
     }
     __syncwarp();
     if (!ok) s_fail = 1;

@@ -418,8 +418,8 @@ const char *kda_status_string(kda_status_t status);
  * ------------------------------------------------------------------------------------------ */
 
 /* Dimensions of the linear-attention calls.  batch, seqlen, num_seqs, heads, dk, dv and dtype as
- * in kda_dims_t; q and k have qk_heads heads, a divisor of `heads`: head h reads q and k of head
- * h / (heads / qk_heads). */
+ * in kda_dims_t (heads at most 2^17); q and k have qk_heads heads, a divisor of `heads`: head h reads
+ * q and k of head h / (heads / qk_heads). */
 typedef struct {
     int32_t batch;
     int32_t seqlen;

@@ -13,7 +13,7 @@ bool dtype_ok(kda_dtype_t t) { return t == KDA_F32 || t == KDA_BF16; }
 kda_status_t check_lin_dims(const kda_lin_dims_t *d) {
     if (d == nullptr) return KDA_ERR_NULL;
     if (!dtype_ok(d->dtype) || !head_size_ok(d->dk) || !head_size_ok(d->dv)) return KDA_ERR_UNSUPPORTED;
-    if (d->heads <= 0 || d->qk_heads <= 0 || d->heads % d->qk_heads != 0 || d->num_seqs <= 0) return KDA_ERR_SHAPE;
+    if (d->heads <= 0 || d->qk_heads <= 0 || d->heads % d->qk_heads != 0 || d->heads > (1 << 17) || d->num_seqs <= 0) return KDA_ERR_SHAPE;
     return KDA_OK;
 }
 

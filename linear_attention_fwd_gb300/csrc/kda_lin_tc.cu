@@ -21,8 +21,8 @@
 // CTA-wide barrier inside the loop.
 //   warps 0-7    S: the state (64 key channels of one value channel per thread); its bf16 terms to
 //                TMEM
-//   warps 8-11   half of K', then the previous chunk's outputs from TMEM to global memory
-//   warps 12-15  half of K', then P (scores by mma.sync, decays and bf16 terms on the fragments)
+//   warps 8-15   K', the scores (mma.sync), the previous chunk's outputs from TMEM to global memory,
+//                P (decays and bf16 terms on the scores' fragments)
 //   warp 16      TMA of the tiles, three chunks ahead, and the decay sums
 //   warp 17      issues the tensor-core products
 // Per chunk the tensor pipe runs (1) 12 x M128 N128 K16, (2) 16 x M128 N64 K16, (3) 8 x M128 N64
@@ -52,7 +52,8 @@ constexpr uint32_t STAGE = 3 * 16384;                       // Q, K, V tiles [64
 constexpr uint32_t OFF_KP = kStages * STAGE;                // K': three terms [64][128] bf16, same layout
 constexpr uint32_t OFF_P = OFF_KP + 3 * 16384;              // P: two terms [64 i][64 j] bf16
 constexpr uint32_t OFF_G = OFF_P + 2 * 8192;                // decay vectors, kGRing slots
-constexpr uint32_t G_SLOT = 4 * 64 * 4 + 16;                //   G hi, G lo, e^{G_63 - G}, e^G; e^{G_63}
+constexpr uint32_t G_SLOT = 5 * 64 * 4 + 16;                //   G hi, G lo, e^{G_63 - G} as bf16 terms (two words a
+                                                            //   token: first and second, third twice), e^G; e^{G_63}
 constexpr uint32_t OFF_BAR = OFF_G + kGRing * G_SLOT;
 // A wait names a phase by its parity, so no barrier may complete a phase before every waiter has
 // passed the one before.  That holds because each phase needs, directly or through others, an
@@ -81,11 +82,6 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Byte offset of element (row, col) in a 128-byte-swizzled tile of 64 rows, 64-column halves 8 KB apart.
-__device__ __forceinline__ uint32_t sw(int row, int col) {
-    return (uint32_t)((col >> 6) * 8192 + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4) + ((col & 7) << 1));
-}
-
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -98,6 +94,41 @@ __device__ __forceinline__ void add2f(float &h, float &l, float x, float y) {
     const float s = h + x, b = s - h;
     l += y + ((h - (s - b)) + (x - b));
     h = s;
+}
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) { return *reinterpret_cast<__nv_bfloat162 *>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t *>(&x); }
+
+// ldmatrix at a constant offset from an address
+template <int OFF> __device__ __forceinline__ void ldsm_x4_at(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr), "n"(OFF));
+}
+
+// Scores of 16 query rows (from qa) against three blocks of 8 keys (from ka) over 32 channels: the
+// KK-th such step.  A row's 16-byte pieces are 128-byte swizzled, halves of 64 channels 8 KB apart.
+template <int KK> __device__ __forceinline__ void scores_step(uint32_t qa, uint32_t ka, float (&acc)[3][4]) {
+    constexpr int H = (KK >> 1) * 8192, X = 64 * (KK & 1);
+    uint32_t q0[4], q1[4], k0[4], k1[4], k2[4];
+    ldsm_x4_at<H>(qa ^ X, q0);
+    ldsm_x4_at<H>(ka ^ X, k0);
+    ldsm_x4_at<H + 1024>(ka ^ X, k1);
+    ldsm_x4_at<H + 2048>(ka ^ X, k2);
+    ldsm_x4_at<H>(qa ^ X ^ 32, q1);
+    mma_16816(acc[0], q0[0], q0[1], q0[2], q0[3], k0[0], k0[1]);
+    mma_16816(acc[1], q0[0], q0[1], q0[2], q0[3], k1[0], k1[1]);
+    mma_16816(acc[2], q0[0], q0[1], q0[2], q0[3], k2[0], k2[1]);
+    mma_16816(acc[0], q1[0], q1[1], q1[2], q1[3], k0[2], k0[3]);
+    mma_16816(acc[1], q1[0], q1[1], q1[2], q1[3], k1[2], k1[3]);
+    mma_16816(acc[2], q1[0], q1[1], q1[2], q1[3], k2[2], k2[3]);
+}
+
+// w as three bf16 terms: the first | the second << 16, the third twice
+__device__ __forceinline__ uint2 three_bf16(float w) {
+    const float a = __bfloat162float(__float2bfloat16_rn(w)), b = __bfloat162float(__float2bfloat16_rn(w - a));
+    const float c = (w - a) - b;
+    return make_uint2(pack_bf16(a, b), pack_bf16(c, c));
 }
 
 // x as a bf16 pair and the rest it leaves
@@ -144,12 +175,12 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
         }
         for (int s = 0; s < kGRing; ++s) mbar_init(bar(kG + s), 32);
         mbar_init(bar(kKp), 256);
-        mbar_init(bar(kP), 128);
+        mbar_init(bar(kP), 256);
         mbar_init(bar(kReady), 256);
         mbar_init(bar(kDone), 1);
         mbar_init(bar(kDone + 1), 1);
         mbar_init(bar(kOFull), 1);
-        mbar_init(bar(kOEmpty), 128);
+        mbar_init(bar(kOEmpty), 256);
         fence_mbar_init();
     }
     if (warp == 17) {
@@ -199,7 +230,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                     break;
                 }
                 tc_fence_after();
-                const float dec = gslot(k - 1)[256];
+                const float dec = gslot(k - 1)[320];
                 const float2 d2 = make_float2(dec, dec);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
@@ -244,44 +275,68 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
             for (int c = 0; c < 64; ++c) to[(int64_t)c * a.dv] = v[c];
         }
     } else if (warp < 16) {
-        // ---- K' (each of the two halves of these warps half of it), then the halves' own work
+        // ---- K', P and O, each of the two halves of these warps half of it
         regs_dec<88>();
         const int half = (warp - 8) >> 2, t = tid & 127;
-        // O: tokens as columns, this thread's value channel.  Lanes 2c and 2c + 1 exchange halves so that
+        // O: 32 tokens as columns, this thread's value channel.  Lanes 2c and 2c + 1 exchange halves so that
         // each stores channel pairs of every other token.
         const int odd = lane & 1;
         const uint32_t sel = odd ? 0x3276u : 0x5410u;
-        const int64_t two = 2 * (int64_t)H * a.dv;   // two tokens
-        // P: 20 blocks of 16 x 8 on or below the diagonal, five a warp, two of them on it: three of row
-        // block I from c0, then two
+        const uint32_t tok_bytes = (uint32_t)H * a.dv * 2;
+        const uint32_t o_off = (32 * half + odd) * tok_bytes + (jl & ~1) * 2;
+        // P: 20 blocks of 16 x 8 on or below the diagonal: the first half's warps take three of row block
+        // I from c0, the second's two, so that each has at most two on the diagonal's 16 tokens
         const int w4 = warp & 3, g = lane >> 2, t4 = lane & 3;
-        const int Ia = w4 < 2 ? 3 : 2, ca = w4 & 1 ? 3 : 0;
-        const int Ib = w4 == 0 ? 0 : (w4 == 2 ? 3 : 1), cb = w4 == 1 ? 2 : (w4 == 2 ? 6 : 0);
+        const int I = half ? (w4 == 0 ? 0 : (w4 == 2 ? 3 : 1)) : (w4 < 2 ? 3 : 2);
+        const int c0 = half ? (w4 == 1 ? 2 : (w4 == 2 ? 6 : 0)) : (w4 & 1 ? 3 : 0);
+        const int i = 16 * I + g;
+        const uint32_t qrow = sb + (16 * I + (lane & 15)) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+        const uint32_t krow = sb + 16384 + (8 * c0 + (lane & 7)) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
+        uint8_t *prow = sm + OFF_P + i * 128 + 4 * t4;
         for (int k = 0; k <= chunks; ++k) {
             const uint32_t st = (k % kStages) * STAGE;
             const float *gv = gslot(k);
+            const int64_t left = eos - (first + (int64_t)k * C);
+            const int nr = left < C ? (int)left : C;
+            float acc[3][4];
             if (k < chunks) {
-                const int64_t left = eos - (first + (int64_t)k * C);
-                const int nr = left < C ? (int)left : C;
                 // the tile and its decays landed, K' of the chunk before consumed
                 ok = wait(kFull + k % kStages, k / kStages) && wait(kG + k % kGRing, k / kGRing) && (k == 0 || done(k - 1));
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
-#pragma unroll 2
-                for (int e = 0; e < 4; ++e) {   // 16-byte pieces lie at the same offsets in K and K'
+                // K' = k w in packed bf16 arithmetic.  The factor comes as three bf16 terms; k w_0 = h + e and
+                // k w_1 = y + y' exactly (8-bit times 8-bit significands), m = e + y rounded, and the third
+                // term is what that rounding left plus y' + k w_2: the sum of the three is within 2^-22
+                // (2^-26 RMS) of k w.  16-byte pieces lie at the same offsets in K and K'.  (Loads come before
+                // stores here and below: the compiler keeps their order, and a load behind a store waits its
+                // whole way.)
+                uint4 uk[4];
+                uint2 wk[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int x = 512 * half + t + 128 * e;
+                    uk[e] = *reinterpret_cast<const uint4 *>(sm + st + 16384 + 16 * x);
+                    wk[e] = reinterpret_cast<const uint2 *>(gv + 128)[(x >> 3) & 63];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
                     const int x = 512 * half + t + 128 * e, r = (x >> 3) & 63;
-                    const uint4 u = *reinterpret_cast<const uint4 *>(sm + st + 16384 + 16 * x);
-                    const float w = gv[128 + r];
-                    const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+                    const __nv_bfloat162 w0 = as_bf162(__byte_perm(wk[e].x, 0, 0x1010)), w1 = as_bf162(__byte_perm(wk[e].x, 0, 0x3232)),
+                                         w2 = as_bf162(wk[e].y);
+                    const uint32_t uw[4] = {uk[e].x, uk[e].y, uk[e].z, uk[e].w};
                     uint32_t o0[4], o1[4], o2[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        float2 y = __fmul2_rn(unpack_bf16(r < nr ? uw[c] : 0u), make_float2(w, w));
-                        o0[c] = take_bf16(y);
-                        o1[c] = take_bf16(y);
-                        o2[c] = pack_bf16(y.x, y.y);
+                        const __nv_bfloat162 kv = as_bf162(r < nr ? uw[c] : 0u);
+                        const __nv_bfloat162 hh = __hmul2_rn(kv, w0), ee = __hfma2(kv, w0, __hneg2(hh));
+                        const __nv_bfloat162 yy = __hmul2_rn(kv, w1), ye = __hfma2(kv, w1, __hneg2(yy));
+                        const __nv_bfloat162 mm = __hadd2_rn(ee, yy);
+                        const __nv_bfloat162 ll = __hadd2_rn(__hsub2_rn(yy, __hsub2_rn(mm, ee)), __hfma2(kv, w2, ye));
+                        o0[c] = as_u32(hh);
+                        o1[c] = as_u32(mm);
+                        o2[c] = as_u32(ll);
                     }
                     uint4 *to = reinterpret_cast<uint4 *>(sm + OFF_KP + 16 * x);
                     to[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
@@ -292,85 +347,81 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 }
                 fence_async_smem();
                 mbar_arrive(bar(kKp));
-            }
-            if (!kFullPass || k == (half ? chunks : 0)) continue;
-            ok = k == 0 || wait(kOFull, k - 1);   // the previous chunk's outputs are there, its P is consumed
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            if (half == 0) {
-                tc_fence_after();
-                const float *eg = gslot(k - 1) + 192;
-                const int64_t t0 = first + (int64_t)(k - 1) * C;
-                const int nr = eos - t0 < C ? (int)(eos - t0) : C;
-                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + ((t0 + odd) * H + h) * a.dv + (jl & ~1);
-                int rows = jl < a.dv ? nr - odd : 0;   // token c + odd is stored where c < rows
-#pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    float v[16], w[16];
-                    tmem_ld16x2(trow + TM_OI + 16 * b, trow + TM_OJ + 16 * b, v, w);
+                if (kFullPass) {   // scores, 32 channels at a time (the second half's third block is not used)
 #pragma unroll
-                    for (int c = 0; c < 16; c += 2) {
-                        const float2 e2 = *reinterpret_cast<const float2 *>(eg + 16 * b + c);
-                        const float2 y = __ffma2_rn(e2, make_float2(v[c], v[c + 1]), make_float2(w[c], w[c + 1]));
-                        const uint32_t x = pack_bf16(y.x, y.y);
-                        const uint32_t z = __byte_perm(x, __shfl_xor_sync(0xffffffffu, x, 1), sel);
-                        if (c < rows) *reinterpret_cast<uint32_t *>(o) = z;
-                        o += two;
+                    for (int b = 0; b < 3; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[b][e] = 0.f;
+                    scores_step<0>(qrow + st, krow + st, acc);
+                    scores_step<1>(qrow + st, krow + st, acc);
+                    scores_step<2>(qrow + st, krow + st, acc);
+                    scores_step<3>(qrow + st, krow + st, acc);
+                }
+            }
+            if (!kFullPass) continue;
+            if (k > 0) {   // the previous chunk's outputs; its P is consumed
+                ok = wait(kOFull, k - 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float *eg = gslot(k - 1) + 256 + 32 * half;
+                const int64_t t0 = first + (int64_t)(k - 1) * C;
+                const int64_t past = eos - t0 - odd - 32 * half;
+                uint8_t *o = static_cast<uint8_t *>(a.out) + (t0 * H + h) * a.dv * 2;   // the tile; offsets stay below 2^32
+                uint32_t off = o_off;
+                int rows = jl < a.dv ? (past < 32 ? (int)past : 32) : 0;   // this lane's token c + odd is stored where c < rows
+#pragma unroll 1
+                for (int b = 0; b < 2; ++b) {
+                    float v[16], w[16];
+                    uint32_t x[8];
+                    tmem_ld16x2(trow + TM_OI + 32 * half + 16 * b, trow + TM_OJ + 32 * half + 16 * b, v, w);
+#pragma unroll
+                    for (int c = 0; c < 16; c += 4) {
+                        const float4 e4 = *reinterpret_cast<const float4 *>(eg + 16 * b + c);
+                        const float2 y0 = __ffma2_rn(make_float2(e4.x, e4.y), make_float2(v[c], v[c + 1]), make_float2(w[c], w[c + 1]));
+                        const float2 y1 = __ffma2_rn(make_float2(e4.z, e4.w), make_float2(v[c + 2], v[c + 3]), make_float2(w[c + 2], w[c + 3]));
+                        x[c / 2] = pack_bf16(y0.x, y0.y);
+                        x[c / 2 + 1] = pack_bf16(y1.x, y1.y);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) x[c] = __byte_perm(x[c], __shfl_xor_sync(0xffffffffu, x[c], 1), sel);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        if (2 * c < rows) *reinterpret_cast<uint32_t *>(o + off) = x[c];
+                        off += 2 * tok_bytes;
                     }
                     rows -= 16;
                 }
                 tc_fence_before();
                 mbar_arrive(bar(kOEmpty));
-            } else {
-                const int64_t left = eos - (first + (int64_t)k * C);
-                const int nr = left < C ? (int)left : C;
-#pragma unroll 1
-                for (int part = 0; part < 2; ++part) {
-                    const int I = part ? Ib : Ia, c0 = part ? cb : ca;
-                    float acc[3][4];
+            }
+            if (k < chunks) {   // P
+                const int m0 = i < nr ? i : nr - 1, m1 = i + 8 < nr ? i + 8 : nr - 1;   // the last key of each row
+                const float2 gh0 = make_float2(gv[i], gv[i]), gh1 = make_float2(gv[i + 8], gv[i + 8]);
+                const float2 gl0 = make_float2(gv[64 + i], gv[64 + i]), gl1 = make_float2(gv[72 + i], gv[72 + i]);
+                const float2 neg = make_float2(-1.f, -1.f);
+                float2 hj[3], lj[3];
 #pragma unroll
-                    for (int b = 0; b < 3; ++b)
+                for (int b = 0; b < 3; ++b) {
+                    const int j = (8 * (c0 + b) + 2 * t4) & 63;
+                    hj[b] = *reinterpret_cast<const float2 *>(gv + j);
+                    lj[b] = *reinterpret_cast<const float2 *>(gv + 64 + j);
+                }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[b][e] = 0.f;
-                    const uint32_t qrow = sb + st + (16 * I + (lane & 15)) * 128, krow = sb + st + 16384 + (8 * c0 + (lane & 7)) * 128;
-#pragma unroll 1
-                    for (int kk = 0; kk < 4; ++kk) {   // 32 channels: 16-byte pieces 4 kk .. 4 kk + 3 of a row's halves
-                        const uint32_t hf = (kk >> 1) * 8192, pc = 4 * (kk & 1);
-                        uint32_t q0[4], q1[4];
-                        ldsm_x4(qrow + hf + (((pc + (lane >> 4)) ^ (lane & 7)) << 4), q0[0], q0[1], q0[2], q0[3]);
-                        ldsm_x4(qrow + hf + (((pc + 2 + (lane >> 4)) ^ (lane & 7)) << 4), q1[0], q1[1], q1[2], q1[3]);
-                        const uint32_t ka = krow + hf + (((pc + (lane >> 3)) ^ (lane & 7)) << 4);
+                for (int b = 0; b < 3; ++b) {
+                    if (b == 2 && half) continue;
+                    const int j = 8 * (c0 + b) + 2 * t4;
+                    uint8_t *to = prow + (((c0 + b) ^ g) << 4);
 #pragma unroll
-                        for (int b = 0; b < 3; ++b) {
-                            if (b == 2 && part) continue;
-                            uint32_t b0, b1, b2, b3;
-                            ldsm_x4(ka + 1024 * b, b0, b1, b2, b3);
-                            mma_16816(acc[b], q0[0], q0[1], q0[2], q0[3], b0, b1);
-                            mma_16816(acc[b], q1[0], q1[1], q1[2], q1[3], b2, b3);
-                        }
-                    }
-                    const int i = 16 * I + g;
-                    const int m0 = i < nr ? i : nr - 1, m1 = i + 8 < nr ? i + 8 : nr - 1;   // the last key of each row
-                    const float2 gh0 = make_float2(gv[i], gv[i]), gh1 = make_float2(gv[i + 8], gv[i + 8]);
-                    const float2 gl0 = make_float2(gv[64 + i], gv[64 + i]), gl1 = make_float2(gv[72 + i], gv[72 + i]);
-                    const float2 neg = make_float2(-1.f, -1.f);
-#pragma unroll
-                    for (int b = 0; b < 3; ++b) {
-                        if (b == 2 && part) continue;
-                        const int j = 8 * (c0 + b) + 2 * t4;
-                        const float2 hj = *reinterpret_cast<const float2 *>(gv + j), lj = *reinterpret_cast<const float2 *>(gv + 64 + j);
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
-                            const float2 d = __fadd2_rn(__ffma2_rn(hj, neg, hh ? gh1 : gh0), __ffma2_rn(lj, neg, hh ? gl1 : gl0));
-                            float2 x = __fmul2_rn(make_float2(acc[b][2 * hh], acc[b][2 * hh + 1]), make_float2(ex2(d.x), ex2(d.y)));
-                            const int m = hh ? m1 : m0;
-                            x = make_float2(j <= m ? x.x : 0.f, j < m ? x.y : 0.f);
-                            const uint32_t at = OFF_P + sw(i + 8 * hh, j);
-                            *reinterpret_cast<uint32_t *>(sm + at) = take_bf16(x);
-                            *reinterpret_cast<uint32_t *>(sm + at + 8192) = pack_bf16(x.x, x.y);
-                        }
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const float2 d = __fadd2_rn(__ffma2_rn(hj[b], neg, hh ? gh1 : gh0), __ffma2_rn(lj[b], neg, hh ? gl1 : gl0));
+                        float2 x = __fmul2_rn(make_float2(acc[b][2 * hh], acc[b][2 * hh + 1]), make_float2(ex2(d.x), ex2(d.y)));
+                        const int m = hh ? m1 : m0;
+                        x = make_float2(j <= m ? x.x : 0.f, j < m ? x.y : 0.f);
+                        *reinterpret_cast<uint32_t *>(to + 1024 * hh) = take_bf16(x);
+                        *reinterpret_cast<uint32_t *>(to + 1024 * hh + 8192) = pack_bf16(x.x, x.y);
                     }
                 }
                 fence_async_smem();
@@ -443,9 +494,10 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 float *gv = gslot(k);
                 reinterpret_cast<float2 *>(gv)[lane] = make_float2(ah, bh);
                 reinterpret_cast<float2 *>(gv + 64)[lane] = make_float2(al, bl);
-                reinterpret_cast<float2 *>(gv + 128)[lane] = make_float2(exp2f((eh - ah) + (el - al)), exp2f((eh - bh) + (el - bl)));
-                reinterpret_cast<float2 *>(gv + 192)[lane] = make_float2(exp2f(ah + al), exp2f(bh + bl));
-                if (lane == 0) gv[256] = exp2f(eh + el);
+                const uint2 wa = three_bf16(exp2f((eh - ah) + (el - al))), wb = three_bf16(exp2f((eh - bh) + (el - bl)));
+                reinterpret_cast<uint4 *>(gv + 128)[lane] = make_uint4(wa.x, wa.y, wb.x, wb.y);
+                reinterpret_cast<float2 *>(gv + 256)[lane] = make_float2(exp2f(ah + al), exp2f(bh + bl));
+                if (lane == 0) gv[320] = exp2f(eh + el);
                 if (!kFullPass) add2f(th, tl, eh, el);
                 mbar_arrive(bar(kG + k % kGRing));
             }

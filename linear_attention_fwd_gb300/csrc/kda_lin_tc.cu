@@ -19,10 +19,10 @@
 //
 // Roles (20 warps, registers shared out by setmaxnreg).  Everything meets at mbarriers; there is no
 // CTA-wide barrier inside the loop.
-//   warps 0-7    S: the state (64 key channels of one value channel per thread); its bf16 terms to
-//                TMEM
-//   warps 8-15   K', the scores (mma.sync), the previous chunk's outputs from TMEM to global memory,
-//                P (decays and bf16 terms on the scores' fragments)
+//   warps 0-7    K', then the state (64 key channels of one value channel per thread) and its bf16
+//                terms to TMEM
+//   warps 8-15   the scores (mma.sync), the previous chunk's outputs from TMEM to global memory, P
+//                (decays and bf16 terms on the scores' fragments)
 //   warp 16      TMA of the tiles, three chunks ahead, and the decay sums
 //   warp 17      issues the tensor-core products
 // Per chunk the tensor pipe runs (1) 12 x M128 N128 K16, (2) 16 x M128 N64 K16, (3) 8 x M128 N64
@@ -82,6 +82,14 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// mbar_wait with its loop kept a loop: unrolled at every place that waits, it would push the loop
+// bodies out of the instruction cache (measured: half of the kernel's time).
+__device__ __forceinline__ bool mbar_wait_small(uint32_t bar, uint32_t parity, uint32_t limit) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < limit; ++i)
+        if (mbar_wait(bar, parity, 1)) return true;
+    return false;
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -104,6 +112,31 @@ template <int OFF> __device__ __forceinline__ void ldsm_x4_at(uint32_t addr, uin
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr), "n"(OFF));
+}
+
+// Two loads of 16 lanes x 32 columns as four 8-column fragments each (row lane / 4, columns 2 (lane % 4)
+// and the next: registers 4 c, 4 c + 1; row + 8: 4 c + 2, 4 c + 3), and one wait.
+__device__ __forceinline__ void tmem_ld_16x256b_x4_pair(uint32_t ta, uint32_t tb, float (&v)[16], float (&w)[16]) {
+    uint32_t r[16], q[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(q[0]), "=r"(q[1]), "=r"(q[2]),
+          "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]), "=r"(q[9]), "=r"(q[10]), "=r"(q[11]),
+          "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15])
+        : "r"(ta), "r"(tb)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        v[i] = __uint_as_float(r[i]);
+        w[i] = __uint_as_float(q[i]);
+    }
+}
+__device__ __forceinline__ void stsm_x4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
 }
 
 // Scores of 16 query rows (from qa) against three blocks of 8 keys (from ka) over 32 channels: the
@@ -134,7 +167,8 @@ __device__ __forceinline__ uint2 three_bf16(float w) {
 // x as a bf16 pair and the rest it leaves
 __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
     const uint32_t h = pack_bf16(x.x, x.y);
-    x = __ffma2_rn(unpack_bf16(h), make_float2(-1.f, -1.f), x);
+    x.x -= __uint_as_float(h << 16);
+    x.y -= __uint_as_float(h & 0xffff0000u);
     return h;
 }
 
@@ -171,7 +205,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
         s_fail = 0;
         for (int s = 0; s < kStages; ++s) {
             mbar_init(bar(kFull + s), 1);
-            mbar_init(bar(kEmpty + s), 1);
+            mbar_init(bar(kEmpty + s), kFullPass ? 9 : 1);   // the products, and the warps that staged outputs there
         }
         for (int s = 0; s < kGRing; ++s) mbar_init(bar(kG + s), 32);
         mbar_init(bar(kKp), 256);
@@ -197,7 +231,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int jl = 32 * (warp & 3) + lane;             // value channel of this thread's TMEM lane
     auto gslot = [&](int k) { return reinterpret_cast<float *>(sm + OFF_G + (k % kGRing) * G_SLOT); };
-    auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity & 1u, kWaitPolls); };
+    auto wait = [&](int b, uint32_t parity) { return mbar_wait_small(bar(b), parity & 1u, kWaitPolls); };
     auto done = [&](int k) { return wait(kDone + (k & 1), k >> 1); };
     bool ok = true;
 
@@ -223,12 +257,63 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
             }
         }
         for (int k = 0; k <= chunks; ++k) {
-            if (k > 0) {
-                ok = done(k - 1) && wait(kG + (k - 1) % kGRing, (k - 1) / kGRing);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
+            // dS and K' of the chunk before are done with; this chunk's tile and decays landed
+            if (k > 0) ok = done(k - 1);
+            if (ok && k < chunks) ok = wait(kFull + k % kStages, k / kStages) && wait(kG + k % kGRing, k / kGRing);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            if (k < chunks) {
+                const uint32_t st = (k % kStages) * STAGE;
+                const float *gv = gslot(k);
+                const int64_t left = eos - (first + (int64_t)k * C);
+                const int nr = left < C ? (int)left : C;
+                // K' = k w in packed bf16 arithmetic.  The factor comes as three bf16 terms; k w_0 = h + e and
+                // k w_1 = y + y' exactly (8-bit times 8-bit significands), m = e + y rounded, and the third
+                // term is what that rounding left plus y' + k w_2: the sum of the three is within 2^-22
+                // (2^-26 RMS) of k w.  16-byte pieces lie at the same offsets in K and K'.  (Loads come before
+                // stores here and below: the compiler keeps their order, and a load behind a store waits its
+                // whole way.)
+                uint4 uk[4];
+                uint2 wk[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int x = tid + 256 * e;
+                    uk[e] = *reinterpret_cast<const uint4 *>(sm + st + 16384 + 16 * x);
+                    wk[e] = reinterpret_cast<const uint2 *>(gv + 128)[(x >> 3) & 63];
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int x = tid + 256 * e, r = (x >> 3) & 63;
+                    const __nv_bfloat162 w0 = as_bf162(__byte_perm(wk[e].x, 0, 0x1010)), w1 = as_bf162(__byte_perm(wk[e].x, 0, 0x3232)),
+                                         w2 = as_bf162(wk[e].y);
+                    if (nr < C && r >= nr) {   // rows past the sequence belong to another one: they never enter a product
+                        uk[e] = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(sm + st + 32768 + 16 * x) = uk[e];
+                    }
+                    const uint32_t uw[4] = {uk[e].x, uk[e].y, uk[e].z, uk[e].w};
+                    uint32_t o0[4], o1[4], o2[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const __nv_bfloat162 kv = as_bf162(uw[c]);
+                        const __nv_bfloat162 hh = __hmul2_rn(kv, w0), ee = __hfma2(kv, w0, __hneg2(hh));
+                        const __nv_bfloat162 yy = __hmul2_rn(kv, w1), ye = __hfma2(kv, w1, __hneg2(yy));
+                        const __nv_bfloat162 mm = __hadd2_rn(ee, yy);
+                        const __nv_bfloat162 ll = __hadd2_rn(__hsub2_rn(yy, __hsub2_rn(mm, ee)), __hfma2(kv, w2, ye));
+                        o0[c] = as_u32(hh);
+                        o1[c] = as_u32(mm);
+                        o2[c] = as_u32(ll);
+                    }
+                    uint4 *to = reinterpret_cast<uint4 *>(sm + OFF_KP + 16 * x);
+                    to[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+                    to[1024] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+                    to[2048] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+                }
+                fence_async_smem();
+                mbar_arrive(bar(kKp));
+            }
+            if (k > 0) {
                 tc_fence_after();
                 const float dec = gslot(k - 1)[320];
                 const float2 d2 = make_float2(dec, dec);
@@ -275,90 +360,48 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
             for (int c = 0; c < 64; ++c) to[(int64_t)c * a.dv] = v[c];
         }
     } else if (warp < 16) {
-        // ---- K', P and O, each of the two halves of these warps half of it
+        // ---- scores, P and O, each of the two halves of these warps half of it
         regs_dec<88>();
-        const int half = (warp - 8) >> 2, t = tid & 127;
-        // O: 32 tokens as columns, this thread's value channel.  Lanes 2c and 2c + 1 exchange halves so that
-        // each stores channel pairs of every other token.
-        const int odd = lane & 1;
-        const uint32_t sel = odd ? 0x3276u : 0x5410u;
-        const uint32_t tok_bytes = (uint32_t)H * a.dv * 2;
-        const uint32_t o_off = (32 * half + odd) * tok_bytes + (jl & ~1) * 2;
+        const int half = (warp - 8) >> 2;
+        const int w4 = warp & 3, g = lane >> 2, t4 = lane & 3;
+        // O: 32 tokens x 32 channels a warp.  TMEM is read as 8 x 8 fragments (channel, token), which stmatrix
+        // turns into rows of a token's channels, 64 bytes with their 16-byte pieces swizzled.
+        const int64_t tok_bytes = (int64_t)H * a.dv * 2;
+        const uint32_t o_row = ((lane >> 4) * 8 + (lane & 7)) * 64, o_sw = (lane & 7) >> 1;
+        const uint32_t o_st[2] = {o_row + ((((lane >> 3) & 1) ^ o_sw) << 4), o_row + (((2 + ((lane >> 3) & 1)) ^ o_sw) << 4)};
+        const uint32_t o_ld = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+        const int64_t o_off = (32 * half + (lane >> 2)) * tok_bytes + (32 * w4 + 8 * (lane & 3)) * 2;
         // P: 20 blocks of 16 x 8 on or below the diagonal: the first half's warps take three of row block
         // I from c0, the second's two, so that each has at most two on the diagonal's 16 tokens
-        const int w4 = warp & 3, g = lane >> 2, t4 = lane & 3;
         const int I = half ? (w4 == 0 ? 0 : (w4 == 2 ? 3 : 1)) : (w4 < 2 ? 3 : 2);
         const int c0 = half ? (w4 == 1 ? 2 : (w4 == 2 ? 6 : 0)) : (w4 & 1 ? 3 : 0);
         const int i = 16 * I + g;
         const uint32_t qrow = sb + (16 * I + (lane & 15)) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
         const uint32_t krow = sb + 16384 + (8 * c0 + (lane & 7)) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
         uint8_t *prow = sm + OFF_P + i * 128 + 4 * t4;
-        for (int k = 0; k <= chunks; ++k) {
+        for (int k = 0; kFullPass && k <= chunks; ++k) {
             const uint32_t st = (k % kStages) * STAGE;
             const float *gv = gslot(k);
             const int64_t left = eos - (first + (int64_t)k * C);
             const int nr = left < C ? (int)left : C;
             float acc[3][4];
             if (k < chunks) {
-                // the tile and its decays landed, K' of the chunk before consumed
-                ok = wait(kFull + k % kStages, k / kStages) && wait(kG + k % kGRing, k / kGRing) && (k == 0 || done(k - 1));
+                ok = wait(kFull + k % kStages, k / kStages) && wait(kG + k % kGRing, k / kGRing);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
-                // K' = k w in packed bf16 arithmetic.  The factor comes as three bf16 terms; k w_0 = h + e and
-                // k w_1 = y + y' exactly (8-bit times 8-bit significands), m = e + y rounded, and the third
-                // term is what that rounding left plus y' + k w_2: the sum of the three is within 2^-22
-                // (2^-26 RMS) of k w.  16-byte pieces lie at the same offsets in K and K'.  (Loads come before
-                // stores here and below: the compiler keeps their order, and a load behind a store waits its
-                // whole way.)
-                uint4 uk[4];
-                uint2 wk[4];
+                // scores, 32 channels at a time (the second half's third block is not used)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int x = 512 * half + t + 128 * e;
-                    uk[e] = *reinterpret_cast<const uint4 *>(sm + st + 16384 + 16 * x);
-                    wk[e] = reinterpret_cast<const uint2 *>(gv + 128)[(x >> 3) & 63];
-                }
+                for (int b = 0; b < 3; ++b)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int x = 512 * half + t + 128 * e, r = (x >> 3) & 63;
-                    const __nv_bfloat162 w0 = as_bf162(__byte_perm(wk[e].x, 0, 0x1010)), w1 = as_bf162(__byte_perm(wk[e].x, 0, 0x3232)),
-                                         w2 = as_bf162(wk[e].y);
-                    const uint32_t uw[4] = {uk[e].x, uk[e].y, uk[e].z, uk[e].w};
-                    uint32_t o0[4], o1[4], o2[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const __nv_bfloat162 kv = as_bf162(r < nr ? uw[c] : 0u);
-                        const __nv_bfloat162 hh = __hmul2_rn(kv, w0), ee = __hfma2(kv, w0, __hneg2(hh));
-                        const __nv_bfloat162 yy = __hmul2_rn(kv, w1), ye = __hfma2(kv, w1, __hneg2(yy));
-                        const __nv_bfloat162 mm = __hadd2_rn(ee, yy);
-                        const __nv_bfloat162 ll = __hadd2_rn(__hsub2_rn(yy, __hsub2_rn(mm, ee)), __hfma2(kv, w2, ye));
-                        o0[c] = as_u32(hh);
-                        o1[c] = as_u32(mm);
-                        o2[c] = as_u32(ll);
-                    }
-                    uint4 *to = reinterpret_cast<uint4 *>(sm + OFF_KP + 16 * x);
-                    to[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-                    to[1024] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-                    to[2048] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
-                    // rows past the sequence belong to another one: their values never enter a product
-                    if (r >= nr) *reinterpret_cast<uint4 *>(sm + st + 32768 + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_async_smem();
-                mbar_arrive(bar(kKp));
-                if (kFullPass) {   // scores, 32 channels at a time (the second half's third block is not used)
-#pragma unroll
-                    for (int b = 0; b < 3; ++b)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[b][e] = 0.f;
-                    scores_step<0>(qrow + st, krow + st, acc);
-                    scores_step<1>(qrow + st, krow + st, acc);
-                    scores_step<2>(qrow + st, krow + st, acc);
-                    scores_step<3>(qrow + st, krow + st, acc);
-                }
+                    for (int e = 0; e < 4; ++e) acc[b][e] = 0.f;
+                scores_step<0>(qrow + st, krow + st, acc);
+                scores_step<1>(qrow + st, krow + st, acc);
+                scores_step<2>(qrow + st, krow + st, acc);
+                scores_step<3>(qrow + st, krow + st, acc);
             }
-            if (!kFullPass) continue;
+            const uint32_t stg = ((k + kStages - 1) % kStages) * STAGE + 2048 * (warp - 8);
             if (k > 0) {   // the previous chunk's outputs; its P is consumed
                 ok = wait(kOFull, k - 1);
                 if (!__all_sync(0xffffffffu, ok)) {
@@ -366,42 +409,30 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                     break;
                 }
                 tc_fence_after();
-                const float *eg = gslot(k - 1) + 256 + 32 * half;
-                const int64_t t0 = first + (int64_t)(k - 1) * C;
-                const int64_t past = eos - t0 - odd - 32 * half;
-                uint8_t *o = static_cast<uint8_t *>(a.out) + (t0 * H + h) * a.dv * 2;   // the tile; offsets stay below 2^32
-                uint32_t off = o_off;
-                int rows = jl < a.dv ? (past < 32 ? (int)past : 32) : 0;   // this lane's token c + odd is stored where c < rows
-#pragma unroll 1
-                for (int b = 0; b < 2; ++b) {
+                const float *eg = gslot(k - 1) + 256 + 32 * half + 2 * t4;
+                // 32 tokens x 32 channels into this warp's 2 KB of the chunk's (consumed) Q tile
+                float2 e2[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) e2[c] = *reinterpret_cast<const float2 *>(eg + 8 * c);
+#pragma unroll
+                for (int L = 0; L < 2; ++L) {   // 16 channels
                     float v[16], w[16];
+                    const uint32_t tl = trow + (L << 20) + 32 * half;
+                    tmem_ld_16x256b_x4_pair(tl + TM_OI, tl + TM_OJ, v, w);
                     uint32_t x[8];
-                    tmem_ld16x2(trow + TM_OI + 32 * half + 16 * b, trow + TM_OJ + 32 * half + 16 * b, v, w);
 #pragma unroll
-                    for (int c = 0; c < 16; c += 4) {
-                        const float4 e4 = *reinterpret_cast<const float4 *>(eg + 16 * b + c);
-                        const float2 y0 = __ffma2_rn(make_float2(e4.x, e4.y), make_float2(v[c], v[c + 1]), make_float2(w[c], w[c + 1]));
-                        const float2 y1 = __ffma2_rn(make_float2(e4.z, e4.w), make_float2(v[c + 2], v[c + 3]), make_float2(w[c + 2], w[c + 3]));
-                        x[c / 2] = pack_bf16(y0.x, y0.y);
-                        x[c / 2 + 1] = pack_bf16(y1.x, y1.y);
-                    }
+                    for (int c = 0; c < 8; ++c)
+                        x[c] = pack_bf16(fmaf(e2[c / 2].x, v[2 * c], w[2 * c]), fmaf(e2[c / 2].y, v[2 * c + 1], w[2 * c + 1]));
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) x[c] = __byte_perm(x[c], __shfl_xor_sync(0xffffffffu, x[c], 1), sel);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        if (2 * c < rows) *reinterpret_cast<uint32_t *>(o + off) = x[c];
-                        off += 2 * tok_bytes;
-                    }
-                    rows -= 16;
+                    for (int e = 0; e < 2; ++e)
+                        stsm_x4_t(sb + stg + o_st[L] + 1024 * e, x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
                 }
                 tc_fence_before();
                 mbar_arrive(bar(kOEmpty));
             }
             if (k < chunks) {   // P
                 const int m0 = i < nr ? i : nr - 1, m1 = i + 8 < nr ? i + 8 : nr - 1;   // the last key of each row
-                const float2 gh0 = make_float2(gv[i], gv[i]), gh1 = make_float2(gv[i + 8], gv[i + 8]);
-                const float2 gl0 = make_float2(gv[64 + i], gv[64 + i]), gl1 = make_float2(gv[72 + i], gv[72 + i]);
-                const float2 neg = make_float2(-1.f, -1.f);
+                const float gh0 = gv[i], gh1 = gv[i + 8], gl0 = gv[64 + i], gl1 = gv[72 + i];
                 float2 hj[3], lj[3];
 #pragma unroll
                 for (int b = 0; b < 3; ++b) {
@@ -416,16 +447,34 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                     uint8_t *to = prow + (((c0 + b) ^ g) << 4);
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
-                        const float2 d = __fadd2_rn(__ffma2_rn(hj[b], neg, hh ? gh1 : gh0), __ffma2_rn(lj[b], neg, hh ? gl1 : gl0));
-                        float2 x = __fmul2_rn(make_float2(acc[b][2 * hh], acc[b][2 * hh + 1]), make_float2(ex2(d.x), ex2(d.y)));
+                        const float gh = hh ? gh1 : gh0, gl = hh ? gl1 : gl0;
                         const int m = hh ? m1 : m0;
-                        x = make_float2(j <= m ? x.x : 0.f, j < m ? x.y : 0.f);
+                        float2 x;
+                        x.x = j <= m ? acc[b][2 * hh] * ex2((gh - hj[b].x) + (gl - lj[b].x)) : 0.f;
+                        x.y = j < m ? acc[b][2 * hh + 1] * ex2((gh - hj[b].y) + (gl - lj[b].y)) : 0.f;
                         *reinterpret_cast<uint32_t *>(to + 1024 * hh) = take_bf16(x);
                         *reinterpret_cast<uint32_t *>(to + 1024 * hh + 8192) = pack_bf16(x.x, x.y);
                     }
                 }
-                fence_async_smem();
-                mbar_arrive(bar(kP));
+            }
+            // (one fence for P and the staged outputs, whose place TMA takes next; the outputs' stores come
+            // after it, as a fence waits for what is in flight)
+            fence_async_smem();
+            if (k < chunks) mbar_arrive(bar(kP));
+            if (k > 0) {
+                __syncwarp();
+                uint4 y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = *reinterpret_cast<const uint4 *>(sm + stg + o_ld + 512 * e);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kEmpty + (k - 1) % kStages));
+                const int64_t t0 = first + (int64_t)(k - 1) * C;
+                const int64_t past = eos - t0 - 32 * half;
+                uint8_t *o = static_cast<uint8_t *>(a.out) + ((t0 * H + h) * a.dv) * 2 + o_off;
+                const int rows = 32 * w4 < a.dv ? (past < 32 ? (int)past : 32) - (lane >> 2) : 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (8 * e < rows) *reinterpret_cast<uint4 *>(o + 8 * e * tok_bytes) = y[e];
             }
         }
     } else {
@@ -556,8 +605,8 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
         // a few milliseconds for both parities), then the part's results are marked.
         if (tid == 0) {
             for (int b = 0; b < kBars; ++b) {
-                mbar_wait(bar(b), 0, 1u << 12);
-                mbar_wait(bar(b), 1, 1u << 12);
+                mbar_wait_small(bar(b), 0, 1u << 12);
+                mbar_wait_small(bar(b), 1, 1u << 12);
             }
             atomicAdd(&g_kda_lin_timeouts, 1u);
         }

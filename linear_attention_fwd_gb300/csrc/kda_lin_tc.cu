@@ -551,46 +551,68 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 mbar_arrive(bar(kG + k % kGRing));
             }
             if (!kFullPass && lane == 0) decays[p * units + unit] = (double)th + (double)tl;
-        } else if (warp == 17 && lane == 0) {
-            // ---- tensor-core products
+        } else if (warp == 17) {
+            // ---- tensor-core products.  The whole warp runs the loop and one lane issues, so that the
+            // operand descriptors are warp-uniform values made outside the issuing branches (made
+            // inside, an MMA took about 115 cycles to issue).
             const uint64_t dsm = sdesc_sw128(sb);
             const uint64_t kpd = sdesc_sw128_mn(sb + OFF_KP, 8192, 1024);
+            const uint64_t v0 = sdesc_sw128_mn(sb + 32768, 8192, 1024);
+            const uint32_t one = lane == 0;
+            int s = 0;
             for (int k = 0; k < chunks; ++k) {
-                const int s = k % kStages;
-                const uint32_t st = s * STAGE;
-                const uint64_t vd = sdesc_sw128_mn(sb + st + 32768, 8192, 1024);
+                const uint64_t vd = v0 + s * (STAGE >> 4), qd = dsm + s * (STAGE >> 4);
                 // dS of two chunks ago was taken before the S warps got ready for the chunk before
                 ok = wait(kFull + s, k / kStages) && wait(kKp, k) && (kFullPass || wait(kReady, k));
-                if (!ok) break;
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
+                const uint32_t ds = tmem + TM_DS + 128 * (k & 1);
+                if (one) {
 #pragma unroll
-                for (int e = 2; e >= 0; --e)   // the smallest terms first
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f16_ss(tmem + TM_DS + 128 * (k & 1), vd + ((2048 * kk) >> 4), kpd + ((16384 * e + 2048 * kk) >> 4), IDESC_KV,
-                                   e < 2 || kk > 0);
-                mma_commit(bar(kDone + (k & 1)));
-                if (kFullPass) {
-                    ok = wait(kReady, k) && (k == 0 || wait(kOEmpty, k - 1));
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_f16_ts(tmem + TM_OI, tmem + TM_S16 + 64 * e + 8 * kk,
-                                       dsm + ((st + (kk >> 2) * 8192 + (kk & 3) * 32) >> 4), IDESC_SQ, e + kk > 0);
-                    ok = wait(kP, k);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                    for (int e = 2; e >= 0; --e)   // the smallest terms first
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_f16_ss(tmem + TM_OJ, vd + ((2048 * kk) >> 4), dsm + ((OFF_P + 8192 * e + 32 * kk) >> 4), IDESC_VP, e + kk > 0);
-                    mma_commit(bar(kOFull));
+                            mma_f16_ss(ds, vd + ((2048 * kk) >> 4), kpd + ((16384 * e + 2048 * kk) >> 4), IDESC_KV, e < 2 || kk > 0);
+                    mma_commit(bar(kDone + (k & 1)));
                 }
-                mma_commit(bar(kEmpty + s));
+                __syncwarp();
+                if (kFullPass) {
+                    ok = wait(kReady, k) && (k == 0 || wait(kOEmpty, k - 1));
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (one) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_f16_ts(tmem + TM_OI, tmem + TM_S16 + 64 * e + 8 * kk, qd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
+                                           IDESC_SQ, e + kk > 0);
+                    }
+                    __syncwarp();
+                    ok = wait(kP, k);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (one) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_f16_ss(tmem + TM_OJ, vd + ((2048 * kk) >> 4), dsm + ((OFF_P + 8192 * e + 32 * kk) >> 4), IDESC_VP, e + kk > 0);
+                        mma_commit(bar(kOFull));
+                    }
+                }
+                if (one) mma_commit(bar(kEmpty + s));
+                __syncwarp();
+                if (++s == kStages) s = 0;
             }
             // nothing arrives at a barrier after the CTA has ended
             for (int k = chunks > kStages ? chunks - kStages : 0; ok && k < chunks; ++k) ok = wait(kEmpty + k % kStages, k / kStages);

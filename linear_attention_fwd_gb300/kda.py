@@ -8,6 +8,7 @@ the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -486,46 +487,82 @@ def kda_chunk_fwd_gated(q, k, v, g, beta, gate, norm_weight=None, eps: float = 1
 
 # ---------------------------------------------------------------------------------------------
 # Linear attention with a decay for each head, and attention over a paged key-value cache.
+#
+# A decode step's calls take a few microseconds on the GPU, so what they cost here counts: the
+# checks of all tensors are one loop, and the dimension structs (and workspace sizes) of the
+# sizes in use are kept.
 
 
-def _need(name, t, dev, dtype, shape):
-    """One required tensor: its device, type, layout and shape."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _refuse(dev, specs):
+    """Raises for the first of (name, tensor, dtype, shape) that is not a contiguous tensor of that kind
+    on CUDA device `dev`."""
+    for name, t, dtype, shape in specs:
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the CUDA device of the others, got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise AssertionError("no tensor to refuse")
 
 
-def _on_current_device(dev):
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current CUDA device, got {dev}")
+def _check_all(dev, specs):
+    for _, t, dtype, shape in specs:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous()):
+            _refuse(dev, specs)
 
 
-def _allocate(stream, *want):
-    """New tensors (shape, dtype, device), made for use on `stream`: memory that the allocator hands
-    out for another stream may still be in use there."""
+def _device_of(t) -> int:
+    """The index of t's device, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device, got {t.device}")
+    return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
     if stream is None:
-        return [torch.empty(s, dtype=t, device=d) for s, t, d in want]
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _allocate(stream, dev: int, shape, dtype):
+    """A new tensor, made for use on `stream`: memory that the allocator hands out for another stream
+    may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}" if dev else "cuda:0")
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(stream):
-        return [torch.empty(s, dtype=t, device=d) for s, t, d in want]
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+@functools.lru_cache(maxsize=1024)
+def _lin_dims(*sizes):
+    """(pointer to the struct, workspace bytes) for these sizes."""
+    p = ctypes.byref(KdaLinDims(*sizes))
+    return p, int(lib().kda_lin_chunk_fwd_workspace_bytes(p))
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_dims(*sizes):
+    p = ctypes.byref(KdaPagedDims(*sizes))
+    return p, int(lib().kda_paged_attention_workspace_bytes(p))
+
+
 def kda_lin_chunk_fwd_workspace_bytes(q, v, cu_seqlens=None) -> int:
     """Bytes of device workspace kda_lin_chunk_fwd needs for these shapes."""
     B, T, H, dv = v.shape
     n = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    dims = KdaLinDims(B, T, n, H, q.shape[2], q.shape[3], dv, _dtype_code(q.dtype))
-    return int(lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(dims)))
+    return _lin_dims(B, T, n, H, q.shape[2], q.shape[3], dv, _dtype_code(q.dtype))[1]
 
 
 def kda_lin_chunk_fwd(q, k, v, g=None, head_g=None, initial_state=None, cu_seqlens=None, *, out=None,
@@ -539,49 +576,38 @@ def kda_lin_chunk_fwd(q, k, v, g=None, head_g=None, initial_state=None, cu_seqle
     workspace: uint8 tensor of kda_lin_chunk_fwd_workspace_bytes bytes (allocated here when None).
     Returns (out [B, T, H, dv], final_state fp32 [N, H, dk, dv] or None).
     """
-    dev, dt = q.device, q.dtype
-    _on_current_device(dev)
-    code = _dtype_code(dt)
+    dev, dt, f32 = _device_of(q), q.dtype, torch.float32
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q must be [B, T, Hk, dk] and v [B, T, H, dv]")
     B, T, Hk, dk = q.shape
     H, dv = v.shape[2:]
-    _need("q", q, dev, dt, q.shape)
-    _need("k", k, dev, dt, q.shape)
-    _need("v", v, dev, dt, (B, T, H, dv))
-    if g is not None:
-        _need("g", g, dev, torch.float32, (B, T, H))
-    if head_g is not None:
-        _need("head_g", head_g, dev, torch.float32, (H,))
-    N = B
+    N, cu_shape = B, None
     if cu_seqlens is not None:
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-            raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
         N = cu_seqlens.numel() - 1
-        _need("cu_seqlens", cu_seqlens, dev, torch.int32, (N + 1,))
-    if initial_state is not None:
-        _need("initial_state", initial_state, dev, torch.float32, (N, H, dk, dv))
-    dims = KdaLinDims(B, T, N, H, Hk, dk, dv, code)
+        cu_shape = (N + 1,)
+        if N < 1:
+            raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
+    states, tokens = (N, H, dk, dv), (B, T, H, dv)
+    _check_all(dev, (("q", q, dt, (B, T, Hk, dk)), ("k", k, dt, (B, T, Hk, dk)), ("v", v, dt, tokens),
+                     ("g", g, f32, (B, T, H)), ("head_g", head_g, f32, (H,)),
+                     ("initial_state", initial_state, f32, states),
+                     ("cu_seqlens", cu_seqlens, torch.int32, cu_shape), ("out", out, dt, tokens),
+                     ("final_state", final_state, f32, states)))
+    dims, need = _lin_dims(B, T, N, H, Hk, dk, dv, _dtype_code(dt))
     if out is None:
-        out, = _allocate(stream, ((B, T, H, dv), dt, dev))
-    else:
-        _need("out", out, dev, dt, (B, T, H, dv))
-    if final_state is not None:
-        _need("final_state", final_state, dev, torch.float32, (N, H, dk, dv))
-    elif output_final_state:
-        final_state, = _allocate(stream, ((N, H, dk, dv), torch.float32, dev))
-    L = lib()
-    dp = ctypes.byref(dims)
+        out = _allocate(stream, dev, tokens, dt)
+    if final_state is None and output_final_state:
+        final_state = _allocate(stream, dev, states, f32)
     if workspace is None:
-        bytes_ = L.kda_lin_chunk_fwd_workspace_bytes(dp)
-        if bytes_:
-            workspace, = _allocate(stream, ((bytes_,), torch.uint8, dev))
+        if need:
+            workspace = _allocate(stream, dev, (need,), torch.uint8)
     else:
-        _need("workspace", workspace, dev, torch.uint8, workspace.shape)
-    st = L.kda_lin_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(g), _addr(head_g),
-                             _addr(initial_state), _addr(cu_seqlens), out.data_ptr(),
-                             _addr(final_state), _addr(workspace),
-                             0 if workspace is None else workspace.numel(), dp, _stream_handle(stream))
+        _check_all(dev, (("workspace", workspace, torch.uint8, workspace.shape),))
+    st = lib().kda_lin_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(g), _addr(head_g),
+                                 _addr(initial_state), _addr(cu_seqlens), out.data_ptr(),
+                                 _addr(final_state), _addr(workspace),
+                                 0 if workspace is None else workspace.numel(), dims,
+                                 _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_lin_chunk_fwd")
     return out, final_state
@@ -594,44 +620,25 @@ def kda_lin_recurrent_step(q, k, v, g, head_g, state, state_indices=None, *, out
     [P, H, dk, dv]; state_indices: int32 [N] (rows outside the pool are skipped: their outputs are
     not written) or None.  Returns out [N, H, dv].
     """
-    dev, dt = q.device, q.dtype
-    _on_current_device(dev)
-    code = _dtype_code(dt)
-    if q.dim() != 3 or v.dim() != 3:
-        raise ValueError("q must be [N, Hk, dk] and v [N, H, dv]")
+    dev, dt, f32 = _device_of(q), q.dtype, torch.float32
+    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
+        raise ValueError("q must be [N, Hk, dk], v [N, H, dv] and state [P, H, dk, dv]")
     N, Hk, dk = q.shape
     H, dv = v.shape[1:]
-    _need("q", q, dev, dt, q.shape)
-    _need("k", k, dev, dt, q.shape)
-    _need("v", v, dev, dt, (N, H, dv))
-    if g is not None:
-        _need("g", g, dev, torch.float32, (N, H))
-    if head_g is not None:
-        _need("head_g", head_g, dev, torch.float32, (H,))
-    _need("state", state, dev, torch.float32, (state.shape[0], H, dk, dv))
-    if state_indices is not None:
-        _need("state_indices", state_indices, dev, torch.int32, (N,))
-    dims = KdaLinDims(N, 1, state.shape[0], H, Hk, dk, dv, code)
+    slots = state.shape[0]
+    _check_all(dev, (("q", q, dt, (N, Hk, dk)), ("k", k, dt, (N, Hk, dk)), ("v", v, dt, (N, H, dv)),
+                     ("g", g, f32, (N, H)), ("head_g", head_g, f32, (H,)),
+                     ("state", state, f32, (slots, H, dk, dv)),
+                     ("state_indices", state_indices, torch.int32, (N,)), ("out", out, dt, (N, H, dv))))
+    dims = _lin_dims(N, 1, slots, H, Hk, dk, dv, _dtype_code(dt))[0]
     if out is None:
-        out, = _allocate(stream, ((N, H, dv), dt, dev))
-    else:
-        _need("out", out, dev, dt, (N, H, dv))
+        out = _allocate(stream, dev, (N, H, dv), dt)
     st = lib().kda_lin_recurrent_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(g), _addr(head_g),
-                                      state.data_ptr(), _addr(state_indices), out.data_ptr(),
-                                      ctypes.byref(dims), _stream_handle(stream))
+                                      state.data_ptr(), _addr(state_indices), out.data_ptr(), dims,
+                                      _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_lin_recurrent_step")
     return out
-
-
-def _paged_dims(rows, heads, k_cache, v_cache, block_table, dev, dt):
-    if k_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("caches must be [pages, page_size, Hkv, d] and block_table [N, max_pages]")
-    pages, page_size, Hkv, d = k_cache.shape
-    _need("k_cache", k_cache, dev, dt, k_cache.shape)
-    _need("v_cache", v_cache, dev, dt, k_cache.shape)
-    _need("block_table", block_table, dev, torch.int32, (rows, block_table.shape[1]))
-    return KdaPagedDims(rows, heads, Hkv, d, pages, page_size, block_table.shape[1], _dtype_code(dt))
 
 
 def kda_paged_append(k, v, k_cache, v_cache, block_table, positions, cu_seqlens=None, *, stream=None):
@@ -642,20 +649,19 @@ def kda_paged_append(k, v, k_cache, v_cache, block_table, positions, cu_seqlens=
     [N+1] (row n's tokens are cu[n] .. cu[n+1]) or None (one token per row).  Tokens at a position
     past the table or on a page outside the pool are skipped.
     """
-    dev, dt = k.device, k.dtype
-    _on_current_device(dev)
-    _dtype_code(dt)
-    N = positions.numel()
-    dims = _paged_dims(N, 1, k_cache, v_cache, block_table, dev, dt)
-    tokens = k.shape[0]
-    _need("k", k, dev, dt, (tokens, dims.kv_heads, dims.head_dim))
-    _need("v", v, dev, dt, (tokens, dims.kv_heads, dims.head_dim))
-    _need("positions", positions, dev, torch.int32, (N,))
-    if cu_seqlens is not None:
-        _need("cu_seqlens", cu_seqlens, dev, torch.int32, (N + 1,))
+    dev, dt, i32 = _device_of(k), k.dtype, torch.int32
+    if k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("caches must be [pages, page_size, Hkv, d] and block_table [N, max_pages]")
+    pages, page_size, Hkv, d = cache = k_cache.shape
+    N, width, tokens = positions.numel(), block_table.shape[1], k.shape[0]
+    _check_all(dev, (("k", k, dt, (tokens, Hkv, d)), ("v", v, dt, (tokens, Hkv, d)),
+                     ("k_cache", k_cache, dt, cache), ("v_cache", v_cache, dt, cache),
+                     ("block_table", block_table, i32, (N, width)), ("positions", positions, i32, (N,)),
+                     ("cu_seqlens", cu_seqlens, i32, (N + 1,))))
+    dims = _paged_dims(N, Hkv, Hkv, d, pages, page_size, width, _dtype_code(dt))[0]
     st = lib().kda_paged_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                 block_table.data_ptr(), positions.data_ptr(), _addr(cu_seqlens), tokens,
-                                ctypes.byref(dims), _stream_handle(stream))
+                                dims, _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_paged_append")
 
@@ -663,9 +669,8 @@ def kda_paged_append(k, v, k_cache, v_cache, block_table, positions, cu_seqlens=
 def kda_paged_attention_workspace_bytes(q, k_cache, block_table) -> int:
     """Bytes of device workspace kda_paged_attention needs for these shapes."""
     pages, page_size, Hkv, d = k_cache.shape
-    dims = KdaPagedDims(q.shape[0], q.shape[1], Hkv, d, pages, page_size, block_table.shape[1],
-                        _dtype_code(q.dtype))
-    return int(lib().kda_paged_attention_workspace_bytes(ctypes.byref(dims)))
+    return _paged_dims(q.shape[0], q.shape[1], Hkv, d, pages, page_size, block_table.shape[1],
+                       _dtype_code(q.dtype))[1]
 
 
 def kda_paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, *, out=None, lse=None,
@@ -677,35 +682,30 @@ def kda_paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, *, ou
     workspace: uint8 tensor of kda_paged_attention_workspace_bytes bytes (allocated here when None).
     Returns (out [N, Hq, d], lse fp32 [N, Hq] or None); a row without tokens gets 0 and -infinity.
     """
-    dev, dt = q.device, q.dtype
-    _on_current_device(dev)
-    _dtype_code(dt)
-    if q.dim() != 3:
-        raise ValueError("q must be [N, Hq, d]")
-    N, Hq, d = q.shape
-    dims = _paged_dims(N, Hq, k_cache, v_cache, block_table, dev, dt)
-    _need("q", q, dev, dt, (N, Hq, dims.head_dim))
-    _need("seq_lens", seq_lens, dev, torch.int32, (N,))
+    dev, dt, i32 = _device_of(q), q.dtype, torch.int32
+    if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q must be [N, Hq, d], caches [pages, page_size, Hkv, d] and block_table [N, max_pages]")
+    pages, page_size, Hkv, d = cache = k_cache.shape
+    N, Hq = q.shape[:2]
+    width = block_table.shape[1]
+    _check_all(dev, (("q", q, dt, (N, Hq, d)), ("k_cache", k_cache, dt, cache), ("v_cache", v_cache, dt, cache),
+                     ("block_table", block_table, i32, (N, width)), ("seq_lens", seq_lens, i32, (N,)),
+                     ("out", out, dt, (N, Hq, d)), ("lse", lse, torch.float32, (N, Hq))))
+    dims, need = _paged_dims(N, Hq, Hkv, d, pages, page_size, width, _dtype_code(dt))
     if out is None:
-        out, = _allocate(stream, ((N, Hq, d), dt, dev))
-    else:
-        _need("out", out, dev, dt, (N, Hq, d))
-    if lse is not None:
-        _need("lse", lse, dev, torch.float32, (N, Hq))
-    elif output_lse:
-        lse, = _allocate(stream, ((N, Hq), torch.float32, dev))
-    L = lib()
-    dp = ctypes.byref(dims)
+        out = _allocate(stream, dev, (N, Hq, d), dt)
+    if lse is None and output_lse:
+        lse = _allocate(stream, dev, (N, Hq), torch.float32)
     if workspace is None:
-        bytes_ = L.kda_paged_attention_workspace_bytes(dp)
-        if bytes_:
-            workspace, = _allocate(stream, ((bytes_,), torch.uint8, dev))
+        if need:
+            workspace = _allocate(stream, dev, (need,), torch.uint8)
     else:
-        _need("workspace", workspace, dev, torch.uint8, workspace.shape)
-    st = L.kda_paged_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                               block_table.data_ptr(), seq_lens.data_ptr(), scale, out.data_ptr(),
-                               _addr(lse), _addr(workspace),
-                               0 if workspace is None else workspace.numel(), dp, _stream_handle(stream))
+        _check_all(dev, (("workspace", workspace, torch.uint8, workspace.shape),))
+    st = lib().kda_paged_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                   block_table.data_ptr(), seq_lens.data_ptr(), scale, out.data_ptr(),
+                                   _addr(lse), _addr(workspace),
+                                   0 if workspace is None else workspace.numel(), dims,
+                                   _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_paged_attention")
     return out, lse

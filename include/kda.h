@@ -447,10 +447,10 @@ typedef struct {
  *   initial_state, final_state : fp32 [num_seqs, heads, dk, dv]; the same pointer is allowed,
  *              partial overlap is not.
  *   cu_seqlens : as in kda_chunk_fwd (NULL for dense batches; clamped on the device).
- *   workspace  : device memory of kda_lin_chunk_fwd_workspace_bytes(dims) bytes, 16-byte aligned
- *              (NULL when that is 0).  Its contents on entry do not matter; calls that overlap in
- *              time need workspaces of their own.  It holds the states of the parts that a
- *              sequence is cut into when there are fewer (sequence, head) pairs than SMs.
+ *   workspace  : device memory of kda_lin_chunk_fwd_workspace_bytes(dims, packed) bytes, 16-byte
+ *              aligned (NULL when that is 0).  Its contents on entry do not matter; calls that
+ *              overlap in time need workspaces of their own.  It holds the states of the parts that
+ *              long sequences are cut into to fill the SMs.
  * v and the states may take any magnitude their formats hold.  Tokens of other sequences (and
  * what lies behind the last) never reach a sequence's results, NaN and infinities included; a
  * NaN or infinity of a sequence's own token may reach its outputs from the start of that token's
@@ -465,8 +465,9 @@ kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const void *v,
                                void *workspace, size_t workspace_bytes,
                                const kda_lin_dims_t *dims, cudaStream_t stream);
 
-/* Bytes of workspace kda_lin_chunk_fwd needs for `dims` (0: none; host arithmetic only). */
-size_t kda_lin_chunk_fwd_workspace_bytes(const kda_lin_dims_t *dims);
+/* Bytes of workspace kda_lin_chunk_fwd needs for `dims`, packed != 0 for calls with cu_seqlens (0: none;
+ * host arithmetic only). */
+size_t kda_lin_chunk_fwd_workspace_bytes(const kda_lin_dims_t *dims, int packed);
 
 /* kda_lin_recurrent_step -- one decode token per row of the same operation, state in place.
  *   q, k    : [N, qk_heads, dk] dtype;  v, out : [N, heads, dv] dtype

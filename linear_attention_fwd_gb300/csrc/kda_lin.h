@@ -76,8 +76,10 @@ struct AppendArgs {
 };
 
 cudaError_t launch_lin_chunk_simt(const LinArgs &a, cudaStream_t st);   // fp32
-// bf16: `parts` CTAs per (sequence, head); with more than one, workspace of lin_workspace_bytes.
-cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, int parts, cudaStream_t st);
+// bf16.  Sequences may be cut into parts that run side by side, which takes a workspace; `whole`: they
+// are not.
+cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, bool whole, cudaStream_t st);
+size_t lin_chunk_tc_workspace_bytes(int64_t tokens, int64_t num_seqs, int64_t heads, int dk, int dv, bool packed);
 // Waits for `st`, then reads and clears the count of expired bounded waits of that kernel.
 cudaError_t take_lin_expiries(cudaStream_t st, unsigned int *count);
 cudaError_t launch_lin_step(const LinStepArgs &a, int dk, int dv, kda_dtype_t dt, cudaStream_t st);

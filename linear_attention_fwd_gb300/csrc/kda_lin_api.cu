@@ -28,21 +28,9 @@ kda_status_t check_paged_dims(const kda_paged_dims_t *d) {
 
 }  // namespace
 
-// CTAs per (sequence, head) of the tensor-core kernel: as many as fill the SMs, at most 16, each of
-// at least 8 chunks of 64 tokens on average.
-static int lin_parts(const kda_lin_dims_t *d) {
-    if (d->dtype != KDA_BF16) return 1;
-    const int64_t units = (int64_t)d->num_seqs * d->heads, chunks = (int64_t)d->batch * d->seqlen / d->num_seqs / 64;
-    int64_t parts = kda::kSms / units;
-    if (parts > 16) parts = 16;
-    if (parts > chunks / 8) parts = chunks / 8;
-    return parts < 1 ? 1 : (int)parts;
-}
-
-extern "C" size_t kda_lin_chunk_fwd_workspace_bytes(const kda_lin_dims_t *d) {
-    if (check_lin_dims(d) != KDA_OK || d->batch <= 0 || d->seqlen <= 0) return 0;
-    // the parts' states, then their decays; all but the last part's
-    return (size_t)(lin_parts(d) - 1) * d->num_seqs * d->heads * ((size_t)d->dk * d->dv * 4 + 8);
+extern "C" size_t kda_lin_chunk_fwd_workspace_bytes(const kda_lin_dims_t *d, int packed) {
+    if (check_lin_dims(d) != KDA_OK || d->batch <= 0 || d->seqlen <= 0 || d->dtype != KDA_BF16) return 0;
+    return kda::lin_chunk_tc_workspace_bytes((int64_t)d->batch * d->seqlen, d->num_seqs, d->heads, d->dk, d->dv, packed != 0);
 }
 
 extern "C" kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const float *g,
@@ -55,7 +43,7 @@ extern "C" kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const vo
     if (d->batch <= 0 || d->seqlen < 0) return KDA_ERR_SHAPE;
     if (cu_seqlens == nullptr ? d->num_seqs != d->batch : d->batch != 1) return KDA_ERR_SHAPE;
     const int64_t tokens = (int64_t)d->batch * d->seqlen;
-    if (tokens > 0x7fffffffLL || (int64_t)d->num_seqs * d->heads > 0x7fffffffLL / 4) return KDA_ERR_SHAPE;
+    if (tokens > 0x7fffffffLL - 64 || (int64_t)d->num_seqs * d->heads > 0x7fffffffLL / 4) return KDA_ERR_SHAPE;
     if (tokens > 0 && (!q || !k || !v || !out)) return KDA_ERR_NULL;
     const void *ptrs[] = {q, k, v, out, initial_state, final_state};
     for (const void *p : ptrs)
@@ -66,7 +54,7 @@ extern "C" kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const vo
         const int64_t bytes = (int64_t)d->num_seqs * d->heads * d->dk * d->dv * 4;
         if (x < y + bytes && y < x + bytes) return KDA_ERR_SHAPE;   // partial overlap
     }
-    const size_t need = kda_lin_chunk_fwd_workspace_bytes(d);
+    const size_t need = kda_lin_chunk_fwd_workspace_bytes(d, cu_seqlens != nullptr);
     if (need > 0) {
         if (workspace == nullptr) return KDA_ERR_NULL;
         if (workspace_bytes < need) return KDA_ERR_WORKSPACE;
@@ -82,9 +70,9 @@ extern "C" kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const vo
     }
     const kda::LinArgs a{q, k, v, g, head_g, initial_state, cu_seqlens, out, final_state,
                          (int64_t)d->seqlen, d->num_seqs, d->heads, d->qk_heads, d->dk, d->dv};
-    // in place, a unit's last part would write the state that its other parts start from
-    const int parts = initial_state && initial_state == final_state ? 1 : lin_parts(d);
-    const cudaError_t e = d->dtype == KDA_BF16 ? kda::launch_lin_chunk_tc(a, workspace, parts, stream)
+    // in place, a sequence's last part would write the state that its other parts start from
+    const bool whole = initial_state && initial_state == final_state;
+    const cudaError_t e = d->dtype == KDA_BF16 ? kda::launch_lin_chunk_tc(a, workspace, whole, stream)
                                                : kda::launch_lin_chunk_simt(a, stream);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -17,7 +17,8 @@
 // carried.  The state itself stays in registers and takes each chunk's dS by an fp32 fused
 // multiply-add: the tensor cores truncate their sums, which over many chunks would pile up.
 //
-// Roles (20 warps, registers shared out by setmaxnreg).  Everything meets at mbarriers; there is no
+// Roles (20 warps; registers shared out by setmaxnreg, 104 / 104 / 96 / 96 / 80 per warpgroup out of the 5 x
+// 96 of the launch: measured against eleven other splits, 285 us and 291 to 440 us for B=4 H=32 T=8192).  Everything meets at mbarriers; there is no
 // CTA-wide barrier inside the loop.
 //   warps 0-7    K', then the state (64 key channels of one value channel per thread) and its bf16
 //                terms to TMEM
@@ -44,23 +45,23 @@ namespace {
 using namespace ptx;
 
 constexpr int C = 64, NT = 20 * 32;
-constexpr int kStages = 3, kGRing = 4;
+constexpr int kStages = 3;
 constexpr uint32_t kWaitPolls = 1u << 20;   // about a second, then the CTA gives up
 
 // shared memory, byte offsets from a 1024-aligned base
 constexpr uint32_t STAGE = 3 * 16384;                       // Q, K, V tiles [64][128] bf16, 128-byte swizzle
 constexpr uint32_t OFF_KP = kStages * STAGE;                // K': three terms [64][128] bf16, same layout
 constexpr uint32_t OFF_P = OFF_KP + 3 * 16384;              // P: two terms [64 i][64 j] bf16
-constexpr uint32_t OFF_G = OFF_P + 2 * 8192;                // decay vectors, kGRing slots
+constexpr uint32_t OFF_G = OFF_P + 2 * 8192;                // decay vectors, a slot per stage
 constexpr uint32_t G_SLOT = 5 * 64 * 4 + 16;                //   G hi, G lo, e^{G_63 - G} as bf16 terms (two words a
                                                             //   token: first and second, third twice), e^G; e^{G_63}
-constexpr uint32_t OFF_BAR = OFF_G + kGRing * G_SLOT;
+constexpr uint32_t OFF_BAR = OFF_G + kStages * G_SLOT;
 // A wait names a phase by its parity, so no barrier may complete a phase before every waiter has
 // passed the one before.  That holds because each phase needs, directly or through others, an
 // arrival that its slowest waiter makes after that pass; the products (1) run ahead of the S warps
 // and so have a barrier for each of dS's buffers.
-enum Bar { kFull = 0, kEmpty = 3, kG = 6, kKp = 10, kP = 11, kReady = 12, kOFull = 13, kOEmpty = 14, kDone = 15, kBars = 17 };
-constexpr uint32_t OFF_TM = OFF_BAR + kBars * 8 + 8;
+enum Bar { kFull = 0, kEmpty = 3, kKp = 6, kP = 7, kReady = 8, kOFull = 9, kDone = 10, kBars = 12 };
+constexpr uint32_t OFF_TM = OFF_BAR + kBars * 8;
 constexpr uint32_t SMEM_BYTES = OFF_TM + 16 + 1024;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 static_assert(OFF_BAR % 8 == 0 && G_SLOT % 16 == 0, "alignment");
@@ -106,6 +107,37 @@ __device__ __forceinline__ void add2f(float &h, float &l, float x, float y) {
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) { return *reinterpret_cast<__nv_bfloat162 *>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t *>(&x); }
+
+// Shared-memory operand descriptors here differ in their low words only: address, and for operands read
+// across their rows (MN-major) the distance of their 64-column halves.  The rest: 8-row groups 1024 bytes
+// apart, version 1, 128-byte swizzle (see sdesc_sw128, sdesc_sw128_mn).
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr) { return (saddr >> 4) | ((8192u >> 4) << 16); }
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem), "r"(a), "r"(b), "r"(idesc), "r"(accumulate),
+        "n"(kDescHigh)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate),
+        "n"(kDescHigh)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(one));
+    return one;
+}
 
 // ldmatrix at a constant offset from an address
 template <int OFF> __device__ __forceinline__ void ldsm_x4_at(uint32_t addr, uint32_t (&r)[4]) {
@@ -172,49 +204,181 @@ __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
     return h;
 }
 
-// One CTA per (sequence, head) unit and part of its chunks: part p of P is chunks
-// [p nc / P, (p + 1) nc / P).  kFull: the whole forward of the part; its state at the start is
-// composed from the initial state and the states that the parts before it reach from zero
-// (`locals`, with their total log2 decays).  Otherwise only that state: the part's from zero.
+// The work of a CTA: part p of P of sequence n's chunks, [p nc / P, (p + 1) nc / P), for head h.  A
+// sequence that is cut (see cut_of) has ceil(nc / target) parts (at most kMaxParts); its parts other than
+// the last have a slot each for states (`slot`: the sequence's first; a sequence that finds too few
+// left is not cut).
+struct Piece {
+    int n, h, p, P, slot;
+};
+constexpr int kMaxParts = 32, kRanked = 256;   // (every kernel here has at least kRanked threads)
+
+struct CutRule {
+    int most, target;   // sequences of more than `most` chunks are cut, into parts of about `target`
+    int slots;
+};
+__device__ __forceinline__ int seq_parts(const LinArgs &a, int n, const CutRule &cut) {
+    int64_t b, e;
+    lin_range(a, n, b, e);
+    const int64_t nc = (e - b + C - 1) / C;
+    if (nc <= cut.most) return 1;
+    const int64_t parts = (nc + cut.target - 1) / cut.target;
+    return parts > kMaxParts ? kMaxParts : (int)parts;
+}
+
+// The piece of CTA `b` (block-wide for packed sequences; false when there is none).  kFullPass: over all
+// parts, else over all but each sequence's last.  Packed sequences come longest first (up to kRanked of them; the hardware
+// dispatches low blocks first), each one's parts and heads together.
 template <bool kFullPass>
+__device__ __forceinline__ bool dense_piece(const LinArgs &a, int b, const CutRule &cut, Piece &out) {
+    const int P = cut.slots / a.num_seqs + 1, per = (kFullPass ? P : P - 1) * a.heads;
+    out.n = b / per;
+    out.p = b % per / a.heads;
+    out.h = b % a.heads;
+    out.P = P;
+    out.slot = out.n * (P - 1);
+    return true;
+}
+template <bool kFullPass, int THREADS>
+__device__ bool packed_piece(const LinArgs &a, int b, const CutRule &cut, Piece &out) {
+    const int H = a.heads, N = a.num_seqs, t = threadIdx.x;
+    __shared__ int s_n, s_parts[kRanked], s_len[kRanked];
+    __shared__ long long s_start, s_slot, s_sum[2][THREADS / 32];
+    if (t == 0) s_n = -1;
+    auto blocks = [&](int parts) { return (long long)(kFullPass ? parts : parts - 1) * H; };
+    if (N <= kRanked) {
+        if (t < N) {
+            int64_t x, y;
+            lin_range(a, t, x, y);
+            s_len[t] = (int)(y - x);
+            s_parts[t] = seq_parts(a, t, cut);
+        }
+        __syncthreads();
+        if (t == 0) {   // in the sequences' order: those that still find slots are cut
+            long long used = 0;
+            for (int i = 0; i < N; ++i) {
+                if (used + s_parts[i] - 1 > cut.slots) s_parts[i] = 1;
+                used += s_parts[i] - 1;
+            }
+        }
+        __syncthreads();
+        if (t < N) {
+            long long first = 0, slot = 0;
+            const int len = s_len[t];
+            for (int i = 0; i < N; ++i) {
+                if (s_len[i] > len || (s_len[i] == len && i < t)) first += blocks(s_parts[i]);
+                if (i < t) slot += s_parts[i] - 1;
+            }
+            if (first <= b && b < first + blocks(s_parts[t])) {
+                s_n = t;
+                s_start = first;
+                s_slot = slot;
+            }
+        }
+        __syncthreads();
+        if (s_n < 0) return false;
+        out.P = s_parts[s_n];
+    } else {
+        long long run = 0, run_slot = 0;
+        for (int base = 0; base < N; base += THREADS) {
+            const int n = base + t, lane = t & 31, warp = t >> 5;
+            const int parts = n < N ? seq_parts(a, n, cut) : 1;
+            const long long w = n < N ? blocks(parts) : 0, ws = parts - 1;
+            long long v = w, vs = ws;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, v, o), ys = __shfl_up_sync(0xffffffffu, vs, o);
+                if (lane >= o) {
+                    v += y;
+                    vs += ys;
+                }
+            }
+            __syncthreads();
+            if (lane == 31) {
+                s_sum[0][warp] = v;
+                s_sum[1][warp] = vs;
+            }
+            __syncthreads();
+            long long off = 0, tot = 0, offs = 0, tots = 0;
+            for (int i = 0; i < THREADS / 32; ++i) {
+                off += i < warp ? s_sum[0][i] : 0;
+                tot += s_sum[0][i];
+                offs += i < warp ? s_sum[1][i] : 0;
+                tots += s_sum[1][i];
+            }
+            const long long first = run + off + v - w;
+            if (n < N && first <= b && b < first + w) {
+                s_n = n;
+                s_start = first;
+                s_slot = run_slot + offs + vs - ws;
+            }
+            run += tot;
+            run_slot += tots;
+        }
+        __syncthreads();
+        if (s_n < 0) return false;
+        out.P = seq_parts(a, s_n, cut);
+        // (the host's bound on the slots holds for offsets as documented; others must not leave them)
+        if (s_slot + out.P - 1 > cut.slots) {
+            if (!kFullPass || b - s_start >= H) return false;
+            out.P = 1;
+        }
+    }
+    out.n = s_n;
+    out.p = (int)((b - s_start) / H);
+    out.h = (int)((b - s_start) % H);
+    out.slot = (int)s_slot;
+    return true;
+}
+
+// kFullPass: the whole forward of a part; a part other than the first starts from the state in the slot
+// of the part before it.  Otherwise only the state that a part reaches from zero, into its slot of
+// `locals`, and its total log2 decay; lin_scan_kernel then turns each slot into the true state behind
+// its part.
+// kPacked: an instantiation of its own for dense batches, whose pieces are arithmetic on the block's number
+// (uniform values throughout): the shared one ran them at 336 us instead of 310 (B=4 H=32 T=8192).
+template <bool kFullPass, bool kPacked>
 __global__ void __launch_bounds__(NT, 1)
 kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                        const __grid_constant__ CUtensorMap tmv, const LinArgs a, const int P,
-                        float *locals, double *decays) {
+                        const __grid_constant__ CUtensorMap tmv, const LinArgs a, const CutRule cut, float *locals, double *decays) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_fail;
+    __shared__ volatile int s_piece[4];   // unit, the part's slot, whether it is the last (read again at the end:
+                                          // registers are scarce in the loop)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int H = a.heads;
-    const int64_t units = (int64_t)a.num_seqs * H;
-    const int p = (int)(blockIdx.x / units);
-    const int64_t unit = blockIdx.x % units;
-    const int n = (int)(unit / H), h = (int)(unit % H), hk = h / (H / a.qk_heads);
-    int64_t bos, eos;
-    lin_range(a, n, bos, eos);
-    const int nc = (int)((eos - bos + C - 1) / C);
+    Piece piece;
+    if (!(kPacked ? packed_piece<kFullPass, NT>(a, blockIdx.x, cut, piece) : dense_piece<kFullPass>(a, blockIdx.x, cut, piece))) return;
+    const int n = piece.n, h = piece.h, p = piece.p, P = piece.P, slot = piece.slot;
+    const int hk = h / (H / a.qk_heads);
+    int64_t bos64, eos64;
+    lin_range(a, n, bos64, eos64);
+    const int bos = (int)bos64, eos = (int)eos64;      // tokens are counted in 31 bits
+    const int nc = (eos - bos + C - 1) / C;
     const int c_lo = (int)((int64_t)p * nc / P), c_hi = (int)((int64_t)(p + 1) * nc / P);
     const int chunks = c_hi - c_lo;
-    const int64_t first = bos + (int64_t)c_lo * C;     // the part's first token
+    const int first = bos + c_lo * C;                  // the part's first token
     const bool last_part = p == P - 1;
-    if (chunks == 0 && !(kFullPass ? last_part && a.sT : true)) return;
+    if (chunks == 0 && kFullPass && !(last_part && a.sT)) return;
 
     auto bar = [&](int b) { return sb + OFF_BAR + 8 * b; };
     if (tid == 0) {
         s_fail = 0;
+        s_piece[0] = n * H + h;
+        s_piece[1] = (slot + p) * H + h;
+        s_piece[2] = last_part;
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(bar(kFull + s), 1);
+            mbar_init(bar(kFull + s), 1 + 32);                // the tiles, and the warp that writes the decay vectors
             mbar_init(bar(kEmpty + s), kFullPass ? 9 : 1);   // the products, and the warps that staged outputs there
         }
-        for (int s = 0; s < kGRing; ++s) mbar_init(bar(kG + s), 32);
         mbar_init(bar(kKp), 256);
         mbar_init(bar(kP), 256);
-        mbar_init(bar(kReady), 256);
+        mbar_init(bar(kReady), kFullPass ? 512 : 256);
         mbar_init(bar(kDone), 1);
         mbar_init(bar(kDone + 1), 1);
         mbar_init(bar(kOFull), 1);
-        mbar_init(bar(kOEmpty), 256);
         fence_mbar_init();
     }
     if (warp == 17) {
@@ -227,17 +391,17 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + OFF_TM);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(sm + OFF_TM), 0);
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int jl = 32 * (warp & 3) + lane;             // value channel of this thread's TMEM lane
-    auto gslot = [&](int k) { return reinterpret_cast<float *>(sm + OFF_G + (k % kGRing) * G_SLOT); };
+    auto gslot = [&](int k) { return reinterpret_cast<float *>(sm + OFF_G + (k % kStages) * G_SLOT); };
     auto wait = [&](int b, uint32_t parity) { return mbar_wait_small(bar(b), parity & 1u, kWaitPolls); };
     auto done = [&](int k) { return wait(kDone + (k & 1), k >> 1); };
     bool ok = true;
 
     if (warp < 8) {
         // ---- S
-        regs_inc<128>();
+        regs_inc<104>();
         const int i0 = 64 * (warp >> 2);
         const int64_t sstep = (int64_t)a.dk * a.dv;
         const bool mine = jl < a.dv && i0 < a.dk;
@@ -246,20 +410,16 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
 #pragma unroll
         for (int c = 0; c < 64; ++c) v[c] = 0.f;
         if (kFullPass && mine) {
-            if (a.s0)
+            const float *from = p > 0 ? locals + ((int64_t)(slot + p - 1) * H + h) * sstep : (a.s0 ? a.s0 + ((int64_t)n * H + h) * sstep : nullptr);
+            if (from)
 #pragma unroll
-                for (int c = 0; c < 64; ++c) v[c] = a.s0[unit * sstep + at + (int64_t)c * a.dv];
-            for (int e = 0; e < p; ++e) {
-                const float f = exp2f((float)decays[e * units + unit]);
-                const float *l = locals + (e * units + unit) * sstep + at;
-#pragma unroll
-                for (int c = 0; c < 64; ++c) v[c] = fmaf(f, v[c], __ldcg(l + (int64_t)c * a.dv));
-            }
+                for (int c = 0; c < 64; ++c) v[c] = __ldcg(from + at + (int64_t)c * a.dv);
         }
+        float dec = 0.f;   // e^(sum of the chunk's log decays)
         for (int k = 0; k <= chunks; ++k) {
             // dS and K' of the chunk before are done with; this chunk's tile and decays landed
             if (k > 0) ok = done(k - 1);
-            if (ok && k < chunks) ok = wait(kFull + k % kStages, k / kStages) && wait(kG + k % kGRing, k / kGRing);
+            if (ok && k < chunks) ok = wait(kFull + k % kStages, k / kStages);
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
@@ -267,55 +427,56 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
             if (k < chunks) {
                 const uint32_t st = (k % kStages) * STAGE;
                 const float *gv = gslot(k);
-                const int64_t left = eos - (first + (int64_t)k * C);
-                const int nr = left < C ? (int)left : C;
+                const int left = eos - (first + k * C), nr = left < C ? left : C;
                 // K' = k w in packed bf16 arithmetic.  The factor comes as three bf16 terms; k w_0 = h + e and
                 // k w_1 = y + y' exactly (8-bit times 8-bit significands), m = e + y rounded, and the third
                 // term is what that rounding left plus y' + k w_2: the sum of the three is within 2^-22
                 // (2^-26 RMS) of k w.  16-byte pieces lie at the same offsets in K and K'.  (Loads come before
                 // stores here and below: the compiler keeps their order, and a load behind a store waits its
                 // whole way.)
-                uint4 uk[4];
-                uint2 wk[4];
+#pragma unroll 1
+                for (int x0 = tid; x0 < 1024; x0 += 512) {
+                    uint4 uk[2];
+                    uint2 wk[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int x = tid + 256 * e;
-                    uk[e] = *reinterpret_cast<const uint4 *>(sm + st + 16384 + 16 * x);
-                    wk[e] = reinterpret_cast<const uint2 *>(gv + 128)[(x >> 3) & 63];
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int x = tid + 256 * e, r = (x >> 3) & 63;
-                    const __nv_bfloat162 w0 = as_bf162(__byte_perm(wk[e].x, 0, 0x1010)), w1 = as_bf162(__byte_perm(wk[e].x, 0, 0x3232)),
-                                         w2 = as_bf162(wk[e].y);
-                    if (nr < C && r >= nr) {   // rows past the sequence belong to another one: they never enter a product
-                        uk[e] = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4 *>(sm + st + 32768 + 16 * x) = uk[e];
+                    for (int e = 0; e < 2; ++e) {
+                        const int x = x0 + 256 * e;
+                        uk[e] = *reinterpret_cast<const uint4 *>(sm + st + 16384 + 16 * x);
+                        wk[e] = reinterpret_cast<const uint2 *>(gv + 128)[(x >> 3) & 63];
                     }
-                    const uint32_t uw[4] = {uk[e].x, uk[e].y, uk[e].z, uk[e].w};
-                    uint32_t o0[4], o1[4], o2[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const __nv_bfloat162 kv = as_bf162(uw[c]);
-                        const __nv_bfloat162 hh = __hmul2_rn(kv, w0), ee = __hfma2(kv, w0, __hneg2(hh));
-                        const __nv_bfloat162 yy = __hmul2_rn(kv, w1), ye = __hfma2(kv, w1, __hneg2(yy));
-                        const __nv_bfloat162 mm = __hadd2_rn(ee, yy);
-                        const __nv_bfloat162 ll = __hadd2_rn(__hsub2_rn(yy, __hsub2_rn(mm, ee)), __hfma2(kv, w2, ye));
-                        o0[c] = as_u32(hh);
-                        o1[c] = as_u32(mm);
-                        o2[c] = as_u32(ll);
+                    for (int e = 0; e < 2; ++e) {
+                        const int x = x0 + 256 * e, r = (x >> 3) & 63;
+                        const __nv_bfloat162 w0 = as_bf162(__byte_perm(wk[e].x, 0, 0x1010)), w1 = as_bf162(__byte_perm(wk[e].x, 0, 0x3232)),
+                                             w2 = as_bf162(wk[e].y);
+                        if (nr < C && r >= nr) {   // rows past the sequence belong to another one: they never enter a product
+                            uk[e] = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4 *>(sm + st + 32768 + 16 * x) = uk[e];
+                        }
+                        const uint32_t uw[4] = {uk[e].x, uk[e].y, uk[e].z, uk[e].w};
+                        uint32_t o0[4], o1[4], o2[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const __nv_bfloat162 kv = as_bf162(uw[c]);
+                            const __nv_bfloat162 hh = __hmul2_rn(kv, w0), ee = __hfma2(kv, w0, __hneg2(hh));
+                            const __nv_bfloat162 yy = __hmul2_rn(kv, w1), ye = __hfma2(kv, w1, __hneg2(yy));
+                            const __nv_bfloat162 mm = __hadd2_rn(ee, yy);
+                            const __nv_bfloat162 ll = __hadd2_rn(__hsub2_rn(yy, __hsub2_rn(mm, ee)), __hfma2(kv, w2, ye));
+                            o0[c] = as_u32(hh);
+                            o1[c] = as_u32(mm);
+                            o2[c] = as_u32(ll);
+                        }
+                        uint4 *to = reinterpret_cast<uint4 *>(sm + OFF_KP + 16 * x);
+                        to[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+                        to[1024] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+                        to[2048] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
                     }
-                    uint4 *to = reinterpret_cast<uint4 *>(sm + OFF_KP + 16 * x);
-                    to[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-                    to[1024] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-                    to[2048] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
                 }
                 fence_async_smem();
                 mbar_arrive(bar(kKp));
             }
             if (k > 0) {
                 tc_fence_after();
-                const float dec = gslot(k - 1)[320];
                 const float2 d2 = make_float2(dec, dec);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
@@ -330,6 +491,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 }
             }
             if (k == chunks) break;
+            dec = gslot(k)[320];
             if (kFullPass) {
                 ok = k == 0 || wait(kOFull, k - 1);   // the chunk before has read its operand
                 if (!__all_sync(0xffffffffu, ok)) {
@@ -353,15 +515,15 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
             tc_fence_before();
             mbar_arrive(bar(kReady));
         }
-        float *to = kFullPass ? (last_part ? a.sT : nullptr) : locals;
+        float *to = kFullPass ? (s_piece[2] ? a.sT : nullptr) : locals;
         if (ok && to && mine) {
-            to += (kFullPass ? unit : p * units + unit) * sstep + at;
+            to += (int64_t)s_piece[kFullPass ? 0 : 1] * sstep + at;
 #pragma unroll
             for (int c = 0; c < 64; ++c) to[(int64_t)c * a.dv] = v[c];
         }
     } else if (warp < 16) {
         // ---- scores, P and O, each of the two halves of these warps half of it
-        regs_dec<88>();
+        regs_dec<96>();
         const int half = (warp - 8) >> 2;
         const int w4 = warp & 3, g = lane >> 2, t4 = lane & 3;
         // O: 32 tokens x 32 channels a warp.  TMEM is read as 8 x 8 fragments (channel, token), which stmatrix
@@ -382,11 +544,10 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
         for (int k = 0; kFullPass && k <= chunks; ++k) {
             const uint32_t st = (k % kStages) * STAGE;
             const float *gv = gslot(k);
-            const int64_t left = eos - (first + (int64_t)k * C);
-            const int nr = left < C ? (int)left : C;
+            const int left = eos - (first + k * C), nr = left < C ? left : C;
             float acc[3][4];
             if (k < chunks) {
-                ok = wait(kFull + k % kStages, k / kStages) && wait(kG + k % kGRing, k / kGRing);
+                ok = wait(kFull + k % kStages, k / kStages);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -428,9 +589,9 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                         stsm_x4_t(sb + stg + o_st[L] + 1024 * e, x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
                 }
                 tc_fence_before();
-                mbar_arrive(bar(kOEmpty));
             }
             if (k < chunks) {   // P
+                mbar_arrive(bar(kReady));
                 const int m0 = i < nr ? i : nr - 1, m1 = i + 8 < nr ? i + 8 : nr - 1;   // the last key of each row
                 const float gh0 = gv[i], gh1 = gv[i + 8], gl0 = gv[64 + i], gl1 = gv[72 + i];
                 float2 hj[3], lj[3];
@@ -468,25 +629,24 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 for (int e = 0; e < 4; ++e) y[e] = *reinterpret_cast<const uint4 *>(sm + stg + o_ld + 512 * e);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kEmpty + (k - 1) % kStages));
-                const int64_t t0 = first + (int64_t)(k - 1) * C;
-                const int64_t past = eos - t0 - 32 * half;
-                uint8_t *o = static_cast<uint8_t *>(a.out) + ((t0 * H + h) * a.dv) * 2 + o_off;
-                const int rows = 32 * w4 < a.dv ? (past < 32 ? (int)past : 32) - (lane >> 2) : 0;
+                const int t0 = first + (k - 1) * C, past = eos - t0 - 32 * half;
+                uint8_t *o = static_cast<uint8_t *>(a.out) + (((int64_t)t0 * H + h) * a.dv) * 2 + o_off;
+                const int rows = 32 * w4 < a.dv ? (past < 32 ? past : 32) - (lane >> 2) : 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (8 * e < rows) *reinterpret_cast<uint4 *>(o + 8 * e * tok_bytes) = y[e];
             }
         }
     } else {
-        regs_dec<48>();
+        regs_dec<80>();
         if (warp == 16) {
             // ---- tiles by TMA, and the decay sums: lane l holds tokens 2l and 2l + 1
             float th = 0.f, tl = 0.f;   // the part's sum
             const float hg = a.head_g ? __ldg(a.head_g + h) : 0.f;
-            const float *gp = a.g ? a.g + (first + 2 * lane) * H + h : nullptr;
+            const float *gp = a.g ? a.g + (int64_t)(first + 2 * lane) * H + h : nullptr;
             float gx = 0.f, gy = 0.f;
             auto load_g = [&](int k) {
-                const int64_t t = first + (int64_t)k * C + 2 * lane;
+                const int t = first + k * C + 2 * lane;
                 gx = gp && t < eos ? __ldg(gp + (int64_t)k * C * H) : 0.f;
                 gy = gp && t + 1 < eos ? __ldg(gp + (int64_t)k * C * H + H) : 0.f;
             };
@@ -512,7 +672,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 }
                 if (lane == 0) {
                     const uint32_t st = sb + s * STAGE, b = bar(kFull + s);
-                    const int tok = (int)(first + (int64_t)k * C);
+                    const int tok = first + k * C;
                     mbar_arrive_expect_tx(b, kFullPass ? 3 * 16384 : 2 * 16384);
                     tma_load_3d(st + 16384, &tmk, b, 0, hk, tok);
                     tma_load_3d(st + 24576, &tmk, b, 64, hk, tok);
@@ -524,14 +684,14 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                     }
                 }
                 __syncwarp();
-                const int64_t t = first + (int64_t)k * C + 2 * lane;
+                const int t = first + k * C + 2 * lane;
                 float xh, xl, yh, yl;
                 log2_decay(gx, t < eos, xh, xl);
                 log2_decay(gy, t + 1 < eos, yh, yl);
                 if (k + 1 < chunks) load_g(k + 1);
                 float bh = xh, bl = xl;            // sums up to the lane's second token
                 add2f(bh, bl, yh, yl);
-#pragma unroll
+#pragma unroll 1
                 for (int o = 1; o < 32; o <<= 1) {
                     const float ph = __shfl_up_sync(0xffffffffu, bh, o), pl = __shfl_up_sync(0xffffffffu, bl, o);
                     if (lane >= o) add2f(bh, bl, ph, pl);
@@ -548,22 +708,19 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 reinterpret_cast<float2 *>(gv + 256)[lane] = make_float2(exp2f(ah + al), exp2f(bh + bl));
                 if (lane == 0) gv[320] = exp2f(eh + el);
                 if (!kFullPass) add2f(th, tl, eh, el);
-                mbar_arrive(bar(kG + k % kGRing));
+                mbar_arrive(bar(kFull + s));
             }
-            if (!kFullPass && lane == 0) decays[p * units + unit] = (double)th + (double)tl;
+            if (!kFullPass && lane == 0) decays[s_piece[1]] = (double)th + (double)tl;
         } else if (warp == 17) {
-            // ---- tensor-core products.  The whole warp runs the loop and one lane issues, so that the
-            // operand descriptors are warp-uniform values made outside the issuing branches (made
-            // inside, an MMA took about 115 cycles to issue).
-            const uint64_t dsm = sdesc_sw128(sb);
-            const uint64_t kpd = sdesc_sw128_mn(sb + OFF_KP, 8192, 1024);
-            const uint64_t v0 = sdesc_sw128_mn(sb + 32768, 8192, 1024);
-            const uint32_t one = lane == 0;
+            // ---- tensor-core products.  The whole warp runs the loop and an elected lane issues, so that the
+            // operand descriptors can stay in uniform registers (half the instructions per product).
+            const uint32_t pd = desc_k(sb + OFF_P), kpd = desc_mn(sb + OFF_KP);
+            const uint32_t one = elect_one();
             int s = 0;
             for (int k = 0; k < chunks; ++k) {
-                const uint64_t vd = v0 + s * (STAGE >> 4), qd = dsm + s * (STAGE >> 4);
+                const uint32_t vd = desc_mn(sb + s * STAGE + 32768), qd = desc_k(sb + s * STAGE);
                 // dS of two chunks ago was taken before the S warps got ready for the chunk before
-                ok = wait(kFull + s, k / kStages) && wait(kKp, k) && (kFullPass || wait(kReady, k));
+                ok = wait(kKp, k) && (kFullPass || wait(kReady, k));
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -571,27 +728,27 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 tc_fence_after();
                 const uint32_t ds = tmem + TM_DS + 128 * (k & 1);
                 if (one) {
-#pragma unroll
+#pragma unroll 1
                     for (int e = 2; e >= 0; --e)   // the smallest terms first
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_f16_ss(ds, vd + ((2048 * kk) >> 4), kpd + ((16384 * e + 2048 * kk) >> 4), IDESC_KV, e < 2 || kk > 0);
+                            mma_ss(ds, vd + ((2048 * kk) >> 4), kpd + ((16384 * e + 2048 * kk) >> 4), IDESC_KV, e < 2 || kk > 0);
                     mma_commit(bar(kDone + (k & 1)));
                 }
                 __syncwarp();
                 if (kFullPass) {
-                    ok = wait(kReady, k) && (k == 0 || wait(kOEmpty, k - 1));
+                    ok = wait(kReady, k);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     if (one) {
-#pragma unroll
+#pragma unroll 1
                         for (int e = 0; e < 2; ++e)
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
-                                mma_f16_ts(tmem + TM_OI, tmem + TM_S16 + 64 * e + 8 * kk, qd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
+                                mma_ts(tmem + TM_OI, tmem + TM_S16 + 64 * e + 8 * kk, qd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
                                            IDESC_SQ, e + kk > 0);
                     }
                     __syncwarp();
@@ -602,11 +759,11 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                     }
                     tc_fence_after();
                     if (one) {
-#pragma unroll
+#pragma unroll 1
                         for (int e = 0; e < 2; ++e)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma_f16_ss(tmem + TM_OJ, vd + ((2048 * kk) >> 4), dsm + ((OFF_P + 8192 * e + 32 * kk) >> 4), IDESC_VP, e + kk > 0);
+                                mma_ss(tmem + TM_OJ, vd + ((2048 * kk) >> 4), pd + ((8192 * e + 32 * kk) >> 4), IDESC_VP, e + kk > 0);
                         mma_commit(bar(kOFull));
                     }
                 }
@@ -633,17 +790,17 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
             atomicAdd(&g_kda_lin_timeouts, 1u);
         }
         const float nan = __int_as_float(0x7fc00000);
-        float *to = kFullPass ? (last_part ? a.sT : nullptr) : locals;
+        float *to = kFullPass ? (s_piece[2] ? a.sT : nullptr) : locals;
         if (to) {
-            to += (kFullPass ? unit : p * units + unit) * (int64_t)a.dk * a.dv;
+            to += (int64_t)s_piece[kFullPass ? 0 : 1] * a.dk * a.dv;
             for (int x = tid; x < a.dk * a.dv; x += NT) to[x] = nan;
         }
         if (kFullPass) {
-            const int64_t t1 = bos + (int64_t)c_hi * C < eos ? bos + (int64_t)c_hi * C : eos;
-            for (int64_t x = tid; x < (t1 - first) * a.dv; x += NT)
+            const int t1 = bos + (int64_t)c_hi * C < eos ? bos + c_hi * C : eos;
+            for (int64_t x = tid; x < (int64_t)(t1 - first) * a.dv; x += NT)
                 static_cast<__nv_bfloat16 *>(a.out)[((first + x / a.dv) * H + h) * a.dv + x % a.dv] = __float2bfloat16(nan);
         } else if (tid == 0) {
-            decays[p * units + unit] = 0.0;
+            decays[s_piece[1]] = 0.0;
         }
         __syncthreads();
     }
@@ -651,6 +808,28 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, TM_COLS);
+    }
+}
+
+// For each sequence that is cut: the state behind part p is e^{its decay} times the one before it plus
+// the part's own from zero.  One CTA per slot, head and 1024 values; those of a sequence's first slot
+// walk its parts.
+constexpr int kScanThreads = 256;
+__global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const LinArgs a, const CutRule cut, float *locals, const double *decays) {
+    Piece piece;
+    const bool some = a.cu ? packed_piece<false, kScanThreads>(a, blockIdx.x, cut, piece) : dense_piece<false>(a, blockIdx.x, cut, piece);
+    if (!some || piece.p != 0) return;
+    const int H = a.heads;
+    const int64_t size = (int64_t)a.dk * a.dv, at = ((int64_t)blockIdx.y * kScanThreads + threadIdx.x) * 4;
+    float4 s = a.s0 ? *reinterpret_cast<const float4 *>(a.s0 + ((int64_t)piece.n * H + piece.h) * size + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < piece.P - 1; ++p) {
+        const int64_t slot = (int64_t)(piece.slot + p) * H + piece.h;
+        float4 *l = reinterpret_cast<float4 *>(locals + slot * size + at);
+        const float f = exp2f((float)decays[slot]);
+        const float4 x = __ldcg(l);
+        s = make_float4(fmaf(f, s.x, x.x), fmaf(f, s.y, x.y), fmaf(f, s.z, x.z), fmaf(f, s.w, x.w));
+        *l = s;
     }
 }
 
@@ -691,27 +870,74 @@ cudaError_t take_lin_expiries(cudaStream_t st, unsigned int *count) {
     return e;
 }
 
-cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, int parts, cudaStream_t st) {
+// How a call is cut, the CTAs of the two passes.  Cutting costs a first pass over K and V (about half the
+// time of the whole) of the parts but the last, so:
+//  - dense batches with fewer (sequence, head) units than SMs get as many parts per unit as fill the SMs,
+//    of at least kMinPart chunks (8 heads of 32767 tokens: 0.13 ms in 19 parts, 1.3 ms whole);
+//  - packed sequences, whose lengths only the device knows, run longest first, and those of more than
+//    1.5 times an SM's equal share of all chunks are cut into quarters of that share (sequences just
+//    above it are not: the first pass costs more than the SMs that wait).
+struct Cut {
+    CutRule rule;
+    int64_t pre, full;
+};
+constexpr int64_t kMinPart = 8;
+static Cut cut_of(int64_t tokens, int64_t num_seqs, int64_t heads, bool packed, bool whole) {
+    const int64_t units = num_seqs * heads, all = packed ? (tokens + C - 1) / C + num_seqs : num_seqs * ((tokens / num_seqs + C - 1) / C);
+    Cut c{{0x7fffffff, 1, 0}, 0, units};
+    if (whole) return c;
+    if (packed) {
+        const int64_t share = (all * heads + kSms - 1) / kSms;
+        int64_t most = share + share / 2, target = share / 4;
+        if (target < kMinPart) target = kMinPart;
+        if (most < 2 * kMinPart) most = 2 * kMinPart;
+        // at most all / (most + 1) sequences are cut, into ceil(nc / target) parts
+        const int64_t slots = all <= most ? 0 : all / target;
+        c.rule = {(int)most, (int)target, (int)slots};
+    } else {
+        const int64_t nc = all / num_seqs;
+        int64_t parts = kSms / units;
+        if (parts > kMaxParts) parts = kMaxParts;
+        if (parts > nc / kMinPart) parts = nc / kMinPart;
+        if (parts <= 1) return c;
+        const int64_t target = (nc + parts - 1) / parts;
+        parts = (nc + target - 1) / target;
+        c.rule = {0, (int)target, (int)(num_seqs * (parts - 1))};
+    }
+    c.pre = c.rule.slots * heads;
+    c.full = units + c.pre;
+    return c;
+}
+
+size_t lin_chunk_tc_workspace_bytes(int64_t tokens, int64_t num_seqs, int64_t heads, int dk, int dv, bool packed) {
+    return (size_t)cut_of(tokens, num_seqs, heads, packed, false).rule.slots * heads * ((size_t)dk * dv * 4 + 8);
+}
+
+cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, bool whole, cudaStream_t st) {
     const int64_t tokens = a.cu ? a.seqlen : (int64_t)a.num_seqs * a.seqlen;
-    const int64_t units = (int64_t)a.num_seqs * a.heads;
+    const Cut c = cut_of(tokens, a.num_seqs, a.heads, a.cu != nullptr, whole);
+    if (c.full > 0x7fffffffLL) return cudaErrorInvalidValue;
     CUtensorMap mq, mk, mv;
     if (!make_map(&mq, a.q, tokens, a.qk_heads, a.dk) || !make_map(&mk, a.k, tokens, a.qk_heads, a.dk) ||
         !make_map(&mv, a.v, tokens, a.heads, a.dv))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(kda_lin_chunk_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
-    if (e != cudaSuccess) return e;
     float *locals = static_cast<float *>(workspace);
-    double *decays = reinterpret_cast<double *>(locals + (int64_t)(parts - 1) * units * a.dk * a.dv);
-    if (parts > 1) {
-        e = cudaFuncSetAttribute(kda_lin_chunk_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    double *decays = reinterpret_cast<double *>(locals + (int64_t)c.rule.slots * a.heads * a.dk * a.dv);
+    auto launch = [&](auto kernel, int64_t ctas) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
         if (e != cudaSuccess) return e;
-        // parts 0 .. parts - 2 of `parts`: the last one's state from zero is not needed
-        kda_lin_chunk_tc_kernel<false><<<(unsigned)(units * (parts - 1)), NT, SMEM_BYTES, st>>>(mq, mk, mv, a, parts, locals, decays);
+        kernel<<<(unsigned)ctas, NT, SMEM_BYTES, st>>>(mq, mk, mv, a, c.rule, locals, decays);
+        return cudaGetLastError();
+    };
+    if (c.pre > 0) {
+        cudaError_t e = a.cu ? launch(kda_lin_chunk_tc_kernel<false, true>, c.pre) : launch(kda_lin_chunk_tc_kernel<false, false>, c.pre);
+        if (e != cudaSuccess) return e;
+        const dim3 grid((unsigned)c.pre, (unsigned)(a.dk * a.dv / (4 * kScanThreads)));
+        lin_scan_kernel<<<grid, kScanThreads, 0, st>>>(a, c.rule, locals, decays);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    kda_lin_chunk_tc_kernel<true><<<(unsigned)(units * parts), NT, SMEM_BYTES, st>>>(mq, mk, mv, a, parts, locals, decays);
-    return cudaGetLastError();
+    return a.cu ? launch(kda_lin_chunk_tc_kernel<true, true>, c.full) : launch(kda_lin_chunk_tc_kernel<true, false>, c.full);
 }
 
 }  // namespace kda

@@ -113,7 +113,7 @@ def lib() -> ctypes.CDLL:
         L.kda_lin_chunk_fwd.restype = ctypes.c_int
         L.kda_lin_chunk_fwd.argtypes = [vp] * 10 + [ctypes.c_size_t, lp, vp]
         L.kda_lin_chunk_fwd_workspace_bytes.restype = ctypes.c_size_t
-        L.kda_lin_chunk_fwd_workspace_bytes.argtypes = [lp]
+        L.kda_lin_chunk_fwd_workspace_bytes.argtypes = [lp, ctypes.c_int]
         L.kda_lin_recurrent_step.restype = ctypes.c_int
         L.kda_lin_recurrent_step.argtypes = [vp] * 8 + [lp, vp]
         L.kda_paged_append.restype = ctypes.c_int
@@ -524,21 +524,26 @@ def _device_of(t) -> int:
     return dev
 
 
+# the current stream's handle without making a Stream object, where torch has it
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _raw_stream(stream, dev: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _current_raw_stream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _allocate(stream, dev: int, shape, dtype):
-    """A new tensor, made for use on `stream`: memory that the allocator hands out for another stream
-    may still be in use there."""
+def _allocate(stream, like, shape, dtype):
+    """A new tensor on like's device, made for use on `stream`: memory that the allocator hands out
+    for another stream may still be in use there."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}" if dev else "cuda:0")
+        return like.new_empty(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _addr(t):
@@ -546,10 +551,10 @@ def _addr(t):
 
 
 @functools.lru_cache(maxsize=1024)
-def _lin_dims(*sizes):
+def _lin_dims(packed, *sizes):
     """(pointer to the struct, workspace bytes) for these sizes."""
     p = ctypes.byref(KdaLinDims(*sizes))
-    return p, int(lib().kda_lin_chunk_fwd_workspace_bytes(p))
+    return p, int(lib().kda_lin_chunk_fwd_workspace_bytes(p, packed))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -562,7 +567,7 @@ def kda_lin_chunk_fwd_workspace_bytes(q, v, cu_seqlens=None) -> int:
     """Bytes of device workspace kda_lin_chunk_fwd needs for these shapes."""
     B, T, H, dv = v.shape
     n = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    return _lin_dims(B, T, n, H, q.shape[2], q.shape[3], dv, _dtype_code(q.dtype))[1]
+    return _lin_dims(int(cu_seqlens is not None), B, T, n, H, q.shape[2], q.shape[3], dv, _dtype_code(q.dtype))[1]
 
 
 def kda_lin_chunk_fwd(q, k, v, g=None, head_g=None, initial_state=None, cu_seqlens=None, *, out=None,
@@ -593,14 +598,14 @@ def kda_lin_chunk_fwd(q, k, v, g=None, head_g=None, initial_state=None, cu_seqle
                      ("initial_state", initial_state, f32, states),
                      ("cu_seqlens", cu_seqlens, torch.int32, cu_shape), ("out", out, dt, tokens),
                      ("final_state", final_state, f32, states)))
-    dims, need = _lin_dims(B, T, N, H, Hk, dk, dv, _dtype_code(dt))
+    dims, need = _lin_dims(int(cu_seqlens is not None), B, T, N, H, Hk, dk, dv, _dtype_code(dt))
     if out is None:
-        out = _allocate(stream, dev, tokens, dt)
+        out = _allocate(stream, q, tokens, dt)
     if final_state is None and output_final_state:
-        final_state = _allocate(stream, dev, states, f32)
+        final_state = _allocate(stream, q, states, f32)
     if workspace is None:
         if need:
-            workspace = _allocate(stream, dev, (need,), torch.uint8)
+            workspace = _allocate(stream, q, (need,), torch.uint8)
     else:
         _check_all(dev, (("workspace", workspace, torch.uint8, workspace.shape),))
     st = lib().kda_lin_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(g), _addr(head_g),
@@ -630,9 +635,9 @@ def kda_lin_recurrent_step(q, k, v, g, head_g, state, state_indices=None, *, out
                      ("g", g, f32, (N, H)), ("head_g", head_g, f32, (H,)),
                      ("state", state, f32, (slots, H, dk, dv)),
                      ("state_indices", state_indices, torch.int32, (N,)), ("out", out, dt, (N, H, dv))))
-    dims = _lin_dims(N, 1, slots, H, Hk, dk, dv, _dtype_code(dt))[0]
+    dims = _lin_dims(0, N, 1, slots, H, Hk, dk, dv, _dtype_code(dt))[0]
     if out is None:
-        out = _allocate(stream, dev, (N, H, dv), dt)
+        out = _allocate(stream, q, (N, H, dv), dt)
     st = lib().kda_lin_recurrent_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(g), _addr(head_g),
                                       state.data_ptr(), _addr(state_indices), out.data_ptr(), dims,
                                       _raw_stream(stream, dev))
@@ -693,12 +698,12 @@ def kda_paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, *, ou
                      ("out", out, dt, (N, Hq, d)), ("lse", lse, torch.float32, (N, Hq))))
     dims, need = _paged_dims(N, Hq, Hkv, d, pages, page_size, width, _dtype_code(dt))
     if out is None:
-        out = _allocate(stream, dev, (N, Hq, d), dt)
+        out = _allocate(stream, q, (N, Hq, d), dt)
     if lse is None and output_lse:
-        lse = _allocate(stream, dev, (N, Hq), torch.float32)
+        lse = _allocate(stream, q, (N, Hq), torch.float32)
     if workspace is None:
         if need:
-            workspace = _allocate(stream, dev, (need,), torch.uint8)
+            workspace = _allocate(stream, q, (need,), torch.uint8)
     else:
         _check_all(dev, (("workspace", workspace, torch.uint8, workspace.shape),))
     st = lib().kda_paged_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),

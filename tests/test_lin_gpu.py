@@ -125,6 +125,33 @@ def test_long_packed_few_heads(K, dt):
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("n,long,H", [(7, 2600, 3), (300, 2100, 1), (300, 2100, 5)])
+def test_one_long_among_short(K, dt, n, long, H):
+    """Packed: the long sequence is cut, the others are not; few sequences and more than are ranked."""
+    lens = [(5 * i) % 9 for i in range(n)]
+    lens[n // 2] = long
+    cu = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
+    d = make(27, 1, sum(lens), H, 1, 64, 64, dt, decay="both", init=n)
+    d["g"] *= 0.02
+    out, fin = K.kda_lin_chunk_fwd(**d, cu_seqlens=cu)
+    R.check_lin(out, fin, reference(d, cu))
+
+
+@pytest.mark.parametrize("n", [4, 300])
+def test_offsets_that_overlap_stay_in_bounds(K, n):
+    """Offsets that are not as documented (every other member is the whole): more parts than there are slots, and
+    nothing outside the tensors is touched.  The members that the first slots hold are right."""
+    T = 1500
+    d = make(28, 1, T, 1, 1, 64, 64, BF16, decay="head")
+    cu = torch.tensor([0, T] * (n // 2) + [0], dtype=torch.int32, device="cuda")
+    out, fin = K.kda_lin_chunk_fwd(**d, cu_seqlens=cu)
+    ref = reference(d)
+    R.check_lin(out, fin[:1], ref)
+    assert not fin[1].any()
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("T", [130, 2500])
 def test_resume_in_place_equals_one_call(K, dt, T):
     d = make(15, 1, T, 2, 2, 128, 128, dt, init=1)

@@ -71,13 +71,16 @@ def test_chunk_pointers(K):
 
 def test_chunk_workspace(K):
     d = lin(K, batch=1, num_seqs=1, seqlen=1 << 16, dv=128)
-    need = K.lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(d))
+    for packed in (0, 1):      # one slot of state and decay per head and part but the last
+        need = K.lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(d), packed)
+        assert need > 0 and need % (4 * (128 * 128 * 4 + 8)) == 0 and need <= 4 * 160 * (128 * 128 * 4 + 8)
+    need = K.lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(d), 0)
     if need:
         assert chunk(K, d, ws=None) == K.KDA_ERR_NULL
         assert chunk(K, d, wb=need - 1) == K.KDA_ERR_WORKSPACE
         assert chunk(K, d, ws=FAKE + 8) == K.KDA_ERR_ALIGN
-    assert K.lib().kda_lin_chunk_fwd_workspace_bytes(None) == 0
-    assert K.lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(lin(K, heads=0))) == 0
+    assert K.lib().kda_lin_chunk_fwd_workspace_bytes(None, 0) == 0
+    assert K.lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(lin(K, heads=0)), 1) == 0
 
 
 @pytest.mark.parametrize("kw,code", [

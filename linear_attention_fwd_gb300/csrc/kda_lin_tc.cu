@@ -206,141 +206,128 @@ __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
 
 // The work of a CTA: part p of P of sequence n's chunks, [p nc / P, (p + 1) nc / P), for head h.  A
 // sequence that is cut (see cut_of) has ceil(nc / target) parts (at most kMaxParts); its parts other than
-// the last have a slot each for states (`slot`: the sequence's first; a sequence that finds too few
-// left is not cut).
+// the last have a slot each for states (`slot`: the sequence's first).  P = 0: nothing.
 struct Piece {
-    int n, h, p, P, slot;
+    int n, h, p, P, slot, bos, eos, pad;
 };
-constexpr int kMaxParts = 32, kRanked = 256;   // (every kernel here has at least kRanked threads)
+static_assert(sizeof(Piece) == 32, "two 16-byte words");
+constexpr int kMaxParts = 32;
 
 struct CutRule {
     int most, target;   // sequences of more than `most` chunks are cut, into parts of about `target`
     int slots;
 };
-__device__ __forceinline__ int seq_parts(const LinArgs &a, int n, const CutRule &cut) {
-    int64_t b, e;
-    lin_range(a, n, b, e);
-    const int64_t nc = (e - b + C - 1) / C;
-    if (nc <= cut.most) return 1;
-    const int64_t parts = (nc + cut.target - 1) / cut.target;
-    return parts > kMaxParts ? kMaxParts : (int)parts;
+
+// Dense batches: the piece of CTA b by arithmetic.  kFullPass: over all parts, else over all but each
+// sequence's last.
+template <bool kFullPass>
+__device__ __forceinline__ Piece dense_piece(const LinArgs &a, int b, const CutRule &cut) {
+    const int P = cut.slots / a.num_seqs + 1, per = (kFullPass ? P : P - 1) * a.heads, n = b / per;
+    return {n, b % a.heads, b % per / a.heads, P, n * (P - 1), (int)(n * a.seqlen), (int)((n + 1) * a.seqlen), 0};
 }
 
-// The piece of CTA `b` (block-wide for packed sequences; false when there is none).  kFullPass: over all
-// parts, else over all but each sequence's last.  Packed sequences come longest first (up to kRanked of them; the hardware
-// dispatches low blocks first), each one's parts and heads together.
-template <bool kFullPass>
-__device__ __forceinline__ bool dense_piece(const LinArgs &a, int b, const CutRule &cut, Piece &out) {
-    const int P = cut.slots / a.num_seqs + 1, per = (kFullPass ? P : P - 1) * a.heads;
-    out.n = b / per;
-    out.p = b % per / a.heads;
-    out.h = b % a.heads;
-    out.P = P;
-    out.slot = out.n * (P - 1);
-    return true;
-}
-template <bool kFullPass, int THREADS>
-__device__ bool packed_piece(const LinArgs &a, int b, const CutRule &cut, Piece &out) {
-    const int H = a.heads, N = a.num_seqs, t = threadIdx.x;
-    __shared__ int s_n, s_parts[kRanked], s_len[kRanked];
-    __shared__ long long s_start, s_slot, s_sum[2][THREADS / 32];
-    if (t == 0) s_n = -1;
-    auto blocks = [&](int parts) { return (long long)(kFullPass ? parts : parts - 1) * H; };
-    if (N <= kRanked) {
-        if (t < N) {
-            int64_t x, y;
-            lin_range(a, t, x, y);
-            s_len[t] = (int)(y - x);
-            s_parts[t] = seq_parts(a, t, cut);
+// Packed sequences: one CTA makes the lists of pieces, `pre` of all parts but each sequence's last, `full`
+// of all, longest sequences first (the hardware dispatches low blocks first; more than kPlanThreads of them
+// keep their order); what is left of the lists is P = 0.  A sequence that would need more slots than there
+// are is not cut (only offsets that are not as documented come to that).  The lists are made here and
+// not by each CTA for itself because that search, merely by being in the main kernel, cost its loops 40 %.
+constexpr int kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads) lin_plan_kernel(const LinArgs a, const CutRule cut, Piece *pre, int pre_n, Piece *full, int full_n) {
+    __shared__ int s_len[kPlanThreads], s_parts[kPlanThreads], s_slot[kPlanThreads], s_first[kPlanThreads], s_pre[kPlanThreads];
+    __shared__ int s_sum[3][kPlanThreads / 32];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, N = a.num_seqs, H = a.heads;
+    int used = 0, seqs = 0, cuts = 0;   // of the tiles before: slots asked for, parts, parts but each sequence's last
+    for (int base = 0; base < N; base += kPlanThreads) {
+        const int here = N - base < kPlanThreads ? N - base : kPlanThreads;
+        int64_t b = 0, e = 0;
+        if (t < here) lin_range(a, base + t, b, e);
+        const int len = (int)(e - b), nc = (len + C - 1) / C;
+        int parts = t < here ? 1 : 0;
+        if (t < here && nc > cut.most) {
+            parts = (nc + cut.target - 1) / cut.target;
+            if (parts > kMaxParts) parts = kMaxParts;
         }
         __syncthreads();
-        if (t == 0) {   // in the sequences' order: those that still find slots are cut
-            long long used = 0;
-            for (int i = 0; i < N; ++i) {
-                if (used + s_parts[i] - 1 > cut.slots) s_parts[i] = 1;
-                used += s_parts[i] - 1;
-            }
-        }
-        __syncthreads();
-        if (t < N) {
-            long long first = 0, slot = 0;
-            const int len = s_len[t];
-            for (int i = 0; i < N; ++i) {
-                if (s_len[i] > len || (s_len[i] == len && i < t)) first += blocks(s_parts[i]);
-                if (i < t) slot += s_parts[i] - 1;
-            }
-            if (first <= b && b < first + blocks(s_parts[t])) {
-                s_n = t;
-                s_start = first;
-                s_slot = slot;
-            }
-        }
-        __syncthreads();
-        if (s_n < 0) return false;
-        out.P = s_parts[s_n];
-    } else {
-        long long run = 0, run_slot = 0;
-        for (int base = 0; base < N; base += THREADS) {
-            const int n = base + t, lane = t & 31, warp = t >> 5;
-            const int parts = n < N ? seq_parts(a, n, cut) : 1;
-            const long long w = n < N ? blocks(parts) : 0, ws = parts - 1;
-            long long v = w, vs = ws;
+        // slots before this sequence; one that would leave them is not cut, nor are those after it
+        auto scan = [&](int x, int row) {   // exclusive over the block; the total in s_sum[row] of the last warp's end
+            int v = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, v, o), ys = __shfl_up_sync(0xffffffffu, vs, o);
-                if (lane >= o) {
-                    v += y;
-                    vs += ys;
+                const int y = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += y;
+            }
+            if (lane == 31) s_sum[row][warp] = v;
+            __syncthreads();
+            int off = 0;
+            for (int i = 0; i < warp; ++i) off += s_sum[row][i];
+            return off + v - x;
+        };
+        auto total = [&](int row) {
+            int x = 0;
+            for (int i = 0; i < kPlanThreads / 32; ++i) x += s_sum[row][i];
+            return x;
+        };
+        int slot = used + scan(parts > 0 ? parts - 1 : 0, 0);
+        if (parts > 1 && slot + parts - 1 > cut.slots) parts = 1;
+        s_len[t] = t < here ? len : -1;
+        s_parts[t] = parts;
+        s_slot[t] = slot;
+        __syncthreads();
+        // parts before this sequence, longest first when one tile holds them all
+        int first = 0, before = 0;
+        if (N <= kPlanThreads) {
+            if (t < here)
+                for (int i = 0; i < here; ++i) {
+                    const bool ahead = s_len[i] > len || (s_len[i] == len && i < t);
+                    first += ahead ? s_parts[i] : 0;
+                    before += ahead ? s_parts[i] - 1 : 0;
                 }
-            }
-            __syncthreads();
-            if (lane == 31) {
-                s_sum[0][warp] = v;
-                s_sum[1][warp] = vs;
-            }
-            __syncthreads();
-            long long off = 0, tot = 0, offs = 0, tots = 0;
-            for (int i = 0; i < THREADS / 32; ++i) {
-                off += i < warp ? s_sum[0][i] : 0;
-                tot += s_sum[0][i];
-                offs += i < warp ? s_sum[1][i] : 0;
-                tots += s_sum[1][i];
-            }
-            const long long first = run + off + v - w;
-            if (n < N && first <= b && b < first + w) {
-                s_n = n;
-                s_start = first;
-                s_slot = run_slot + offs + vs - ws;
-            }
-            run += tot;
-            run_slot += tots;
+        } else {
+            first = seqs + scan(parts, 1);
+            before = cuts + scan(parts > 0 ? parts - 1 : 0, 2);
+        }
+        s_first[t] = first;
+        s_pre[t] = before;
+        used += total(0);
+        if (N > kPlanThreads) {
+            seqs += total(1);
+            cuts += total(2);
         }
         __syncthreads();
-        if (s_n < 0) return false;
-        out.P = seq_parts(a, s_n, cut);
-        // (the host's bound on the slots holds for offsets as documented; others must not leave them)
-        if (s_slot + out.P - 1 > cut.slots) {
-            if (!kFullPass || b - s_start >= H) return false;
-            out.P = 1;
+        for (int i = warp; i < here; i += kPlanThreads / 32) {   // a warp per sequence
+            int64_t sb, se;
+            lin_range(a, base + i, sb, se);
+            const int P = s_parts[i];
+            for (int x = lane; x < P * H; x += 32) {
+                const Piece piece{base + i, x % H, x / H, P, s_slot[i], (int)sb, (int)se, 0};
+                const int f = s_first[i] * H + x, q = s_pre[i] * H + x;
+                if (f < full_n) full[f] = piece;
+                if (x < (P - 1) * H && q < pre_n) pre[q] = piece;
+            }
+        }
+        if (N <= kPlanThreads) {   // all parts of all sequences
+            int x = 0, y = 0;
+            for (int i = 0; i < here; ++i) {
+                x += s_parts[i];
+                y += s_parts[i] - 1;
+            }
+            seqs = x;
+            cuts = y;
         }
     }
-    out.n = s_n;
-    out.p = (int)((b - s_start) / H);
-    out.h = (int)((b - s_start) % H);
-    out.slot = (int)s_slot;
-    return true;
+    for (int x = seqs * H + t; x < full_n; x += kPlanThreads) full[x].P = 0;
+    for (int x = cuts * H + t; x < pre_n; x += kPlanThreads) pre[x].P = 0;
 }
 
 // kFullPass: the whole forward of a part; a part other than the first starts from the state in the slot
 // of the part before it.  Otherwise only the state that a part reaches from zero, into its slot of
 // `locals`, and its total log2 decay; lin_scan_kernel then turns each slot into the true state behind
 // its part.
-// kPacked: an instantiation of its own for dense batches, whose pieces are arithmetic on the block's number
-// (uniform values throughout): the shared one ran them at 336 us instead of 310 (B=4 H=32 T=8192).
-template <bool kFullPass, bool kPacked>
+template <bool kFullPass>
 __global__ void __launch_bounds__(NT, 1)
 kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                        const __grid_constant__ CUtensorMap tmv, const LinArgs a, const CutRule cut, float *locals, double *decays) {
+                        const __grid_constant__ CUtensorMap tmv, const LinArgs a, const CutRule cut, const Piece *plan,
+                        float *locals, double *decays) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_fail;
     __shared__ volatile int s_piece[4];   // unit, the part's slot, whether it is the last (read again at the end:
@@ -349,13 +336,11 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int H = a.heads;
-    Piece piece;
-    if (!(kPacked ? packed_piece<kFullPass, NT>(a, blockIdx.x, cut, piece) : dense_piece<kFullPass>(a, blockIdx.x, cut, piece))) return;
+    const Piece piece = plan ? plan[blockIdx.x] : dense_piece<kFullPass>(a, blockIdx.x, cut);
     const int n = piece.n, h = piece.h, p = piece.p, P = piece.P, slot = piece.slot;
+    if (P == 0) return;
     const int hk = h / (H / a.qk_heads);
-    int64_t bos64, eos64;
-    lin_range(a, n, bos64, eos64);
-    const int bos = (int)bos64, eos = (int)eos64;      // tokens are counted in 31 bits
+    const int bos = piece.bos, eos = piece.eos;        // tokens are counted in 31 bits
     const int nc = (eos - bos + C - 1) / C;
     const int c_lo = (int)((int64_t)p * nc / P), c_hi = (int)((int64_t)(p + 1) * nc / P);
     const int chunks = c_hi - c_lo;
@@ -815,10 +800,9 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
 // the part's own from zero.  One CTA per slot, head and 1024 values; those of a sequence's first slot
 // walk its parts.
 constexpr int kScanThreads = 256;
-__global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const LinArgs a, const CutRule cut, float *locals, const double *decays) {
-    Piece piece;
-    const bool some = a.cu ? packed_piece<false, kScanThreads>(a, blockIdx.x, cut, piece) : dense_piece<false>(a, blockIdx.x, cut, piece);
-    if (!some || piece.p != 0) return;
+__global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const LinArgs a, const CutRule cut, const Piece *plan, float *locals, const double *decays) {
+    const Piece piece = plan ? plan[blockIdx.x] : dense_piece<false>(a, blockIdx.x, cut);
+    if (piece.P == 0 || piece.p != 0) return;
     const int H = a.heads;
     const int64_t size = (int64_t)a.dk * a.dv, at = ((int64_t)blockIdx.y * kScanThreads + threadIdx.x) * 4;
     float4 s = a.s0 ? *reinterpret_cast<const float4 *>(a.s0 + ((int64_t)piece.n * H + piece.h) * size + at) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -909,8 +893,10 @@ static Cut cut_of(int64_t tokens, int64_t num_seqs, int64_t heads, bool packed, 
     return c;
 }
 
+// The workspace: the parts' states, their decays, and for packed sequences the two lists of pieces.
 size_t lin_chunk_tc_workspace_bytes(int64_t tokens, int64_t num_seqs, int64_t heads, int dk, int dv, bool packed) {
-    return (size_t)cut_of(tokens, num_seqs, heads, packed, false).rule.slots * heads * ((size_t)dk * dv * 4 + 8);
+    const Cut c = cut_of(tokens, num_seqs, heads, packed, false);
+    return (size_t)c.rule.slots * heads * ((size_t)dk * dv * 4 + 8) + (packed ? (size_t)(c.pre + c.full) * sizeof(Piece) + 16 : 0);
 }
 
 cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, bool whole, cudaStream_t st) {
@@ -923,21 +909,25 @@ cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, bool whole, c
         return cudaErrorInvalidValue;
     float *locals = static_cast<float *>(workspace);
     double *decays = reinterpret_cast<double *>(locals + (int64_t)c.rule.slots * a.heads * a.dk * a.dv);
-    auto launch = [&](auto kernel, int64_t ctas) {
+    Piece *pre = nullptr, *full = nullptr;
+    if (a.cu) {
+        pre = reinterpret_cast<Piece *>((reinterpret_cast<uintptr_t>(decays + (int64_t)c.rule.slots * a.heads) + 15) & ~uintptr_t(15));
+        full = pre + c.pre;
+        lin_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, c.rule, pre, (int)c.pre, full, (int)c.full);
+    }
+    auto launch = [&](auto kernel, int64_t ctas, const Piece *plan) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
         if (e != cudaSuccess) return e;
-        kernel<<<(unsigned)ctas, NT, SMEM_BYTES, st>>>(mq, mk, mv, a, c.rule, locals, decays);
+        kernel<<<(unsigned)ctas, NT, SMEM_BYTES, st>>>(mq, mk, mv, a, c.rule, plan, locals, decays);
         return cudaGetLastError();
     };
     if (c.pre > 0) {
-        cudaError_t e = a.cu ? launch(kda_lin_chunk_tc_kernel<false, true>, c.pre) : launch(kda_lin_chunk_tc_kernel<false, false>, c.pre);
+        const cudaError_t e = launch(kda_lin_chunk_tc_kernel<false>, c.pre, pre);
         if (e != cudaSuccess) return e;
         const dim3 grid((unsigned)c.pre, (unsigned)(a.dk * a.dv / (4 * kScanThreads)));
-        lin_scan_kernel<<<grid, kScanThreads, 0, st>>>(a, c.rule, locals, decays);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
+        lin_scan_kernel<<<grid, kScanThreads, 0, st>>>(a, c.rule, pre, locals, decays);
     }
-    return a.cu ? launch(kda_lin_chunk_tc_kernel<true, true>, c.full) : launch(kda_lin_chunk_tc_kernel<true, false>, c.full);
+    return launch(kda_lin_chunk_tc_kernel<true>, c.full, full);
 }
 
 }  // namespace kda

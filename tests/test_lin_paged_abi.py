@@ -71,9 +71,11 @@ def test_chunk_pointers(K):
 
 def test_chunk_workspace(K):
     d = lin(K, batch=1, num_seqs=1, seqlen=1 << 16, dv=128)
-    for packed in (0, 1):      # one slot of state and decay per head and part but the last
-        need = K.lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(d), packed)
-        assert need > 0 and need % (4 * (128 * 128 * 4 + 8)) == 0 and need <= 4 * 160 * (128 * 128 * 4 + 8)
+    slot = 128 * 128 * 4 + 8   # one slot of state and decay per head and part but the last; packed: lists of pieces too
+    need = K.lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(d), 0)
+    assert need > 0 and need % (4 * slot) == 0 and need <= 160 * slot
+    assert 0 < K.lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(d), 1) <= 4 * 160 * (slot + 64) + 4 * 32 + 16
+    assert K.lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(lin(K, dtype=0, batch=1, num_seqs=1, seqlen=1 << 16)), 1) == 0
     need = K.lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(d), 0)
     if need:
         assert chunk(K, d, ws=None) == K.KDA_ERR_NULL

@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan_kernel(const LinArgs a,
     __shared__ int s_len[kPlanThreads], s_parts[kPlanThreads], s_slot[kPlanThreads], s_first[kPlanThreads], s_pre[kPlanThreads];
     __shared__ int s_sum[3][kPlanThreads / 32];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, N = a.num_seqs, H = a.heads;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int used = 0, seqs = 0, cuts = 0;   // of the tiles before: slots asked for, parts, parts but each sequence's last
     for (int base = 0; base < N; base += kPlanThreads) {
         const int here = N - base < kPlanThreads ? N - base : kPlanThreads;
@@ -336,6 +337,8 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int H = a.heads;
+    // (launched before the kernel ahead of it has ended, see launch_lin_chunk_tc)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const Piece piece = plan ? plan[blockIdx.x] : dense_piece<kFullPass>(a, blockIdx.x, cut);
     const int n = piece.n, h = piece.h, p = piece.p, P = piece.P, slot = piece.slot;
     if (P == 0) return;
@@ -579,6 +582,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 mbar_arrive(bar(kReady));
                 const int m0 = i < nr ? i : nr - 1, m1 = i + 8 < nr ? i + 8 : nr - 1;   // the last key of each row
                 const float gh0 = gv[i], gh1 = gv[i + 8], gl0 = gv[64 + i], gl1 = gv[72 + i];
+                const float2 neg = make_float2(-1.f, -1.f);
                 float2 hj[3], lj[3];
 #pragma unroll
                 for (int b = 0; b < 3; ++b) {
@@ -596,8 +600,9 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                         const float gh = hh ? gh1 : gh0, gl = hh ? gl1 : gl0;
                         const int m = hh ? m1 : m0;
                         float2 x;
-                        x.x = j <= m ? acc[b][2 * hh] * ex2((gh - hj[b].x) + (gl - lj[b].x)) : 0.f;
-                        x.y = j < m ? acc[b][2 * hh + 1] * ex2((gh - hj[b].y) + (gl - lj[b].y)) : 0.f;
+                        const float2 d = __fadd2_rn(__ffma2_rn(hj[b], neg, make_float2(gh, gh)), __ffma2_rn(lj[b], neg, make_float2(gl, gl)));
+                        x = __fmul2_rn(make_float2(acc[b][2 * hh], acc[b][2 * hh + 1]), make_float2(ex2(d.x), ex2(d.y)));
+                        x = make_float2(j <= m ? x.x : 0.f, j < m ? x.y : 0.f);
                         *reinterpret_cast<uint32_t *>(to + 1024 * hh) = take_bf16(x);
                         *reinterpret_cast<uint32_t *>(to + 1024 * hh + 8192) = pack_bf16(x.x, x.y);
                     }
@@ -915,19 +920,31 @@ cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, bool whole, c
         full = pre + c.pre;
         lin_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, c.rule, pre, (int)c.pre, full, (int)c.full);
     }
-    auto launch = [&](auto kernel, int64_t ctas, const Piece *plan) {
+    // A kernel right behind the list's maker may be launched before that one has ended (it waits for it at its
+    // start): its launch is then over when the list is there.
+    auto launch = [&](auto kernel, int64_t ctas, const Piece *plan, bool behind_plan) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
         if (e != cudaSuccess) return e;
-        kernel<<<(unsigned)ctas, NT, SMEM_BYTES, st>>>(mq, mk, mv, a, c.rule, plan, locals, decays);
-        return cudaGetLastError();
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)ctas);
+        cfg.blockDim = dim3(NT);
+        cfg.dynamicSmemBytes = SMEM_BYTES;
+        cfg.stream = st;
+        cfg.attrs = at;
+        cfg.numAttrs = behind_plan ? 1 : 0;
+        return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a, c.rule, plan, locals, decays);
     };
     if (c.pre > 0) {
-        const cudaError_t e = launch(kda_lin_chunk_tc_kernel<false>, c.pre, pre);
+        const cudaError_t e = launch(kda_lin_chunk_tc_kernel<false>, c.pre, pre, a.cu != nullptr);
         if (e != cudaSuccess) return e;
         const dim3 grid((unsigned)c.pre, (unsigned)(a.dk * a.dv / (4 * kScanThreads)));
         lin_scan_kernel<<<grid, kScanThreads, 0, st>>>(a, c.rule, pre, locals, decays);
+        if (cudaGetLastError() != cudaSuccess) return cudaErrorLaunchFailure;
     }
-    return launch(kda_lin_chunk_tc_kernel<true>, c.full, full);
+    return launch(kda_lin_chunk_tc_kernel<true>, c.full, full, a.cu != nullptr && c.pre == 0);
 }
 
 }  // namespace kda

@@ -1,6 +1,10 @@
 // Paged key-value cache: append, and attention of one new token per row.
+#include <cooperative_groups.h>
+
 #include "kda_lin.h"
 #include "tc_ptx.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace kda {
 namespace {
@@ -67,6 +71,9 @@ __global__ void __launch_bounds__(kAppendThreads) kda_paged_append_kernel(Append
 // device, since the host does not see the lengths.  A unit that ends up in several shares leaves
 // one partial (running maximum, sum, unnormalised output) per share in the workspace, and a second
 // kernel joins them in the order of the tokens, so results do not depend on timing.
+// Where the rows can only be short (a row's share of the longest possible one at most kShortTokens),
+// one cluster of CTAs takes a unit instead, equal parts each, and joins them through distributed shared
+// memory: one launch and no workspace (one row of 777 tokens, 8 key/value heads: 5.6 us against 8.2).
 //
 // Within a CTA each of 4 warps takes every fourth group of tokens through a ring of its own (three
 // stages of cp.async, page numbers fetched one group ahead), so that the loop has no barrier wider
@@ -96,6 +103,7 @@ struct AttArgs {
     FastDiv by_page;
     int32_t rep, blocks, rp;   // query heads per key/value head, head blocks, heads per block
     float *part_o, *part_ml;   // partials: [2 G][rp][D], [2 G][rp][2]
+    int32_t cluster;           // CTAs of a unit (short rows)
 };
 
 __device__ __forceinline__ int row_length(const PagedArgs &a, int n) {
@@ -185,7 +193,7 @@ template <typename T, int D> struct Att {
     static __device__ __forceinline__ int swz(int r) { return kF32 ? ((r & 1) << 2) | ((r >> 1) & 3) : (r & 7); }
 };
 
-template <typename T, int D, int RP>
+template <typename T, int D, int RP, bool kShort>
 __global__ void __launch_bounds__(kAttThreads, 2) kda_paged_attention_kernel(const AttArgs a) {
     using A = Att<T, D>;
     using namespace ptx;
@@ -194,25 +202,34 @@ __global__ void __launch_bounds__(kAttThreads, 2) kda_paged_attention_kernel(con
     __shared__ uint32_t sm_mask[kWarps][kStages];
     __shared__ float sm_m[kWarps][RP], sm_l[kWarps][RP];
     __shared__ __align__(16) float sm_q[A::kF32 ? RP : 1][A::kF32 ? D : 4];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ float sm_pm[kShort ? RP : 1], sm_pl[kShort ? RP : 1];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const PagedArgs &p = a.p;
     const int per = p.kv_heads * a.blocks;
-    // this CTA's share of the items
-    long long mine = 0;
-    for (int n = tid; n < p.rows; n += kAttThreads) mine += row_tiles(p, n);
-    const long long W = per * block_sum<kAttThreads>(mine, sm_sum);
-    const long long G = W < gridDim.x ? W : gridDim.x;   // shares: at least one item each
-    if (blockIdx.x >= G) return;
-    const long long x1 = (blockIdx.x + 1) * W / G;
-    long long x = blockIdx.x * W / G;
-    int n;
-    long long us;   // the current unit's first item
-    find_row<kAttThreads>(p, per, x, sm_sum, n, us);
-    int tiles = row_tiles(p, n);
-    int unit = (int)((x - us) / tiles);   // key/value head and head block within the row
-    us += (long long)unit * tiles;
+    long long x, x1, us = 0;   // this CTA's share of the items; the current unit's first item
+    int n, tiles, unit;        // row, its tiles, key/value head and head block within it
+    if constexpr (kShort) {
+        const int ru = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
+        n = ru / per;
+        unit = ru % per;
+        tiles = row_tiles(p, n);
+        x = (long long)rank * tiles / a.cluster;
+        x1 = (long long)(rank + 1) * tiles / a.cluster;
+    } else {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        long long mine = 0;
+        for (int i = tid; i < p.rows; i += kAttThreads) mine += row_tiles(p, i);
+        const long long W = per * block_sum<kAttThreads>(mine, sm_sum);
+        const long long G = W < gridDim.x ? W : gridDim.x;   // shares: at least one item each
+        if (blockIdx.x >= G) return;
+        x1 = (blockIdx.x + 1) * W / G;
+        x = blockIdx.x * W / G;
+        find_row<kAttThreads>(p, per, x, sm_sum, n, us);
+        tiles = row_tiles(p, n);
+        unit = (int)((x - us) / tiles);
+        us += (long long)unit * tiles;
+    }
 
     uint8_t *ring = ring_all + warp * A::RING;
     const uint32_t ring_s = smem_u32(ring);
@@ -225,7 +242,7 @@ __global__ void __launch_bounds__(kAttThreads, 2) kda_paged_attention_kernel(con
         const int heads = a.rep - h0 < RP ? a.rep - h0 : RP;      // query heads of this block
         const int64_t hq = (int64_t)n * p.heads + (int64_t)hk * a.rep + h0;
         const long long xe = us + tiles < x1 ? us + tiles : x1;
-        const bool whole = x == us && xe == us + tiles;
+        const bool whole = kShort ? a.cluster == 1 : x == us && xe == us + tiles;
         const int len = row_length(p, n);
         const int ta = (int)(x - us) * kTile;
         const int tb = (int)(xe - us) * kTile < len ? (int)(xe - us) * kTile : len;
@@ -493,6 +510,12 @@ __global__ void __launch_bounds__(kAttThreads, 2) kda_paged_attention_kernel(con
             if (whole) {
                 static_cast<T *>(p.out)[hq * D + c] = from_f<T>(sum == 0.f ? 0.f : acc / sum);
                 if (p.lse && c % D == 0) p.lse[hq + r] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+            } else if constexpr (kShort) {
+                reinterpret_cast<float *>(ring_all)[c] = acc;   // (read by this thread alone)
+                if (c % D == 0) {
+                    sm_pm[r] = mx;
+                    sm_pl[r] = sum;
+                }
             } else {
                 a.part_o[slot * RP * D + c] = acc;
                 if (c % D == 0) {
@@ -500,6 +523,27 @@ __global__ void __launch_bounds__(kAttThreads, 2) kda_paged_attention_kernel(con
                     a.part_ml[(slot * RP + r) * 2 + 1] = sum;
                 }
             }
+        }
+        if constexpr (kShort) {
+            if (whole) break;
+            cg::cluster_group cluster = cg::this_cluster();
+            cluster.sync();
+            for (int c = tid + kAttThreads * (int)cluster.block_rank(); c < heads * D; c += kAttThreads * a.cluster) {
+                const int r = c / D;
+                float mx = -INFINITY;
+                for (int e = 0; e < a.cluster; ++e) mx = fmaxf(mx, cluster.map_shared_rank(sm_pm, e)[r]);
+                const float z = mx == -INFINITY ? 0.f : mx;
+                float sum = 0.f, acc = 0.f;
+                for (int e = 0; e < a.cluster; ++e) {
+                    const float f = ex2(cluster.map_shared_rank(sm_pm, e)[r] - z);
+                    sum = fmaf(cluster.map_shared_rank(sm_pl, e)[r], f, sum);
+                    acc = fmaf(reinterpret_cast<const float *>(cluster.map_shared_rank(ring_all, e))[c], f, acc);
+                }
+                static_cast<T *>(p.out)[hq * D + c] = from_f<T>(sum == 0.f ? 0.f : acc / sum);
+                if (p.lse && c % D == 0) p.lse[hq + r] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+            }
+            cluster.sync();   // the others have read this CTA's part
+            break;
         }
         x = xe;
         if (x >= x1) break;
@@ -571,23 +615,44 @@ __global__ void __launch_bounds__(D) kda_paged_join_kernel(const AttArgs a, cons
 // holds a key/value head's (more heads than that read the keys and values once per block).
 int heads_per_block(kda_dtype_t dt, int rep) { return dt == KDA_BF16 ? 16 : (rep == 1 ? 1 : (rep <= 4 ? 4 : 8)); }
 
+// Rows no longer than kShortTokens per CTA of a cluster take the one-launch form (a.cluster CTAs a unit):
+// as many CTAs as two per SM, up to 8.  0: the rows may be longer.
+constexpr int kShortTokens = 1024, kMaxCluster = 8;
+int short_cluster(int64_t units, int64_t max_tokens) {
+    int c = kMaxCluster;
+    while (c > 1 && units * c > kCtas) c /= 2;
+    return max_tokens <= (int64_t)c * kShortTokens ? c : 0;
+}
+
 template <typename T, int D, int RP>
 cudaError_t launch_att(const AttArgs &a, int grid, cudaStream_t st) {
     constexpr int smem = kWarps * Att<T, D>::RING;
     static_assert(RP * D * 4 <= Att<T, D>::RING, "a warp's outputs fit its ring");
-    cudaError_t e = cudaFuncSetAttribute(kda_paged_attention_kernel<T, D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    kda_paged_attention_kernel<T, D, RP><<<grid, kAttThreads, smem, st>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || grid == 1 || (int64_t)a.p.max_pages * a.p.page_size <= kTile) return e;   // nothing is split
     cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    cfg.stream = st;
+    cfg.attrs = at;
+    if (a.cluster) {
+        const cudaError_t e = cudaFuncSetAttribute(kda_paged_attention_kernel<T, D, RP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        cfg.gridDim = dim3((unsigned)((int64_t)a.p.rows * a.p.kv_heads * a.blocks * a.cluster));
+        cfg.blockDim = dim3(kAttThreads);
+        cfg.dynamicSmemBytes = smem;
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)a.cluster;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+        return cudaLaunchKernelEx(&cfg, kda_paged_attention_kernel<T, D, RP, true>, a);
+    }
+    cudaError_t e = cudaFuncSetAttribute(kda_paged_attention_kernel<T, D, RP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kda_paged_attention_kernel<T, D, RP, false><<<grid, kAttThreads, smem, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || grid == 1) return e;   // (one CTA: nothing is split)
     cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)(a.rep < RP ? a.rep : RP));
     cfg.blockDim = dim3(D);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];   // the join's CTAs may start, find their parts and wait before the first kernel has ended
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // the join's CTAs may start, find their parts
+    at[0].val.programmaticStreamSerializationAllowed = 1;            // and wait before the first kernel has ended
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kda_paged_join_kernel<T, D>, a, grid);
 }
@@ -609,7 +674,7 @@ cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st) {
 
 size_t paged_attention_workspace_bytes(int64_t rows, int heads, int kv_heads, int64_t max_tokens, int d, kda_dtype_t dt) {
     const int rep = heads / kv_heads, rp = heads_per_block(dt, rep), blocks = (rep + rp - 1) / rp;
-    if (rows <= 0 || max_tokens <= kTile) return 0;
+    if (rows <= 0 || short_cluster(rows * kv_heads * blocks, max_tokens)) return 0;
     return (size_t)attention_ctas(rows, (int64_t)kv_heads * blocks, max_tokens) * 2 * rp * (d + 2) * 4;
 }
 
@@ -617,7 +682,8 @@ cudaError_t launch_paged_attention(const PagedArgs &p, int d, kda_dtype_t dt, vo
     const int rep = p.heads / p.kv_heads, rp = heads_per_block(dt, rep), blocks = (rep + rp - 1) / rp;
     const int grid = attention_ctas(p.rows, (int64_t)p.kv_heads * blocks, (int64_t)p.max_pages * p.page_size);
     float *ws = static_cast<float *>(workspace);
-    const AttArgs a{p, FastDiv((uint32_t)p.page_size), rep, blocks, rp, ws, ws ? ws + (size_t)grid * 2 * rp * d : nullptr};
+    const AttArgs a{p, FastDiv((uint32_t)p.page_size), rep, blocks, rp, ws, ws ? ws + (size_t)grid * 2 * rp * d : nullptr,
+                    short_cluster((int64_t)p.rows * p.kv_heads * blocks, (int64_t)p.max_pages * p.page_size)};
     if (dt == KDA_BF16)
         return d == 128 ? launch_att<__nv_bfloat16, 128, 16>(a, grid, st) : launch_att<__nv_bfloat16, 64, 16>(a, grid, st);
     if (d == 128)

@@ -10,55 +10,70 @@ namespace kda {
 namespace {
 
 // ------------------------------------------------------------------ append
-// A CTA moves kTokens consecutive tokens: one thread per token finds the token's place (row by
-// bisection in the offsets, then page and offset), then all threads copy 16-byte vectors.  Bound
-// by one read and one write of the new rows.
-constexpr int kTokens = 8, kAppendThreads = 256;
+// A CTA moves `per` consecutive tokens, a vector of 16 bytes of keys and one of values per thread and step.
+// The first kAhead vectors of each are requested before the tokens' places are known: one thread per
+// token finds its place (row by bisection in the offsets, then page and offset).  Bound by one read and
+// one write of the new rows (49,700 tokens of 8 x 128 bf16: 30.6 us, 82 % of the measured copy rate;
+// 32 us when the places come first).
+constexpr int kAppendThreads = 256, kAhead = 4, kMaxTokens = 32;
 
-__global__ void __launch_bounds__(kAppendThreads) kda_paged_append_kernel(AppendArgs a) {
-    __shared__ int64_t place[kTokens];   // the token's index in the cache, or -1
-    const int64_t u0 = (int64_t)blockIdx.x * kTokens;
-    if (threadIdx.x < kTokens) {
+__global__ void __launch_bounds__(kAppendThreads) kda_paged_append_kernel(const AppendArgs a, const int per) {
+    __shared__ int64_t place[kMaxTokens];   // the token's index in the cache, or -1
+    const int64_t u0 = (int64_t)blockIdx.x * per;
+    const int tokens = a.tokens - u0 < per ? (int)(a.tokens - u0) : per, vecs = tokens * a.row_vecs;
+    const uint4 *k = static_cast<const uint4 *>(a.k) + u0 * a.row_vecs, *v = static_cast<const uint4 *>(a.v) + u0 * a.row_vecs;
+    uint4 kv[kAhead], vv[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+        const int x = threadIdx.x + kAppendThreads * e;
+        if (x < vecs) {
+            kv[e] = __ldcs(k + x);
+            vv[e] = __ldcs(v + x);
+        }
+    }
+    if (threadIdx.x < tokens) {
         const int64_t u = u0 + threadIdx.x;
         int64_t at = -1;
-        if (u < a.tokens) {
-            int row = (int)u;
-            int64_t first = u;
-            if (a.cu) {   // the last row that starts at or before u
-                int lo = 0, hi = a.rows;   // cu[lo] <= u < cu[hi]
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) / 2;
-                    if (__ldg(a.cu + mid) <= u) lo = mid;
-                    else hi = mid;
-                }
-                row = lo;
-                first = __ldg(a.cu + lo);
-                if (first > u || __ldg(a.cu + lo + 1) <= u) row = -1;
-                if (first < 0) first = 0;
+        int row = (int)u;
+        int64_t first = u;
+        if (a.cu) {   // the last row that starts at or before u
+            int lo = 0, hi = a.rows;   // cu[lo] <= u < cu[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (__ldg(a.cu + mid) <= u) lo = mid;
+                else hi = mid;
             }
-            if (row >= 0) {
-                const int64_t p = (int64_t)__ldg(a.positions + row) + (u - first);
-                if (p >= 0 && p < (int64_t)a.max_pages * a.page_size) {
-                    const int pg = (int)p / a.page_size;
-                    const int page = __ldg(a.table + (int64_t)row * a.max_pages + pg);
-                    if (page >= 0 && page < a.pages) at = (int64_t)page * a.page_size + ((int)p - pg * a.page_size);
-                }
+            row = lo;
+            first = __ldg(a.cu + lo);
+            if (first > u || __ldg(a.cu + lo + 1) <= u) row = -1;
+            if (first < 0) first = 0;
+        }
+        if (row >= 0) {
+            const int64_t p = (int64_t)__ldg(a.positions + row) + (u - first);
+            if (p >= 0 && p < (int64_t)a.max_pages * a.page_size) {
+                const int pg = (int)p / a.page_size;
+                const int page = __ldg(a.table + (int64_t)row * a.max_pages + pg);
+                if (page >= 0 && page < a.pages) at = (int64_t)page * a.page_size + ((int)p - pg * a.page_size);
             }
         }
         place[threadIdx.x] = at;
     }
     __syncthreads();
-    const uint4 *k = static_cast<const uint4 *>(a.k), *v = static_cast<const uint4 *>(a.v);
     uint4 *kc = static_cast<uint4 *>(a.k_cache), *vc = static_cast<uint4 *>(a.v_cache);
-    for (int x = threadIdx.x; x < kTokens * a.row_vecs; x += kAppendThreads) {
-        const int tk = x / a.row_vecs, c = x - tk * a.row_vecs;
+    auto store = [&](int x, const uint4 &key, const uint4 &value) {
+        const int tk = x / a.row_vecs;
         const int64_t at = place[tk];
-        if (at < 0) continue;
-        const int64_t src = (u0 + tk) * a.row_vecs + c, dst = at * a.row_vecs + c;
-        const uint4 kv = __ldcs(k + src), vv = __ldcs(v + src);
-        kc[dst] = kv;
-        vc[dst] = vv;
+        if (at < 0) return;
+        const int64_t to = at * a.row_vecs + (x - tk * a.row_vecs);
+        kc[to] = key;
+        vc[to] = value;
+    };
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+        const int x = threadIdx.x + kAppendThreads * e;
+        if (x < vecs) store(x, kv[e], vv[e]);
     }
+    for (int x = threadIdx.x + kAppendThreads * kAhead; x < vecs; x += kAppendThreads) store(x, __ldcs(k + x), __ldcs(v + x));
 }
 
 // ------------------------------------------------------------------ attention
@@ -667,8 +682,10 @@ int attention_ctas(int64_t rows, int64_t per, int64_t max_tokens) {
 }  // namespace
 
 cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st) {
-    const int64_t grid = (a.tokens + kTokens - 1) / kTokens;
-    kda_paged_append_kernel<<<(unsigned)grid, kAppendThreads, 0, st>>>(a);
+    // tokens of a CTA: what its threads request ahead, one at least
+    int per = kAppendThreads * kAhead / a.row_vecs;
+    per = per < 1 ? 1 : (per > kMaxTokens ? kMaxTokens : per);
+    kda_paged_append_kernel<<<(unsigned)((a.tokens + per - 1) / per), kAppendThreads, 0, st>>>(a, per);
     return cudaGetLastError();
 }
 

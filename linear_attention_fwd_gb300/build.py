@@ -1,4 +1,5 @@
-"""Build libkda.so in-tree for sm_103a (nvcc, no cmake).
+"""Build libkda.so in-tree for sm_103a (nvcc, no cmake), and _binding.so, the C++ side of the Python
+binding, with the host compiler.
 
 Each .cu under csrc/ compiles to its own object in parallel; the objects link
 into ``libkda.so`` beside this file.  The CUDA runtime is linked statically and
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkda.so")
 LIB_DEBUG = os.path.join(HERE, "libkda_debug.so")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-v"]
@@ -51,8 +54,39 @@ def _digest(paths, extra=""):
     return h.hexdigest()
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/binding.cpp against the installed PyTorch into _binding.so; returns its path."""
+    import torch
+    src = os.path.join(CSRC, "binding.cpp")
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    flags = ["-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda]
+    libs = ["torch_python", "torch_cuda", "torch_cpu", "c10_cuda", "c10"]
+    want = _digest([src, os.path.join(INCLUDE, "kda.h")], " ".join(flags + inc + [torch.__version__, sys.version]))
+    stamp = os.path.join(BUILD, "stamp_binding")
+    os.makedirs(BUILD, exist_ok=True)
+    if not force and os.path.exists(BINDING) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == want:
+                return BINDING
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), *flags, *(f"-I{i}" for i in inc), src, "-o", tmp,
+           f"-L{os.path.join(root, 'lib')}", *(f"-l{x}" for x in libs)]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(want)
+    return BINDING
+
+
 def build(verbose: bool = False, force: bool = False, debug: bool = False) -> str:
-    """Compile csrc/*.cu for sm_103a and link libkda.so; returns its path.
+    """Compile csrc/*.cu for sm_103a and link libkda.so (and build _binding.so beside it); returns the
+    library's path.
 
     debug=True builds libkda_debug.so instead (objects in _build_debug/): the same kernels with
     KDA_DEBUG_CHECKS defined, so that every chunk forward and decode call first checks g and the
@@ -66,6 +100,14 @@ def build(verbose: bool = False, force: bool = False, debug: bool = False) -> st
     hdr_digest = _digest(_headers(), " ".join(ARCH + flags))
     stamp = os.path.join(build_dir, "stamp")
     want = _digest(srcs, hdr_digest)
+    with ThreadPoolExecutor(max_workers=1) as side:   # beside the kernels; its errors are raised below
+        binding = side.submit(build_binding, force)
+        path = _build_library(verbose, force, build_dir, lib_path, flags, nvcc, srcs, stamp, want)
+        binding.result()
+    return path
+
+
+def _build_library(verbose, force, build_dir, lib_path, flags, nvcc, srcs, stamp, want) -> str:
     if not force and os.path.exists(lib_path) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read() == want:

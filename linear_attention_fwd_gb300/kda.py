@@ -8,7 +8,8 @@ the first call raises.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -135,9 +136,10 @@ def kda_status_string(status: int) -> str:
 def use_library(path: str) -> None:
     """Load libkda from `path` for the calls that follow (LIB_PATH, or DEBUG_LIB_PATH for the
     build with device-side input checks)."""
-    global _lib, LIB_PATH
+    global _lib, LIB_PATH, _binding
     LIB_PATH = path
     _lib = None
+    _binding = None
     lib()
 
 
@@ -488,86 +490,46 @@ def kda_chunk_fwd_gated(q, k, v, g, beta, gate, norm_weight=None, eps: float = 1
 # ---------------------------------------------------------------------------------------------
 # Linear attention with a decay for each head, and attention over a paged key-value cache.
 #
-# A decode step's calls take a few microseconds on the GPU, so what they cost here counts: the
-# checks of all tensors are one loop, and the dimension structs (and workspace sizes) of the
-# sizes in use are kept.
+# A decode step's calls take a few microseconds on the GPU, so what they cost here counts: arguments are
+# checked and outputs allocated in C++ (csrc/binding.cpp, built beside the library).
+
+_binding = None
 
 
-def _refuse(dev, specs):
-    """Raises for the first of (name, tensor, dtype, shape) that is not a contiguous tensor of that kind
-    on CUDA device `dev`."""
-    for name, t, dtype, shape in specs:
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} must be on the CUDA device of the others, got {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise AssertionError("no tensor to refuse")
+def _raise_status(status: int, where: str):
+    raise KdaError(status, where)
 
 
-def _check_all(dev, specs):
-    for _, t, dtype, shape in specs:
-        if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous()):
-            _refuse(dev, specs)
+def _bound():
+    """The C++ side of the binding, bound to the loaded library."""
+    global _binding
+    L = lib()
+    path = os.path.join(_HERE, "_binding.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with "
+                           "`python -c 'import __graft_entry__ as g; g.build()'`")
+    loader = importlib.machinery.ExtensionFileLoader("linear_attention_fwd_gb300._binding", path)
+    spec = importlib.util.spec_from_file_location("linear_attention_fwd_gb300._binding", path, loader=loader)
+    mod = importlib.util.module_from_spec(spec)
+    loader.exec_module(mod)
+    mod.bind(_raise_status, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.kda_lin_chunk_fwd, L.kda_lin_chunk_fwd_workspace_bytes, L.kda_lin_recurrent_step, L.kda_paged_append,
+        L.kda_paged_attention, L.kda_paged_attention_workspace_bytes)))
+    _binding = mod
+    return mod
 
 
-def _device_of(t) -> int:
-    """The index of t's device, which has to be the current one."""
-    dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current CUDA device, got {t.device}")
-    return dev
-
-
-# the current stream's handle without making a Stream object, where torch has it
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _raw_stream(stream, dev: int) -> int:
-    if stream is None:
-        return _current_raw_stream(dev)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _allocate(stream, like, shape, dtype):
-    """A new tensor on like's device, made for use on `stream`: memory that the allocator hands out
-    for another stream may still be in use there."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-@functools.lru_cache(maxsize=1024)
-def _lin_dims(packed, *sizes):
-    """(pointer to the struct, workspace bytes) for these sizes."""
-    p = ctypes.byref(KdaLinDims(*sizes))
-    return p, int(lib().kda_lin_chunk_fwd_workspace_bytes(p, packed))
-
-
-@functools.lru_cache(maxsize=1024)
-def _paged_dims(*sizes):
-    p = ctypes.byref(KdaPagedDims(*sizes))
-    return p, int(lib().kda_paged_attention_workspace_bytes(p))
+def _handle(stream):
+    """None for the current stream, else the stream's handle."""
+    return None if stream is None else int(getattr(stream, "cuda_stream", stream))
 
 
 def kda_lin_chunk_fwd_workspace_bytes(q, v, cu_seqlens=None) -> int:
     """Bytes of device workspace kda_lin_chunk_fwd needs for these shapes."""
     B, T, H, dv = v.shape
     n = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    return _lin_dims(int(cu_seqlens is not None), B, T, n, H, q.shape[2], q.shape[3], dv, _dtype_code(q.dtype))[1]
+    dims = KdaLinDims(B, T, n, H, q.shape[2], q.shape[3], dv, _dtype_code(q.dtype))
+    return int(lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(dims), int(cu_seqlens is not None)))
 
 
 def kda_lin_chunk_fwd(q, k, v, g=None, head_g=None, initial_state=None, cu_seqlens=None, *, out=None,
@@ -581,41 +543,8 @@ def kda_lin_chunk_fwd(q, k, v, g=None, head_g=None, initial_state=None, cu_seqle
     workspace: uint8 tensor of kda_lin_chunk_fwd_workspace_bytes bytes (allocated here when None).
     Returns (out [B, T, H, dv], final_state fp32 [N, H, dk, dv] or None).
     """
-    dev, dt, f32 = _device_of(q), q.dtype, torch.float32
-    if q.dim() != 4 or v.dim() != 4:
-        raise ValueError("q must be [B, T, Hk, dk] and v [B, T, H, dv]")
-    B, T, Hk, dk = q.shape
-    H, dv = v.shape[2:]
-    N, cu_shape = B, None
-    if cu_seqlens is not None:
-        N = cu_seqlens.numel() - 1
-        cu_shape = (N + 1,)
-        if N < 1:
-            raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
-    states, tokens = (N, H, dk, dv), (B, T, H, dv)
-    _check_all(dev, (("q", q, dt, (B, T, Hk, dk)), ("k", k, dt, (B, T, Hk, dk)), ("v", v, dt, tokens),
-                     ("g", g, f32, (B, T, H)), ("head_g", head_g, f32, (H,)),
-                     ("initial_state", initial_state, f32, states),
-                     ("cu_seqlens", cu_seqlens, torch.int32, cu_shape), ("out", out, dt, tokens),
-                     ("final_state", final_state, f32, states)))
-    dims, need = _lin_dims(int(cu_seqlens is not None), B, T, N, H, Hk, dk, dv, _dtype_code(dt))
-    if out is None:
-        out = _allocate(stream, q, tokens, dt)
-    if final_state is None and output_final_state:
-        final_state = _allocate(stream, q, states, f32)
-    if workspace is None:
-        if need:
-            workspace = _allocate(stream, q, (need,), torch.uint8)
-    else:
-        _check_all(dev, (("workspace", workspace, torch.uint8, workspace.shape),))
-    st = lib().kda_lin_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(g), _addr(head_g),
-                                 _addr(initial_state), _addr(cu_seqlens), out.data_ptr(),
-                                 _addr(final_state), _addr(workspace),
-                                 0 if workspace is None else workspace.numel(), dims,
-                                 _raw_stream(stream, dev))
-    if st != KDA_OK:
-        raise KdaError(st, "kda_lin_chunk_fwd")
-    return out, final_state
+    return (_binding or _bound()).lin_chunk(q, k, v, g, head_g, initial_state, cu_seqlens, out, final_state,
+                                            output_final_state, workspace, _handle(stream))
 
 
 def kda_lin_recurrent_step(q, k, v, g, head_g, state, state_indices=None, *, out=None, stream=None):
@@ -625,25 +554,7 @@ def kda_lin_recurrent_step(q, k, v, g, head_g, state, state_indices=None, *, out
     [P, H, dk, dv]; state_indices: int32 [N] (rows outside the pool are skipped: their outputs are
     not written) or None.  Returns out [N, H, dv].
     """
-    dev, dt, f32 = _device_of(q), q.dtype, torch.float32
-    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
-        raise ValueError("q must be [N, Hk, dk], v [N, H, dv] and state [P, H, dk, dv]")
-    N, Hk, dk = q.shape
-    H, dv = v.shape[1:]
-    slots = state.shape[0]
-    _check_all(dev, (("q", q, dt, (N, Hk, dk)), ("k", k, dt, (N, Hk, dk)), ("v", v, dt, (N, H, dv)),
-                     ("g", g, f32, (N, H)), ("head_g", head_g, f32, (H,)),
-                     ("state", state, f32, (slots, H, dk, dv)),
-                     ("state_indices", state_indices, torch.int32, (N,)), ("out", out, dt, (N, H, dv))))
-    dims = _lin_dims(0, N, 1, slots, H, Hk, dk, dv, _dtype_code(dt))[0]
-    if out is None:
-        out = _allocate(stream, q, (N, H, dv), dt)
-    st = lib().kda_lin_recurrent_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(g), _addr(head_g),
-                                      state.data_ptr(), _addr(state_indices), out.data_ptr(), dims,
-                                      _raw_stream(stream, dev))
-    if st != KDA_OK:
-        raise KdaError(st, "kda_lin_recurrent_step")
-    return out
+    return (_binding or _bound()).lin_step(q, k, v, g, head_g, state, state_indices, out, _handle(stream))
 
 
 def kda_paged_append(k, v, k_cache, v_cache, block_table, positions, cu_seqlens=None, *, stream=None):
@@ -654,28 +565,15 @@ def kda_paged_append(k, v, k_cache, v_cache, block_table, positions, cu_seqlens=
     [N+1] (row n's tokens are cu[n] .. cu[n+1]) or None (one token per row).  Tokens at a position
     past the table or on a page outside the pool are skipped.
     """
-    dev, dt, i32 = _device_of(k), k.dtype, torch.int32
-    if k_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("caches must be [pages, page_size, Hkv, d] and block_table [N, max_pages]")
-    pages, page_size, Hkv, d = cache = k_cache.shape
-    N, width, tokens = positions.numel(), block_table.shape[1], k.shape[0]
-    _check_all(dev, (("k", k, dt, (tokens, Hkv, d)), ("v", v, dt, (tokens, Hkv, d)),
-                     ("k_cache", k_cache, dt, cache), ("v_cache", v_cache, dt, cache),
-                     ("block_table", block_table, i32, (N, width)), ("positions", positions, i32, (N,)),
-                     ("cu_seqlens", cu_seqlens, i32, (N + 1,))))
-    dims = _paged_dims(N, Hkv, Hkv, d, pages, page_size, width, _dtype_code(dt))[0]
-    st = lib().kda_paged_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                block_table.data_ptr(), positions.data_ptr(), _addr(cu_seqlens), tokens,
-                                dims, _raw_stream(stream, dev))
-    if st != KDA_OK:
-        raise KdaError(st, "kda_paged_append")
+    (_binding or _bound()).append(k, v, k_cache, v_cache, block_table, positions, cu_seqlens, _handle(stream))
 
 
 def kda_paged_attention_workspace_bytes(q, k_cache, block_table) -> int:
     """Bytes of device workspace kda_paged_attention needs for these shapes."""
     pages, page_size, Hkv, d = k_cache.shape
-    return _paged_dims(q.shape[0], q.shape[1], Hkv, d, pages, page_size, block_table.shape[1],
-                       _dtype_code(q.dtype))[1]
+    dims = KdaPagedDims(q.shape[0], q.shape[1], Hkv, d, pages, page_size, block_table.shape[1],
+                        _dtype_code(q.dtype))
+    return int(lib().kda_paged_attention_workspace_bytes(ctypes.byref(dims)))
 
 
 def kda_paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, *, out=None, lse=None,
@@ -687,30 +585,5 @@ def kda_paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, *, ou
     workspace: uint8 tensor of kda_paged_attention_workspace_bytes bytes (allocated here when None).
     Returns (out [N, Hq, d], lse fp32 [N, Hq] or None); a row without tokens gets 0 and -infinity.
     """
-    dev, dt, i32 = _device_of(q), q.dtype, torch.int32
-    if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("q must be [N, Hq, d], caches [pages, page_size, Hkv, d] and block_table [N, max_pages]")
-    pages, page_size, Hkv, d = cache = k_cache.shape
-    N, Hq = q.shape[:2]
-    width = block_table.shape[1]
-    _check_all(dev, (("q", q, dt, (N, Hq, d)), ("k_cache", k_cache, dt, cache), ("v_cache", v_cache, dt, cache),
-                     ("block_table", block_table, i32, (N, width)), ("seq_lens", seq_lens, i32, (N,)),
-                     ("out", out, dt, (N, Hq, d)), ("lse", lse, torch.float32, (N, Hq))))
-    dims, need = _paged_dims(N, Hq, Hkv, d, pages, page_size, width, _dtype_code(dt))
-    if out is None:
-        out = _allocate(stream, q, (N, Hq, d), dt)
-    if lse is None and output_lse:
-        lse = _allocate(stream, q, (N, Hq), torch.float32)
-    if workspace is None:
-        if need:
-            workspace = _allocate(stream, q, (need,), torch.uint8)
-    else:
-        _check_all(dev, (("workspace", workspace, torch.uint8, workspace.shape),))
-    st = lib().kda_paged_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                   block_table.data_ptr(), seq_lens.data_ptr(), scale, out.data_ptr(),
-                                   _addr(lse), _addr(workspace),
-                                   0 if workspace is None else workspace.numel(), dims,
-                                   _raw_stream(stream, dev))
-    if st != KDA_OK:
-        raise KdaError(st, "kda_paged_attention")
-    return out, lse
+    return (_binding or _bound()).attend(q, k_cache, v_cache, block_table, seq_lens, scale, out, lse, output_lse,
+                                         workspace, _handle(stream))

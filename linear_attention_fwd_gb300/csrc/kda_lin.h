@@ -9,10 +9,6 @@ namespace kda {
 // host, without asking the device (so that workspace sizes are plain arithmetic).
 constexpr int kSms = 152;
 
-// Log decays are taken in log2 units from here up: a decay of 2^-1e5 is zero in every format, and
-// sums of 64 of them stay exact in the two-float form the kernels use.
-constexpr double kMinLog2Decay = -1e5;
-
 struct LinArgs {
     const void *q, *k, *v;
     const float *g;           // [tokens, H] or nullptr
@@ -48,13 +44,26 @@ __device__ __forceinline__ void lin_range(const LinArgs &a, int n, int64_t &bos,
     }
 }
 
-// A token's log decay in log2 units, fp64 (NaN passes through).
-__device__ __forceinline__ double lin_log2_decay(const LinArgs &a, int64_t tok, int h) {
-    double x = 0.0;
-    if (a.g) x += (double)a.g[tok * a.heads + h];
-    if (a.head_g) x += (double)__ldg(a.head_g + h);
-    x *= 1.4426950408889634074;
-    return x < kMinLog2Decay ? kMinLog2Decay : x;
+// Sums of log decays are kept as two floats (large part, rest), so that differences of them are exact to
+// fp32 whatever their magnitude.
+// (h, l) + (x, y): the sum of the large parts is split exactly, the small parts are added.
+__device__ __forceinline__ void add2f(float &h, float &l, float x, float y) {
+    const float s = h + x, b = s - h;
+    l += y + ((h - (s - b)) + (x - b));
+    h = s;
+}
+// A token's log decay g + hg in log2 units, 0 where `in` is false.  Below -1e5 it is that: the decay is zero
+// in every format and the sums stay finite.  (NaN passes through.)
+__device__ __forceinline__ void log2_decay(float g, float hg, bool in, float &hi, float &lo) {
+    constexpr float kL = 1.44269502e+00f, kLl = 1.92596299e-08f;   // log2 e = kL + kLl
+    const float s = g + hg, b = s - g, e = (g - (s - b)) + (hg - b);
+    hi = s * kL;
+    lo = fmaf(s, kL, -hi) + fmaf(s, kLl, e * kL);
+    if (s < -6.9e4f) {
+        hi = -1e5f;
+        lo = 0.f;
+    }
+    if (!in) hi = lo = 0.f;
 }
 
 struct PagedArgs {

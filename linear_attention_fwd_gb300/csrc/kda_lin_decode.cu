@@ -8,10 +8,8 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
-
 // One CTA per (row, head, block of CB value channels).
-template <typename Tin, int DK, int DV, int CB>
+template <typename Tin, int DK, int DV, int CB, int kThreads>
 __global__ void __launch_bounds__(kThreads) kda_lin_step_kernel(LinStepArgs a) {
     constexpr int CG = CB / 4;               // float4 column groups
     constexpr int RG = kThreads / CG;        // row groups
@@ -69,10 +67,14 @@ __global__ void __launch_bounds__(kThreads) kda_lin_step_kernel(LinStepArgs a) {
     }
 }
 
+// Fewer units than two per SM leave SMs idle or with half the work of others: a unit's columns then go to
+// CTAs of 32 each, 128-byte rows (32 states of 128 x 128: 2.5 us against 3.2).  More units take whole states
+// (470 of them: 12.8 us against 14.4 in blocks).
 template <typename Tin, int DK, int DV>
 cudaError_t launch_t(const LinStepArgs &a, cudaStream_t st) {
     const unsigned units = (unsigned)(a.rows * a.heads);
-    kda_lin_step_kernel<Tin, DK, DV, DV><<<units, kThreads, 0, st>>>(a);
+    if (units >= 2 * kSms) kda_lin_step_kernel<Tin, DK, DV, DV, 256><<<units, 256, 0, st>>>(a);
+    else kda_lin_step_kernel<Tin, DK, DV, 32, 128><<<units * (DV / 32), 128, 0, st>>>(a);
     return cudaGetLastError();
 }
 

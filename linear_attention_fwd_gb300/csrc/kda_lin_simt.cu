@@ -4,8 +4,7 @@
 // before the chunk:
 //   o_i = e^{G_i} S^T q_i + sum_{j <= i} (q_i . k_j) e^{G_i - G_j} v_j
 //   S  <- e^{G_31} S + sum_j e^{G_31 - G_j} k_j v_j^T
-// Every exponent is <= 0.  The sums G are taken in fp64 and kept as two floats, so that a
-// difference is exact to fp32 whatever the magnitude of the sums (a token that forgets everything
+// Every exponent is <= 0.  The sums G are kept as two floats, so that a difference is exact to fp32 whatever the magnitude of the sums (a token that forgets everything
 // may stand next to tokens that forget nothing).
 //
 // The value channels of S are independent: a CTA runs a block of 32 of them for one (sequence,
@@ -41,7 +40,7 @@ __global__ void __launch_bounds__(kThreads) kda_lin_chunk_simt_kernel(const LinA
     extern __shared__ __align__(16) float smem[];
     float *sQ = smem, *sK = sQ + C * LD, *sV = sK + C * LD, *sS = sV + C * CB, *sA = sS + DK * CB;
     __shared__ float sGh[C], sGl[C], sW[C], sE[C], sDec;
-    __shared__ double s_total;                 // this CTA's chunks' log decay
+    __shared__ float s_decay;                  // e^(the log decays of this CTA's chunks)
     const int t = threadIdx.x, blocks = a.dv / CB;
     const int rank = blockIdx.x % X, ub = blockIdx.x / X;
     const int unit = ub / blocks, c0 = (ub % blocks) * CB;
@@ -60,6 +59,8 @@ __global__ void __launch_bounds__(kThreads) kda_lin_chunk_simt_kernel(const LinA
     float4 s[RT];
 
     float4 pq[PER], pk[PER], pv;               // the next chunk's pieces
+    float pg = 0.f, total_h = 0.f, total_l = 0.f;   // a token's log decay; (thread 31) the sum of the chunks'
+    const float hg = a.head_g ? __ldg(a.head_g + h) : 0.f;
     auto fetch = [&](int64_t t0, bool with_q) {
         const int nr = last - t0 < C ? (int)(last - t0) : C;
 #pragma unroll
@@ -69,6 +70,7 @@ __global__ void __launch_bounds__(kThreads) kda_lin_chunk_simt_kernel(const LinA
             pk[e] = r < nr ? ld4(k + at) : make_float4(0.f, 0.f, 0.f, 0.f);
             if (with_q) pq[e] = r < nr ? ld4(q + at) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        if (t < 32) pg = a.g && t < nr ? __ldg(a.g + (t0 + t) * a.heads + h) : 0.f;
         const int r = t / 8, c = 4 * (t % 8);
         pv = r < nr ? ld4(v + ((t0 + r) * a.heads + h) * a.dv + c0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
@@ -84,20 +86,21 @@ __global__ void __launch_bounds__(kThreads) kda_lin_chunk_simt_kernel(const LinA
         }
         st4(sV + (t / 8) * CB + 4 * (t % 8), pv);
         if (t < 32) {
-            double G = t0 + t < last ? lin_log2_decay(a, t0 + t, h) : 0.0;
+            float Gh, Gl;
+            log2_decay(pg, hg, t0 + t < last, Gh, Gl);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, G, o);
-                if (t >= o) G += y;
+                const float yh = __shfl_up_sync(0xffffffffu, Gh, o), yl = __shfl_up_sync(0xffffffffu, Gl, o);
+                if (t >= o) add2f(Gh, Gl, yh, yl);
             }
-            const double end = __shfl_sync(0xffffffffu, G, 31);
-            sGh[t] = (float)G;
-            sGl[t] = (float)(G - (double)(float)G);
-            sE[t] = exp2f((float)G);
-            sW[t] = exp2f((float)(end - G));
+            const float eh = __shfl_sync(0xffffffffu, Gh, 31), el = __shfl_sync(0xffffffffu, Gl, 31);
+            sGh[t] = Gh;
+            sGl[t] = Gl;
+            sE[t] = exp2f(Gh + Gl);
+            sW[t] = exp2f((eh - Gh) + (el - Gl));
             if (t == 31) {
-                sDec = exp2f((float)G);
-                s_total += G;
+                sDec = exp2f(Gh + Gl);
+                add2f(total_h, total_l, Gh, Gl);
             }
         }
         if (t0 + C < last) fetch(t0 + C, with_q);
@@ -129,8 +132,6 @@ __global__ void __launch_bounds__(kThreads) kda_lin_chunk_simt_kernel(const LinA
         }
     };
 
-    if (t == 0) s_total = 0.0;
-    __syncthreads();
     if (X > 1) {
         // the part's state from zero (not needed of the last part)
 #pragma unroll
@@ -143,6 +144,7 @@ __global__ void __launch_bounds__(kThreads) kda_lin_chunk_simt_kernel(const LinA
             }
 #pragma unroll
             for (int m = 0; m < RT; ++m) st4(sS + (r0 + m) * CB + cc, s[m]);
+            if (t == 31) s_decay = exp2f(total_h + total_l);
         }
         if (first < last) fetch(first, true);
         cg::cluster_group cluster = cg::this_cluster();
@@ -150,14 +152,20 @@ __global__ void __launch_bounds__(kThreads) kda_lin_chunk_simt_kernel(const LinA
 #pragma unroll
         for (int m = 0; m < RT; ++m)
             s[m] = a.s0 ? ld4(a.s0 + sbase + (int64_t)(r0 + m) * a.dv) : make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int e = 0; e < rank; ++e) {
-            const float *from = cluster.map_shared_rank(sS, e);
-            const float f = exp2f((float)*cluster.map_shared_rank(&s_total, e));
+        // (all remote reads of a row are in flight together: the parts' number is fixed, those not before this
+        // one weigh nothing)
+        float f[kMaxCluster - 1];
 #pragma unroll
-            for (int m = 0; m < RT; ++m) {
-                const float4 x = ld4(from + (r0 + m) * CB + cc);
-                s[m] = make_float4(fmaf(f, s[m].x, x.x), fmaf(f, s[m].y, x.y), fmaf(f, s[m].z, x.z), fmaf(f, s[m].w, x.w));
-            }
+        for (int e = 0; e < kMaxCluster - 1; ++e) f[e] = e < rank ? *cluster.map_shared_rank(&s_decay, e) : 1.f;
+#pragma unroll
+        for (int m = 0; m < RT; ++m) {
+            float4 x[kMaxCluster - 1];
+#pragma unroll
+            for (int e = 0; e < kMaxCluster - 1; ++e)
+                x[e] = e < rank ? ld4(cluster.map_shared_rank(sS, e) + (r0 + m) * CB + cc) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < kMaxCluster - 1; ++e)
+                s[m] = make_float4(fmaf(f[e], s[m].x, x[e].x), fmaf(f[e], s[m].y, x[e].y), fmaf(f[e], s[m].z, x[e].z), fmaf(f[e], s[m].w, x[e].w));
         }
         cluster.sync();   // every state (the initial one too, which may be the final one's place) is read
     } else {

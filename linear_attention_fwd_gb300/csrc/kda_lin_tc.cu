@@ -1,6 +1,6 @@
 // Linear attention with a decay for each head, chunkwise, on the sm_103a tensor cores
-// (tcgen05 + TMEM + TMA).  bf16 inputs and outputs, fp32 state, computed at d_k = d_v = 128 (a
-// 64-wide head reads its missing channels as zeros).
+// (tcgen05 + TMEM + TMA).  bf16 inputs and outputs, fp32 state, d_k of 64 or 128, computed at d_v = 128 (a
+// head of 64 value channels reads the missing ones as zeros).
 //
 // Chunks of C = 64 tokens; G_i = sum of the chunk's log decays up to token i, S the state before
 // the chunk, all products transposed so that the state's value channels are TMEM lanes:
@@ -73,7 +73,6 @@ constexpr uint32_t TM_OI = 384;     // (2)                                      
 constexpr uint32_t TM_OJ = 448;     // (3)                                      64
 constexpr uint32_t TM_COLS = 512;
 
-constexpr uint32_t IDESC_KV = idesc_bf16_f32(128, 128) | (1u << 15) | (1u << 16);   // A (V) and B (K') MN-major
 constexpr uint32_t IDESC_SQ = idesc_bf16_f32(128, 64);                              // A in TMEM, B (Q) K-major
 constexpr uint32_t IDESC_VP = idesc_bf16_f32(128, 64) | (1u << 15);                 // A (V) MN-major, B (P) K-major
 
@@ -97,13 +96,6 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 
 template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-// (h, l) + (x, y) as two floats: the sum of the large parts is split exactly, the small parts are added
-__device__ __forceinline__ void add2f(float &h, float &l, float x, float y) {
-    const float s = h + x, b = s - h;
-    l += y + ((h - (s - b)) + (x - b));
-    h = s;
-}
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) { return *reinterpret_cast<__nv_bfloat162 *>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t *>(&x); }
@@ -324,11 +316,14 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan_kernel(const LinArgs a,
 // of the part before it.  Otherwise only the state that a part reaches from zero, into its slot of
 // `locals`, and its total log2 decay; lin_scan_kernel then turns each slot into the true state behind
 // its part.
-template <bool kFullPass>
+// kDk: the key channels, 64 or 128 (value channels are always 128 lanes; those a head lacks read as zeros).
+template <bool kFullPass, int kDk>
 __global__ void __launch_bounds__(NT, 1)
 kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv, const LinArgs a, const CutRule cut, const Piece *plan,
                         float *locals, double *decays) {
+    constexpr uint32_t IDESC_KV = idesc_bf16_f32(128, kDk) | (1u << 15) | (1u << 16);   // A (V) and B (K') MN-major
+    constexpr int KC = kDk / 2;                // key channels of the state per thread
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_fail;
     __shared__ volatile int s_piece[4];   // unit, the part's slot, whether it is the last (read again at the end:
@@ -390,18 +385,18 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
     if (warp < 8) {
         // ---- S
         regs_inc<104>();
-        const int i0 = 64 * (warp >> 2);
-        const int64_t sstep = (int64_t)a.dk * a.dv;
-        const bool mine = jl < a.dv && i0 < a.dk;
+        const int i0 = KC * (warp >> 2);
+        const int64_t sstep = (int64_t)kDk * a.dv;
+        const bool mine = jl < a.dv;
         const int64_t at = (int64_t)i0 * a.dv + jl;
-        float v[64];
+        float v[KC];
 #pragma unroll
-        for (int c = 0; c < 64; ++c) v[c] = 0.f;
+        for (int c = 0; c < KC; ++c) v[c] = 0.f;
         if (kFullPass && mine) {
             const float *from = p > 0 ? locals + ((int64_t)(slot + p - 1) * H + h) * sstep : (a.s0 ? a.s0 + ((int64_t)n * H + h) * sstep : nullptr);
             if (from)
 #pragma unroll
-                for (int c = 0; c < 64; ++c) v[c] = __ldcg(from + at + (int64_t)c * a.dv);
+                for (int c = 0; c < KC; ++c) v[c] = __ldcg(from + at + (int64_t)c * a.dv);
         }
         float dec = 0.f;   // e^(sum of the chunk's log decays)
         for (int k = 0; k <= chunks; ++k) {
@@ -423,7 +418,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 // stores here and below: the compiler keeps their order, and a load behind a store waits its
                 // whole way.)
 #pragma unroll 1
-                for (int x0 = tid; x0 < 1024; x0 += 512) {
+                for (int x0 = tid; x0 < 8 * kDk; x0 += 512) {
                     uint4 uk[2];
                     uint2 wk[2];
 #pragma unroll
@@ -440,6 +435,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                         if (nr < C && r >= nr) {   // rows past the sequence belong to another one: they never enter a product
                             uk[e] = make_uint4(0u, 0u, 0u, 0u);
                             *reinterpret_cast<uint4 *>(sm + st + 32768 + 16 * x) = uk[e];
+                            if (kDk == 64) *reinterpret_cast<uint4 *>(sm + st + 40960 + 16 * x) = uk[e];   // V is 128 wide
                         }
                         const uint32_t uw[4] = {uk[e].x, uk[e].y, uk[e].z, uk[e].w};
                         uint32_t o0[4], o1[4], o2[4];
@@ -467,7 +463,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 tc_fence_after();
                 const float2 d2 = make_float2(dec, dec);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int b = 0; b < KC / 32; ++b) {
                     float w[32];
                     tmem_ld32(trow + TM_DS + 128 * ((k - 1) & 1) + i0 + 32 * b, w);
 #pragma unroll
@@ -487,7 +483,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                     break;
                 }
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
+                for (int b = 0; b < KC / 16; ++b) {
                     uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
@@ -507,7 +503,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
         if (ok && to && mine) {
             to += (int64_t)s_piece[kFullPass ? 0 : 1] * sstep + at;
 #pragma unroll
-            for (int c = 0; c < 64; ++c) to[(int64_t)c * a.dv] = v[c];
+            for (int c = 0; c < KC; ++c) to[(int64_t)c * a.dv] = v[c];
         }
     } else if (warp < 16) {
         // ---- scores, P and O, each of the two halves of these warps half of it
@@ -547,8 +543,10 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                     for (int e = 0; e < 4; ++e) acc[b][e] = 0.f;
                 scores_step<0>(qrow + st, krow + st, acc);
                 scores_step<1>(qrow + st, krow + st, acc);
-                scores_step<2>(qrow + st, krow + st, acc);
-                scores_step<3>(qrow + st, krow + st, acc);
+                if constexpr (kDk == 128) {
+                    scores_step<2>(qrow + st, krow + st, acc);
+                    scores_step<3>(qrow + st, krow + st, acc);
+                }
             }
             const uint32_t stg = ((k + kStages - 1) % kStages) * STAGE + 2048 * (warp - 8);
             if (k > 0) {   // the previous chunk's outputs; its P is consumed
@@ -640,18 +638,6 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 gx = gp && t < eos ? __ldg(gp + (int64_t)k * C * H) : 0.f;
                 gy = gp && t + 1 < eos ? __ldg(gp + (int64_t)k * C * H + H) : 0.f;
             };
-            // g + hg in log2 units as two floats (below -1e5 it is that: the decay is zero)
-            auto log2_decay = [&](float x, bool in, float &hi, float &lo) {
-                constexpr float kL = 1.44269502e+00f, kLl = 1.92596299e-08f;   // log2 e = kL + kLl
-                const float s = x + hg, b = s - x, e = (x - (s - b)) + (hg - b);
-                hi = s * kL;
-                lo = fmaf(s, kL, -hi) + fmaf(s, kLl, e * kL);
-                if (s < -6.9e4f) {
-                    hi = -1e5f;
-                    lo = 0.f;
-                }
-                if (!in) hi = lo = 0.f;
-            };
             if (chunks > 0) load_g(0);
             for (int k = 0; k < chunks; ++k) {
                 const int s = k % kStages;
@@ -663,21 +649,21 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 if (lane == 0) {
                     const uint32_t st = sb + s * STAGE, b = bar(kFull + s);
                     const int tok = first + k * C;
-                    mbar_arrive_expect_tx(b, kFullPass ? 3 * 16384 : 2 * 16384);
+                    mbar_arrive_expect_tx(b, 16384 + (kFullPass ? 2 : 1) * 128 * kDk);
                     tma_load_3d(st + 16384, &tmk, b, 0, hk, tok);
-                    tma_load_3d(st + 24576, &tmk, b, 64, hk, tok);
+                    if (kDk == 128) tma_load_3d(st + 24576, &tmk, b, 64, hk, tok);
                     tma_load_3d(st + 32768, &tmv, b, 0, h, tok);
                     tma_load_3d(st + 40960, &tmv, b, 64, h, tok);
                     if (kFullPass) {
                         tma_load_3d(st, &tmq, b, 0, hk, tok);
-                        tma_load_3d(st + 8192, &tmq, b, 64, hk, tok);
+                        if (kDk == 128) tma_load_3d(st + 8192, &tmq, b, 64, hk, tok);
                     }
                 }
                 __syncwarp();
                 const int t = first + k * C + 2 * lane;
                 float xh, xl, yh, yl;
-                log2_decay(gx, t < eos, xh, xl);
-                log2_decay(gy, t + 1 < eos, yh, yl);
+                log2_decay(gx, hg, t < eos, xh, xl);
+                log2_decay(gy, hg, t + 1 < eos, yh, yl);
                 if (k + 1 < chunks) load_g(k + 1);
                 float bh = xh, bl = xl;            // sums up to the lane's second token
                 add2f(bh, bl, yh, yl);
@@ -737,7 +723,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
 #pragma unroll 1
                         for (int e = 0; e < 2; ++e)
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
+                            for (int kk = 0; kk < kDk / 16; ++kk)
                                 mma_ts(tmem + TM_OI, tmem + TM_S16 + 64 * e + 8 * kk, qd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
                                            IDESC_SQ, e + kk > 0);
                     }
@@ -937,14 +923,17 @@ cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, bool whole, c
         cfg.numAttrs = behind_plan ? 1 : 0;
         return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a, c.rule, plan, locals, decays);
     };
+    const bool wide = a.dk == 128;
     if (c.pre > 0) {
-        const cudaError_t e = launch(kda_lin_chunk_tc_kernel<false>, c.pre, pre, a.cu != nullptr);
+        const cudaError_t e = wide ? launch(kda_lin_chunk_tc_kernel<false, 128>, c.pre, pre, a.cu != nullptr)
+                                   : launch(kda_lin_chunk_tc_kernel<false, 64>, c.pre, pre, a.cu != nullptr);
         if (e != cudaSuccess) return e;
         const dim3 grid((unsigned)c.pre, (unsigned)(a.dk * a.dv / (4 * kScanThreads)));
         lin_scan_kernel<<<grid, kScanThreads, 0, st>>>(a, c.rule, pre, locals, decays);
         if (cudaGetLastError() != cudaSuccess) return cudaErrorLaunchFailure;
     }
-    return launch(kda_lin_chunk_tc_kernel<true>, c.full, full, a.cu != nullptr && c.pre == 0);
+    const bool behind = a.cu != nullptr && c.pre == 0;
+    return wide ? launch(kda_lin_chunk_tc_kernel<true, 128>, c.full, full, behind) : launch(kda_lin_chunk_tc_kernel<true, 64>, c.full, full, behind);
 }
 
 }  // namespace kda

@@ -631,11 +631,12 @@ __global__ void __launch_bounds__(D) kda_paged_join_kernel(const AttArgs a, cons
 int heads_per_block(kda_dtype_t dt, int rep) { return dt == KDA_BF16 ? 16 : (rep == 1 ? 1 : (rep <= 4 ? 4 : 8)); }
 
 // Rows no longer than kShortTokens per CTA of a cluster take the one-launch form (a.cluster CTAs a unit):
-// as many CTAs as two per SM, up to 8.  0: the rows may be longer.
+// as many CTAs as the SMs hold, up to 8.  0: the rows may be longer.
 constexpr int kShortTokens = 1024, kMaxCluster = 8;
-int short_cluster(int64_t units, int64_t max_tokens) {
+int short_cluster(int64_t units, int64_t max_tokens, int d) {
+    const int ctas = d == 64 ? 3 * kSms : kCtas;   // what the SMs hold at once
     int c = kMaxCluster;
-    while (c > 1 && units * c > kCtas) c /= 2;
+    while (c > 1 && units * c > ctas) c /= 2;
     return max_tokens <= (int64_t)c * kShortTokens ? c : 0;
 }
 
@@ -691,7 +692,7 @@ cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st) {
 
 size_t paged_attention_workspace_bytes(int64_t rows, int heads, int kv_heads, int64_t max_tokens, int d, kda_dtype_t dt) {
     const int rep = heads / kv_heads, rp = heads_per_block(dt, rep), blocks = (rep + rp - 1) / rp;
-    if (rows <= 0 || short_cluster(rows * kv_heads * blocks, max_tokens)) return 0;
+    if (rows <= 0 || short_cluster(rows * kv_heads * blocks, max_tokens, d)) return 0;
     return (size_t)attention_ctas(rows, (int64_t)kv_heads * blocks, max_tokens) * 2 * rp * (d + 2) * 4;
 }
 
@@ -700,7 +701,7 @@ cudaError_t launch_paged_attention(const PagedArgs &p, int d, kda_dtype_t dt, vo
     const int grid = attention_ctas(p.rows, (int64_t)p.kv_heads * blocks, (int64_t)p.max_pages * p.page_size);
     float *ws = static_cast<float *>(workspace);
     const AttArgs a{p, FastDiv((uint32_t)p.page_size), rep, blocks, rp, ws, ws ? ws + (size_t)grid * 2 * rp * d : nullptr,
-                    short_cluster((int64_t)p.rows * p.kv_heads * blocks, (int64_t)p.max_pages * p.page_size)};
+                    short_cluster((int64_t)p.rows * p.kv_heads * blocks, (int64_t)p.max_pages * p.page_size, d)};
     if (dt == KDA_BF16)
         return d == 128 ? launch_att<__nv_bfloat16, 128, 16>(a, grid, st) : launch_att<__nv_bfloat16, 64, 16>(a, grid, st);
     if (d == 128)

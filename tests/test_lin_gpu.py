@@ -86,13 +86,13 @@ def test_packed_with_empty_members(K, dt, dk):
     R.check_lin(out, fin, reference(d, cu))
 
 
-@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("dt,dk,dv", [(F32, 128, 128), (BF16, 128, 128), (BF16, 64, 128), (BF16, 128, 64), (BF16, 64, 64), (F32, 64, 64)])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
-def test_neighbours_never_leak(K, dt, bad):
+def test_neighbours_never_leak(K, dt, dk, dv, bad):
     """NaN and infinities of one sequence stay in it, whatever shares its tiles."""
     lens = [70, 5, 129, 64]
     cu = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
-    d = make(12, 1, sum(lens), 2, 1, 128, 128, dt, init=4)
+    d = make(12, 1, sum(lens), 2, 1, dk, dv, dt, init=4)
     clean = reference(d, cu)
     for x in ("q", "k", "v", "g"):
         for b, e in ((70, 75), (204, 268)):
@@ -104,11 +104,11 @@ def test_neighbours_never_leak(K, dt, bad):
         R.check_lin(out[:, :0], fin[n], (clean[0][:, :0], clean[1][n], clean[2][:, :0], clean[3][n]))
 
 
-@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("dt,dk,dv", [(F32, 128, 128), (BF16, 128, 128), (BF16, 64, 128), (BF16, 64, 64)])
 @pytest.mark.parametrize("B,T,H", [(1, 1500, 2), (1, 4200, 1), (2, 2100, 3)])
-def test_long_few_heads(K, dt, B, T, H):
+def test_long_few_heads(K, dt, dk, dv, B, T, H):
     """Fewer (sequence, head) pairs than SMs: sequences may be cut into parts."""
-    d = make(13, B, T, H, 1, 128, 128, dt, decay="both", init=B)
+    d = make(13, B, T, H, 1, dk, dv, dt, decay="both", init=B)
     d["g"] *= 0.02      # slow enough that every part sees the ones before it
     out, fin = K.kda_lin_chunk_fwd(**d)
     R.check_lin(out, fin, reference(d))

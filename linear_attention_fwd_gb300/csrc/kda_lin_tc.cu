@@ -333,6 +333,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int H = a.heads;
     // (launched before the kernel ahead of it has ended, see launch_lin_chunk_tc)
+    if (!kFullPass) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Piece piece = plan ? plan[blockIdx.x] : dense_piece<kFullPass>(a, blockIdx.x, cut);
     const int n = piece.n, h = piece.h, p = piece.p, P = piece.P, slot = piece.slot;
@@ -792,6 +793,8 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
 // walk its parts.
 constexpr int kScanThreads = 256;
 __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const LinArgs a, const CutRule cut, const Piece *plan, float *locals, const double *decays) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const Piece piece = plan ? plan[blockIdx.x] : dense_piece<false>(a, blockIdx.x, cut);
     if (piece.P == 0 || piece.p != 0) return;
     const int H = a.heads;
@@ -900,40 +903,45 @@ cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, bool whole, c
         return cudaErrorInvalidValue;
     float *locals = static_cast<float *>(workspace);
     double *decays = reinterpret_cast<double *>(locals + (int64_t)c.rule.slots * a.heads * a.dk * a.dv);
-    Piece *pre = nullptr, *full = nullptr;
-    if (a.cu) {
-        pre = reinterpret_cast<Piece *>((reinterpret_cast<uintptr_t>(decays + (int64_t)c.rule.slots * a.heads) + 15) & ~uintptr_t(15));
-        full = pre + c.pre;
-        lin_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, c.rule, pre, (int)c.pre, full, (int)c.full);
-    }
-    // A kernel right behind the list's maker may be launched before that one has ended (it waits for it at its
-    // start): its launch is then over when the list is there.
-    auto launch = [&](auto kernel, int64_t ctas, const Piece *plan, bool behind_plan) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    // Up to four kernels, each needing all of the one before: every one but the first may be launched before
+    // that has ended and waits for it at its start, so that the launches overlap.
+    bool first = true;
+    auto launch = [&](auto kernel, dim3 grid, int threads, size_t smem, auto... args) {
+        cudaError_t e = smem ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
         if (e != cudaSuccess) return e;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[0].val.programmaticStreamSerializationAllowed = 1;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)ctas);
-        cfg.blockDim = dim3(NT);
-        cfg.dynamicSmemBytes = SMEM_BYTES;
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = smem;
         cfg.stream = st;
         cfg.attrs = at;
-        cfg.numAttrs = behind_plan ? 1 : 0;
-        return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a, c.rule, plan, locals, decays);
+        cfg.numAttrs = first ? 0 : 1;
+        first = false;
+        return cudaLaunchKernelEx(&cfg, kernel, args...);
     };
     const bool wide = a.dk == 128;
-    if (c.pre > 0) {
-        const cudaError_t e = wide ? launch(kda_lin_chunk_tc_kernel<false, 128>, c.pre, pre, a.cu != nullptr)
-                                   : launch(kda_lin_chunk_tc_kernel<false, 64>, c.pre, pre, a.cu != nullptr);
-        if (e != cudaSuccess) return e;
-        const dim3 grid((unsigned)c.pre, (unsigned)(a.dk * a.dv / (4 * kScanThreads)));
-        lin_scan_kernel<<<grid, kScanThreads, 0, st>>>(a, c.rule, pre, locals, decays);
-        if (cudaGetLastError() != cudaSuccess) return cudaErrorLaunchFailure;
+    Piece *pre = nullptr, *full = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (a.cu) {
+        pre = reinterpret_cast<Piece *>((reinterpret_cast<uintptr_t>(decays + (int64_t)c.rule.slots * a.heads) + 15) & ~uintptr_t(15));
+        full = pre + c.pre;
+        e = launch(lin_plan_kernel, dim3(1), kPlanThreads, 0, a, c.rule, pre, (int)c.pre, full, (int)c.full);
     }
-    const bool behind = a.cu != nullptr && c.pre == 0;
-    return wide ? launch(kda_lin_chunk_tc_kernel<true, 128>, c.full, full, behind) : launch(kda_lin_chunk_tc_kernel<true, 64>, c.full, full, behind);
+    const Piece *cpre = pre, *cfull = full;
+    const double *cdecays = decays;
+    if (e == cudaSuccess && c.pre > 0) {
+        e = launch(wide ? kda_lin_chunk_tc_kernel<false, 128> : kda_lin_chunk_tc_kernel<false, 64>, dim3((unsigned)c.pre), NT, SMEM_BYTES,
+                   mq, mk, mv, a, c.rule, cpre, locals, decays);
+        if (e == cudaSuccess)
+            e = launch(lin_scan_kernel, dim3((unsigned)c.pre, (unsigned)(a.dk * a.dv / (4 * kScanThreads))), kScanThreads, 0,
+                       a, c.rule, cpre, locals, cdecays);
+    }
+    if (e != cudaSuccess) return e;
+    return launch(wide ? kda_lin_chunk_tc_kernel<true, 128> : kda_lin_chunk_tc_kernel<true, 64>, dim3((unsigned)c.full), NT, SMEM_BYTES,
+                  mq, mk, mv, a, c.rule, cfull, locals, decays);
 }
 
 }  // namespace kda

@@ -456,14 +456,27 @@ typedef struct {
  * NaN or infinity of a sequence's own token may reach its outputs from the start of that token's
  * chunk (at most 64 tokens, counted from the sequence's start) on, and its state.
  * Returns KDA_OK or an error found on the host before any launch: KDA_ERR_NULL, KDA_ERR_SHAPE,
- * KDA_ERR_UNSUPPORTED, KDA_ERR_ALIGN, KDA_ERR_WORKSPACE.  seqlen = 0 is valid (final_state becomes
- * a copy of the initial state, or zeros). */
+ * KDA_ERR_UNSUPPORTED, KDA_ERR_ALIGN, KDA_ERR_WORKSPACE; KDA_ERR_CUDA when a launch fails.
+ * seqlen = 0 is valid (final_state becomes a copy of the initial state, or zeros). */
 kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const void *v,
                                const float *g, const float *head_g,
                                const float *initial_state, const int32_t *cu_seqlens,
                                void *out, float *final_state,
                                void *workspace, size_t workspace_bytes,
                                const kda_lin_dims_t *dims, cudaStream_t stream);
+
+/* kda_lin_chunk_fwd_bounded -- kda_lin_chunk_fwd with an explicit bound on every device-side wait of the
+ * tensor-core kernel (bf16): `wait_polls` polls of at most about a microsecond each (kda_lin_chunk_fwd
+ * uses 2^20).  When a wait gives up, the CTA lets what is in flight land (bounded separately), writes
+ * NaN to its tokens' outputs and to the final state where it holds it, and kda_device_status reports
+ * KDA_ERR_TIMEOUT.  wait_polls = 0 makes every wait give up at once: a test of that path.  fp32 calls
+ * have no such waits. */
+kda_status_t kda_lin_chunk_fwd_bounded(const void *q, const void *k, const void *v,
+                                       const float *g, const float *head_g,
+                                       const float *initial_state, const int32_t *cu_seqlens,
+                                       void *out, float *final_state,
+                                       void *workspace, size_t workspace_bytes, uint32_t wait_polls,
+                                       const kda_lin_dims_t *dims, cudaStream_t stream);
 
 /* Bytes of workspace kda_lin_chunk_fwd needs for `dims`, packed != 0 for calls with cu_seqlens (0: none;
  * host arithmetic only). */

@@ -19,6 +19,7 @@ struct LinArgs {
     float *sT;                // [N, H, dk, dv] or nullptr
     int64_t seqlen;           // tokens per dense row, or total packed tokens
     int32_t num_seqs, heads, qk_heads, dk, dv;
+    uint32_t wait_polls;      // bound on each device wait of the tensor-core kernel (polls)
 };
 
 struct LinStepArgs {

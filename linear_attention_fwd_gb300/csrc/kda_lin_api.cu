@@ -33,11 +33,11 @@ extern "C" size_t kda_lin_chunk_fwd_workspace_bytes(const kda_lin_dims_t *d, int
     return kda::lin_chunk_tc_workspace_bytes((int64_t)d->batch * d->seqlen, d->num_seqs, d->heads, d->dk, d->dv, packed != 0);
 }
 
-extern "C" kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const float *g,
-                                          const float *head_g, const float *initial_state,
-                                          const int32_t *cu_seqlens, void *out, float *final_state,
-                                          void *workspace, size_t workspace_bytes, const kda_lin_dims_t *d,
-                                          cudaStream_t stream) {
+extern "C" kda_status_t kda_lin_chunk_fwd_bounded(const void *q, const void *k, const void *v, const float *g,
+                                                  const float *head_g, const float *initial_state,
+                                                  const int32_t *cu_seqlens, void *out, float *final_state,
+                                                  void *workspace, size_t workspace_bytes, uint32_t wait_polls,
+                                                  const kda_lin_dims_t *d, cudaStream_t stream) {
     kda_status_t st = check_lin_dims(d);
     if (st != KDA_OK) return st;
     if (d->batch <= 0 || d->seqlen < 0) return KDA_ERR_SHAPE;
@@ -69,12 +69,21 @@ extern "C" kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const vo
         return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     }
     const kda::LinArgs a{q, k, v, g, head_g, initial_state, cu_seqlens, out, final_state,
-                         (int64_t)d->seqlen, d->num_seqs, d->heads, d->qk_heads, d->dk, d->dv};
+                         (int64_t)d->seqlen, d->num_seqs, d->heads, d->qk_heads, d->dk, d->dv, wait_polls};
     // in place, a sequence's last part would write the state that its other parts start from
     const bool whole = initial_state && initial_state == final_state;
     const cudaError_t e = d->dtype == KDA_BF16 ? kda::launch_lin_chunk_tc(a, workspace, whole, stream)
                                                : kda::launch_lin_chunk_simt(a, stream);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const float *g,
+                                          const float *head_g, const float *initial_state,
+                                          const int32_t *cu_seqlens, void *out, float *final_state,
+                                          void *workspace, size_t workspace_bytes, const kda_lin_dims_t *d,
+                                          cudaStream_t stream) {
+    return kda_lin_chunk_fwd_bounded(q, k, v, g, head_g, initial_state, cu_seqlens, out, final_state, workspace,
+                                     workspace_bytes, 1u << 20, d, stream);
 }
 
 extern "C" kda_status_t kda_lin_recurrent_step(const void *q, const void *k, const void *v, const float *g,

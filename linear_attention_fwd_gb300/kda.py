@@ -32,7 +32,8 @@ EXPORTED = ("kda_chunk_fwd", "kda_chunk_fwd_with", "kda_chunk_fwd_bounded", "kda
             "kda_chunk_fwd_workspace_bytes", "kda_chunk_fwd_noalloc", "kda_debug_checks",
             "kda_chunk_fwd_qknorm", "kda_recurrent_step_qknorm", "kda_recurrent_steps_qknorm",
             "kda_status_string",
-            "kda_lin_chunk_fwd", "kda_lin_chunk_fwd_workspace_bytes", "kda_lin_recurrent_step",
+            "kda_lin_chunk_fwd", "kda_lin_chunk_fwd_bounded", "kda_lin_chunk_fwd_workspace_bytes",
+            "kda_lin_recurrent_step",
             "kda_paged_append", "kda_paged_attention", "kda_paged_attention_workspace_bytes")
 
 
@@ -113,6 +114,8 @@ def lib() -> ctypes.CDLL:
         lp, pp = ctypes.POINTER(KdaLinDims), ctypes.POINTER(KdaPagedDims)
         L.kda_lin_chunk_fwd.restype = ctypes.c_int
         L.kda_lin_chunk_fwd.argtypes = [vp] * 10 + [ctypes.c_size_t, lp, vp]
+        L.kda_lin_chunk_fwd_bounded.restype = ctypes.c_int
+        L.kda_lin_chunk_fwd_bounded.argtypes = [vp] * 10 + [ctypes.c_size_t, ctypes.c_uint32, lp, vp]
         L.kda_lin_chunk_fwd_workspace_bytes.restype = ctypes.c_size_t
         L.kda_lin_chunk_fwd_workspace_bytes.argtypes = [lp, ctypes.c_int]
         L.kda_lin_recurrent_step.restype = ctypes.c_int
@@ -545,6 +548,33 @@ def kda_lin_chunk_fwd(q, k, v, g=None, head_g=None, initial_state=None, cu_seqle
     """
     return (_binding or _bound()).lin_chunk(q, k, v, g, head_g, initial_state, cu_seqlens, out, final_state,
                                             output_final_state, workspace, _handle(stream))
+
+
+def kda_lin_chunk_fwd_bounded(q, k, v, g, head_g, initial_state, cu_seqlens, out, final_state, workspace,
+                              wait_polls: int, stream=None):
+    """kda_lin_chunk_fwd with an explicit bound on the kernel's device-side waits.  Every tensor is the
+    caller's (g, head_g, initial_state, cu_seqlens, final_state and workspace may be None)."""
+    dev = q.device
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+        _check_dev(name, t, dev, q.dtype)
+    for name, t in (("g", g), ("head_g", head_g), ("initial_state", initial_state), ("final_state", final_state)):
+        _check_dev(name, t, dev, torch.float32)
+    _check_dev("cu_seqlens", cu_seqlens, dev, torch.int32)
+    _check_dev("workspace", workspace, dev, torch.uint8)
+    B, T, H, dv = v.shape
+    N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    if k.shape != q.shape or q.shape[:2] != v.shape[:2] or out.shape != v.shape \
+            or (g is not None and g.shape != v.shape[:3]) or (head_g is not None and head_g.shape != (H,)) \
+            or any(t is not None and t.shape != (N, H, q.shape[3], dv) for t in (initial_state, final_state)):
+        raise ValueError("inconsistent shapes")
+    dims = KdaLinDims(B, T, N, H, q.shape[2], q.shape[3], dv, _dtype_code(q.dtype))
+    st = lib().kda_lin_chunk_fwd_bounded(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(head_g), _ptr(initial_state),
+                                         _ptr(cu_seqlens), _ptr(out), _ptr(final_state), _ptr(workspace),
+                                         0 if workspace is None else workspace.numel(), int(wait_polls),
+                                         ctypes.byref(dims), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_lin_chunk_fwd_bounded")
+    return out, final_state
 
 
 def kda_lin_recurrent_step(q, k, v, g, head_g, state, state_indices=None, *, out=None, stream=None):

@@ -268,3 +268,23 @@ def test_many_units(K):
     d = make(26, 1, sum(lens), 4, 4, 128, 128, BF16)
     out, fin = K.kda_lin_chunk_fwd(**d, cu_seqlens=cu)
     R.check_lin(out, fin, reference(d, cu))
+
+
+@pytest.mark.parametrize("T,H,dk", [(150, 2, 128), (2500, 2, 64)])
+def test_waits_that_give_up(K, T, H, dk):
+    """With a bound of zero every wait gives up at once: outputs and states are NaN, the status says so, and the
+    next call on the same context is right."""
+    d = make(29, 1, T, H, H, dk, 128, BF16, init=1)
+    ref = reference(d)
+    out = torch.zeros(1, T, H, 128, dtype=BF16, device="cuda")
+    fin = torch.zeros(1, H, dk, 128, device="cuda")
+    ws = torch.empty(max(1, K.kda_lin_chunk_fwd_workspace_bytes(d["q"], d["v"])), dtype=torch.uint8, device="cuda")
+    assert K.kda_device_status() == K.KDA_OK
+    args = (d["q"], d["k"], d["v"], d["g"], None, d["initial_state"], None, out, fin, ws)
+    K.kda_lin_chunk_fwd_bounded(*args, 0)
+    assert K.kda_device_status() == K.KDA_ERR_TIMEOUT
+    assert bool(out.isnan().all()) and bool(fin.isnan().all())
+    assert K.kda_device_status() == K.KDA_OK
+    K.kda_lin_chunk_fwd_bounded(*args, 1 << 20)
+    R.check_lin(out, fin, ref)
+    assert K.kda_device_status() == K.KDA_OK

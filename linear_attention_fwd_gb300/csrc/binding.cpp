@@ -1,6 +1,6 @@
 // Python binding of the linear-attention and paged-cache calls: argument checks, output allocation and the
 // current stream, in C++.  A decode step's calls take a few microseconds on the GPU; the same work done
-// in Python around ctypes cost 8 to 20 us of host time per call, here 5 to 8.
+// in Python around ctypes cost 8 to 20 us of host time per call, here 3 to 6.
 //
 // The library itself is reached through the addresses that `bind` is given, so that the module works with
 // whichever build of it the Python side has loaded.

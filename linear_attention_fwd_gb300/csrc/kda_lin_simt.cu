@@ -13,7 +13,7 @@
 // each CTA but the last first takes its chunks' state from zero, the states are exchanged through
 // distributed shared memory (the true state before part r is the initial state and the parts before
 // it, each decayed by what follows), and every CTA then runs its chunks.  (256 tokens x 2 heads of
-// 64: 42 us with one CTA per sequence and block, 13 us with clusters of 8.)
+// 64: 42 us with one CTA per sequence and block, 10 us with clusters of 8.)
 //
 // Bound by shared-memory reads: about 1.4 16-byte reads per 16 multiply-adds.
 #include <cooperative_groups.h>

@@ -30,10 +30,11 @@
 // K16, in this order: K' of the next chunk is made during (2) and (3), and the S warps have the
 // whole of (1) to turn dS of the chunk before into the operand of (2).
 //
-// Measured (B=4 H=32 T=8192 d=128): 287 us, 3.8 TB/s, 56 % of the measured copy rate; 2.2 us a chunk, in
-// which an SM issues about 9,400 warp instructions at 2.16 a cycle.  That issue rate is the bound: the S
-// warps are busy 85 % of the time (half of it making K'), the tensor pipe 40 %, DRAM 56 %.  With the
-// products left out it takes 270 us; without K', S's terms, the scores or P each about 20 us less.
+// Measured (B=4 H=32 T=8192 d=128, 128 CTAs): 287 us, 3.8 TB/s, 56 % of the measured copy rate; 2.2 us a
+// chunk, in which an SM issues about 9,400 warp instructions at 2.16 a cycle.  What bounds it is that issue
+// rate with the chunk's chain of hand-overs: the S warps are busy 85 % of the time, the tensor pipe 40 %.
+// No single part carries it: left out one at a time, P and K' save 35 us each, the scores 29, the
+// products 27, S's terms 20, the outputs 15, the decay sums 9.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -212,14 +213,16 @@ constexpr int kMaxParts = 32;
 struct CutRule {
     int most, target;   // sequences of more than `most` chunks are cut, into parts of about `target`
     int slots;
+    int whole, parts;   // dense: (sequence, head) units before `whole` are not cut, the others into `parts`
 };
 
 // Dense batches: the piece of CTA b by arithmetic.  kFullPass: over all parts, else over all but each
-// sequence's last.
+// cut unit's last.
 template <bool kFullPass>
 __device__ __forceinline__ Piece dense_piece(const LinArgs &a, int b, const CutRule &cut) {
-    const int P = cut.slots / a.num_seqs + 1, per = (kFullPass ? P : P - 1) * a.heads, n = b / per;
-    return {n, b % a.heads, b % per / a.heads, P, n * (P - 1), (int)(n * a.seqlen), (int)((n + 1) * a.seqlen), 0};
+    const int x = kFullPass ? b - cut.whole : b, cuts = a.num_seqs * a.heads - cut.whole;
+    const int p = x >= 0 ? x / cuts : 0, u = x >= 0 ? cut.whole + x % cuts : b, P = x >= 0 ? cut.parts : 1, n = u / a.heads;
+    return {n, u % a.heads, p, P, (n - cut.whole / a.heads) * (P - 1), (int)(n * a.seqlen), (int)((n + 1) * a.seqlen), 0};
 }
 
 // Packed sequences: one CTA makes the lists of pieces, `pre` of all parts but each sequence's last, `full`
@@ -854,8 +857,10 @@ cudaError_t take_lin_expiries(cudaStream_t st, unsigned int *count) {
 
 // How a call is cut, the CTAs of the two passes.  Cutting costs a first pass over K and V (about half the
 // time of the whole) of the parts but the last, so:
-//  - dense batches with fewer (sequence, head) units than SMs get as many parts per unit as fill the SMs,
-//    of at least kMinPart chunks (8 heads of 32767 tokens: 0.13 ms in 19 parts, 1.3 ms whole);
+//  - of a dense batch's (sequence, head) units those that the last round of SMs has no full set of are cut
+//    into as many parts as fill the SMs, of at least kMinPart chunks (T=8192: 160 units 342 us, whole 573;
+//    192 units 472, whole 579; T=1536: 8 units 44 us, whole 60); two parts are worth the first pass from 48
+//    chunks on (70 units of 64 chunks 141 us, whole 150; of 32 both 80; of 16 48 us, whole 43);
 //  - packed sequences, whose lengths only the device knows, run longest first, and those of more than
 //    1.5 times an SM's equal share of all chunks are cut into quarters of that share (sequences just
 //    above it are not: the first pass costs more than the SMs that wait).
@@ -866,7 +871,7 @@ struct Cut {
 constexpr int64_t kMinPart = 8;
 static Cut cut_of(int64_t tokens, int64_t num_seqs, int64_t heads, bool packed, bool whole) {
     const int64_t units = num_seqs * heads, all = packed ? (tokens + C - 1) / C + num_seqs : num_seqs * ((tokens / num_seqs + C - 1) / C);
-    Cut c{{0x7fffffff, 1, 0}, 0, units};
+    Cut c{{0x7fffffff, 1, 0, (int)units, 1}, 0, units};
     if (whole) return c;
     if (packed) {
         const int64_t share = (all * heads + kSms - 1) / kSms;
@@ -875,19 +880,22 @@ static Cut cut_of(int64_t tokens, int64_t num_seqs, int64_t heads, bool packed, 
         if (most < 2 * kMinPart) most = 2 * kMinPart;
         // at most all / (most + 1) sequences are cut, into ceil(nc / target) parts
         const int64_t slots = all <= most ? 0 : all / target;
-        c.rule = {(int)most, (int)target, (int)slots};
+        c.rule = {(int)most, (int)target, (int)slots, 0, 1};
+        c.pre = slots * heads;
+        c.full = units + c.pre;
     } else {
-        const int64_t nc = all / num_seqs;
-        int64_t parts = kSms / units;
+        const int64_t nc = all / num_seqs, cuts = units % kSms, kept = units - cuts;
+        if (cuts == 0) return c;
+        int64_t parts = kSms / cuts;
         if (parts > kMaxParts) parts = kMaxParts;
         if (parts > nc / kMinPart) parts = nc / kMinPart;
-        if (parts <= 1) return c;
+        if (parts <= 1 || (parts == 2 && nc < 48)) return c;
         const int64_t target = (nc + parts - 1) / parts;
         parts = (nc + target - 1) / target;
-        c.rule = {0, (int)target, (int)(num_seqs * (parts - 1))};
+        c.rule = {0, (int)target, (int)((num_seqs - kept / heads) * (parts - 1)), (int)kept, (int)parts};
+        c.pre = cuts * (parts - 1);
+        c.full = units + c.pre;
     }
-    c.pre = c.rule.slots * heads;
-    c.full = units + c.pre;
     return c;
 }
 

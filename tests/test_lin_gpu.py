@@ -288,3 +288,12 @@ def test_waits_that_give_up(K, T, H, dk):
     K.kda_lin_chunk_fwd_bounded(*args, 1 << 20)
     R.check_lin(out, fin, ref)
     assert K.kda_device_status() == K.KDA_OK
+
+
+@pytest.mark.parametrize("B,H,T", [(5, 32, 1100), (1, 160, 2100), (4, 40, 2085), (9, 24, 3077), (3, 57, 1536), (1, 304, 1100), (16, 19, 1090), (20, 19, 640)])
+def test_more_heads_than_one_round(K, B, H, T):
+    """(sequence, head) pairs just above a round of one CTA per SM: the ones left over are cut, from the middle of a
+    sequence's heads on."""
+    d = make(31, B, T, H, H, 64, 64, BF16, decay="head", init=B)
+    out, fin = K.kda_lin_chunk_fwd(**d)
+    R.check_lin(out, fin, reference(d))

@@ -81,7 +81,9 @@ __global__ void __launch_bounds__(kAppendThreads) kda_paged_append_kernel(const 
 // has 4 D FLOP per query head and token for 2 D elements read, far below the tensor cores' rate.
 //
 // Work.  A unit is a row's key/value head with a block of up to RP of its query heads; a unit's
-// items are its tiles of 64 tokens (at least one).  The items of all units, in order, are cut into
+// items are its tiles of 64 tokens (at least one) and, ahead of them, kStart that stand for the time a
+// unit's start takes (30 rows of 1 to 16316 tokens, 8 key/value heads: 45 us, 89 us without them, 50 and
+// 47 with two and five).  The items of all units, in order, are cut into
 // equal shares, one per CTA (two CTAs per SM): each CTA finds its share from seq_lens on the
 // device, since the host does not see the lengths.  A unit that ends up in several shares leaves
 // one partial (running maximum, sum, unnormalised output) per share in the workspace, and a second
@@ -99,6 +101,7 @@ __global__ void __launch_bounds__(kAppendThreads) kda_paged_append_kernel(const 
 //    the output's own rounding.
 //  - fp32: the same walk in fp32 arithmetic (four lanes share a token's channels).
 constexpr int kWarps = 4, kTile = 64, kStages = 3, kAttThreads = 32 * kWarps;
+constexpr int kStart = 3;   // a unit's start, in tiles
 constexpr int kCtas = 2 * kSms;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -129,6 +132,7 @@ __device__ __forceinline__ int row_tiles(const PagedArgs &a, int n) {
     const int t = (row_length(a, n) + kTile - 1) / kTile;
     return t > 0 ? t : 1;
 }
+__device__ __forceinline__ int row_items(const PagedArgs &a, int n) { return kStart + row_tiles(a, n); }   // of each of its units
 
 // Block-wide sum of one value per thread, in every thread.
 template <int THREADS>
@@ -144,8 +148,8 @@ __device__ __forceinline__ long long block_sum(long long x, long long *sm) {
     return s;
 }
 
-// Block-wide: the row that holds item x (items of `per` units for each of a row's tiles, in row
-// order) and the number of items before that row.
+// Block-wide: the row that holds item x (rows in order, `per` units of row_items each) and the number of
+// items before that row.
 template <int THREADS>
 __device__ void find_row(const PagedArgs &a, int per, long long x, long long *sm, int &row, long long &before) {
     __shared__ int s_row;
@@ -154,7 +158,7 @@ __device__ void find_row(const PagedArgs &a, int per, long long x, long long *sm
     long long run = 0;
     for (int base = 0; base < a.rows; base += THREADS) {
         const int n = base + t;
-        const long long w = n < a.rows ? (long long)per * row_tiles(a, n) : 0;
+        const long long w = n < a.rows ? (long long)per * row_items(a, n) : 0;
         long long v = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -223,27 +227,27 @@ __global__ void __launch_bounds__(kAttThreads, 2) kda_paged_attention_kernel(con
     const PagedArgs &p = a.p;
     const int per = p.kv_heads * a.blocks;
     long long x, x1, us = 0;   // this CTA's share of the items; the current unit's first item
-    int n, tiles, unit;        // row, its tiles, key/value head and head block within it
+    int n, items, unit;        // row, its units' items, key/value head and head block within it
     if constexpr (kShort) {
         const int ru = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
         n = ru / per;
         unit = ru % per;
-        tiles = row_tiles(p, n);
-        x = (long long)rank * tiles / a.cluster;
-        x1 = (long long)(rank + 1) * tiles / a.cluster;
+        items = row_tiles(p, n);
+        x = (long long)rank * items / a.cluster;
+        x1 = (long long)(rank + 1) * items / a.cluster;
     } else {
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         long long mine = 0;
-        for (int i = tid; i < p.rows; i += kAttThreads) mine += row_tiles(p, i);
+        for (int i = tid; i < p.rows; i += kAttThreads) mine += row_items(p, i);
         const long long W = per * block_sum<kAttThreads>(mine, sm_sum);
         const long long G = W < gridDim.x ? W : gridDim.x;   // shares: at least one item each
         if (blockIdx.x >= G) return;
         x1 = (blockIdx.x + 1) * W / G;
         x = blockIdx.x * W / G;
         find_row<kAttThreads>(p, per, x, sm_sum, n, us);
-        tiles = row_tiles(p, n);
-        unit = (int)((x - us) / tiles);
-        us += (long long)unit * tiles;
+        items = row_items(p, n);
+        unit = (int)((x - us) / items);
+        us += (long long)unit * items;
     }
 
     uint8_t *ring = ring_all + warp * A::RING;
@@ -256,11 +260,12 @@ __global__ void __launch_bounds__(kAttThreads, 2) kda_paged_attention_kernel(con
         const int hk = unit / a.blocks, h0 = (unit - hk * a.blocks) * RP;
         const int heads = a.rep - h0 < RP ? a.rep - h0 : RP;      // query heads of this block
         const int64_t hq = (int64_t)n * p.heads + (int64_t)hk * a.rep + h0;
-        const long long xe = us + tiles < x1 ? us + tiles : x1;
-        const bool whole = kShort ? a.cluster == 1 : x == us && xe == us + tiles;
+        const long long xe = us + items < x1 ? us + items : x1;
+        const bool whole = kShort ? a.cluster == 1 : x == us && xe == us + items;
         const int len = row_length(p, n);
-        const int ta = (int)(x - us) * kTile;
-        const int tb = (int)(xe - us) * kTile < len ? (int)(xe - us) * kTile : len;
+        constexpr int S = kShort ? 0 : kStart;   // a unit's first items stand for its start
+        const int ia = (int)(x - us) - S, ib = (int)(xe - us) - S;
+        const int ta = ia > 0 ? ia * kTile : 0, tb = ib * kTile < len ? ib * kTile : len;
         const int groups = tb > ta ? (tb - ta + A::GT - 1) / A::GT : 0;
         const int mygroups = groups > warp ? (groups - warp + kWarps - 1) / kWarps : 0;
         const int32_t *table = p.table + (int64_t)n * p.max_pages;
@@ -562,67 +567,112 @@ __global__ void __launch_bounds__(kAttThreads, 2) kda_paged_attention_kernel(con
         }
         x = xe;
         if (x >= x1) break;
-        us += tiles;          // the next unit
+        us += items;          // the next unit
         if (++unit == per) {
             unit = 0;
             ++n;
-            tiles = row_tiles(p, n);
+            items = row_items(p, n);
         }
         __syncthreads();      // the rings and the warps' sums are read
     }
 }
 
-// Joins the parts of the units that fell into several shares.  One CTA per boundary between two
-// shares (blockIdx.x + 1 is the share after it) and head of the block: it joins the unit that the
-// boundary cuts, unless an earlier boundary cuts it too.  Every CTA waits for the first kernel to
+// Joins the parts of the units that fell into several shares, a head of the block per CTA.  Where there are
+// few units (256 threads), one CTA per unit; else (128) one per boundary between two shares (blockIdx.x + 1
+// is the share after it), which joins the unit that the boundary cuts, unless an earlier one cuts it too.
+// Groups of D / 4 threads take every kGroups-th part, four of them at once, each group with a maximum
+// and a sum of its own, which are joined in shared memory: a long row alone has some 300 parts, whose
+// loads would otherwise wait for one another (a row of 100,000 tokens, one key/value head: 22 us for the
+// whole call, 45 us with one group and a CTA per boundary).  Every CTA waits for the first kernel to
 // end, so that nothing behind this kernel in the stream starts before that.
-template <typename T, int D>
-__global__ void __launch_bounds__(D) kda_paged_join_kernel(const AttArgs a, const int ctas) {
-    __shared__ long long sm_sum[D / 32];
-    __shared__ float sm_m[D / 32];
+template <typename T, int D, int kJoinThreads>
+__global__ void __launch_bounds__(kJoinThreads) kda_paged_join_kernel(const AttArgs a, const int ctas) {
+    constexpr bool by_unit = kJoinThreads > 128;
+    constexpr int kGroups = kJoinThreads / (D / 4), kAtOnce = 4;
+    __shared__ long long sm_sum[kJoinThreads / 32];
+    __shared__ float sm_m[kGroups], sm_l[kGroups];
+    __shared__ __align__(16) float sm_o[kGroups][D];
     const PagedArgs &p = a.p;
     const int per = p.kv_heads * a.blocks, tid = threadIdx.x, r = blockIdx.y;
-    long long mine = 0;
-    for (int i = tid; i < p.rows; i += D) mine += row_tiles(p, i);
-    const long long W = per * block_sum<D>(mine, sm_sum);
+    long long mine = 0, ahead = 0;   // items of all rows (per unit), and of those before this CTA's
+    int n = by_unit ? (int)blockIdx.x / per : 0;
+    for (int i = tid; i < p.rows; i += kJoinThreads) {
+        const int t = row_items(p, i);
+        mine += t;
+        ahead += i < n ? t : 0;
+    }
+    const long long W = per * block_sum<kJoinThreads>(mine, sm_sum);
     const long long G = W < ctas ? W : ctas;
-    const int b0 = blockIdx.x;                          // the share before the boundary
-    const long long x = (b0 + 1) * W / G;
-    int n = 0, h = a.rep, b1 = b0;
+    int unit = 0, h = a.rep, b0 = blockIdx.x, b1 = b0;   // the unit's first share and its last
     long long us = 0;
-    int hk = 0;
-    if (b0 + 1 < G) {
-        find_row<D>(p, per, x, sm_sum, n, us);
-        const int tiles = row_tiles(p, n), unit = (int)((x - us) / tiles);
-        us += (long long)unit * tiles;
-        hk = unit / a.blocks;
-        h = (unit - hk * a.blocks) * a.rp + r;
-        if (x > us && b0 * W / G <= us) b1 = (int)(((us + tiles) * G - 1) / W);   // the share of its last item
+    if (by_unit) {
+        unit = (int)blockIdx.x % per;
+        const int items = row_items(p, n);
+        us = per * block_sum<kJoinThreads>(ahead, sm_sum) + (long long)unit * items;
+        b0 = (int)(((us + 1) * G - 1) / W);
+        b1 = (int)(((us + items) * G - 1) / W);
+        h = unit % a.blocks * a.rp + r;
+    } else if (b0 + 1 < G) {
+        const long long x = (b0 + 1) * W / G;
+        find_row<kJoinThreads>(p, per, x, sm_sum, n, us);
+        const int items = row_items(p, n);
+        unit = (int)((x - us) / items);
+        us += (long long)unit * items;
+        h = unit % a.blocks * a.rp + r;
+        if (x > us && b0 * W / G <= us) b1 = (int)(((us + items) * G - 1) / W);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (b1 == b0 || h >= a.rep) return;
     const int64_t s0 = 2 * (int64_t)b0 + (us > b0 * W / G ? 1 : 0);   // its part in b0; then slot 0 of b0 + 1 .. b1
     const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
-    float mx = -INFINITY;
-    for (int b = b0 + tid; b <= b1; b += D) mx = fmaxf(mx, __ldcg(ml + (b == b0 ? s0 : 2 * (int64_t)b) * a.rp + r).x);
+    const int grp = tid / (D / 4), c4 = tid % (D / 4);
+    float mx = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = b0 + grp; b <= b1; b += kAtOnce * kGroups) {
+        float2 v[kAtOnce];
+        float4 o[kAtOnce];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if ((tid & 31) == 0) sm_m[tid >> 5] = mx;
-    __syncthreads();
+        for (int e = 0; e < kAtOnce; ++e) {
+            const int be = b + e * kGroups;
+            const int64_t at = (be == b0 ? s0 : 2 * (int64_t)be) * a.rp + r;
+            v[e] = be <= b1 ? __ldcg(ml + at) : make_float2(-INFINITY, 0.f);
+            o[e] = be <= b1 ? __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * D) + c4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float top = mx;
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) mx = fmaxf(mx, sm_m[w]);
-    const float z = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f, acc = 0.f;
-#pragma unroll 8
-    for (int b = b0; b <= b1; ++b) {
-        const int64_t at = (b == b0 ? s0 : 2 * (int64_t)b) * a.rp + r;
-        const float2 v = __ldcg(ml + at);
-        const float f = ex2(v.x - z);
-        sum = fmaf(v.y, f, sum);
-        acc = fmaf(__ldcg(a.part_o + at * D + tid), f, acc);
+        for (int e = 0; e < kAtOnce; ++e) top = fmaxf(top, v[e].x);
+        const float z = top == -INFINITY ? 0.f : top, f0 = ex2(mx - z);
+        mx = top;
+        sum *= f0;
+        acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) {
+            const float f = ex2(v[e].x - z);
+            sum = fmaf(v[e].y, f, sum);
+            acc = make_float4(fmaf(o[e].x, f, acc.x), fmaf(o[e].y, f, acc.y), fmaf(o[e].z, f, acc.z), fmaf(o[e].w, f, acc.w));
+        }
     }
-    const int64_t hq = (int64_t)n * p.heads + (int64_t)hk * a.rep + h;
-    static_cast<T *>(p.out)[hq * D + tid] = from_f<T>(sum == 0.f ? 0.f : acc / sum);
+    *reinterpret_cast<float4 *>(&sm_o[grp][4 * c4]) = acc;
+    if (c4 == 0) {
+        sm_m[grp] = mx;
+        sm_l[grp] = sum;
+    }
+    __syncthreads();
+    if (tid >= D) return;
+    mx = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < kGroups; ++e) mx = fmaxf(mx, sm_m[e]);
+    const float z = mx == -INFINITY ? 0.f : mx;
+    float out = 0.f;
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kGroups; ++e) {
+        const float f = ex2(sm_m[e] - z);
+        sum = fmaf(sm_l[e], f, sum);
+        out = fmaf(sm_o[e][tid], f, out);
+    }
+    const int64_t hq = (int64_t)n * p.heads + (int64_t)(unit / a.blocks) * a.rep + h;
+    static_cast<T *>(p.out)[hq * D + tid] = from_f<T>(sum == 0.f ? 0.f : out / sum);
     if (p.lse && tid == 0) p.lse[hq] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
@@ -665,12 +715,14 @@ cudaError_t launch_att(const AttArgs &a, int grid, cudaStream_t st) {
     kda_paged_attention_kernel<T, D, RP, false><<<grid, kAttThreads, smem, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1) return e;   // (one CTA: nothing is split)
-    cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)(a.rep < RP ? a.rep : RP));
-    cfg.blockDim = dim3(D);
+    const int64_t units = (int64_t)a.p.rows * a.p.kv_heads * a.blocks;
+    const bool few = 2 * units <= grid;
+    cfg.gridDim = dim3((unsigned)(few ? units : grid - 1), (unsigned)(a.rep < RP ? a.rep : RP));
+    cfg.blockDim = dim3(few ? 256 : 128);
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // the join's CTAs may start, find their parts
     at[0].val.programmaticStreamSerializationAllowed = 1;            // and wait before the first kernel has ended
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kda_paged_join_kernel<T, D>, a, grid);
+    return few ? cudaLaunchKernelEx(&cfg, kda_paged_join_kernel<T, D, 256>, a, grid) : cudaLaunchKernelEx(&cfg, kda_paged_join_kernel<T, D, 128>, a, grid);
 }
 
 // CTAs of the attention kernel: the items' share-out never needs more than there can be items.

@@ -223,3 +223,17 @@ def test_append_then_attend_on_another_stream_and_in_a_graph(K):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("dt,d", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("lens,Hq,Hkv", [([20011], 4, 1), ([1, 14533], 24, 2), ([0, 0, 9999, 0], 2, 2), ([1], 3, 1), ([0], 2, 1), ([64, 65, 1, 0], 8, 4),
+                                         ([(i * 7919) % 400 for i in range(39)] + [12000], 8, 4), ([0] * 63 + [9000] + [5] * 30, 6, 3),
+                                         ([8000] + [1] * 400, 1, 1)])
+def test_shares_of_all_kinds(K, dt, d, lens, Hq, Hkv):
+    """Tables wide enough for the shared-out form whatever the lengths: few units with many parts, more units than
+    shares, shares that hold a unit's start only."""
+    c = cache(8, lens, Hq, Hkv, d, 16, dt)
+    wide = torch.full((len(lens), 600 * 16), -1, dtype=torch.int32, device="cuda")
+    wide[:, : c["block_table"].shape[1]] = c["block_table"]
+    c["block_table"] = wide
+    R.check_paged(*K.kda_paged_attention(**c), reference(c))

@@ -24,8 +24,9 @@
 //                terms to TMEM
 //   warps 8-15   the scores (mma.sync), the previous chunk's outputs from TMEM to global memory, P
 //                (decays and bf16 terms on the scores' fragments)
-//   warp 16      TMA of the tiles, three chunks ahead, and the decay sums
+//   warp 16      TMA of the tiles, three chunks ahead
 //   warp 17      issues the tensor-core products
+//   warps 18, 19 the decay sums, each of every other chunk
 // Per chunk the tensor pipe runs (1) 12 x M128 N128 K16, (2) 16 x M128 N64 K16, (3) 8 x M128 N64
 // K16, in this order: K' of the next chunk is made during (2) and (3), and the S warps have the
 // whole of (1) to turn dS of the chunk before into the operand of (2).
@@ -65,7 +66,7 @@ constexpr uint32_t OFF_BAR = OFF_G + kStages * G_SLOT;
 // passed the one before.  That holds because each phase needs, directly or through others, an
 // arrival that its slowest waiter makes after that pass; the products (1) run ahead of the S warps
 // and so have a barrier for each of dS's buffers.
-enum Bar { kFull = 0, kEmpty = 3, kKp = 6, kP = 7, kReady = 8, kOFull = 9, kDone = 10, kBars = 12 };
+enum Bar { kFull = 0, kEmpty = 3, kKp = 6, kP = 7 /* kKp + 1 */, kReady = 8, kOFull = 9, kDone = 10, kBars = 12 };
 constexpr uint32_t OFF_TM = OFF_BAR + kBars * 8;
 constexpr uint32_t SMEM_BYTES = OFF_TM + 16 + 1024;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
@@ -191,6 +192,56 @@ __device__ __forceinline__ uint2 three_bf16(float w) {
     const float a = __bfloat162float(__float2bfloat16_rn(w)), b = __bfloat162float(__float2bfloat16_rn(w - a));
     const float c = (w - a) - b;
     return make_uint2(pack_bf16(a, b), pack_bf16(c, c));
+}
+
+// K' = k w in packed bf16 arithmetic, by THREADS threads: the keys of the tiles at `st` into three terms at
+// `kp`, `term` bytes apart.  The factor comes as three bf16 terms; k w_0 = h + e and k w_1 = y + y' exactly
+// (8-bit times 8-bit significands), m = e + y rounded, and the third term is what that rounding left
+// plus y' + k w_2: the sum of the three is within 2^-22 (2^-26 RMS) of k w.  16-byte pieces lie at the
+// same offsets in K and K'.  (Loads come before stores here and below: the compiler keeps their order,
+// and a load behind a store waits its whole way.)
+template <int THREADS, int kDk>
+__device__ __forceinline__ void scale_keys(uint8_t *sm, uint32_t st, uint32_t kp, uint32_t term, const float *gv, int nr, int tid) {
+    constexpr int E = 8 * kDk >= 2 * THREADS ? 2 : 1;
+#pragma unroll 1
+    for (int x0 = tid; x0 < 8 * kDk; x0 += E * THREADS) {
+        uint4 uk[E];
+        uint2 wk[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int x = x0 + THREADS * e;
+            uk[e] = *reinterpret_cast<const uint4 *>(sm + st + 16384 + 16 * x);
+            wk[e] = reinterpret_cast<const uint2 *>(gv + 128)[(x >> 3) & 63];
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int x = x0 + THREADS * e, r = (x >> 3) & 63;
+            const __nv_bfloat162 w0 = as_bf162(__byte_perm(wk[e].x, 0, 0x1010)), w1 = as_bf162(__byte_perm(wk[e].x, 0, 0x3232)),
+                                 w2 = as_bf162(wk[e].y);
+            if (nr < C && r >= nr) {   // rows past the sequence belong to another one: they never enter a product
+                uk[e] = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4 *>(sm + st + 32768 + 16 * x) = uk[e];
+                if (kDk == 64) *reinterpret_cast<uint4 *>(sm + st + 40960 + 16 * x) = uk[e];   // V is 128 wide
+            }
+            const uint32_t uw[4] = {uk[e].x, uk[e].y, uk[e].z, uk[e].w};
+            uint32_t o0[4], o1[4], o2[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const __nv_bfloat162 kv = as_bf162(uw[c]);
+                const __nv_bfloat162 hh = __hmul2_rn(kv, w0), ee = __hfma2(kv, w0, __hneg2(hh));
+                const __nv_bfloat162 yy = __hmul2_rn(kv, w1), ye = __hfma2(kv, w1, __hneg2(yy));
+                const __nv_bfloat162 mm = __hadd2_rn(ee, yy);
+                const __nv_bfloat162 ll = __hadd2_rn(__hsub2_rn(yy, __hsub2_rn(mm, ee)), __hfma2(kv, w2, ye));
+                o0[c] = as_u32(hh);
+                o1[c] = as_u32(mm);
+                o2[c] = as_u32(ll);
+            }
+            uint4 *to = reinterpret_cast<uint4 *>(sm + kp + 16 * x);
+            to[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+            to[term / 16] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+            to[term / 8] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+        }
+    }
 }
 
 // x as a bf16 pair and the rest it leaves
@@ -322,7 +373,8 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan_kernel(const LinArgs a,
 // kFullPass: the whole forward of a part; a part other than the first starts from the state in the slot
 // of the part before it.  Otherwise only the state that a part reaches from zero, into its slot of
 // `locals`, and its total log2 decay; lin_scan_kernel then turns each slot into the true state behind
-// its part.
+// its part.  There warps 0-15 make K' together, a chunk ahead of the products, and warps 0-7 the state: 1.1 us
+// a chunk, its chain of hand-overs (8 warps and one K' at a time: 1.75 us).
 // kDk: the key channels, 64 or 128 (value channels are always 128 lanes; those a head lacks read as zeros).
 template <bool kFullPass, int kDk>
 __global__ void __launch_bounds__(NT, 1)
@@ -333,6 +385,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
     constexpr int KC = kDk / 2;                // key channels of the state per thread
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_fail;
+    __shared__ double s_decay[2];
     __shared__ volatile int s_piece[4];   // unit, the part's slot, whether it is the last (read again at the end:
                                           // registers are scarce in the loop)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -364,9 +417,9 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
             mbar_init(bar(kFull + s), 1 + 32);                // the tiles, and the warp that writes the decay vectors
             mbar_init(bar(kEmpty + s), kFullPass ? 9 : 1);   // the products, and the warps that staged outputs there
         }
-        mbar_init(bar(kKp), 256);
-        mbar_init(bar(kP), 256);
-        mbar_init(bar(kReady), kFullPass ? 512 : 256);
+        mbar_init(bar(kKp), kFullPass ? 256 : 512);
+        mbar_init(bar(kP), kFullPass ? 256 : 512);   // first pass: K' of odd chunks
+        mbar_init(bar(kReady), 512);
         mbar_init(bar(kDone), 1);
         mbar_init(bar(kDone + 1), 1);
         mbar_init(bar(kOFull), 1);
@@ -389,6 +442,16 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
     auto wait = [&](int b, uint32_t parity) { return mbar_wait_small(bar(b), parity & 1u, a.wait_polls); };
     auto done = [&](int k) { return wait(kDone + (k & 1), k >> 1); };
     bool ok = true;
+    // K' of chunk k in the first pass, by 512 threads: chunk k + 1's is made while the products of chunk k run,
+    // odd chunks' in the places of the Q tiles, which that pass does not load (the last products to read
+    // from there, chunk k - 2's, are done).
+    auto keys_of_pass_one = [&](int k) {
+        if (!((k < 2 || done(k - 2)) && wait(kFull + k % kStages, k / kStages))) return false;
+        const int left = eos - (first + k * C);
+        scale_keys<512, kDk>(sm, (k % kStages) * STAGE, k & 1 ? 0 : OFF_KP, k & 1 ? STAGE : 16384, gslot(k), left < C ? left : C, tid);
+        fence_async_smem();
+        return true;
+    };
 
     if (warp < 8) {
         // ---- S
@@ -406,8 +469,45 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
 #pragma unroll
                 for (int c = 0; c < KC; ++c) v[c] = __ldcg(from + at + (int64_t)c * a.dv);
         }
+        auto take_ds = [&](int k, float f) {   // v <- f v + dS of chunk k
+            tc_fence_after();
+            const float2 d2 = make_float2(f, f);
+#pragma unroll
+            for (int b = 0; b < KC / 32; ++b) {
+                float w[32];
+                tmem_ld32(trow + TM_DS + 128 * (k & 1) + i0 + 32 * b, w);
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    const float2 x = __ffma2_rn(d2, make_float2(v[32 * b + c], v[32 * b + c + 1]), make_float2(w[c], w[c + 1]));
+                    v[32 * b + c] = x.x;
+                    v[32 * b + c + 1] = x.y;
+                }
+            }
+        };
         float dec = 0.f;   // e^(sum of the chunk's log decays)
-        for (int k = 0; k <= chunks; ++k) {
+        for (int k = 0; !kFullPass && k <= chunks; ++k) {
+            float next = 0.f;
+            if (k < chunks) {
+                ok = keys_of_pass_one(k);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                next = gslot(k)[320];
+                mbar_arrive(bar(kKp + (k & 1)));
+            }
+            if (k > 0) {
+                ok = done(k - 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                take_ds(k - 1, dec);
+                tc_fence_before();
+            }
+            dec = next;
+        }
+        for (int k = 0; kFullPass && k <= chunks; ++k) {
             // dS and K' of the chunk before are done with; this chunk's tile and decays landed
             if (k > 0) ok = done(k - 1);
             if (ok && k < chunks) ok = wait(kFull + k % kStages, k / kStages);
@@ -419,69 +519,11 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 const uint32_t st = (k % kStages) * STAGE;
                 const float *gv = gslot(k);
                 const int left = eos - (first + k * C), nr = left < C ? left : C;
-                // K' = k w in packed bf16 arithmetic.  The factor comes as three bf16 terms; k w_0 = h + e and
-                // k w_1 = y + y' exactly (8-bit times 8-bit significands), m = e + y rounded, and the third
-                // term is what that rounding left plus y' + k w_2: the sum of the three is within 2^-22
-                // (2^-26 RMS) of k w.  16-byte pieces lie at the same offsets in K and K'.  (Loads come before
-                // stores here and below: the compiler keeps their order, and a load behind a store waits its
-                // whole way.)
-#pragma unroll 1
-                for (int x0 = tid; x0 < 8 * kDk; x0 += 512) {
-                    uint4 uk[2];
-                    uint2 wk[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int x = x0 + 256 * e;
-                        uk[e] = *reinterpret_cast<const uint4 *>(sm + st + 16384 + 16 * x);
-                        wk[e] = reinterpret_cast<const uint2 *>(gv + 128)[(x >> 3) & 63];
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int x = x0 + 256 * e, r = (x >> 3) & 63;
-                        const __nv_bfloat162 w0 = as_bf162(__byte_perm(wk[e].x, 0, 0x1010)), w1 = as_bf162(__byte_perm(wk[e].x, 0, 0x3232)),
-                                             w2 = as_bf162(wk[e].y);
-                        if (nr < C && r >= nr) {   // rows past the sequence belong to another one: they never enter a product
-                            uk[e] = make_uint4(0u, 0u, 0u, 0u);
-                            *reinterpret_cast<uint4 *>(sm + st + 32768 + 16 * x) = uk[e];
-                            if (kDk == 64) *reinterpret_cast<uint4 *>(sm + st + 40960 + 16 * x) = uk[e];   // V is 128 wide
-                        }
-                        const uint32_t uw[4] = {uk[e].x, uk[e].y, uk[e].z, uk[e].w};
-                        uint32_t o0[4], o1[4], o2[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const __nv_bfloat162 kv = as_bf162(uw[c]);
-                            const __nv_bfloat162 hh = __hmul2_rn(kv, w0), ee = __hfma2(kv, w0, __hneg2(hh));
-                            const __nv_bfloat162 yy = __hmul2_rn(kv, w1), ye = __hfma2(kv, w1, __hneg2(yy));
-                            const __nv_bfloat162 mm = __hadd2_rn(ee, yy);
-                            const __nv_bfloat162 ll = __hadd2_rn(__hsub2_rn(yy, __hsub2_rn(mm, ee)), __hfma2(kv, w2, ye));
-                            o0[c] = as_u32(hh);
-                            o1[c] = as_u32(mm);
-                            o2[c] = as_u32(ll);
-                        }
-                        uint4 *to = reinterpret_cast<uint4 *>(sm + OFF_KP + 16 * x);
-                        to[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-                        to[1024] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-                        to[2048] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
-                    }
-                }
+                scale_keys<256, kDk>(sm, st, OFF_KP, 16384, gv, nr, tid);
                 fence_async_smem();
                 mbar_arrive(bar(kKp));
             }
-            if (k > 0) {
-                tc_fence_after();
-                const float2 d2 = make_float2(dec, dec);
-#pragma unroll
-                for (int b = 0; b < KC / 32; ++b) {
-                    float w[32];
-                    tmem_ld32(trow + TM_DS + 128 * ((k - 1) & 1) + i0 + 32 * b, w);
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        const float2 x = __ffma2_rn(d2, make_float2(v[32 * b + c], v[32 * b + c + 1]), make_float2(w[c], w[c + 1]));
-                        v[32 * b + c] = x.x;
-                        v[32 * b + c + 1] = x.y;
-                    }
-                }
-            }
+            if (k > 0) take_ds(k - 1, dec);
             if (k == chunks) break;
             dec = gslot(k)[320];
             if (kFullPass) {
@@ -533,6 +575,14 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
         const uint32_t qrow = sb + (16 * I + (lane & 15)) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
         const uint32_t krow = sb + 16384 + (8 * c0 + (lane & 7)) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
         uint8_t *prow = sm + OFF_P + i * 128 + 4 * t4;
+        for (int k = 0; !kFullPass && k < chunks; ++k) {
+            ok = keys_of_pass_one(k);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            mbar_arrive(bar(kKp + (k & 1)));
+        }
         for (int k = 0; kFullPass && k <= chunks; ++k) {
             const uint32_t st = (k % kStages) * STAGE;
             const float *gv = gslot(k);
@@ -636,17 +686,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
     } else {
         regs_dec<80>();
         if (warp == 16) {
-            // ---- tiles by TMA, and the decay sums: lane l holds tokens 2l and 2l + 1
-            float th = 0.f, tl = 0.f;   // the part's sum
-            const float hg = a.head_g ? __ldg(a.head_g + h) : 0.f;
-            const float *gp = a.g ? a.g + (int64_t)(first + 2 * lane) * H + h : nullptr;
-            float gx = 0.f, gy = 0.f;
-            auto load_g = [&](int k) {
-                const int t = first + k * C + 2 * lane;
-                gx = gp && t < eos ? __ldg(gp + (int64_t)k * C * H) : 0.f;
-                gy = gp && t + 1 < eos ? __ldg(gp + (int64_t)k * C * H + H) : 0.f;
-            };
-            if (chunks > 0) load_g(0);
+            // ---- tiles by TMA
             for (int k = 0; k < chunks; ++k) {
                 const int s = k % kStages;
                 ok = k < kStages || wait(kEmpty + s, k / kStages - 1);
@@ -668,33 +708,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                     }
                 }
                 __syncwarp();
-                const int t = first + k * C + 2 * lane;
-                float xh, xl, yh, yl;
-                log2_decay(gx, hg, t < eos, xh, xl);
-                log2_decay(gy, hg, t + 1 < eos, yh, yl);
-                if (k + 1 < chunks) load_g(k + 1);
-                float bh = xh, bl = xl;            // sums up to the lane's second token
-                add2f(bh, bl, yh, yl);
-#pragma unroll 1
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float ph = __shfl_up_sync(0xffffffffu, bh, o), pl = __shfl_up_sync(0xffffffffu, bl, o);
-                    if (lane >= o) add2f(bh, bl, ph, pl);
-                }
-                float ah = __shfl_up_sync(0xffffffffu, bh, 1), al = __shfl_up_sync(0xffffffffu, bl, 1);
-                if (lane == 0) ah = al = 0.f;
-                add2f(ah, al, xh, xl);             // and up to its first
-                const float eh = __shfl_sync(0xffffffffu, bh, 31), el = __shfl_sync(0xffffffffu, bl, 31);
-                float *gv = gslot(k);
-                reinterpret_cast<float2 *>(gv)[lane] = make_float2(ah, bh);
-                reinterpret_cast<float2 *>(gv + 64)[lane] = make_float2(al, bl);
-                const uint2 wa = three_bf16(exp2f((eh - ah) + (el - al))), wb = three_bf16(exp2f((eh - bh) + (el - bl)));
-                reinterpret_cast<uint4 *>(gv + 128)[lane] = make_uint4(wa.x, wa.y, wb.x, wb.y);
-                reinterpret_cast<float2 *>(gv + 256)[lane] = make_float2(exp2f(ah + al), exp2f(bh + bl));
-                if (lane == 0) gv[320] = exp2f(eh + el);
-                if (!kFullPass) add2f(th, tl, eh, el);
-                mbar_arrive(bar(kFull + s));
             }
-            if (!kFullPass && lane == 0) decays[s_piece[1]] = (double)th + (double)tl;
         } else if (warp == 17) {
             // ---- tensor-core products.  The whole warp runs the loop and an elected lane issues, so that the
             // operand descriptors can stay in uniform registers (half the instructions per product).
@@ -703,8 +717,9 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
             int s = 0;
             for (int k = 0; k < chunks; ++k) {
                 const uint32_t vd = desc_mn(sb + s * STAGE + 32768), qd = desc_k(sb + s * STAGE);
-                // dS of two chunks ago was taken before the S warps got ready for the chunk before
-                ok = wait(kKp, k) && (kFullPass || wait(kReady, k));
+                // dS of two chunks ago was taken before the S warps got ready for the chunk before (full pass) or
+                // made this chunk's K' (first pass)
+                ok = kFullPass ? wait(kKp, k) : wait(kKp + (k & 1), k >> 1);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -712,11 +727,12 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                 tc_fence_after();
                 const uint32_t ds = tmem + TM_DS + 128 * (k & 1);
                 if (one) {
+                    const uint32_t kd = kFullPass || !(k & 1) ? kpd : desc_mn(sb), term = (kFullPass || !(k & 1) ? 16384 : STAGE) >> 4;
 #pragma unroll 1
                     for (int e = 2; e >= 0; --e)   // the smallest terms first
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(ds, vd + ((2048 * kk) >> 4), kpd + ((16384 * e + 2048 * kk) >> 4), IDESC_KV, e < 2 || kk > 0);
+                            mma_ss(ds, vd + ((2048 * kk) >> 4), kd + term * e + ((2048 * kk) >> 4), IDESC_KV, e < 2 || kk > 0);
                     mma_commit(bar(kDone + (k & 1)));
                 }
                 __syncwarp();
@@ -757,6 +773,53 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
             }
             // nothing arrives at a barrier after the CTA has ended
             for (int k = chunks > kStages ? chunks - kStages : 0; ok && k < chunks; ++k) ok = wait(kEmpty + k % kStages, k / kStages);
+        } else {
+            // ---- the decay sums, every other chunk's: lane l holds tokens 2l and 2l + 1
+            float th = 0.f, tl = 0.f;   // the part's sum
+            const float hg = a.head_g ? __ldg(a.head_g + h) : 0.f;
+            const float *gp = a.g ? a.g + (int64_t)(first + 2 * lane) * H + h : nullptr;
+            float gx = 0.f, gy = 0.f;
+            auto load_g = [&](int k) {
+                const int t = first + k * C + 2 * lane;
+                gx = gp && t < eos ? __ldg(gp + (int64_t)k * C * H) : 0.f;
+                gy = gp && t + 1 < eos ? __ldg(gp + (int64_t)k * C * H + H) : 0.f;
+            };
+            const int k0 = warp & 1;
+            if (k0 < chunks) load_g(k0);
+            for (int k = k0; k < chunks; k += 2) {
+                const int s = k % kStages;
+                ok = k < kStages || wait(kEmpty + s, k / kStages - 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                const int t = first + k * C + 2 * lane;
+                float xh, xl, yh, yl;
+                log2_decay(gx, hg, t < eos, xh, xl);
+                log2_decay(gy, hg, t + 1 < eos, yh, yl);
+                if (k + 2 < chunks) load_g(k + 2);
+                float bh = xh, bl = xl;            // sums up to the lane's second token
+                add2f(bh, bl, yh, yl);
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float ph = __shfl_up_sync(0xffffffffu, bh, o), pl = __shfl_up_sync(0xffffffffu, bl, o);
+                    if (lane >= o) add2f(bh, bl, ph, pl);
+                }
+                float ah = __shfl_up_sync(0xffffffffu, bh, 1), al = __shfl_up_sync(0xffffffffu, bl, 1);
+                if (lane == 0) ah = al = 0.f;
+                add2f(ah, al, xh, xl);             // and up to its first
+                const float eh = __shfl_sync(0xffffffffu, bh, 31), el = __shfl_sync(0xffffffffu, bl, 31);
+                float *gv = gslot(k);
+                reinterpret_cast<float2 *>(gv)[lane] = make_float2(ah, bh);
+                reinterpret_cast<float2 *>(gv + 64)[lane] = make_float2(al, bl);
+                const uint2 wa = three_bf16(exp2f((eh - ah) + (el - al))), wb = three_bf16(exp2f((eh - bh) + (el - bl)));
+                reinterpret_cast<uint4 *>(gv + 128)[lane] = make_uint4(wa.x, wa.y, wb.x, wb.y);
+                reinterpret_cast<float2 *>(gv + 256)[lane] = make_float2(exp2f(ah + al), exp2f(bh + bl));
+                if (lane == 0) gv[320] = exp2f(eh + el);
+                if (!kFullPass) add2f(th, tl, eh, el);
+                mbar_arrive(bar(kFull + s));
+            }
+            if (!kFullPass && lane == 0) s_decay[k0] = (double)th + (double)tl;
         }
     }
     __syncwarp();
@@ -787,6 +850,8 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
             decays[s_piece[1]] = 0.0;
         }
         __syncthreads();
+    } else if (!kFullPass && tid == 0) {
+        decays[s_piece[1]] = s_decay[0] + s_decay[1];
     }
     if (warp == 17) {
         __syncwarp();
@@ -807,14 +872,25 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const LinArgs a,
     const int H = a.heads;
     const int64_t size = (int64_t)a.dk * a.dv, at = ((int64_t)blockIdx.y * kScanThreads + threadIdx.x) * 4;
     float4 s = a.s0 ? *reinterpret_cast<const float4 *>(a.s0 + ((int64_t)piece.n * H + piece.h) * size + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int p = 0; p < piece.P - 1; ++p) {
-        const int64_t slot = (int64_t)(piece.slot + p) * H + piece.h;
-        float4 *l = reinterpret_cast<float4 *>(locals + slot * size + at);
-        const float f = exp2f((float)decays[slot]);
-        const float4 x = __ldcg(l);
-        s = make_float4(fmaf(f, s.x, x.x), fmaf(f, s.y, x.y), fmaf(f, s.z, x.z), fmaf(f, s.w, x.w));
-        *l = s;
+    auto part = [&](int p) { return (int64_t)(piece.slot + p) * H + piece.h; };
+    auto state = [&](int p) { return reinterpret_cast<float4 *>(locals + part(p) * size + at); };
+    constexpr int kAtOnce = 8;   // parts whose loads are in flight together
+    for (int p0 = 0; p0 < piece.P - 1; p0 += kAtOnce) {
+        float4 x[kAtOnce];
+        double d[kAtOnce];
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e)
+            if (p0 + e < piece.P - 1) {
+                x[e] = __ldcg(state(p0 + e));
+                d[e] = __ldcg(decays + part(p0 + e));
+            }
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e)
+            if (p0 + e < piece.P - 1) {
+                const float f = exp2f((float)d[e]);
+                s = make_float4(fmaf(f, s.x, x[e].x), fmaf(f, s.y, x[e].y), fmaf(f, s.z, x[e].z), fmaf(f, s.w, x[e].w));
+                *state(p0 + e) = s;
+            }
     }
 }
 
@@ -855,47 +931,62 @@ cudaError_t take_lin_expiries(cudaStream_t st, unsigned int *count) {
     return e;
 }
 
-// How a call is cut, the CTAs of the two passes.  Cutting costs a first pass over K and V (about half the
-// time of the whole) of the parts but the last, so:
+// How a call is cut, the CTAs of the two passes.  Cutting costs a first pass over K and V (half the time
+// of the whole) of the parts but the last, so:
 //  - of a dense batch's (sequence, head) units those that the last round of SMs has no full set of are cut
-//    into as many parts as fill the SMs, of at least kMinPart chunks (T=8192: 160 units 342 us, whole 573;
-//    192 units 472, whole 579; T=1536: 8 units 44 us, whole 60); two parts are worth the first pass from 48
-//    chunks on (70 units of 64 chunks 141 us, whole 150; of 32 both 80; of 16 48 us, whole 43);
+//    into as many parts as should end first (best_parts; T=8192: 160 units 336 us, whole 573; 70 units 229,
+//    in two parts 264; 56 units of 13805 tokens 316, in two parts 364; 8 units of 32767 114 in 19);
 //  - packed sequences, whose lengths only the device knows, run longest first, and those of more than
-//    1.5 times an SM's equal share of all chunks are cut into quarters of that share (sequences just
-//    above it are not: the first pass costs more than the SMs that wait).
+//    1.5 times an SM's equal share of all chunks are cut into halves of that share (13 mixes of lengths:
+//    quarters take 2 to 25 % more time, whole shares between 21 % less and 22 % more; cutting from 1.1
+//    times the share on costs up to 46 %).  One sequence alone is cut as in a dense batch.
 struct Cut {
     CutRule rule;
     int64_t pre, full;
 };
 constexpr int64_t kMinPart = 8;
+
+// Parts, of at least kMinPart chunks, for `units` units of nc chunks each.  A CTA's time in tenths of a
+// microsecond is about 22 a chunk and 70 once, in the first pass 11 and 60; the scan and the launches take 100.
+static int64_t best_parts(int64_t units, int64_t nc) {
+    auto rounds = [](int64_t ctas) { return (ctas + kSms - 1) / kSms; };
+    int64_t parts = 1, best = rounds(units) * (22 * nc + 70);
+    for (int64_t p = 2; p <= kMaxParts && p * kMinPart <= nc; ++p) {
+        const int64_t per = (nc + p - 1) / p;
+        const int64_t cost = rounds(units * p) * (22 * per + 70) + rounds(units * (p - 1)) * (11 * per + 60) + 100;
+        if (cost < best) {
+            best = cost;
+            parts = p;
+        }
+    }
+    const int64_t per = (nc + parts - 1) / parts;
+    return (nc + per - 1) / per;
+}
+
 static Cut cut_of(int64_t tokens, int64_t num_seqs, int64_t heads, bool packed, bool whole) {
-    const int64_t units = num_seqs * heads, all = packed ? (tokens + C - 1) / C + num_seqs : num_seqs * ((tokens / num_seqs + C - 1) / C);
+    const int64_t units = num_seqs * heads, chunks = ((packed ? tokens : tokens / num_seqs) + C - 1) / C;
     Cut c{{0x7fffffff, 1, 0, (int)units, 1}, 0, units};
     if (whole) return c;
-    if (packed) {
-        const int64_t share = (all * heads + kSms - 1) / kSms;
-        int64_t most = share + share / 2, target = share / 4;
+    if (!packed) {
+        const int64_t cuts = units % kSms, kept = units - cuts, parts = cuts ? best_parts(cuts, chunks) : 1;
+        if (parts == 1) return c;
+        c.rule = {0, 1, (int)((num_seqs - kept / heads) * (parts - 1)), (int)kept, (int)parts};
+        c.pre = cuts * (parts - 1);
+    } else if (num_seqs == 1) {
+        const int64_t parts = best_parts(heads, chunks), target = (chunks + parts - 1) / parts;
+        c.rule = {(int)target, (int)target, (int)(parts - 1), 0, 1};
+        c.pre = heads * (parts - 1);
+    } else {
+        const int64_t all = chunks + num_seqs, share = (all * heads + kSms - 1) / kSms;   // (each sequence's last chunk may be short)
+        int64_t most = share + share / 2, target = share / 2;
         if (target < kMinPart) target = kMinPart;
         if (most < 2 * kMinPart) most = 2 * kMinPart;
         // at most all / (most + 1) sequences are cut, into ceil(nc / target) parts
         const int64_t slots = all <= most ? 0 : all / target;
         c.rule = {(int)most, (int)target, (int)slots, 0, 1};
         c.pre = slots * heads;
-        c.full = units + c.pre;
-    } else {
-        const int64_t nc = all / num_seqs, cuts = units % kSms, kept = units - cuts;
-        if (cuts == 0) return c;
-        int64_t parts = kSms / cuts;
-        if (parts > kMaxParts) parts = kMaxParts;
-        if (parts > nc / kMinPart) parts = nc / kMinPart;
-        if (parts <= 1 || (parts == 2 && nc < 48)) return c;
-        const int64_t target = (nc + parts - 1) / parts;
-        parts = (nc + target - 1) / target;
-        c.rule = {0, (int)target, (int)((num_seqs - kept / heads) * (parts - 1)), (int)kept, (int)parts};
-        c.pre = cuts * (parts - 1);
-        c.full = units + c.pre;
     }
+    c.full = units + c.pre;
     return c;
 }
 

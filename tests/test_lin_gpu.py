@@ -297,3 +297,12 @@ def test_more_heads_than_one_round(K, B, H, T):
     d = make(31, B, T, H, H, 64, 64, BF16, decay="head", init=B)
     out, fin = K.kda_lin_chunk_fwd(**d)
     R.check_lin(out, fin, reference(d))
+
+
+@pytest.mark.parametrize("lens,H", [([2500], 8), ([1000], 3), ([64], 160), ([2200, 1], 8), ([513, 0, 1900], 12), ([30000], 1)])
+def test_few_packed_sequences(K, lens, H):
+    """One packed sequence is cut like a dense batch's, few by their share."""
+    d = make(33, 1, sum(lens), H, H, 128, 64, BF16, decay="head", init=len(lens))
+    d["cu_seqlens"] = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
+    out, fin = K.kda_lin_chunk_fwd(**d)
+    R.check_lin(out, fin, reference({k: x for k, x in d.items() if k != "cu_seqlens"}, d["cu_seqlens"]))

@@ -388,8 +388,8 @@ kda_status_t kda_recurrent_steps_qknorm(const void *q, const void *k, const void
 
 /* kda_device_status -- waits for the work queued on `stream` to finish, then reads and
  * clears the current device's count of device-side waits of the tensor-core chunk kernels
- * that gave up (see kda_chunk_fwd_bounded; the two passes of kda_chunk_fwd_ws count theirs
- * too) and its word of failed debug-build input checks.  Returns KDA_ERR_INPUT when a check
+ * that gave up (see kda_chunk_fwd_bounded and kda_lin_chunk_fwd_bounded; the two passes of
+ * kda_chunk_fwd_ws count theirs too) and its word of failed debug-build input checks.  Returns KDA_ERR_INPUT when a check
  * failed since the previous call on this device (only a library built with debug checks
  * makes any), else KDA_ERR_TIMEOUT when at least one wait gave up, KDA_OK when neither
  * happened, and KDA_ERR_CUDA when the stream or the copies fail.  Both are device-global:
@@ -545,7 +545,7 @@ kda_status_t kda_paged_append(const void *k, const void *v, void *k_cache, void 
  *   workspace   : device memory of kda_paged_attention_workspace_bytes(dims) bytes, 16-byte
  *                 aligned (NULL when that is 0), contents on entry of no matter; one per
  *                 call in flight.  It holds the parts of rows that are split over their length.
- * Results do not depend on timing (parts are joined in the order of the tokens). */
+ * Results do not depend on timing (parts are joined in a fixed order). */
 kda_status_t kda_paged_attention(const void *q, const void *k_cache, const void *v_cache,
                                  const int32_t *block_table, const int32_t *seq_lens, float scale,
                                  void *out, float *lse, void *workspace, size_t workspace_bytes,

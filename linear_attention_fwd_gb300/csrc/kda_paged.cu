@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kAppendThreads) kda_paged_append_kernel(const 
 // equal shares, one per CTA (two CTAs per SM): each CTA finds its share from seq_lens on the
 // device, since the host does not see the lengths.  A unit that ends up in several shares leaves
 // one partial (running maximum, sum, unnormalised output) per share in the workspace, and a second
-// kernel joins them in the order of the tokens, so results do not depend on timing.
+// kernel joins them in a fixed order, so results do not depend on timing.
 // Where the rows can only be short (a row's share of the longest possible one at most kShortTokens),
 // one cluster of CTAs takes a unit instead, equal parts each, and joins them through distributed shared
 // memory: one launch and no workspace (one row of 777 tokens, 8 key/value heads: 5.8 us against 8.2).

@@ -18,7 +18,7 @@
 // multiply-add: the tensor cores truncate their sums, which over many chunks would pile up.
 //
 // Roles (20 warps; registers shared out by setmaxnreg, 104 / 104 / 96 / 96 / 80 per warpgroup out of the 5 x
-// 96 of the launch: measured against eleven other splits, 287 us and 291 to 440 us for B=4 H=32 T=8192).
+// 96 of the launch: measured against eleven other splits, 1 to 50 % slower for B=4 H=32 T=8192).
 // Everything meets at mbarriers; there is no CTA-wide barrier inside the loop.
 //   warps 0-7    K', then the state (64 key channels of one value channel per thread) and its bf16
 //                terms to TMEM
@@ -31,9 +31,9 @@
 // K16, in this order: K' of the next chunk is made during (2) and (3), and the S warps have the
 // whole of (1) to turn dS of the chunk before into the operand of (2).
 //
-// Measured (B=4 H=32 T=8192 d=128, 128 CTAs): 287 us, 3.8 TB/s, 56 % of the measured copy rate; 2.2 us a
-// chunk, in which an SM issues about 9,400 warp instructions at 2.16 a cycle.  What bounds it is that issue
-// rate with the chunk's chain of hand-overs: the S warps are busy 85 % of the time, the tensor pipe 40 %.
+// Measured (B=4 H=32 T=8192 d=128, 128 CTAs): 291 us, 3.7 TB/s, 55 % of the measured copy rate; 2.2 us a
+// chunk, in which an SM issues about 10,000 warp instructions at 2.1 a cycle.  What bounds it is that issue
+// rate with the chunk's chain of hand-overs: the S warps are busy 85 % of the time, the tensor pipe 38 %.
 // No single part carries it: left out one at a time, P and K' save 35 us each, the scores 29, the
 // products 27, S's terms 20, the outputs 15, the decay sums 9.
 #include <cuda.h>

@@ -31,7 +31,7 @@
 // K16, in this order: K' of the next chunk is made during (2) and (3), and the S warps have the
 // whole of (1) to turn dS of the chunk before into the operand of (2).
 //
-// Measured (B=4 H=32 T=8192 d=128, 128 CTAs): 291 us, 3.7 TB/s, 55 % of the measured copy rate; 2.2 us a
+// Measured (B=4 H=32 T=8192 d=128, 128 CTAs): 286 us, 3.8 TB/s, 56 % of the measured copy rate; 2.2 us a
 // chunk, in which an SM issues about 10,000 warp instructions at 2.1 a cycle.  What bounds it is that issue
 // rate with the chunk's chain of hand-overs: the S warps are busy 85 % of the time, the tensor pipe 38 %.
 // No single part carries it: left out one at a time, P and K' save 35 us each, the scores 29, the
@@ -247,8 +247,7 @@ __device__ __forceinline__ void scale_keys(uint8_t *sm, uint32_t st, uint32_t kp
 // x as a bf16 pair and the rest it leaves
 __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
     const uint32_t h = pack_bf16(x.x, x.y);
-    x.x -= __uint_as_float(h << 16);
-    x.y -= __uint_as_float(h & 0xffff0000u);
+    x = __ffma2_rn(make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)), make_float2(-1.f, -1.f), x);
     return h;
 }
 
@@ -626,8 +625,10 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
                     tmem_ld_16x256b_x4_pair(tl + TM_OI, tl + TM_OJ, v, w);
                     uint32_t x[8];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        x[c] = pack_bf16(fmaf(e2[c / 2].x, v[2 * c], w[2 * c]), fmaf(e2[c / 2].y, v[2 * c + 1], w[2 * c + 1]));
+                    for (int c = 0; c < 8; ++c) {
+                        const float2 y = __ffma2_rn(e2[c / 2], make_float2(v[2 * c], v[2 * c + 1]), make_float2(w[2 * c], w[2 * c + 1]));
+                        x[c] = pack_bf16(y.x, y.y);
+                    }
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         stsm_x4_t(sb + stg + o_st[L] + 1024 * e, x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);

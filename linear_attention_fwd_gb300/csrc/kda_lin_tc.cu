@@ -264,7 +264,13 @@ struct CutRule {
     int most, target;   // sequences of more than `most` chunks are cut, into parts of about `target`
     int slots;
     int whole, parts;   // dense: (sequence, head) units before `whole` are not cut, the others into `parts`
+    bool fold;          // no scan (see kFold)
 };
+
+__device__ __forceinline__ Piece load_piece(const Piece *from) {
+    const int4 x = __ldcg(reinterpret_cast<const int4 *>(from)), y = __ldcg(reinterpret_cast<const int4 *>(from) + 1);
+    return {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+}
 
 // Dense batches: the piece of CTA b by arithmetic.  kFullPass: over all parts, else over all but each
 // cut unit's last.
@@ -276,7 +282,7 @@ __device__ __forceinline__ Piece dense_piece(const LinArgs &a, int b, const CutR
 }
 
 // Packed sequences: one CTA makes the lists of pieces, `pre` of all parts but each sequence's last, `full`
-// of all, longest sequences first (the hardware dispatches low blocks first; more than kPlanThreads of them
+// of all, longest parts first (the hardware dispatches low blocks first; more than kPlanThreads of them
 // keep their order); what is left of the lists is P = 0.  A sequence that would need more slots than there
 // are is not cut (only offsets that are not as documented come to that).  The lists are made here and
 // not by each CTA for itself because that search, merely by being in the main kernel, cost its loops 40 %.
@@ -319,7 +325,8 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan_kernel(const LinArgs a,
         };
         int slot = used + scan(parts > 0 ? parts - 1 : 0, 0);
         if (parts > 1 && slot + parts - 1 > cut.slots) parts = 1;
-        s_len[t] = t < here ? len : -1;
+        const int key = parts > 0 ? (len + parts - 1) / parts : -1;   // a part's tokens
+        s_len[t] = key;
         s_parts[t] = parts;
         s_slot[t] = slot;
         __syncthreads();
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan_kernel(const LinArgs a,
         if (N <= kPlanThreads) {
             if (t < here)
                 for (int i = 0; i < here; ++i) {
-                    const bool ahead = s_len[i] > len || (s_len[i] == len && i < t);
+                    const bool ahead = s_len[i] > key || (s_len[i] == key && i < t);
                     first += ahead ? s_parts[i] : 0;
                     before += ahead ? s_parts[i] - 1 : 0;
                 }
@@ -374,8 +381,12 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan_kernel(const LinArgs a,
 // `locals`, and its total log2 decay; lin_scan_kernel then turns each slot into the true state behind
 // its part.  There warps 0-15 make K' together, a chunk ahead of the products, and warps 0-7 the state: 1.1 us
 // a chunk, its chain of hand-overs (8 warps and one K' at a time: 1.75 us).
+// kFold (full pass over several packed sequences, after a first pass): sequences that are not cut start beside
+// the first pass, and each part chains the states before it itself, so that there is no scan between the
+// passes (16384 + 8192 + 8192 + 4096 tokens of 32 heads: 378 us, with a scan 473).  The CTAs of a part wait for the
+// first pass at their start, all others at their end, so that the call's memory is not reused too early.
 // kDk: the key channels, 64 or 128 (value channels are always 128 lanes; those a head lacks read as zeros).
-template <bool kFullPass, int kDk>
+template <bool kFullPass, int kDk, bool kFold>
 __global__ void __launch_bounds__(NT, 1)
 kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv, const LinArgs a, const CutRule cut, const Piece *plan,
@@ -392,10 +403,13 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int H = a.heads;
     // (launched before the kernel ahead of it has ended, see launch_lin_chunk_tc)
+    auto wait_ahead = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
+    if (!kFold) wait_ahead();
+    // (behind the wait: what depends on this pass may read the lists, which an earlier kernel made)
     if (!kFullPass) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Piece piece = plan ? plan[blockIdx.x] : dense_piece<kFullPass>(a, blockIdx.x, cut);
+    const Piece piece = plan ? load_piece(plan + blockIdx.x) : dense_piece<kFullPass>(a, blockIdx.x, cut);
     const int n = piece.n, h = piece.h, p = piece.p, P = piece.P, slot = piece.slot;
+    if (kFold && P != 1) wait_ahead();
     if (P == 0) return;
     const int hk = h / (H / a.qk_heads);
     const int bos = piece.bos, eos = piece.eos;        // tokens are counted in 31 bits
@@ -404,7 +418,10 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
     const int chunks = c_hi - c_lo;
     const int first = bos + c_lo * C;                  // the part's first token
     const bool last_part = p == P - 1;
-    if (chunks == 0 && kFullPass && !(last_part && a.sT)) return;
+    if (chunks == 0 && kFullPass && !(last_part && a.sT)) {
+        if (kFold) wait_ahead();
+        return;
+    }
 
     auto bar = [&](int b) { return sb + OFF_BAR + 8 * b; };
     if (tid == 0) {
@@ -463,10 +480,17 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
 #pragma unroll
         for (int c = 0; c < KC; ++c) v[c] = 0.f;
         if (kFullPass && mine) {
-            const float *from = p > 0 ? locals + ((int64_t)(slot + p - 1) * H + h) * sstep : (a.s0 ? a.s0 + ((int64_t)n * H + h) * sstep : nullptr);
+            const float *from = p > 0 && !kFold ? locals + ((int64_t)(slot + p - 1) * H + h) * sstep : (a.s0 ? a.s0 + ((int64_t)n * H + h) * sstep : nullptr);
             if (from)
 #pragma unroll
                 for (int c = 0; c < KC; ++c) v[c] = __ldcg(from + at + (int64_t)c * a.dv);
+#pragma unroll 1
+            for (int e = 0; kFold && e < p; ++e) {   // the parts before this one
+                const int64_t of = (int64_t)(slot + e) * H + h;
+                const float f = exp2f((float)__ldcg(decays + of));
+#pragma unroll
+                for (int c = 0; c < KC; ++c) v[c] = fmaf(f, v[c], __ldcg(locals + of * sstep + at + (int64_t)c * a.dv));
+            }
         }
         auto take_ds = [&](int k, float f) {   // v <- f v + dS of chunk k
             tc_fence_after();
@@ -859,6 +883,7 @@ kda_lin_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_co
         tc_fence_after();
         tmem_dealloc(tmem, TM_COLS);
     }
+    if (kFold) wait_ahead();   // (what this call's kernels read must not be overwritten by the next call's before)
 }
 
 // For each sequence that is cut: the state behind part p is e^{its decay} times the one before it plus
@@ -868,7 +893,7 @@ constexpr int kScanThreads = 256;
 __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const LinArgs a, const CutRule cut, const Piece *plan, float *locals, const double *decays) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Piece piece = plan ? plan[blockIdx.x] : dense_piece<false>(a, blockIdx.x, cut);
+    const Piece piece = plan ? load_piece(plan + blockIdx.x) : dense_piece<false>(a, blockIdx.x, cut);
     if (piece.P == 0 || piece.p != 0) return;
     const int H = a.heads;
     const int64_t size = (int64_t)a.dk * a.dv, at = ((int64_t)blockIdx.y * kScanThreads + threadIdx.x) * 4;
@@ -938,9 +963,9 @@ cudaError_t take_lin_expiries(cudaStream_t st, unsigned int *count) {
 //    into as many parts as should end first (best_parts; T=8192: 160 units 336 us, whole 573; 70 units 229,
 //    in two parts 264; 56 units of 13805 tokens 316, in two parts 364; 8 units of 32767 114 in 19);
 //  - packed sequences, whose lengths only the device knows, run longest first, and those of more than
-//    1.5 times an SM's equal share of all chunks are cut into halves of that share (13 mixes of lengths:
-//    quarters take 2 to 25 % more time, whole shares between 21 % less and 22 % more; cutting from 1.1
-//    times the share on costs up to 46 %).  One sequence alone is cut as in a dense batch.
+//    1.2 times an SM's equal share of all chunks are cut into parts of two thirds of it (15 mixes of lengths:
+//    halves take between 9 % less and 14 % more time, thirds up to 29 % more; cutting from the whole share on
+//    up to 26 % more).  One sequence alone is cut as in a dense batch.
 struct Cut {
     CutRule rule;
     int64_t pre, full;
@@ -966,25 +991,25 @@ static int64_t best_parts(int64_t units, int64_t nc) {
 
 static Cut cut_of(int64_t tokens, int64_t num_seqs, int64_t heads, bool packed, bool whole) {
     const int64_t units = num_seqs * heads, chunks = ((packed ? tokens : tokens / num_seqs) + C - 1) / C;
-    Cut c{{0x7fffffff, 1, 0, (int)units, 1}, 0, units};
+    Cut c{{0x7fffffff, 1, 0, (int)units, 1, false}, 0, units};
     if (whole) return c;
     if (!packed) {
         const int64_t cuts = units % kSms, kept = units - cuts, parts = cuts ? best_parts(cuts, chunks) : 1;
         if (parts == 1) return c;
-        c.rule = {0, 1, (int)((num_seqs - kept / heads) * (parts - 1)), (int)kept, (int)parts};
+        c.rule = {0, 1, (int)((num_seqs - kept / heads) * (parts - 1)), (int)kept, (int)parts, false};
         c.pre = cuts * (parts - 1);
     } else if (num_seqs == 1) {
         const int64_t parts = best_parts(heads, chunks), target = (chunks + parts - 1) / parts;
-        c.rule = {(int)target, (int)target, (int)(parts - 1), 0, 1};
+        c.rule = {(int)target, (int)target, (int)(parts - 1), 0, 1, false};
         c.pre = heads * (parts - 1);
     } else {
         const int64_t all = chunks + num_seqs, share = (all * heads + kSms - 1) / kSms;   // (each sequence's last chunk may be short)
-        int64_t most = share + share / 2, target = share / 2;
+        int64_t most = share + share / 5, target = share * 2 / 3;
         if (target < kMinPart) target = kMinPart;
         if (most < 2 * kMinPart) most = 2 * kMinPart;
         // at most all / (most + 1) sequences are cut, into ceil(nc / target) parts
         const int64_t slots = all <= most ? 0 : all / target;
-        c.rule = {(int)most, (int)target, (int)slots, 0, 1};
+        c.rule = {(int)most, (int)target, (int)slots, 0, 1, slots > 0};
         c.pre = slots * heads;
     }
     c.full = units + c.pre;
@@ -1007,7 +1032,7 @@ cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, bool whole, c
         return cudaErrorInvalidValue;
     float *locals = static_cast<float *>(workspace);
     double *decays = reinterpret_cast<double *>(locals + (int64_t)c.rule.slots * a.heads * a.dk * a.dv);
-    // Up to four kernels, each needing all of the one before: every one but the first may be launched before
+    // Up to four kernels, each needing all of the one before (but see kFold): every one but the first may be launched before
     // that has ended and waits for it at its start, so that the launches overlap.
     bool first = true;
     auto launch = [&](auto kernel, dim3 grid, int threads, size_t smem, auto... args) {
@@ -1037,15 +1062,16 @@ cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, bool whole, c
     const Piece *cpre = pre, *cfull = full;
     const double *cdecays = decays;
     if (e == cudaSuccess && c.pre > 0) {
-        e = launch(wide ? kda_lin_chunk_tc_kernel<false, 128> : kda_lin_chunk_tc_kernel<false, 64>, dim3((unsigned)c.pre), NT, SMEM_BYTES,
+        e = launch(wide ? kda_lin_chunk_tc_kernel<false, 128, false> : kda_lin_chunk_tc_kernel<false, 64, false>, dim3((unsigned)c.pre), NT, SMEM_BYTES,
                    mq, mk, mv, a, c.rule, cpre, locals, decays);
-        if (e == cudaSuccess)
+        if (e == cudaSuccess && !c.rule.fold)
             e = launch(lin_scan_kernel, dim3((unsigned)c.pre, (unsigned)(a.dk * a.dv / (4 * kScanThreads))), kScanThreads, 0,
                        a, c.rule, cpre, locals, cdecays);
     }
     if (e != cudaSuccess) return e;
-    return launch(wide ? kda_lin_chunk_tc_kernel<true, 128> : kda_lin_chunk_tc_kernel<true, 64>, dim3((unsigned)c.full), NT, SMEM_BYTES,
-                  mq, mk, mv, a, c.rule, cfull, locals, decays);
+    const auto whole_pass = c.rule.fold ? (wide ? kda_lin_chunk_tc_kernel<true, 128, true> : kda_lin_chunk_tc_kernel<true, 64, true>)
+                                        : (wide ? kda_lin_chunk_tc_kernel<true, 128, false> : kda_lin_chunk_tc_kernel<true, 64, false>);
+    return launch(whole_pass, dim3((unsigned)c.full), NT, SMEM_BYTES, mq, mk, mv, a, c.rule, cfull, locals, decays);
 }
 
 }  // namespace kda

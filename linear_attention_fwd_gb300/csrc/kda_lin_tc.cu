@@ -265,6 +265,7 @@ struct CutRule {
     int slots;
     int whole, parts;   // dense: (sequence, head) units before `whole` are not cut, the others into `parts`
     bool fold;          // no scan (see kFold)
+    int alone;          // packed: the target where one sequence has four fifths of all chunks (0: none)
 };
 
 __device__ __forceinline__ Piece load_piece(const Piece *from) {
@@ -298,9 +299,23 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan_kernel(const LinArgs a,
         int64_t b = 0, e = 0;
         if (t < here) lin_range(a, base + t, b, e);
         const int len = (int)(e - b), nc = (len + C - 1) / C;
-        int parts = t < here ? 1 : 0;
+        int parts = t < here ? 1 : 0, target = cut.target;
+        if (cut.alone > 0 && N <= kPlanThreads) {
+            const int most = __reduce_max_sync(0xffffffffu, nc), sum = __reduce_add_sync(0xffffffffu, nc);
+            if (lane == 0) {
+                s_sum[0][warp] = most;
+                s_sum[1][warp] = sum;
+            }
+            __syncthreads();
+            int x = 0, y = 0;
+            for (int i = 0; i < kPlanThreads / 32; ++i) {
+                x = s_sum[0][i] > x ? s_sum[0][i] : x;
+                y += s_sum[1][i];
+            }
+            if ((int64_t)x * 5 > (int64_t)y * 4) target = cut.alone;
+        }
         if (t < here && nc > cut.most) {
-            parts = (nc + cut.target - 1) / cut.target;
+            parts = (nc + target - 1) / target;
             if (parts > kMaxParts) parts = kMaxParts;
         }
         __syncthreads();
@@ -965,7 +980,9 @@ cudaError_t take_lin_expiries(cudaStream_t st, unsigned int *count) {
 //  - packed sequences, whose lengths only the device knows, run longest first, and those of more than
 //    1.2 times an SM's equal share of all chunks are cut into parts of two thirds of it (15 mixes of lengths:
 //    halves take between 9 % less and 14 % more time, thirds up to 29 % more; cutting from the whole share on
-//    up to 26 % more).  One sequence alone is cut as in a dense batch.
+//    up to 26 % more).  Where one has four fifths of all chunks, that would make part of a second round: it is cut into
+//    as many as one round holds (20000 of 21200 tokens, 16 heads: 148 us, 203 by two thirds).  One sequence
+//    alone is cut as in a dense batch.
 struct Cut {
     CutRule rule;
     int64_t pre, full;
@@ -991,16 +1008,16 @@ static int64_t best_parts(int64_t units, int64_t nc) {
 
 static Cut cut_of(int64_t tokens, int64_t num_seqs, int64_t heads, bool packed, bool whole) {
     const int64_t units = num_seqs * heads, chunks = ((packed ? tokens : tokens / num_seqs) + C - 1) / C;
-    Cut c{{0x7fffffff, 1, 0, (int)units, 1, false}, 0, units};
+    Cut c{{0x7fffffff, 1, 0, (int)units, 1, false, 0}, 0, units};
     if (whole) return c;
     if (!packed) {
         const int64_t cuts = units % kSms, kept = units - cuts, parts = cuts ? best_parts(cuts, chunks) : 1;
         if (parts == 1) return c;
-        c.rule = {0, 1, (int)((num_seqs - kept / heads) * (parts - 1)), (int)kept, (int)parts, false};
+        c.rule = {0, 1, (int)((num_seqs - kept / heads) * (parts - 1)), (int)kept, (int)parts, false, 0};
         c.pre = cuts * (parts - 1);
     } else if (num_seqs == 1) {
         const int64_t parts = best_parts(heads, chunks), target = (chunks + parts - 1) / parts;
-        c.rule = {(int)target, (int)target, (int)(parts - 1), 0, 1, false};
+        c.rule = {(int)target, (int)target, (int)(parts - 1), 0, 1, false, 0};
         c.pre = heads * (parts - 1);
     } else {
         const int64_t all = chunks + num_seqs, share = (all * heads + kSms - 1) / kSms;   // (each sequence's last chunk may be short)
@@ -1009,7 +1026,9 @@ static Cut cut_of(int64_t tokens, int64_t num_seqs, int64_t heads, bool packed, 
         if (most < 2 * kMinPart) most = 2 * kMinPart;
         // at most all / (most + 1) sequences are cut, into ceil(nc / target) parts
         const int64_t slots = all <= most ? 0 : all / target;
-        c.rule = {(int)most, (int)target, (int)slots, 0, 1, slots > 0};
+        // one sequence with nearly all chunks: as many parts as one round of SMs holds
+        const int64_t round = kSms / heads, alone = round >= 2 && (all + round - 1) / round >= target ? (all + round - 1) / round : 0;
+        c.rule = {(int)most, (int)target, (int)slots, 0, 1, slots > 0, (int)alone};
         c.pre = slots * heads;
     }
     c.full = units + c.pre;

@@ -299,7 +299,7 @@ def test_more_heads_than_one_round(K, B, H, T):
     R.check_lin(out, fin, reference(d))
 
 
-@pytest.mark.parametrize("lens,H", [([2500], 8), ([1000], 3), ([64], 160), ([2200, 1], 8), ([513, 0, 1900], 12), ([30000], 1)])
+@pytest.mark.parametrize("lens,H", [([2500], 8), ([1000], 3), ([64], 160), ([2200, 1], 8), ([513, 0, 1900], 12), ([30000], 1), ([100, 5000, 7, 90], 5), ([3000, 64], 40), ([40, 9000], 1)])
 def test_few_packed_sequences(K, lens, H):
     """One packed sequence is cut like a dense batch's, few by their share."""
     d = make(33, 1, sum(lens), H, H, 128, 64, BF16, decay="head", init=len(lens))

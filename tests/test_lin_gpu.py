@@ -306,3 +306,36 @@ def test_few_packed_sequences(K, lens, H):
     d["cu_seqlens"] = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
     out, fin = K.kda_lin_chunk_fwd(**d)
     R.check_lin(out, fin, reference({k: x for k, x in d.items() if k != "cu_seqlens"}, d["cu_seqlens"]))
+
+
+def test_overlapping_launches_share_a_workspace(K):
+    """Calls back to back on one stream with one workspace, whose cut and uncut sequences start at different times,
+    and the same in a replayed graph: bit for bit what each gives alone."""
+    H, mixes = 12, [[4000, 900, 100, 0], [300, 2500, 1200, 1000], [5000, 0, 0, 0]]
+    cases = []
+    for i, lens in enumerate(mixes):
+        d = make(40 + i, 1, 5000, H, H, 128, 128, BF16, decay="head", init=4)
+        d["cu_seqlens"] = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
+        cases.append((d, *K.kda_lin_chunk_fwd(**d)))
+    torch.cuda.synchronize()
+    ws = torch.empty(K.kda_lin_chunk_fwd_workspace_bytes(d["q"], d["v"], d["cu_seqlens"]), dtype=torch.uint8, device="cuda")
+    got = [K.kda_lin_chunk_fwd(**cases[i % 3][0], workspace=ws) for i in range(24)]
+    torch.cuda.synchronize()
+    for i, (out, fin) in enumerate(got):
+        assert torch.equal(out, cases[i % 3][1]) and torch.equal(fin, cases[i % 3][2])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got = [K.kda_lin_chunk_fwd(**cases[i][0], workspace=ws) for i in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for out, fin in got:
+            out.zero_()
+            fin.zero_()
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (out, fin) in enumerate(got):
+            assert torch.equal(out, cases[i][1]) and torch.equal(fin, cases[i][2])

@@ -1051,8 +1051,8 @@ cudaError_t launch_lin_chunk_tc(const LinArgs &a, void *workspace, bool whole, c
         return cudaErrorInvalidValue;
     float *locals = static_cast<float *>(workspace);
     double *decays = reinterpret_cast<double *>(locals + (int64_t)c.rule.slots * a.heads * a.dk * a.dv);
-    // Up to four kernels, each needing all of the one before (but see kFold): every one but the first may be launched before
-    // that has ended and waits for it at its start, so that the launches overlap.
+    // Up to four kernels, each needing all of the one before (but see kFold): every one but the first may be
+    // launched before that has ended and waits for it at its start, so that the launches overlap.
     bool first = true;
     auto launch = [&](auto kernel, dim3 grid, int threads, size_t smem, auto... args) {
         cudaError_t e = smem ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;

@@ -451,10 +451,13 @@ typedef struct {
  *              aligned (NULL when that is 0).  Its contents on entry do not matter; calls that
  *              overlap in time need workspaces of their own.  It holds the states of the parts that
  *              long sequences are cut into to fill the SMs.
- * v and the states may take any magnitude their formats hold.  Tokens of other sequences (and
- * what lies behind the last) never reach a sequence's results, NaN and infinities included; a
- * NaN or infinity of a sequence's own token may reach its outputs from the start of that token's
- * chunk (at most 64 tokens, counted from the sequence's start) on, and its state.
+ * v and the states may take any magnitude their formats hold, the largest floats included, as long
+ * as the sums stay finite in fp32: S^T q of the state before a chunk (formed before that chunk's decay
+ * is applied) and the chunk's sum of k v^T.  (bf16: the state enters S^T q as two bf16 terms, the
+ * smallest of them 2^-133, so outputs of states below about 2^-117 are less accurate than 2^-16.)
+ * Tokens of other sequences (and what lies behind the last) never reach a sequence's results, NaN
+ * and infinities included; a NaN or infinity of a sequence's own token may reach its outputs from the
+ * start of that token's chunk (at most 64 tokens, counted from the sequence's start) on, and its state.
  * Returns KDA_OK or an error found on the host before any launch: KDA_ERR_NULL, KDA_ERR_SHAPE,
  * KDA_ERR_UNSUPPORTED, KDA_ERR_ALIGN, KDA_ERR_WORKSPACE; KDA_ERR_CUDA when a launch fails.
  * seqlen = 0 is valid (final_state becomes a copy of the initial state, or zeros). */

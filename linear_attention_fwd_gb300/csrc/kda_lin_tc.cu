@@ -244,9 +244,12 @@ __device__ __forceinline__ void scale_keys(uint8_t *sm, uint32_t st, uint32_t kp
     }
 }
 
-// x as a bf16 pair and the rest it leaves
+// x as a bf16 pair and the rest it leaves.  Values past the largest bf16 take that one (rounded they would be
+// infinite, their rest minus infinity and the two terms' products NaN); the rest of a finite x is then at most
+// 2^-8 of it and exact, as for any other x.
 __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
-    const uint32_t h = pack_bf16(x.x, x.y);
+    uint32_t h;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x.y), "f"(x.x));
     x = __ffma2_rn(make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)), make_float2(-1.f, -1.f), x);
     return h;
 }

@@ -339,3 +339,18 @@ def test_overlapping_launches_share_a_workspace(K):
         torch.cuda.synchronize()
         for i, (out, fin) in enumerate(got):
             assert torch.equal(out, cases[i][1]) and torch.equal(fin, cases[i][2])
+
+
+@pytest.mark.parametrize("dt,dk,dv", [(F32, 128, 128), (BF16, 128, 128), (BF16, 64, 128), (BF16, 128, 64)])
+@pytest.mark.parametrize("T", [1, 150, 2500])
+def test_states_up_to_the_largest_float(K, dt, dk, dv, T):
+    """States within 2^-6 of the largest finite value, most of them past what rounds to a finite bf16; q small enough
+    that every sum stays finite (sum |q_i| <= sqrt(dk) / 16)."""
+    d = make(51, 1, T, 2, 2, dk, dv, dt, decay="none", init=1)
+    gen = torch.Generator(device="cuda").manual_seed(52)
+    rnd = lambda: torch.rand(d["initial_state"].shape, generator=gen, device="cuda")  # noqa: E731
+    d["initial_state"] = torch.finfo(F32).max * (1 - 2.0 ** -6 * rnd()) * torch.where(rnd() < 0.5, -1.0, 1.0)
+    d["initial_state"][0, :, 0, :] = torch.finfo(F32).max
+    d["q"] = d["q"] / 16
+    out, fin = K.kda_lin_chunk_fwd(**d)
+    R.check_lin(out, fin, reference(d))

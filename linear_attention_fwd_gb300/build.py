@@ -1,5 +1,6 @@
 """Build libkda.so in-tree for sm_103a (nvcc, no cmake), and _binding.so, the C++ side of the Python
-binding, with the host compiler.
+binding, with the host compiler.  The library needs neither Python's headers nor PyTorch: where the binding
+cannot be built, build() warns and returns the library all the same (build_binding() raises).
 
 Each .cu under csrc/ compiles to its own object in parallel; the objects link
 into ``libkda.so`` beside this file.  The CUDA runtime is linked statically and
@@ -14,6 +15,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +25,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkda.so")
 LIB_DEBUG = os.path.join(HERE, "libkda_debug.so")
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_STAMP = os.path.join(BUILD, "stamp_binding")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-v"]
@@ -55,7 +58,8 @@ def _digest(paths, extra=""):
 
 
 def build_binding(force: bool = False) -> str:
-    """Compile csrc/binding.cpp against the installed PyTorch into _binding.so; returns its path."""
+    """Compile csrc/binding.cpp against the installed PyTorch into _binding.so; returns its path.  Raises
+    where that fails; a _binding.so of other sources is then removed (it may not fit the library)."""
     import torch
     src = os.path.join(CSRC, "binding.cpp")
     root = os.path.dirname(torch.__file__)
@@ -66,27 +70,32 @@ def build_binding(force: bool = False) -> str:
            os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda]
     libs = ["torch_python", "torch_cuda", "torch_cpu", "c10_cuda", "c10"]
     want = _digest([src, os.path.join(INCLUDE, "kda.h")], " ".join(flags + inc + [torch.__version__, sys.version]))
-    stamp = os.path.join(BUILD, "stamp_binding")
-    os.makedirs(BUILD, exist_ok=True)
-    if not force and os.path.exists(BINDING) and os.path.exists(stamp):
-        with open(stamp) as f:
+    os.makedirs(os.path.dirname(BINDING_STAMP), exist_ok=True)
+    if not force and os.path.exists(BINDING) and os.path.exists(BINDING_STAMP):
+        with open(BINDING_STAMP) as f:
             if f.read() == want:
                 return BINDING
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), *flags, *(f"-I{i}" for i in inc), src, "-o", tmp,
            f"-L{os.path.join(root, 'lib')}", *(f"-l{x}" for x in libs)]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    except (OSError, RuntimeError):
+        for old in (BINDING_STAMP, BINDING):
+            if os.path.exists(old):
+                os.remove(old)
+        raise
     os.replace(tmp, BINDING)
-    with open(stamp, "w") as f:
+    with open(BINDING_STAMP, "w") as f:
         f.write(want)
     return BINDING
 
 
 def build(verbose: bool = False, force: bool = False, debug: bool = False) -> str:
-    """Compile csrc/*.cu for sm_103a and link libkda.so (and build _binding.so beside it); returns the
-    library's path.
+    """Compile csrc/*.cu for sm_103a and link libkda.so (and build _binding.so beside it, warning where
+    that cannot be done); returns the library's path.
 
     debug=True builds libkda_debug.so instead (objects in _build_debug/): the same kernels with
     KDA_DEBUG_CHECKS defined, so that every chunk forward and decode call first checks g and the
@@ -100,10 +109,13 @@ def build(verbose: bool = False, force: bool = False, debug: bool = False) -> st
     hdr_digest = _digest(_headers(), " ".join(ARCH + flags))
     stamp = os.path.join(build_dir, "stamp")
     want = _digest(srcs, hdr_digest)
-    with ThreadPoolExecutor(max_workers=1) as side:   # beside the kernels; its errors are raised below
+    with ThreadPoolExecutor(max_workers=1) as side:   # beside the kernels
         binding = side.submit(build_binding, force)
         path = _build_library(verbose, force, build_dir, lib_path, flags, nvcc, srcs, stamp, want)
-        binding.result()
+        failed = binding.exception()
+    if failed is not None:
+        warnings.warn(f"{os.path.basename(path)} is built, {os.path.basename(BINDING)} is not; the calls bound through it "
+                      f"(linear attention, paged cache) raise from Python: {failed}", RuntimeWarning, stacklevel=2)
     return path
 
 

@@ -389,18 +389,18 @@ kda_status_t kda_recurrent_steps_qknorm(const void *q, const void *k, const void
 /* kda_device_status -- waits for the work queued on `stream` to finish, then reads and
  * clears the current device's count of device-side waits of the tensor-core chunk kernels
  * that gave up (see kda_chunk_fwd_bounded and kda_lin_chunk_fwd_bounded; the two passes of
- * kda_chunk_fwd_ws count theirs too) and its word of failed debug-build input checks.  Returns KDA_ERR_INPUT when a check
- * failed since the previous call on this device (only a library built with debug checks
- * makes any), else KDA_ERR_TIMEOUT when at least one wait gave up, KDA_OK when neither
- * happened, and KDA_ERR_CUDA when the stream or the copies fail.  Both are device-global:
+ * kda_chunk_fwd_ws count theirs too) and its word of failed debug-build input checks.  Returns
+ * KDA_ERR_INPUT when a check failed since the previous call on this device (only a library
+ * built with debug checks makes any), else KDA_ERR_TIMEOUT when at least one wait gave up,
+ * KDA_OK when neither happened, and KDA_ERR_CUDA when the stream or the copies fail.  Both are device-global:
  * calls that run concurrently on other streams of the device report into the same word and
  * count.  This is the only call of the library that synchronises the host; it does not
  * depend on final_state being requested. */
 kda_status_t kda_device_status(cudaStream_t stream);
 
 /* kda_debug_checks -- which device-side input checks this build of the library runs before
- * each chunk forward and decode call: a bit mask, 1 = g in [-5, 0] (NaN fails), 2 = packed
- * offsets 0 = cu[0] <= ... <= cu[N] = seqlen; 0 for the release build, which runs none (the
+ * each chunk forward and decode call: a bit mask, 1 = g in [-5, 0], for linear attention
+ * g + head_g <= 0 (NaN fails), 2 = packed offsets 0 = cu[0] <= ... <= cu[N] = seqlen; 0 for the release build, which runs none (the
  * precondition is "はじめての自然言語処理 -- Kimi K3", section 3.1: g = -5 sigmoid(x)).  A failed
  * check launches nothing extra and traps nothing: the call still runs, its results are
  * unspecified, and kda_device_status returns KDA_ERR_INPUT.  A host query. */
@@ -443,7 +443,8 @@ typedef struct {
  *   g        : fp32 [batch, seqlen, heads] log decay of each token, or NULL (zeros)
  *   head_g   : fp32 [heads] log decay of each head, or NULL (zeros); both may be given
  *              The log decays are <= 0, of any magnitude; -infinity forgets everything before
- *              the token.  (A positive sum g + head_g is outside the precondition.)
+ *              the token.  (A positive sum g + head_g is outside the precondition;
+ *              a library built with debug checks reports it.)
  *   initial_state, final_state : fp32 [num_seqs, heads, dk, dv]; the same pointer is allowed,
  *              partial overlap is not.
  *   cu_seqlens : as in kda_chunk_fwd (NULL for dense batches; clamped on the device).

@@ -98,8 +98,8 @@ def build(verbose: bool = False, force: bool = False, debug: bool = False) -> st
     that cannot be done); returns the library's path.
 
     debug=True builds libkda_debug.so instead (objects in _build_debug/): the same kernels with
-    KDA_DEBUG_CHECKS defined, so that every chunk forward and decode call first checks g and the
-    packed offsets on the device (kda_debug_checks, kda_device_status)."""
+    KDA_DEBUG_CHECKS defined, so that every chunk forward and decode call first checks the log decays
+    and the packed offsets on the device (kda_debug_checks, kda_device_status)."""
     build_dir = BUILD + "_debug" if debug else BUILD
     lib_path = LIB_DEBUG if debug else LIB
     flags = NVCC_FLAGS + (["-DKDA_DEBUG_CHECKS=1"] if debug else [])

@@ -5,6 +5,8 @@
 //   - the log decay is bounded, g in [-5, 0] ("はじめての自然言語処理 -- Kimi K3", section 3.1:
 //     g = -5 sigmoid(x); the tensor-core kernels keep a 16-token cumulative decay within e^-80
 //     on the strength of it);
+//     For the linear-attention calls: the sum of a token's and its head's log decay is at most 0, of any
+//     magnitude (-infinity included);
 //   - packed offsets satisfy 0 = cu[0] <= cu[1] <= ... <= cu[N] = seqlen.
 // A library built with KDA_DEBUG_CHECKS (build.build(debug=True) -> libkda_debug.so) checks both
 // on the device before a call's kernels run and records a failure as a bit in a device-wide
@@ -13,7 +15,7 @@
 // release library compiles the error word and its reader but launches no check.
 #include <cuda_bf16.h>
 
-#include "kda_internal.h"
+#include "kda_lin.h"
 
 __device__ unsigned int g_kda_input_errors = 0;
 
@@ -32,6 +34,18 @@ __global__ void __launch_bounds__(kCheckThreads) check_decay_kernel(const void *
         const float x = is_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(g)[i])
                                 : static_cast<const float *>(g)[i];
         bad |= !(x >= -5.f && x <= 0.f);
+    }
+    if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(&g_kda_input_errors, kErrDecay);
+}
+
+// Linear attention: flags any g + head_g above 0 (NaN included) among n sums, those of token i / heads and head
+// i % heads; either may be missing (n = heads without g).
+__global__ void __launch_bounds__(kCheckThreads) check_lin_decay_kernel(const float *g, const float *head_g, int64_t n, int heads) {
+    bool bad = false;
+    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
+        const float x = (g ? g[i] : 0.f) + (head_g ? head_g[i % heads] : 0.f);
+        bad |= !(x <= 0.f);
     }
     if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(&g_kda_input_errors, kErrDecay);
 }
@@ -62,6 +76,22 @@ cudaError_t debug_check_inputs(const void *g, int64_t g_elems, kda_dtype_t dt, c
     return cudaGetLastError();
 #else
     (void)g, (void)g_elems, (void)dt, (void)cu, (void)num_seqs, (void)seqlen, (void)st;
+    return cudaSuccess;
+#endif
+}
+
+cudaError_t debug_check_lin_inputs(const float *g, const float *head_g, int64_t tokens, int heads, const int32_t *cu,
+                                   int num_seqs, int64_t seqlen, cudaStream_t st) {
+#ifdef KDA_DEBUG_CHECKS
+    const int64_t n = g ? tokens * heads : (head_g ? heads : 0);
+    if (tokens > 0 && n > 0) {
+        const int64_t blocks = (n + 4 * kCheckThreads - 1) / (4 * kCheckThreads);
+        check_lin_decay_kernel<<<(unsigned)(blocks < 1024 ? blocks : 1024), kCheckThreads, 0, st>>>(g, head_g, n, heads);
+    }
+    if (cu != nullptr) check_offsets_kernel<<<1, kCheckThreads, 0, st>>>(cu, num_seqs, seqlen);
+    return cudaGetLastError();
+#else
+    (void)g, (void)head_g, (void)tokens, (void)heads, (void)cu, (void)num_seqs, (void)seqlen, (void)st;
     return cudaSuccess;
 #endif
 }

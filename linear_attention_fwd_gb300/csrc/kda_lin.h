@@ -85,6 +85,10 @@ struct AppendArgs {
     int32_t row_vecs;         // 16-byte vectors of one token's keys (kv_heads * head_dim * size / 16)
 };
 
+// As debug_check_inputs, for linear attention: g [tokens, heads] + head_g [heads] at most 0 (either may be
+// nullptr), packed offsets.
+cudaError_t debug_check_lin_inputs(const float *g, const float *head_g, int64_t tokens, int heads, const int32_t *cu,
+                                   int num_seqs, int64_t seqlen, cudaStream_t st);
 cudaError_t launch_lin_chunk_simt(const LinArgs &a, cudaStream_t st);   // fp32
 // bf16.  Sequences may be cut into parts that run side by side, which takes a workspace; `whole`: they
 // are not.

@@ -60,6 +60,7 @@ extern "C" kda_status_t kda_lin_chunk_fwd_bounded(const void *q, const void *k, 
         if (workspace_bytes < need) return KDA_ERR_WORKSPACE;
         if (!aligned(workspace, 16)) return KDA_ERR_ALIGN;
     }
+    if (kda::debug_check_lin_inputs(g, head_g, tokens, d->heads, cu_seqlens, d->num_seqs, d->seqlen, stream) != cudaSuccess) return KDA_ERR_CUDA;
     if (tokens == 0) {
         if (final_state == nullptr || final_state == initial_state) return KDA_OK;
         const size_t bytes = (size_t)d->num_seqs * d->heads * d->dk * d->dv * 4;
@@ -101,7 +102,9 @@ extern "C" kda_status_t kda_lin_recurrent_step(const void *q, const void *k, con
         if (!aligned(p, 16)) return KDA_ERR_ALIGN;
     if (!aligned(g, 4) || !aligned(head_g, 4) || !aligned(state_indices, 4)) return KDA_ERR_ALIGN;
     const kda::LinStepArgs a{q, k, v, g, head_g, state, state_indices, out, d->batch, d->num_seqs, d->heads, d->qk_heads};
-    return kda::launch_lin_step(a, d->dk, d->dv, d->dtype, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    cudaError_t e = kda::debug_check_lin_inputs(g, head_g, d->batch, d->heads, nullptr, 0, 0, stream);
+    if (e == cudaSuccess) e = kda::launch_lin_step(a, d->dk, d->dv, d->dtype, stream);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 extern "C" kda_status_t kda_paged_append(const void *k, const void *v, void *k_cache, void *v_cache,

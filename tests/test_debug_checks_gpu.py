@@ -84,3 +84,57 @@ def test_packed_offsets(K, offsets, ok):
     cu = torch.tensor(offsets, dtype=torch.int32, device="cuda")
     fwd(K, inp, cu=cu)
     assert K.kda_device_status() == (K.KDA_OK if ok else K.KDA_ERR_INPUT)
+
+
+# Linear attention: the sum of a token's and its head's log decay is at most 0 (-infinity included), of any magnitude.
+def lin_inputs(dt=BF, T=150, H=3):
+    gen = torch.Generator(device="cuda").manual_seed(505)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    return dict(q=rnd(1, T, H, 64).to(dt), k=rnd(1, T, H, 64).to(dt), v=rnd(1, T, H, 64).to(dt), g=-rnd(1, T, H).abs(),
+                head_g=-torch.arange(1.0, H + 1, device="cuda"))
+
+
+@pytest.mark.parametrize("dt", [BF, torch.float32])
+@pytest.mark.parametrize("name,at,bad", [("g", (0, 77, 2), 3.5), ("g", (0, 149, 0), float("nan")), ("head_g", (1,), 20.0),
+                                         ("head_g", (2,), float("nan"))])
+def test_linear_attention_decay_is_reported(K, dt, name, at, bad):
+    d = lin_inputs(dt)
+    d["g"][0, 5, 1] = -float("inf")
+    d["g"][0, 6, 0] = 0.5          # with head_g = -1 below 0
+    d["g"][0, 7, 0] = -1e30
+    K.kda_lin_chunk_fwd(**d)
+    assert K.kda_device_status() == K.KDA_OK
+    d[name][at] = bad
+    K.kda_lin_chunk_fwd(**d)
+    assert K.kda_device_status() == K.KDA_ERR_INPUT
+    assert K.kda_device_status() == K.KDA_OK
+
+
+@pytest.mark.parametrize("only", ["g", "head_g"])
+def test_linear_attention_one_kind_of_decay(K, only):
+    d = lin_inputs()
+    d["head_g" if only == "g" else "g"] = None
+    K.kda_lin_chunk_fwd(**d)
+    assert K.kda_device_status() == K.KDA_OK
+    d[only].view(-1)[1] = 0.25
+    K.kda_lin_chunk_fwd(**d)
+    assert K.kda_device_status() == K.KDA_ERR_INPUT
+
+
+@pytest.mark.parametrize("offsets,ok", [([0, 40, 40, 150], True), ([0, 100, 60, 150], False), ([1, 40, 60, 150], False),
+                                        ([0, 40, 60, 149], False), ([0, 40, 60, 151], False)])
+def test_linear_attention_offsets(K, offsets, ok):
+    d = lin_inputs()
+    K.kda_lin_chunk_fwd(**d, cu_seqlens=torch.tensor(offsets, dtype=torch.int32, device="cuda"))
+    assert K.kda_device_status() == (K.KDA_OK if ok else K.KDA_ERR_INPUT)
+
+
+def test_linear_attention_step_decay_is_reported(K):
+    d = lin_inputs(T=6)
+    args = [d[n][0] for n in ("q", "k", "v", "g")] + [d["head_g"]]
+    state = torch.zeros(6, 3, 64, 64, device="cuda")
+    K.kda_lin_recurrent_step(*args, state)
+    assert K.kda_device_status() == K.KDA_OK
+    args[3][5, 2] = 3.25
+    K.kda_lin_recurrent_step(*args, state)
+    assert K.kda_device_status() == K.KDA_ERR_INPUT

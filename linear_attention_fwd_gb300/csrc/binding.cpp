@@ -110,6 +110,12 @@ int32_t narrow(int64_t x, const char *what) {
     return (int32_t)x;
 }
 
+bool truth(PyObject *o) {
+    const int r = PyObject_IsTrue(o);
+    if (r < 0) throw Refused{};   // (asking raised)
+    return r != 0;
+}
+
 void finish(kda_status_t st, const char *name) {
     if (st == KDA_OK) return;
     PyObject *r = PyObject_CallFunction(raise_status, "is", (int)st, name);
@@ -181,7 +187,7 @@ PyObject *lin_chunk(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Stream s(a[11], dev);
         at::Tensor o, f, w;
         const at::Tensor *op = or_made(out, o, s, {B, T, H, dv}, dt), *fp = nullptr;
-        if (fin || PyObject_IsTrue(a[9])) fp = or_made(fin, f, s, {N, H, dk, dv}, at::kFloat);
+        if (fin || truth(a[9])) fp = or_made(fin, f, s, {N, H, dk, dv}, at::kFloat);
         const at::Tensor *wp = ws.t;
         if (!wp)
             if (const size_t bytes = f_chunk_bytes(&d, cu ? 1 : 0)) wp = or_made(ws, w, s, {(int64_t)bytes}, at::kByte);
@@ -276,7 +282,7 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Stream s(a[10], dev);
         at::Tensor o, l, w;
         const at::Tensor *op = or_made(out, o, s, {N, Hq, d.head_dim}, dt), *lp = nullptr;
-        if (lse || PyObject_IsTrue(a[8])) lp = or_made(lse, l, s, {N, Hq}, at::kFloat);
+        if (lse || truth(a[8])) lp = or_made(lse, l, s, {N, Hq}, at::kFloat);
         const at::Tensor *wp = ws.t;
         if (!wp)
             if (const size_t bytes = f_attend_bytes(&d)) wp = or_made(ws, w, s, {(int64_t)bytes}, at::kByte);

@@ -118,3 +118,19 @@ def test_the_library_can_be_switched(K):
     finally:
         K.use_library(path)
     assert torch.equal(got, want) and K.kda_debug_checks() == 0
+
+
+def test_flags_without_a_truth_value_are_refused(K):
+    """A flag whose truth cannot be asked raises what asking raises, and nothing is written."""
+    both = torch.ones(2)
+    a = chunk_args()
+    a["out"] += 5
+    a["final_state"] = None
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        K.kda_lin_chunk_fwd(**a, output_final_state=both)
+    kc, table, lens = z(4, 16, 2, 64), z(2, 3, dt=torch.int32), z(2, dt=torch.int32)
+    out = z(2, 4, 64) + 5
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        K.kda_paged_attention(z(2, 4, 64), kc, kc, table, lens, 1.0, out=out, output_lse=both)
+    torch.cuda.synchronize()
+    assert bool((a["out"] == 5).all()) and bool((out == 5).all())

@@ -237,3 +237,139 @@ def test_shares_of_all_kinds(K, dt, d, lens, Hq, Hkv):
     wide[:, : c["block_table"].shape[1]] = c["block_table"]
     c["block_table"] = wide
     R.check_paged(*K.kda_paged_attention(**c), reference(c))
+
+
+# The shared-out form of attention (tables wider than a cluster's 8 x 1024 tokens) on everything that the one-launch
+# form is tested on above.  What the table holds past a row's pages is never looked up.
+def widen(K, c):
+    ps = c["k_cache"].shape[1]
+    rows, width = c["block_table"].shape
+    wide = torch.full((rows, max(width, -(-8200 // ps))), 1 << 30, dtype=torch.int32, device="cuda")
+    wide[:, :width] = c["block_table"]
+    c["block_table"] = wide
+    assert K.kda_paged_attention_workspace_bytes(c["q"], c["k_cache"], wide) > 0
+    return c
+
+
+def test_narrow_tables_take_one_launch(K):
+    for c in (cache(40, [64] * 3, 8, 2, 128, 16, BF16), cache(40, [8192], 8, 2, 64, 64, F32)):
+        assert K.kda_paged_attention_workspace_bytes(c["q"], c["k_cache"], c["block_table"]) == 0
+
+
+@pytest.mark.parametrize("length", [1, 2, 15, 16, 17, 31, 63, 64, 65, 100, 257, 1000])
+@pytest.mark.parametrize("dt,d", [(F32, 64), (F32, 128), (BF16, 64), (BF16, 128)])
+def test_lengths_shared_out(K, length, dt, d):
+    c = widen(K, cache(length, [length, max(1, length // 3)], 8, 2, d, 16, dt))
+    R.check_paged(*K.kda_paged_attention(**c), reference(c))
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 1), (5, 1), (7, 7), (12, 4), (16, 1), (24, 2), (17, 1), (40, 1), (64, 1), (66, 2)])
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("lens", [[150, 33, 1], [2000], [300] * 60])
+def test_head_layouts_shared_out(K, Hq, Hkv, dt, lens):
+    """Few rows (a join per unit) and many (a join per boundary), heads in one block and in several."""
+    c = widen(K, cache(3, lens, Hq, Hkv, 128, 32, dt))
+    R.check_paged(*K.kda_paged_attention(**c), reference(c))
+
+
+@pytest.mark.parametrize("ps", [1, 2, 7, 13, 64, 100, 128, 1000])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_page_sizes_shared_out(K, ps, dt):
+    c = widen(K, cache(4, [200, 64, 1, 129], 8, 2, 64, ps, dt))
+    R.check_paged(*K.kda_paged_attention(**c), reference(c))
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_empty_rows_shared_out(K, dt):
+    c = widen(K, cache(5, [0, 40, 0, 0, 300, 0], 8, 2, 128, 16, dt))
+    out, lse = K.kda_paged_attention(**c)
+    R.check_paged(out, lse, reference(c))
+    assert not out[0].any() and bool((lse[3] == -math.inf).all())
+    c["seq_lens"].zero_()
+    out, lse = K.kda_paged_attention(**c)
+    assert not out.any() and bool((lse == -math.inf).all())
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("ps", [16, 13])
+def test_what_lies_past_a_row_never_reaches_it_shared_out(K, dt, bad, ps):
+    lens = [100, 1, 64, 0, 37, 1500]
+    c = widen(K, cache(8, lens, 8, 2, 128, ps, dt, extra=2))
+    ref = reference(c)
+    used = torch.zeros(c["k_cache"].shape[:2], dtype=torch.bool, device="cuda")
+    for n, length in enumerate(lens):
+        t = torch.arange(length, device="cuda")
+        used[c["block_table"][n].long()[t // ps], t % ps] = True
+    for x in ("k_cache", "v_cache"):
+        c[x][~used] = bad
+    R.check_paged(*K.kda_paged_attention(**c), ref)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_pages_outside_the_pool_are_left_out_shared_out(K, dt):
+    c = widen(K, cache(9, [200, 90, 33, 1000], 4, 2, 128, 16, dt))
+    pages = c["k_cache"].shape[0]
+    c["block_table"][0, 3] = -1
+    c["block_table"][0, 11] = pages
+    c["block_table"][1, :] = 1 << 30          # a row whose every page is bad
+    c["block_table"][2, 0] = -(1 << 31)
+    c["block_table"][3, 8:40] = -1            # whole tiles, and more than a CTA's share
+    R.check_paged(*K.kda_paged_attention(**c), reference(c))
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_lengths_are_clamped_shared_out(K, dt):
+    c = widen(K, cache(10, [64, 48], 4, 2, 64, 16, dt))
+    c["seq_lens"] = torch.tensor([1 << 30, -5], dtype=torch.int32, device="cuda")
+    R.check_paged(*K.kda_paged_attention(**c), reference(c))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
+def test_scales_shared_out(K, scale):
+    c = widen(K, cache(12, [700, 7], 8, 2, 128, 16, BF16))
+    c["scale"] = scale
+    R.check_paged(*K.kda_paged_attention(**c), reference(c))
+
+
+def test_no_lse_and_a_used_workspace(K):
+    c = widen(K, cache(13, [3000, 20], 8, 2, 128, 16, BF16))
+    ws = torch.full((K.kda_paged_attention_workspace_bytes(c["q"], c["k_cache"], c["block_table"]),), 255, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(c["q"])
+    got, lse = K.kda_paged_attention(**c, out=out, output_lse=False, workspace=ws)
+    assert got is out and lse is None
+    R.check_paged(out, None, reference(c))
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_calls_share_a_workspace(K, dt):
+    """Calls back to back on one stream with one workspace (its contents on entry all ones), splits and joins of
+    each kind, and the same in a replayed graph: bit for bit what each gives alone, and right."""
+    cases = [widen(K, cache(41 + i, lens, 24, 2, 128, 16, dt)) for i, lens in
+             enumerate([[5000], [(i * 7919) % 900 for i in range(50)], [0, 3, 2500], [64] * 200])]
+    alone = [K.kda_paged_attention(**c) for c in cases]
+    for c, (out, lse) in zip(cases, alone):
+        R.check_paged(out, lse, reference(c))
+    need = max(K.kda_paged_attention_workspace_bytes(c["q"], c["k_cache"], c["block_table"]) for c in cases)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    got = [K.kda_paged_attention(**cases[i % 4], workspace=ws) for i in range(24)]
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, alone[i % 4][0]) and torch.equal(lse, alone[i % 4][1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got = [K.kda_paged_attention(**c, workspace=ws) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for out, lse in got:
+            out.zero_(), lse.zero_()
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        for (out, lse), (want, wl) in zip(got, alone):
+            assert torch.equal(out, want) and torch.equal(lse, wl)

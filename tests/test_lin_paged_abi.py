@@ -154,3 +154,26 @@ def test_binding_refuses_host_tensors(K):
         K.kda_lin_chunk_fwd(x, x, x)
     with pytest.raises((ValueError, RuntimeError, AssertionError)):
         K.kda_paged_append(x[0], x[0], x, x, torch.zeros(4, 1, dtype=torch.int32), torch.zeros(4, dtype=torch.int32))
+
+
+def test_attention_workspace(K):
+    """Tables wider than a cluster's rows take the shared-out form, which needs a workspace; narrow ones none."""
+    d = paged(K, max_pages=1024)
+    need = K.lib().kda_paged_attention_workspace_bytes(ctypes.byref(d))
+    # 304 CTAs at most, two parts each, of 16 heads' 128 sums, a maximum and a sum
+    assert 0 < need <= 304 * 2 * 16 * 130 * 4
+    assert attend(K, d, ws=None) == K.KDA_ERR_NULL
+    assert attend(K, d, wb=need - 1) == K.KDA_ERR_WORKSPACE
+    assert attend(K, d, ws=FAKE + 4) == K.KDA_ERR_ALIGN
+    assert K.lib().kda_paged_attention_workspace_bytes(ctypes.byref(paged(K))) == 0
+    assert K.lib().kda_paged_attention_workspace_bytes(ctypes.byref(paged(K, max_pages=1024, rows=0))) == 0
+
+
+def test_packed_chunk_workspace_is_checked(K):
+    d = lin(K, batch=1, num_seqs=5, seqlen=1 << 14, dv=128)
+    need = K.lib().kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(d), 1)
+    assert need > 0
+    for s0, sT in ((None, None), (FAKE, FAKE)):           # in place too
+        assert chunk(K, d, cu=FAKE, s0=s0, sT=sT, ws=None) == K.KDA_ERR_NULL
+        assert chunk(K, d, cu=FAKE, s0=s0, sT=sT, wb=need - 1) == K.KDA_ERR_WORKSPACE
+        assert chunk(K, d, cu=FAKE, s0=s0, sT=sT, ws=FAKE + 8) == K.KDA_ERR_ALIGN

@@ -77,7 +77,10 @@ class HybridStack:
         x = self._add(x, o, 1)
         q, k, v = self._att_in(x)
         kda.kda_paged_append(k, v, self.k_cache, self.v_cache, self.table, torch.zeros_like(self.lens), cu)
-        # a prompt's token t attends to positions 0 .. t of its row: one query row per token of the pack
+        # A prompt's token t attends to positions 0 .. t of its row.  The cache's attention takes one new token per
+        # row, so each token of the pack becomes a row with a block table of its own: it reads its row's keys and
+        # values anew, some tokens^2 / 2 of them a prompt, which is fit for an example's short prompts only.  A
+        # server would attend among a prompt's tokens with a kernel for prompts and fill the cache beside it.
         n = cu.long()
         row = torch.repeat_interleave(torch.arange(self.rows, device=x.device), n[1:] - n[:-1])
         seen = (torch.arange(x.shape[0], device=x.device) - n[row] + 1).to(torch.int32)

@@ -14,12 +14,13 @@
 // each CTA but the last first takes its chunks' state from zero, the states are exchanged through
 // distributed shared memory (the true state before part r is the initial state and the parts before
 // it, each decayed by what follows), and every CTA then runs its chunks.  (256 tokens x 2 heads of
-// 64: 29 us with one CTA per sequence and block, 11.5 us with clusters of 8.)
+// 64: 29 us with one CTA per sequence and block, 10.3 us with clusters of 8.)
 //
 // The products are 4 x 4 tiles of four lanes each, in packed fp32 pairs, so that eight 16-byte reads of
 // shared memory feed 64 multiply-adds (with 2 x 2 tiles, 16 to 24: 8 x 1024 tokens x 32 heads of 128 took
-// 1119 us, now 921).  Bound by the latency of a chunk's dependent steps at two CTAs per SM (128
-// registers a thread): 1.7 instructions a cycle, the fp32 pipe 45 % busy.
+// 1119 us, now 921).  Bound by the latency of a chunk's dependent steps, shared memory's above all, at two CTAs
+// per SM (128 registers a thread): on that case 1.8 instructions a cycle, the fp32 pipe 47 % busy.  The CTAs of a
+// head each compute its whole score tile, at d = 128 31 % of a CTA's multiply-adds.
 #include <cooperative_groups.h>
 
 #include "kda_lin.h"
@@ -329,7 +330,8 @@ cudaError_t launch_t(const LinArgs &a, cudaStream_t st) {
     // the work) and two more for its start, half as much again per chunk where CTAs share an SM (5 x 1310
     // tokens x 10 heads: 201 us as one CTA, 190 to 227 as clusters; 1 x 1310: 82 us in clusters of 6, 197 as one).
     const int64_t ctas = (int64_t)a.num_seqs * a.heads * (a.dv / CB);
-    const int64_t chunks = ((a.cu ? a.seqlen / a.num_seqs : a.seqlen) + C - 1) / C;   // of a sequence, on average
+    // (packed: of the average one, whatever the lengths; the sequences run in the order given)
+    const int64_t chunks = ((a.cu ? a.seqlen / a.num_seqs : a.seqlen) + C - 1) / C;   // of a sequence
     int X = 1;
     int64_t best = 0;
     for (int x = 1; x <= kMaxCluster && (x == 1 || x <= chunks); ++x) {

@@ -12,8 +12,8 @@
 //
 // Precision.  The tensor cores multiply bf16 exactly and add in fp32.  q, k and v enter as they
 // are; what is computed enters as a sum of bf16 terms, each the rounding of what the ones before it
-// left: K' as three (2^-24 of each product: the state is an fp32 result), S and P as two (2^-16:
-// they end in bf16 outputs, whose own rounding is 2^-8).  bf16 has fp32's range, so no scale is
+// left: K' as three (within 2^-22 of each product, 2^-26 RMS: the state is an fp32 result), S and P as two
+// (2^-16: they end in bf16 outputs, whose own rounding is 2^-8).  bf16 has fp32's range, so no scale is
 // carried.  The state itself stays in registers and takes each chunk's dS by an fp32 fused
 // multiply-add: the tensor cores truncate their sums, which over many chunks would pile up.
 //
@@ -32,8 +32,8 @@
 // whole of (1) to turn dS of the chunk before into the operand of (2).
 //
 // Measured (B=4 H=32 T=8192 d=128, 128 CTAs): 286 us, 3.8 TB/s, 56 % of the measured copy rate; 2.2 us a
-// chunk, in which an SM issues about 10,000 warp instructions at 2.1 a cycle.  What bounds it is that issue
-// rate with the chunk's chain of hand-overs: the S warps are busy 85 % of the time, the tensor pipe 38 %.
+// chunk.  What bounds it is the issue rate with the chunk's chain of hand-overs.  Counted at T=1024: an SM issues
+// about 10,000 warp instructions a chunk at 2.1 a cycle, the tensor pipe is busy 38 % of the time.
 // No single part carries it: left out one at a time, P and K' save 35 us each, the scores 29, the
 // products 27, S's terms 20, the outputs 15, the decay sums 9.
 #include <cuda.h>

@@ -543,6 +543,8 @@ def kda_lin_chunk_fwd(q, k, v, g=None, head_g=None, initial_state=None, cu_seqle
     q, k: [B, T, Hk, dk]; v: [B, T, H, dv] with Hk a divisor of H (all fp32 or all bf16); g: fp32
     [B, T, H] log decay of each token or None; head_g: fp32 [H] log decay of each head or None;
     initial_state: fp32 [N, H, dk, dv] or None; cu_seqlens: int32 [N+1] (packed, B == 1) or None.
+    final_state may be initial_state, but bf16 sequences are then not cut to fill the SMs: a long prompt
+    of few heads takes up to ten times as long as with a state of its own.
     workspace: uint8 tensor of kda_lin_chunk_fwd_workspace_bytes bytes (allocated here when None).
     Returns (out [B, T, H, dv], final_state fp32 [N, H, dk, dv] or None).
     """
@@ -611,7 +613,8 @@ def kda_paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, *, ou
     """Softmax attention of one new token per row over its cached tokens.
 
     q: [N, Hq, d]; k_cache, v_cache: [pages, page_size, Hkv, d] with Hkv a divisor of Hq;
-    block_table: int32 [N, max_pages]; seq_lens: int32 [N]; scale: multiplies q . k.
+    block_table: int32 [N, max_pages], no wider than the rows may need (the width chooses between one
+    launch and two); seq_lens: int32 [N]; scale: multiplies q . k.
     workspace: uint8 tensor of kda_paged_attention_workspace_bytes bytes (allocated here when None).
     Returns (out [N, Hq, d], lse fp32 [N, Hq] or None); a row without tokens gets 0 and -infinity.
     """

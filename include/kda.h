@@ -571,6 +571,143 @@ kda_status_t kda_paged_attention(const void *q, const void *k_cache, const void 
 /* Bytes of workspace kda_paged_attention needs for `dims` (host arithmetic only). */
 size_t kda_paged_attention_workspace_bytes(const kda_paged_dims_t *dims);
 
+/* ------------------------------------------------------------------------------------------
+ * Branching decode.  Several drafted continuations of a sequence form a tree that one pass verifies
+ * (speculative decoding); beams and parallel samples share a prompt's pages, fork and end.
+ *
+ * A row's draft has up to `tokens` <= KDA_TREE_TOKENS tokens, stored before the tokens that continue them:
+ *   parents    : int32 [rows, tokens], for each drafted token i the one it continues, -1 (the row's own
+ *                last token) <= parents[n, i] < i.  A value outside that range counts as -1.  NULL: every
+ *                token continues the one before it (a single line of tokens).
+ *   num_tokens : int32 [rows], the row's drafted tokens (clamped to [0, tokens]), or NULL (all).
+ *   accepted   : int32 [rows], the last drafted token that is kept; with it all tokens on its path, from
+ *                the first one to itself, are.  Outside [0, num_tokens[n]): none is.
+ * Below, A(i) is the path to token i, itself included.
+ * ------------------------------------------------------------------------------------------ */
+#define KDA_TREE_TOKENS 64
+
+/* kda_recurrent_tree -- KDA outputs of every token of a draft, the states left as they are.
+ *
+ * Per row n, head h and drafted token i, from S_-1 = state[slot][h] (slot as in kda_recurrent_step):
+ *   S_i = (I - beta_i k_i k_i^T) Diag(exp g_i) S_parent(i) + beta_i k_i v_i^T,   o_i = S_i^T q_i.
+ * No S_i is formed: with E_ij = exp of the sum of g over A(i) \ A(j) (E_i: over A(i)),
+ *   u_i = beta_i (v_i - (E_i k_i)^T S) - beta_i sum_{j in A(i), j != i} (k_i . E_ij k_j) u_j,
+ *   o_i = (E_i q_i)^T S + sum_{j in A(i)} (q_i . E_ij k_j) u_j.
+ * (kda_recurrent_steps is the same for one line of tokens, and can write the state.)
+ *   q, k, g : [N, T, H, dk] dtype;  v, out : [N, T, H, dv] dtype;  beta : [N, T, H] dtype
+ *   state   : fp32 [num_seqs, H, dk, dv], only read
+ * Outputs of tokens past a row's count, and of rows whose slot is outside the pool, are set to zero.
+ * g may be any log decay <= 0 (the bound g >= -5 is not needed here).  bf16: the products with S take S and
+ * E_i k_i, E_i q_i rounded to 11 bits (2^-11 relative, an eighth of the output's own rounding); fp32 calls split them in
+ * two such parts.  A NaN or infinity among a token's inputs reaches the outputs of the tokens that continue
+ * it, and no other's.
+ * dims: batch = N rows, seqlen = T in [1, KDA_TREE_TOKENS], num_seqs = pool slots.  Errors as in
+ * kda_recurrent_step. */
+kda_status_t kda_recurrent_tree(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                                const float *state, const int32_t *state_indices, const int32_t *parents,
+                                const int32_t *num_tokens, void *out, const kda_dims_t *dims, cudaStream_t stream);
+
+/* kda_recurrent_tree_qknorm -- kda_recurrent_tree with q and k L2-normalised first, as in
+ * kda_chunk_fwd_qknorm.  qk_eps >= 0 and finite, else KDA_ERR_SHAPE. */
+kda_status_t kda_recurrent_tree_qknorm(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                                       float qk_eps, const float *state, const int32_t *state_indices,
+                                       const int32_t *parents, const int32_t *num_tokens, void *out,
+                                       const kda_dims_t *dims, cudaStream_t stream);
+
+/* kda_recurrent_tree_commit -- brings each row's accepted path into its state, in place: S_accepted[n] of
+ * kda_recurrent_tree, computed token by token in fp32 as in kda_recurrent_step.  Rows that accept none keep their
+ * state (it is not read).  Two rows must not name the same slot.  Arguments and errors as in
+ * kda_recurrent_tree; accepted is required. */
+kda_status_t kda_recurrent_tree_commit(const void *k, const void *v, const void *g, const void *beta, float *state,
+                                       const int32_t *state_indices, const int32_t *parents, const int32_t *num_tokens,
+                                       const int32_t *accepted, const kda_dims_t *dims, cudaStream_t stream);
+
+/* kda_recurrent_tree_commit_qknorm -- the same with k L2-normalised first. */
+kda_status_t kda_recurrent_tree_commit_qknorm(const void *k, const void *v, const void *g, const void *beta,
+                                              float qk_eps, float *state, const int32_t *state_indices,
+                                              const int32_t *parents, const int32_t *num_tokens,
+                                              const int32_t *accepted, const kda_dims_t *dims, cudaStream_t stream);
+
+/* kda_paged_tree_attention -- softmax attention of a row's drafted tokens over its cached tokens and their
+ * own paths.
+ *
+ * Row n holds len = seq_lens[n] tokens (clamped as in kda_paged_attention); its drafted token j is at position
+ * len + j of the cache (kda_paged_append with positions = seq_lens puts it there).  Token i attends to
+ * positions [0, len) and len + j for j in A(i); scores, sums and lse are kda_paged_attention's.
+ *   q, out : [rows, tokens, heads, head_dim] dtype (out is written);  lse : fp32 [rows, tokens, heads] or NULL
+ * Tokens past a row's count get out = 0 and lse = -infinity, as does a token that is left with nothing to attend
+ * to.  Positions past the table's width, on pages outside the pool, or with a score of -infinity weigh nothing.
+ * What the cache holds at places a token does not attend to (other branches of the draft, tokens
+ * past the count) never reaches its results, NaN and infinities included.
+ * bf16: K and V enter the tensor cores as they are, the weights as a rounded bf16 and the rounded
+ * rest (16 bits); sums are fp32.
+ *   tokens    : in [1, KDA_TREE_TOKENS];  pages * page_size * kv_heads at most 2^31 - 1, else KDA_ERR_SHAPE
+ *   workspace : kda_paged_tree_attention_workspace_bytes(tokens, dims) bytes, 16-byte aligned (NULL when that is
+ *               0), contents on entry of no matter; one per call in flight.
+ * Results do not depend on timing.  Other arguments and errors as in kda_paged_attention. */
+kda_status_t kda_paged_tree_attention(const void *q, const void *k_cache, const void *v_cache,
+                                      const int32_t *block_table, const int32_t *seq_lens, const int32_t *parents,
+                                      const int32_t *num_tokens, int32_t tokens, float scale, void *out, float *lse,
+                                      void *workspace, size_t workspace_bytes, const kda_paged_dims_t *dims,
+                                      cudaStream_t stream);
+
+/* Bytes of workspace kda_paged_tree_attention needs (host arithmetic only; 0 for arguments that it refuses). */
+size_t kda_paged_tree_attention_workspace_bytes(int32_t tokens, const kda_paged_dims_t *dims);
+
+/* kda_paged_tree_commit -- moves the keys and values of each row's accepted path to the end of the row's cached
+ * tokens: the r-th token a_r of the path goes from position len + a_r to len + r, len = seq_lens[n] clamped to
+ * [0, max_pages * page_size].  Then new_lens[n] = len + the path's length, at most max_pages * page_size (NULL:
+ * not written; it may be seq_lens itself where the cache has one layer: others need the old lengths).  Tokens whose
+ * old or new place is past the table or outside the pool are not moved.  No two positions of the rows' drafts may
+ * lie in the same place.  Errors as in kda_paged_append; tokens in [1, KDA_TREE_TOKENS]. */
+kda_status_t kda_paged_tree_commit(void *k_cache, void *v_cache, const int32_t *block_table, const int32_t *seq_lens,
+                                   const int32_t *parents, const int32_t *num_tokens, const int32_t *accepted,
+                                   int32_t tokens, int32_t *new_lens, const kda_paged_dims_t *dims, cudaStream_t stream);
+
+/* kda_paged_fork -- forks, reorders, ends and extends the rows of a block table.
+ *
+ * page_refs[p] counts the table entries that name page p; a page with 0 is free.  Entries outside [0, pages) name no
+ * page (-1 is written for them).  Row n of the new table continues row s = sources[n] of the old one, or is
+ * empty (sources[n] outside [0, rows): all -1, length 0); an old row that nothing continues ends, and its
+ * pages lose a reference.  With len = seq_lens[s] clamped to [0, max_pages * page_size]:
+ *   - The entries of the pages that len fills are shared.
+ *   - A last page that is only partly filled is kept by the first row n that continues s where page_refs counts
+ *     no other reference to it, and copied by the others: they get a free page, and copies[n] = (old page, new
+ *     page); else copies[n] = (-1, -1).  kda_paged_copy then copies it in each layer's cache.
+ *   - The pages that s holds past len stay with that first row.
+ *   - Entries below ceil((len + new_tokens[n]) / page_size), at most max_pages, that name no page get a free one.
+ * Free pages are those that page_refs counts no reference to on entry (pages that this call frees are
+ * available to the next one), lowest first, to the rows in order and within a row to its entries in order.
+ * Where there are too few, *short_of is the number that is missing, the new table, lengths and counts are copies of
+ * the old ones and all copies (-1, -1); else *short_of = 0.
+ *   block_table, new_table : int32 [rows, max_pages];  seq_lens, new_lens, sources : int32 [rows]
+ *   new_tokens : int32 [rows], or NULL (0; negative values count as 0)
+ *   page_refs, new_refs : int32 [pages];  copies : int32 [rows, 2];  short_of : int32 [1]
+ * Outputs may not overlap inputs (KDA_ERR_SHAPE where an output is one of the inputs).  dims: rows in
+ * [1, 65536], pages at most 2^23, rows * max_pages at most 2^31 - 1 (else KDA_ERR_SHAPE), page_size; the rest is
+ * not read. */
+kda_status_t kda_paged_fork(const int32_t *block_table, const int32_t *seq_lens, const int32_t *page_refs,
+                            const int32_t *sources, const int32_t *new_tokens, int32_t *new_table, int32_t *new_lens,
+                            int32_t *new_refs, int32_t *copies, int32_t *short_of, const kda_paged_dims_t *dims,
+                            cudaStream_t stream);
+
+/* kda_paged_compact -- closes the gaps of a pool, so that its pages in use are the first ones.
+ *
+ * With U the number of pages that page_refs counts references to, the used pages at or past U move, in
+ * order, into the free pages below U, in order; the table and the counts follow them.
+ *   copies : int32 [pages / 2, 2], the moves (old page, new page) in order, then (-1, -1); kda_paged_copy carries
+ *            them out in each layer's cache.
+ * Every entry that the counts stand for has to be in this table.  Other arguments, limits and errors
+ * as in kda_paged_fork (rows may be 0). */
+kda_status_t kda_paged_compact(const int32_t *block_table, const int32_t *page_refs, int32_t *new_table,
+                               int32_t *new_refs, int32_t *copies, const kda_paged_dims_t *dims, cudaStream_t stream);
+
+/* kda_paged_copy -- copies whole pages within a cache: for each of `count` pairs of copies, int32 [count, 2], page
+ * copies[i][1] becomes a copy of page copies[i][0].  Pairs with a page outside the pool are skipped.  A page that is
+ * copied to may not be in another pair.  dims as in kda_paged_append (rows and max_pages are not used). */
+kda_status_t kda_paged_copy(void *k_cache, void *v_cache, const int32_t *copies, int64_t count,
+                            const kda_paged_dims_t *dims, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,4 +1,4 @@
-// Python binding of the linear-attention and paged-cache calls: argument checks, output allocation and the
+// Python binding of the linear-attention, paged-cache and branching-decode calls: argument checks, output allocation and the
 // current stream, in C++.  A decode step's calls take a few microseconds on the GPU; the same work done
 // in Python around ctypes cost 8 to 20 us of host time per call, here 3 to 6.
 //
@@ -14,6 +14,7 @@
 #include <cstdarg>
 #include <initializer_list>
 #include <optional>
+#include <tuple>
 
 #include "../../include/kda.h"
 
@@ -25,6 +26,16 @@ decltype(&kda_lin_recurrent_step) f_step;
 decltype(&kda_paged_append) f_append;
 decltype(&kda_paged_attention) f_attend;
 decltype(&kda_paged_attention_workspace_bytes) f_attend_bytes;
+decltype(&kda_recurrent_tree) f_tree;
+decltype(&kda_recurrent_tree_qknorm) f_tree_norm;
+decltype(&kda_recurrent_tree_commit) f_replay;
+decltype(&kda_recurrent_tree_commit_qknorm) f_replay_norm;
+decltype(&kda_paged_tree_attention) f_tree_attend;
+decltype(&kda_paged_tree_attention_workspace_bytes) f_tree_attend_bytes;
+decltype(&kda_paged_tree_commit) f_keep;
+decltype(&kda_paged_fork) f_fork;
+decltype(&kda_paged_compact) f_compact;
+decltype(&kda_paged_copy) f_copy;
 PyObject *raise_status;   // called with (status, name); raises
 
 struct Refused {};        // a Python error is set
@@ -50,6 +61,7 @@ struct Arg {
     }
     explicit operator bool() const { return t != nullptr; }
     void *ptr() const { return t ? t->data_ptr() : nullptr; }
+    const int32_t *ints() const { return static_cast<const int32_t *>(ptr()); }
     int64_t size(int64_t d) const { return t->size(d); }
     const Arg &need(int64_t dims, const char *what) const {
         if (!t || t->dim() != dims) refuse(PyExc_ValueError, "%s must be %s", name, what);
@@ -294,26 +306,255 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// (raise_status, six addresses in the order of the declarations above)
+// The inputs that kda_recurrent_tree (q given) and kda_recurrent_tree_commit share.
+kda_dims_t tree_dims(const Arg &q, const Arg &k, const Arg &v, const Arg &g, const Arg &beta, const Arg &state, const Arg &parents, const Arg &idx, const Arg &num, int &dev) {
+    k.need(4, "[N, T, H, dk]"), v.need(4, "[N, T, H, dv]"), g.need(4, "shaped like k"), beta.need(3, "[N, T, H]"), state.need(4, "[P, H, dk, dv]");
+    dev = device_of(k);
+    const kda_dtype_t code = dtype_of(k);
+    const at::ScalarType dt = k.t->scalar_type();
+    const int64_t N = k.size(0), T = k.size(1), H = k.size(2), dk = k.size(3), dv = v.size(3), slots = state.size(0);
+    q.check(dt, dev, {N, T, H, dk});
+    k.check(dt, dev, {N, T, H, dk});
+    g.check(dt, dev, {N, T, H, dk});
+    v.check(dt, dev, {N, T, H, dv});
+    beta.check(dt, dev, {N, T, H});
+    state.check(at::kFloat, dev, {slots, H, dk, dv});
+    parents.check(at::kInt, dev, {N, T});
+    idx.check(at::kInt, dev, {N});
+    num.check(at::kInt, dev, {N});
+    return {narrow(N, "N"), narrow(T, "T"), narrow(slots, "P"), narrow(H, "H"), narrow(dk, "dk"), narrow(dv, "dv"), code};
+}
+
+// None, or a number
+std::optional<float> epsilon(PyObject *o) {
+    if (o == Py_None) return std::nullopt;
+    const double x = PyFloat_AsDouble(o);
+    if (PyErr_Occurred()) throw Refused{};
+    return (float)x;
+}
+
+// (q, k, v, g, beta, state, parents, state_indices, num_tokens, out, qk_eps, stream)
+PyObject *tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        count(n, 12, "tree");
+        const Arg q(a[0], "q"), k(a[1], "k"), v(a[2], "v"), g(a[3], "g"), beta(a[4], "beta"), state(a[5], "state"), parents(a[6], "parents");
+        const Arg idx(a[7], "state_indices"), num(a[8], "num_tokens"), out(a[9], "out");
+        q.need(4, "[N, T, H, dk]");
+        int dev;
+        const kda_dims_t d = tree_dims(q, k, v, g, beta, state, parents, idx, num, dev);
+        const at::ScalarType dt = k.t->scalar_type();
+        out.check(dt, dev, {d.batch, d.seqlen, d.heads, d.dv});
+        const std::optional<float> eps = epsilon(a[10]);
+        const Stream s(a[11], dev);
+        at::Tensor o;
+        const at::Tensor *op = or_made(out, o, s, {d.batch, d.seqlen, d.heads, d.dv}, dt);
+        const float *S = static_cast<const float *>(state.ptr());
+        if (eps)
+            finish(f_tree_norm(q.ptr(), k.ptr(), v.ptr(), g.ptr(), beta.ptr(), *eps, S, idx.ints(), parents.ints(), num.ints(), op->data_ptr(), &d, s.handle),
+                   "kda_recurrent_tree_qknorm");
+        else
+            finish(f_tree(q.ptr(), k.ptr(), v.ptr(), g.ptr(), beta.ptr(), S, idx.ints(), parents.ints(), num.ints(), op->data_ptr(), &d, s.handle), "kda_recurrent_tree");
+        return wrap(a[9], o);
+    });
+}
+
+// (k, v, g, beta, state, parents, accepted, state_indices, num_tokens, qk_eps, stream)
+PyObject *replay(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        count(n, 11, "replay");
+        const Arg q(Py_None, "q"), k(a[0], "k"), v(a[1], "v"), g(a[2], "g"), beta(a[3], "beta"), state(a[4], "state"), parents(a[5], "parents");
+        const Arg accepted(a[6], "accepted"), idx(a[7], "state_indices"), num(a[8], "num_tokens");
+        accepted.need(1, "[N]");
+        int dev;
+        const kda_dims_t d = tree_dims(q, k, v, g, beta, state, parents, idx, num, dev);
+        accepted.check(at::kInt, dev, {d.batch});
+        const std::optional<float> eps = epsilon(a[9]);
+        const Stream s(a[10], dev);
+        float *S = static_cast<float *>(state.ptr());
+        if (eps)
+            finish(f_replay_norm(k.ptr(), v.ptr(), g.ptr(), beta.ptr(), *eps, S, idx.ints(), parents.ints(), num.ints(), accepted.ints(), &d, s.handle),
+                   "kda_recurrent_tree_commit_qknorm");
+        else
+            finish(f_replay(k.ptr(), v.ptr(), g.ptr(), beta.ptr(), S, idx.ints(), parents.ints(), num.ints(), accepted.ints(), &d, s.handle),
+                   "kda_recurrent_tree_commit");
+        return Py_NewRef(Py_None);
+    });
+}
+
+// (q, k_cache, v_cache, block_table, seq_lens, parents, scale, num_tokens, out, lse, want_lse, workspace, stream)
+PyObject *tree_attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        count(n, 13, "tree_attend");
+        const Arg q(a[0], "q"), kc(a[1], "k_cache"), vc(a[2], "v_cache"), table(a[3], "block_table"), lens(a[4], "seq_lens"), parents(a[5], "parents");
+        const Arg num(a[7], "num_tokens"), out(a[8], "out"), lse(a[9], "lse"), ws(a[11], "workspace");
+        q.need(4, "[N, T, Hq, d]"), lens.need(1, "[N]");
+        const int dev = device_of(q);
+        const at::ScalarType dt = q.t->scalar_type();
+        const int64_t N = q.size(0), T = q.size(1), Hq = q.size(2);
+        kda_paged_dims_t d = paged_dims(kc, vc, table, N, Hq, dt, dtype_of(q), dev);
+        d.heads = narrow(Hq, "Hq");
+        q.check(dt, dev, {N, T, Hq, d.head_dim});
+        lens.check(at::kInt, dev, {N});
+        parents.check(at::kInt, dev, {N, T});
+        num.check(at::kInt, dev, {N});
+        out.check(dt, dev, {N, T, Hq, d.head_dim});
+        lse.check(at::kFloat, dev, {N, T, Hq});
+        if (ws) ws.check(at::kByte, dev, {ws.t->numel()});
+        const double scale = PyFloat_AsDouble(a[6]);
+        if (PyErr_Occurred()) throw Refused{};
+        const int32_t tokens = narrow(T, "T");
+        const Stream s(a[12], dev);
+        at::Tensor o, l, w;
+        const at::Tensor *op = or_made(out, o, s, {N, T, Hq, d.head_dim}, dt), *lp = nullptr;
+        if (lse || truth(a[10])) lp = or_made(lse, l, s, {N, T, Hq}, at::kFloat);
+        const at::Tensor *wp = ws.t;
+        if (!wp)
+            if (const size_t bytes = f_tree_attend_bytes(tokens, &d)) wp = or_made(ws, w, s, {(int64_t)bytes}, at::kByte);
+        finish(f_tree_attend(q.ptr(), kc.ptr(), vc.ptr(), table.ints(), lens.ints(), parents.ints(), num.ints(), tokens, (float)scale, op->data_ptr(),
+                             lp ? static_cast<float *>(lp->data_ptr()) : nullptr, wp ? wp->data_ptr() : nullptr, wp ? (size_t)wp->numel() : 0, &d, s.handle),
+               "kda_paged_tree_attention");
+        return pair(wrap(a[8], o), wrap(a[9], l));
+    });
+}
+
+// (k_cache, v_cache, block_table, seq_lens, parents, accepted, num_tokens, tokens, new_lens, stream)
+PyObject *keep(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        count(n, 10, "keep");
+        const Arg kc(a[0], "k_cache"), vc(a[1], "v_cache"), table(a[2], "block_table"), lens(a[3], "seq_lens"), parents(a[4], "parents");
+        const Arg accepted(a[5], "accepted"), num(a[6], "num_tokens"), to(a[8], "new_lens");
+        kc.need(4, "[pages, page_size, Hkv, d]"), lens.need(1, "[N]"), accepted.need(1, "[N]");
+        const int dev = device_of(kc);
+        const int64_t N = lens.size(0);
+        int64_t T = 0;
+        if (parents) {
+            T = parents.need(2, "[N, T]").size(1);
+        } else {
+            T = PyLong_AsLongLong(a[7]);
+            if (PyErr_Occurred()) throw Refused{};
+        }
+        const kda_paged_dims_t d = paged_dims(kc, vc, table, N, 0, kc.t->scalar_type(), dtype_of(kc), dev);
+        lens.check(at::kInt, dev, {N});
+        parents.check(at::kInt, dev, {N, T});
+        accepted.check(at::kInt, dev, {N});
+        num.check(at::kInt, dev, {N});
+        to.check(at::kInt, dev, {N});
+        const Stream s(a[9], dev);
+        at::Tensor made;
+        const at::Tensor *tp = or_made(to, made, s, {N}, at::kInt);
+        finish(f_keep(kc.ptr(), vc.ptr(), table.ints(), lens.ints(), parents.ints(), num.ints(), accepted.ints(), narrow(T, "T"),
+                      static_cast<int32_t *>(tp->data_ptr()), &d, s.handle),
+               "kda_paged_tree_commit");
+        return wrap(a[8], made);
+    });
+}
+
+kda_paged_dims_t pool_dims(const Arg &table, const Arg &refs, int64_t page_size) {
+    return {narrow(table.size(0), "N"), 1, 1, 64, narrow(refs.size(0), "pages"), narrow(page_size, "page_size"), narrow(table.size(1), "max_pages"), KDA_BF16};
+}
+
+// (block_table, seq_lens, page_refs, sources, new_tokens, page_size, new_table, new_lens, new_refs, copies, short_of, stream)
+PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        count(n, 12, "fork");
+        const Arg table(a[0], "block_table"), lens(a[1], "seq_lens"), refs(a[2], "page_refs"), sources(a[3], "sources"), more(a[4], "new_tokens");
+        const Arg out[5] = {{a[6], "new_table"}, {a[7], "new_lens"}, {a[8], "new_refs"}, {a[9], "copies"}, {a[10], "short_of"}};
+        table.need(2, "[N, max_pages]"), lens.need(1, "[N]"), refs.need(1, "[pages]"), sources.need(1, "[N]");
+        const int dev = device_of(table);
+        const int64_t N = table.size(0), W = table.size(1), pages = refs.size(0), ps = PyLong_AsLongLong(a[5]);
+        if (PyErr_Occurred()) throw Refused{};
+        table.check(at::kInt, dev, {N, W});
+        lens.check(at::kInt, dev, {N});
+        refs.check(at::kInt, dev, {pages});
+        sources.check(at::kInt, dev, {N});
+        more.check(at::kInt, dev, {N});
+        out[0].check(at::kInt, dev, {N, W});
+        out[1].check(at::kInt, dev, {N});
+        out[2].check(at::kInt, dev, {pages});
+        out[3].check(at::kInt, dev, {N, 2});
+        out[4].check(at::kInt, dev, {1});
+        const kda_paged_dims_t d = pool_dims(table, refs, ps);
+        const Stream s(a[11], dev);
+        at::Tensor made[5];
+        int32_t *p[5];
+        p[0] = static_cast<int32_t *>(or_made(out[0], made[0], s, {N, W}, at::kInt)->data_ptr());
+        p[1] = static_cast<int32_t *>(or_made(out[1], made[1], s, {N}, at::kInt)->data_ptr());
+        p[2] = static_cast<int32_t *>(or_made(out[2], made[2], s, {pages}, at::kInt)->data_ptr());
+        p[3] = static_cast<int32_t *>(or_made(out[3], made[3], s, {N, 2}, at::kInt)->data_ptr());
+        p[4] = static_cast<int32_t *>(or_made(out[4], made[4], s, {1}, at::kInt)->data_ptr());
+        finish(f_fork(table.ints(), lens.ints(), refs.ints(), sources.ints(), more.ints(), p[0], p[1], p[2], p[3], p[4], &d, s.handle), "kda_paged_fork");
+        PyObject *r = PyTuple_New(5);
+        for (int i = 0; r && i < 5; ++i) PyTuple_SET_ITEM(r, i, wrap(a[6 + i], made[i]));
+        return r;
+    });
+}
+
+// (block_table, page_refs, new_table, new_refs, copies, stream)
+PyObject *compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        count(n, 6, "compact");
+        const Arg table(a[0], "block_table"), refs(a[1], "page_refs"), nt(a[2], "new_table"), nr(a[3], "new_refs"), copies(a[4], "copies");
+        table.need(2, "[N, max_pages]"), refs.need(1, "[pages]");
+        const int dev = device_of(table);
+        const int64_t N = table.size(0), W = table.size(1), pages = refs.size(0);
+        table.check(at::kInt, dev, {N, W});
+        refs.check(at::kInt, dev, {pages});
+        nt.check(at::kInt, dev, {N, W});
+        nr.check(at::kInt, dev, {pages});
+        copies.check(at::kInt, dev, {pages / 2, 2});
+        const kda_paged_dims_t d = pool_dims(table, refs, 1);
+        const Stream s(a[5], dev);
+        at::Tensor made[3];
+        int32_t *p[3];
+        p[0] = static_cast<int32_t *>(or_made(nt, made[0], s, {N, W}, at::kInt)->data_ptr());
+        p[1] = static_cast<int32_t *>(or_made(nr, made[1], s, {pages}, at::kInt)->data_ptr());
+        p[2] = static_cast<int32_t *>(or_made(copies, made[2], s, {pages / 2, 2}, at::kInt)->data_ptr());
+        finish(f_compact(table.ints(), refs.ints(), p[0], p[1], p[2], &d, s.handle), "kda_paged_compact");
+        PyObject *r = PyTuple_New(3);
+        for (int i = 0; r && i < 3; ++i) PyTuple_SET_ITEM(r, i, wrap(a[2 + i], made[i]));
+        return r;
+    });
+}
+
+// (k_cache, v_cache, copies, stream)
+PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        count(n, 4, "copy");
+        const Arg kc(a[0], "k_cache"), vc(a[1], "v_cache"), copies(a[2], "copies");
+        kc.need(4, "[pages, page_size, Hkv, d]"), vc.need(4, "shaped like k_cache"), copies.need(2, "[M, 2]");
+        const int dev = device_of(kc);
+        const at::ScalarType dt = kc.t->scalar_type();
+        const int64_t pages = kc.size(0), ps = kc.size(1), hkv = kc.size(2), d = kc.size(3), M = copies.size(0);
+        const kda_dtype_t code = dtype_of(kc);
+        kc.check(dt, dev, {pages, ps, hkv, d});
+        vc.check(dt, dev, {pages, ps, hkv, d});
+        copies.check(at::kInt, dev, {M, 2});
+        const kda_paged_dims_t dims{0, narrow(hkv, "Hkv"), narrow(hkv, "Hkv"), narrow(d, "d"), narrow(pages, "pages"), narrow(ps, "page_size"), 1, code};
+        const Stream s(a[3], dev);
+        finish(f_copy(kc.ptr(), vc.ptr(), copies.ints(), M, &dims, s.handle), "kda_paged_copy");
+        return Py_NewRef(Py_None);
+    });
+}
+
+// (raise_status, the addresses in the order of the declarations above)
+template <typename F> void take(F &f, PyObject *o) { f = reinterpret_cast<F>(PyLong_AsVoidPtr(o)); }
+
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
-        count(n, 7, "bind");
-        void *p[6];
-        for (int i = 0; i < 6; ++i) p[i] = PyLong_AsVoidPtr(a[i + 1]);
+        count(n, 17, "bind");
+        PyObject *const *p = a + 1;
+        std::apply([&](auto &...f) { (take(f, *p++), ...); },
+                   std::tie(f_chunk, f_chunk_bytes, f_step, f_append, f_attend, f_attend_bytes, f_tree, f_tree_norm, f_replay, f_replay_norm, f_tree_attend,
+                            f_tree_attend_bytes, f_keep, f_fork, f_compact, f_copy));
         if (PyErr_Occurred()) throw Refused{};
-        f_chunk = reinterpret_cast<decltype(f_chunk)>(p[0]);
-        f_chunk_bytes = reinterpret_cast<decltype(f_chunk_bytes)>(p[1]);
-        f_step = reinterpret_cast<decltype(f_step)>(p[2]);
-        f_append = reinterpret_cast<decltype(f_append)>(p[3]);
-        f_attend = reinterpret_cast<decltype(f_attend)>(p[4]);
-        f_attend_bytes = reinterpret_cast<decltype(f_attend_bytes)>(p[5]);
         Py_XSETREF(raise_status, Py_NewRef(a[0]));
         return Py_NewRef(Py_None);
     });
 }
 
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD(bind), METHOD(lin_chunk), METHOD(lin_step), METHOD(append), METHOD(attend), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {METHOD(bind), METHOD(lin_chunk), METHOD(lin_step), METHOD(append), METHOD(attend), METHOD(tree), METHOD(replay), METHOD(tree_attend),
+                         METHOD(keep), METHOD(fork), METHOD(compact), METHOD(copy), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,146 @@
+// Attention of a draft's tokens over a paged cache: how its work is shared out (both kernels and the join).
+//
+// A unit is a row's key/value head with a block of up to RB of its query rows (drafted token x query head of the
+// group, token-major).  Its items are its tiles of cached tokens, its tiles of drafted tokens and, ahead of them,
+// kTreeStart that stand for the time a unit's start takes.  The items of all units, in order, are cut into equal
+// shares, one per CTA; each CTA finds its share from seq_lens and num_tokens on the device.  A unit in
+// several shares leaves one partial (maximum, sum, unnormalised output) per share in the workspace,
+// and a second kernel joins them in a fixed order, so that results do not depend on timing.
+#pragma once
+
+#include "kda_paged.cuh"
+#include "kda_tree.h"
+
+namespace kda {
+
+constexpr int kTreeStart = 1;   // a unit's start, in tiles
+
+struct TreeAtt {
+    PagedTreeArgs t;
+    FastDiv by_page, by_rep;
+    int32_t rep, rb, kt;       // query heads per key/value head, query rows per block, keys per tile
+    float *part_o, *part_ml;   // partials: [2 ctas][rb][D], [2 ctas][rb][2]
+};
+
+struct TreeRow {
+    int m, len, ctx, tiles, blocks;   // drafted and cached tokens; tiles of cached ones; all; query blocks
+    long long items;                  // of one unit
+};
+__device__ __forceinline__ TreeRow tree_row(const TreeAtt &a, int n) {
+    TreeRow r;
+    r.m = tree_count(a.t.num, a.t.tokens, n);
+    r.len = row_length(a.t.p, n);
+    r.ctx = (r.len + a.kt - 1) / a.kt;
+    r.tiles = r.ctx + (r.m + a.kt - 1) / a.kt;
+    r.blocks = (r.m * a.rep + a.rb - 1) / a.rb;
+    r.items = kTreeStart + r.tiles;
+    return r;
+}
+__device__ __forceinline__ long long tree_items(const TreeAtt &a, int n) {   // of all its units
+    const TreeRow r = tree_row(a, n);
+    return r.items * r.blocks * a.t.p.kv_heads;
+}
+
+// Block-wide: the items of all rows.
+template <int THREADS> __device__ __forceinline__ long long tree_total(const TreeAtt &a, long long *sm) {
+    long long mine = 0;
+    for (int i = threadIdx.x; i < a.t.p.rows; i += THREADS) mine += tree_items(a, i);
+    return block_sum<THREADS>(mine, sm);
+}
+
+// Block-wide: the row that holds item x and the number of items before that row.
+template <int THREADS>
+__device__ void tree_find(const TreeAtt &a, long long x, long long *sm, int &row, long long &before) {
+    __shared__ int s_row;
+    __shared__ long long s_before;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    long long run = 0;
+    for (int base = 0; base < a.t.p.rows; base += THREADS) {
+        const int n = base + t;
+        const long long w = n < a.t.p.rows ? tree_items(a, n) : 0;
+        long long v = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        __syncthreads();
+        if (lane == 31) sm[warp] = v;
+        __syncthreads();
+        long long off = 0, tot = 0;
+#pragma unroll
+        for (int i = 0; i < THREADS / 32; ++i) {
+            off += i < warp ? sm[i] : 0;
+            tot += sm[i];
+        }
+        const long long first = run + off + v - w;
+        if (first <= x && x < first + w) {
+            s_row = n;
+            s_before = first;
+        }
+        run += tot;
+        if (x < run) break;   // uniform
+    }
+    __syncthreads();
+    row = s_row;
+    before = s_before;
+}
+
+// Path masks of row n's drafted tokens (bit j of anc[i]: token j lies on the path to i), by one warp, path lengths
+// doubled each step.
+__device__ __forceinline__ void tree_masks(const TreeAtt &a, int n, int m, uint64_t *anc, int *up) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i = lane + 32 * e;
+        anc[i] = i < m ? 1ull << i : 0;
+        up[i] = i < m ? tree_parent(a.t.parents, a.t.tokens, n, i) : -1;
+    }
+    __syncwarp();
+    for (int step = 1; step < kTreeMax; step <<= 1) {
+        uint64_t x[2];
+        int p[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            p[e] = up[lane + 32 * e];
+            x[e] = p[e] >= 0 ? anc[p[e]] : 0;
+            p[e] = p[e] >= 0 ? up[p[e]] : -1;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            anc[lane + 32 * e] |= x[e];
+            up[lane + 32 * e] = p[e];
+        }
+        __syncwarp();
+    }
+}
+
+// Place of a row's position in the cache of single tokens, -1 for none.
+__device__ __forceinline__ int64_t tree_place(const TreeAtt &a, const int32_t *table, int pos) {
+    const uint32_t pg = a.by_page((uint32_t)pos);
+    if (pg >= (uint32_t)a.t.p.max_pages) return -1;
+    const int page = __ldg(table + pg);
+    if (page < 0 || page >= a.t.p.pages) return -1;
+    return (int64_t)page * a.t.p.page_size + (pos - (int)pg * a.t.p.page_size);
+}
+
+// Outputs of the tokens past their row's count: zero and -infinity, spread over the CTAs.
+template <typename T, int D, int THREADS> __device__ __forceinline__ void tree_clear(const TreeAtt &a, int ctas) {
+    if (a.t.num == nullptr) return;
+    const PagedArgs &p = a.t.p;
+    for (int x = blockIdx.x; x < p.rows; x += ctas) {
+        const int m = tree_count(a.t.num, a.t.tokens, x);
+        const int64_t first = ((int64_t)x * a.t.tokens + m) * p.heads;
+        const int rows = (a.t.tokens - m) * p.heads;
+        uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + first * D);
+        for (int i = threadIdx.x; i < rows * (D * (int)sizeof(T) / 16); i += THREADS) out[i] = make_uint4(0, 0, 0, 0);
+        if (p.lse)
+            for (int i = threadIdx.x; i < rows; i += THREADS) p.lse[first + i] = -INFINITY;
+    }
+}
+
+// Joins the partials that a kernel of `ctas` shares left.
+cudaError_t launch_tree_join(const TreeAtt &a, int d, kda_dtype_t dt, int ctas, cudaStream_t st);
+
+}  // namespace kda

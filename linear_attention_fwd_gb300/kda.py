@@ -34,7 +34,12 @@ EXPORTED = ("kda_chunk_fwd", "kda_chunk_fwd_with", "kda_chunk_fwd_bounded", "kda
             "kda_status_string",
             "kda_lin_chunk_fwd", "kda_lin_chunk_fwd_bounded", "kda_lin_chunk_fwd_workspace_bytes",
             "kda_lin_recurrent_step",
-            "kda_paged_append", "kda_paged_attention", "kda_paged_attention_workspace_bytes")
+            "kda_paged_append", "kda_paged_attention", "kda_paged_attention_workspace_bytes",
+            "kda_recurrent_tree", "kda_recurrent_tree_qknorm", "kda_recurrent_tree_commit",
+            "kda_recurrent_tree_commit_qknorm", "kda_paged_tree_attention",
+            "kda_paged_tree_attention_workspace_bytes", "kda_paged_tree_commit", "kda_paged_fork",
+            "kda_paged_compact", "kda_paged_copy")
+TREE_TOKENS = 64   # drafted tokens of a row, at most (KDA_TREE_TOKENS)
 
 
 class KdaDims(ctypes.Structure):
@@ -126,6 +131,21 @@ def lib() -> ctypes.CDLL:
         L.kda_paged_attention.argtypes = [vp] * 5 + [ctypes.c_float] + [vp] * 3 + [ctypes.c_size_t, pp, vp]
         L.kda_paged_attention_workspace_bytes.restype = ctypes.c_size_t
         L.kda_paged_attention_workspace_bytes.argtypes = [pp]
+        i32, f32, sz = ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+        for name, args in (
+                ("kda_recurrent_tree", [vp] * 9 + [vp, dp, vp]),
+                ("kda_recurrent_tree_qknorm", [vp] * 5 + [f32] + [vp] * 5 + [dp, vp]),
+                ("kda_recurrent_tree_commit", [vp] * 9 + [dp, vp]),
+                ("kda_recurrent_tree_commit_qknorm", [vp] * 4 + [f32] + [vp] * 5 + [dp, vp]),
+                ("kda_paged_tree_attention", [vp] * 7 + [i32, f32] + [vp] * 3 + [sz, pp, vp]),
+                ("kda_paged_tree_commit", [vp] * 7 + [i32, vp, pp, vp]),
+                ("kda_paged_fork", [vp] * 10 + [pp, vp]),
+                ("kda_paged_compact", [vp] * 5 + [pp, vp]),
+                ("kda_paged_copy", [vp] * 3 + [ctypes.c_int64, pp, vp])):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = args
+        L.kda_paged_tree_attention_workspace_bytes.restype = sz
+        L.kda_paged_tree_attention_workspace_bytes.argtypes = [i32, pp]
         L.kda_status_string.restype = ctypes.c_char_p
         L.kda_status_string.argtypes = [ctypes.c_int]
         _lib = L
@@ -517,7 +537,10 @@ def _bound():
     loader.exec_module(mod)
     mod.bind(_raise_status, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
         L.kda_lin_chunk_fwd, L.kda_lin_chunk_fwd_workspace_bytes, L.kda_lin_recurrent_step, L.kda_paged_append,
-        L.kda_paged_attention, L.kda_paged_attention_workspace_bytes)))
+        L.kda_paged_attention, L.kda_paged_attention_workspace_bytes, L.kda_recurrent_tree, L.kda_recurrent_tree_qknorm,
+        L.kda_recurrent_tree_commit, L.kda_recurrent_tree_commit_qknorm, L.kda_paged_tree_attention,
+        L.kda_paged_tree_attention_workspace_bytes, L.kda_paged_tree_commit, L.kda_paged_fork, L.kda_paged_compact,
+        L.kda_paged_copy)))
     _binding = mod
     return mod
 
@@ -620,3 +643,92 @@ def kda_paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, *, ou
     """
     return (_binding or _bound()).attend(q, k_cache, v_cache, block_table, seq_lens, scale, out, lse, output_lse,
                                          workspace, _handle(stream))
+
+
+# ---------------------------------------------------------------------------------------------
+# Branching decode: a tree of drafted tokens per row, the accepted path kept, rows that fork and end.
+#
+# parents: int32 [N, T], the drafted token that each one continues (an earlier one, or -1: the row itself), or
+# None (a single line); num_tokens: int32 [N] drafted tokens of each row, or None (all T); accepted: int32
+# [N], the last token of the path that is kept, or -1.  T is at most TREE_TOKENS.
+
+def kda_recurrent_tree(q, k, v, g, beta, state, parents=None, state_indices=None, num_tokens=None, *, out=None,
+                       stream=None, qk_eps: float | None = None):
+    """KDA outputs of every drafted token, each from the state behind the token that it continues; the states are
+    left as they are (kda_recurrent_tree_commit brings the accepted path into them).
+
+    q, k, g: [N, T, H, dk]; v: [N, T, H, dv]; beta: [N, T, H]; state: fp32 [P, H, dk, dv]; state_indices: int32
+    [N] or None.  Returns out [N, T, H, dv], zero for tokens past a row's count and rows outside the pool.
+    qk_eps: when given, kda_recurrent_tree_qknorm (q and k L2-normalised first).
+    """
+    return (_binding or _bound()).tree(q, k, v, g, beta, state, parents, state_indices, num_tokens, out, qk_eps, _handle(stream))
+
+
+def kda_recurrent_tree_commit(k, v, g, beta, state, parents, accepted, state_indices=None, num_tokens=None, *,
+                              stream=None, qk_eps: float | None = None):
+    """Bring each row's accepted path into its state, in place.  Arguments as in kda_recurrent_tree."""
+    (_binding or _bound()).replay(k, v, g, beta, state, parents, accepted, state_indices, num_tokens, qk_eps, _handle(stream))
+
+
+def kda_paged_tree_attention_workspace_bytes(q, k_cache, block_table) -> int:
+    """Bytes of device workspace kda_paged_tree_attention needs for these shapes (q: [N, T, Hq, d])."""
+    pages, page_size, Hkv, d = k_cache.shape
+    dims = KdaPagedDims(q.shape[0], q.shape[2], Hkv, d, pages, page_size, block_table.shape[1], _dtype_code(q.dtype))
+    return int(lib().kda_paged_tree_attention_workspace_bytes(q.shape[1], ctypes.byref(dims)))
+
+
+def kda_paged_tree_attention(q, k_cache, v_cache, block_table, seq_lens, parents, scale, num_tokens=None, *, out=None,
+                             lse=None, output_lse: bool = True, workspace=None, stream=None):
+    """Softmax attention of each row's drafted tokens over its cached tokens and the path to themselves.
+
+    q: [N, T, Hq, d]; k_cache, v_cache: [pages, page_size, Hkv, d] with Hkv a divisor of Hq; block_table: int32 [N,
+    max_pages]; seq_lens: int32 [N], the tokens cached before the draft (drafted token j of row n is at position
+    seq_lens[n] + j: kda_paged_append with positions=seq_lens); scale: multiplies q . k.
+    workspace: uint8 tensor of kda_paged_tree_attention_workspace_bytes bytes (allocated here when None).
+    Returns (out [N, T, Hq, d], lse fp32 [N, T, Hq] or None); 0 and -infinity for tokens past a row's count.
+    """
+    return (_binding or _bound()).tree_attend(q, k_cache, v_cache, block_table, seq_lens, parents, scale, num_tokens, out, lse,
+                                              output_lse, workspace, _handle(stream))
+
+
+def kda_paged_tree_commit(k_cache, v_cache, block_table, seq_lens, parents, accepted, num_tokens=None, *,
+                          tokens: int = TREE_TOKENS, new_lens=None, stream=None):
+    """Move the accepted path's keys and values to the end of each row's cached tokens, in place.
+
+    seq_lens: int32 [N], the lengths before the draft; tokens: the draft's width where parents is None.
+    Returns new_lens, int32 [N]: the lengths with the accepted tokens.  A stack calls it for the cache
+    of each layer with the same seq_lens.
+    """
+    return (_binding or _bound()).keep(k_cache, v_cache, block_table, seq_lens, parents, accepted, num_tokens, tokens, new_lens,
+                                       _handle(stream))
+
+
+def kda_paged_fork(block_table, seq_lens, page_refs, sources, new_tokens=None, *, page_size: int, new_table=None,
+                   new_lens=None, new_refs=None, copies=None, short_of=None, stream=None):
+    """Fork, reorder, end and extend rows: row n of the new table continues row sources[n] of the old one (-1: it
+    is empty), sharing its full pages; a partly filled last page that others hold too is copied.
+
+    block_table: int32 [N, max_pages], -1 where a row has no page; seq_lens, sources: int32 [N]; page_refs: int32
+    [pages], how many entries name each page (0: free); new_tokens: int32 [N] or None, the tokens that each row
+    gets room for behind its length.
+    Returns (new_table, new_lens, new_refs, copies int32 [N, 2], short_of int32 [1]): kda_paged_copy carries the
+    copies out in each layer's cache; short_of > 0 is the number of free pages that were missing, and
+    then nothing has changed.
+    """
+    return (_binding or _bound()).fork(block_table, seq_lens, page_refs, sources, new_tokens, page_size, new_table, new_lens,
+                                       new_refs, copies, short_of, _handle(stream))
+
+
+def kda_paged_compact(block_table, page_refs, *, new_table=None, new_refs=None, copies=None, stream=None):
+    """Close the gaps of a pool: its pages in use become the first ones.
+
+    Returns (new_table, new_refs, copies int32 [pages // 2, 2]); kda_paged_copy carries the copies out in each
+    layer's cache.  block_table has to hold every entry that page_refs counts.
+    """
+    return (_binding or _bound()).compact(block_table, page_refs, new_table, new_refs, copies, _handle(stream))
+
+
+def kda_paged_copy(k_cache, v_cache, copies, *, stream=None):
+    """Copy pages within a cache, in place: for each pair of copies, int32 [M, 2], page pair[1] becomes page
+    pair[0]'s copy.  Pairs with a page outside the pool (-1) are skipped."""
+    (_binding or _bound()).copy(k_cache, v_cache, copies, _handle(stream))

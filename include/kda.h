@@ -388,7 +388,7 @@ kda_status_t kda_recurrent_steps_qknorm(const void *q, const void *k, const void
 
 /* kda_device_status -- waits for the work queued on `stream` to finish, then reads and
  * clears the current device's count of device-side waits of the tensor-core chunk kernels
- * that gave up (see kda_chunk_fwd_bounded and kda_lin_chunk_fwd_bounded; the two passes of
+ * that gave up (see kda_chunk_fwd_bounded, kda_lin_chunk_fwd_bounded and kda_paged_tree_attention_bounded; the two passes of
  * kda_chunk_fwd_ws count theirs too) and its word of failed debug-build input checks.  Returns
  * KDA_ERR_INPUT when a check failed since the previous call on this device (only a library
  * built with debug checks makes any), else KDA_ERR_TIMEOUT when at least one wait gave up,
@@ -650,6 +650,17 @@ kda_status_t kda_paged_tree_attention(const void *q, const void *k_cache, const 
                                       const int32_t *num_tokens, int32_t tokens, float scale, void *out, float *lse,
                                       void *workspace, size_t workspace_bytes, const kda_paged_dims_t *dims,
                                       cudaStream_t stream);
+
+/* kda_paged_tree_attention_bounded -- kda_paged_tree_attention with an explicit bound on every device-side wait of the
+ * tensor-core kernel (bf16), as in kda_lin_chunk_fwd_bounded: when one gives up, the CTA lets what is in flight land
+ * (bounded separately), its share's outputs and lse become NaN, and kda_device_status reports KDA_ERR_TIMEOUT.
+ * wait_polls = 0 makes every wait give up at once: a test of that path.  fp32 calls have no such waits. */
+kda_status_t kda_paged_tree_attention_bounded(const void *q, const void *k_cache, const void *v_cache,
+                                              const int32_t *block_table, const int32_t *seq_lens,
+                                              const int32_t *parents, const int32_t *num_tokens, int32_t tokens,
+                                              float scale, void *out, float *lse, void *workspace,
+                                              size_t workspace_bytes, uint32_t wait_polls,
+                                              const kda_paged_dims_t *dims, cudaStream_t stream);
 
 /* Bytes of workspace kda_paged_tree_attention needs (host arithmetic only; 0 for arguments that it refuses). */
 size_t kda_paged_tree_attention_workspace_bytes(int32_t tokens, const kda_paged_dims_t *dims);

@@ -6,6 +6,7 @@
 
 #include "kda_internal.h"
 #include "kda_lin.h"
+#include "kda_tree.h"
 
 namespace {
 
@@ -63,13 +64,13 @@ extern "C" const char *kda_status_string(kda_status_t s) {
 }
 
 extern "C" kda_status_t kda_device_status(cudaStream_t stream) {
-    unsigned int n1 = 0, n2 = 0, n3 = 0, n4 = 0, bad = 0;
+    unsigned int n1 = 0, n2 = 0, n3 = 0, n4 = 0, n5 = 0, bad = 0;
     if (kda::take_wait_expiries(stream, &n1) != cudaSuccess || kda::take_prep_expiries(stream, &n2) != cudaSuccess ||
         kda::take_state_expiries(stream, &n3) != cudaSuccess || kda::take_lin_expiries(stream, &n4) != cudaSuccess ||
-        kda::take_input_errors(stream, &bad) != cudaSuccess)
+        kda::take_tree_expiries(stream, &n5) != cudaSuccess || kda::take_input_errors(stream, &bad) != cudaSuccess)
         return KDA_ERR_CUDA;
     if (bad) return KDA_ERR_INPUT;
-    return (n1 || n2 || n3 || n4) ? KDA_ERR_TIMEOUT : KDA_OK;
+    return (n1 || n2 || n3 || n4 || n5) ? KDA_ERR_TIMEOUT : KDA_OK;
 }
 
 extern "C" int kda_debug_checks(void) { return kda::debug_checks_built(); }

@@ -17,17 +17,12 @@ template <int D> struct Simt {
 };
 
 __device__ __forceinline__ float4 load4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-    const float2 x = ptx::unpack_bf16(u.x), y = ptx::unpack_bf16(u.y);
-    return make_float4(x.x, x.y, y.x, y.y);
-}
 __device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(ptx::pack_bf16(v.x, v.y), ptx::pack_bf16(v.z, v.w));
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2) kda_paged_tree_attention_kernel(const TreeAtt a) {
     using S = Simt<D>;
     constexpr int CH = D / 4, RPT = kThreads / CH, LD = kKt / RPT;   // 16-byte chunks of a key, keys per step, steps of a tile
@@ -41,7 +36,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_paged_tree_attention_kernel(c
 
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const PagedArgs &p = a.t.p;
-    tree_clear<T, D, kThreads>(a, gridDim.x);
+    tree_clear<float, D, kThreads>(a, gridDim.x);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long W = tree_total<kThreads>(a, sm_sum);
     const long long G = W < gridDim.x ? W : gridDim.x;
@@ -55,7 +50,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_paged_tree_attention_kernel(c
     us += unit * row.items;
 
     const float sc = p.scale * kLog2e;
-    const T *kc = static_cast<const T *>(p.k_cache), *vc = static_cast<const T *>(p.v_cache);
+    const float *kc = static_cast<const float *>(p.k_cache), *vc = static_cast<const float *>(p.v_cache);
     for (bool first = true;; first = false) {
         const int hk = unit / row.blocks, r0 = (unit - hk * row.blocks) * kRb;
         const int rows = row.m * a.rep - r0 < kRb ? row.m * a.rep - r0 : kRb;
@@ -75,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_paged_tree_attention_kernel(c
             const int r = c / CH, ch = c % CH;
             int i;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < rows) v = load4(static_cast<const T *>(p.q) + q_row(r, i) * D + 4 * ch);
+            if (r < rows) v = load4(static_cast<const float *>(p.q) + q_row(r, i) * D + 4 * ch);
             *reinterpret_cast<float4 *>(sq + r * S::QS + 4 * ch) = v;
         }
         auto locate = [&](int t) {   // places of tile t's keys (one warp)
@@ -197,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_paged_tree_attention_kernel(c
 #pragma unroll
                 for (int c = 0; c < OC; ++c) {
                     const float4 y = l[r] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv);
-                    store4(static_cast<T *>(p.out) + to * D + 64 * c + 4 * tx, y);
+                    store4(static_cast<float *>(p.out) + to * D + 64 * c + 4 * tx, y);
                 }
                 if (p.lse && tx == 0) p.lse[to] = l[r] == 0.f ? -INFINITY : (mx[r] + log2f(l[r])) * kLn2;
             } else {
@@ -284,13 +279,13 @@ __global__ void __launch_bounds__(kJoinThreads) kda_paged_tree_join_kernel(const
     }
 }
 
-template <typename T, int D> cudaError_t launch_simt(const TreeAtt &a, kda_dtype_t dt, int ctas, cudaStream_t st) {
+template <int D> cudaError_t launch_simt(const TreeAtt &a, int ctas, cudaStream_t st) {
     constexpr int smem = Simt<D>::FLOATS * 4;
-    cudaError_t e = cudaFuncSetAttribute(kda_paged_tree_attention_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(kda_paged_tree_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kda_paged_tree_attention_kernel<T, D><<<ctas, kThreads, smem, st>>>(a);
+    kda_paged_tree_attention_kernel<D><<<ctas, kThreads, smem, st>>>(a);
     e = cudaGetLastError();
-    return e != cudaSuccess || ctas == 1 ? e : launch_tree_join(a, D, dt, ctas, st);   // (one CTA: nothing is split)
+    return e != cudaSuccess || ctas == 1 ? e : launch_tree_join(a, D, KDA_F32, ctas, st);   // (one CTA: nothing is split)
 }
 
 // CTAs of the kernel: never more than there can be items.
@@ -319,17 +314,18 @@ cudaError_t launch_tree_join(const TreeAtt &a, int d, kda_dtype_t dt, int ctas, 
     return d == 128 ? cudaLaunchKernelEx(&cfg, kda_paged_tree_join_kernel<__nv_bfloat16, 128>, a, ctas) : cudaLaunchKernelEx(&cfg, kda_paged_tree_join_kernel<__nv_bfloat16, 64>, a, ctas);
 }
 
-size_t paged_tree_workspace_bytes(const PagedTreeArgs &t, int d, kda_dtype_t) {
+size_t paged_tree_workspace_bytes(const PagedTreeArgs &t, int d, kda_dtype_t dt) {
     if (t.p.rows <= 0) return 0;
+    if (dt == KDA_BF16) return tree_tc_workspace_bytes(t, d);
     return (size_t)simt_ctas(t) * 2 * kRb * (d + 2) * 4;
 }
 
-cudaError_t launch_paged_tree(const PagedTreeArgs &t, int d, kda_dtype_t dt, void *workspace, cudaStream_t st) {
+cudaError_t launch_paged_tree(const PagedTreeArgs &t, int d, kda_dtype_t dt, void *workspace, uint32_t polls, cudaStream_t st) {
+    if (dt == KDA_BF16) return launch_tree_tc(t, d, workspace, polls, st);
     const int rep = t.p.heads / t.p.kv_heads, ctas = simt_ctas(t);
     float *ws = static_cast<float *>(workspace);
     const TreeAtt a{t, FastDiv((uint32_t)t.p.page_size), FastDiv((uint32_t)rep), rep, kRb, kKt, ws, ws + (size_t)ctas * 2 * kRb * d};
-    if (dt == KDA_BF16) return d == 128 ? launch_simt<__nv_bfloat16, 128>(a, dt, ctas, st) : launch_simt<__nv_bfloat16, 64>(a, dt, ctas, st);
-    return d == 128 ? launch_simt<float, 128>(a, dt, ctas, st) : launch_simt<float, 64>(a, dt, ctas, st);
+    return d == 128 ? launch_simt<128>(a, ctas, st) : launch_simt<64>(a, ctas, st);
 }
 
 }  // namespace kda

@@ -52,7 +52,10 @@ struct ForkArgs {
 cudaError_t launch_recurrent_tree(const TreeArgs &a, int dk, int dv, kda_dtype_t dt, cudaStream_t st);
 cudaError_t launch_recurrent_tree_commit(const TreeArgs &a, int dk, int dv, kda_dtype_t dt, cudaStream_t st);
 size_t paged_tree_workspace_bytes(const PagedTreeArgs &a, int d, kda_dtype_t dt);
-cudaError_t launch_paged_tree(const PagedTreeArgs &a, int d, kda_dtype_t dt, void *workspace, cudaStream_t st);
+// polls: bound on each device wait of the tensor-core kernel (bf16)
+cudaError_t launch_paged_tree(const PagedTreeArgs &a, int d, kda_dtype_t dt, void *workspace, uint32_t polls, cudaStream_t st);
+// Waits for `st`, then reads and clears the count of expired bounded waits of that kernel.
+cudaError_t take_tree_expiries(cudaStream_t st, unsigned int *count);
 cudaError_t launch_tree_commit(const TreeCommitArgs &a, cudaStream_t st);
 cudaError_t launch_fork(const ForkArgs &a, cudaStream_t st);
 cudaError_t launch_compact(const ForkArgs &a, cudaStream_t st);

@@ -114,11 +114,12 @@ extern "C" size_t kda_paged_tree_attention_workspace_bytes(int32_t tokens, const
     return kda::paged_tree_workspace_bytes(attention_args(tokens, d), d->head_dim, d->dtype);
 }
 
-extern "C" kda_status_t kda_paged_tree_attention(const void *q, const void *k_cache, const void *v_cache,
-                                                 const int32_t *block_table, const int32_t *seq_lens,
-                                                 const int32_t *parents, const int32_t *num_tokens, int32_t tokens,
-                                                 float scale, void *out, float *lse, void *workspace,
-                                                 size_t workspace_bytes, const kda_paged_dims_t *d, cudaStream_t stream) {
+extern "C" kda_status_t kda_paged_tree_attention_bounded(const void *q, const void *k_cache, const void *v_cache,
+                                                         const int32_t *block_table, const int32_t *seq_lens,
+                                                         const int32_t *parents, const int32_t *num_tokens, int32_t tokens,
+                                                         float scale, void *out, float *lse, void *workspace,
+                                                         size_t workspace_bytes, uint32_t wait_polls,
+                                                         const kda_paged_dims_t *d, cudaStream_t stream) {
     const kda_status_t st = check_attention_dims(tokens, d);
     if (st != KDA_OK) return st;
     if (!std::isfinite(scale)) return KDA_ERR_SHAPE;
@@ -140,7 +141,16 @@ extern "C" kda_status_t kda_paged_tree_attention(const void *q, const void *k_ca
     a.p.q = q, a.p.k_cache = k_cache, a.p.v_cache = v_cache, a.p.table = block_table, a.p.lens = seq_lens;
     a.p.out = out, a.p.lse = lse, a.p.scale = scale;
     a.parents = parents, a.num = num_tokens;
-    return kda::launch_paged_tree(a, d->head_dim, d->dtype, workspace, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return kda::launch_paged_tree(a, d->head_dim, d->dtype, workspace, wait_polls, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" kda_status_t kda_paged_tree_attention(const void *q, const void *k_cache, const void *v_cache,
+                                                 const int32_t *block_table, const int32_t *seq_lens,
+                                                 const int32_t *parents, const int32_t *num_tokens, int32_t tokens,
+                                                 float scale, void *out, float *lse, void *workspace,
+                                                 size_t workspace_bytes, const kda_paged_dims_t *d, cudaStream_t stream) {
+    return kda_paged_tree_attention_bounded(q, k_cache, v_cache, block_table, seq_lens, parents, num_tokens, tokens, scale, out, lse,
+                                            workspace, workspace_bytes, 1u << 20, d, stream);
 }
 
 extern "C" kda_status_t kda_paged_tree_commit(void *k_cache, void *v_cache, const int32_t *block_table,

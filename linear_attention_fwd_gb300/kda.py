@@ -37,7 +37,7 @@ EXPORTED = ("kda_chunk_fwd", "kda_chunk_fwd_with", "kda_chunk_fwd_bounded", "kda
             "kda_paged_append", "kda_paged_attention", "kda_paged_attention_workspace_bytes",
             "kda_recurrent_tree", "kda_recurrent_tree_qknorm", "kda_recurrent_tree_commit",
             "kda_recurrent_tree_commit_qknorm", "kda_paged_tree_attention",
-            "kda_paged_tree_attention_workspace_bytes", "kda_paged_tree_commit", "kda_paged_fork",
+            "kda_paged_tree_attention_bounded", "kda_paged_tree_attention_workspace_bytes", "kda_paged_tree_commit", "kda_paged_fork",
             "kda_paged_compact", "kda_paged_copy")
 TREE_TOKENS = 64   # drafted tokens of a row, at most (KDA_TREE_TOKENS)
 
@@ -138,6 +138,7 @@ def lib() -> ctypes.CDLL:
                 ("kda_recurrent_tree_commit", [vp] * 9 + [dp, vp]),
                 ("kda_recurrent_tree_commit_qknorm", [vp] * 4 + [f32] + [vp] * 5 + [dp, vp]),
                 ("kda_paged_tree_attention", [vp] * 7 + [i32, f32] + [vp] * 3 + [sz, pp, vp]),
+                ("kda_paged_tree_attention_bounded", [vp] * 7 + [i32, f32] + [vp] * 3 + [sz, ctypes.c_uint32, pp, vp]),
                 ("kda_paged_tree_commit", [vp] * 7 + [i32, vp, pp, vp]),
                 ("kda_paged_fork", [vp] * 10 + [pp, vp]),
                 ("kda_paged_compact", [vp] * 5 + [pp, vp]),
@@ -689,6 +690,33 @@ def kda_paged_tree_attention(q, k_cache, v_cache, block_table, seq_lens, parents
     """
     return (_binding or _bound()).tree_attend(q, k_cache, v_cache, block_table, seq_lens, parents, scale, num_tokens, out, lse,
                                               output_lse, workspace, _handle(stream))
+
+
+def kda_paged_tree_attention_bounded(q, k_cache, v_cache, block_table, seq_lens, parents, scale, num_tokens, out, lse,
+                                     workspace, wait_polls: int, stream=None):
+    """kda_paged_tree_attention with an explicit bound on the kernel's device-side waits.  Every tensor is the caller's
+    (parents, num_tokens, lse and workspace may be None)."""
+    dev = q.device
+    for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("out", out)):
+        _check_dev(name, t, dev, q.dtype)
+    for name, t in (("block_table", block_table), ("seq_lens", seq_lens), ("parents", parents), ("num_tokens", num_tokens)):
+        _check_dev(name, t, dev, torch.int32)
+    _check_dev("lse", lse, dev, torch.float32)
+    _check_dev("workspace", workspace, dev, torch.uint8)
+    N, T, Hq, d = q.shape
+    pages, page_size, Hkv = k_cache.shape[:3]
+    if k_cache.shape[3] != d or v_cache.shape != k_cache.shape or out.shape != q.shape or block_table.shape[0] != N \
+            or seq_lens.shape != (N,) or (parents is not None and parents.shape != (N, T)) \
+            or (num_tokens is not None and num_tokens.shape != (N,)) or (lse is not None and lse.shape != (N, T, Hq)):
+        raise ValueError("inconsistent shapes")
+    dims = KdaPagedDims(N, Hq, Hkv, d, pages, page_size, block_table.shape[1], _dtype_code(q.dtype))
+    st = lib().kda_paged_tree_attention_bounded(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
+                                                _ptr(parents), _ptr(num_tokens), T, float(scale), _ptr(out), _ptr(lse),
+                                                _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                                int(wait_polls), ctypes.byref(dims), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_paged_tree_attention_bounded")
+    return out, lse
 
 
 def kda_paged_tree_commit(k_cache, v_cache, block_table, seq_lens, parents, accepted, num_tokens=None, *,

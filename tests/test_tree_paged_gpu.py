@@ -227,6 +227,25 @@ def test_captured(K):
         assert lens.tolist() == [x + len(R.path(p, i)) for x, p, i in zip(ls, rows, (6, 2))]
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_every_wait_giving_up(K, d):
+    """wait_polls = 0: all results are NaN, the status says so, and the next call is right."""
+    c = cache(30, [600, 0, 3000], 9, 8, 2, d, 16, BF16)
+    rows, parents = R.drafts(30, 3, 9)
+    need = K.kda_paged_tree_attention_workspace_bytes(c["q"], c["k_cache"], c["block_table"])
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    out, lse = torch.zeros_like(c["q"]), torch.zeros(3, 9, 8, device="cuda")
+    a = [c[x] for x in ("q", "k_cache", "v_cache", "block_table", "seq_lens")]
+    assert K.kda_device_status() == K.KDA_OK
+    K.kda_paged_tree_attention_bounded(*a, parents, c["scale"], None, out, lse, ws, 0)
+    torch.cuda.synchronize()
+    assert bool(out.isnan().all()) and bool(lse.isnan().all())
+    assert K.kda_device_status() == K.KDA_ERR_TIMEOUT
+    assert K.kda_device_status() == K.KDA_OK
+    run(K, c, rows, parents, workspace=ws)
+    assert K.kda_device_status() == K.KDA_OK
+
+
 # ------------------------------------------------------------------ the accepted path
 def committed(c, rows, accepted):
     """The caches and lengths after the call, by indexing."""

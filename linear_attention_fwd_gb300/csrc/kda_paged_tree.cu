@@ -8,7 +8,7 @@ namespace {
 // 256 threads take a block of 64 query rows and tiles of 32 keys in fp32 arithmetic: a thread has 4 rows x 2 keys of
 // the scores and 4 rows x D / 16 channels of the outputs, both from shared memory in 16-byte reads; a row's maximum, sum
 // and weights stay within the half warp that has the row.  The next tile is on its way in registers meanwhile.
-constexpr int kThreads = 256, kRb = 64, kKt = 32;
+constexpr int kThreads = 256, kRb = 64, kKt = 32, kStart = 1;
 constexpr int kSimtCtas = 2 * kSms;
 
 template <int D> struct Simt {
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_paged_tree_attention_kernel(c
         const int rows = row.m * a.rep - r0 < kRb ? row.m * a.rep - r0 : kRb;
         const long long xe = us + row.items < x1 ? us + row.items : x1;
         const bool whole = x == us && xe == us + row.items;
-        const int ia = (int)(x - us) - kTreeStart, ib = (int)(xe - us) - kTreeStart;
+        const int ia = (int)(x - us) - a.start, ib = (int)(xe - us) - a.start;
         const int ta = ia > 0 ? ia : 0, tb = ib;   // this share's tiles
         const int32_t *table = p.table + (int64_t)n * p.max_pages;
         // query row r: token i, head g of the group
@@ -324,7 +324,7 @@ cudaError_t launch_paged_tree(const PagedTreeArgs &t, int d, kda_dtype_t dt, voi
     if (dt == KDA_BF16) return launch_tree_tc(t, d, workspace, polls, st);
     const int rep = t.p.heads / t.p.kv_heads, ctas = simt_ctas(t);
     float *ws = static_cast<float *>(workspace);
-    const TreeAtt a{t, FastDiv((uint32_t)t.p.page_size), FastDiv((uint32_t)rep), rep, kRb, kKt, ws, ws + (size_t)ctas * 2 * kRb * d};
+    const TreeAtt a{t, FastDiv((uint32_t)t.p.page_size), FastDiv((uint32_t)rep), rep, kRb, kKt, kStart, ws, ws + (size_t)ctas * 2 * kRb * d};
     return d == 128 ? launch_simt<128>(a, ctas, st) : launch_simt<64>(a, ctas, st);
 }
 

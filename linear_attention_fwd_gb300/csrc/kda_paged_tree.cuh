@@ -2,7 +2,7 @@
 //
 // A unit is a row's key/value head with a block of up to RB of its query rows (drafted token x query head of the
 // group, token-major).  Its items are its tiles of cached tokens, its tiles of drafted tokens and, ahead of them,
-// kTreeStart that stand for the time a unit's start takes.  The items of all units, in order, are cut into equal
+// `start` that stand for the time a unit's start takes.  The items of all units, in order, are cut into equal
 // shares, one per CTA; each CTA finds its share from seq_lens and num_tokens on the device.  A unit in
 // several shares leaves one partial (maximum, sum, unnormalised output) per share in the workspace,
 // and a second kernel joins them in a fixed order, so that results do not depend on timing.
@@ -13,12 +13,11 @@
 
 namespace kda {
 
-constexpr int kTreeStart = 1;   // a unit's start, in tiles
-
 struct TreeAtt {
     PagedTreeArgs t;
     FastDiv by_page, by_rep;
     int32_t rep, rb, kt;       // query heads per key/value head, query rows per block, keys per tile
+    int32_t start;             // a unit's start, in tiles
     float *part_o, *part_ml;   // partials: [2 ctas][rb][D], [2 ctas][rb][2]
 };
 
@@ -33,7 +32,7 @@ __device__ __forceinline__ TreeRow tree_row(const TreeAtt &a, int n) {
     r.ctx = (r.len + a.kt - 1) / a.kt;
     r.tiles = r.ctx + (r.m + a.kt - 1) / a.kt;
     r.blocks = (r.m * a.rep + a.rb - 1) / a.rb;
-    r.items = kTreeStart + r.tiles;
+    r.items = a.start + r.tiles;
     return r;
 }
 __device__ __forceinline__ long long tree_items(const TreeAtt &a, int n) {   // of all its units

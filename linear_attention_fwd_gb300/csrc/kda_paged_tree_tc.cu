@@ -1,25 +1,26 @@
 // Attention of a draft's tokens over a paged cache on the sm_103a tensor cores (tcgen05 + TMEM + TMA), bf16.
 //
-// A unit has up to 256 query rows (drafted token x query head) of a row's key/value head; a CTA walks tiles of 128 keys
-// with two chains of products, each with its scores and its outputs in tensor memory:
+// A unit has up to 256 query rows (drafted token x query head) of a row's key/value head; a CTA walks tiles of 64 keys
+// with two chains of products, each with its outputs and two buffers of scores in tensor memory:
 //   S = Q K^T (M = query rows, N = keys),   P = 2^(sc S - m) by the chain's warpgroup, a query row per thread,
-//   O += P V, P from tensor memory as a rounded bf16 and the rounded rest (16 bits: one rounding alone would cost
+//   O += P V, P from tensor memory as the upper half of its bits and the rounded rest (16 bits: bf16 alone would cost
 //   2^-9 per weight, as much as the outputs' own rounding), V read across its rows.
 // With more than 128 query rows the chains have 128 of them each and share the tiles; with fewer both have the same
 // rows and take every second tile, and are joined at the end (a row's outputs of both chains lie in the same
-// lane of tensor memory).  So one chain's softmax runs beside the other's products in either case.
+// lane of tensor memory).  A chain's next scores are made while its softmax runs, so that the softmax waits for
+// nothing but a tile's arrival.
 // m follows the running maximum only where that has grown by more than 2^8, which is rare after the first
-// tiles: then the chain's warpgroup scales O in tensor memory (its scores being there says that the
-// product before has ended).
+// tiles: then the chain's warpgroup waits for the last product into O and scales it in tensor memory.
 //
-// Keys and values are gathered by TMA, four rows of the cache (page, offset, head) an instruction, so that pages
-// of any size fit; places without a token (past the length, pages outside the pool) are rows past
-// the tensor and arrive as zeros, and their scores are masked.  The drafted tokens have a tile of their own, masked
-// by their paths.  A non-finite value among them is replaced by zero before the product (zero times NaN
-// would reach other branches) and put back as NaN in the outputs of the tokens that weigh it.
+// Tiles that lie whole on pages of a multiple of 8 tokens come by TMA, a box of tokens an instruction; others (the last
+// cached tokens, pages of other sizes, places without a token, which become zeros and whose scores are masked)
+// by cp.async of three warps.  (Gathers of four rows by TMA take 50 ns each, 6.5 us for 128 keys of 128
+// channels: 131,071 tokens x 8 heads, 512 query rows: 700 us, 430 by boxes.)  The drafted tokens have a tile of their own,
+// masked by their paths.  A non-finite value among them is replaced by zero before the product (zero
+// times NaN would reach other branches) and put back as NaN in the outputs of the tokens that weigh it.
 //
-// Roles: warps 0-3 and 4-7 the chains' softmax, warp 8 the loads, warp 9 the products (two more make up the warpgroup;
-// 2 x 208 + 88 registers a thread out of the 3 x 168 of the launch).  They meet at mbarriers with bounded waits.
+// Roles: warps 0-3 and 4-7 the chains' softmax, warps 8, 10 and 11 the loads, warp 9 the products.  They meet at
+// mbarriers with bounded waits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -35,22 +36,25 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 384, kRb = 256, kKt = 128;
-constexpr int kRegsChain = 208, kRegsRest = 88;
+constexpr int kThreads = 384, kRb = 256, kKt = 64, kStart = 3;
 constexpr float kSlack = 8.f;   // growth of the maximum, in powers of two, that m does not follow
+constexpr int kLoaders = 3;     // warps
 
 template <int D> struct Tc {
-    static constexpr uint32_t TILE = kKt * D * 2;                 // a tile of keys, of values, or of 128 query rows
-    static constexpr int STAGES = D == 128 ? 4 : 8;
-    static constexpr uint32_t Q = 0, RING = 2 * TILE, MISC = RING + STAGES * TILE;
-    static constexpr uint32_t BAR = MISC, MASK = BAR + 256, ANC = MASK + 8 * 16, UP = ANC + 512, ML = UP + 256;
+    static constexpr uint32_t TILE = kKt * D * 2, QTILE = 128 * D * 2;   // keys or values; query rows of a chain
+    static constexpr int STAGES = D == 128 ? 9 : 16;
+    static constexpr uint32_t Q = 0, RING = 2 * QTILE, BAR = RING + STAGES * TILE;
+    static constexpr uint32_t MASK = BAR + 512, ANC = MASK + 32 * 8, UP = ANC + 512, ML = UP + 256;
     static constexpr uint32_t SEE = ML + 2 * 128 * 8, NF = SEE + 128 * 8, NFANY = NF + 2 * D * 8, TM = NFANY + 16;
     static constexpr uint32_t BYTES = TM + 16 + 1024;
     static_assert(BYTES <= 226 * 1024, "shared memory budget");
 };
-enum Bar { kFull = 0, kEmpty = 8, kQFull = 16, kQEmpty = 17, kS = 18 /* 2 */, kP = 20 /* 2 */, kO = 22 /* 2 */, kMeet = 24, kBars = 25 };
+// kS, kP and kV are of a chain and a buffer (2 k + b): scores, weights, outputs.  A wait names a phase by its parity, so a
+// barrier may be at most one phase behind what is waited for and none ahead.  That holds because the scores of a
+// chain's tile j follow the outputs of its tile j - 2, and those of tile j the weights that their waiter makes.
+enum Bar { kFull = 0, kEmpty = 16, kQFull = 32, kQEmpty = 33, kS = 34, kP = 38, kV = 42, kMeet = 46, kBars = 47 };
 
-constexpr uint32_t TM_S = 0, TM_O = 256;   // + 128 for the second chain
+constexpr uint32_t TM_S = 0, TM_O = 256;   // + 128 for the second chain, + 64 for the second buffer
 
 __device__ __forceinline__ bool wait_small(uint32_t bar, uint32_t parity, uint32_t limit) {
 #pragma unroll 1
@@ -58,27 +62,19 @@ __device__ __forceinline__ bool wait_small(uint32_t bar, uint32_t parity, uint32
         if (mbar_wait(bar, parity & 1u, 1)) return true;
     return false;
 }
+__device__ __forceinline__ bool test(uint32_t bar, uint32_t parity) {   // without waiting
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity & 1u)
+                 : "memory");
+    return done != 0;
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory"); }
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t one;
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(one));
     return one;
-}
-template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-// Four rows of a two-dimensional tensor, 64 elements from x on: 4 x 128 bytes, one behind the other.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, const int (&r)[4]) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&w)[32]) {
-    float v[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(w[i]);
-    tmem_st32(taddr, v);
 }
 
 // A CTA's share of the items, piece by piece (every role walks it by itself).
@@ -97,7 +93,7 @@ struct Walk {
         two = rows > 128;
         xe = us + row.items < x1 ? us + row.items : x1;
         whole = x == us && xe == us + row.items;
-        const int ia = (int)(x - us) - kTreeStart, ib = (int)(xe - us) - kTreeStart;
+        const int ia = (int)(x - us) - a.start, ib = (int)(xe - us) - a.start;
         ta = ia > 0 ? ia : 0;
         c = ib - ta > 0 ? ib - ta : 0;
     }
@@ -112,21 +108,23 @@ struct Walk {
         piece(a);
         return true;
     }
-    // Tiles of chain k, and the loads (counted within the piece) of tile i's keys and values: in the order of their use
+    // Chain k has jobs(k) tiles, the j-th is tile(k, j).  Scores are made `ahead` tiles ahead of the outputs; the loads of
+    // tile i's keys and values, counted within the piece, are in that order.
     __device__ __forceinline__ int jobs(int k) const { return two ? c : (c + 1 - k) / 2; }
     __device__ __forceinline__ int tile(int k, int j) const { return two ? j : 2 * j + k; }
-    __device__ __forceinline__ int k_load(int i) const { return two ? 2 * i : (i == 0 ? 0 : 2 * i - 1); }
-    __device__ __forceinline__ int v_load(int i) const { return two ? 2 * i + 1 : (i < c - 1 ? 2 * i + 2 : 2 * c - 1); }
+    __device__ __forceinline__ int ahead() const { return two ? 2 : 4; }
+    __device__ __forceinline__ int k_load(int i) const { return i < ahead() ? i : 2 * i + 1 - ahead(); }
+    __device__ __forceinline__ int v_load(int i) const { return i < c - ahead() ? 2 * i + ahead() : c + i; }
 };
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                         const TreeAtt a, const uint32_t polls) {
+kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const TreeAtt a, const int box,
+                         const uint32_t polls) {
     using L = Tc<D>;
     constexpr int S = L::STAGES, HALVES = D / 64;
-    constexpr uint32_t HALF = L::TILE / HALVES;            // 64 channels of a tile's rows
-    constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128), IDESC_PV = idesc_bf16_f32(128, D) | (1u << 16);   // B (V) MN-major
+    constexpr uint32_t HALF = L::TILE / HALVES, QHALF = L::QTILE / HALVES;   // 64 channels of a tile's rows
+    constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, kKt), IDESC_PV = idesc_bf16_f32(128, D) | (1u << 16);   // B (V) MN-major
     extern __shared__ uint8_t smem_raw[];
     __shared__ long long sm_sum[kThreads / 32];
     __shared__ int s_fail;
@@ -148,7 +146,6 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
     w.unit = (int)((w.x - w.us) / w.row.items);
     w.us += w.unit * w.row.items;
     w.piece(a);
-    const Walk start = w;
 
     auto bar = [&](int b) { return sb + L::BAR + 8 * b; };
     auto wait = [&](int b, uint32_t phase) { return wait_small(bar(b), phase, polls); };
@@ -158,18 +155,18 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
     if (tid == 0) {
         s_fail = 0;
         nf_any[0] = nf_any[1] = 0;
-        for (int s = 0; s < kQFull - kEmpty; ++s) {   // (also those past the stages: what gives up looks at all of them)
-            mbar_init(bar(kFull + s), 1);
+        for (int s = 0; s < 16; ++s) {             // (also those past the stages: what gives up looks at all of them)
+            mbar_init(bar(kFull + s), kLoaders);
             mbar_init(bar(kEmpty + s), 1);
         }
-        mbar_init(bar(kQFull), 1);
+        mbar_init(bar(kQFull), kLoaders);
         mbar_init(bar(kQEmpty), 1);
-        for (int k = 0; k < 2; ++k) {
-            mbar_init(bar(kS + k), 2);     // the product, and the thread that issued it (which has seen the tile's masks)
-            mbar_init(bar(kP + k), 4);     // the chain's warps
-            mbar_init(bar(kO + k), 1);
+        for (int x = 0; x < 4; ++x) {
+            mbar_init(bar(kS + x), 2);             // the product, and the thread that issued it (which has seen the tile's masks)
+            mbar_init(bar(kP + x), 4);             // the chain's warps
+            mbar_init(bar(kV + x), 1);
         }
-        mbar_init(bar(kMeet), 8);          // both chains' warps
+        mbar_init(bar(kMeet), 8);                  // both chains' warps
         fence_mbar_init();
     }
     for (int x = tid; x < 2 * D; x += kThreads) nf[x] = 0;
@@ -185,16 +182,16 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
 
     if (warp < 8) {
         // ---- softmax
-        regs_inc<kRegsChain>();
         const int k = warp >> 2, th = tid & 127;           // chain; query row of it
-        const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16), ts = trow + TM_S + 128 * k;
+        const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float sc = p.scale * kLog2e;
-        const uint32_t *masks = reinterpret_cast<const uint32_t *>(sm + L::MASK);
+        const float2 sc2 = make_float2(sc, sc);
+        const uint2 *masks = reinterpret_cast<const uint2 *>(sm + L::MASK);
         uint64_t *anc = reinterpret_cast<uint64_t *>(sm + L::ANC);
         float2 *ml = reinterpret_cast<float2 *>(sm + L::ML);
         uint64_t *sees = reinterpret_cast<uint64_t *>(sm + L::SEE);
-        uint32_t count = 0, ends = 0, tiles = 0, loads = 0, pieces = 0;   // phases so far
-        uint32_t meets = 0;
+        uint32_t count = 0, meets = 0, tiles = 0, loads = 0, pieces = 0;   // jobs, barriers, tiles, loads and pieces so far
+        auto outputs = [&] { return all(wait(kV + 2 * k + (int)((count - 1) & 1), (count - 1) >> 1)); };   // of the chain's last tile
         auto meet = [&] {   // all 256 threads of the chains
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kMeet));
@@ -214,30 +211,40 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
             float mr = -INFINITY, l = 0.f;
             const int jobs = w.jobs(k);
             for (int j = 0; j < jobs; ++j, ++count) {
-                const int i = w.tile(k, j);
+                const int i = w.tile(k, j), b = 2 * k + (int)(count & 1);
                 const bool draft = w.ta + i == w.row.ctx;
-                ok = all(wait(kS + k, count));
+                ok = all(wait(kS + b, count >> 1));
                 if (!ok) break;
                 tc_fence_after();
-                const uint4 mk = *reinterpret_cast<const uint4 *>(masks + 4 * ((tiles + i) & 7));
-                const bool open = !draft && (mk.x & mk.y & mk.z & mk.w) == 0xffffffffu;
-                const uint32_t mw[4] = {mk.x, mk.y, mk.z, mk.w};   // column 4 x + e: bit x of word e
-                auto in = [&](int col) {
-                    const bool here = (mw[col & 3] >> (col >> 2)) & 1u;
-                    return draft ? here && col < 64 && ((see >> (col & 63)) & 1u) : here;
-                };
-                float top = -INFINITY;
+                const uint32_t ts = trow + TM_S + 64 * b;
+                float v0[32], v1[32];
+                tmem_ld32x2(ts, ts + 32, v0, v1);
+                uint2 mk = masks[(tiles + i) & 31];
+                const bool open = !draft && (mk.x & mk.y) == 0xffffffffu;
+                if (!open) {
+                    if (draft) mk.x &= (uint32_t)see, mk.y &= (uint32_t)(see >> 32);
+                    const float no = sc >= 0.f ? -INFINITY : INFINITY;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float v[32];
-                    tmem_ld32(ts + 32 * q, v);
-                    if (open && sc >= 0.f) {
+                    for (int e = 0; e < 32; ++e) {
+                        v0[e] = (mk.x >> e) & 1u ? v0[e] : no;
+                        v1[e] = (mk.y >> e) & 1u ? v1[e] : no;
+                    }
+                }
+                float top;
+                {
+                    float x[4];
+                    if (sc >= 0.f) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e]);
+                        for (int e = 0; e < 4; ++e) x[e] = fmaxf(v0[e], v1[e]);
+#pragma unroll
+                        for (int e = 4; e < 32; ++e) x[e & 3] = fmaxf(fmaxf(x[e & 3], v0[e]), v1[e]);
+                        top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (open || in(32 * q + e)) top = fmaxf(top, sc >= 0.f ? v[e] : -v[e]);
+                        for (int e = 0; e < 4; ++e) x[e] = fminf(v0[e], v1[e]);
+#pragma unroll
+                        for (int e = 4; e < 32; ++e) x[e & 3] = fminf(fminf(x[e & 3], v0[e]), v1[e]);
+                        top = -fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
                     }
                 }
                 top = top == -INFINITY ? top : top * fabsf(sc);
@@ -247,46 +254,53 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                     if (grow) mr = top;
                     l *= f;
                     if (j > 0) {
-#pragma unroll
+                        ok = outputs();
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
-                            float v[32];
-                            tmem_ld32(trow + TM_O + 128 * k + 32 * q, v);
+                            float o[32];
+                            tmem_ld32(trow + TM_O + 128 * k + 32 * q, o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] *= f;
-                            tmem_st32(trow + TM_O + 128 * k + 32 * q, v);
+                            for (int e = 0; e < 32; ++e) o[e] *= f;
+                            tmem_st32(trow + TM_O + 128 * k + 32 * q, o);
                         }
                     }
                 }
-                const float z = mr == -INFINITY ? 0.f : mr;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float z = mr == -INFINITY ? 0.f : -mr;
+                const float2 z2 = make_float2(z, z);
+                float2 sum = make_float2(0.f, 0.f);
+                auto weigh = [&](float (&v)[32], uint32_t in, int col) {
+                    float u[32];   // 16 pairs of upper halves, then of the rests: in the place of the scores that they come from
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float v[32];
-                    uint32_t u[32];   // 16 words of pairs, then of their rests: in the place of the scores that they come from
-                    tmem_ld32(ts + 32 * q, v);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = ex2(fmaf(v[e], sc, -z));
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 y = __ffma2_rn(make_float2(v[e], v[e + 1]), sc2, z2);
+                        v[e] = ex2(y.x);
+                        v[e + 1] = ex2(y.y);
+                    }
                     if (!open) {
+                        uint32_t bits = 0;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = in(32 * q + e) ? v[e] : 0.f;
-                        if (draft && q < 2) {
-                            uint32_t bits = 0;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) bits |= v[e] != 0.f ? 1u << e : 0u;
-                            weighs |= (uint64_t)bits << (32 * q);
+                        for (int e = 0; e < 32; ++e) {
+                            v[e] = (in >> e) & 1u ? v[e] : 0.f;
+                            bits |= v[e] != 0.f ? 1u << e : 0u;
                         }
+                        if (draft) weighs |= (uint64_t)bits << col;
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) sum[e & 3] += v[e];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        u[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-                        const float2 b = unpack_bf16(u[e]);
-                        u[16 + e] = pack_bf16(v[2 * e] - b.x, v[2 * e + 1] - b.y);
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 x = make_float2(v[e], v[e + 1]);
+                        sum = __fadd2_rn(sum, x);
+                        const uint32_t a0 = __float_as_uint(x.x), a1 = __float_as_uint(x.y);
+                        u[e / 2] = __uint_as_float(__byte_perm(a0, a1, 0x7632));
+                        const float2 rest = __fadd2_rn(x, make_float2(-__uint_as_float(a0 & 0xffff0000u), -__uint_as_float(a1 & 0xffff0000u)));
+                        u[16 + e / 2] = __uint_as_float(pack_bf16(rest.x, rest.y));
                     }
-                    st32(ts + 32 * q, u);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_st32(ts + col, u);
+                };
+                weigh(v0, mk.x, 0);
+                weigh(v1, mk.y, 32);
+                l += sum.x + sum.y;
                 if (draft && (k == 0 || !w.two)) {
                     // the drafted tokens' values: what is not finite becomes zero
                     const int vl = (int)loads + w.v_load(i), st = vl % S;
@@ -317,11 +331,11 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kP + k));
+                if (lane == 0) mbar_arrive(bar(kP + b));
             }
             if (!ok) break;
             // outputs
-            if (jobs > 0) ok = all(wait(kO + k, ends++));
+            if (jobs > 0) ok = outputs();
             if (!ok) break;
             tc_fence_after();
             const bool stale = nf_any[(pieces + 1) & 1] != 0;
@@ -329,15 +343,16 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                 ml[128 * k + th] = make_float2(mr, l);
                 if (has_draft && ((w.c - 1) & 1) == k) sees[th] = weighs;   // (the chain that has the draft's tile)
             }
+            tc_fence_before();
             ok = meet();
             if (!ok) break;
             tc_fence_after();
             const bool sick = has_draft && nf_any[pieces & 1] != 0;
             const unsigned long long *bad = nf + (pieces & 1) * D;
-            if (has_draft && !w.two) weighs = sees[th];
             float f0 = 1.f, f1 = 0.f;
             const bool both = !w.two && w.c > 1;
             if (!w.two) {
+                if (has_draft) weighs = sees[th];
                 const float2 x0 = ml[th], x1 = ml[128 + th];
                 mr = fmaxf(x0.x, x1.x);
                 const float z = mr == -INFINITY ? 0.f : mr;
@@ -345,7 +360,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                 f1 = ex2(x1.x - z);
                 l = fmaf(x0.y, f0, x1.y * f1);
             }
-            if (w.two || w.c > 0) {
+            if (w.c > 0) {
                 // two: this chain's rows, all channels; else every row, this chain's half of the channels
                 const int c0 = w.two ? 0 : k * (D / 2), c1 = w.two ? D : c0 + D / 2;
                 const uint32_t to = trow + TM_O + (w.two ? 128 * k : 0);
@@ -353,24 +368,20 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                 const int row = (int)a.by_rep((uint32_t)(w.r0 + r));
                 const int64_t at = ((int64_t)w.n * a.t.tokens + row) * p.heads + w.hk * a.rep + (w.r0 + r - row * a.rep);
                 const int64_t slot = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * kRb + r;
+#pragma unroll 1
                 for (int ch = c0; ch < c1; ch += 32) {
                     float v[32];
                     tmem_ld32(to + ch, v);
-                    if (!w.two) {
-                        if (both) {
-                            float y[32];
-                            tmem_ld32(to + 128 + ch, y);
+                    if (both) {
+                        float y[32];
+                        tmem_ld32(to + 128 + ch, y);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = fmaf(v[e], f0, y[e] * f1);
-                        }
+                        for (int e = 0; e < 32; ++e) v[e] = fmaf(v[e], f0, y[e] * f1);
                     }
                     if (sick)
-#pragma unroll 1
-                        for (int e = 0; e < 32; ++e)
-                            if (bad[ch + e] & weighs) {
 #pragma unroll
-                                for (int g = 0; g < 32; ++g) v[g] = g == e ? __int_as_float(0x7fc00000) : v[g];
-                            }
+                        for (int e = 0; e < 32; ++e)
+                            if (bad[ch + e] & weighs) v[e] = __int_as_float(0x7fc00000);
                     if (r < w.rows) {
                         if (w.whole) {
                             uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at * D + ch);
@@ -395,8 +406,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                         *reinterpret_cast<float2 *>(a.part_ml + 2 * slot) = make_float2(mr, l);
                     }
                 }
-            }
-            if (w.c == 0) {   // a share that ends within a unit's start: nothing of it
+            } else {   // a share that ends within a unit's start: nothing of it
                 const int64_t slot = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * kRb;
                 for (int x = tid; x < w.rows * (D / 4); x += 256) reinterpret_cast<float4 *>(a.part_o + slot * D)[x] = make_float4(0.f, 0.f, 0.f, 0.f);
                 for (int x = tid; x < w.rows; x += 256) reinterpret_cast<float2 *>(a.part_ml + 2 * slot)[x] = make_float2(-INFINITY, 0.f);
@@ -413,150 +423,208 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
             ++pieces;
             if (!w.next(a)) break;
         }
-    } else if (warp >= 10) {
-        regs_dec<kRegsRest>();
-    } else if (warp == 8) {
-        // ---- loads
-        regs_dec<kRegsRest>();
-        const int none = p.pages * p.page_size * p.kv_heads, noq = p.rows * a.t.tokens * p.heads;   // rows past the tensors
+    } else if (warp != 9) {
+        // ---- loads: the three warps take the same steps; warp 8 alone issues TMA
+        const int wi = warp == 8 ? 0 : warp - 9;
+        constexpr int CH = D / 8, RPI = 32 / CH;            // 16-byte chunks of a row, rows of a warp's instruction
+        const __nv_bfloat16 *kc = static_cast<const __nv_bfloat16 *>(p.k_cache), *vc = static_cast<const __nv_bfloat16 *>(p.v_cache);
         uint32_t load = 0, qs = 0, tiles = 0;
+        // Loads by cp.async that have not been reported yet (barriers, eight bits each, the oldest lowest): they are once
+        // they have landed, before this warp waits for anything, and when there are four of them.
+        uint32_t queue = 0;
+        int queued = 0;
+        auto report = [&] {
+            switch (queued) {
+                case 1: cp_wait<0>(); break;
+                case 2: cp_wait<1>(); break;
+                case 3: cp_wait<2>(); break;
+                default: cp_wait<3>(); break;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(queue & 255));
+            queue >>= 8;
+            --queued;
+        };
+        auto sent = [&](int b) {
+            cp_commit();
+            queue |= (uint32_t)b << (8 * queued);
+            if (++queued == 4) report();
+        };
+        auto reach = [&](int b, uint32_t phase) {           // waits for a barrier
+            if (!all(test(bar(b), phase))) {
+                while (queued > 0) report();
+                ok = all(wait(b, phase));
+            }
+            return ok;
+        };
+        struct Place {
+            bool box;         // a full tile: at[0] is the first token of this lane's box
+            int at[2];        // else the places of tokens `lane` and 32 + lane, -1 for none
+            uint2 mask;
+        };
         for (;; ) {
             if (w.c > 0) {
                 const int32_t *table = p.table + (int64_t)w.n * p.max_pages;
-                auto places = [&](int i, int (&r)[4]) {
+                auto places = [&](int i) {
+                    Place x;
                     const int t = w.ta + i;
                     const bool draft = t == w.row.ctx;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = 4 * lane + e + (draft ? 0 : t * kKt);
-                        const int64_t at = j < (draft ? w.row.m : w.row.len) ? tree_place(a, table, draft ? w.row.len + j : j) : -1;
-                        r[e] = at < 0 ? none : (int)(at * p.kv_heads) + w.hk;
+                    const int base = draft ? w.row.len : t * kKt, left = draft ? w.row.m : w.row.len - base;
+                    if (box && !draft && left >= kKt) {
+                        x.at[0] = lane * box < kKt ? (int)tree_place(a, table, base + lane * box) : 0;
+                        if (all(x.at[0] >= 0)) {
+                            x.box = true;
+                            x.mask = make_uint2(0xffffffffu, 0xffffffffu);
+                            return x;
+                        }
                     }
-                };
-                auto tile = [&](const CUtensorMap *map, const int (&r)[4]) {
-                    const int s = load % S;
-                    ok = all(load < S || wait(kEmpty + s, load / S - 1));
-                    if (!ok) return false;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(kFull + s), L::TILE);
-                    __syncwarp();
+                    x.box = false;
 #pragma unroll
-                    for (int h = 0; h < HALVES; ++h) tma_gather4(sb + L::RING + s * L::TILE + h * HALF + lane * 512, map, bar(kFull + s), 64 * h, r);
+                    for (int e = 0; e < 2; ++e) x.at[e] = lane + 32 * e < left ? (int)tree_place(a, table, base + lane + 32 * e) : -1;
+                    x.mask = make_uint2(__ballot_sync(0xffffffffu, x.at[0] >= 0), __ballot_sync(0xffffffffu, x.at[1] >= 0));
+                    return x;
+                };
+                auto tile = [&](const CUtensorMap *map, const __nv_bfloat16 *cache, const Place &x) {
+                    const int s = load % S, full = kFull + s;
+                    if (load >= S && !reach(kEmpty + s, load / S - 1)) return false;
+                    const uint32_t to = sb + L::RING + s * L::TILE;
+                    if (x.box) {
+                        if (wi == 0) {
+                            if (lane == 0) mbar_arrive_expect_tx(bar(full), L::TILE);
+                            __syncwarp();
+                            if (lane * box < kKt)
+#pragma unroll
+                                for (int h = 0; h < HALVES; ++h) tma_load_3d(to + h * HALF + lane * box * 128, map, bar(full), 64 * h, w.hk, x.at[0]);
+                        } else if (lane == 0) {
+                            mbar_arrive(bar(full));
+                        }
+                    } else {
+                        const int c = lane % CH;
+                        for (int y = wi; y < kKt / RPI; y += kLoaders) {
+                            const int r = y * RPI + lane / CH;
+                            const int a0 = __shfl_sync(0xffffffffu, x.at[0], r & 31), a1 = __shfl_sync(0xffffffffu, x.at[1], r & 31), at = r < 32 ? a0 : a1;
+                            cp16(to + (c >> 3) * HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4), cache + ((int64_t)(at < 0 ? 0 : at) * p.kv_heads + w.hk) * D + 8 * c,
+                                 at < 0 ? 0u : 16u);
+                        }
+                        sent(full);
+                    }
                     ++load;
                     return true;
                 };
-                auto mask = [&](int i, const int (&r)[4]) {
-                    uint32_t m[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) m[e] = __ballot_sync(0xffffffffu, r[e] != none);
-                    if (lane == 0) *reinterpret_cast<uint4 *>(sm + L::MASK + 16 * ((tiles + i) & 7)) = make_uint4(m[0], m[1], m[2], m[3]);
+                auto keys = [&](int i, const Place &x) {
+                    if (wi == 0 && lane == 0) *reinterpret_cast<uint2 *>(sm + L::MASK + 8 * ((tiles + i) & 31)) = x.mask;
                     __syncwarp();
+                    return tile(&tmk, kc, x);
                 };
-                int r[4], next[4];
-                places(0, r);
                 // the queries
-                ok = all(qs == 0 || wait(kQEmpty, qs - 1));
-                if (!ok) break;
+                if (qs > 0 && !reach(kQEmpty, qs - 1)) break;
                 ++qs;
-                if (lane == 0) mbar_arrive_expect_tx(bar(kQFull), (w.two ? 2 : 1) * L::TILE);
-                __syncwarp();
-                for (int b = 0; b < (w.two ? 2 : 1); ++b) {
-                    int qr[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int x = 128 * b + 4 * lane + e, i = (int)a.by_rep((uint32_t)(w.r0 + x));
-                        qr[e] = x < w.rows ? (w.n * a.t.tokens + i) * p.heads + w.hk * a.rep + (w.r0 + x - i * a.rep) : noq;
-                    }
-#pragma unroll
-                    for (int h = 0; h < HALVES; ++h) tma_gather4(sb + L::Q + b * L::TILE + h * HALF + lane * 512, &tmq, bar(kQFull), 64 * h, qr);
+                for (int y = wi; y < (w.two ? 256 : 128) / RPI; y += kLoaders) {
+                    const int r = y * RPI + lane / CH, c = lane % CH, i = (int)a.by_rep((uint32_t)(w.r0 + r));
+                    const bool in = r < w.rows;
+                    const int64_t at = in ? ((int64_t)w.n * a.t.tokens + i) * p.heads + w.hk * a.rep + (w.r0 + r - i * a.rep) : 0;
+                    cp16(sb + L::Q + (r >> 7) * L::QTILE + (c >> 3) * QHALF + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
+                         static_cast<const __nv_bfloat16 *>(p.q) + at * D + 8 * c, in ? 16u : 0u);
                 }
-                mask(0, r);
-                if (!tile(&tmk, r)) break;
+                sent(kQFull);
+                // keys `ahead` tiles ahead of the values; a tile's places are kept until its values are loaded
+                const int ahead = w.ahead();
+                Place x[5];
                 bool fine = true;
-                for (int i = 0; i < w.c && fine; ++i) {
-                    if (i + 1 < w.c) places(i + 1, next);
-                    if (!w.two && i + 1 < w.c) {
-                        mask(i + 1, next);
-                        fine = tile(&tmk, next);
-                    }
-                    fine = fine && tile(&tmv, r);
-                    if (w.two && i + 1 < w.c && fine) {
-                        mask(i + 1, next);
-                        fine = tile(&tmk, next);
-                    }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) r[e] = next[e];
+                for (int i = 0; i < 4; ++i)
+                    if (i < ahead && i < w.c && fine) {
+                        x[i] = places(i);
+                        fine = keys(i, x[i]);
+                    }
+                for (int i = 0; i < w.c && fine; ++i) {
+                    const bool more = i + ahead < w.c;
+                    if (more) x[4] = places(i + ahead);
+                    fine = tile(&tmv, vc, x[0]) && (!more || keys(i + ahead, x[4]));
+                    if (ahead == 2) {
+                        x[0] = x[1];
+                        x[1] = x[4];
+                    } else {
+                        x[0] = x[1];
+                        x[1] = x[2];
+                        x[2] = x[3];
+                        x[3] = x[4];
+                    }
                 }
                 if (!fine) break;
                 tiles += w.c;
             }
             if (!w.next(a)) break;
         }
+        while (queued > 0) report();
     } else {
         // ---- products; an elected lane issues
-        regs_dec<kRegsRest>();
         const uint32_t one = elect_one();
-        uint32_t loads = 0, qs = 0, jobs[2] = {0, 0};
+        uint32_t loads = 0, qs = 0, made[2] = {0, 0}, used[2] = {0, 0};   // loads, pieces, scores and weights so far
         const uint64_t qd = sdesc_sw128(sb + L::Q), kd = sdesc_sw128(sb + L::RING), vd = sdesc_sw128_mn(sb + L::RING, HALF, 1024);
         for (;; ) {
             if (w.c > 0) {
                 // scores of chain k, tile i; `loaded`: the tile has been waited for, `last`: its last use
                 auto qk = [&](int k, int i, bool loaded, bool last) {
-                    const int ld = (int)loads + w.k_load(i), s = ld % S;
+                    const int ld = (int)loads + w.k_load(i), s = ld % S, b = 2 * k + (int)(made[k] & 1);
                     ok = all(loaded || wait(kFull + s, ld / S));
                     if (!ok) return false;
                     tc_fence_after();
                     if (one) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-                            mma_f16_ss(tmem + TM_S + 128 * k, qd + (w.two ? k * (L::TILE >> 4) : 0) + off, kd + s * (L::TILE >> 4) + off, IDESC_QK, kk > 0);
-                        }
-                        mma_commit(bar(kS + k));
-                        mbar_arrive(bar(kS + k));
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            mma_f16_ss(tmem + TM_S + 64 * b, qd + (w.two ? k * (L::QTILE >> 4) : 0) + (((kk >> 2) * QHALF + (kk & 3) * 32) >> 4),
+                                       kd + s * (L::TILE >> 4) + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), IDESC_QK, kk > 0);
+                        mma_commit(bar(kS + b));
+                        mbar_arrive(bar(kS + b));
                         if (last) mma_commit(bar(kEmpty + s));
                     }
                     __syncwarp();
+                    ++made[k];
                     return true;
                 };
                 // outputs of chain k, tile i, its j-th
                 auto pv = [&](int k, int i, int j, bool loaded, bool last) {
-                    const int ld = (int)loads + w.v_load(i), s = ld % S;
-                    ok = all((loaded || wait(kFull + s, ld / S)) && wait(kP + k, jobs[k]));
+                    const int ld = (int)loads + w.v_load(i), s = ld % S, b = 2 * k + (int)(used[k] & 1);
+                    ok = all((loaded || wait(kFull + s, ld / S)) && wait(kP + b, used[k] >> 1));
                     if (!ok) return false;
-                    ++jobs[k];
                     tc_fence_after();
                     if (one) {
 #pragma unroll
                         for (int e = 1; e >= 0; --e)   // the rests first
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
-                                mma_f16_ts(tmem + TM_O + 128 * k, tmem + TM_S + 128 * k + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * e,
+                            for (int kk = 0; kk < kKt / 16; ++kk)
+                                mma_f16_ts(tmem + TM_O + 128 * k, tmem + TM_S + 64 * b + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * e,
                                            vd + s * (L::TILE >> 4) + ((2048 * kk) >> 4), IDESC_PV, j > 0 || e == 0 || kk > 0);
                         if (last) mma_commit(bar(kEmpty + s));
-                        if (j + 1 == w.jobs(k)) mma_commit(bar(kO + k));
+                        mma_commit(bar(kV + b));
                     }
                     __syncwarp();
+                    ++used[k];
                     return true;
                 };
                 ok = all(wait(kQFull, qs++));
                 if (!ok) break;
                 bool fine = true;
-                if (w.two) {
-                    fine = qk(0, 0, false, false) && qk(1, 0, true, true);
-                    for (int i = 0; i < w.c && fine; ++i) {
-                        const bool more = i + 1 < w.c;
-                        fine = pv(0, i, i, false, false) && (!more || qk(0, i + 1, false, false)) && pv(1, i, i, true, true) && (!more || qk(1, i + 1, true, true));
-                        if (fine && i + 2 >= w.c && (more || w.c == 1) && one) mma_commit(bar(kQEmpty));
-                    }
-                } else {
-                    fine = qk(0, 0, false, true) && (w.c < 2 || qk(1, 1, false, true));
-                    if (fine && w.c <= 2 && one) mma_commit(bar(kQEmpty));
-                    for (int i = 0; i < w.c && fine; ++i) {
-                        fine = pv(i & 1, i, i >> 1, false, true) && (i + 2 >= w.c || qk(i & 1, i + 2, false, true));
-                        if (fine && i + 3 == w.c && one) mma_commit(bar(kQEmpty));
-                    }
+                const int ahead = w.ahead();
+                auto made_last = [&](int i) {              // the piece's queries are read
+                    if (fine && i + 1 == w.c && one) mma_commit(bar(kQEmpty));
+                    __syncwarp();
+                };
+                for (int i = 0; i < ahead && i < w.c && fine; ++i) {
+                    fine = w.two ? qk(0, i, false, false) && qk(1, i, true, true) : qk(i & 1, i, false, true);
+                    made_last(i);
                 }
-                __syncwarp();
+                for (int i = 0; i < w.c && fine; ++i) {
+                    const int y = i + ahead;
+                    if (w.two) {
+                        fine = pv(0, i, i, false, false) && (y >= w.c || qk(0, y, false, false)) && pv(1, i, i, true, true) && (y >= w.c || qk(1, y, true, true));
+                    } else {
+                        fine = pv(i & 1, i, i >> 1, false, true) && (y >= w.c || qk(i & 1, y, false, true));
+                    }
+                    made_last(y);
+                }
                 if (!fine) break;
                 loads += 2 * w.c;
             }
@@ -581,7 +649,12 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
             atomicAdd(&g_kda_tree_timeouts, 1u);
         }
         const float nan = __int_as_float(0x7fc00000);
-        w = start;
+        w.x = blockIdx.x * W / G;                          // from the start of the share
+        tree_find<kThreads>(a, w.x, sm_sum, w.n, w.us);
+        w.row = tree_row(a, w.n);
+        w.unit = (int)((w.x - w.us) / w.row.items);
+        w.us += w.unit * w.row.items;
+        w.piece(a);
         for (bool first = true;; first = false) {
             const int64_t slot = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * kRb;
             for (int x = tid; x < w.rows * D; x += kThreads) {
@@ -617,15 +690,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// [rows][d] bf16 for gathers: boxes of 64 channels of one row, 128-byte swizzle; rows past the tensor are zeros.
-bool make_map(CUtensorMap *m, const void *ptr, int64_t rows, int d) {
+// [tokens][kv_heads][d] bf16 as (d, kv_heads, tokens): boxes of 64 channels of one head and `box` tokens, in the same layout.
+bool make_map(CUtensorMap *m, const void *ptr, int64_t tokens, int heads, int d, int box) {
     auto enc = encode_fn();
     if (enc == nullptr) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)d * 2};
-    cuuint32_t box[2] = {64, 1};
-    cuuint32_t es[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
+    cuuint32_t boxes[3] = {64, 1, (cuuint32_t)box};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -633,25 +706,23 @@ bool make_map(CUtensorMap *m, const void *ptr, int64_t rows, int d) {
 int tc_ctas(const PagedTreeArgs &t) {
     const int rep = t.p.heads / t.p.kv_heads;
     const int64_t units = (int64_t)t.p.rows * t.p.kv_heads * (((int64_t)t.tokens * rep + kRb - 1) / kRb);
-    const int64_t items = ((int64_t)t.p.max_pages * t.p.page_size + kKt - 1) / kKt + 1 + kTreeStart;
+    const int64_t items = ((int64_t)t.p.max_pages * t.p.page_size + kKt - 1) / kKt + 1 + kStart;
     return units >= kSms || units * items >= kSms ? kSms : (int)(units * items);
 }
 
 template <int D> cudaError_t launch_tc(const TreeAtt &a, int ctas, uint32_t polls, cudaStream_t st) {
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mk, mv;
     const PagedArgs &p = a.t.p;
-    const int64_t cached = (int64_t)p.pages * p.page_size * p.kv_heads;
-    if (!make_map(&mq, p.q, (int64_t)p.rows * a.t.tokens * p.heads, D) || !make_map(&mk, p.k_cache, cached, D) || !make_map(&mv, p.v_cache, cached, D))
+    // tokens of a box: the largest power of two that divides the pages, of eight rows (a swizzle's period) at least
+    int box = kKt;
+    while (p.page_size % box) box /= 2;
+    if (box < 8) box = 0;
+    const int64_t cached = (int64_t)p.pages * p.page_size;
+    if (!make_map(&mk, p.k_cache, cached, p.kv_heads, D, box ? box : 8) || !make_map(&mv, p.v_cache, cached, p.kv_heads, D, box ? box : 8))
         return cudaErrorInvalidValue;
-    // what the roles' shares of registers add up to has to be there at the launch, else they would wait for ever
-    static const bool enough = [] {
-        cudaFuncAttributes f;
-        return cudaFuncGetAttributes(&f, kda_paged_tree_tc_kernel<D>) == cudaSuccess && f.numRegs * kThreads >= 256 * kRegsChain + 128 * kRegsRest;
-    }();
-    if (!enough) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(kda_paged_tree_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tc<D>::BYTES);
     if (e != cudaSuccess) return e;
-    kda_paged_tree_tc_kernel<D><<<ctas, kThreads, Tc<D>::BYTES, st>>>(mq, mk, mv, a, polls);
+    kda_paged_tree_tc_kernel<D><<<ctas, kThreads, Tc<D>::BYTES, st>>>(mk, mv, a, box, polls);
     e = cudaGetLastError();
     return e != cudaSuccess || ctas == 1 ? e : launch_tree_join(a, D, KDA_BF16, ctas, st);   // (one CTA: nothing is split)
 }
@@ -663,7 +734,7 @@ size_t tree_tc_workspace_bytes(const PagedTreeArgs &t, int d) { return (size_t)t
 cudaError_t launch_tree_tc(const PagedTreeArgs &t, int d, void *workspace, uint32_t polls, cudaStream_t st) {
     const int rep = t.p.heads / t.p.kv_heads, ctas = tc_ctas(t);
     float *ws = static_cast<float *>(workspace);
-    const TreeAtt a{t, FastDiv((uint32_t)t.p.page_size), FastDiv((uint32_t)rep), rep, kRb, kKt, ws, ws + (size_t)ctas * 2 * kRb * d};
+    const TreeAtt a{t, FastDiv((uint32_t)t.p.page_size), FastDiv((uint32_t)rep), rep, kRb, kKt, kStart, ws, ws + (size_t)ctas * 2 * kRb * d};
     return d == 128 ? launch_tc<128>(a, ctas, polls, st) : launch_tc<64>(a, ctas, polls, st);
 }
 

@@ -212,31 +212,54 @@ __global__ void __launch_bounds__(kThreads, 2) kda_paged_tree_attention_kernel(c
     }
 }
 
-// Joins the parts of the units that fell into several shares: one CTA per boundary between two shares (blockIdx.x + 1
-// is the share behind it) and kJoinRows query rows; it takes the unit that the boundary cuts, unless an earlier
-// one cuts it too.  Every CTA waits for the first kernel to end, so that nothing behind this kernel
-// in the stream starts before that.
+// Joins the parts of the units that fell into several shares, kJoinRows query rows a CTA.  Where there are few units, one
+// CTA per unit and rows; else one per boundary between two shares (blockIdx.x + 1 is the share behind it),
+// which takes the unit that the boundary cuts, unless an earlier one cuts it too.  Every CTA waits for the
+// first kernel to end, so that nothing behind this kernel in the stream starts before that.
 constexpr int kJoinThreads = 256, kJoinRows = 8;
 
-template <typename T, int D>
+template <typename T, int D, bool kByUnit>
 __global__ void __launch_bounds__(kJoinThreads) kda_paged_tree_join_kernel(const TreeAtt a, const int ctas) {
     __shared__ long long sm_sum[kJoinThreads / 32];
     const PagedArgs &p = a.t.p;
-    const long long W = tree_total<kJoinThreads>(a, sm_sum);
-    const long long G = W < ctas ? W : ctas;
-    const int b0 = blockIdx.x;
-    int n = 0, b1 = b0, hk = 0, r0 = 0, rows = 0;
-    long long us = 0;
-    if (b0 + 1 < G) {
-        const long long x = (b0 + 1) * W / G;
-        tree_find<kJoinThreads>(a, x, sm_sum, n, us);
+    int n = 0, b0 = blockIdx.x, b1 = b0, hk = 0, r0 = 0, rows = 0;
+    long long us = 0, W, G;
+    if (kByUnit) {
+        const int blocks = (a.t.tokens * a.rep + a.rb - 1) / a.rb;   // of a row with all its tokens
+        n = blockIdx.x / (p.kv_heads * blocks);
+        const int u = blockIdx.x - n * p.kv_heads * blocks;
+        long long mine = 0, ahead = 0;
+        for (int i = threadIdx.x; i < p.rows; i += kJoinThreads) {
+            const long long x = tree_items(a, i);
+            mine += x;
+            ahead += i < n ? x : 0;
+        }
+        W = block_sum<kJoinThreads>(mine, sm_sum);
+        us = block_sum<kJoinThreads>(ahead, sm_sum);
+        G = W < ctas ? W : ctas;
         const TreeRow row = tree_row(a, n);
-        const int unit = (int)((x - us) / row.items);
-        us += unit * row.items;
-        hk = unit / row.blocks;
-        r0 = (unit - hk * row.blocks) * a.rb;
-        rows = row.m * a.rep - r0 < a.rb ? row.m * a.rep - r0 : a.rb;
-        if (x > us && b0 * W / G <= us) b1 = (int)(((us + row.items) * G - 1) / W);
+        if (u < row.blocks * p.kv_heads) {
+            us += u * row.items;
+            hk = u / row.blocks;
+            r0 = (u - hk * row.blocks) * a.rb;
+            rows = row.m * a.rep - r0 < a.rb ? row.m * a.rep - r0 : a.rb;
+            b0 = (int)(((us + 1) * G - 1) / W);
+            b1 = (int)(((us + row.items) * G - 1) / W);
+        }
+    } else {
+        W = tree_total<kJoinThreads>(a, sm_sum);
+        G = W < ctas ? W : ctas;
+        if (b0 + 1 < G) {
+            const long long x = (b0 + 1) * W / G;
+            tree_find<kJoinThreads>(a, x, sm_sum, n, us);
+            const TreeRow row = tree_row(a, n);
+            const int unit = (int)((x - us) / row.items);
+            us += unit * row.items;
+            hk = unit / row.blocks;
+            r0 = (unit - hk * row.blocks) * a.rb;
+            rows = row.m * a.rep - r0 < a.rb ? row.m * a.rep - r0 : a.rb;
+            if (x > us && b0 * W / G <= us) b1 = (int)(((us + row.items) * G - 1) / W);
+        }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (b1 == b0) return;
@@ -246,7 +269,7 @@ __global__ void __launch_bounds__(kJoinThreads) kda_paged_tree_join_kernel(const
     for (int r = blockIdx.y * kJoinRows + threadIdx.x / L; r < (int)(blockIdx.y + 1) * kJoinRows && r < rows; r += PER) {
         float mx = -INFINITY, sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kAtOnce = 4;
+        constexpr int kAtOnce = 8;
         for (int b = b0; b <= b1; b += kAtOnce) {
             float2 v[kAtOnce];
             float4 o[kAtOnce];
@@ -302,16 +325,22 @@ cudaError_t launch_tree_join(const TreeAtt &a, int d, kda_dtype_t dt, int ctas, 
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     const int rows = a.rep * a.t.tokens < a.rb ? a.rep * a.t.tokens : a.rb;
-    cfg.gridDim = dim3((unsigned)(ctas - 1), (unsigned)((rows + kJoinRows - 1) / kJoinRows));
+    const int64_t units = (int64_t)a.t.p.rows * a.t.p.kv_heads * (((int64_t)a.t.tokens * a.rep + a.rb - 1) / a.rb);
+    const bool few = 2 * units <= ctas;
+    cfg.gridDim = dim3((unsigned)(few ? units : ctas - 1), (unsigned)((rows + kJoinRows - 1) / kJoinRows));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cfg.attrs = at;
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // its CTAs may find their parts and wait before the
     at[0].val.programmaticStreamSerializationAllowed = 1;            // first kernel has ended
     cfg.numAttrs = 1;
+    auto launch = [&](auto by_unit, auto by_boundary) { return few ? cudaLaunchKernelEx(&cfg, by_unit, a, ctas) : cudaLaunchKernelEx(&cfg, by_boundary, a, ctas); };
+    using B = __nv_bfloat16;
     if (dt == KDA_F32)
-        return d == 128 ? cudaLaunchKernelEx(&cfg, kda_paged_tree_join_kernel<float, 128>, a, ctas) : cudaLaunchKernelEx(&cfg, kda_paged_tree_join_kernel<float, 64>, a, ctas);
-    return d == 128 ? cudaLaunchKernelEx(&cfg, kda_paged_tree_join_kernel<__nv_bfloat16, 128>, a, ctas) : cudaLaunchKernelEx(&cfg, kda_paged_tree_join_kernel<__nv_bfloat16, 64>, a, ctas);
+        return d == 128 ? launch(kda_paged_tree_join_kernel<float, 128, true>, kda_paged_tree_join_kernel<float, 128, false>)
+                        : launch(kda_paged_tree_join_kernel<float, 64, true>, kda_paged_tree_join_kernel<float, 64, false>);
+    return d == 128 ? launch(kda_paged_tree_join_kernel<B, 128, true>, kda_paged_tree_join_kernel<B, 128, false>)
+                    : launch(kda_paged_tree_join_kernel<B, 64, true>, kda_paged_tree_join_kernel<B, 64, false>);
 }
 
 size_t paged_tree_workspace_bytes(const PagedTreeArgs &t, int d, kda_dtype_t dt) {

@@ -14,13 +14,15 @@
 //
 // Tiles that lie whole on pages of a multiple of 8 tokens come by TMA, a box of tokens an instruction; others (the last
 // cached tokens, pages of other sizes, places without a token, which become zeros and whose scores are masked)
-// by cp.async of three warps.  (Gathers of four rows by TMA take 50 ns each, 6.5 us for 128 keys of 128
+// by cp.async of two warps.  (Gathers of four rows by TMA take 50 ns each, 6.5 us for 128 keys of 128
 // channels: 131,071 tokens x 8 heads, 512 query rows: 700 us, 430 by boxes.)  The drafted tokens have a tile of their own,
 // masked by their paths.  A non-finite value among them is replaced by zero before the product (zero
 // times NaN would reach other branches) and put back as NaN in the outputs of the tokens that weigh it.
 //
-// Roles: warps 0-3 and 4-7 the chains' softmax, warps 8, 10 and 11 the loads, warp 9 the products.  They meet at
-// mbarriers with bounded waits.
+// Roles: warps 0-7 and 8-15 the chains' softmax, half of a tile's keys each four (a row's two threads agree on m; with
+// one thread per row a chain's softmax took 2600 cycles a tile, mostly waits of its one warp per scheduler for its own
+// results, twice the products' time); warps 16 and 17 the chains' products, 18 and 19 the loads.  They meet at mbarriers
+// with bounded waits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -36,23 +38,23 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 384, kRb = 256, kKt = 64, kStart = 3;
+constexpr int kThreads = 640, kRb = 256, kKt = 64, kStart = 3;
 constexpr float kSlack = 8.f;   // growth of the maximum, in powers of two, that m does not follow
-constexpr int kLoaders = 3;     // warps
+constexpr int kLoaders = 2;     // warps
 
 template <int D> struct Tc {
     static constexpr uint32_t TILE = kKt * D * 2, QTILE = 128 * D * 2;   // keys or values; query rows of a chain
     static constexpr int STAGES = D == 128 ? 9 : 16;
     static constexpr uint32_t Q = 0, RING = 2 * QTILE, BAR = RING + STAGES * TILE;
     static constexpr uint32_t MASK = BAR + 512, ANC = MASK + 32 * 8, UP = ANC + 512, ML = UP + 256;
-    static constexpr uint32_t SEE = ML + 2 * 128 * 8, NF = SEE + 128 * 8, NFANY = NF + 2 * D * 8, TM = NFANY + 16;
+    static constexpr uint32_t SEE = ML + 6 * 128 * 4, NF = SEE + 4 * 128 * 4, NFANY = NF + 2 * D * 8, TM = NFANY + 16;
     static constexpr uint32_t BYTES = TM + 16 + 1024;
     static_assert(BYTES <= 226 * 1024, "shared memory budget");
 };
 // kS, kP and kV are of a chain and a buffer (2 k + b): scores, weights, outputs.  A wait names a phase by its parity, so a
 // barrier may be at most one phase behind what is waited for and none ahead.  That holds because the scores of a
 // chain's tile j follow the outputs of its tile j - 2, and those of tile j the weights that their waiter makes.
-enum Bar { kFull = 0, kEmpty = 16, kQFull = 32, kQEmpty = 33, kS = 34, kP = 38, kV = 42, kMeet = 46, kBars = 47 };
+enum Bar { kFull = 0, kEmpty = 16, kQFull = 32, kQEmpty = 33, kS = 34, kP = 38, kV = 42, kMeet = 46, kSane = 47, kBars = 48 };
 
 constexpr uint32_t TM_S = 0, TM_O = 256;   // + 128 for the second chain, + 64 for the second buffer
 
@@ -71,10 +73,38 @@ __device__ __forceinline__ bool test(uint32_t bar, uint32_t parity) {   // witho
     return done != 0;
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory"); }
+// Barrier `id` of 256 threads: whether x holds in any of them.
+__device__ __forceinline__ bool any_of(int id, bool x) {
+    uint32_t y;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(y)
+                 : "r"((uint32_t)x), "r"(id)
+                 : "memory");
+    return y != 0;
+}
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t one;
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(one));
     return one;
+}
+
+// Shared-memory operand descriptors here differ in their low words only: address, and for operands read across their rows
+// the distance of their 64-channel halves.  The rest: 8-row groups 1024 bytes apart, version 1, 128-byte swizzle (see
+// sdesc_sw128, sdesc_sw128_mn).
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tmov.b64 db, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+        : "memory");
 }
 
 // A CTA's share of the items, piece by piece (every role walks it by itself).
@@ -157,20 +187,21 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
         nf_any[0] = nf_any[1] = 0;
         for (int s = 0; s < 16; ++s) {             // (also those past the stages: what gives up looks at all of them)
             mbar_init(bar(kFull + s), kLoaders);
-            mbar_init(bar(kEmpty + s), 1);
+            mbar_init(bar(kEmpty + s), 2);         // both chains
         }
         mbar_init(bar(kQFull), kLoaders);
-        mbar_init(bar(kQEmpty), 1);
+        mbar_init(bar(kQEmpty), 2);                // both chains
         for (int x = 0; x < 4; ++x) {
             mbar_init(bar(kS + x), 2);             // the product, and the thread that issued it (which has seen the tile's masks)
-            mbar_init(bar(kP + x), 4);             // the chain's warps
+            mbar_init(bar(kP + x), 8);             // the chain's warps
             mbar_init(bar(kV + x), 1);
         }
-        mbar_init(bar(kMeet), 8);                  // both chains' warps
+        mbar_init(bar(kMeet), 16);                 // both chains' warps
+        mbar_init(bar(kSane), 8);                  // the first chain's warps
         fence_mbar_init();
     }
     for (int x = tid; x < 2 * D; x += kThreads) nf[x] = 0;
-    if (warp == 9) {
+    if (warp == 16) {
         tmem_alloc(sb + L::TM, 512);
         tmem_relinquish();
     }
@@ -180,189 +211,205 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(sm + L::TM), 0);
     bool ok = true;
 
-    if (warp < 8) {
+    if (warp < 16) {
         // ---- softmax
-        const int k = warp >> 2, th = tid & 127;           // chain; query row of it
+        const int k = warp >> 3, half = (warp >> 2) & 1, th = tid & 127;   // chain; half of a tile's keys; query row
         const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float sc = p.scale * kLog2e;
         const float2 sc2 = make_float2(sc, sc);
-        const uint2 *masks = reinterpret_cast<const uint2 *>(sm + L::MASK);
+        const uint32_t *masks = reinterpret_cast<const uint32_t *>(sm + L::MASK);
         uint64_t *anc = reinterpret_cast<uint64_t *>(sm + L::ANC);
-        float2 *ml = reinterpret_cast<float2 *>(sm + L::ML);
-        uint64_t *sees = reinterpret_cast<uint64_t *>(sm + L::SEE);
-        uint32_t count = 0, meets = 0, tiles = 0, loads = 0, pieces = 0;   // jobs, barriers, tiles, loads and pieces so far
+        float *tops = reinterpret_cast<float *>(sm + L::ML), *sums = tops + 2 * 128;   // [chain][row]; [chain][half][row]
+        uint32_t *sees = reinterpret_cast<uint32_t *>(sm + L::SEE);                    // [chain][half][row]
+        uint32_t count = 0, meets = 0, sane = 0, tiles = 0, loads = 0, pieces = 0;   // jobs, barriers, tiles, loads and pieces so far
         auto outputs = [&] { return all(wait(kV + 2 * k + (int)((count - 1) & 1), (count - 1) >> 1)); };   // of the chain's last tile
-        auto meet = [&] {   // all 256 threads of the chains
+        auto meet = [&] {   // all 512 threads of the chains
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kMeet));
-            return all(wait(kMeet, meets++));
+            const uint32_t phase = meets++;
+            return ok && all(wait(kMeet, phase));
         };
+        // A warp that has given up (!ok) goes on without waiting until its chain leaves together, at one of the chain's barriers.
+        bool gone = false;
         for (bool first = true;; first = false) {
             const bool has_draft = w.ta + w.c == w.row.tiles && w.c > 0;
             const int r = (w.two ? 128 * k : 0) + th;
-            uint64_t see = 0;
+            uint32_t see = 0;                               // of this half's drafted tokens
             if (has_draft) {
                 if (warp == 0) tree_masks(a, w.n, w.row.m, anc, reinterpret_cast<int *>(sm + L::UP));
                 ok = meet();
-                if (!ok) break;
-                if (r < w.rows) see = anc[a.by_rep((uint32_t)(w.r0 + r))];
+                if (r < w.rows) see = (uint32_t)(anc[a.by_rep((uint32_t)(w.r0 + r))] >> (32 * half));
             }
-            uint64_t weighs = 0;                            // drafted tokens with a weight
+            uint32_t weighs = 0;                            // drafted tokens with a weight
             float mr = -INFINITY, l = 0.f;
             const int jobs = w.jobs(k);
             for (int j = 0; j < jobs; ++j, ++count) {
                 const int i = w.tile(k, j), b = 2 * k + (int)(count & 1);
                 const bool draft = w.ta + i == w.row.ctx;
-                ok = all(wait(kS + b, count >> 1));
-                if (!ok) break;
+                ok = ok && all(wait(kS + b, count >> 1));
                 tc_fence_after();
-                const uint32_t ts = trow + TM_S + 64 * b;
-                float v0[32], v1[32];
-                tmem_ld32x2(ts, ts + 32, v0, v1);
-                uint2 mk = masks[(tiles + i) & 31];
-                const bool open = !draft && (mk.x & mk.y) == 0xffffffffu;
+                const uint32_t ts = trow + TM_S + 64 * b + 32 * half;
+                float v[32];
+                tmem_ld32(ts, v);
+                uint32_t in = masks[2 * ((tiles + i) & 31) + half];
+                const bool open = !draft && in == 0xffffffffu;
                 if (!open) {
-                    if (draft) mk.x &= (uint32_t)see, mk.y &= (uint32_t)(see >> 32);
+                    if (draft) in &= see;
                     const float no = sc >= 0.f ? -INFINITY : INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        v0[e] = (mk.x >> e) & 1u ? v0[e] : no;
-                        v1[e] = (mk.y >> e) & 1u ? v1[e] : no;
-                    }
+                    for (int e = 0; e < 32; ++e) v[e] = (in >> e) & 1u ? v[e] : no;
                 }
                 float top;
                 {
                     float x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = v[e];
                     if (sc >= 0.f) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = fmaxf(v0[e], v1[e]);
+                        for (int e = 4; e < 32; e += 8)
 #pragma unroll
-                        for (int e = 4; e < 32; ++e) x[e & 3] = fmaxf(fmaxf(x[e & 3], v0[e]), v1[e]);
+                            for (int f = 0; f < 4; ++f) x[f] = e + 4 < 32 ? fmaxf(fmaxf(x[f], v[e + f]), v[(e + 4 + f) & 31]) : fmaxf(x[f], v[e + f]);
                         top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = fminf(v0[e], v1[e]);
+                        for (int e = 4; e < 32; e += 4)
 #pragma unroll
-                        for (int e = 4; e < 32; ++e) x[e & 3] = fminf(fminf(x[e & 3], v0[e]), v1[e]);
+                            for (int f = 0; f < 4; ++f) x[f] = fminf(x[f], v[e + f]);
                         top = -fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
                     }
                 }
                 top = top == -INFINITY ? top : top * fabsf(sc);
-                const bool grow = top > mr + kSlack || (mr == -INFINITY && top > mr);
-                if (__any_sync(0xffffffffu, grow)) {
+                // the chain's threads go on together: where one has given up, or a row's maximum has grown
+                if (any_of(1 + k, !ok || top > mr + kSlack || (mr == -INFINITY && top > mr))) {
+                    if (any_of(1 + k, !ok)) {
+                        gone = true;
+                        break;
+                    }
+                    // (a row's two threads hand their maxima to one another in `sums`)
+                    sums[(2 * k + half) * 128 + th] = top;
+                    any_of(1 + k, false);
+                    top = fmaxf(top, sums[(2 * k + (half ^ 1)) * 128 + th]);
+                    any_of(1 + k, false);
+                    const bool grow = top > mr + kSlack || (mr == -INFINITY && top > mr);
                     const float f = grow ? ex2(mr - top) : 1.f;
                     if (grow) mr = top;
                     l *= f;
                     if (j > 0) {
                         ok = outputs();
-                        if (!ok) break;
+                        if (any_of(1 + k, !ok)) {
+                            gone = true;
+                            break;
+                        }
                         tc_fence_after();
 #pragma unroll 1
-                        for (int q = 0; q < D / 32; ++q) {
+                        for (int q = 0; q < D / 64; ++q) {   // this half's channels
+                            const uint32_t to = trow + TM_O + 128 * k + half * (D / 2) + 32 * q;
                             float o[32];
-                            tmem_ld32(trow + TM_O + 128 * k + 32 * q, o);
+                            tmem_ld32(to, o);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) o[e] *= f;
-                            tmem_st32(trow + TM_O + 128 * k + 32 * q, o);
+                            tmem_st32(to, o);
                         }
                     }
                 }
                 const float z = mr == -INFINITY ? 0.f : -mr;
                 const float2 z2 = make_float2(z, z);
-                float2 sum = make_float2(0.f, 0.f);
-                auto weigh = [&](float (&v)[32], uint32_t in, int col) {
-                    float u[32];   // 16 pairs of upper halves, then of the rests: in the place of the scores that they come from
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 y = __ffma2_rn(make_float2(v[e], v[e + 1]), sc2, z2);
-                        v[e] = ex2(y.x);
-                        v[e + 1] = ex2(y.y);
-                    }
-                    if (!open) {
-                        uint32_t bits = 0;
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 y = __ffma2_rn(make_float2(v[e], v[e + 1]), sc2, z2);
+                    v[e] = ex2(y.x);
+                    v[e + 1] = ex2(y.y);
+                }
+                if (!open) {
+                    uint32_t bits = 0;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            v[e] = (in >> e) & 1u ? v[e] : 0.f;
-                            bits |= v[e] != 0.f ? 1u << e : 0u;
-                        }
-                        if (draft) weighs |= (uint64_t)bits << col;
+                    for (int e = 0; e < 32; ++e) {
+                        v[e] = (in >> e) & 1u ? v[e] : 0.f;
+                        bits |= v[e] != 0.f ? 1u << e : 0u;
                     }
+                    if (draft) weighs = bits;
+                }
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                float u[32];   // 16 pairs of upper halves, then of the rests: in the place of the scores that they come from
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 x = make_float2(v[e], v[e + 1]);
-                        sum = __fadd2_rn(sum, x);
-                        const uint32_t a0 = __float_as_uint(x.x), a1 = __float_as_uint(x.y);
-                        u[e / 2] = __uint_as_float(__byte_perm(a0, a1, 0x7632));
-                        const float2 rest = __fadd2_rn(x, make_float2(-__uint_as_float(a0 & 0xffff0000u), -__uint_as_float(a1 & 0xffff0000u)));
-                        u[16 + e / 2] = __uint_as_float(pack_bf16(rest.x, rest.y));
-                    }
-                    tmem_st32(ts + col, u);
-                };
-                weigh(v0, mk.x, 0);
-                weigh(v1, mk.y, 32);
-                l += sum.x + sum.y;
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 x = make_float2(v[e], v[e + 1]);
+                    sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], x);
+                    const uint32_t a0 = __float_as_uint(x.x), a1 = __float_as_uint(x.y);
+                    u[e / 2] = __uint_as_float(__byte_perm(a0, a1, 0x7632));
+                    const float2 rest = __fadd2_rn(x, make_float2(-__uint_as_float(a0 & 0xffff0000u), -__uint_as_float(a1 & 0xffff0000u)));
+                    u[16 + e / 2] = __uint_as_float(pack_bf16(rest.x, rest.y));
+                }
+                tmem_st32(ts, u);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 if (draft && (k == 0 || !w.two)) {
                     // the drafted tokens' values: what is not finite becomes zero
                     const int vl = (int)loads + w.v_load(i), st = vl % S;
-                    ok = all(wait(kFull + st, vl / S));
-                    if (!ok) break;
-                    for (int x = th; x < w.row.m * (D / 8); x += 128) {
-                        const int key = x / (D / 8), ch = x % (D / 8);
-                        uint4 *at = reinterpret_cast<uint4 *>(sm + L::RING + st * L::TILE + (ch >> 3) * HALF + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
-                        uint4 v = *at;
-                        uint32_t *q = &v.x;
-                        bool bad = false;
+                    ok = ok && all(wait(kFull + st, vl / S));
+                    if (ok)
+                        for (int x = 128 * half + th; x < w.row.m * (D / 8); x += 256) {
+                            const int key = x / (D / 8), ch = x % (D / 8);
+                            uint4 *at = reinterpret_cast<uint4 *>(sm + L::RING + st * L::TILE + (ch >> 3) * HALF + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+                            uint4 y = *at;
+                            uint32_t *q = &y.x;
+                            bool bad = false;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                            for (int e = 0; e < 4; ++e)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                if (((q[e] >> (16 * h)) & 0x7f80u) == 0x7f80u) {
-                                    bad = true;
-                                    q[e] &= h ? 0x0000ffffu : 0xffff0000u;
-                                    atomicOr(nf + (pieces & 1) * D + 8 * ch + 2 * e + h, 1ull << key);
-                                }
-                        if (bad) {
-                            *at = v;
-                            nf_any[pieces & 1] = 1;
-                            fence_async_smem();
+                                for (int g = 0; g < 2; ++g)
+                                    if (((q[e] >> (16 * g)) & 0x7f80u) == 0x7f80u) {
+                                        bad = true;
+                                        q[e] &= g ? 0x0000ffffu : 0xffff0000u;
+                                        atomicOr(nf + (pieces & 1) * D + 8 * ch + 2 * e + g, 1ull << key);
+                                    }
+                            if (bad) {
+                                *at = y;
+                                nf_any[pieces & 1] = 1;
+                                fence_async_smem();
+                            }
                         }
+                }
+                if (draft && w.two) {   // the second chain's product waits for that
+                    __syncwarp();
+                    if (k == 0) {
+                        if (lane == 0) mbar_arrive(bar(kSane));
+                    } else {
+                        ok = ok && all(wait(kSane, sane));
                     }
+                    ++sane;
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kP + b));
             }
-            if (!ok) break;
+            if (gone) break;
             // outputs
-            if (jobs > 0) ok = outputs();
-            if (!ok) break;
+            if (jobs > 0) ok = ok && outputs();
             tc_fence_after();
             const bool stale = nf_any[(pieces + 1) & 1] != 0;
-            if (!w.two) {
-                ml[128 * k + th] = make_float2(mr, l);
-                if (has_draft && ((w.c - 1) & 1) == k) sees[th] = weighs;   // (the chain that has the draft's tile)
-            }
+            if (half == 0) tops[128 * k + th] = mr;
+            sums[(2 * k + half) * 128 + th] = l;
+            if (has_draft && (w.two || ((w.c - 1) & 1) == k)) sees[((w.two ? 2 * k : 0) + half) * 128 + th] = weighs;   // (of the chain that has the draft)
             tc_fence_before();
             ok = meet();
-            if (!ok) break;
             tc_fence_after();
             const bool sick = has_draft && nf_any[pieces & 1] != 0;
-            const unsigned long long *bad = nf + (pieces & 1) * D;
-            float f0 = 1.f, f1 = 0.f;
             const bool both = !w.two && w.c > 1;
-            if (!w.two) {
-                if (has_draft) weighs = sees[th];
-                const float2 x0 = ml[th], x1 = ml[128 + th];
-                mr = fmaxf(x0.x, x1.x);
+            float f0 = 1.f, f1 = 0.f;
+            if (w.two) {
+                l = sums[2 * k * 128 + th] + sums[(2 * k + 1) * 128 + th];
+            } else {
+                const float x0 = tops[th], x1 = tops[128 + th];
+                mr = fmaxf(x0, x1);
                 const float z = mr == -INFINITY ? 0.f : mr;
-                f0 = ex2(x0.x - z);
-                f1 = ex2(x1.x - z);
-                l = fmaf(x0.y, f0, x1.y * f1);
+                f0 = ex2(x0 - z);
+                f1 = ex2(x1 - z);
+                l = fmaf(sums[th] + sums[128 + th], f0, (sums[256 + th] + sums[384 + th]) * f1);
             }
             if (w.c > 0) {
-                // two: this chain's rows, all channels; else every row, this chain's half of the channels
-                const int c0 = w.two ? 0 : k * (D / 2), c1 = w.two ? D : c0 + D / 2;
+                // two: this chain's rows, this half of the channels; else every row, 32 channels of each warpgroup
+                const int c0 = w.two ? half * (D / 2) : 32 * (2 * k + half), c1 = w.two ? c0 + D / 2 : (c0 < D ? c0 + 32 : c0);
                 const uint32_t to = trow + TM_O + (w.two ? 128 * k : 0);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const int row = (int)a.by_rep((uint32_t)(w.r0 + r));
@@ -378,10 +425,15 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = fmaf(v[e], f0, y[e] * f1);
                     }
-                    if (sick)
+                    if (sick) {
+                        // drafted tokens' values that are not finite, where they are weighed
+                        const uint32_t *mask = sees + (w.two ? 256 * k : 0) + th;
+                        const uint64_t mine = (uint64_t)mask[128] << 32 | mask[0];
+                        const unsigned long long *bad = nf + (pieces & 1) * D + ch;
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (bad[ch + e] & weighs) v[e] = __int_as_float(0x7fc00000);
+                            if (bad[e] & mine) v[e] = __int_as_float(0x7fc00000);
+                    }
                     if (r < w.rows) {
                         if (w.whole) {
                             uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at * D + ch);
@@ -399,7 +451,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
                         }
                     }
                 }
-                if (r < w.rows && (w.two || k == 0)) {
+                if (r < w.rows && half == 0 && (w.two || k == 0)) {
                     if (w.whole) {
                         if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : (mr + log2f(l)) * kLn2;
                     } else {
@@ -408,24 +460,23 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
                 }
             } else {   // a share that ends within a unit's start: nothing of it
                 const int64_t slot = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * kRb;
-                for (int x = tid; x < w.rows * (D / 4); x += 256) reinterpret_cast<float4 *>(a.part_o + slot * D)[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int x = tid; x < w.rows; x += 256) reinterpret_cast<float2 *>(a.part_ml + 2 * slot)[x] = make_float2(-INFINITY, 0.f);
+                for (int x = tid; x < w.rows * (D / 4); x += 512) reinterpret_cast<float4 *>(a.part_o + slot * D)[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int x = tid; x < w.rows; x += 512) reinterpret_cast<float2 *>(a.part_ml + 2 * slot)[x] = make_float2(-INFINITY, 0.f);
             }
             if (stale) {   // the next piece starts with a clean slate
-                for (int x = tid; x < D; x += 256) nf[((pieces + 1) & 1) * D + x] = 0;
+                for (int x = tid; x < D; x += 512) nf[((pieces + 1) & 1) * D + x] = 0;
                 if (tid == 0) nf_any[(pieces + 1) & 1] = 0;
             }
             tc_fence_before();
-            ok = meet();                                   // (the other chain has read its outputs, masks and sums)
-            if (!ok) break;
+            ok = meet();                                   // (the others have read this thread's outputs, masks and sums)
             tiles += w.c;
             loads += 2 * w.c;
             ++pieces;
             if (!w.next(a)) break;
         }
-    } else if (warp != 9) {
-        // ---- loads: the three warps take the same steps; warp 8 alone issues TMA
-        const int wi = warp == 8 ? 0 : warp - 9;
+    } else if (warp >= 18) {
+        // ---- loads: the two warps take the same steps; the first alone issues TMA
+        const int wi = warp - 18;
         constexpr int CH = D / 8, RPI = 32 / CH;            // 16-byte chunks of a row, rows of a warp's instruction
         const __nv_bfloat16 *kc = static_cast<const __nv_bfloat16 *>(p.k_cache), *vc = static_cast<const __nv_bfloat16 *>(p.v_cache);
         uint32_t load = 0, qs = 0, tiles = 0;
@@ -559,71 +610,84 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
         }
         while (queued > 0) report();
     } else {
-        // ---- products; an elected lane issues
+        // ---- products, a warp for each chain.  Both go through all loads in order: one that is the other chain's alone is
+        // awaited and released as well, so that no stage is ever two loads ahead of what a warp waits for.
+        // The whole warp runs the loop and an elected lane issues, so that the operand descriptors can stay in
+        // uniform registers.
+        const int k = warp - 16;
         const uint32_t one = elect_one();
-        uint32_t loads = 0, qs = 0, made[2] = {0, 0}, used[2] = {0, 0};   // loads, pieces, scores and weights so far
-        const uint64_t qd = sdesc_sw128(sb + L::Q), kd = sdesc_sw128(sb + L::RING), vd = sdesc_sw128_mn(sb + L::RING, HALF, 1024);
+        uint32_t loads = 0, qs = 0, made = 0, used = 0;   // loads, pieces, scores and weights so far
+        const uint32_t qd = ((sb + L::Q) >> 4) | (1u << 16), kd = ((sb + L::RING) >> 4) | (1u << 16), vd = ((sb + L::RING) >> 4) | ((HALF >> 4) << 16);
         for (;; ) {
             if (w.c > 0) {
-                // scores of chain k, tile i; `loaded`: the tile has been waited for, `last`: its last use
-                auto qk = [&](int k, int i, bool loaded, bool last) {
-                    const int ld = (int)loads + w.k_load(i), s = ld % S, b = 2 * k + (int)(made[k] & 1);
-                    ok = all(loaded || wait(kFull + s, ld / S));
+                const int ahead = w.ahead();
+                const uint32_t q0 = qd + (w.two ? k * (L::QTILE >> 4) : 0u);
+                auto mine = [&](int i) { return w.two || (i & 1) == k; };
+                auto pass = [&](uint32_t ld) {   // the other chain's
+                    const uint32_t s = ld % S;
+                    ok = all(wait(kFull + s, ld / S));
+                    if (ok && lane == 0) mbar_arrive(bar(kEmpty + s));
+                    return ok;
+                };
+                // scores of tile i
+                auto qk = [&](int i) {
+                    const uint32_t ld = loads + w.k_load(i), s = ld % S, b = 2 * k + (made & 1);
+                    if (!mine(i)) return pass(ld);
+                    ok = all(wait(kFull + s, ld / S));
                     if (!ok) return false;
                     tc_fence_after();
+                    const uint32_t to = tmem + TM_S + 64 * b, k0 = kd + s * (L::TILE >> 4);
                     if (one) {
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
-                            mma_f16_ss(tmem + TM_S + 64 * b, qd + (w.two ? k * (L::QTILE >> 4) : 0) + (((kk >> 2) * QHALF + (kk & 3) * 32) >> 4),
-                                       kd + s * (L::TILE >> 4) + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), IDESC_QK, kk > 0);
+                            mma_ss(to, q0 + (((kk >> 2) * QHALF + (kk & 3) * 32) >> 4), k0 + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), IDESC_QK, kk > 0);
                         mma_commit(bar(kS + b));
                         mbar_arrive(bar(kS + b));
-                        if (last) mma_commit(bar(kEmpty + s));
+                        mma_commit(bar(kEmpty + s));
                     }
                     __syncwarp();
-                    ++made[k];
+                    ++made;
                     return true;
                 };
-                // outputs of chain k, tile i, its j-th
-                auto pv = [&](int k, int i, int j, bool loaded, bool last) {
-                    const int ld = (int)loads + w.v_load(i), s = ld % S, b = 2 * k + (int)(used[k] & 1);
-                    ok = all((loaded || wait(kFull + s, ld / S)) && wait(kP + b, used[k] >> 1));
+                // outputs of tile i
+                auto pv = [&](int i) {
+                    const uint32_t ld = loads + w.v_load(i), s = ld % S, b = 2 * k + (used & 1);
+                    if (!mine(i)) return pass(ld);
+                    ok = all(wait(kFull + s, ld / S) && wait(kP + b, used >> 1));
                     if (!ok) return false;
                     tc_fence_after();
+                    const uint32_t to = tmem + TM_O + 128 * k, from = tmem + TM_S + 64 * b, v0 = vd + s * (L::TILE >> 4);
+                    const uint32_t more = w.two ? i > 0 : i > 1;   // not the chain's first tile
                     if (one) {
 #pragma unroll
                         for (int e = 1; e >= 0; --e)   // the rests first
 #pragma unroll
                             for (int kk = 0; kk < kKt / 16; ++kk)
-                                mma_f16_ts(tmem + TM_O + 128 * k, tmem + TM_S + 64 * b + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * e,
-                                           vd + s * (L::TILE >> 4) + ((2048 * kk) >> 4), IDESC_PV, j > 0 || e == 0 || kk > 0);
-                        if (last) mma_commit(bar(kEmpty + s));
+                                mma_ts(to, from + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * e, v0 + ((2048 * kk) >> 4), IDESC_PV, e == 0 || kk > 0 ? 1u : more);
+                        mma_commit(bar(kEmpty + s));
                         mma_commit(bar(kV + b));
                     }
                     __syncwarp();
-                    ++used[k];
+                    ++used;
                     return true;
                 };
                 ok = all(wait(kQFull, qs++));
                 if (!ok) break;
                 bool fine = true;
-                const int ahead = w.ahead();
-                auto made_last = [&](int i) {              // the piece's queries are read
-                    if (fine && i + 1 == w.c && one) mma_commit(bar(kQEmpty));
+                auto queries = [&](int made_all) {                // the piece's queries are read
+                    if (fine && made_all && one) mma_commit(bar(kQEmpty));
                     __syncwarp();
                 };
                 for (int i = 0; i < ahead && i < w.c && fine; ++i) {
-                    fine = w.two ? qk(0, i, false, false) && qk(1, i, true, true) : qk(i & 1, i, false, true);
-                    made_last(i);
+                    fine = qk(i);
+                    queries(i + 1 == w.c);
                 }
                 for (int i = 0; i < w.c && fine; ++i) {
-                    const int y = i + ahead;
-                    if (w.two) {
-                        fine = pv(0, i, i, false, false) && (y >= w.c || qk(0, y, false, false)) && pv(1, i, i, true, true) && (y >= w.c || qk(1, y, true, true));
-                    } else {
-                        fine = pv(i & 1, i, i >> 1, false, true) && (y >= w.c || qk(i & 1, y, false, true));
+                    fine = pv(i);
+                    if (fine && i + ahead < w.c) {
+                        fine = qk(i + ahead);
+                        queries(i + ahead + 1 == w.c);
                     }
-                    made_last(y);
                 }
                 if (!fine) break;
                 loads += 2 * w.c;
@@ -635,7 +699,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
         if (ok && qs > 0) ok = all(wait(kQEmpty, qs - 1));
     }
     __syncwarp();
-    if (!ok) s_fail = 1;
+    if (!ok) s_fail = 1;   // (where a chain has left together, one of its warps has given up)
     tc_fence_before();
     __syncthreads();
     if (s_fail) {
@@ -672,7 +736,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
         }
         __syncthreads();
     }
-    if (warp == 9) {
+    if (warp == 16) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);

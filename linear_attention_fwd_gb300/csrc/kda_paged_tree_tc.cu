@@ -12,9 +12,9 @@
 // m follows the running maximum only where that has grown by more than 2^8, which is rare after the first
 // tiles: then the chain's warpgroup waits for the last product into O and scales it in tensor memory.
 //
-// Tiles that lie whole on pages of a multiple of 8 tokens come by TMA, a box of tokens an instruction; others (the last
-// cached tokens, pages of other sizes, places without a token, which become zeros and whose scores are masked)
-// by cp.async of two warps.  (Gathers of four rows by TMA take 50 ns each, 6.5 us for 128 keys of 128
+// Tiles on pages of a multiple of 8 tokens come by TMA, a box of tokens an instruction, and so do the queries where a
+// power of two of heads shares a key/value head; others, and the drafted tokens, by cp.async of two warps.
+// Scores of places without a token are masked, their values made zero behind the load.  (Gathers of four rows by TMA take 50 ns each, 6.5 us for 128 keys of 128
 // channels: 131,071 tokens x 8 heads, 512 query rows: 700 us, 430 by boxes.)  The drafted tokens have a tile of their own,
 // masked by their paths.  A non-finite value among them is replaced by zero before the product (zero
 // times NaN would reach other branches) and put back as NaN in the outputs of the tokens that weigh it.
@@ -46,7 +46,7 @@ template <int D> struct Tc {
     static constexpr uint32_t TILE = kKt * D * 2, QTILE = 128 * D * 2;   // keys or values; query rows of a chain
     static constexpr int STAGES = D == 128 ? 9 : 16;
     static constexpr uint32_t Q = 0, RING = 2 * QTILE, BAR = RING + STAGES * TILE;
-    static constexpr uint32_t MASK = BAR + 512, ANC = MASK + 32 * 8, UP = ANC + 512, ML = UP + 256;
+    static constexpr uint32_t MASK = BAR + 512, ANC = MASK + 32 * 8, UP = ANC + 1024, ML = UP + 256;
     static constexpr uint32_t SEE = ML + 6 * 128 * 4, NF = SEE + 4 * 128 * 4, NFANY = NF + 2 * D * 8, TM = NFANY + 16;
     static constexpr uint32_t BYTES = TM + 16 + 1024;
     static_assert(BYTES <= 226 * 1024, "shared memory budget");
@@ -54,7 +54,7 @@ template <int D> struct Tc {
 // kS, kP and kV are of a chain and a buffer (2 k + b): scores, weights, outputs.  A wait names a phase by its parity, so a
 // barrier may be at most one phase behind what is waited for and none ahead.  That holds because the scores of a
 // chain's tile j follow the outputs of its tile j - 2, and those of tile j the weights that their waiter makes.
-enum Bar { kFull = 0, kEmpty = 16, kQFull = 32, kQEmpty = 33, kS = 34, kP = 38, kV = 42, kMeet = 46, kSane = 47, kBars = 48 };
+enum Bar { kFull = 0, kEmpty = 16, kQFull = 32, kQEmpty = 33, kS = 34, kP = 38, kV = 42, kMeet = 46, kBars = 47 };
 
 constexpr uint32_t TM_S = 0, TM_O = 256;   // + 128 for the second chain, + 64 for the second buffer
 
@@ -149,8 +149,8 @@ struct Walk {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const TreeAtt a, const int box,
-                         const uint32_t polls) {
+kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                         const TreeAtt a, const int qbox, const int box, const uint32_t polls) {
     using L = Tc<D>;
     constexpr int S = L::STAGES, HALVES = D / 64;
     constexpr uint32_t HALF = L::TILE / HALVES, QHALF = L::QTILE / HALVES;   // 64 channels of a tile's rows
@@ -197,7 +197,6 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
             mbar_init(bar(kV + x), 1);
         }
         mbar_init(bar(kMeet), 16);                 // both chains' warps
-        mbar_init(bar(kSane), 8);                  // the first chain's warps
         fence_mbar_init();
     }
     for (int x = tid; x < 2 * D; x += kThreads) nf[x] = 0;
@@ -217,11 +216,11 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
         const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float sc = p.scale * kLog2e;
         const float2 sc2 = make_float2(sc, sc);
-        const uint32_t *masks = reinterpret_cast<const uint32_t *>(sm + L::MASK);
-        uint64_t *anc = reinterpret_cast<uint64_t *>(sm + L::ANC);
+        const uint2 *masks = reinterpret_cast<const uint2 *>(sm + L::MASK);
+        const uint64_t *anc = reinterpret_cast<const uint64_t *>(sm + L::ANC);         // [piece's parity][token]
         float *tops = reinterpret_cast<float *>(sm + L::ML), *sums = tops + 2 * 128;   // [chain][row]; [chain][half][row]
         uint32_t *sees = reinterpret_cast<uint32_t *>(sm + L::SEE);                    // [chain][half][row]
-        uint32_t count = 0, meets = 0, sane = 0, tiles = 0, loads = 0, pieces = 0;   // jobs, barriers, tiles, loads and pieces so far
+        uint32_t count = 0, meets = 0, tiles = 0, loads = 0, pieces = 0;   // jobs, barriers, tiles, loads and pieces so far
         auto outputs = [&] { return all(wait(kV + 2 * k + (int)((count - 1) & 1), (count - 1) >> 1)); };   // of the chain's last tile
         auto meet = [&] {   // all 512 threads of the chains
             __syncwarp();
@@ -234,12 +233,6 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
         for (bool first = true;; first = false) {
             const bool has_draft = w.ta + w.c == w.row.tiles && w.c > 0;
             const int r = (w.two ? 128 * k : 0) + th;
-            uint32_t see = 0;                               // of this half's drafted tokens
-            if (has_draft) {
-                if (warp == 0) tree_masks(a, w.n, w.row.m, anc, reinterpret_cast<int *>(sm + L::UP));
-                ok = meet();
-                if (r < w.rows) see = (uint32_t)(anc[a.by_rep((uint32_t)(w.r0 + r))] >> (32 * half));
-            }
             uint32_t weighs = 0;                            // drafted tokens with a weight
             float mr = -INFINITY, l = 0.f;
             const int jobs = w.jobs(k);
@@ -251,10 +244,11 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
                 const uint32_t ts = trow + TM_S + 64 * b + 32 * half;
                 float v[32];
                 tmem_ld32(ts, v);
-                uint32_t in = masks[2 * ((tiles + i) & 31) + half];
-                const bool open = !draft && in == 0xffffffffu;
+                const uint2 here = masks[(tiles + i) & 31];   // places with a token
+                uint32_t in = half ? here.y : here.x;
+                const bool open = !draft && (here.x & here.y) == 0xffffffffu;   // (the same for the row's two threads)
                 if (!open) {
-                    if (draft) in &= see;
+                    if (draft) in &= r < w.rows ? (uint32_t)(anc[64 * (pieces & 1) + a.by_rep((uint32_t)(w.r0 + r))] >> (32 * half)) : 0u;
                     const float no = sc >= 0.f ? -INFINITY : INFINITY;
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = (in >> e) & 1u ? v[e] : no;
@@ -342,17 +336,19 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
                 }
                 tmem_st32(ts, u);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                if (draft && (k == 0 || !w.two)) {
-                    // the drafted tokens' values: what is not finite becomes zero
+                if (!open) {
+                    // values of places without a token become zero, and what is not finite among the drafted tokens' (by each
+                    // chain that reads them, so that neither waits for the other: the second finds or writes the same)
                     const int vl = (int)loads + w.v_load(i), st = vl % S;
                     ok = ok && all(wait(kFull + st, vl / S));
                     if (ok)
-                        for (int x = 128 * half + th; x < w.row.m * (D / 8); x += 256) {
+                        for (int x = 128 * half + th; x < kKt * (D / 8); x += 256) {
                             const int key = x / (D / 8), ch = x % (D / 8);
                             uint4 *at = reinterpret_cast<uint4 *>(sm + L::RING + st * L::TILE + (ch >> 3) * HALF + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
-                            uint4 y = *at;
+                            const bool token = ((key < 32 ? here.x : here.y) >> (key & 31)) & 1u;
+                            uint4 y = token && draft ? *at : make_uint4(0u, 0u, 0u, 0u);
                             uint32_t *q = &y.x;
-                            bool bad = false;
+                            bool bad = !token;
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -361,22 +357,11 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
                                         bad = true;
                                         q[e] &= g ? 0x0000ffffu : 0xffff0000u;
                                         atomicOr(nf + (pieces & 1) * D + 8 * ch + 2 * e + g, 1ull << key);
+                                        nf_any[pieces & 1] = 1;
                                     }
-                            if (bad) {
-                                *at = y;
-                                nf_any[pieces & 1] = 1;
-                                fence_async_smem();
-                            }
+                            if (bad) *at = y;
                         }
-                }
-                if (draft && w.two) {   // the second chain's product waits for that
-                    __syncwarp();
-                    if (k == 0) {
-                        if (lane == 0) mbar_arrive(bar(kSane));
-                    } else {
-                        ok = ok && all(wait(kSane, sane));
-                    }
-                    ++sane;
+                    fence_async_smem();
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -471,7 +456,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
             ok = meet();                                   // (the others have read this thread's outputs, masks and sums)
             tiles += w.c;
             loads += 2 * w.c;
-            ++pieces;
+            pieces += w.c > 0;
             if (!w.next(a)) break;
         }
     } else if (warp >= 18) {
@@ -479,7 +464,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
         const int wi = warp - 18;
         constexpr int CH = D / 8, RPI = 32 / CH;            // 16-byte chunks of a row, rows of a warp's instruction
         const __nv_bfloat16 *kc = static_cast<const __nv_bfloat16 *>(p.k_cache), *vc = static_cast<const __nv_bfloat16 *>(p.v_cache);
-        uint32_t load = 0, qs = 0, tiles = 0;
+        uint32_t load = 0, pieces = 0, tiles = 0;
         // Loads by cp.async that have not been reported yet (barriers, eight bits each, the oldest lowest): they are once
         // they have landed, before this warp waits for anything, and when there are four of them.
         uint32_t queue = 0;
@@ -509,44 +494,44 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
             }
             return ok;
         };
+        // Places of a tile's tokens `lane` and 32 + lane, -1 for none.  Their pages are fetched a step before they are needed.
         struct Place {
-            bool box;         // a full tile: at[0] is the first token of this lane's box
-            int at[2];        // else the places of tokens `lane` and 32 + lane, -1 for none
+            int at[2];
             uint2 mask;
         };
         for (;; ) {
             if (w.c > 0) {
                 const int32_t *table = p.table + (int64_t)w.n * p.max_pages;
-                auto places = [&](int i) {
-                    Place x;
+                auto fetch = [&](int i) {
                     const int t = w.ta + i;
                     const bool draft = t == w.row.ctx;
-                    const int base = draft ? w.row.len : t * kKt, left = draft ? w.row.m : w.row.len - base;
-                    if (box && !draft && left >= kKt) {
-                        x.at[0] = lane * box < kKt ? (int)tree_place(a, table, base + lane * box) : 0;
-                        if (all(x.at[0] >= 0)) {
-                            x.box = true;
-                            x.mask = make_uint2(0xffffffffu, 0xffffffffu);
-                            return x;
-                        }
-                    }
-                    x.box = false;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) x.at[e] = lane + 32 * e < left ? (int)tree_place(a, table, base + lane + 32 * e) : -1;
-                    x.mask = make_uint2(__ballot_sync(0xffffffffu, x.at[0] >= 0), __ballot_sync(0xffffffffu, x.at[1] >= 0));
+                    const int base = draft ? w.row.len : t * kKt, left = i < w.c ? (draft ? w.row.m : w.row.len - base) : 0;
+                    int2 x;
+                    x.x = lane < left ? (int)tree_place(a, table, base + lane) : -1;
+                    x.y = lane + 32 < left ? (int)tree_place(a, table, base + lane + 32) : -1;
                     return x;
                 };
-                auto tile = [&](const CUtensorMap *map, const __nv_bfloat16 *cache, const Place &x) {
+                auto place = [&](int2 y) {
+                    Place x;
+                    x.at[0] = y.x, x.at[1] = y.y;
+                    x.mask = make_uint2(__ballot_sync(0xffffffffu, y.x >= 0), __ballot_sync(0xffffffffu, y.y >= 0));
+                    return x;
+                };
+                auto tile = [&](const CUtensorMap *map, const __nv_bfloat16 *cache, const Place &x, int i) {
                     const int s = load % S, full = kFull + s;
                     if (load >= S && !reach(kEmpty + s, load / S - 1)) return false;
                     const uint32_t to = sb + L::RING + s * L::TILE;
-                    if (x.box) {
+                    if (box && w.ta + i != w.row.ctx) {
+                        // boxes: of the places without a token, scores are masked and values made zero behind the load
+                        const int t0 = lane * box;                    // this lane's box: its first token is there
+                        const int a0 = __shfl_sync(0xffffffffu, x.at[0], t0 & 31), a1 = __shfl_sync(0xffffffffu, x.at[1], t0 & 31), at = t0 < 32 ? a0 : a1;
+                        const uint32_t boxes = __ballot_sync(0xffffffffu, t0 < kKt && at >= 0);
                         if (wi == 0) {
-                            if (lane == 0) mbar_arrive_expect_tx(bar(full), L::TILE);
+                            if (lane == 0) mbar_arrive_expect_tx(bar(full), __popc(boxes) * box * D * 2);
                             __syncwarp();
-                            if (lane * box < kKt)
+                            if ((boxes >> lane) & 1u)
 #pragma unroll
-                                for (int h = 0; h < HALVES; ++h) tma_load_3d(to + h * HALF + lane * box * 128, map, bar(full), 64 * h, w.hk, x.at[0]);
+                                for (int h = 0; h < HALVES; ++h) tma_load_3d(to + h * HALF + t0 * 128, map, bar(full), 64 * h, w.hk, at);
                         } else if (lane == 0) {
                             mbar_arrive(bar(full));
                         }
@@ -564,35 +549,58 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
                     return true;
                 };
                 auto keys = [&](int i, const Place &x) {
-                    if (wi == 0 && lane == 0) *reinterpret_cast<uint2 *>(sm + L::MASK + 8 * ((tiles + i) & 31)) = x.mask;
+                    if (wi == 0) {
+                        if (w.ta + i == w.row.ctx)       // the drafted tokens' paths
+                            tree_masks(a, w.n, w.row.m, reinterpret_cast<uint64_t *>(sm + L::ANC) + 64 * (pieces & 1), reinterpret_cast<int *>(sm + L::UP));
+                        if (lane == 0) *reinterpret_cast<uint2 *>(sm + L::MASK + 8 * ((tiles + i) & 31)) = x.mask;
+                    }
                     __syncwarp();
-                    return tile(&tmk, kc, x);
+                    return tile(&tmk, kc, x, i);
                 };
-                // the queries
-                if (qs > 0 && !reach(kQEmpty, qs - 1)) break;
-                ++qs;
-                for (int y = wi; y < (w.two ? 256 : 128) / RPI; y += kLoaders) {
-                    const int r = y * RPI + lane / CH, c = lane % CH, i = (int)a.by_rep((uint32_t)(w.r0 + r));
-                    const bool in = r < w.rows;
-                    const int64_t at = in ? ((int64_t)w.n * a.t.tokens + i) * p.heads + w.hk * a.rep + (w.r0 + r - i * a.rep) : 0;
-                    cp16(sb + L::Q + (r >> 7) * L::QTILE + (c >> 3) * QHALF + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
-                         static_cast<const __nv_bfloat16 *>(p.q) + at * D + 8 * c, in ? 16u : 0u);
-                }
-                sent(kQFull);
-                // keys `ahead` tiles ahead of the values; a tile's places are kept until its values are loaded
                 const int ahead = w.ahead();
+                int2 first[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) first[i] = fetch(i);
+                // the queries
+                if (pieces > 0 && !reach(kQEmpty, pieces - 1)) break;
+                if (qbox) {
+                    if (wi == 0) {
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(bar(kQFull), (w.two ? 2 : 1) * L::QTILE);
+                            const int at = w.n * a.t.tokens + (int)a.by_rep((uint32_t)w.r0);
+                            for (int e = 0; e < (w.two ? 2 : 1); ++e)
+#pragma unroll
+                                for (int h = 0; h < HALVES; ++h) tma_load_3d(sb + L::Q + e * L::QTILE + h * QHALF, &tmq, bar(kQFull), 64 * h, w.hk * a.rep, at + e * qbox);
+                        }
+                    } else if (lane == 0) {
+                        mbar_arrive(bar(kQFull));
+                    }
+                    __syncwarp();
+                } else {
+                    for (int y = wi; y < (w.two ? 256 : 128) / RPI; y += kLoaders) {
+                        const int r = y * RPI + lane / CH, c = lane % CH, i = (int)a.by_rep((uint32_t)(w.r0 + r));
+                        const bool in = r < w.rows;
+                        const int64_t at = in ? ((int64_t)w.n * a.t.tokens + i) * p.heads + w.hk * a.rep + (w.r0 + r - i * a.rep) : 0;
+                        cp16(sb + L::Q + (r >> 7) * L::QTILE + (c >> 3) * QHALF + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
+                             static_cast<const __nv_bfloat16 *>(p.q) + at * D + 8 * c, in ? 16u : 0u);
+                    }
+                    sent(kQFull);
+                }
+                // keys `ahead` tiles ahead of the values; a tile's places are kept until its values are loaded
                 Place x[5];
                 bool fine = true;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (i < ahead && i < w.c && fine) {
-                        x[i] = places(i);
+                        x[i] = place(first[i]);
                         fine = keys(i, x[i]);
                     }
+                int2 next = ahead == 2 ? first[2] : fetch(4);
                 for (int i = 0; i < w.c && fine; ++i) {
                     const bool more = i + ahead < w.c;
-                    if (more) x[4] = places(i + ahead);
-                    fine = tile(&tmv, vc, x[0]) && (!more || keys(i + ahead, x[4]));
+                    if (more) x[4] = place(next);
+                    next = fetch(i + ahead + 1);
+                    fine = tile(&tmv, vc, x[0], i) && (!more || keys(i + ahead, x[4]));
                     if (ahead == 2) {
                         x[0] = x[1];
                         x[1] = x[4];
@@ -605,6 +613,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
                 }
                 if (!fine) break;
                 tiles += w.c;
+                ++pieces;
             }
             if (!w.next(a)) break;
         }
@@ -754,13 +763,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// [tokens][kv_heads][d] bf16 as (d, kv_heads, tokens): boxes of 64 channels of one head and `box` tokens, in the same layout.
-bool make_map(CUtensorMap *m, const void *ptr, int64_t tokens, int heads, int d, int box) {
+// [tokens][heads][d] bf16 as (d, heads, tokens): boxes of 64 channels of `of` heads and `box` tokens, 128-byte swizzle; what lies
+// past the tensor is zeros.
+bool make_map(CUtensorMap *m, const void *ptr, int64_t tokens, int heads, int d, int of, int box) {
     auto enc = encode_fn();
     if (enc == nullptr) return false;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
     cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
-    cuuint32_t boxes[3] = {64, 1, (cuuint32_t)box};
+    cuuint32_t boxes[3] = {64, (cuuint32_t)of, (cuuint32_t)box};
     cuuint32_t es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -775,18 +785,21 @@ int tc_ctas(const PagedTreeArgs &t) {
 }
 
 template <int D> cudaError_t launch_tc(const TreeAtt &a, int ctas, uint32_t polls, cudaStream_t st) {
-    CUtensorMap mk, mv;
+    CUtensorMap mq, mk, mv;
     const PagedArgs &p = a.t.p;
     // tokens of a box: the largest power of two that divides the pages, of eight rows (a swizzle's period) at least
     int box = kKt;
     while (p.page_size % box) box /= 2;
     if (box < 8) box = 0;
+    // the queries of 128 rows are a box where whole tokens make up 128 rows (those of the next row's tokens are not written)
+    const int qbox = 128 % a.rep == 0 ? 128 / a.rep : 0;
     const int64_t cached = (int64_t)p.pages * p.page_size;
-    if (!make_map(&mk, p.k_cache, cached, p.kv_heads, D, box ? box : 8) || !make_map(&mv, p.v_cache, cached, p.kv_heads, D, box ? box : 8))
+    if (!make_map(&mq, p.q, (int64_t)p.rows * a.t.tokens, p.heads, D, qbox ? a.rep : 1, qbox ? qbox : 8) ||
+        !make_map(&mk, p.k_cache, cached, p.kv_heads, D, 1, box ? box : 8) || !make_map(&mv, p.v_cache, cached, p.kv_heads, D, 1, box ? box : 8))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(kda_paged_tree_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tc<D>::BYTES);
     if (e != cudaSuccess) return e;
-    kda_paged_tree_tc_kernel<D><<<ctas, kThreads, Tc<D>::BYTES, st>>>(mk, mv, a, box, polls);
+    kda_paged_tree_tc_kernel<D><<<ctas, kThreads, Tc<D>::BYTES, st>>>(mq, mk, mv, a, qbox, box, polls);
     e = cudaGetLastError();
     return e != cudaSuccess || ctas == 1 ? e : launch_tree_join(a, D, KDA_BF16, ctas, st);   // (one CTA: nothing is split)
 }

@@ -494,15 +494,24 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
             }
             return ok;
         };
-        // Places of a tile's tokens `lane` and 32 + lane, -1 for none.  Their pages are fetched a step before they are needed.
         struct Place {
-            int at[2];
-            uint2 mask;
+            int at[2];        // by boxes: the place of this lane's box, -1 for none; else of tokens `lane` and 32 + lane
+            uint2 mask;       // places with a token
         };
         for (;; ) {
             if (w.c > 0) {
                 const int32_t *table = p.table + (int64_t)w.n * p.max_pages;
-                auto fetch = [&](int i) {
+                const int boxes = box ? kKt / box : 0;                      // of a tile, 8 at most
+                auto by_box = [&](int i) { return box && w.ta + i != w.row.ctx; };
+                // Pages are fetched well before they are needed: by boxes, those of four tiles by one load (eight lanes a tile), four
+                // tiles ahead; else a tile's, a tile ahead.
+                auto group_token = [&](int g) { return (w.ta + 4 * g + (lane >> 3)) * kKt + (lane & 7) * box; };
+                auto group_page = [&](int g) {
+                    const int t = group_token(g);
+                    if ((lane & 7) >= boxes || 4 * g + (lane >> 3) >= w.c || t >= w.row.len) return -1;
+                    return __ldg(table + a.by_page((uint32_t)t));           // (t is below the table's width)
+                };
+                auto tokens = [&](int i) {
                     const int t = w.ta + i;
                     const bool draft = t == w.row.ctx;
                     const int base = draft ? w.row.len : t * kKt, left = i < w.c ? (draft ? w.row.m : w.row.len - base) : 0;
@@ -511,27 +520,47 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                     x.y = lane + 32 < left ? (int)tree_place(a, table, base + lane + 32) : -1;
                     return x;
                 };
-                auto place = [&](int2 y) {
+                int group = -1, page = box ? group_page(0) : -1;            // places of the current four tiles; pages of the next
+                int2 pre = tokens(box ? (w.ta + w.c > w.row.ctx ? w.c - 1 : w.c) : 0);   // (by boxes: the drafted tokens, where they are here)
+                auto place = [&](int i) {                                   // asked for in order
                     Place x;
-                    x.at[0] = y.x, x.at[1] = y.y;
-                    x.mask = make_uint2(__ballot_sync(0xffffffffu, y.x >= 0), __ballot_sync(0xffffffffu, y.y >= 0));
+                    if (by_box(i)) {
+                        if ((i & 3) == 0) {
+                            const int t = group_token(i >> 2), pg = (int)a.by_page((uint32_t)t);
+                            group = page >= 0 && page < p.pages ? page * p.page_size + (t - pg * p.page_size) : -1;
+                            page = group_page((i >> 2) + 1);
+                        }
+                        const int at = __shfl_sync(0xffffffffu, group, (i & 3) * 8 + (lane & 7));
+                        x.at[0] = lane < boxes ? at : -1;
+                        x.at[1] = -1;
+                        const uint32_t have = __ballot_sync(0xffffffffu, x.at[0] >= 0);
+                        const int left = w.row.len - (w.ta + i) * kKt;
+                        x.mask = make_uint2(0xffffffffu, 0xffffffffu);
+                        if (have != (1u << boxes) - 1 || left < kKt) {
+                            const int per = __ffs(box) - 1;                 // (a power of two)
+                            x.mask.x = __ballot_sync(0xffffffffu, lane < left && ((have >> (lane >> per)) & 1u));
+                            x.mask.y = __ballot_sync(0xffffffffu, lane + 32 < left && ((have >> ((lane + 32) >> per)) & 1u));
+                        }
+                        return x;
+                    }
+                    x.at[0] = pre.x, x.at[1] = pre.y;
+                    x.mask = make_uint2(__ballot_sync(0xffffffffu, pre.x >= 0), __ballot_sync(0xffffffffu, pre.y >= 0));
+                    if (!box) pre = tokens(i + 1);
                     return x;
                 };
                 auto tile = [&](const CUtensorMap *map, const __nv_bfloat16 *cache, const Place &x, int i) {
                     const int s = load % S, full = kFull + s;
                     if (load >= S && !reach(kEmpty + s, load / S - 1)) return false;
                     const uint32_t to = sb + L::RING + s * L::TILE;
-                    if (box && w.ta + i != w.row.ctx) {
-                        // boxes: of the places without a token, scores are masked and values made zero behind the load
-                        const int t0 = lane * box;                    // this lane's box: its first token is there
-                        const int a0 = __shfl_sync(0xffffffffu, x.at[0], t0 & 31), a1 = __shfl_sync(0xffffffffu, x.at[1], t0 & 31), at = t0 < 32 ? a0 : a1;
-                        const uint32_t boxes = __ballot_sync(0xffffffffu, t0 < kKt && at >= 0);
+                    if (by_box(i)) {
+                        // (of the places without a token, scores are masked and values made zero behind the load)
+                        const uint32_t have = __ballot_sync(0xffffffffu, x.at[0] >= 0);
                         if (wi == 0) {
-                            if (lane == 0) mbar_arrive_expect_tx(bar(full), __popc(boxes) * box * D * 2);
+                            if (lane == 0) mbar_arrive_expect_tx(bar(full), __popc(have) * box * D * 2);
                             __syncwarp();
-                            if ((boxes >> lane) & 1u)
+                            if (x.at[0] >= 0)
 #pragma unroll
-                                for (int h = 0; h < HALVES; ++h) tma_load_3d(to + h * HALF + t0 * 128, map, bar(full), 64 * h, w.hk, at);
+                                for (int h = 0; h < HALVES; ++h) tma_load_3d(to + h * HALF + lane * box * 128, map, bar(full), 64 * h, w.hk, x.at[0]);
                         } else if (lane == 0) {
                             mbar_arrive(bar(full));
                         }
@@ -549,18 +578,13 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                     return true;
                 };
                 auto keys = [&](int i, const Place &x) {
-                    if (wi == 0) {
-                        if (w.ta + i == w.row.ctx)       // the drafted tokens' paths
-                            tree_masks(a, w.n, w.row.m, reinterpret_cast<uint64_t *>(sm + L::ANC) + 64 * (pieces & 1), reinterpret_cast<int *>(sm + L::UP));
-                        if (lane == 0) *reinterpret_cast<uint2 *>(sm + L::MASK + 8 * ((tiles + i) & 31)) = x.mask;
-                    }
+                    if (wi == 1 && w.ta + i == w.row.ctx)   // the drafted tokens' paths
+                        tree_masks(a, w.n, w.row.m, reinterpret_cast<uint64_t *>(sm + L::ANC) + 64 * (pieces & 1), reinterpret_cast<int *>(sm + L::UP));
+                    if (wi == 0 && lane == 0) *reinterpret_cast<uint2 *>(sm + L::MASK + 8 * ((tiles + i) & 31)) = x.mask;
                     __syncwarp();
                     return tile(&tmk, kc, x, i);
                 };
                 const int ahead = w.ahead();
-                int2 first[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) first[i] = fetch(i);
                 // the queries
                 if (pieces > 0 && !reach(kQEmpty, pieces - 1)) break;
                 if (qbox) {
@@ -592,14 +616,12 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (i < ahead && i < w.c && fine) {
-                        x[i] = place(first[i]);
+                        x[i] = place(i);
                         fine = keys(i, x[i]);
                     }
-                int2 next = ahead == 2 ? first[2] : fetch(4);
                 for (int i = 0; i < w.c && fine; ++i) {
                     const bool more = i + ahead < w.c;
-                    if (more) x[4] = place(next);
-                    next = fetch(i + ahead + 1);
+                    if (more) x[4] = place(i + ahead);
                     fine = tile(&tmv, vc, x[0], i) && (!more || keys(i + ahead, x[4]));
                     if (ahead == 2) {
                         x[0] = x[1];

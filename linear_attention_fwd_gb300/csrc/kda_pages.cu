@@ -66,83 +66,117 @@ __global__ void __launch_bounds__(kCommitThreads) kda_paged_tree_commit_kernel(c
 }
 
 // ------------------------------------------------------------------ tables and counts
-// One cluster of CTAs does a call: its CTAs split the pages and the table between them, meet at cluster barriers, and read
-// one another's bitmap of free pages and prefix sums through distributed shared memory, so that a call is
-// one launch without a workspace.
+// One cluster of CTAs does a call: its CTAs split the pages and the rows between them, meet at cluster barriers, and exchange
+// their bitmaps of free pages with prefix sums over blocks and words through distributed shared memory, so that a
+// call is one launch without a workspace.  Bound by its chains of dependent reads (row, length, page, count) and by the
+// barriers: what a row needs is gathered by a thread each before warps go over its entries.
 constexpr int kPoolThreads = 1024, kPoolWarps = kPoolThreads / 32, kBlock = 1024;   // pages of a block: 32 words of the bitmap
-constexpr int kMaxCtas = 8;
+constexpr int kMaxCtas = 16, kLocalPages = 1 << 18, kLocalRows = 8192, kBatch = 1024;
 
 struct PoolPlan {
-    int ctas, blocks;          // CTAs; blocks of pages per CTA
-    int chunk, per_row, segs;  // entries of a segment of a row; segments of a row; per CTA
+    int ctas, blocks, all;     // CTAs; blocks of pages per CTA; all blocks where every CTA keeps the whole bitmap, else 0
+    int rows;                  // rows per CTA
+    int chunk, per_row;        // entries of a segment of a row; segments of a row
+    int first;                 // rows where their first continuing row is found in shared memory, else 0
+    int vec;                   // four entries of a table lie on 16 bytes
     int smem;
 };
 
+// A bitmap of free pages: words, free pages before each word within its block, and before each block.
+struct Bitmap {
+    uint32_t *words;
+    uint16_t *in_block;
+    int *blk;
+    __device__ __forceinline__ Bitmap(uint8_t *at, int blocks)
+        : words(reinterpret_cast<uint32_t *>(at)), in_block(reinterpret_cast<uint16_t *>(at + 128 * blocks)), blk(reinterpret_cast<int *>(at + 192 * blocks)) {}
+};
+__host__ __device__ constexpr int bitmap_bytes(int blocks) { return 192 * blocks + 4 * (blocks + 1); }
+
 struct Pool {
     cg::cluster_group cluster;
-    uint32_t *words;           // of this CTA's blocks: bit set: free
-    int *blk;                  // free pages before each block (within the CTA); [blocks]: all
-    int *totals;               // free pages; requests
-    int before[kMaxCtas + 1];  // free pages before each CTA's blocks
-    int blocks;
+    Bitmap mine, whole;        // of this CTA's blocks; of all
+    const int *before;         // (shared) free pages before each CTA's blocks, [kMaxCtas]: all
+    int blocks, all;
 
+    __device__ __forceinline__ int free_pages() const { return before[kMaxCtas]; }
     // The number of free pages before page p.
     __device__ int free_before(int p) const {
-        const int b = p / kBlock, c = b / blocks, lb = b - c * blocks;
-        const uint32_t *w = cluster.map_shared_rank(words, c) + lb * 32;
-        int x = before[c] + cluster.map_shared_rank(blk, c)[lb];
-        const int word = (p % kBlock) / 32;
-        for (int i = 0; i < word; ++i) x += __popc(w[i]);
-        return x + __popc(w[word] & ((1u << (p % 32)) - 1));
+        const int b = p / kBlock, word = (p % kBlock) / 32;
+        const uint32_t below = (1u << (p % 32)) - 1;
+        if (all) return whole.blk[b] + whole.in_block[32 * b + word] + __popc(whole.words[32 * b + word] & below);
+        const int c = b / blocks, at = 32 * (b - c * blocks) + word;
+        return before[c] + cluster.map_shared_rank(mine.blk, c)[b - c * blocks] + cluster.map_shared_rank(mine.in_block, c)[at] +
+               __popc(cluster.map_shared_rank(mine.words, c)[at] & below);
     }
-    // The k-th free page (k < their number).
-    __device__ int nth_free(int k) const {
-        int c = 0;
-        while (k >= before[c + 1]) ++c;
-        k -= before[c];
-        const int *pre = cluster.map_shared_rank(blk, c);
-        int lo = 0, hi = blocks;   // pre[lo] <= k < pre[hi]
-        while (hi - lo > 1) {
+    // The k-th free page (k < their number).  (Not inlined: a short kernel's time is largely that of fetching its code.)
+    __device__ __noinline__ int nth_free(int k) const {
+        int c = 0, n = all;
+        const int *pre = whole.blk;
+        const uint16_t *in_block = whole.in_block;
+        const uint32_t *words = whole.words;
+        if (!all) {
+            while (k >= before[c + 1]) ++c;
+            k -= before[c];
+            n = blocks;
+            pre = cluster.map_shared_rank(mine.blk, c);
+            in_block = cluster.map_shared_rank(mine.in_block, c);
+            words = cluster.map_shared_rank(mine.words, c);
+        }
+        int lo = 0;   // pre[lo] <= k < pre[hi]
+        for (int hi = n; hi - lo > 1;) {
             const int mid = (lo + hi) / 2;
             if (pre[mid] <= k) lo = mid;
             else hi = mid;
         }
         k -= pre[lo];
-        const uint32_t *w = cluster.map_shared_rank(words, c) + lo * 32;
-        int i = 0;
-        uint32_t x = w[0];
-        for (int y = __popc(x); k >= y; y = __popc(x)) {
-            k -= y;
-            x = w[++i];
+        int w = 0;
+#pragma unroll
+        for (int step = 16; step > 0; step /= 2)
+            if (in_block[32 * lo + w + step] <= k) w += step;
+        k -= in_block[32 * lo + w];
+        uint32_t x = words[32 * lo + w];
+        int at = 0;
+#pragma unroll
+        for (int step = 16; step > 0; step /= 2) {   // the k-th bit set
+            const int n_low = __popc(x & ((1u << step) - 1));
+            if (k >= n_low) {
+                k -= n_low;
+                x >>= step;
+                at += step;
+            }
         }
-        for (; k > 0; --k) x &= x - 1;
-        return (c * blocks + lo) * kBlock + 32 * i + __ffs(x) - 1;
+        return (c * blocks + lo) * kBlock + 32 * w + at;
     }
 };
 
-// The bitmap of this CTA's pages (a warp per block); each page's count goes to `each`.
+// The bitmap of this CTA's pages, eight words a warp; `each` sees every page's count.  Block-wide.
 template <typename F> __device__ __forceinline__ void scan_pages(const ForkArgs &a, Pool &P, F each) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int b = warp; b < P.blocks; b += kPoolWarps) {
-        const int64_t p0 = ((int64_t)P.cluster.block_rank() * P.blocks + b) * kBlock + lane;
-        int sum = 0;
-        for (int w0 = 0; w0 < 32; w0 += 8) {
-            int r[8];
+    for (int u = warp; u < 4 * P.blocks; u += kPoolWarps) {
+        const int64_t p0 = (int64_t)P.cluster.block_rank() * P.blocks * kBlock + 256 * (int64_t)u + lane;
+        int r[8];
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const int64_t p = p0 + 32 * (w0 + w);
-                r[w] = p < a.pages ? __ldg(a.refs + p) : 1;
-            }
+        for (int w = 0; w < 8; ++w) r[w] = p0 + 32 * w < a.pages ? __ldg(a.refs + p0 + 32 * w) : 1;
+        uint32_t own = 0;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const uint32_t bits = __ballot_sync(0xffffffffu, r[w] == 0);
-                if (lane == 0) P.words[32 * b + w0 + w] = bits;
-                sum += __popc(bits);
-                const int64_t p = p0 + 32 * (w0 + w);
-                if (p < a.pages) each((int)p, r[w]);
-            }
+        for (int w = 0; w < 8; ++w) {
+            const uint32_t bits = __ballot_sync(0xffffffffu, r[w] == 0);
+            if (lane == w) own = bits;
+            if (p0 + 32 * w < a.pages) each((int)(p0 + 32 * w), r[w]);
         }
-        if (lane == 0) P.blk[b] = sum;
+        if (lane < 8) P.mine.words[8 * u + lane] = own;
+    }
+    __syncthreads();
+    for (int b = warp; b < P.blocks; b += kPoolWarps) {
+        const int n = __popc(P.mine.words[32 * b + lane]);
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        P.mine.in_block[32 * b + lane] = (uint16_t)(sum - n);
+        if (lane == 31) P.mine.blk[b] = sum;
     }
 }
 
@@ -164,218 +198,312 @@ __device__ __forceinline__ int scan_warp(int *x, int n) {
     return run;
 }
 
-__device__ __forceinline__ Pool make_pool(const PoolPlan &plan, uint8_t *sm, int *totals) {
-    Pool P{cg::this_cluster()};
-    P.blocks = plan.blocks;
-    P.words = reinterpret_cast<uint32_t *>(sm);
-    P.blk = reinterpret_cast<int *>(P.words + 32 * plan.blocks);
-    P.totals = totals;
-    return P;
-}
-// After a cluster barrier behind the CTAs' totals.
-__device__ __forceinline__ void meet(Pool &P, const PoolPlan &plan) {
-    int x = 0;
-#pragma unroll
-    for (int c = 0; c < kMaxCtas; ++c) {
-        P.before[c] = x;
-        x += c < plan.ctas ? P.cluster.map_shared_rank(P.totals, c)[0] : 0;
-    }
-    P.before[kMaxCtas] = x;
+// A barrier of all CTAs.
+__device__ __forceinline__ void pool_sync(Pool &P, const PoolPlan &plan) {
+    if (plan.ctas > 1) P.cluster.sync();
+    else __syncthreads();
 }
 
-// An entry of the new table, before free pages are given out.
+__device__ __forceinline__ Pool make_pool(const PoolPlan &plan, uint8_t *&sm) {
+    Bitmap mine(sm, plan.blocks);
+    sm += bitmap_bytes(plan.blocks);
+    Bitmap whole(sm, plan.all);
+    if (plan.all) sm += bitmap_bytes(plan.all);
+    Pool P{cg::this_cluster(), mine, plan.ctas == 1 ? mine : whole};
+    P.blocks = plan.blocks;
+    P.all = plan.all;
+    return P;
+}
+// The CTAs' totals (free pages; pages asked for), and theirs before each CTA.
+struct Totals {
+    int mine[2], free_before[kMaxCtas + 1];
+    long long asked, ahead;   // by all CTAs, by those before this one
+};
+// Behind the CTAs' own bitmaps and totals: takes over what the others have.  Block-wide, with a barrier of all CTAs.
+__device__ __forceinline__ void meet(Pool &P, const PoolPlan &plan, Totals &t) {
+    pool_sync(P, plan);
+    const int lane = threadIdx.x & 31, rank = (int)P.cluster.block_rank();
+    if (threadIdx.x < 32) {
+        const int *other = lane < plan.ctas ? P.cluster.map_shared_rank(t.mine, lane) : nullptr;
+        const int free = other ? other[0] : 0, asked = other ? other[1] : 0;
+        int f = free;
+        long long s = asked;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, f, o);
+            const long long z = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) f += y, s += z;
+        }
+        if (lane < kMaxCtas) t.free_before[lane] = f - free;
+        if (lane == 31) t.free_before[kMaxCtas] = f, t.asked = s;
+        if (lane == rank) t.ahead = s - asked;
+    }
+    P.before = t.free_before;
+    __syncthreads();
+    if (!plan.all || plan.ctas == 1) return;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < plan.all * 32; i += kPoolThreads) {
+        const int c = i / (32 * plan.blocks), at = i - c * 32 * plan.blocks;
+        P.whole.words[i] = P.cluster.map_shared_rank(P.mine.words, c)[at];
+        P.whole.in_block[i] = P.cluster.map_shared_rank(P.mine.in_block, c)[at];
+        if (at % 32 == 0) P.whole.blk[i / 32] = P.before[c] + P.cluster.map_shared_rank(P.mine.blk, c)[at / 32];
+    }
+    if (threadIdx.x == 0) P.whole.blk[plan.all] = P.free_pages();
+    __syncthreads();
+}
+
+// A row of the new table.
 struct NewRow {
     int src, len, full, need;   // the old row (-1: none), its length, pages that it fills, entries that have to name a page
-    bool heir, copy;            // the first row that continues src; its last page is copied
-    __device__ __forceinline__ NewRow(const ForkArgs &a, const FastDiv &by_page, int n) {
-        src = __ldg(a.sources + n);
-        if (src < 0 || src >= a.rows) src = -1;
-        len = full = need = 0;
-        heir = copy = false;
-        if (src < 0) return;
-        const int most = a.max_pages * a.page_size;
-        len = __ldg(a.lens + src);
-        len = len < 0 ? 0 : (len > most ? most : len);
-        full = (int)by_page((uint32_t)len);
-        const int more = a.new_tokens ? __ldg(a.new_tokens + n) : 0;
-        const int64_t end = (int64_t)len + (more > 0 ? more : 0);
-        need = a.max_pages;
-        if (end < most) {
-            need = (int)by_page((uint32_t)end);
-            need += end > (int64_t)need * a.page_size;
-        }
-    }
-    __device__ __forceinline__ bool part(const ForkArgs &a) const { return len > full * a.page_size; }
-    // the old entry that entry e keeps, -1 for none
-    __device__ __forceinline__ int kept(const ForkArgs &a, int e) const {
-        if (src < 0 || !(heir || e < full + (part(a) ? 1 : 0))) return -1;
-        const int p = __ldg(a.table + (int64_t)src * a.max_pages + e);
-        return p < 0 || p >= a.pages ? -1 : p;
-    }
-    __device__ __forceinline__ bool wants(int e, int p) const { return (e < need && p < 0) || (copy && e == full); }
 };
-constexpr int kHeir = 1, kContinued = 2, kCopy = 4;
+constexpr int kHeir = 1, kContinued = 2, kCopy = 4;   // the first row that continues src; the old row of this number goes on; its last page is copied
+__device__ __forceinline__ bool row_part(const ForkArgs &a, const NewRow &r) { return r.len > r.full * a.page_size; }
+__device__ __forceinline__ NewRow new_row(const ForkArgs &a, const FastDiv &by_page, int n) {
+    NewRow r;
+    r.src = __ldg(a.sources + n);
+    r.len = r.full = r.need = 0;
+    if (r.src < 0 || r.src >= a.rows) {
+        r.src = -1;
+        return r;
+    }
+    const int most = a.max_pages * a.page_size;
+    r.len = __ldg(a.lens + r.src);
+    r.len = r.len < 0 ? 0 : (r.len > most ? most : r.len);
+    r.full = (int)by_page((uint32_t)r.len);
+    const int more = a.new_tokens ? __ldg(a.new_tokens + n) : 0;
+    const int64_t end = (int64_t)r.len + (more > 0 ? more : 0);
+    r.need = a.max_pages;
+    if (end < most) {
+        r.need = (int)by_page((uint32_t)end);
+        r.need += end > (int64_t)r.need * a.page_size;
+    }
+    return r;
+}
+// Whether entry e keeps the old row's, and what it then is (-1 for none).
+__device__ __forceinline__ bool keeps(const ForkArgs &a, const NewRow &r, int flags, int e) { return r.src >= 0 && ((flags & kHeir) || e < r.full + (row_part(a, r) ? 1 : 0)); }
+__device__ __forceinline__ int valid(const ForkArgs &a, int p) { return p < 0 || p >= a.pages ? -1 : p; }
+// Entries e .. e + 3 of a row of a table, -1 past its end.
+__device__ __forceinline__ int4 load4(const int32_t *row, int e, int end, bool vec) {
+    if (vec && e + 4 <= end) return __ldg(reinterpret_cast<const int4 *>(row + e));
+    int4 x;
+    x.x = e < end ? __ldg(row + e) : -1;
+    x.y = e + 1 < end ? __ldg(row + e + 1) : -1;
+    x.z = e + 2 < end ? __ldg(row + e + 2) : -1;
+    x.w = e + 3 < end ? __ldg(row + e + 3) : -1;
+    return x;
+}
+__device__ __forceinline__ void store4(int32_t *row, int e, int end, bool vec, int4 x) {
+    if (vec && e + 4 <= end) {
+        *reinterpret_cast<int4 *>(row + e) = x;
+        return;
+    }
+    if (e < end) row[e] = x.x;
+    if (e + 1 < end) row[e + 1] = x.y;
+    if (e + 2 < end) row[e + 2] = x.z;
+    if (e + 3 < end) row[e + 3] = x.w;
+}
+__device__ __forceinline__ bool wants(const NewRow &r, int flags, int e, int p) { return (e < r.need && p < 0) || ((flags & kCopy) && e == r.full); }
 
 __global__ void __launch_bounds__(kPoolThreads) kda_paged_fork_kernel(const ForkArgs a, const PoolPlan plan, const FastDiv by_page) {
     extern __shared__ __align__(16) uint8_t sm[];
-    __shared__ int totals[2];
-    Pool P = make_pool(plan, sm, totals);
-    int *count = P.blk + plan.blocks + 1;                                     // pages that each segment asks for, then before it
-    uint8_t *flags = reinterpret_cast<uint8_t *>(count + plan.segs);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ Totals totals;
+    uint8_t *at = sm;
+    NewRow *info = reinterpret_cast<NewRow *>(at);                            // of a batch of rows
+    at += kBatch * sizeof(NewRow);
+    Pool P = make_pool(plan, at);
+    int *count = reinterpret_cast<int *>(at);                                 // pages that each segment asks for, then before it
+    int *first = count + plan.rows * plan.per_row;                            // the first row that continues each old one
+    uint8_t *flags = reinterpret_cast<uint8_t *>(first + plan.first);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = (int)P.cluster.block_rank();
-    const int threads = plan.ctas * kPoolThreads, gt = rank * kPoolThreads + tid;
+    const int lo = rank * plan.rows, rows = a.rows - lo < plan.rows ? (a.rows - lo > 0 ? a.rows - lo : 0) : plan.rows;   // this CTA's rows
+    constexpr int kNone = 0x7fffffff;
 
-    // the first row that continues each old row: kept in `copies` until they are written
-    for (int n = gt; n < a.rows; n += threads) a.copies[2 * n] = 0x7fffffff;
-    P.cluster.sync();
-    for (int n = gt; n < a.rows; n += threads) {
-        const int s = __ldg(a.sources + n);
-        if (s >= 0 && s < a.rows) atomicMin(a.copies + 2 * (int64_t)s, n);
+    // (more rows than fit are kept in `copies` until those are written)
+    if (plan.first) {
+        for (int n = tid; n < a.rows; n += kPoolThreads) first[n] = kNone;
+        __syncthreads();
+        for (int n = tid; n < a.rows; n += kPoolThreads) {
+            const int s = __ldg(a.sources + n);
+            if (s >= 0 && s < a.rows) atomicMin(first + s, n);
+        }
+        scan_pages(a, P, [&](int p, int r) { a.new_refs[p] = r; });
+        __syncthreads();
+    } else {
+        for (int n = lo + tid; n < lo + rows; n += kPoolThreads) a.copies[2 * (int64_t)n] = kNone;
+        P.cluster.sync();
+        for (int n = lo + tid; n < lo + rows; n += kPoolThreads) {
+            const int s = __ldg(a.sources + n);
+            if (s >= 0 && s < a.rows) atomicMin(a.copies + 2 * (int64_t)s, n);
+        }
+        scan_pages(a, P, [&](int p, int r) { a.new_refs[p] = r; });
+        P.cluster.sync();
     }
-    scan_pages(a, P, [&](int p, int r) { a.new_refs[p] = r; });
-    P.cluster.sync();
+    auto first_of = [&](int s) { return plan.first ? first[s] : __ldcg(a.copies + 2 * (int64_t)s); };
 
-    // segment sg of the CTA: entries [e0, e1) of row n
-    auto segment = [&](int sg, int &n, int &e0, int &e1) {
-        const int64_t g = (int64_t)rank * plan.segs + sg;
-        n = (int)(g / plan.per_row);
-        e0 = (int)(g - (int64_t)n * plan.per_row) * plan.chunk;
-        e1 = a.max_pages - e0 < plan.chunk ? a.max_pages : e0 + plan.chunk;
-        return n < a.rows;
-    };
-    for (int sg = warp; sg < plan.segs; sg += kPoolWarps) {
-        int n, e0, e1, sum = 0, fl = 0;
-        if (segment(sg, n, e0, e1)) {
-            NewRow r(a, by_page, n);
-            r.heir = r.src >= 0 && __ldcg(a.copies + 2 * (int64_t)r.src) == n;
-            if (r.src >= 0 && r.part(a)) {
-                const int p = r.kept(a, r.full);
-                r.copy = p >= 0 && !(r.heir && __ldg(a.refs + p) == 1);
+    for (int r0 = 0; r0 < rows; r0 += kBatch) {
+        const int nr = rows - r0 < kBatch ? rows - r0 : kBatch;
+        if (tid < nr) {
+            const int n = lo + r0 + tid;
+            const NewRow r = new_row(a, by_page, n);
+            int fl = (r.src >= 0 && first_of(r.src) == n ? kHeir : 0) | (first_of(n) != kNone ? kContinued : 0);
+            if (r.src >= 0 && row_part(a, r)) {
+                const int p = valid(a, __ldg(a.table + (int64_t)r.src * a.max_pages + r.full));
+                if (p >= 0 && !((fl & kHeir) && __ldg(a.refs + p) == 1)) fl |= kCopy;
             }
-            for (int e = e0 + lane; e < e1; e += 32) sum += r.wants(e, r.kept(a, e));
-            fl = (r.heir ? kHeir : 0) | (__ldcg(a.copies + 2 * (int64_t)n) != 0x7fffffff ? kContinued : 0) | (r.copy ? kCopy : 0);
+            info[tid] = r;
+            flags[r0 + tid] = (uint8_t)fl;
         }
-        sum = __reduce_add_sync(0xffffffffu, sum);
-        if (lane == 0) {
-            count[sg] = sum;
-            flags[sg] = (uint8_t)fl;
+        __syncthreads();
+        for (int sg = warp; sg < nr * plan.per_row; sg += kPoolWarps) {
+            const int i = sg / plan.per_row, e0 = (sg - i * plan.per_row) * plan.chunk;
+            const NewRow r = info[i];
+            const int fl = flags[r0 + i], e1 = e0 + plan.chunk < a.max_pages ? e0 + plan.chunk : a.max_pages;
+            int sum = 0;
+            if (r.src >= 0 && e0 < r.need)
+                for (int e = e0 + 4 * lane; e < e1; e += 128) {
+                    const int4 x = load4(a.table + (int64_t)r.src * a.max_pages, e, e1, plan.vec);
+                    const int p[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) sum += e + y < e1 && wants(r, fl, e + y, keeps(a, r, fl, e + y) ? valid(a, p[y]) : -1);
+                }
+            sum = __reduce_add_sync(0xffffffffu, sum);
+            if (lane == 0) count[r0 * plan.per_row + sg] = sum;
         }
+        __syncthreads();
     }
-    __syncthreads();
     if (warp == 0) {
-        const int x = scan_warp(P.blk, plan.blocks);
-        if (lane == 0) P.blk[plan.blocks] = totals[0] = x;
+        const int x = scan_warp(P.mine.blk, plan.blocks);
+        if (lane == 0) P.mine.blk[plan.blocks] = totals.mine[0] = x;
     } else if (warp == 1) {
-        const int x = scan_warp(count, plan.segs);
-        if (lane == 0) totals[1] = x;
+        const int x = scan_warp(count, rows * plan.per_row);
+        if (lane == 0) totals.mine[1] = x;
     }
-    P.cluster.sync();
-    meet(P, plan);
-    int64_t asked = 0, ahead = 0;
-    for (int c = 0; c < plan.ctas; ++c) {
-        const int x = P.cluster.map_shared_rank(totals, c)[1];
-        ahead += c < rank ? x : 0;
-        asked += x;
-    }
-    const int missing = asked > P.before[kMaxCtas] ? (int)(asked - P.before[kMaxCtas]) : 0;
-    if (gt == 0) *a.short_of = missing;
+    meet(P, plan, totals);
+    const long long ahead = totals.ahead;
+    const int missing = totals.asked > P.free_pages() ? (int)(totals.asked - P.free_pages()) : 0;
+    if (rank == 0 && tid == 0) *a.short_of = missing;
 
-    for (int sg = warp; sg < plan.segs; sg += kPoolWarps) {
-        int n, e0, e1;
-        if (!segment(sg, n, e0, e1)) continue;
-        const int32_t *old = a.table + (int64_t)n * a.max_pages;
-        int32_t *to = a.new_table + (int64_t)n * a.max_pages;
-        if (missing > 0) {
-            for (int e = e0 + lane; e < e1; e += 32) to[e] = __ldg(old + e);
-            if (e0 == 0 && lane == 0) {
-                a.new_lens[n] = __ldg(a.lens + n);
-                a.copies[2 * (int64_t)n] = a.copies[2 * (int64_t)n + 1] = -1;
-            }
-            continue;
+    for (int r0 = 0; r0 < rows; r0 += kBatch) {
+        const int nr = rows - r0 < kBatch ? rows - r0 : kBatch;
+        if (r0 > 0) __syncthreads();
+        if (tid < nr) {
+            const int n = lo + r0 + tid;
+            if (rows > kBatch) info[tid] = new_row(a, by_page, n);            // (else they are still there)
+            a.new_lens[n] = missing > 0 ? __ldg(a.lens + n) : info[tid].len;
+            if (missing > 0 || !(flags[r0 + tid] & kCopy)) a.copies[2 * (int64_t)n] = a.copies[2 * (int64_t)n + 1] = -1;
         }
-        NewRow r(a, by_page, n);
-        r.heir = flags[sg] & kHeir;
-        r.copy = flags[sg] & kCopy;
-        int k = (int)ahead + count[sg];
-        for (int eb = e0; eb < e1; eb += 32) {
-            const int e = eb + lane;
-            int p = e < e1 ? r.kept(a, e) : -1;
-            const bool want = e < e1 && r.wants(e, p);
-            const uint32_t all = __ballot_sync(0xffffffffu, want);
-            const int was = p;
-            if (want) {
-                p = P.nth_free(k + __popc(all & ((1u << lane) - 1)));
-                a.new_refs[p] = 1;
-            }
-            k += __popc(all);
-            if (e < e1) {
-                to[e] = p;
-                if (r.copy && e == r.full) {
-                    a.copies[2 * (int64_t)n] = was;
-                    a.copies[2 * (int64_t)n + 1] = p;
-                    if (r.heir) atomicSub(a.new_refs + was, 1);          // the old row's own reference
-                } else if (!r.heir && was >= 0) {
-                    atomicAdd(a.new_refs + was, 1);
+        if (rows > kBatch) __syncthreads();
+        for (int sg = warp; sg < nr * plan.per_row; sg += kPoolWarps) {
+            const int i = sg / plan.per_row, e0 = (sg - i * plan.per_row) * plan.chunk, n = lo + r0 + i;
+            const NewRow r = info[i];
+            const int fl = flags[r0 + i], e1 = e0 + plan.chunk < a.max_pages ? e0 + plan.chunk : a.max_pages;
+            const int32_t *old = a.table + (int64_t)n * a.max_pages;
+            int32_t *to = a.new_table + (int64_t)n * a.max_pages;
+            int k = (int)ahead + count[r0 * plan.per_row + sg];
+            for (int eb = e0; eb < e1; eb += 128) {
+                const int e = eb + 4 * lane;
+                if (missing > 0) {
+                    store4(to, e, e1, plan.vec, load4(old, e, e1, plan.vec));
+                    continue;
                 }
-                if (!(flags[sg] & kContinued)) {                          // old row n ends
-                    const int q = __ldg(old + e);
-                    if (q >= 0 && q < a.pages) atomicSub(a.new_refs + q, 1);
+                int4 x = make_int4(-1, -1, -1, -1), y = x;
+                if (r.src >= 0) x = load4(a.table + (int64_t)r.src * a.max_pages, e, e1, plan.vec);
+                const bool ends = !(fl & kContinued);                             // the old row of this number
+                if (ends) y = load4(old, e, e1, plan.vec);
+                int p[4] = {x.x, x.y, x.z, x.w};
+                const int q[4] = {y.x, y.y, y.z, y.w};
+                int want = 0;                                                     // a bit for each entry
+#pragma unroll
+                for (int i2 = 0; i2 < 4; ++i2) {
+                    p[i2] = keeps(a, r, fl, e + i2) ? valid(a, p[i2]) : -1;
+                    if (e + i2 < e1 && wants(r, fl, e + i2, p[i2])) want |= 1 << i2;
                 }
+                const bool shared = !(fl & kHeir);
+                if (shared || ends)
+#pragma unroll
+                    for (int i2 = 0; i2 < 4; ++i2) {
+                        if (shared && e + i2 < e1 && p[i2] >= 0 && !((fl & kCopy) && e + i2 == r.full)) atomicAdd(a.new_refs + p[i2], 1);
+                        if (ends && e + i2 < e1 && valid(a, q[i2]) >= 0) atomicSub(a.new_refs + q[i2], 1);
+                    }
+                if (__any_sync(0xffffffffu, want != 0)) {
+                    int s = __popc(want);
+                    const int mine = s;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int z = __shfl_up_sync(0xffffffffu, s, o);
+                        if (lane >= o) s += z;
+                    }
+                    int at = k + s - mine;
+                    k += __shfl_sync(0xffffffffu, s, 31);
+#pragma unroll 1
+                    for (; want; want &= want - 1) {
+                        const int i2 = __ffs(want) - 1, was = i2 == 0 ? p[0] : i2 == 1 ? p[1] : i2 == 2 ? p[2] : p[3], now = P.nth_free(at++);
+                        p[0] = i2 == 0 ? now : p[0], p[1] = i2 == 1 ? now : p[1], p[2] = i2 == 2 ? now : p[2], p[3] = i2 == 3 ? now : p[3];
+                        a.new_refs[now] = 1;
+                        if ((fl & kCopy) && e + i2 == r.full) {
+                            a.copies[2 * (int64_t)n] = was;
+                            a.copies[2 * (int64_t)n + 1] = now;
+                            if (fl & kHeir) atomicSub(a.new_refs + was, 1);       // the old row's own reference
+                        }
+                    }
+                }
+                store4(to, e, e1, plan.vec, make_int4(p[0], p[1], p[2], p[3]));
             }
-        }
-        if (e0 == 0 && lane == 0) {
-            a.new_lens[n] = r.len;
-            if (!r.copy) a.copies[2 * (int64_t)n] = a.copies[2 * (int64_t)n + 1] = -1;
         }
     }
-    P.cluster.sync();   // the others have read this CTA's bitmap
+    if (plan.ctas > 1) P.cluster.sync();  // the others have read this CTA's bitmap and totals
 }
 
 __global__ void __launch_bounds__(kPoolThreads) kda_paged_compact_kernel(const ForkArgs a, const PoolPlan plan) {
     extern __shared__ __align__(16) uint8_t sm[];
-    __shared__ int totals[2];
-    Pool P = make_pool(plan, sm, totals);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ Totals totals;
+    uint8_t *at = sm;
+    Pool P = make_pool(plan, at);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = (int)P.cluster.block_rank();
     const int threads = plan.ctas * kPoolThreads, gt = rank * kPoolThreads + tid;
     scan_pages(a, P, [](int, int) {});
     __syncthreads();
     if (warp == 0) {
-        const int x = scan_warp(P.blk, plan.blocks);
-        if (lane == 0) P.blk[plan.blocks] = totals[0] = x;
+        const int x = scan_warp(P.mine.blk, plan.blocks);
+        if (lane == 0) P.mine.blk[plan.blocks] = totals.mine[0] = x;
     }
-    P.cluster.sync();
-    meet(P, plan);
-    const int used = a.pages - P.before[kMaxCtas];
+    meet(P, plan, totals);
+    const int used = a.pages - P.free_pages();
     const int moves = used < a.pages ? P.free_before(used) : 0;   // free pages below `used`, and used ones past it
-    // pages: those that move leave their new place in new_refs until the table is rewritten
-    for (int b = warp; b < plan.blocks; b += kPoolWarps) {
-        const int p0 = (rank * plan.blocks + b) * kBlock;
-        int ahead = P.before[rank] + P.blk[b];                    // free pages before the word
-        for (int w = 0; w < 32; ++w) {
-            const uint32_t bits = P.words[32 * b + w];
-            const int p = p0 + 32 * w + lane;
-            const bool in_use = p < a.pages && !((bits >> lane) & 1u);
-            if (in_use && p < used) {
-                a.new_refs[p] = __ldg(a.refs + p);
-            } else if (in_use) {
-                const int r = p - (ahead + __popc(bits & ((1u << lane) - 1))) - (used - moves);
-                const int to = P.nth_free(r);
-                a.new_refs[to] = __ldg(a.refs + p);
-                a.new_refs[p] = to;
-                a.copies[2 * r] = p;
-                a.copies[2 * r + 1] = to;
-            } else if (p < a.pages && p >= used) {
-                a.new_refs[p] = 0;
-            }
-            ahead += __popc(bits);
+    // pages, a word a warp: those that move leave their new place in new_refs until the table is rewritten
+    for (int w = warp; w < 32 * plan.blocks; w += kPoolWarps) {
+        const int64_t p64 = (int64_t)rank * plan.blocks * kBlock + 32 * w + lane;
+        if (p64 >= a.pages) continue;
+        const int p = (int)p64;
+        const uint32_t bits = P.mine.words[w];
+        const bool in_use = !((bits >> lane) & 1u);
+        if (in_use && p < used) {
+            a.new_refs[p] = __ldg(a.refs + p);
+        } else if (in_use) {
+            const int ahead = P.before[rank] + P.mine.blk[w / 32] + P.mine.in_block[w] + __popc(bits & ((1u << lane) - 1));   // free pages before it
+            const int r = p - ahead - (used - moves), to = P.nth_free(r);
+            a.new_refs[to] = __ldg(a.refs + p);
+            a.new_refs[p] = to;
+            a.copies[2 * r] = p;
+            a.copies[2 * r + 1] = to;
+        } else if (p >= used) {
+            a.new_refs[p] = 0;
         }
     }
     for (int r = moves + gt; r < a.pages / 2; r += threads) a.copies[2 * r] = a.copies[2 * r + 1] = -1;
     P.cluster.sync();
     const int64_t entries = (int64_t)a.rows * a.max_pages;
-    for (int64_t i = gt; i < entries; i += threads) {
-        const int p = __ldg(a.table + i);
-        a.new_table[i] = p >= used && p < a.pages ? __ldcg(a.new_refs + p) : (p >= 0 && p < a.pages ? p : -1);
+    for (int64_t i0 = gt; i0 < entries; i0 += 8 * (int64_t)threads) {
+        int p[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) p[x] = i0 + x * (int64_t)threads < entries ? __ldg(a.table + i0 + x * (int64_t)threads) : -1;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) p[x] = p[x] >= used && p[x] < a.pages ? __ldcg(a.new_refs + p[x]) : (p[x] >= 0 && p[x] < a.pages ? p[x] : -1);
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            if (i0 + x * (int64_t)threads < entries) a.new_table[i0 + x * (int64_t)threads] = p[x];
     }
     P.cluster.sync();
     for (int p = used + gt; p < a.pages; p += threads) a.new_refs[p] = 0;
@@ -388,6 +516,7 @@ constexpr int kCopyThreads = 256, kCopyAhead = 4, kCopyVecs = kCopyThreads * kCo
 
 __global__ void __launch_bounds__(kCopyThreads) kda_paged_copy_kernel(uint4 *kc, uint4 *vc, const int32_t *copies, const int64_t works,
                                                                       const int per_page, const int64_t page_vecs, const int pages) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // (launched before the kernel ahead of it has ended)
     for (int64_t w = blockIdx.x; w < works; w += gridDim.x) {
         const int64_t i = w / per_page;
         const int from = __ldg(copies + 2 * i), to = __ldg(copies + 2 * i + 1);
@@ -410,18 +539,23 @@ PoolPlan pool_plan(const ForkArgs &a, bool fork) {
     p.ctas = 1;
     while (p.ctas < kMaxCtas && (blocks * kBlock + entries) > (int64_t)p.ctas * 4 * kPoolThreads) p.ctas *= 2;
     p.blocks = (int)((blocks + p.ctas - 1) / p.ctas);
+    p.all = p.ctas == 1 ? p.blocks : a.pages <= kLocalPages ? p.blocks * p.ctas : 0;
+    p.smem = bitmap_bytes(p.blocks) + (p.all ? bitmap_bytes(p.all) : 0);
     if (fork) {
         p.chunk = 128;
-        while (p.chunk < a.max_pages && (int64_t)a.rows * ((a.max_pages + p.chunk - 1) / p.chunk) > 65536) p.chunk *= 2;
+        p.rows = (a.rows + p.ctas - 1) / p.ctas;
+        while (p.chunk < a.max_pages && (int64_t)p.rows * ((a.max_pages + p.chunk - 1) / p.chunk) > 16384) p.chunk *= 2;
         p.per_row = (a.max_pages + p.chunk - 1) / p.chunk;
-        p.segs = (int)(((int64_t)a.rows * p.per_row + p.ctas - 1) / p.ctas);
+        p.first = a.rows <= kLocalRows ? a.rows : 0;
+        p.smem += kBatch * (int)sizeof(NewRow) + 4 * p.rows * p.per_row + 4 * p.first + p.rows;
+        p.vec = a.max_pages % 4 == 0 && (reinterpret_cast<uintptr_t>(a.table) | reinterpret_cast<uintptr_t>(a.new_table)) % 16 == 0;
     }
-    p.smem = 128 * p.blocks + 4 * (p.blocks + 1) + 5 * p.segs;
     return p;
 }
 
 template <typename... A> cudaError_t launch_pool(void (*kernel)(A...), const PoolPlan &plan, cudaStream_t st, std::common_type_t<A>... args) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
@@ -456,9 +590,16 @@ cudaError_t launch_page_copy(void *kc, void *vc, const int32_t *copies, int64_t 
     const int64_t per_page = (2 * page_vecs + kCopyVecs - 1) / kCopyVecs, works = count * per_page;
     if (per_page > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int64_t most = 8 * kSms;
-    kda_paged_copy_kernel<<<(unsigned)(works < most ? works : most), kCopyThreads, 0, st>>>(static_cast<uint4 *>(kc), static_cast<uint4 *>(vc), copies, works,
-                                                                                           (int)per_page, page_vecs, pages);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    cfg.gridDim = dim3((unsigned)(works < most ? works : most));
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, kda_paged_copy_kernel, static_cast<uint4 *>(kc), static_cast<uint4 *>(vc), copies, works, (int)per_page, page_vecs, pages);
 }
 
 }  // namespace kda

@@ -47,6 +47,12 @@ __device__ __forceinline__ float4 mul4(float4 a, float4 b) { return make_float4(
 __device__ __forceinline__ float4 mul4(float4 a, float b) { return make_float4(a.x * b, a.y * b, a.z * b, a.w * b); }
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c) { return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c)))); }
 
+// An operand as it is kept: rounded to tf32 once (fp32 calls split it where it is used).
+template <bool kF32> __device__ __forceinline__ float4 operand(float4 x) {
+    if constexpr (kF32) return x;
+    return make_float4(__uint_as_float(tf32(x.x)), __uint_as_float(tf32(x.y)), __uint_as_float(tf32(x.z)), __uint_as_float(tf32(x.w)));
+}
+
 // Sum over the eight lanes of a group (every lane of the warp takes part).
 __device__ __forceinline__ float sum8(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 1);
@@ -186,13 +192,19 @@ __global__ void __launch_bounds__(2 * DV, 256 / DV) kda_recurrent_tree_kernel(co
             if (l == 0) depth[i] = e;
 #pragma unroll
             for (int x = 0; x < DK / 32; ++x) {
-                *reinterpret_cast<float4 *>(sb + i * S::B + 32 * x + 4 * l) = mul4(k.x[x], d[x]);
-                *reinterpret_cast<float4 *>(sb + (m + i) * S::B + 32 * x + 4 * l) = mul4(q.x[x], d[x]);
+                *reinterpret_cast<float4 *>(sb + i * S::B + 32 * x + 4 * l) = operand<kF32>(mul4(k.x[x], d[x]));
+                *reinterpret_cast<float4 *>(sb + (m + i) * S::B + 32 * x + 4 * l) = operand<kF32>(mul4(q.x[x], d[x]));
             }
         }
     }
     __syncthreads();   // keys and decays are read: their place takes the products
 
+    if constexpr (!kF32) {   // the state as an operand
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[st][e] = make_float2(__uint_as_float(tf32(s[st][e].x)), __uint_as_float(tf32(s[st][e].y)));
+    }
     for (int r0 = 0; r0 < 2 * m; r0 += 16) {   // rows r0 .. r0 + 15 of (E k; E q); those past 2 m hold anything
         float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         float4 v0, v1;
@@ -206,24 +218,28 @@ __global__ void __launch_bounds__(2 * DV, 256 / DV) kda_recurrent_tree_kernel(co
 #pragma unroll
             for (int p = 0; p < 2; ++p) {   // two steps of 8 key channels
                 const float f[4] = {p ? x.z : x.x, p ? y.z : y.x, p ? x.w : x.y, p ? y.w : y.y};
-                uint32_t fh[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) fh[e] = tf32(f[e]);
                 const float2 b0 = s[st][2 * p], b1 = s[st][2 * p + 1];
-                const uint32_t h00 = tf32(b0.x), h10 = tf32(b1.x), h01 = tf32(b0.y), h11 = tf32(b1.y);
                 if constexpr (kF32) {
-                    uint32_t fl[4];
+                    uint32_t fh[4], fl[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) fl[e] = tf32(f[e] - __uint_as_float(fh[e]));
+                    for (int e = 0; e < 4; ++e) {
+                        fh[e] = tf32(f[e]);
+                        fl[e] = tf32(f[e] - __uint_as_float(fh[e]));
+                    }
+                    const uint32_t h00 = tf32(b0.x), h10 = tf32(b1.x), h01 = tf32(b0.y), h11 = tf32(b1.y);
                     const uint32_t l00 = tf32(b0.x - __uint_as_float(h00)), l10 = tf32(b1.x - __uint_as_float(h10));
                     const uint32_t l01 = tf32(b0.y - __uint_as_float(h01)), l11 = tf32(b1.y - __uint_as_float(h11));
                     mma_1688(c[0], fl[0], fl[1], fl[2], fl[3], h00, h10);
                     mma_1688(c[1], fl[0], fl[1], fl[2], fl[3], h01, h11);
                     mma_1688(c[0], fh[0], fh[1], fh[2], fh[3], l00, l10);
                     mma_1688(c[1], fh[0], fh[1], fh[2], fh[3], l01, l11);
+                    mma_1688(c[0], fh[0], fh[1], fh[2], fh[3], h00, h10);
+                    mma_1688(c[1], fh[0], fh[1], fh[2], fh[3], h01, h11);
+                } else {
+                    const uint32_t a0 = __float_as_uint(f[0]), a1 = __float_as_uint(f[1]), a2 = __float_as_uint(f[2]), a3 = __float_as_uint(f[3]);
+                    mma_1688(c[0], a0, a1, a2, a3, __float_as_uint(b0.x), __float_as_uint(b1.x));
+                    mma_1688(c[1], a0, a1, a2, a3, __float_as_uint(b0.y), __float_as_uint(b1.y));
                 }
-                mma_1688(c[0], fh[0], fh[1], fh[2], fh[3], h00, h10);
-                mma_1688(c[1], fh[0], fh[1], fh[2], fh[3], h01, h11);
             }
         }
         // c[t][0..1]: row ra, value channels c0 + 4 t4 + t and + 2 + t; c[t][2..3]: row rb

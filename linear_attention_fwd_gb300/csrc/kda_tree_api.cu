@@ -42,7 +42,7 @@ kda_status_t check_attention_dims(int32_t tokens, const kda_paged_dims_t *d) {
 
 kda_status_t check_pool_dims(const kda_paged_dims_t *d) {
     if (d == nullptr) return KDA_ERR_NULL;
-    if (d->rows < 0 || d->rows > 65536 || d->pages <= 0 || d->pages > (1 << 23) || d->page_size <= 0 || d->max_pages <= 0) return KDA_ERR_SHAPE;
+    if (d->rows < 0 || d->rows > 65536 || d->pages <= 0 || d->pages > (1 << 22) || d->page_size <= 0 || d->max_pages <= 0) return KDA_ERR_SHAPE;
     if ((int64_t)d->max_pages * d->page_size > 0x7fffffffLL - 64 || (int64_t)d->rows * d->max_pages > 0x7fffffffLL) return KDA_ERR_SHAPE;
     return KDA_OK;
 }

@@ -12,8 +12,8 @@
 //     at most 1, no exponent of a sum is taken, and lines of 64 tokens need no bound on g.  They leave the two
 //     coefficients of each pair, E_i k_i and E_i q_i;
 //  3. (E k; E q) S on tensor cores (mma.sync, tf32; fp32 calls: three products of parts of 11 bits);
-//  4. each warp solves for its channels' u in the order of the tokens, and adds up the outputs as it goes, without
-//     a barrier: half of its lanes take every second pair.
+//  4. each warp solves for its channels' u in the order of the tokens' depth, and adds up the outputs as it goes,
+//     without a barrier: four tokens of a depth at a time.
 // Bound by reading the state: 64 KB per row and head at 128 x 128.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -93,7 +93,7 @@ template <int DK, int DV> struct Shared {
     static __host__ __device__ int region_b(int T) { return 2 * T * A * 4; }
     static __host__ __device__ int pairs(int T) { return region_b(T) + rows(T) * B * 4; }
     static __host__ __device__ int ints(int T) { return pairs(T) + T * T * (int)sizeof(Pair); }
-    static __host__ __device__ int bytes(int T) { return ints(T) + 3 * T * 4; }
+    static __host__ __device__ int bytes(int T) { return ints(T) + 4 * T * 4; }
 };
 
 template <typename Tin, int DK, int DV>
@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(2 * DV, 256 / DV) kda_recurrent_tree_kernel(co
     Pair *pairs = reinterpret_cast<Pair *>(sm + S::pairs(T));
     int *depth = reinterpret_cast<int *>(sm + S::ints(T)), *parent = depth + T;
     float *beta = reinterpret_cast<float *>(parent + T);
+    int *order = reinterpret_cast<int *>(beta + T);                           // tokens by depth; their depth above bit 8
 
     const int n = blockIdx.x / a.heads, h = blockIdx.x - n * a.heads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -198,6 +199,12 @@ __global__ void __launch_bounds__(2 * DV, 256 / DV) kda_recurrent_tree_kernel(co
         }
     }
     __syncthreads();   // keys and decays are read: their place takes the products
+    if (tid < m) {     // (read behind the next barrier)
+        const int mine = depth[tid];
+        int rank = 0;
+        for (int j = 0; j < m; ++j) rank += depth[j] < mine || (depth[j] == mine && j < tid);
+        order[rank] = mine << 8 | tid;
+    }
 
     if constexpr (!kF32) {   // the state as an operand
 #pragma unroll
@@ -254,27 +261,48 @@ __global__ void __launch_bounds__(2 * DV, 256 / DV) kda_recurrent_tree_kernel(co
         put(ra, make_float4(c[0][0], c[1][0], c[0][1], c[1][1]), v0);
         put(rb, make_float4(c[0][2], c[1][2], c[0][3], c[1][3]), v1);
     }
-    __syncwarp();
+    __syncthreads();
 
-    // u and the outputs of this warp's 16 value channels
+    // u and the outputs of this warp's 16 value channels.  Tokens of the same depth do not depend on one another: each half of
+    // the warp takes two of them at a time; of one alone, half of its pairs.
     const int ch = c0 + (lane & 15), half = lane >> 4;
-    for (int i = 0; i < m; ++i) {
-        const Pair *row = pairs + i * T;
-        const int len = depth[i];
-        float x = 0.f, y = 0.f;
-        for (int e = 1 + half; e < len; e += 2) {
-            const Pair p = row[e];
-            const float u = pk[p.at * S::A + ch];
-            x = fmaf(p.a, u, x);
-            y = fmaf(p.b, u, y);
-        }
-        x += __shfl_xor_sync(0xffffffffu, x, 16);
-        y += __shfl_xor_sync(0xffffffffu, y, 16);
+    auto give = [&](int i, float w, float y, float x) {   // a token's sums: u, and its output
         const float u = pk[i * S::A + ch] - x;
-        if (half == 0) {
-            pk[i * S::A + ch] = u;
-            static_cast<Tin *>(a.out)[(first + (int64_t)i * a.heads) * DV + ch] = from_f<Tin>(fmaf(row[0].b, u, pq[i * S::A + ch] + y));
+        pk[i * S::A + ch] = u;
+        static_cast<Tin *>(a.out)[(first + (int64_t)i * a.heads) * DV + ch] = from_f<Tin>(fmaf(w, u, pq[i * S::A + ch] + y));
+    };
+    for (int pos = 0; pos < m;) {
+        const int o = order[pos + (lane & 3) < m ? pos + (lane & 3) : pos];
+        const int depth0 = __shfl_sync(0xffffffffu, o, 0) >> 8;
+        const int same = __popc(__ballot_sync(0xffffffffu, lane < 4 && pos + lane < m && (o >> 8) == depth0));   // (sorted: the first ones)
+        const bool alone = same == 1, go0 = half < same, go1 = 2 + half < same;
+        const int i0 = __shfl_sync(0xffffffffu, o, alone ? 0 : half) & 255, i1 = __shfl_sync(0xffffffffu, o, go1 ? 2 + half : 0) & 255;
+        const Pair *r0 = pairs + i0 * T, *r1 = pairs + i1 * T;
+        float x0 = 0.f, y0 = 0.f, x1 = 0.f, y1 = 0.f;
+        if (alone) {
+#pragma unroll 4
+            for (int e = 1 + half; e < depth0; e += 2) {
+                const Pair p = r0[e];
+                const float u = pk[p.at * S::A + ch];
+                x0 = fmaf(p.a, u, x0);
+                y0 = fmaf(p.b, u, y0);
+            }
+            x0 += __shfl_xor_sync(0xffffffffu, x0, 16);
+            y0 += __shfl_xor_sync(0xffffffffu, y0, 16);
+        } else {
+#pragma unroll 4
+            for (int e = 1; e < depth0; ++e) {
+                const Pair p0 = r0[e], p1 = r1[e];
+                const float u0 = pk[p0.at * S::A + ch], u1 = pk[p1.at * S::A + ch];
+                x0 = fmaf(p0.a, u0, x0);
+                y0 = fmaf(p0.b, u0, y0);
+                x1 = fmaf(p1.a, u1, x1);
+                y1 = fmaf(p1.b, u1, y1);
+            }
         }
+        if (go0) give(i0, r0[0].b, y0, x0);
+        if (go1) give(i1, r1[0].b, y1, x1);
+        pos += same;
         __syncwarp();
     }
 }

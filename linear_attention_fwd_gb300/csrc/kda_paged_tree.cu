@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_paged_tree_attention_kernel(c
             return ((int64_t)n * a.t.tokens + i) * p.heads + hk * a.rep + (r0 + r - i * a.rep);
         };
         __syncthreads();   // the last unit's tiles are read
-        if (tid < 32) tree_masks(a, n, row.m, anc, up);
+        if (tid < 32) tree_masks(tree_parents(a, n, row.m), row.m, anc, up);
         for (int c = tid; c < kRb * CH; c += kThreads) {
             const int r = c / CH, ch = c % CH;
             int i;

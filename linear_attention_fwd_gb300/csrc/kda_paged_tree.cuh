@@ -85,17 +85,21 @@ __device__ void tree_find(const TreeAtt &a, long long x, long long *sm, int &row
     before = s_before;
 }
 
-// Path masks of row n's drafted tokens (bit j of anc[i]: token j lies on the path to i), by one warp, path lengths
+// This lane's drafted tokens `lane` and 32 + lane of row n: what they continue.
+__device__ __forceinline__ int2 tree_parents(const TreeAtt &a, int n, int m) {
+    const int i = threadIdx.x & 31;
+    return make_int2(i < m ? tree_parent(a.t.parents, a.t.tokens, n, i) : -1, i + 32 < m ? tree_parent(a.t.parents, a.t.tokens, n, i + 32) : -1);
+}
+// Path masks of a row's drafted tokens (bit j of anc[i]: token j lies on the path to i), by one warp, path lengths
 // doubled each step.
-__device__ __forceinline__ void tree_masks(const TreeAtt &a, int n, int m, uint64_t *anc, int *up) {
+__device__ __forceinline__ void tree_masks(int2 parents, int m, uint64_t *anc, int *up) {
     const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int i = lane + 32 * e;
-        anc[i] = i < m ? 1ull << i : 0;
-        up[i] = i < m ? tree_parent(a.t.parents, a.t.tokens, n, i) : -1;
-    }
+    anc[lane] = lane < m ? 1ull << lane : 0;
+    anc[lane + 32] = lane + 32 < m ? 1ull << (lane + 32) : 0;
+    up[lane] = parents.x;
+    up[lane + 32] = parents.y;
     __syncwarp();
+#pragma unroll 1
     for (int step = 1; step < kTreeMax; step <<= 1) {
         uint64_t x[2];
         int p[2];
@@ -105,6 +109,7 @@ __device__ __forceinline__ void tree_masks(const TreeAtt &a, int n, int m, uint6
             x[e] = p[e] >= 0 ? anc[p[e]] : 0;
             p[e] = p[e] >= 0 ? up[p[e]] : -1;
         }
+        if (!__any_sync(0xffffffffu, (x[0] | x[1]) != 0)) break;
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -113,6 +118,7 @@ __device__ __forceinline__ void tree_masks(const TreeAtt &a, int n, int m, uint6
         }
         __syncwarp();
     }
+    __syncwarp();
 }
 
 // Place of a row's position in the cache of single tokens, -1 for none.

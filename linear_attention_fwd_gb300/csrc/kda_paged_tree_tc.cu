@@ -38,7 +38,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 640, kRb = 256, kKt = 64, kStart = 3;
+constexpr int kThreads = 640, kRb = 256, kKt = 64, kStart = 5;
 constexpr float kSlack = 8.f;   // growth of the maximum, in powers of two, that m does not follow
 constexpr int kLoaders = 2;     // warps
 
@@ -143,6 +143,11 @@ struct Walk {
     __device__ __forceinline__ int jobs(int k) const { return two ? c : (c + 1 - k) / 2; }
     __device__ __forceinline__ int tile(int k, int j) const { return two ? j : 2 * j + k; }
     __device__ __forceinline__ int ahead() const { return two ? 2 : 4; }
+    // The drafted tokens' row in their tile where it comes by boxes (from the start of a box of the cache on), -1 where it does not
+    __device__ __forceinline__ int shift(int box) const {
+        const int o = box ? row.len & (box - 1) : 0;
+        return box && o + row.m <= kKt ? o : -1;
+    }
     __device__ __forceinline__ int k_load(int i) const { return i < ahead() ? i : 2 * i + 1 - ahead(); }
     __device__ __forceinline__ int v_load(int i) const { return i < c - ahead() ? 2 * i + ahead() : c + i; }
 };
@@ -248,7 +253,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                 uint32_t in = half ? here.y : here.x;
                 const bool open = !draft && (here.x & here.y) == 0xffffffffu;   // (the same for the row's two threads)
                 if (!open) {
-                    if (draft) in &= r < w.rows ? (uint32_t)(anc[64 * (pieces & 1) + a.by_rep((uint32_t)(w.r0 + r))] >> (32 * half)) : 0u;
+                    if (draft) in &= r < w.rows ? (uint32_t)((anc[64 * (pieces & 1) + a.by_rep((uint32_t)(w.r0 + r))] << max(w.shift(box), 0)) >> (32 * half)) : 0u;
                     const float no = sc >= 0.f ? -INFINITY : INFINITY;
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = (in >> e) & 1u ? v[e] : no;
@@ -502,7 +507,8 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
             if (w.c > 0) {
                 const int32_t *table = p.table + (int64_t)w.n * p.max_pages;
                 const int boxes = box ? kKt / box : 0;                      // of a tile, 8 at most
-                auto by_box = [&](int i) { return box && w.ta + i != w.row.ctx; };
+                const int shift = w.shift(box);
+                auto by_box = [&](int i) { return box && (w.ta + i != w.row.ctx || shift >= 0); };
                 // Pages are fetched well before they are needed: by boxes, those of four tiles by one load (eight lanes a tile), four
                 // tiles ahead; else a tile's, a tile ahead.
                 auto group_token = [&](int g) { return (w.ta + 4 * g + (lane >> 3)) * kKt + (lane & 7) * box; };
@@ -521,25 +527,36 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                     return x;
                 };
                 int group = -1, page = box ? group_page(0) : -1;            // places of the current four tiles; pages of the next
-                int2 pre = tokens(box ? (w.ta + w.c > w.row.ctx ? w.c - 1 : w.c) : 0);   // (by boxes: the drafted tokens, where they are here)
+                const bool has_draft = w.ta + w.c > w.row.ctx;
+                int2 pre = make_int2(-1, -1);
+                if (!box) {
+                    pre = tokens(0);
+                } else if (has_draft && shift < 0) {
+                    pre = tokens(w.c - 1);
+                } else if (has_draft) {
+                    const int t = w.row.len - shift + lane * box;           // the boxes of the drafted tokens
+                    if (lane < boxes && t < w.row.len + w.row.m) pre.x = (int)tree_place(a, table, t);
+                }
+                const int2 parents = wi == 1 && has_draft ? tree_parents(a, w.n, w.row.m) : make_int2(-1, -1);
                 auto place = [&](int i) {                                   // asked for in order
                     Place x;
                     if (by_box(i)) {
+                        const bool draft = w.ta + i == w.row.ctx;
                         if ((i & 3) == 0) {
                             const int t = group_token(i >> 2), pg = (int)a.by_page((uint32_t)t);
                             group = page >= 0 && page < p.pages ? page * p.page_size + (t - pg * p.page_size) : -1;
                             page = group_page((i >> 2) + 1);
                         }
                         const int at = __shfl_sync(0xffffffffu, group, (i & 3) * 8 + (lane & 7));
-                        x.at[0] = lane < boxes ? at : -1;
+                        x.at[0] = lane >= boxes ? -1 : draft ? pre.x : at;
                         x.at[1] = -1;
                         const uint32_t have = __ballot_sync(0xffffffffu, x.at[0] >= 0);
-                        const int left = w.row.len - (w.ta + i) * kKt;
+                        const int from = draft ? shift : 0, left = draft ? shift + w.row.m : w.row.len - (w.ta + i) * kKt;
                         x.mask = make_uint2(0xffffffffu, 0xffffffffu);
-                        if (have != (1u << boxes) - 1 || left < kKt) {
+                        if (have != (1u << boxes) - 1 || left < kKt || draft) {
                             const int per = __ffs(box) - 1;                 // (a power of two)
-                            x.mask.x = __ballot_sync(0xffffffffu, lane < left && ((have >> (lane >> per)) & 1u));
-                            x.mask.y = __ballot_sync(0xffffffffu, lane + 32 < left && ((have >> ((lane + 32) >> per)) & 1u));
+                            x.mask.x = __ballot_sync(0xffffffffu, lane >= from && lane < left && ((have >> (lane >> per)) & 1u));
+                            x.mask.y = __ballot_sync(0xffffffffu, lane + 32 >= from && lane + 32 < left && ((have >> ((lane + 32) >> per)) & 1u));
                         }
                         return x;
                     }
@@ -579,7 +596,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                 };
                 auto keys = [&](int i, const Place &x) {
                     if (wi == 1 && w.ta + i == w.row.ctx)   // the drafted tokens' paths
-                        tree_masks(a, w.n, w.row.m, reinterpret_cast<uint64_t *>(sm + L::ANC) + 64 * (pieces & 1), reinterpret_cast<int *>(sm + L::UP));
+                        tree_masks(parents, w.row.m, reinterpret_cast<uint64_t *>(sm + L::ANC) + 64 * (pieces & 1), reinterpret_cast<int *>(sm + L::UP));
                     if (wi == 0 && lane == 0) *reinterpret_cast<uint2 *>(sm + L::MASK + 8 * ((tiles + i) & 31)) = x.mask;
                     __syncwarp();
                     return tile(&tmk, kc, x, i);

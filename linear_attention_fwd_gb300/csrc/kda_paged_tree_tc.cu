@@ -336,7 +336,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                     sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], x);
                     const uint32_t a0 = __float_as_uint(x.x), a1 = __float_as_uint(x.y);
                     u[e / 2] = __uint_as_float(__byte_perm(a0, a1, 0x7632));
-                    const float2 rest = __fadd2_rn(x, make_float2(-__uint_as_float(a0 & 0xffff0000u), -__uint_as_float(a1 & 0xffff0000u)));
+                    const float2 rest = __ffma2_rn(make_float2(__uint_as_float(a0 & 0xffff0000u), __uint_as_float(a1 & 0xffff0000u)), make_float2(-1.f, -1.f), x);
                     u[16 + e / 2] = __uint_as_float(pack_bf16(rest.x, rest.y));
                 }
                 tmem_st32(ts, u);

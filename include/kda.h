@@ -644,6 +644,8 @@ kda_status_t kda_recurrent_tree_commit_qknorm(const void *k, const void *v, cons
  *   tokens    : in [1, KDA_TREE_TOKENS];  pages * page_size * kv_heads at most 2^31 - 1, else KDA_ERR_SHAPE
  *   workspace : kda_paged_tree_attention_workspace_bytes(tokens, dims) bytes, 16-byte aligned (NULL when that is
  *               0), contents on entry of no matter; one per call in flight.
+ * bf16 calls whose rows can only be short (max_pages * page_size and few query rows: up to 8192 tokens) are one launch
+ * without a workspace; a table cut to the rows' needs is the faster one, as in kda_paged_attention.
  * Results do not depend on timing.  Other arguments and errors as in kda_paged_attention. */
 kda_status_t kda_paged_tree_attention(const void *q, const void *k_cache, const void *v_cache,
                                       const int32_t *block_table, const int32_t *seq_lens, const int32_t *parents,
@@ -654,7 +656,8 @@ kda_status_t kda_paged_tree_attention(const void *q, const void *k_cache, const 
 /* kda_paged_tree_attention_bounded -- kda_paged_tree_attention with an explicit bound on every device-side wait of the
  * tensor-core kernel (bf16), as in kda_lin_chunk_fwd_bounded: when one gives up, the CTA lets what is in flight land
  * (bounded separately), its share's outputs and lse become NaN, and kda_device_status reports KDA_ERR_TIMEOUT.
- * wait_polls = 0 makes every wait give up at once: a test of that path.  fp32 calls have no such waits. */
+ * wait_polls = 0 makes every wait give up at once: a test of that path.  fp32 calls, and those in one launch, have no such
+ * waits. */
 kda_status_t kda_paged_tree_attention_bounded(const void *q, const void *k_cache, const void *v_cache,
                                               const int32_t *block_table, const int32_t *seq_lens,
                                               const int32_t *parents, const int32_t *num_tokens, int32_t tokens,

@@ -148,6 +148,9 @@ template <typename T, int D, int THREADS> __device__ __forceinline__ void tree_c
 size_t tree_tc_workspace_bytes(const PagedTreeArgs &t, int d);
 // bf16; polls: bound on each device wait
 cudaError_t launch_tree_tc(const PagedTreeArgs &t, int d, void *workspace, uint32_t polls, cudaStream_t st);
+// The one-launch form of bf16 calls whose rows can only be short: CTAs per unit (0: not taken), and its launch.
+int tree_short_cluster(const PagedTreeArgs &t, int d);
+cudaError_t launch_tree_short(const TreeAtt &a, int d, int ctas, cudaStream_t st);
 // Joins the partials that a kernel of `ctas` shares left.
 cudaError_t launch_tree_join(const TreeAtt &a, int d, kda_dtype_t dt, int ctas, cudaStream_t st);
 

@@ -845,12 +845,13 @@ template <int D> cudaError_t launch_tc(const TreeAtt &a, int ctas, uint32_t poll
 
 }  // namespace
 
-size_t tree_tc_workspace_bytes(const PagedTreeArgs &t, int d) { return (size_t)tc_ctas(t) * 2 * kRb * (d + 2) * 4; }
+size_t tree_tc_workspace_bytes(const PagedTreeArgs &t, int d) { return tree_short_cluster(t, d) ? 0 : (size_t)tc_ctas(t) * 2 * kRb * (d + 2) * 4; }
 
 cudaError_t launch_tree_tc(const PagedTreeArgs &t, int d, void *workspace, uint32_t polls, cudaStream_t st) {
     const int rep = t.p.heads / t.p.kv_heads, ctas = tc_ctas(t);
     float *ws = static_cast<float *>(workspace);
     const TreeAtt a{t, FastDiv((uint32_t)t.p.page_size), FastDiv((uint32_t)rep), rep, kRb, kKt, kStart, ws, ws + (size_t)ctas * 2 * kRb * d};
+    if (const int c = tree_short_cluster(t, d)) return launch_tree_short(a, d, c, st);
     return d == 128 ? launch_tc<128>(a, ctas, polls, st) : launch_tc<64>(a, ctas, polls, st);
 }
 

@@ -34,11 +34,23 @@ def reference(c, rows):
     return R.attention(c["q"], c["k_cache"], c["v_cache"], c["block_table"], c["seq_lens"], rows, c["scale"])
 
 
+def widened(c):
+    """The same call under a table for 9000 tokens more: rows that may be long take the shared-out form, with a workspace."""
+    table = c["block_table"]
+    return {**c, "block_table": torch.cat([table, torch.full((table.shape[0], -(-9000 // c["k_cache"].shape[1])), -1, dtype=torch.int32, device="cuda")], 1)}
+
+
+def forms(c):
+    return [c, widened(c)] if c["q"].dtype == BF16 else [c]
+
+
 def run(K, c, rows, parents, num=None, **kw):
-    out, lse = K.kda_paged_tree_attention(**c, parents=parents, num_tokens=num, **kw)
-    check_paged(out, lse, reference(c, rows))
-    for n, p in enumerate(rows):
-        assert not out[n, len(p):].any() and bool((lse[n, len(p):] == -math.inf).all())
+    ref = reference(c, rows)
+    for form in reversed(forms(c)):
+        out, lse = K.kda_paged_tree_attention(**form, parents=parents, num_tokens=num, **kw)
+        check_paged(out, lse, ref)
+        for n, p in enumerate(rows):
+            assert not out[n, len(p):].any() and bool((lse[n, len(p):] == -math.inf).all())
     return out, lse
 
 
@@ -128,12 +140,14 @@ def test_places_that_a_token_does_not_see(K, dt, bad):
     for n, p in enumerate(rows):
         parents[n, : len(p)] = torch.tensor(p, dtype=torch.int32)
     num = torch.tensor([6, 7], dtype=torch.int32, device="cuda")
-    out, lse = run(K, c, rows, parents, num)
-    for n, sick in ((0, 2), (1, 0)):
+    run(K, c, rows, parents, num)
+    for n, sick, c in [(n, sick, form) for form in forms(c) for n, sick in ((0, 2), (1, 0))]:
+        out, lse = K.kda_paged_tree_attention(**c, parents=parents, num_tokens=num)
         d = {x: t.clone() if isinstance(t, torch.Tensor) else t for x, t in c.items()}
         at = lambda pos: (int(c["block_table"][n, pos // 16]), pos % 16)  # noqa: E731
         length = int(c["seq_lens"][n])
-        for pos in [length + sick] + list(range(length + len(rows[n]), c["block_table"].shape[1] * 16)):
+        behind = [pos for pos in range(length + len(rows[n]), c["block_table"].shape[1] * 16) if int(c["block_table"][n, pos // 16]) >= 0]
+        for pos in [length + sick] + behind:
             d["k_cache"][at(pos)] = bad
             d["v_cache"][at(pos)] = bad
         got, got_lse = K.kda_paged_tree_attention(**d, parents=parents, num_tokens=num)
@@ -163,7 +177,11 @@ def test_lengths_past_the_table(K, dt):
     c = cache(12, [50, 40, 20], 7, 4, 2, 64, 16, dt)
     width = c["block_table"].shape[1] * 16
     c["seq_lens"].copy_(torch.tensor([1 << 30, width - 3, -5]))
-    run(K, c, *R.drafts(12, 3, 7))
+    rows, parents = R.drafts(12, 3, 7)
+    check_paged(*K.kda_paged_tree_attention(**c, parents=parents), reference(c, rows))
+    if dt == BF16:
+        c = widened(c)     # (the lengths then end elsewhere)
+        check_paged(*K.kda_paged_tree_attention(**c, parents=parents), reference(c, rows))
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
@@ -189,10 +207,11 @@ def test_large_scores_and_equal_scores(K):
 @pytest.mark.parametrize("dt", [F32, BF16])
 def test_streams_workspaces_repeats(K, dt):
     """The same bits each time: with a workspace of the caller's full of NaN, on another stream, two calls at once."""
-    c = cache(15, [3000, 700], 11, 8, 2, 128, 16, dt)
+    c = widened(cache(15, [3000, 700], 11, 8, 2, 128, 16, dt))
     rows, parents = R.drafts(15, 2, 11)
     out, lse = run(K, c, rows, parents)
     need = K.kda_paged_tree_attention_workspace_bytes(c["q"], c["k_cache"], c["block_table"])
+    assert need > 0
     ws = [torch.full((max(need, 16),), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
     side = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
@@ -230,7 +249,7 @@ def test_captured(K):
 @pytest.mark.parametrize("d", [64, 128])
 def test_every_wait_giving_up(K, d):
     """wait_polls = 0: all results are NaN, the status says so, and the next call is right."""
-    c = cache(30, [600, 0, 3000], 9, 8, 2, d, 16, BF16)
+    c = widened(cache(30, [600, 0, 3000], 9, 8, 2, d, 16, BF16))
     rows, parents = R.drafts(30, 3, 9)
     need = K.kda_paged_tree_attention_workspace_bytes(c["q"], c["k_cache"], c["block_table"])
     ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")

@@ -644,7 +644,7 @@ kda_status_t kda_recurrent_tree_commit_qknorm(const void *k, const void *v, cons
  *   tokens    : in [1, KDA_TREE_TOKENS];  pages * page_size * kv_heads at most 2^31 - 1, else KDA_ERR_SHAPE
  *   workspace : kda_paged_tree_attention_workspace_bytes(tokens, dims) bytes, 16-byte aligned (NULL when that is
  *               0), contents on entry of no matter; one per call in flight.
- * bf16 calls whose rows can only be short (max_pages * page_size and few query rows: up to 8192 tokens) are one launch
+ * bf16 calls whose rows can only be short (max_pages * page_size and few query rows: up to 4096 tokens) are one launch
  * without a workspace; a table cut to the rows' needs is the faster one, as in kda_paged_attention.
  * Results do not depend on timing.  Other arguments and errors as in kda_paged_attention. */
 kda_status_t kda_paged_tree_attention(const void *q, const void *k_cache, const void *v_cache,

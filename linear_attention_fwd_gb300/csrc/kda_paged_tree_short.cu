@@ -20,7 +20,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kStages = 3, kGroup = 16, kRows = 16;
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kStages = 3, kGroup = 16, kRows = 16, kMaxCluster = 8;
 
 template <int D> struct Ring {
     static constexpr int RB = D * 2, CH = RB / 16;        // bytes of a key, 16-byte chunks of it
@@ -289,19 +289,36 @@ __global__ void __launch_bounds__(kThreads) kda_paged_tree_short_kernel(const Tr
     }
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    for (int c = tid + kThreads * rank; c < rows * D; c += kThreads * ctas) {
+    for (int c = 4 * (tid + kThreads * rank); c < rows * D; c += 4 * kThreads * ctas) {
         const int r = c / D;
-        float mx = -INFINITY;
-        for (int e = 0; e < ctas; ++e) mx = fmaxf(mx, cluster.map_shared_rank(sm_pm, e)[r]);
-        const float z = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f, acc = 0.f;
-        for (int e = 0; e < ctas; ++e) {
-            const float f = ex2(cluster.map_shared_rank(sm_pm, e)[r] - z);
-            sum = fmaf(cluster.map_shared_rank(sm_pl, e)[r], f, sum);
-            acc = fmaf(reinterpret_cast<const float *>(cluster.map_shared_rank(ring_all, e))[c], f, acc);
+        float pm[kMaxCluster], pl[kMaxCluster];   // (all parts asked for at once: each is a trip to another SM)
+        float4 po[kMaxCluster];
+#pragma unroll
+        for (int e = 0; e < kMaxCluster; ++e) {
+            pm[e] = -INFINITY;
+            if (e < ctas) {
+                pm[e] = cluster.map_shared_rank(sm_pm, e)[r];
+                pl[e] = cluster.map_shared_rank(sm_pl, e)[r];
+                po[e] = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(cluster.map_shared_rank(ring_all, e)) + c);
+            }
         }
+        float mx = pm[0];
+#pragma unroll
+        for (int e = 1; e < kMaxCluster; ++e) mx = fmaxf(mx, pm[e]);
+        const float z = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < kMaxCluster; ++e)
+            if (e < ctas) {
+                const float f = ex2(pm[e] - z);
+                sum = fmaf(pl[e], f, sum);
+                acc = make_float4(fmaf(po[e].x, f, acc.x), fmaf(po[e].y, f, acc.y), fmaf(po[e].z, f, acc.z), fmaf(po[e].w, f, acc.w));
+            }
         const int64_t to = q_row(r);
-        static_cast<__nv_bfloat16 *>(p.out)[to * D + c % D] = from_f<__nv_bfloat16>(sum == 0.f ? 0.f : acc / sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (sum == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + to * D + c % D) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
         if (p.lse && c % D == 0) p.lse[to] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
     }
     cluster.sync();   // the others have read this CTA's part
@@ -333,7 +350,8 @@ int row_blocks(const PagedTreeArgs &t) { return (t.tokens * (t.p.heads / t.p.kv_
 // CTAs of a cluster, as many as the SMs hold, up to 8.  0: the rows may be longer than a cluster takes in about the time that the
 // two launches of the other form cost, or there are too many of them.
 int tree_short_cluster(const PagedTreeArgs &t, int d) {
-    constexpr int kShortTokens = 1024, kMaxCluster = 8;
+    constexpr int kShortTokens = 512;   // of a CTA (one row, 8 drafted tokens, 8 key/value heads: 4000 tokens 19.5 us, 22.1 in the
+                                        // other form; 8000: 29.4 and 25.0; 4 rows of 2000: 22.3 and 22.8; 8 of 1500: 29.7 and 29.2)
     const int64_t units = (int64_t)t.p.rows * t.p.kv_heads * row_blocks(t);
     const int most = d == 64 ? 4 * kSms : 2 * kSms;   // what the SMs hold at once
     int c = kMaxCluster;

@@ -682,8 +682,8 @@ kda_status_t kda_paged_tree_commit(void *k_cache, void *v_cache, const int32_t *
  *
  * page_refs[p] counts the table entries that name page p; a page with 0 is free.  Entries outside [0, pages) name no
  * page (-1 is written for them).  Row n of the new table continues row s = sources[n] of the old one, or is
- * empty (sources[n] outside [0, rows): all -1, length 0); an old row that nothing continues ends, and its
- * pages lose a reference.  With len = seq_lens[s] clamped to [0, max_pages * page_size]:
+ * empty (sources[n] outside [0, rows): all -1, length 0, whatever new_tokens[n] is; a later call that continues it
+ * gives it pages); an old row that nothing continues ends, and its pages lose a reference.  With len = seq_lens[s] clamped to [0, max_pages * page_size]:
  *   - The entries of the pages that len fills are shared.
  *   - A last page that is only partly filled is kept by the first row n that continues s where page_refs counts
  *     no other reference to it, and copied by the others: they get a free page, and copies[n] = (old page, new

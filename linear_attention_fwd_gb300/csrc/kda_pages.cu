@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(kCommitThreads) kda_paged_tree_commit_kernel(c
     __shared__ int up[kTreeMax], path[kTreeMax], s_len;
     __shared__ int64_t from[kTreeMax], to[kTreeMax];
     const int n = blockIdx.x, tid = threadIdx.x, most = a.max_pages * a.page_size;
-    int old = __ldg(a.lens + n);
+    int old = *static_cast<const volatile int32_t *>(a.lens + n);   // (new_lens may be the same array: read before it is written)
     old = old < 0 ? 0 : (old > most ? most : old);
     int last = __ldg(a.accepted + n);
     if (last >= tree_count(a.num, a.tokens, n)) last = -1;

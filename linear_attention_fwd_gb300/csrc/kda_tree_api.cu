@@ -218,6 +218,7 @@ extern "C" kda_status_t kda_paged_copy(void *k_cache, void *v_cache, const int32
     if (d == nullptr) return KDA_ERR_NULL;
     if (!dtype_ok(d->dtype) || !head_size_ok(d->head_dim)) return KDA_ERR_UNSUPPORTED;
     if (d->kv_heads <= 0 || d->pages <= 0 || d->page_size <= 0 || count < 0 || count > 0x7fffffffLL) return KDA_ERR_SHAPE;
+    if ((int64_t)d->pages * d->page_size > 0xffffffffLL) return KDA_ERR_SHAPE;
     if (count == 0) return KDA_OK;
     if (!k_cache || !v_cache || !copies) return KDA_ERR_NULL;
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(copies, 4)) return KDA_ERR_ALIGN;

@@ -149,7 +149,7 @@ def test_commit_refusals(K):
     assert keep(K, paged(K, rows=0), kc=None) == K.KDA_OK
 
 
-@pytest.mark.parametrize("kw", [dict(rows=-1), dict(rows=65537), dict(pages=0), dict(pages=(1 << 23) + 1), dict(page_size=0), dict(max_pages=0),
+@pytest.mark.parametrize("kw", [dict(rows=-1), dict(rows=65537), dict(pages=0), dict(pages=(1 << 22) + 1), dict(page_size=0), dict(max_pages=0),
                                 dict(page_size=1 << 20, max_pages=1 << 12), dict(rows=65536, max_pages=1 << 16, page_size=1)])
 def test_pool_dims(K, kw):
     assert fork(K, paged(K, **kw)) == K.KDA_ERR_SHAPE
@@ -178,7 +178,7 @@ def test_copy_refusals(K):
     assert copy(K, None) == K.KDA_ERR_NULL
     for kw in (dict(head_dim=96), dict(dtype=5)):
         assert copy(K, paged(K, **kw)) == K.KDA_ERR_UNSUPPORTED
-    for kw in (dict(kv_heads=0), dict(pages=0), dict(page_size=0)):
+    for kw in (dict(kv_heads=0), dict(pages=0), dict(page_size=0), dict(pages=1 << 22, page_size=1 << 11)):
         assert copy(K, paged(K, **kw)) == K.KDA_ERR_SHAPE
     assert copy(K, paged(K), count=-1) == copy(K, paged(K), count=1 << 31) == K.KDA_ERR_SHAPE
     for x in ("kc", "vc", "copies"):

@@ -320,3 +320,16 @@ def test_commit_at_the_edges(K):
     lens = committed(c, rows, accepted)[2]
     got = K.kda_paged_tree_commit(c["k_cache"], c["v_cache"], c["block_table"], c["seq_lens"], None, at, tokens=6, new_lens=c["seq_lens"])
     assert got is c["seq_lens"] and got.tolist() == lens
+
+
+def test_commit_with_lengths_in_place(K):
+    """new_lens may be seq_lens: every token still goes by the old length."""
+    T, N = 40, 300
+    c = cache(22, [n % 70 for n in range(N)], T, 2, 2, 64, 16, BF16)
+    rows, parents = R.drafts(22, N, T, "tree", None)
+    accepted = [T - 1 - n % 5 for n in range(N)]
+    kc, vc, lens = committed(c, rows, accepted)
+    K.kda_paged_tree_commit(c["k_cache"], c["v_cache"], c["block_table"], c["seq_lens"], parents,
+                            torch.tensor(accepted, dtype=torch.int32, device="cuda"), new_lens=c["seq_lens"])
+    assert c["seq_lens"].tolist() == lens
+    assert torch.equal(c["k_cache"].cpu(), kc) and torch.equal(c["v_cache"].cpu(), vc)

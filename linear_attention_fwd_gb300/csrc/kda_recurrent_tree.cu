@@ -5,15 +5,18 @@
 // ("はじめての自然言語処理 -- Kimi K3", section 3.1, the chunkwise form, with a tree in the place of a line),
 //   u_i = beta_i (v_i - (E_i k_i)^T S) - sum_{j in A(i), j != i} beta_i (k_i . E_ij k_j) u_j,
 //   o_i = (E_i q_i)^T S + sum_{j in A(i)} (q_i . E_ij k_j) u_j,
-// so that the state is read once and no token's own state is formed.  A CTA takes a row's head:
-//  1. the state is requested straight into B fragments (each warp the 16 value channels that it keeps to the
-//     end), then the tokens' keys and decays are put into shared memory;
+// so that the state is read once and no token's own state is formed.  Nor is any u: with A the matrix of the pairs'
+// beta_i (k_i . E_ij k_j) below its diagonal, B that of q_i . E_ij k_j and W_i = beta_i (v_i - (E_i k_i)^T S),
+//   o = (E q) S + C W,   C (1 + A) = B,
+// and a row of C comes from the rows of A on the token's path alone, without the state.  |c_ij| <= |q_i| |k_j| for
+// normalised keys and beta <= 2 (a product of reflections at most lies between them).  A CTA takes a row's head:
+//  1. the tokens' keys, decays and queries are requested; the state and the values are only sent for to the L2 cache,
+//     which costs no registers, so that three CTAs share an SM and one's walks run beside another's products;
 //  2. eight lanes walk a token's path to its root with the running product of the decays: every factor is
-//     at most 1, no exponent of a sum is taken, and lines of 64 tokens need no bound on g.  They leave the two
-//     coefficients of each pair, E_i k_i and E_i q_i;
-//  3. (E k; E q) S on tensor cores (mma.sync, tf32; fp32 calls: three products of parts of 11 bits);
-//  4. each warp solves for its channels' u in the order of the tokens' depth, and adds up the outputs as it goes,
-//     without a barrier: four tokens of a depth at a time.
+//     at most 1, no exponent of a sum is taken, and lines of 64 tokens need no bound on g.  They leave A, B, E k and E q;
+//  3. the same eight lanes walk the path again for the token's row of C;
+//  4. (E k; E q) S, S straight into B fragments (each warp the 16 value channels that it keeps to the end), and C W on tensor cores (mma.sync, tf32; all of C W, and of fp32 calls, in three products of parts
+//     of 11 bits), the second added to the first in place.  A W that is not finite is left out of that and added along the paths.
 // Bound by reading the state: 64 KB per row and head at 128 x 128.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -43,6 +46,11 @@ template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bf
     const float2 x = __bfloat1622float2(a), y = __bfloat1622float2(b);
     return make_float4(x.x, x.y, y.x, y.y);
 }
+__device__ __forceinline__ void put4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 v) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+}
 __device__ __forceinline__ float4 mul4(float4 a, float4 b) { return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w); }
 __device__ __forceinline__ float4 mul4(float4 a, float b) { return make_float4(a.x * b, a.y * b, a.z * b, a.w * b); }
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c) { return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c)))); }
@@ -69,241 +77,333 @@ template <int DK> struct Row {
         for (int m = 0; m < DK / 32; ++m) s = dot4(x[m], x[m], s);
         return sum8(s);
     }
-    __device__ __forceinline__ void normalise(float eps) {   // x / sqrt(|x|^2 + eps); a zero row stays zero
-        const float den = norm2() + eps, sc = den > 0.f ? rsqrtf(den) : 0.f;
+    __device__ __forceinline__ float scale(float eps) const {   // 1 / sqrt(|x|^2 + eps); of a zero row, zero
+        const float den = norm2() + eps;
+        return den > 0.f ? rsqrtf(den) : 0.f;
+    }
+    __device__ __forceinline__ void normalise(float eps) {
+        const float sc = scale(eps);
 #pragma unroll
         for (int m = 0; m < DK / 32; ++m) x[m] = mul4(x[m], sc);
     }
 };
 
-// One pair of a token with a token j of its path.
-struct __align__(16) Pair {
-    float a, b;   // beta_i (k_i . E_ij k_j), q_i . E_ij k_j
-    int at;       // j
-    int pad;
+// Shared memory of a CTA, in bytes:
+//   keys as they are [T][DK] and decays [T][DK]; later W, [T rounded up to 8][DV + 8] (strides: so that what a warp reads
+//   at once falls into different banks)
+//   E k and E q, [rows][DK + 16]
+//   two square matrices of the pairs, [T][stride]: beta_i (k_i . E_ij k_j) and q_i . E_ij k_j, later C; zero off the paths
+//   parent, beta, what scales the key [T]
+template <int SIZE, int DK, int DV> struct Shared {
+    static constexpr int W = DV + 8, B = DK + 16;
+    static __host__ __device__ int rows(int T) { return T <= 8 ? 16 : 2 * ((T + 15) / 16 * 16); }
+    static __host__ __device__ int stride(int T) { return (T + 7) / 8 * 8 + 4; }
+    static __host__ __device__ int region_b(int T) {
+        const int x = T * DK * (4 + SIZE), y = (T + 7) / 8 * 8 * W * 4;
+        return x > y ? x : y;
+    }
+    static __host__ __device__ int pairs(int T) { return region_b(T) + rows(T) * B * 4; }
+    static __host__ __device__ int ints(int T) { return pairs(T) + 2 * T * stride(T) * 4; }
+    static __host__ __device__ int bytes(int T) { return ints(T) + 3 * T * 4; }
 };
 
-// Shared memory of a CTA, in bytes: [tokens] keys and decays, later the products with S (a: both, [2][T][max(DK, DV)]);
-// E k and E q [2 T rounded up to 16][DK + 16] (so that a quarter-warp's 16-byte reads of two rows fall into
-// different banks); pairs [T][T]; depth, parent, beta [T].
-template <int DK, int DV> struct Shared {
-    static constexpr int A = DK > DV ? DK : DV;   // a row of the first region
-    static constexpr int B = DK + 16;
-    static __host__ __device__ int rows(int T) { return (2 * T + 15) / 16 * 16; }
-    static __host__ __device__ int region_b(int T) { return 2 * T * A * 4; }
-    static __host__ __device__ int pairs(int T) { return region_b(T) + rows(T) * B * 4; }
-    static __host__ __device__ int ints(int T) { return pairs(T) + T * T * (int)sizeof(Pair); }
-    static __host__ __device__ int bytes(int T) { return ints(T) + 4 * T * 4; }
+// Four channels of an input as they are.
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+    float4 x;
+    __device__ __forceinline__ void load(const float *p) { x = load4(p); }
+    __device__ __forceinline__ float4 get() const { return x; }
 };
+template <> struct Raw<__nv_bfloat16> {
+    uint2 x;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { x = __ldg(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ float4 get() const {
+        return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
+    }
+};
+
+// Whether x may enter a product whose other operand can be zero (and neither of its parts overflows).
+__device__ __forceinline__ bool tame(float x) { return fabsf(x) <= 1e38f; }
+
+// c += A B in three products of parts of 11 bits, B of two tiles whose columns are interleaved.
+struct Parts {
+    uint32_t h, l;
+    __device__ __forceinline__ explicit Parts(float x) {
+        h = tf32(x);
+        l = tf32(x - __uint_as_float(h));
+    }
+};
+__device__ __forceinline__ void mma_parts(float (&c)[2][4], const float (&f)[4], float2 b0, float2 b1) {
+    const Parts a0(f[0]), a1(f[1]), a2(f[2]), a3(f[3]), x0(b0.x), x1(b1.x), y0(b0.y), y1(b1.y);
+    mma_1688(c[0], a0.l, a1.l, a2.l, a3.l, x0.h, x1.h);
+    mma_1688(c[1], a0.l, a1.l, a2.l, a3.l, y0.h, y1.h);
+    mma_1688(c[0], a0.h, a1.h, a2.h, a3.h, x0.l, x1.l);
+    mma_1688(c[1], a0.h, a1.h, a2.h, a3.h, y0.l, y1.l);
+    mma_1688(c[0], a0.h, a1.h, a2.h, a3.h, x0.h, x1.h);
+    mma_1688(c[1], a0.h, a1.h, a2.h, a3.h, y0.h, y1.h);
+}
+
+// Four channels of a token's key in shared memory.
+__device__ __forceinline__ float4 read4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 read4(const __nv_bfloat16 *p) {
+    Raw<__nv_bfloat16> r;
+    r.x = *reinterpret_cast<const uint2 *>(p);
+    return r.get();
+}
+__device__ __forceinline__ void keep4(__nv_bfloat16 *p, const Raw<__nv_bfloat16> &r) { *reinterpret_cast<uint2 *>(p) = r.x; }
+__device__ __forceinline__ void keep4(float *p, const Raw<float> &r) { *reinterpret_cast<float4 *>(p) = r.x; }
 
 template <typename Tin, int DK, int DV>
-__global__ void __launch_bounds__(2 * DV, 256 / DV) kda_recurrent_tree_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(2 * DV, (sizeof(Tin) == 4 ? 256 : 384) / DV) kda_recurrent_tree_kernel(const TreeArgs a) {
     constexpr bool kF32 = sizeof(Tin) == 4;
-    constexpr int kThreads = 2 * DV, kGroups = kThreads / 8, kSteps = DK / 16;
-    using S = Shared<DK, DV>;
+    constexpr int kThreads = 2 * DV, kGroups = kThreads / 8, kSteps = DK / 16, kTiles = 4, kAhead = 2;
+    using S = Shared<sizeof(Tin), DK, DV>;
     extern __shared__ __align__(16) uint8_t sm[];
-    const int T = a.tokens;
-    float *sk = reinterpret_cast<float *>(sm), *sa = sk + T * DK;             // keys, decays
-    float *pk = sk, *pq = sk + T * S::A;                                      // later: products (u in place of the first)
-    float *sb = reinterpret_cast<float *>(sm + S::region_b(T));               // E k, then E q
-    Pair *pairs = reinterpret_cast<Pair *>(sm + S::pairs(T));
-    int *depth = reinterpret_cast<int *>(sm + S::ints(T)), *parent = depth + T;
-    float *beta = reinterpret_cast<float *>(parent + T);
-    int *order = reinterpret_cast<int *>(beta + T);                           // tokens by depth; their depth above bit 8
+    const int T = a.tokens, ST = S::stride(T);
+    float *sa = reinterpret_cast<float *>(sm), *sw = sa;                      // decays; later W
+    Tin *sk = reinterpret_cast<Tin *>(sa + T * DK);                           // keys
+    float *sb = reinterpret_cast<float *>(sm + S::region_b(T));               // E k, E q
+    float *pa = reinterpret_cast<float *>(sm + S::pairs(T)), *pc = pa + T * ST;
+    int *parent = reinterpret_cast<int *>(sm + S::ints(T));
+    float *beta = reinterpret_cast<float *>(parent + T), *norm = beta + T;
 
     const int n = blockIdx.x / a.heads, h = blockIdx.x - n * a.heads;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int slot = a.idx ? __ldg(a.idx + n) : n;
-    const int m = slot < 0 || slot >= a.slots ? 0 : tree_count(a.num, T, n);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = tid >> 3, l = tid & 7;
+    const int slot = a.idx ? __ldg(a.idx + n) : n, count = tree_count(a.num, T, n);
     const int64_t first = ((int64_t)n * T * a.heads + h);                     // token i's row: first + i * heads
-    for (int x = tid; x < (T - m) * DV; x += kThreads)                        // tokens past the count
-        static_cast<Tin *>(a.out)[(first + (int64_t)(m + x / DV) * a.heads) * DV + x % DV] = from_f<Tin>(0.f);
-    if (m == 0) return;
+    // a lane's x-th four channels (odd groups swap pairs, so that two groups' 64 bytes fall into different banks)
+    auto chan = [&](int x) { return (x & 1 ? 32 * x - 32 * (grp & 1) : 32 * x + 32 * (grp & 1)) + 4 * l; };
+    Raw<Tin> k_raw[DK / 32], g_raw[DK / 32], q_raw[DK / 32];
+    auto ask = [&](Raw<Tin> (&to)[DK / 32], const void *from, int i) {
+        const Tin *p = static_cast<const Tin *>(from) + (first + (int64_t)i * a.heads) * DK;
+#pragma unroll
+        for (int x = 0; x < DK / 32; ++x) to[x].load(p + chan(x));
+    };
+    const int i_first = grp < T ? grp : T - 1;
+    ask(k_raw, a.k, i_first);
+    ask(g_raw, a.g, i_first);
+    if constexpr (!kF32) ask(q_raw, a.q, i_first);
+    const int t_own = tid < T ? tid : T - 1;
+    const float beta_own = to_f(static_cast<const Tin *>(a.beta)[first + (int64_t)t_own * a.heads]);
+    const int parent_own = tree_parent(a.parents, T, n, t_own);
+    const int m = slot < 0 || slot >= a.slots ? 0 : count;
 
-    // the state as B fragments: this lane's channels 16 s + 4 t4 + e of the keys, value channels c0 + 2 g and + 1
-    const int g = lane >> 2, t4 = lane & 3, c0 = 16 * warp;
-    float2 s[kSteps][4];
-    {
-        const float *src = a.state + ((int64_t)slot * a.heads + h) * (DK * DV) + (4 * t4) * DV + c0 + 2 * g;
-#pragma unroll
-        for (int st = 0; st < kSteps; ++st)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[st][e] = __ldcs(reinterpret_cast<const float2 *>(src + (16 * st + e) * DV));
+    // the state and the values are on their way to the L2 cache while the walks run
+    const float *state = a.state + ((int64_t)(m > 0 ? slot : 0) * a.heads + h) * (DK * DV);
+    if (m > 0) {
+        constexpr int kPart = DK * DV * 4 / 4;
+        if (tid < 4) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<const uint8_t *>(state) + tid * kPart), "n"(kPart) : "memory");
+        constexpr int kLines = DV * (int)sizeof(Tin) / 128;
+        for (int x = tid; x < m * kLines; x += kThreads)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const Tin *>(a.v) + (first + (int64_t)(x / kLines) * a.heads) * DV + x % kLines * (128 / (int)sizeof(Tin))));
     }
-    const int grp = tid >> 3, l = tid & 7;
+    constexpr int kVecs = DV * (int)sizeof(Tin) / 16;
+    for (int x = tid; x < (T - m) * kVecs; x += kThreads)                     // outputs of tokens past the count
+        reinterpret_cast<uint4 *>(static_cast<Tin *>(a.out) + (first + (int64_t)(m + x / kVecs) * a.heads) * DV)[x % kVecs] = make_uint4(0, 0, 0, 0);
+    if (m == 0) return;
+    for (int x = tid; x < 2 * m * ST / 4; x += kThreads) {                    // (rows of both; strides are multiples of four)
+        const int half = x >= m * ST / 4;
+        reinterpret_cast<float4 *>(half ? pc : pa)[x - half * (m * ST / 4)] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (tid < m) parent[tid] = parent_own, beta[tid] = beta_own;
     for (int i0 = 0; i0 < m; i0 += kGroups) {
         const int i = i0 + grp < m ? i0 + grp : m - 1;   // (groups without a token repeat the last one's)
-        const int64_t at = (first + (int64_t)i * a.heads) * DK + 4 * l;
-        Row<DK> k;
-        float4 d[DK / 32];
+        if (i0 > 0 || i != i_first) {
+            ask(k_raw, a.k, i);
+            ask(g_raw, a.g, i);
+        }
+        float scale = 1.f;
+        if (a.qk_eps >= 0.f) {
+            Row<DK> k;
+#pragma unroll
+            for (int x = 0; x < DK / 32; ++x) k.x[x] = k_raw[x].get();
+            scale = k.scale(a.qk_eps);
+        }
+        if (l == 0) norm[i] = scale;
 #pragma unroll
         for (int x = 0; x < DK / 32; ++x) {
-            k.x[x] = load4(static_cast<const Tin *>(a.k) + at + 32 * x);
-            d[x] = load4(static_cast<const Tin *>(a.g) + at + 32 * x);
-        }
-        if (a.qk_eps >= 0.f) k.normalise(a.qk_eps);
-#pragma unroll
-        for (int x = 0; x < DK / 32; ++x) {
-            *reinterpret_cast<float4 *>(sk + i * DK + 32 * x + 4 * l) = k.x[x];
-            *reinterpret_cast<float4 *>(sa + i * DK + 32 * x + 4 * l) = make_float4(expf(d[x].x), expf(d[x].y), expf(d[x].z), expf(d[x].w));
-        }
-        if (l == 0) {
-            parent[i] = tree_parent(a.parents, T, n, i);
-            beta[i] = to_f(static_cast<const Tin *>(a.beta)[first + (int64_t)i * a.heads]);
+            const float4 d = g_raw[x].get();
+            keep4(sk + i * DK + chan(x), k_raw[x]);
+            *reinterpret_cast<float4 *>(sa + i * DK + chan(x)) = make_float4(expf(d.x), expf(d.y), expf(d.z), expf(d.w));
         }
     }
     __syncthreads();
 
     // the walks
+    const int q0 = m <= 8 ? 8 : (m + 15) / 16 * 16;      // E q's first row: up to 8 tokens share a tile of 16 rows
     for (int i0 = 0; i0 < m; i0 += kGroups) {
         const bool mine = i0 + grp < m;
         const int i = mine ? i0 + grp : m - 1;
-        const int64_t at = (first + (int64_t)i * a.heads) * DK + 4 * l;
+        if (kF32 || i0 > 0 || i != i_first) ask(q_raw, a.q, i);
         Row<DK> k, q;
         float4 d[DK / 32];
+        const float own = norm[i];
 #pragma unroll
         for (int x = 0; x < DK / 32; ++x) {
-            q.x[x] = load4(static_cast<const Tin *>(a.q) + at + 32 * x);
-            k.x[x] = *reinterpret_cast<const float4 *>(sk + i * DK + 32 * x + 4 * l);
+            q.x[x] = q_raw[x].get();
+            k.x[x] = mul4(read4(sk + i * DK + chan(x)), own);
             d[x] = make_float4(1.f, 1.f, 1.f, 1.f);
         }
-        if (a.qk_eps >= 0.f) q.normalise(a.qk_eps);
+        if (a.qk_eps >= 0.f) {
+            const float scale = q.scale(a.qk_eps);
+#pragma unroll
+            for (int x = 0; x < DK / 32; ++x) q.x[x] = mul4(q.x[x], scale);
+        }
         const float bt = beta[i];
-        int j = mine ? i : -1, e = 0;
+        int j = mine ? i : -1;
         while (__any_sync(0xffffffffu, j >= 0)) {
             const int jj = j >= 0 ? j : 0;
             float kk = 0.f, qq = 0.f;
 #pragma unroll
             for (int x = 0; x < DK / 32; ++x) {
-                const float4 y = mul4(*reinterpret_cast<const float4 *>(sk + jj * DK + 32 * x + 4 * l), d[x]);
+                const float4 y = mul4(read4(sk + jj * DK + chan(x)), d[x]);
                 kk = dot4(k.x[x], y, kk);
                 qq = dot4(q.x[x], y, qq);
             }
             kk = sum8(kk);
             qq = sum8(qq);
             if (j >= 0) {
-                if (l == 0) pairs[i * T + e] = Pair{bt * kk, qq, j, 0};
+                if (l == 0) {
+                    const float scale = norm[jj];
+                    if (j != i) pa[i * ST + j] = bt * scale * kk;
+                    pc[i * ST + j] = scale * qq;
+                }
 #pragma unroll
-                for (int x = 0; x < DK / 32; ++x) d[x] = mul4(d[x], *reinterpret_cast<const float4 *>(sa + jj * DK + 32 * x + 4 * l));
+                for (int x = 0; x < DK / 32; ++x) d[x] = mul4(d[x], read4(sa + jj * DK + chan(x)));
                 j = parent[jj];
-                ++e;
             }
         }
         if (mine) {
-            if (l == 0) depth[i] = e;
 #pragma unroll
             for (int x = 0; x < DK / 32; ++x) {
-                *reinterpret_cast<float4 *>(sb + i * S::B + 32 * x + 4 * l) = operand<kF32>(mul4(k.x[x], d[x]));
-                *reinterpret_cast<float4 *>(sb + (m + i) * S::B + 32 * x + 4 * l) = operand<kF32>(mul4(q.x[x], d[x]));
+                *reinterpret_cast<float4 *>(sb + i * S::B + chan(x)) = operand<kF32>(mul4(k.x[x], d[x]));
+                *reinterpret_cast<float4 *>(sb + (q0 + i) * S::B + chan(x)) = operand<kF32>(mul4(q.x[x], d[x]));
             }
         }
     }
-    __syncthreads();   // keys and decays are read: their place takes the products
-    if (tid < m) {     // (read behind the next barrier)
-        const int mine = depth[tid];
-        int rank = 0;
-        for (int j = 0; j < m; ++j) rank += depth[j] < mine || (depth[j] == mine && j < tid);
-        order[rank] = mine << 8 | tid;
+    __syncthreads();   // keys and decays are read: W takes their place
+
+    // the state's B fragments: this lane's channels 16 st + 4 t4 + e of the keys, value channels c0 + 2 g and + 1
+    const int g = lane >> 2, t4 = lane & 3, c0 = 16 * warp;
+    float2 s[kAhead][4];
+    auto load_state = [&](int st) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[st % kAhead][e] = __ldcs(reinterpret_cast<const float2 *>(state + (16 * st + 4 * t4 + e) * DV + c0 + 2 * g));
+    };
+#pragma unroll
+    for (int st = 0; st < kAhead; ++st) load_state(st);
+
+    // C's rows: along the path, each c_ij that is final is taken out of those above it.  Lane l has j = 8 x + l.
+    for (int i0 = 0; i0 < m; i0 += kGroups) {
+        const bool mine = i0 + grp < m;
+        const int i = mine ? i0 + grp : m - 1;
+        float r[kTreeMax / 8];
+#pragma unroll
+        for (int x = 0; x < kTreeMax / 8; ++x) r[x] = 8 * x <= i ? pc[i * ST + 8 * x + l] : 0.f;
+        int j = mine ? i : -1;
+        while (__any_sync(0xffffffffu, j >= 0)) {
+            const int jj = j >= 0 ? j : 0;
+            float c = r[0];
+#pragma unroll
+            for (int x = 1; x < kTreeMax / 8; ++x) c = (jj >> 3) == x ? r[x] : c;
+            c = __shfl_sync(0xffffffffu, c, (lane & 24) | (jj & 7));
+            if (j >= 0) {
+#pragma unroll
+                for (int x = 0; x < kTreeMax / 8; ++x)
+                    if (8 * x < jj) r[x] = fmaf(-c, pa[jj * ST + 8 * x + l], r[x]);
+                j = parent[jj];
+            }
+        }
+        if (mine)
+#pragma unroll
+            for (int x = 0; x < kTreeMax / 8; ++x)
+                if (8 * x <= i) pc[i * ST + 8 * x + l] = r[x];
     }
 
-    if constexpr (!kF32) {   // the state as an operand
+    const int m8 = (m + 7) / 8 * 8, tiles = (q0 + m + 15) / 16;
+    bool met = false, bad = false;
+    for (int t0 = 0; t0 < tiles; t0 += kTiles) {   // tiles of 16 rows of (E k; E q), four at a time; rows of no token hold anything
+        float c[kTiles][2][4] = {};
+        if (t0 > 0)
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[st][e] = make_float2(__uint_as_float(tf32(s[st][e].x)), __uint_as_float(tf32(s[st][e].y)));
-    }
-    for (int r0 = 0; r0 < 2 * m; r0 += 16) {   // rows r0 .. r0 + 15 of (E k; E q); those past 2 m hold anything
-        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        float4 v0, v1;
-        const int ra = r0 + g, rb = ra + 8;
-        if (ra < m) v0 = load4(static_cast<const Tin *>(a.v) + (first + (int64_t)ra * a.heads) * DV + c0 + 4 * t4);
-        if (rb < m) v1 = load4(static_cast<const Tin *>(a.v) + (first + (int64_t)rb * a.heads) * DV + c0 + 4 * t4);
+            for (int st = 0; st < kAhead; ++st) load_state(st);
 #pragma unroll
         for (int st = 0; st < kSteps; ++st) {
-            const float4 x = *reinterpret_cast<const float4 *>(sb + ra * S::B + 16 * st + 4 * t4);
-            const float4 y = *reinterpret_cast<const float4 *>(sb + rb * S::B + 16 * st + 4 * t4);
+            float2 b[4];
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {   // two steps of 8 key channels
-                const float f[4] = {p ? x.z : x.x, p ? y.z : y.x, p ? x.w : x.y, p ? y.w : y.y};
-                const float2 b0 = s[st][2 * p], b1 = s[st][2 * p + 1];
-                if constexpr (kF32) {
-                    uint32_t fh[4], fl[4];
+            for (int e = 0; e < 4; ++e) {
+                b[e] = s[st % kAhead][e];
+                if constexpr (!kF32) b[e] = make_float2(__uint_as_float(tf32(b[e].x)), __uint_as_float(tf32(b[e].y)));
+            }
+            if (st + kAhead < kSteps) load_state(st + kAhead);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        fh[e] = tf32(f[e]);
-                        fl[e] = tf32(f[e] - __uint_as_float(fh[e]));
+            for (int t = 0; t < kTiles; ++t) {
+                if (t0 + t >= tiles) break;
+                const float *row = sb + (16 * (t0 + t) + g) * S::B + 16 * st + 4 * t4;
+                const float4 x = *reinterpret_cast<const float4 *>(row), y = *reinterpret_cast<const float4 *>(row + 8 * S::B);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {   // two steps of 8 key channels
+                    const float f[4] = {p ? x.z : x.x, p ? y.z : y.x, p ? x.w : x.y, p ? y.w : y.y};
+                    const float2 b0 = b[2 * p], b1 = b[2 * p + 1];
+                    if constexpr (kF32) {
+                        mma_parts(c[t], f, b0, b1);
+                    } else {
+                        const uint32_t a0 = __float_as_uint(f[0]), a1 = __float_as_uint(f[1]), a2 = __float_as_uint(f[2]), a3 = __float_as_uint(f[3]);
+                        mma_1688(c[t][0], a0, a1, a2, a3, __float_as_uint(b0.x), __float_as_uint(b1.x));
+                        mma_1688(c[t][1], a0, a1, a2, a3, __float_as_uint(b0.y), __float_as_uint(b1.y));
                     }
-                    const uint32_t h00 = tf32(b0.x), h10 = tf32(b1.x), h01 = tf32(b0.y), h11 = tf32(b1.y);
-                    const uint32_t l00 = tf32(b0.x - __uint_as_float(h00)), l10 = tf32(b1.x - __uint_as_float(h10));
-                    const uint32_t l01 = tf32(b0.y - __uint_as_float(h01)), l11 = tf32(b1.y - __uint_as_float(h11));
-                    mma_1688(c[0], fl[0], fl[1], fl[2], fl[3], h00, h10);
-                    mma_1688(c[1], fl[0], fl[1], fl[2], fl[3], h01, h11);
-                    mma_1688(c[0], fh[0], fh[1], fh[2], fh[3], l00, l10);
-                    mma_1688(c[1], fh[0], fh[1], fh[2], fh[3], l01, l11);
-                    mma_1688(c[0], fh[0], fh[1], fh[2], fh[3], h00, h10);
-                    mma_1688(c[1], fh[0], fh[1], fh[2], fh[3], h01, h11);
-                } else {
-                    const uint32_t a0 = __float_as_uint(f[0]), a1 = __float_as_uint(f[1]), a2 = __float_as_uint(f[2]), a3 = __float_as_uint(f[3]);
-                    mma_1688(c[0], a0, a1, a2, a3, __float_as_uint(b0.x), __float_as_uint(b1.x));
-                    mma_1688(c[1], a0, a1, a2, a3, __float_as_uint(b0.y), __float_as_uint(b1.y));
                 }
             }
         }
-        // c[t][0..1]: row ra, value channels c0 + 4 t4 + t and + 2 + t; c[t][2..3]: row rb
-        auto put = [&](int r, float4 x, float4 v) {
-            if (r < m) {
-                const float b = beta[r];
-                *reinterpret_cast<float4 *>(pk + r * S::A + c0 + 4 * t4) = make_float4(b * (v.x - x.x), b * (v.y - x.y), b * (v.z - x.z), b * (v.w - x.w));
-            } else if (r < 2 * m) {
-                *reinterpret_cast<float4 *>(pq + (r - m) * S::A + c0 + 4 * t4) = x;
-            }
-        };
-        put(ra, make_float4(c[0][0], c[1][0], c[0][1], c[1][1]), v0);
-        put(rb, make_float4(c[0][2], c[1][2], c[0][3], c[1][3]), v1);
-    }
-    __syncthreads();
-
-    // u and the outputs of this warp's 16 value channels.  Tokens of the same depth do not depend on one another: each half of
-    // the warp takes two of them at a time; of one alone, half of its pairs.
-    const int ch = c0 + (lane & 15), half = lane >> 4;
-    auto give = [&](int i, float w, float y, float x) {   // a token's sums: u, and its output
-        const float u = pk[i * S::A + ch] - x;
-        pk[i * S::A + ch] = u;
-        static_cast<Tin *>(a.out)[(first + (int64_t)i * a.heads) * DV + ch] = from_f<Tin>(fmaf(w, u, pq[i * S::A + ch] + y));
-    };
-    for (int pos = 0; pos < m;) {
-        const int o = order[pos + (lane & 3) < m ? pos + (lane & 3) : pos];
-        const int depth0 = __shfl_sync(0xffffffffu, o, 0) >> 8;
-        const int same = __popc(__ballot_sync(0xffffffffu, lane < 4 && pos + lane < m && (o >> 8) == depth0));   // (sorted: the first ones)
-        const bool alone = same == 1, go0 = half < same, go1 = 2 + half < same;
-        const int i0 = __shfl_sync(0xffffffffu, o, alone ? 0 : half) & 255, i1 = __shfl_sync(0xffffffffu, o, go1 ? 2 + half : 0) & 255;
-        const Pair *r0 = pairs + i0 * T, *r1 = pairs + i1 * T;
-        float x0 = 0.f, y0 = 0.f, x1 = 0.f, y1 = 0.f;
-        if (alone) {
-#pragma unroll 4
-            for (int e = 1 + half; e < depth0; e += 2) {
-                const Pair p = r0[e];
-                const float u = pk[p.at * S::A + ch];
-                x0 = fmaf(p.a, u, x0);
-                y0 = fmaf(p.b, u, y0);
-            }
-            x0 += __shfl_xor_sync(0xffffffffu, x0, 16);
-            y0 += __shfl_xor_sync(0xffffffffu, y0, 16);
-        } else {
-#pragma unroll 4
-            for (int e = 1; e < depth0; ++e) {
-                const Pair p0 = r0[e], p1 = r1[e];
-                const float u0 = pk[p0.at * S::A + ch], u1 = pk[p1.at * S::A + ch];
-                x0 = fmaf(p0.a, u0, x0);
-                y0 = fmaf(p0.b, u0, y0);
-                x1 = fmaf(p1.a, u1, x1);
-                y1 = fmaf(p1.b, u1, y1);
-            }
+        // c[t][e][0..1]: row ra, value channels c0 + 4 t4 + e and + 2 + e; c[t][e][2..3]: row rb
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const int ra = 16 * (t0 + t) + g, rb = ra + 8;
+            auto put = [&](int r, float4 x) {   // W, and zeros up to a multiple of eight
+                if (r >= m8 || r >= q0) return;
+                float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < m) {
+                    const float4 v = load4(static_cast<const Tin *>(a.v) + (first + (int64_t)r * a.heads) * DV + c0 + 4 * t4);
+                    const float b = beta[r];
+                    w = make_float4(b * (v.x - x.x), b * (v.y - x.y), b * (v.z - x.z), b * (v.w - x.w));
+                    bad |= !(tame(w.x) && tame(w.y) && tame(w.z) && tame(w.w));
+                }
+                *reinterpret_cast<float4 *>(sw + r * S::W + c0 + 4 * t4) = w;
+            };
+            put(ra, make_float4(c[t][0][0], c[t][1][0], c[t][0][1], c[t][1][1]));
+            put(rb, make_float4(c[t][0][2], c[t][1][2], c[t][0][3], c[t][1][3]));
         }
-        if (go0) give(i0, r0[0].b, y0, x0);
-        if (go1) give(i1, r1[0].b, y1, x1);
-        pos += same;
-        __syncwarp();
+        if (16 * (t0 + kTiles) <= q0) continue;
+        if (!met) __syncthreads();   // C is there
+        met = true;
+        __syncwarp();                // and this warp's W
+        const bool any_bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const int i0 = 16 * (t0 + t) - q0, ia = i0 + g, ib = ia + 8;
+            if (t0 + t >= tiles || i0 + 8 < 0) continue;   // (16 rows of E k; up to 8 tokens share one tile)
+            const bool in_a = ia >= 0 && ia < m, in_b = ib < m;
+            for (int j = 0; j < m8 && j < i0 + 16; j += 8) {
+                const float f[4] = {in_a ? pc[ia * ST + j + t4] : 0.f, in_b ? pc[ib * ST + j + t4] : 0.f,
+                                    in_a ? pc[ia * ST + j + 4 + t4] : 0.f, in_b ? pc[ib * ST + j + 4 + t4] : 0.f};
+                const float2 x = *reinterpret_cast<const float2 *>(sw + (j + t4) * S::W + c0 + 2 * g);
+                const float2 y = *reinterpret_cast<const float2 *>(sw + (j + 4 + t4) * S::W + c0 + 2 * g);
+                mma_parts(c[t], f, make_float2(tame(x.x) ? x.x : 0.f, tame(x.y) ? x.y : 0.f), make_float2(tame(y.x) ? y.x : 0.f, tame(y.y) ? y.y : 0.f));
+            }
+            if (any_bad) {   // what is not finite reaches the tokens that continue it, and no others
+                auto add = [&](float x, float w, float &to) { to = tame(w) ? to : fmaf(x, w, to); };
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    for (int i = e ? ib : ia, j = (e ? in_b : in_a) ? i : -1; j >= 0; j = parent[j]) {
+                        const float x = pc[i * ST + j];
+                        const float4 w = *reinterpret_cast<const float4 *>(sw + j * S::W + c0 + 4 * t4);
+                        add(x, w.x, c[t][0][2 * e]), add(x, w.y, c[t][1][2 * e]), add(x, w.z, c[t][0][2 * e + 1]), add(x, w.w, c[t][1][2 * e + 1]);
+                    }
+            }
+            auto give = [&](int i, float4 o) { put4(static_cast<Tin *>(a.out) + (first + (int64_t)i * a.heads) * DV + c0 + 4 * t4, o); };
+            if (in_a) give(ia, make_float4(c[t][0][0], c[t][1][0], c[t][0][1], c[t][1][1]));
+            if (in_b) give(ib, make_float4(c[t][0][2], c[t][1][2], c[t][0][3], c[t][1][3]));
+        }
     }
 }
 
@@ -402,9 +502,9 @@ cudaError_t launch(const TreeArgs &a, bool commit, cudaStream_t st) {
         kda_recurrent_tree_commit_kernel<Tin, DK, DV><<<grid, 2 * DV, 0, st>>>(a);
         return cudaGetLastError();
     }
-    const int bytes = Shared<DK, DV>::bytes(a.tokens);
+    const int bytes = Shared<sizeof(Tin), DK, DV>::bytes(a.tokens);
     const cudaError_t e = cudaFuncSetAttribute(kda_recurrent_tree_kernel<Tin, DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Shared<DK, DV>::bytes(kTreeMax));
+                                               Shared<sizeof(Tin), DK, DV>::bytes(kTreeMax));
     if (e != cudaSuccess) return e;
     kda_recurrent_tree_kernel<Tin, DK, DV><<<grid, 2 * DV, bytes, st>>>(a);
     return cudaGetLastError();

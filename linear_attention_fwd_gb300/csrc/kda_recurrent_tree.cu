@@ -11,7 +11,7 @@
 // and a row of C comes from the rows of A on the token's path alone, without the state.  |c_ij| <= |q_i| |k_j| for
 // normalised keys and beta <= 2 (a product of reflections at most lies between them).  A CTA takes a row's head:
 //  1. the tokens' keys, decays and queries are requested; the state and the values are only sent for to the L2 cache,
-//     which costs no registers, so that three CTAs share an SM and one's walks run beside another's products;
+//     which costs no registers, and are there when the walks are done;
 //  2. eight lanes walk a token's path to its root with the running product of the decays: every factor is
 //     at most 1, no exponent of a sum is taken, and lines of 64 tokens need no bound on g.  They leave A, B, E k and E q;
 //  3. the same eight lanes walk the path again for the token's row of C;
@@ -20,6 +20,8 @@
 // Bound by reading the state: 64 KB per row and head at 128 x 128.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "kda_internal.h"
 #include "kda_tree.h"
@@ -89,22 +91,22 @@ template <int DK> struct Row {
 };
 
 // Shared memory of a CTA, in bytes:
-//   keys as they are [T][DK] and decays [T][DK]; later W, [T rounded up to 8][DV + 8] (strides: so that what a warp reads
-//   at once falls into different banks)
-//   E k and E q, [rows][DK + 16]
+//   keys and decays, [2][T][DK]; later W, [T rounded up to 8][DV + 8] (strides: so that what a warp reads at once falls
+//   into different banks)
+//   E k and E q, [rows][DK], chunk c of 16 bytes of row r at c ^ 4 (r & 1) for the same reason
 //   two square matrices of the pairs, [T][stride]: beta_i (k_i . E_ij k_j) and q_i . E_ij k_j, later C; zero off the paths
-//   parent, beta, what scales the key [T]
-template <int SIZE, int DK, int DV> struct Shared {
-    static constexpr int W = DV + 8, B = DK + 16;
+//   parent, beta [T]
+template <int DK, int DV> struct Shared {
+    static constexpr int W = DV + 8;
     static __host__ __device__ int rows(int T) { return T <= 8 ? 16 : 2 * ((T + 15) / 16 * 16); }
     static __host__ __device__ int stride(int T) { return (T + 7) / 8 * 8 + 4; }
     static __host__ __device__ int region_b(int T) {
-        const int x = T * DK * (4 + SIZE), y = (T + 7) / 8 * 8 * W * 4;
+        const int x = 2 * T * DK * 4, y = (T + 7) / 8 * 8 * W * 4;
         return x > y ? x : y;
     }
-    static __host__ __device__ int pairs(int T) { return region_b(T) + rows(T) * B * 4; }
+    static __host__ __device__ int pairs(int T) { return region_b(T) + rows(T) * DK * 4; }
     static __host__ __device__ int ints(int T) { return pairs(T) + 2 * T * stride(T) * 4; }
-    static __host__ __device__ int bytes(int T) { return ints(T) + 3 * T * 4; }
+    static __host__ __device__ int bytes(int T) { return ints(T) + 2 * T * 4; }
 };
 
 // Four channels of an input as they are.
@@ -143,41 +145,64 @@ __device__ __forceinline__ void mma_parts(float (&c)[2][4], const float (&f)[4],
     mma_1688(c[1], a0.h, a1.h, a2.h, a3.h, y0.h, y1.h);
 }
 
-// Four channels of a token's key in shared memory.
-__device__ __forceinline__ float4 read4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 read4(const __nv_bfloat16 *p) {
-    Raw<__nv_bfloat16> r;
-    r.x = *reinterpret_cast<const uint2 *>(p);
-    return r.get();
+// Four channels as two pairs for packed arithmetic: a walk's time is largely that of issuing its instructions.
+struct Two {
+    uint64_t lo, hi;
+    __device__ __forceinline__ Two() {}
+    __device__ __forceinline__ explicit Two(const float *p) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(p);
+        lo = x.x, hi = x.y;
+    }
+    __device__ __forceinline__ explicit Two(float4 v) {
+        asm("mov.b64 %0, {%1, %2};" : "=l"(lo) : "f"(v.x), "f"(v.y));
+        asm("mov.b64 %0, {%1, %2};" : "=l"(hi) : "f"(v.z), "f"(v.w));
+    }
+    __device__ __forceinline__ float4 get() const {
+        float4 v;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(lo));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(v.z), "=f"(v.w) : "l"(hi));
+        return v;
+    }
+};
+__device__ __forceinline__ Two mul2(const Two &a, const Two &b) {
+    Two c;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(c.lo) : "l"(a.lo), "l"(b.lo));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(c.hi) : "l"(a.hi), "l"(b.hi));
+    return c;
 }
-__device__ __forceinline__ void keep4(__nv_bfloat16 *p, const Raw<__nv_bfloat16> &r) { *reinterpret_cast<uint2 *>(p) = r.x; }
-__device__ __forceinline__ void keep4(float *p, const Raw<float> &r) { *reinterpret_cast<float4 *>(p) = r.x; }
+__device__ __forceinline__ void dot2(const Two &a, const Two &b, uint64_t &c) {   // (c's halves are summed at the end)
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a.lo), "l"(b.lo));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a.hi), "l"(b.hi));
+}
+__device__ __forceinline__ float halves(uint64_t c) {
+    float x, y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(c));
+    return x + y;
+}
 
 template <typename Tin, int DK, int DV>
-__global__ void __launch_bounds__(2 * DV, (sizeof(Tin) == 4 ? 256 : 384) / DV) kda_recurrent_tree_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(2 * DV, 256 / DV) kda_recurrent_tree_kernel(const TreeArgs a) {
     constexpr bool kF32 = sizeof(Tin) == 4;
-    constexpr int kThreads = 2 * DV, kGroups = kThreads / 8, kSteps = DK / 16, kTiles = 4, kAhead = 2;
-    using S = Shared<sizeof(Tin), DK, DV>;
+    constexpr int kThreads = 2 * DV, kGroups = kThreads / 8, kSteps = DK / 16, kTiles = 4, kAhead = 4;
+    using S = Shared<DK, DV>;
     extern __shared__ __align__(16) uint8_t sm[];
     const int T = a.tokens, ST = S::stride(T);
-    float *sa = reinterpret_cast<float *>(sm), *sw = sa;                      // decays; later W
-    Tin *sk = reinterpret_cast<Tin *>(sa + T * DK);                           // keys
+    float *sk = reinterpret_cast<float *>(sm), *sa = sk + T * DK;             // keys, decays
+    float *sw = sk;                                                           // later: W
     float *sb = reinterpret_cast<float *>(sm + S::region_b(T));               // E k, E q
     float *pa = reinterpret_cast<float *>(sm + S::pairs(T)), *pc = pa + T * ST;
     int *parent = reinterpret_cast<int *>(sm + S::ints(T));
-    float *beta = reinterpret_cast<float *>(parent + T), *norm = beta + T;
+    float *beta = reinterpret_cast<float *>(parent + T);
 
     const int n = blockIdx.x / a.heads, h = blockIdx.x - n * a.heads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = tid >> 3, l = tid & 7;
     const int slot = a.idx ? __ldg(a.idx + n) : n, count = tree_count(a.num, T, n);
     const int64_t first = ((int64_t)n * T * a.heads + h);                     // token i's row: first + i * heads
-    // a lane's x-th four channels (odd groups swap pairs, so that two groups' 64 bytes fall into different banks)
-    auto chan = [&](int x) { return (x & 1 ? 32 * x - 32 * (grp & 1) : 32 * x + 32 * (grp & 1)) + 4 * l; };
     Raw<Tin> k_raw[DK / 32], g_raw[DK / 32], q_raw[DK / 32];
     auto ask = [&](Raw<Tin> (&to)[DK / 32], const void *from, int i) {
         const Tin *p = static_cast<const Tin *>(from) + (first + (int64_t)i * a.heads) * DK;
 #pragma unroll
-        for (int x = 0; x < DK / 32; ++x) to[x].load(p + chan(x));
+        for (int x = 0; x < DK / 32; ++x) to[x].load(p + 32 * x + 4 * l);
     };
     const int i_first = grp < T ? grp : T - 1;
     ask(k_raw, a.k, i_first);
@@ -212,19 +237,15 @@ __global__ void __launch_bounds__(2 * DV, (sizeof(Tin) == 4 ? 256 : 384) / DV) k
             ask(k_raw, a.k, i);
             ask(g_raw, a.g, i);
         }
-        float scale = 1.f;
-        if (a.qk_eps >= 0.f) {
-            Row<DK> k;
+        Row<DK> k;
 #pragma unroll
-            for (int x = 0; x < DK / 32; ++x) k.x[x] = k_raw[x].get();
-            scale = k.scale(a.qk_eps);
-        }
-        if (l == 0) norm[i] = scale;
+        for (int x = 0; x < DK / 32; ++x) k.x[x] = k_raw[x].get();
+        if (a.qk_eps >= 0.f) k.normalise(a.qk_eps);
 #pragma unroll
         for (int x = 0; x < DK / 32; ++x) {
             const float4 d = g_raw[x].get();
-            keep4(sk + i * DK + chan(x), k_raw[x]);
-            *reinterpret_cast<float4 *>(sa + i * DK + chan(x)) = make_float4(expf(d.x), expf(d.y), expf(d.z), expf(d.w));
+            *reinterpret_cast<float4 *>(sk + i * DK + 32 * x + 4 * l) = k.x[x];
+            *reinterpret_cast<float4 *>(sa + i * DK + 32 * x + 4 * l) = make_float4(expf(d.x), expf(d.y), expf(d.z), expf(d.w));
         }
     }
     __syncthreads();
@@ -235,49 +256,49 @@ __global__ void __launch_bounds__(2 * DV, (sizeof(Tin) == 4 ? 256 : 384) / DV) k
         const bool mine = i0 + grp < m;
         const int i = mine ? i0 + grp : m - 1;
         if (kF32 || i0 > 0 || i != i_first) ask(q_raw, a.q, i);
-        Row<DK> k, q;
-        float4 d[DK / 32];
-        const float own = norm[i];
+        Two k[DK / 32], q[DK / 32], d[DK / 32];
+        {
+            Row<DK> y;
 #pragma unroll
-        for (int x = 0; x < DK / 32; ++x) {
-            q.x[x] = q_raw[x].get();
-            k.x[x] = mul4(read4(sk + i * DK + chan(x)), own);
-            d[x] = make_float4(1.f, 1.f, 1.f, 1.f);
-        }
-        if (a.qk_eps >= 0.f) {
-            const float scale = q.scale(a.qk_eps);
+            for (int x = 0; x < DK / 32; ++x) y.x[x] = q_raw[x].get();
+            if (a.qk_eps >= 0.f) y.normalise(a.qk_eps);
 #pragma unroll
-            for (int x = 0; x < DK / 32; ++x) q.x[x] = mul4(q.x[x], scale);
+            for (int x = 0; x < DK / 32; ++x) {
+                q[x] = Two(y.x[x]);
+                k[x] = Two(sk + i * DK + 32 * x + 4 * l);
+                d[x] = Two(make_float4(1.f, 1.f, 1.f, 1.f));
+            }
         }
-        const float bt = beta[i];
+        const float weight = l & 1 ? 1.f : beta[i];
+        float *to = (l & 1 ? pc : pa) + i * ST;              // odd lanes end up with q's sum, even ones with k's
         int j = mine ? i : -1;
         while (__any_sync(0xffffffffu, j >= 0)) {
             const int jj = j >= 0 ? j : 0;
-            float kk = 0.f, qq = 0.f;
+            const float *kj = sk + jj * DK + 4 * l, *aj = kj + T * DK;
+            uint64_t k2 = 0, q2 = 0;
 #pragma unroll
             for (int x = 0; x < DK / 32; ++x) {
-                const float4 y = mul4(read4(sk + jj * DK + chan(x)), d[x]);
-                kk = dot4(k.x[x], y, kk);
-                qq = dot4(q.x[x], y, qq);
+                const Two y = mul2(Two(kj + 32 * x), d[x]);
+                dot2(k[x], y, k2);
+                dot2(q[x], y, q2);
             }
-            kk = sum8(kk);
-            qq = sum8(qq);
+            const float kk = halves(k2), qq = halves(q2);
+            float sum = (l & 1 ? qq : kk) + __shfl_xor_sync(0xffffffffu, l & 1 ? kk : qq, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
             if (j >= 0) {
-                if (l == 0) {
-                    const float scale = norm[jj];
-                    if (j != i) pa[i * ST + j] = bt * scale * kk;
-                    pc[i * ST + j] = scale * qq;
-                }
+                if (l == 1 || (l == 0 && j != i)) to[j] = weight * sum;
 #pragma unroll
-                for (int x = 0; x < DK / 32; ++x) d[x] = mul4(d[x], read4(sa + jj * DK + chan(x)));
+                for (int x = 0; x < DK / 32; ++x) d[x] = mul2(d[x], Two(aj + 32 * x));
                 j = parent[jj];
             }
         }
         if (mine) {
+            const int swap = 4 * (i & 1);
 #pragma unroll
             for (int x = 0; x < DK / 32; ++x) {
-                *reinterpret_cast<float4 *>(sb + i * S::B + chan(x)) = operand<kF32>(mul4(k.x[x], d[x]));
-                *reinterpret_cast<float4 *>(sb + (q0 + i) * S::B + chan(x)) = operand<kF32>(mul4(q.x[x], d[x]));
+                *reinterpret_cast<float4 *>(sb + i * DK + 4 * ((8 * x + l) ^ swap)) = operand<kF32>(mul2(k[x], d[x]).get());
+                *reinterpret_cast<float4 *>(sb + (q0 + i) * DK + 4 * ((8 * x + l) ^ swap)) = operand<kF32>(mul2(q[x], d[x]).get());
             }
         }
     }
@@ -294,31 +315,37 @@ __global__ void __launch_bounds__(2 * DV, (sizeof(Tin) == 4 ? 256 : 384) / DV) k
     for (int st = 0; st < kAhead; ++st) load_state(st);
 
     // C's rows: along the path, each c_ij that is final is taken out of those above it.  Lane l has j = 8 x + l.
-    for (int i0 = 0; i0 < m; i0 += kGroups) {
-        const bool mine = i0 + grp < m;
-        const int i = mine ? i0 + grp : m - 1;
-        float r[kTreeMax / 8];
+    auto rows_of_c = [&](auto n_regs) {
+        constexpr int R = decltype(n_regs)::value;
+        for (int i0 = 0; i0 < m; i0 += kGroups) {
+            const bool mine = i0 + grp < m;
+            const int i = mine ? i0 + grp : m - 1;
+            float r[R];
 #pragma unroll
-        for (int x = 0; x < kTreeMax / 8; ++x) r[x] = 8 * x <= i ? pc[i * ST + 8 * x + l] : 0.f;
-        int j = mine ? i : -1;
-        while (__any_sync(0xffffffffu, j >= 0)) {
-            const int jj = j >= 0 ? j : 0;
-            float c = r[0];
+            for (int x = 0; x < R; ++x) r[x] = 8 * x <= i ? pc[i * ST + 8 * x + l] : 0.f;
+            int j = mine ? i : -1;
+            while (__any_sync(0xffffffffu, j >= 0)) {
+                const int jj = j >= 0 ? j : 0;
+                const float *aj = pa + jj * ST + l;
+                float c = r[0];
 #pragma unroll
-            for (int x = 1; x < kTreeMax / 8; ++x) c = (jj >> 3) == x ? r[x] : c;
-            c = __shfl_sync(0xffffffffu, c, (lane & 24) | (jj & 7));
-            if (j >= 0) {
+                for (int x = 1; x < R; ++x) c = jj >= 8 * x ? r[x] : c;
+                c = __shfl_sync(0xffffffffu, c, (lane & 24) | (jj & 7));
+                if (j >= 0) {
 #pragma unroll
-                for (int x = 0; x < kTreeMax / 8; ++x)
-                    if (8 * x < jj) r[x] = fmaf(-c, pa[jj * ST + 8 * x + l], r[x]);
-                j = parent[jj];
+                    for (int x = 0; x < R; ++x)
+                        if (8 * x < jj) r[x] = fmaf(-c, aj[8 * x], r[x]);
+                    j = parent[jj];
+                }
             }
-        }
-        if (mine)
+            if (mine)
 #pragma unroll
-            for (int x = 0; x < kTreeMax / 8; ++x)
-                if (8 * x <= i) pc[i * ST + 8 * x + l] = r[x];
-    }
+                for (int x = 0; x < R; ++x)
+                    if (8 * x <= i) pc[i * ST + 8 * x + l] = r[x];
+        }
+    };
+    if (m <= 32) rows_of_c(std::integral_constant<int, 4>());
+    else rows_of_c(std::integral_constant<int, kTreeMax / 8>());
 
     const int m8 = (m + 7) / 8 * 8, tiles = (q0 + m + 15) / 16;
     bool met = false, bad = false;
@@ -339,8 +366,8 @@ __global__ void __launch_bounds__(2 * DV, (sizeof(Tin) == 4 ? 256 : 384) / DV) k
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
                 if (t0 + t >= tiles) break;
-                const float *row = sb + (16 * (t0 + t) + g) * S::B + 16 * st + 4 * t4;
-                const float4 x = *reinterpret_cast<const float4 *>(row), y = *reinterpret_cast<const float4 *>(row + 8 * S::B);
+                const float *row = sb + (16 * (t0 + t) + g) * DK + 4 * ((4 * st + t4) ^ (4 * (g & 1)));
+                const float4 x = *reinterpret_cast<const float4 *>(row), y = *reinterpret_cast<const float4 *>(row + 8 * DK);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {   // two steps of 8 key channels
                     const float f[4] = {p ? x.z : x.x, p ? y.z : y.x, p ? x.w : x.y, p ? y.w : y.y};
@@ -386,9 +413,13 @@ __global__ void __launch_bounds__(2 * DV, (sizeof(Tin) == 4 ? 256 : 384) / DV) k
             for (int j = 0; j < m8 && j < i0 + 16; j += 8) {
                 const float f[4] = {in_a ? pc[ia * ST + j + t4] : 0.f, in_b ? pc[ib * ST + j + t4] : 0.f,
                                     in_a ? pc[ia * ST + j + 4 + t4] : 0.f, in_b ? pc[ib * ST + j + 4 + t4] : 0.f};
-                const float2 x = *reinterpret_cast<const float2 *>(sw + (j + t4) * S::W + c0 + 2 * g);
-                const float2 y = *reinterpret_cast<const float2 *>(sw + (j + 4 + t4) * S::W + c0 + 2 * g);
-                mma_parts(c[t], f, make_float2(tame(x.x) ? x.x : 0.f, tame(x.y) ? x.y : 0.f), make_float2(tame(y.x) ? y.x : 0.f, tame(y.y) ? y.y : 0.f));
+                float2 x = *reinterpret_cast<const float2 *>(sw + (j + t4) * S::W + c0 + 2 * g);
+                float2 y = *reinterpret_cast<const float2 *>(sw + (j + 4 + t4) * S::W + c0 + 2 * g);
+                if (any_bad) {
+                    x = make_float2(tame(x.x) ? x.x : 0.f, tame(x.y) ? x.y : 0.f);
+                    y = make_float2(tame(y.x) ? y.x : 0.f, tame(y.y) ? y.y : 0.f);
+                }
+                mma_parts(c[t], f, x, y);
             }
             if (any_bad) {   // what is not finite reaches the tokens that continue it, and no others
                 auto add = [&](float x, float w, float &to) { to = tame(w) ? to : fmaf(x, w, to); };
@@ -502,9 +533,9 @@ cudaError_t launch(const TreeArgs &a, bool commit, cudaStream_t st) {
         kda_recurrent_tree_commit_kernel<Tin, DK, DV><<<grid, 2 * DV, 0, st>>>(a);
         return cudaGetLastError();
     }
-    const int bytes = Shared<sizeof(Tin), DK, DV>::bytes(a.tokens);
+    const int bytes = Shared<DK, DV>::bytes(a.tokens);
     const cudaError_t e = cudaFuncSetAttribute(kda_recurrent_tree_kernel<Tin, DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Shared<sizeof(Tin), DK, DV>::bytes(kTreeMax));
+                                               Shared<DK, DV>::bytes(kTreeMax));
     if (e != cudaSuccess) return e;
     kda_recurrent_tree_kernel<Tin, DK, DV><<<grid, 2 * DV, bytes, st>>>(a);
     return cudaGetLastError();

@@ -180,10 +180,12 @@ __device__ __forceinline__ float halves(uint64_t c) {
     return x + y;
 }
 
-template <typename Tin, int DK, int DV>
-__global__ void __launch_bounds__(2 * DV, 256 / DV) kda_recurrent_tree_kernel(const TreeArgs a) {
+// Up to 16 tokens have two tiles of products, whose accumulators leave the registers for three CTAs an SM (bf16): 4096
+// heads of 8 tokens take 88 us, and 96 in the form for more, where three CTAs would spill (up to 32 tokens: 154 to 166 us, 145 with two).
+template <typename Tin, int DK, int DV, bool kFew>
+__global__ void __launch_bounds__(2 * DV, (kFew ? 384 : 256) / DV) kda_recurrent_tree_kernel(const TreeArgs a) {
     constexpr bool kF32 = sizeof(Tin) == 4;
-    constexpr int kThreads = 2 * DV, kGroups = kThreads / 8, kSteps = DK / 16, kTiles = 4, kAhead = 4;
+    constexpr int kThreads = 2 * DV, kGroups = kThreads / 8, kSteps = DK / 16, kTiles = kFew ? 2 : 4, kAhead = kFew ? 2 : 4;
     using S = Shared<DK, DV>;
     extern __shared__ __align__(16) uint8_t sm[];
     const int T = a.tokens, ST = S::stride(T);
@@ -533,11 +535,11 @@ cudaError_t launch(const TreeArgs &a, bool commit, cudaStream_t st) {
         kda_recurrent_tree_commit_kernel<Tin, DK, DV><<<grid, 2 * DV, 0, st>>>(a);
         return cudaGetLastError();
     }
-    const int bytes = Shared<DK, DV>::bytes(a.tokens);
-    const cudaError_t e = cudaFuncSetAttribute(kda_recurrent_tree_kernel<Tin, DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Shared<DK, DV>::bytes(kTreeMax));
+    const bool few = sizeof(Tin) == 2 && a.tokens <= 16;
+    const auto kernel = few ? kda_recurrent_tree_kernel<Tin, DK, DV, sizeof(Tin) == 2> : kda_recurrent_tree_kernel<Tin, DK, DV, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shared<DK, DV>::bytes(few ? 16 : kTreeMax));
     if (e != cudaSuccess) return e;
-    kda_recurrent_tree_kernel<Tin, DK, DV><<<grid, 2 * DV, bytes, st>>>(a);
+    kernel<<<grid, 2 * DV, Shared<DK, DV>::bytes(a.tokens), st>>>(a);
     return cudaGetLastError();
 }
 

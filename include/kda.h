@@ -639,7 +639,7 @@ kda_status_t kda_recurrent_tree_commit_qknorm(const void *k, const void *v, cons
  * to.  Positions past the table's width, on pages outside the pool, or with a score of -infinity weigh nothing.
  * What the cache holds at places a token does not attend to (other branches of the draft, tokens
  * past the count) never reaches its results, NaN and infinities included.
- * bf16: K and V enter the tensor cores as they are, the weights as a rounded bf16 and the rounded
+ * bf16: K and V enter the tensor cores as they are, the weights as two bf16 terms, a leading one and the rounded
  * rest (16 bits); sums are fp32.
  *   tokens    : in [1, KDA_TREE_TOKENS];  pages * page_size * kv_heads at most 2^31 - 1, else KDA_ERR_SHAPE
  *   workspace : kda_paged_tree_attention_workspace_bytes(tokens, dims) bytes, 16-byte aligned (NULL when that is

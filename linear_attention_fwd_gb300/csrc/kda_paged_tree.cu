@@ -8,6 +8,8 @@ namespace {
 // 256 threads take a block of 64 query rows and tiles of 32 keys in fp32 arithmetic: a thread has 4 rows x 2 keys of
 // the scores and 4 rows x D / 16 channels of the outputs, both from shared memory in 16-byte reads; a row's maximum, sum
 // and weights stay within the half warp that has the row.  The next tile is on its way in registers meanwhile.
+// The accurate mode, bound by fp32 arithmetic and shared memory: 131,071 tokens x 8 heads, 512 query rows a head:
+// 7.95 ms, 35 TFLOP/s; 32 rows of 200 to 16,384 tokens, 8 heads, up to 128 query rows each: 1.48 ms.
 constexpr int kThreads = 256, kRb = 64, kKt = 32, kStart = 1;
 constexpr int kSimtCtas = 2 * kSms;
 

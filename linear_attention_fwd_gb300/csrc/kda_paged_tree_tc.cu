@@ -14,15 +14,20 @@
 //
 // Tiles on pages of a multiple of 8 tokens come by TMA, a box of tokens an instruction, and so do the queries where a
 // power of two of heads shares a key/value head; others, and the drafted tokens, by cp.async of two warps.
-// Scores of places without a token are masked, their values made zero behind the load.  (Gathers of four rows by TMA take 50 ns each, 6.5 us for 128 keys of 128
-// channels: 131,071 tokens x 8 heads, 512 query rows: 700 us, 430 by boxes.)  The drafted tokens have a tile of their own,
-// masked by their paths.  A non-finite value among them is replaced by zero before the product (zero
+// Scores of places without a token are masked, their values made zero behind the load.  (Gathers of four rows by TMA
+// take 50 ns each, 6.5 us for 128 keys of 128 channels: 131,071 tokens x 8 heads, 512 query rows: 700 us, 430 by boxes at
+// the time.)  The drafted tokens have a tile of their own, masked by their paths.  A non-finite value among them is replaced by zero before the product (zero
 // times NaN would reach other branches) and put back as NaN in the outputs of the tokens that weigh it.
 //
 // Roles: warps 0-7 and 8-15 the chains' softmax, half of a tile's keys each four (a row's two threads agree on m; with
 // one thread per row a chain's softmax took 2600 cycles a tile, mostly waits of its one warp per scheduler for its own
 // results, twice the products' time); warps 16 and 17 the chains' products, 18 and 19 the loads.  They meet at mbarriers
 // with bounded waits.
+//
+// Bound by the chains' hand-overs: 64 keys of 256 query rows take 2440 cycles, the products 1536 of them (the rests are a
+// third), tensor pipe 63 % busy, instruction issue 61 %.  131,071 tokens x 8 heads, 512 query rows a head: 301 us, 0.91 PFLOP/s
+// without the rests, 1.37 with them.  32 rows of 200 to 16,384 tokens, 8 heads, 32 to 128 query rows each: 159 us, 3.2 TB/s of
+// keys and values (a tile of 32 rows costs what one of 128 does).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -13,7 +13,8 @@ namespace {
 // ------------------------------------------------------------------ the accepted path
 // One CTA per row.  A path's tokens ascend (a token continues an earlier one), so its r-th token a_r >= r goes to
 // place r, which is no later token's old place: a thread that moves its 16 bytes of all tokens in order, some at a
-// time, reads each before it is written.  Bound by the chain of reads ahead of the data (path, pages).
+// time, reads each before it is written.  Bound by the chain of reads ahead of the data (path, pages): 3.5 us for 256 rows of up
+// to 32 drafted tokens, 8 heads of 128, bf16; 2.9 for one row.
 constexpr int kCommitThreads = 256, kCommitAhead = 4;
 
 __global__ void __launch_bounds__(kCommitThreads) kda_paged_tree_commit_kernel(const TreeCommitArgs a, const FastDiv by_page) {
@@ -69,7 +70,9 @@ __global__ void __launch_bounds__(kCommitThreads) kda_paged_tree_commit_kernel(c
 // One cluster of CTAs does a call: its CTAs split the pages and the rows between them, meet at cluster barriers, and exchange
 // their bitmaps of free pages with prefix sums over blocks and words through distributed shared memory, so that a
 // call is one launch without a workspace.  Bound by its chains of dependent reads (row, length, page, count) and by the
-// barriers: what a row needs is gathered by a thread each before warps go over its entries.
+// barriers: what a row needs is gathered by a thread each before warps go over its entries.  Fork of 8 rows of 44 pages and
+// the copies of their last pages: 9.0 us; of 256 rows of 100 to 8000 tokens on pages of 16: 20.5 us (16 and 45 where each warp
+// fetched what its rows need by itself).
 constexpr int kPoolThreads = 1024, kPoolWarps = kPoolThreads / 32, kBlock = 1024;   // pages of a block: 32 words of the bitmap
 constexpr int kMaxCtas = 16, kLocalPages = 1 << 18, kLocalRows = 8192, kBatch = 1024;
 
@@ -511,7 +514,7 @@ __global__ void __launch_bounds__(kPoolThreads) kda_paged_compact_kernel(const F
 
 // ------------------------------------------------------------------ copies
 // Works of 16 KB of a page, a page's keys and then its values, over CTAs that stay: each thread moves four 16-byte
-// vectors at a time.
+// vectors at a time.  Bound by DRAM: 6,570 pages of 32 KB of keys and as much of values: 140 us, 6.1 TB/s of reads and writes.
 constexpr int kCopyThreads = 256, kCopyAhead = 4, kCopyVecs = kCopyThreads * kCopyAhead;
 
 __global__ void __launch_bounds__(kCopyThreads) kda_paged_copy_kernel(uint4 *kc, uint4 *vc, const int32_t *copies, const int64_t works,

@@ -15,9 +15,15 @@
 //  2. eight lanes walk a token's path to its root with the running product of the decays: every factor is
 //     at most 1, no exponent of a sum is taken, and lines of 64 tokens need no bound on g.  They leave A, B, E k and E q;
 //  3. the same eight lanes walk the path again for the token's row of C;
-//  4. (E k; E q) S, S straight into B fragments (each warp the 16 value channels that it keeps to the end), and C W on tensor cores (mma.sync, tf32; all of C W, and of fp32 calls, in three products of parts
-//     of 11 bits), the second added to the first in place.  A W that is not finite is left out of that and added along the paths.
-// Bound by reading the state: 64 KB per row and head at 128 x 128.
+//  4. (E k; E q) S and C W on tensor cores (mma.sync, tf32), the second added to the first in place, each warp the 16
+//     value channels of which it reads the state straight into B fragments.  bf16 calls round E k, E q and S to 11 bits
+//     (2^-11 relative, an eighth of the outputs' own rounding); C W, and everything in fp32 calls, is three products
+//     of parts of 11 bits.  A W that is not finite is left out of the product and added along the paths.
+// 64 rows of 8 to 32 tokens, 64 heads of 128 x 128, bf16: 145 us, 361 MB, 2.5 TB/s.  Not DRAM but a CTA's chain of short phases bounds
+// it: two CTAs an SM (three do not fit the registers, see below) issue in 45 % of the cycles, and the L1 data path, which the
+// state's sectors and the walks' and tiles' shared-memory reads cross, is busy in 63 %.  Solving for u, channel by
+// channel, and holding the state in registers from the start took 180 us.  tcgen05 would have to
+// round the state on its way (its tf32 truncates) through 64 KB more of shared memory.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
@@ -443,7 +449,8 @@ __global__ void __launch_bounds__(2 * DV, (kFew ? 384 : 256) / DV) kda_recurrent
 // Commit.  The path's tokens in order, each as in the decode step: vhat = (Diag(e^g) S)^T k, e = v - vhat,
 // S <- Diag(e^g) S + beta k e^T.  A warp keeps all key channels of 16 value channels in registers (a lane every eighth
 // key channel of four value channels), so that nothing between tokens is wider than a warp.  Bound by
-// reading and writing the state once.
+// reading and writing the state once: 256 rows of 1 to 16 accepted tokens, 64 heads, bf16: 368 us, 2.0 GB, 5.4 TB/s; with three CTAs an
+// SM it spills (461 us).
 constexpr int kStaged = 8;   // tokens whose vectors are staged at once
 
 template <typename Tin, int DK, int DV>

@@ -13,7 +13,7 @@
 // tiles: then the chain's warpgroup waits for the last product into O and scales it in tensor memory.
 //
 // Tiles on pages of a multiple of 8 tokens come by TMA, a box of tokens an instruction, and so do the queries where a
-// power of two of heads shares a key/value head; others, and the drafted tokens, by cp.async of two warps.
+// power of two of heads shares a key/value head; others, and most drafts, by cp.async.
 // Scores of places without a token are masked, their values made zero behind the load.  (Gathers of four rows by TMA
 // take 50 ns each, 6.5 us for 128 keys of 128 channels: 131,071 tokens x 8 heads, 512 query rows: 700 us, 430 by boxes at
 // the time.)  The drafted tokens have a tile of their own, masked by their paths.  A non-finite value among them is replaced by zero before the product (zero
@@ -21,7 +21,7 @@
 //
 // Roles: warps 0-7 and 8-15 the chains' softmax, half of a tile's keys each four (a row's two threads agree on m; with
 // one thread per row a chain's softmax took 2600 cycles a tile, mostly waits of its one warp per scheduler for its own
-// results, twice the products' time); warps 16 and 17 the chains' products, 18 and 19 the loads.  They meet at mbarriers
+// results, twice the products' time); warps 16 and 17 the chains' products, 18 the keys' loads, 19 the values' and queries'.  They meet at mbarriers
 // with bounded waits.
 //
 // Bound by the chains' hand-overs: 64 keys of 256 query rows take 2440 cycles, the products 1536 of them (the rests are a
@@ -45,7 +45,6 @@ using namespace ptx;
 
 constexpr int kThreads = 640, kRb = 256, kKt = 64, kStart = 5;
 constexpr float kSlack = 8.f;   // growth of the maximum, in powers of two, that m does not follow
-constexpr int kLoaders = 2;     // warps
 
 template <int D> struct Tc {
     static constexpr uint32_t TILE = kKt * D * 2, QTILE = 128 * D * 2;   // keys or values; query rows of a chain
@@ -196,10 +195,10 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
         s_fail = 0;
         nf_any[0] = nf_any[1] = 0;
         for (int s = 0; s < 16; ++s) {             // (also those past the stages: what gives up looks at all of them)
-            mbar_init(bar(kFull + s), kLoaders);
+            mbar_init(bar(kFull + s), 1);
             mbar_init(bar(kEmpty + s), 2);         // both chains
         }
-        mbar_init(bar(kQFull), kLoaders);
+        mbar_init(bar(kQFull), 1);
         mbar_init(bar(kQEmpty), 2);                // both chains
         for (int x = 0; x < 4; ++x) {
             mbar_init(bar(kS + x), 2);             // the product, and the thread that issued it (which has seen the tile's masks)
@@ -470,11 +469,12 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
             if (!w.next(a)) break;
         }
     } else if (warp >= 18) {
-        // ---- loads: the two warps take the same steps; the first alone issues TMA
-        const int wi = warp - 18;
+        // ---- loads: one warp the keys, one the queries and the values (a load costs a warp 900 cycles, mostly waits for its own
+        // results; where one warp had both, it was what bound the kernel)
+        const bool keys = warp == 18;
         constexpr int CH = D / 8, RPI = 32 / CH;            // 16-byte chunks of a row, rows of a warp's instruction
         const __nv_bfloat16 *kc = static_cast<const __nv_bfloat16 *>(p.k_cache), *vc = static_cast<const __nv_bfloat16 *>(p.v_cache);
-        uint32_t load = 0, pieces = 0, tiles = 0;
+        uint32_t loads = 0, pieces = 0, tiles = 0;
         // Loads by cp.async that have not been reported yet (barriers, eight bits each, the oldest lowest): they are once
         // they have landed, before this warp waits for anything, and when there are four of them.
         uint32_t queue = 0;
@@ -542,7 +542,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                     const int t = w.row.len - shift + lane * box;           // the boxes of the drafted tokens
                     if (lane < boxes && t < w.row.len + w.row.m) pre.x = (int)tree_place(a, table, t);
                 }
-                const int2 parents = wi == 1 && has_draft ? tree_parents(a, w.n, w.row.m) : make_int2(-1, -1);
+                const int2 parents = keys && has_draft ? tree_parents(a, w.n, w.row.m) : make_int2(-1, -1);
                 auto place = [&](int i) {                                   // asked for in order
                     Place x;
                     if (by_box(i)) {
@@ -570,25 +570,24 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                     if (!box) pre = tokens(i + 1);
                     return x;
                 };
-                auto tile = [&](const CUtensorMap *map, const __nv_bfloat16 *cache, const Place &x, int i) {
-                    const int s = load % S, full = kFull + s;
+                const CUtensorMap *map = keys ? &tmk : &tmv;
+                const __nv_bfloat16 *cache = keys ? kc : vc;
+                auto tile = [&](const Place &x, int i) {
+                    const uint32_t load = loads + (keys ? w.k_load(i) : w.v_load(i)), s = load % S;
+                    const int full = kFull + (int)s;
                     if (load >= S && !reach(kEmpty + s, load / S - 1)) return false;
                     const uint32_t to = sb + L::RING + s * L::TILE;
                     if (by_box(i)) {
                         // (of the places without a token, scores are masked and values made zero behind the load)
                         const uint32_t have = __ballot_sync(0xffffffffu, x.at[0] >= 0);
-                        if (wi == 0) {
-                            if (lane == 0) mbar_arrive_expect_tx(bar(full), __popc(have) * box * D * 2);
-                            __syncwarp();
-                            if (x.at[0] >= 0)
+                        if (lane == 0) mbar_arrive_expect_tx(bar(full), __popc(have) * box * D * 2);
+                        __syncwarp();
+                        if (x.at[0] >= 0)
 #pragma unroll
-                                for (int h = 0; h < HALVES; ++h) tma_load_3d(to + h * HALF + lane * box * 128, map, bar(full), 64 * h, w.hk, x.at[0]);
-                        } else if (lane == 0) {
-                            mbar_arrive(bar(full));
-                        }
+                            for (int h = 0; h < HALVES; ++h) tma_load_3d(to + h * HALF + lane * box * 128, map, bar(full), 64 * h, w.hk, x.at[0]);
                     } else {
                         const int c = lane % CH;
-                        for (int y = wi; y < kKt / RPI; y += kLoaders) {
+                        for (int y = 0; y < kKt / RPI; ++y) {
                             const int r = y * RPI + lane / CH;
                             const int a0 = __shfl_sync(0xffffffffu, x.at[0], r & 31), a1 = __shfl_sync(0xffffffffu, x.at[1], r & 31), at = r < 32 ? a0 : a1;
                             cp16(to + (c >> 3) * HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4), cache + ((int64_t)(at < 0 ? 0 : at) * p.kv_heads + w.hk) * D + 8 * c,
@@ -596,34 +595,21 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                         }
                         sent(full);
                     }
-                    ++load;
                     return true;
                 };
-                auto keys = [&](int i, const Place &x) {
-                    if (wi == 1 && w.ta + i == w.row.ctx)   // the drafted tokens' paths
-                        tree_masks(parents, w.row.m, reinterpret_cast<uint64_t *>(sm + L::ANC) + 64 * (pieces & 1), reinterpret_cast<int *>(sm + L::UP));
-                    if (wi == 0 && lane == 0) *reinterpret_cast<uint2 *>(sm + L::MASK + 8 * ((tiles + i) & 31)) = x.mask;
-                    __syncwarp();
-                    return tile(&tmk, kc, x, i);
-                };
-                const int ahead = w.ahead();
-                // the queries
-                if (pieces > 0 && !reach(kQEmpty, pieces - 1)) break;
-                if (qbox) {
-                    if (wi == 0) {
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(bar(kQFull), (w.two ? 2 : 1) * L::QTILE);
-                            const int at = w.n * a.t.tokens + (int)a.by_rep((uint32_t)w.r0);
-                            for (int e = 0; e < (w.two ? 2 : 1); ++e)
+                if (pieces > 0 && !reach(kQEmpty, pieces - 1)) break;   // (the queries, and the paths before the last, are read)
+                if (keys) {
+                } else if (qbox) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar(kQFull), (w.two ? 2 : 1) * L::QTILE);
+                        const int at = w.n * a.t.tokens + (int)a.by_rep((uint32_t)w.r0);
+                        for (int e = 0; e < (w.two ? 2 : 1); ++e)
 #pragma unroll
-                                for (int h = 0; h < HALVES; ++h) tma_load_3d(sb + L::Q + e * L::QTILE + h * QHALF, &tmq, bar(kQFull), 64 * h, w.hk * a.rep, at + e * qbox);
-                        }
-                    } else if (lane == 0) {
-                        mbar_arrive(bar(kQFull));
+                            for (int h = 0; h < HALVES; ++h) tma_load_3d(sb + L::Q + e * L::QTILE + h * QHALF, &tmq, bar(kQFull), 64 * h, w.hk * a.rep, at + e * qbox);
                     }
                     __syncwarp();
                 } else {
-                    for (int y = wi; y < (w.two ? 256 : 128) / RPI; y += kLoaders) {
+                    for (int y = 0; y < (w.two ? 256 : 128) / RPI; ++y) {
                         const int r = y * RPI + lane / CH, c = lane % CH, i = (int)a.by_rep((uint32_t)(w.r0 + r));
                         const bool in = r < w.rows;
                         const int64_t at = in ? ((int64_t)w.n * a.t.tokens + i) * p.heads + w.hk * a.rep + (w.r0 + r - i * a.rep) : 0;
@@ -632,30 +618,19 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                     }
                     sent(kQFull);
                 }
-                // keys `ahead` tiles ahead of the values; a tile's places are kept until its values are loaded
-                Place x[5];
                 bool fine = true;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < ahead && i < w.c && fine) {
-                        x[i] = place(i);
-                        fine = keys(i, x[i]);
-                    }
                 for (int i = 0; i < w.c && fine; ++i) {
-                    const bool more = i + ahead < w.c;
-                    if (more) x[4] = place(i + ahead);
-                    fine = tile(&tmv, vc, x[0], i) && (!more || keys(i + ahead, x[4]));
-                    if (ahead == 2) {
-                        x[0] = x[1];
-                        x[1] = x[4];
-                    } else {
-                        x[0] = x[1];
-                        x[1] = x[2];
-                        x[2] = x[3];
-                        x[3] = x[4];
+                    const Place x = place(i);
+                    if (keys) {
+                        if (w.ta + i == w.row.ctx)   // the drafted tokens' paths
+                            tree_masks(parents, w.row.m, reinterpret_cast<uint64_t *>(sm + L::ANC) + 64 * (pieces & 1), reinterpret_cast<int *>(sm + L::UP));
+                        if (lane == 0) *reinterpret_cast<uint2 *>(sm + L::MASK + 8 * ((tiles + i) & 31)) = x.mask;
+                        __syncwarp();
                     }
+                    fine = tile(x, i);
                 }
                 if (!fine) break;
+                loads += 2 * w.c;
                 tiles += w.c;
                 ++pieces;
             }

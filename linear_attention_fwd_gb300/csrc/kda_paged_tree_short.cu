@@ -152,21 +152,19 @@ __global__ void __launch_bounds__(kThreads) kda_paged_tree_short_kernel(const Tr
                 if (j < 0 || j >= m) continue;
                 uint4 *at = reinterpret_cast<uint4 *>(ring + st * R::STAGE + (kGroup + r) * R::RB + ((ch ^ (r & 7)) << 4));
                 uint4 v = *at;
+                auto ones = [](uint32_t z) { return (z & 0x7f807f80u) + 0x00800080u; };   // bits 15, 31: an exponent of all ones
+                if (!((ones(v.x) | ones(v.y) | ones(v.z) | ones(v.w)) & 0x80008000u)) continue;
                 uint32_t *w = &v.x;
-                bool bad = false;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         if (((w[e] >> (16 * h)) & 0x7f80u) == 0x7f80u) {
-                            bad = true;
                             w[e] &= h ? 0x0000ffffu : 0xffff0000u;
                             atomicOr(nf + 8 * ch + 2 * e + h, 1ull << j);
                         }
-                if (bad) {
-                    *at = v;
-                    s_sick = 1;
-                }
+                *at = v;
+                s_sick = 1;
             }
         __syncwarp();
         float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};

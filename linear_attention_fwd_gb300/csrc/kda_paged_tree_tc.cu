@@ -351,24 +351,29 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                     const int vl = (int)loads + w.v_load(i), st = vl % S;
                     ok = ok && all(wait(kFull + st, vl / S));
                     if (ok)
-                        for (int x = 128 * half + th; x < kKt * (D / 8); x += 256) {
-                            const int key = x / (D / 8), ch = x % (D / 8);
+#pragma unroll
+                        for (int x0 = 0; x0 < kKt * (D / 8); x0 += 256) {
+                            const int x = x0 + 128 * half + th, key = x / (D / 8), ch = x % (D / 8);
                             uint4 *at = reinterpret_cast<uint4 *>(sm + L::RING + st * L::TILE + (ch >> 3) * HALF + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
                             const bool token = ((key < 32 ? here.x : here.y) >> (key & 31)) & 1u;
                             uint4 y = token && draft ? *at : make_uint4(0u, 0u, 0u, 0u);
-                            uint32_t *q = &y.x;
-                            bool bad = !token;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                                for (int g = 0; g < 2; ++g)
-                                    if (((q[e] >> (16 * g)) & 0x7f80u) == 0x7f80u) {
-                                        bad = true;
-                                        q[e] &= g ? 0x0000ffffu : 0xffff0000u;
-                                        atomicOr(nf + (pieces & 1) * D + 8 * ch + 2 * e + g, 1ull << key);
-                                        nf_any[pieces & 1] = 1;
-                                    }
-                            if (bad) *at = y;
+                            auto ones = [](uint32_t z) { return (z & 0x7f807f80u) + 0x00800080u; };   // bits 15, 31: an exponent of all ones
+                            const uint32_t full = ones(y.x) | ones(y.y) | ones(y.z) | ones(y.w);
+                            if (full & 0x80008000u) {
+#pragma unroll 1
+                                for (int e = 0; e < 8; ++e) {
+                                    uint32_t z = e < 4 ? (e < 2 ? y.x : y.y) : (e < 6 ? y.z : y.w);
+                                    if (((z >> (16 * (e & 1))) & 0x7f80u) != 0x7f80u) continue;
+                                    z &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+                                    if (e < 2) y.x = z;
+                                    else if (e < 4) y.y = z;
+                                    else if (e < 6) y.z = z;
+                                    else y.w = z;
+                                    atomicOr(nf + (pieces & 1) * D + 8 * ch + e, 1ull << key);
+                                    nf_any[pieces & 1] = 1;
+                                }
+                            }
+                            if (!token || (full & 0x80008000u)) *at = y;
                         }
                     fence_async_smem();
                 }

@@ -12,6 +12,7 @@ namespace {
 // 7.95 ms, 35 TFLOP/s; 32 rows of 200 to 16,384 tokens, 8 heads, up to 128 query rows each: 1.48 ms.
 constexpr int kThreads = 256, kRb = 64, kKt = 32, kStart = 1;
 constexpr int kSimtCtas = 2 * kSms;
+static_assert(kRb == 1 << 6 && kKt == 1 << 5 && kSimtCtas <= 1 << 10, "their logarithms; see tree_cut");
 
 template <int D> struct Simt {
     static constexpr int QS = D + 4, KS = D + 4, PS = kKt + 4;   // row strides in floats
@@ -38,17 +39,13 @@ __global__ void __launch_bounds__(kThreads, 2) kda_paged_tree_attention_kernel(c
 
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const PagedArgs &p = a.t.p;
-    tree_clear<float, D, kThreads>(a, gridDim.x);
+    if (gridDim.x == 1) tree_clear<float, D, kThreads>(a, 0, 1);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long W = tree_total<kThreads>(a, sm_sum);
-    const long long G = W < gridDim.x ? W : gridDim.x;
-    if (blockIdx.x >= G) return;
-    long long x = blockIdx.x * W / G, us;
-    const long long x1 = (blockIdx.x + 1) * W / G;
+    long long W, G, x, x1, us;
     int n;
-    tree_find<kThreads>(a, x, sm_sum, n, us);
+    if (!tree_share<kThreads>(a, sm_sum, W, G, x, x1, n, us)) return;
     TreeRow row = tree_row(a, n);
-    int unit = (int)((x - us) / row.items);
+    int unit = tree_quotient(x - us, row.items);
     us += unit * row.items;
 
     const float sc = p.scale * kLog2e;
@@ -79,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_paged_tree_attention_kernel(c
             if (tid < kKt && t < tb) {
                 const bool draft = t >= row.ctx;
                 const int j = (draft ? t - row.ctx : t) * kKt + tid;
-                place[t % 3][tid] = j < (draft ? row.m : row.len) ? tree_place(a, table, draft ? row.len + j : j) : -1;
+                place[t % 3][tid] = j < (draft ? row.m : row.len) ? tree_place(a, tree_page(a, table, draft ? row.len + j : j), draft ? row.len + j : j) : -1;
             }
         };
         float4 kr[LD], vr[LD];
@@ -224,6 +221,7 @@ template <typename T, int D, bool kByUnit>
 __global__ void __launch_bounds__(kJoinThreads) kda_paged_tree_join_kernel(const TreeAtt a, const int ctas) {
     __shared__ long long sm_sum[kJoinThreads / 32];
     const PagedArgs &p = a.t.p;
+    tree_clear<T, D, kJoinThreads>(a, blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
     int n = 0, b0 = blockIdx.x, b1 = b0, hk = 0, r0 = 0, rows = 0;
     long long us = 0, W, G;
     if (kByUnit) {
@@ -245,7 +243,7 @@ __global__ void __launch_bounds__(kJoinThreads) kda_paged_tree_join_kernel(const
             hk = u / row.blocks;
             r0 = (u - hk * row.blocks) * a.rb;
             rows = row.m * a.rep - r0 < a.rb ? row.m * a.rep - r0 : a.rb;
-            b0 = (int)(((us + 1) * G - 1) / W);
+            b0 = (int)(((us + 1) * G - 1) / W);   // (the shares that hold the unit's first item and its last)
             b1 = (int)(((us + row.items) * G - 1) / W);
         }
     } else {
@@ -355,7 +353,7 @@ cudaError_t launch_paged_tree(const PagedTreeArgs &t, int d, kda_dtype_t dt, voi
     if (dt == KDA_BF16) return launch_tree_tc(t, d, workspace, polls, st);
     const int rep = t.p.heads / t.p.kv_heads, ctas = simt_ctas(t);
     float *ws = static_cast<float *>(workspace);
-    const TreeAtt a{t, FastDiv((uint32_t)t.p.page_size), FastDiv((uint32_t)rep), rep, kRb, kKt, kStart, ws, ws + (size_t)ctas * 2 * kRb * d};
+    const TreeAtt a{t, FastDiv((uint32_t)t.p.page_size), FastDiv((uint32_t)rep), rep, kRb, kKt, 6, 5, kStart, ws, ws + (size_t)ctas * 2 * kRb * d};
     return d == 128 ? launch_simt<128>(a, ctas, st) : launch_simt<64>(a, ctas, st);
 }
 

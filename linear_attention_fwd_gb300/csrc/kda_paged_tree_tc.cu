@@ -44,6 +44,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kThreads = 640, kRb = 256, kKt = 64, kStart = 5;
+static_assert(kRb == 1 << 8 && kKt == 1 << 6, "their logarithms");
 constexpr float kSlack = 8.f;   // growth of the maximum, in powers of two, that m does not follow
 
 template <int D> struct Tc {
@@ -172,17 +173,18 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const PagedArgs &p = a.t.p;
 
-    tree_clear<__nv_bfloat16, D, kThreads>(a, gridDim.x);
+    if (tid == 0) {
+        prefetch_tmap(&tmq);
+        prefetch_tmap(&tmk);
+        prefetch_tmap(&tmv);
+    }
+    if (gridDim.x == 1) tree_clear<__nv_bfloat16, D, kThreads>(a, 0, 1);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long W = tree_total<kThreads>(a, sm_sum);
-    const long long G = W < gridDim.x ? W : gridDim.x;
-    if (blockIdx.x >= G) return;
+    long long W, G;
     Walk w;
-    w.x = blockIdx.x * W / G;
-    w.x1 = (blockIdx.x + 1) * W / G;
-    tree_find<kThreads>(a, w.x, sm_sum, w.n, w.us);
+    if (!tree_share<kThreads>(a, sm_sum, W, G, w.x, w.x1, w.n, w.us)) return;
     w.row = tree_row(a, w.n);
-    w.unit = (int)((w.x - w.us) / w.row.items);
+    w.unit = tree_quotient(w.x - w.us, w.row.items);
     w.us += w.unit * w.row.items;
     w.piece(a);
 
@@ -351,7 +353,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                     const int vl = (int)loads + w.v_load(i), st = vl % S;
                     ok = ok && all(wait(kFull + st, vl / S));
                     if (ok)
-#pragma unroll
+#pragma unroll 1
                         for (int x0 = 0; x0 < kKt * (D / 8); x0 += 256) {
                             const int x = x0 + 128 * half + th, key = x / (D / 8), ch = x % (D / 8);
                             uint4 *at = reinterpret_cast<uint4 *>(sm + L::RING + st * L::TILE + (ch >> 3) * HALF + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
@@ -531,21 +533,18 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                     const int t = w.ta + i;
                     const bool draft = t == w.row.ctx;
                     const int base = draft ? w.row.len : t * kKt, left = i < w.c ? (draft ? w.row.m : w.row.len - base) : 0;
-                    int2 x;
-                    x.x = lane < left ? (int)tree_place(a, table, base + lane) : -1;
-                    x.y = lane + 32 < left ? (int)tree_place(a, table, base + lane + 32) : -1;
-                    return x;
+                    return make_int2(lane < left ? tree_page(a, table, base + lane) : -1, lane + 32 < left ? tree_page(a, table, base + lane + 32) : -1);
                 };
                 int group = -1, page = box ? group_page(0) : -1;            // places of the current four tiles; pages of the next
                 const bool has_draft = w.ta + w.c > w.row.ctx;
-                int2 pre = make_int2(-1, -1);
+                int2 pre = make_int2(-1, -1);                               // pages that are asked for ahead
                 if (!box) {
                     pre = tokens(0);
                 } else if (has_draft && shift < 0) {
                     pre = tokens(w.c - 1);
                 } else if (has_draft) {
                     const int t = w.row.len - shift + lane * box;           // the boxes of the drafted tokens
-                    if (lane < boxes && t < w.row.len + w.row.m) pre.x = (int)tree_place(a, table, t);
+                    if (lane < boxes && t < w.row.len + w.row.m) pre.x = tree_page(a, table, t);
                 }
                 const int2 parents = keys && has_draft ? tree_parents(a, w.n, w.row.m) : make_int2(-1, -1);
                 auto place = [&](int i) {                                   // asked for in order
@@ -558,7 +557,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                             page = group_page((i >> 2) + 1);
                         }
                         const int at = __shfl_sync(0xffffffffu, group, (i & 3) * 8 + (lane & 7));
-                        x.at[0] = lane >= boxes ? -1 : draft ? pre.x : at;
+                        x.at[0] = lane >= boxes ? -1 : draft ? (int)tree_place(a, pre.x, w.row.len - shift + lane * box) : at;
                         x.at[1] = -1;
                         const uint32_t have = __ballot_sync(0xffffffffu, x.at[0] >= 0);
                         const int from = draft ? shift : 0, left = draft ? shift + w.row.m : w.row.len - (w.ta + i) * kKt;
@@ -570,8 +569,9 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
                         }
                         return x;
                     }
-                    x.at[0] = pre.x, x.at[1] = pre.y;
-                    x.mask = make_uint2(__ballot_sync(0xffffffffu, pre.x >= 0), __ballot_sync(0xffffffffu, pre.y >= 0));
+                    const int base = (w.ta + i == w.row.ctx ? w.row.len : (w.ta + i) * kKt) + lane;
+                    x.at[0] = (int)tree_place(a, pre.x, base), x.at[1] = (int)tree_place(a, pre.y, base + 32);
+                    x.mask = make_uint2(__ballot_sync(0xffffffffu, x.at[0] >= 0), __ballot_sync(0xffffffffu, x.at[1] >= 0));
                     if (!box) pre = tokens(i + 1);
                     return x;
                 };
@@ -746,7 +746,7 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
             atomicAdd(&g_kda_tree_timeouts, 1u);
         }
         const float nan = __int_as_float(0x7fc00000);
-        w.x = blockIdx.x * W / G;                          // from the start of the share
+        w.x = tree_cut(blockIdx.x, W, G);                  // from the start of the share
         tree_find<kThreads>(a, w.x, sm_sum, w.n, w.us);
         w.row = tree_row(a, w.n);
         w.unit = (int)((w.x - w.us) / w.row.items);
@@ -835,7 +835,7 @@ size_t tree_tc_workspace_bytes(const PagedTreeArgs &t, int d) { return tree_shor
 cudaError_t launch_tree_tc(const PagedTreeArgs &t, int d, void *workspace, uint32_t polls, cudaStream_t st) {
     const int rep = t.p.heads / t.p.kv_heads, ctas = tc_ctas(t);
     float *ws = static_cast<float *>(workspace);
-    const TreeAtt a{t, FastDiv((uint32_t)t.p.page_size), FastDiv((uint32_t)rep), rep, kRb, kKt, kStart, ws, ws + (size_t)ctas * 2 * kRb * d};
+    const TreeAtt a{t, FastDiv((uint32_t)t.p.page_size), FastDiv((uint32_t)rep), rep, kRb, kKt, 8, 6, kStart, ws, ws + (size_t)ctas * 2 * kRb * d};
     if (const int c = tree_short_cluster(t, d)) return launch_tree_short(a, d, c, st);
     return d == 128 ? launch_tc<128>(a, ctas, polls, st) : launch_tc<64>(a, ctas, polls, st);
 }

@@ -131,6 +131,33 @@ def test_many_rows(K, dt):
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
+def test_more_rows_than_a_cta_has_threads(K, dt):
+    lens = [(i * i * 7919) % 40 for i in range(700)]
+    num = [(i * 31) % 4 for i in range(700)]
+    c = cache(23, lens, 3, 2, 1, 64, 16, dt)
+    rows, parents = R.drafts(23, 700, 3, num=num)
+    run(K, c, rows, parents, torch.tensor(num, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_many_tiles(K, dt):
+    """More than 2^20 tiles: rows that share all their pages give what one of them gives alone.  Both sides round values that agree
+    to 2^-14 of sum p |v| <= max |v| (weights of 16 bits, parts joined in another order) to the type."""
+    tile = 64 if dt == BF16 else 32
+    N, width = 2048, 512 * tile // 64
+    c = cache(24, [64 * width - 7], 1, 1, 1, 64, 64, dt)
+    rows = torch.tensor([[-1]], dtype=torch.int32, device="cuda")
+    args = lambda n: (c["q"].expand(n, 1, 1, 64).contiguous(), c["k_cache"], c["v_cache"],  # noqa: E731
+                      c["block_table"].expand(n, -1).contiguous(), c["seq_lens"].expand(n).contiguous(), rows.expand(n, 1).contiguous(), c["scale"])
+    one, lse1 = K.kda_paged_tree_attention(*args(1))
+    assert N * (c["seq_lens"].item() // tile + 1) >= 1 << 20
+    out, lse = K.kda_paged_tree_attention(*args(N))
+    step = torch.finfo(dt).eps * one.float().abs()
+    assert bool(((out.float() - one.float()).abs() <= step + 2 ** -14 * c["v_cache"].abs().max().float()).all())
+    assert bool(((lse - lse1).abs() <= 1e-4).all())
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_places_that_a_token_does_not_see(K, dt, bad):
     """Other branches, tokens past the count, and whatever lies behind: nothing of them reaches a token's results."""

@@ -7,7 +7,7 @@
 // page numbers fetched a group ahead), with the 16 query rows as the rows of mma.sync's tile; the weights enter the
 // second product as a rounded bf16 and the rounded rest, as in kda_paged_attention.
 // Bound by latency: a launch, the chain length - page - keys - scores - join.  One row of 777 tokens, 8 drafted, 8 heads of 4
-// queries: 10.8 us, 17.8 in the other form.  Blocks of a head read the same keys anew, which counts against it where
+// queries: 10.5 us, 17 in the other form.  Blocks of a head read the same keys anew, which counts against it where
 // there are many (see tree_short_cluster).
 #include <cooperative_groups.h>
 

@@ -24,10 +24,11 @@
 // results, twice the products' time); warps 16 and 17 the chains' products, 18 the keys' loads, 19 the values' and queries'.  They meet at mbarriers
 // with bounded waits.
 //
-// Bound by the chains' hand-overs: 64 keys of 256 query rows take 2440 cycles, the products 1536 of them (the rests are a
-// third), tensor pipe 63 % busy, instruction issue 61 %.  131,071 tokens x 8 heads, 512 query rows a head: 301 us, 0.91 PFLOP/s
-// without the rests, 1.37 with them.  32 rows of 200 to 16,384 tokens, 8 heads, 32 to 128 query rows each: 159 us, 3.2 TB/s of
-// keys and values (a tile of 32 rows costs what one of 128 does).
+// With 256 query rows bound by the softmax and its hand-overs: 64 keys take 2260 cycles, 1900 of them the softmax warps' work,
+// the products 1536 (the rests are a third); tensor pipe 63 % busy, instruction issue 61 %.  131,071 tokens x 8 heads, 512
+// query rows a head: 298 us, 0.92 PFLOP/s without the rests, 1.38 with them.  With 128 rows or fewer a tile takes 1500 cycles,
+// 5.9 TB/s of keys and values, and a unit's start and end 20 thousand beside them: 32 rows of 200 to 16,384 tokens, 8
+// heads, 32 to 128 query rows each: 128 us, 4.0 TB/s.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -35,7 +35,8 @@ __global__ void __launch_bounds__(kThreads) kda_paged_tree_short_kernel(const Tr
     using R = Ring<D>;
     extern __shared__ __align__(128) uint8_t ring_all[];
     __shared__ uint32_t sm_mask[kWarps][kStages];
-    __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows], sm_pm[kRows], sm_pl[kRows];
+    __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows], sm_f[kWarps][kRows];
+    __shared__ float2 got_ml[kRows];                       // maxima and sums of this CTA's rows, by each CTA
     __shared__ uint64_t anc[kTreeMax];
     __shared__ int up[kTreeMax], s_sick;
     __shared__ unsigned long long nf[D], weigh[kRows];    // drafted tokens whose value is not finite; that a row weighs
@@ -54,6 +55,8 @@ __global__ void __launch_bounds__(kThreads) kda_paged_tree_short_kernel(const Tr
     }
     const int rows = m * a.rep - r0 < kRows ? m * a.rep - r0 : kRows;
     if (rows <= 0) return;                                 // (the whole cluster)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this CTA runs (see the join)
+    const int2 parents = warp == 0 ? tree_parents(a, n, m) : make_int2(-1, -1);
 
     // this CTA's keys, in groups; positions past the table's width have no token
     const int groups_all = (end + kGroup - 1) / kGroup;
@@ -94,14 +97,9 @@ __global__ void __launch_bounds__(kThreads) kda_paged_tree_short_kernel(const Tr
         }
         cp_commit();
     };
-    {
-        int pg[kStages - 1];
+    int pg[kStages - 1];
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) pg[i] = fetch(i);
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue(i, pg[i]);
-    }
-    int page = fetch(kStages - 1);
+    for (int i = 0; i < kStages - 1; ++i) pg[i] = fetch(i);
 
     // the block's queries as A fragments (rows g and g + 8), their tokens' paths
     const int g = lane >> 2, t4 = lane & 3;
@@ -121,7 +119,10 @@ __global__ void __launch_bounds__(kThreads) kda_paged_tree_short_kernel(const Tr
             qa[kk][3] = g + 8 < rows ? __ldg(q1 + 8 * kk + 4) : 0u;
         }
     }
-    if (warp == 0) tree_masks(tree_parents(a, n, m), m, anc, up);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i, pg[i]);
+    int page = fetch(kStages - 1);
+    if (warp == 0) tree_masks(parents, m, anc, up);
     for (int x = tid; x < D; x += kThreads) nf[x] = 0;
     if (tid < kRows) weigh[tid] = 0;
     if (tid == 0) s_sick = 0;
@@ -265,66 +266,80 @@ __global__ void __launch_bounds__(kThreads) kda_paged_tree_short_kernel(const Tr
         *reinterpret_cast<float2 *>(os + (g + 8) * D + 8 * j + 2 * t4) = make_float2(o[j][2], o[j][3]);
     }
     __syncthreads();
-    // join the warps, then the cluster's CTAs
-    for (int c = tid; c < rows * D; c += kThreads) {
-        const int r = c / D;
-        float mx = sm_m[0][r];
+    // Join the warps, and hand each row's outputs, maximum and sum to the CTA that has the row: what is written to another
+    // SM is not waited for but at the barrier.  (Reading the others' parts behind the barrier, and a second barrier before
+    // leaving, took 5000 cycles in the place of 3000.)
+    const int share = kRows / ctas;                        // rows of a CTA
+    cg::cluster_group cluster = cg::this_cluster();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // all CTAs run
+    if (tid < rows) {
+        float mx = sm_m[0][tid], sum = 0.f;
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][r]);
+        for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][tid]);
         const float z = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f, acc = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(sm_m[w][r] - z);
-            sum = fmaf(sm_l[w][r], f, sum);
-            acc = fmaf(reinterpret_cast<const float *>(ring_all + w * R::BYTES)[c], f, acc);
+            const float f = ex2(sm_m[w][tid] - z);
+            sm_f[w][tid] = f;
+            sum = fmaf(sm_l[w][tid], f, sum);
         }
-        if (s_sick && (nf[c % D] & weigh[r])) acc = __int_as_float(0x7fc00000);
-        reinterpret_cast<float *>(ring_all)[c] = acc;   // (read by this thread alone)
-        if (c % D == 0) {
-            sm_pm[r] = mx;
-            sm_pl[r] = sum;
-        }
+        cluster.map_shared_rank(got_ml, tid / share)[rank * share + tid % share] = make_float2(mx, sum);
     }
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();
-    for (int c = 4 * (tid + kThreads * rank); c < rows * D; c += 4 * kThreads * ctas) {
-        const int r = c / D;
-        float pm[kMaxCluster], pl[kMaxCluster];   // (all parts asked for at once: each is a trip to another SM)
-        float4 po[kMaxCluster];
-#pragma unroll
-        for (int e = 0; e < kMaxCluster; ++e) {
-            pm[e] = -INFINITY;
-            if (e < ctas) {
-                pm[e] = cluster.map_shared_rank(sm_pm, e)[r];
-                pl[e] = cluster.map_shared_rank(sm_pl, e)[r];
-                po[e] = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(cluster.map_shared_rank(ring_all, e)) + c);
-            }
-        }
-        float mx = pm[0];
-#pragma unroll
-        for (int e = 1; e < kMaxCluster; ++e) mx = fmaxf(mx, pm[e]);
-        const float z = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f;
+    __syncthreads();
+    float *got = reinterpret_cast<float *>(ring_all + kWarps * R::BYTES);   // [CTA][share][D]
+#pragma unroll 2
+    for (int c = 4 * tid; c < rows * D; c += 4 * kThreads) {
+        const int r = c / D, ch = c % D;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = sm_f[w][r];
+            const float4 x = *reinterpret_cast<const float4 *>(ring_all + w * R::BYTES + 4 * c);
+            acc = make_float4(fmaf(x.x, f, acc.x), fmaf(x.y, f, acc.y), fmaf(x.z, f, acc.z), fmaf(x.w, f, acc.w));
+        }
+        if (s_sick) {
+            const unsigned long long weighs = weigh[r];
+            const float nan = __int_as_float(0x7fc00000);
+            if (nf[ch] & weighs) acc.x = nan;
+            if (nf[ch + 1] & weighs) acc.y = nan;
+            if (nf[ch + 2] & weighs) acc.z = nan;
+            if (nf[ch + 3] & weighs) acc.w = nan;
+        }
+        *reinterpret_cast<float4 *>(cluster.map_shared_rank(got, r / share) + (rank * share + r % share) * D + ch) = acc;
+    }
+    cluster.sync();
+    for (int x = tid; x < share * (D / 2); x += kThreads) {
+        const int mine_r = x / (D / 2), r = rank * share + mine_r, ch = 2 * (x % (D / 2));
+        if (r >= rows) break;
+        float2 ml[kMaxCluster], po[kMaxCluster];
+        float mx = -INFINITY;
 #pragma unroll
         for (int e = 0; e < kMaxCluster; ++e)
             if (e < ctas) {
-                const float f = ex2(pm[e] - z);
-                sum = fmaf(pl[e], f, sum);
-                acc = make_float4(fmaf(po[e].x, f, acc.x), fmaf(po[e].y, f, acc.y), fmaf(po[e].z, f, acc.z), fmaf(po[e].w, f, acc.w));
+                ml[e] = got_ml[e * share + mine_r];
+                po[e] = *reinterpret_cast<const float2 *>(got + (e * share + mine_r) * D + ch);
+                mx = fmaxf(mx, ml[e].x);
+            }
+        const float z = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f;
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < kMaxCluster; ++e)
+            if (e < ctas) {
+                const float f = ex2(ml[e].x - z);
+                sum = fmaf(ml[e].y, f, sum);
+                acc = make_float2(fmaf(po[e].x, f, acc.x), fmaf(po[e].y, f, acc.y));
             }
         const int64_t to = q_row(r);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        if (sum == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + to * D + c % D) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-        if (p.lse && c % D == 0) p.lse[to] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+        if (sum == 0.f) acc = make_float2(0.f, 0.f);
+        *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.out) + to * D + ch) = pack_bf16(acc.x * inv, acc.y * inv);
+        if (p.lse && ch == 0) p.lse[to] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
     }
-    cluster.sync();   // the others have read this CTA's part
 }
 
 template <int D> cudaError_t launch_short(const TreeAtt &a, int blocks, int ctas, cudaStream_t st) {
-    constexpr int smem = kWarps * Ring<D>::BYTES;
+    constexpr int smem = kWarps * Ring<D>::BYTES + kRows * D * 4;
     static_assert(kRows * D * 4 <= Ring<D>::BYTES, "a warp's outputs fit its ring");
     const cudaError_t e = cudaFuncSetAttribute(kda_paged_tree_short_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

@@ -80,6 +80,7 @@ struct PoolPlan {
     int ctas, blocks, all;     // CTAs; blocks of pages per CTA; all blocks where every CTA keeps the whole bitmap, else 0
     int rows;                  // rows per CTA
     int chunk, per_row;        // entries of a segment of a row; segments of a row
+    int lanes;                 // of a warp for a segment: fewer than 32 where a row has no more than four entries for each
     int first;                 // rows where their first continuing row is found in shared memory, else 0
     int vec;                   // four entries of a table lie on 16 bytes
     int smem;
@@ -307,6 +308,9 @@ __device__ __forceinline__ void store4(int32_t *row, int e, int end, bool vec, i
 }
 __device__ __forceinline__ bool wants(const NewRow &r, int flags, int e, int p) { return (e < r.need && p < 0) || ((flags & kCopy) && e == r.full); }
 
+// kNarrow: more rows than warps, of up to 64 entries, several to a warp (141 rows of one page: 10 us, 20 with a row a warp; 256
+// wide rows by the same code: 21.6 us, 20.5 by their own).
+template <bool kNarrow>
 __global__ void __launch_bounds__(kPoolThreads) kda_paged_fork_kernel(const ForkArgs a, const PoolPlan plan, const FastDiv by_page) {
     extern __shared__ __align__(16) uint8_t sm[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -342,6 +346,7 @@ __global__ void __launch_bounds__(kPoolThreads) kda_paged_fork_kernel(const Fork
         scan_pages(a, P, [&](int p, int r) { a.new_refs[p] = r; });
         P.cluster.sync();
     }
+    const int lanes = kNarrow ? plan.lanes : 32, at_once = 32 / lanes, sub = lane % lanes, part = lane / lanes;   // a segment's lanes; segments of a warp
     auto first_of = [&](int s) { return plan.first ? first[s] : __ldcg(a.copies + 2 * (int64_t)s); };
 
     for (int r0 = 0; r0 < rows; r0 += kBatch) {
@@ -358,20 +363,23 @@ __global__ void __launch_bounds__(kPoolThreads) kda_paged_fork_kernel(const Fork
             flags[r0 + tid] = (uint8_t)fl;
         }
         __syncthreads();
-        for (int sg = warp; sg < nr * plan.per_row; sg += kPoolWarps) {
-            const int i = sg / plan.per_row, e0 = (sg - i * plan.per_row) * plan.chunk;
+        for (int s0 = warp * at_once; s0 < nr * plan.per_row; s0 += kPoolWarps * at_once) {
+            const bool here = !kNarrow || s0 + part < nr * plan.per_row;
+            const int sg = here ? s0 + part : s0, i = sg / plan.per_row, e0 = (sg - i * plan.per_row) * plan.chunk;
             const NewRow r = info[i];
             const int fl = flags[r0 + i], e1 = e0 + plan.chunk < a.max_pages ? e0 + plan.chunk : a.max_pages;
             int sum = 0;
-            if (r.src >= 0 && e0 < r.need)
-                for (int e = e0 + 4 * lane; e < e1; e += 128) {
+            if (here && r.src >= 0 && e0 < r.need)
+                for (int e = e0 + 4 * sub; e < e1; e += 4 * lanes) {
                     const int4 x = load4(a.table + (int64_t)r.src * a.max_pages, e, e1, plan.vec);
                     const int p[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int y = 0; y < 4; ++y) sum += e + y < e1 && wants(r, fl, e + y, keeps(a, r, fl, e + y) ? valid(a, p[y]) : -1);
                 }
-            sum = __reduce_add_sync(0xffffffffu, sum);
-            if (lane == 0) count[r0 * plan.per_row + sg] = sum;
+            if constexpr (kNarrow)
+                for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            else sum = __reduce_add_sync(0xffffffffu, sum);
+            if (here && sub == 0) count[r0 * plan.per_row + sg] = sum;
         }
         __syncthreads();
     }
@@ -397,15 +405,17 @@ __global__ void __launch_bounds__(kPoolThreads) kda_paged_fork_kernel(const Fork
             if (missing > 0 || !(flags[r0 + tid] & kCopy)) a.copies[2 * (int64_t)n] = a.copies[2 * (int64_t)n + 1] = -1;
         }
         if (rows > kBatch) __syncthreads();
-        for (int sg = warp; sg < nr * plan.per_row; sg += kPoolWarps) {
-            const int i = sg / plan.per_row, e0 = (sg - i * plan.per_row) * plan.chunk, n = lo + r0 + i;
+        for (int s0 = warp * at_once; s0 < nr * plan.per_row; s0 += kPoolWarps * at_once) {
+            const bool here = !kNarrow || s0 + part < nr * plan.per_row;
+            const int sg = here ? s0 + part : s0, i = sg / plan.per_row, e0 = (sg - i * plan.per_row) * plan.chunk, n = lo + r0 + i;
             const NewRow r = info[i];
-            const int fl = flags[r0 + i], e1 = e0 + plan.chunk < a.max_pages ? e0 + plan.chunk : a.max_pages;
+            const int last = e0 + plan.chunk < a.max_pages ? e0 + plan.chunk : a.max_pages, e1 = here ? last : e0;   // (no entries: nothing)
+            const int fl = flags[r0 + i];
             const int32_t *old = a.table + (int64_t)n * a.max_pages;
             int32_t *to = a.new_table + (int64_t)n * a.max_pages;
             int k = (int)ahead + count[r0 * plan.per_row + sg];
-            for (int eb = e0; eb < e1; eb += 128) {
-                const int e = eb + 4 * lane;
+            for (int eb = e0; eb < last; eb += 4 * lanes) {   // (once where a warp has several segments)
+                const int e = eb + 4 * sub;
                 if (missing > 0) {
                     store4(to, e, e1, plan.vec, load4(old, e, e1, plan.vec));
                     continue;
@@ -435,10 +445,10 @@ __global__ void __launch_bounds__(kPoolThreads) kda_paged_fork_kernel(const Fork
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const int z = __shfl_up_sync(0xffffffffu, s, o);
-                        if (lane >= o) s += z;
+                        if (sub >= o) s += z;
                     }
                     int at = k + s - mine;
-                    k += __shfl_sync(0xffffffffu, s, 31);
+                    k += __shfl_sync(0xffffffffu, s, lane | (lanes - 1));
 #pragma unroll 1
                     for (; want; want &= want - 1) {
                         const int i2 = __ffs(want) - 1, was = i2 == 0 ? p[0] : i2 == 1 ? p[1] : i2 == 2 ? p[2] : p[3], now = P.nth_free(at++);
@@ -549,6 +559,8 @@ PoolPlan pool_plan(const ForkArgs &a, bool fork) {
         p.rows = (a.rows + p.ctas - 1) / p.ctas;
         while (p.chunk < a.max_pages && (int64_t)p.rows * ((a.max_pages + p.chunk - 1) / p.chunk) > 16384) p.chunk *= 2;
         p.per_row = (a.max_pages + p.chunk - 1) / p.chunk;
+        p.lanes = p.rows > kPoolWarps ? 1 : 32;   // (a warp has one row anyway)
+        while (p.lanes < 32 && 4 * p.lanes < a.max_pages) p.lanes *= 2;
         p.first = a.rows <= kLocalRows ? a.rows : 0;
         p.smem += kBatch * (int)sizeof(NewRow) + 4 * p.rows * p.per_row + 4 * p.first + p.rows;
         p.vec = a.max_pages % 4 == 0 && (reinterpret_cast<uintptr_t>(a.table) | reinterpret_cast<uintptr_t>(a.new_table)) % 16 == 0;
@@ -582,7 +594,8 @@ cudaError_t launch_tree_commit(const TreeCommitArgs &a, cudaStream_t st) {
 }
 
 cudaError_t launch_fork(const ForkArgs &a, cudaStream_t st) {
-    return launch_pool(kda_paged_fork_kernel, pool_plan(a, true), st, a, pool_plan(a, true), FastDiv((uint32_t)a.page_size));
+    const PoolPlan plan = pool_plan(a, true);
+    return launch_pool(plan.lanes < 32 ? kda_paged_fork_kernel<true> : kda_paged_fork_kernel<false>, plan, st, a, plan, FastDiv((uint32_t)a.page_size));
 }
 
 cudaError_t launch_compact(const ForkArgs &a, cudaStream_t st) {

@@ -697,7 +697,7 @@ kda_status_t kda_paged_tree_commit(void *k_cache, void *v_cache, const int32_t *
  *   block_table, new_table : int32 [rows, max_pages];  seq_lens, new_lens, sources : int32 [rows]
  *   new_tokens : int32 [rows], or NULL (0; negative values count as 0)
  *   page_refs, new_refs : int32 [pages];  copies : int32 [rows, 2];  short_of : int32 [1]
- * Outputs may not overlap inputs (KDA_ERR_SHAPE where an output is one of the inputs).  dims: rows in
+ * Outputs may not overlap inputs or one another (else KDA_ERR_SHAPE).  dims: rows in
  * [1, 65536], pages at most 2^22, rows * max_pages at most 2^31 - 1 (else KDA_ERR_SHAPE), page_size; the rest is
  * not read. */
 kda_status_t kda_paged_fork(const int32_t *block_table, const int32_t *seq_lens, const int32_t *page_refs,

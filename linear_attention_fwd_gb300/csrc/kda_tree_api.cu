@@ -12,6 +12,25 @@ bool dtype_ok(kda_dtype_t t) { return t == KDA_F32 || t == KDA_BF16; }
 bool tokens_ok(int t) { return t >= 1 && t <= kda::kTreeMax; }
 bool eps_ok(float e) { return e >= 0.f && e <= 1e30f; }   // also rejects NaN
 
+// Whether any of the arrays of 32-bit numbers `out` overlaps another of them or one of `in` (NULL: none).
+struct Ints {
+    const void *p;
+    int64_t n;
+};
+template <size_t O, size_t I> bool overlap(const Ints (&out)[O], const Ints (&in)[I]) {
+    auto meet = [](const Ints &a, const Ints &b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return a.p && b.p && x < y + 4 * (uintptr_t)b.n && y < x + 4 * (uintptr_t)a.n;
+    };
+    for (size_t i = 0; i < O; ++i) {
+        for (size_t j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return true;
+        for (const Ints &x : in)
+            if (meet(out[i], x)) return true;
+    }
+    return false;
+}
+
 kda_status_t check_state_dims(const kda_dims_t *d, const int32_t *state_indices) {
     if (d == nullptr) return KDA_ERR_NULL;
     if (!dtype_ok(d->dtype) || !head_size_ok(d->dk) || !head_size_ok(d->dv)) return KDA_ERR_UNSUPPORTED;
@@ -180,19 +199,18 @@ extern "C" kda_status_t kda_paged_fork(const int32_t *block_table, const int32_t
     const kda_status_t st = check_pool_dims(d);
     if (st != KDA_OK) return st;
     if (d->rows == 0) return KDA_ERR_SHAPE;
-    const void *in[] = {block_table, seq_lens, page_refs, sources};
-    const void *out[] = {new_table, new_lens, new_refs, copies, short_of};
-    for (const void *p : in)
-        if (!p) return KDA_ERR_NULL;
-    for (const void *p : out)
-        if (!p) return KDA_ERR_NULL;
-    for (const void *o : out) {
-        if (!aligned(o, 4)) return KDA_ERR_ALIGN;
-        for (const void *p : in) {
-            if (!aligned(p, 4) || !aligned(new_tokens, 4)) return KDA_ERR_ALIGN;
-            if (o == p || o == new_tokens) return KDA_ERR_SHAPE;
-        }
-    }
+    const int64_t rows = d->rows, entries = rows * d->max_pages;
+    const Ints in[] = {{block_table, entries}, {seq_lens, rows}, {page_refs, d->pages}, {sources, rows}, {new_tokens, rows}};
+    const Ints out[] = {{new_table, entries}, {new_lens, rows}, {new_refs, d->pages}, {copies, 2 * rows}, {short_of, 1}};
+    for (const Ints &x : in)
+        if (!x.p && &x != &in[4]) return KDA_ERR_NULL;   // (new_tokens may be)
+    for (const Ints &x : out)
+        if (!x.p) return KDA_ERR_NULL;
+    for (const Ints &x : in)
+        if (!aligned(x.p, 4)) return KDA_ERR_ALIGN;
+    for (const Ints &x : out)
+        if (!aligned(x.p, 4)) return KDA_ERR_ALIGN;
+    if (overlap(out, in)) return KDA_ERR_SHAPE;
     const kda::ForkArgs a{block_table, seq_lens, page_refs, sources, new_tokens, new_table, new_lens, new_refs, copies, short_of,
                           d->rows, d->pages, d->page_size, d->max_pages};
     return kda::launch_fork(a, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
@@ -206,8 +224,10 @@ extern "C" kda_status_t kda_paged_compact(const int32_t *block_table, const int3
     const void *ints[] = {block_table, page_refs, new_table, new_refs, copies};
     for (const void *p : ints)
         if (!aligned(p, 4)) return KDA_ERR_ALIGN;
-    for (const void *o : {(const void *)new_table, (const void *)new_refs, (const void *)copies})
-        if (o && (o == block_table || o == page_refs)) return KDA_ERR_SHAPE;
+    const int64_t entries = (int64_t)d->rows * d->max_pages;
+    const Ints in[] = {{block_table, entries}, {page_refs, d->pages}};
+    const Ints out[] = {{new_table, entries}, {new_refs, d->pages}, {copies, d->pages / 2 * 2}};
+    if (overlap(out, in)) return KDA_ERR_SHAPE;
     const kda::ForkArgs a{block_table, nullptr, page_refs, nullptr, nullptr, new_table, nullptr, new_refs, copies, nullptr,
                           d->rows, d->pages, d->page_size, d->max_pages};
     return kda::launch_compact(a, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

@@ -174,6 +174,23 @@ def test_pool_refusals(K):
             assert compact(K, paged(K), **{x: PLACES[y]}) == K.KDA_ERR_SHAPE
 
 
+def test_outputs_that_overlap(K):
+    """In part, too: an array that starts within another's last number, or ends within its first."""
+    size = dict(table=12, lens=3, refs=10, sources=3, new=3, new_table=12, new_lens=3, new_refs=10, copies=6, short=1)
+    outs = ("new_table", "new_lens", "new_refs", "copies", "short")
+    for x in outs:
+        for y in size:
+            if x != y:
+                assert fork(K, paged(K), **{x: PLACES[y] + 4 * (size[y] - 1)}) == K.KDA_ERR_SHAPE, (x, y)
+                assert fork(K, paged(K), **{x: PLACES[y] - 4 * (size[x] - 1)}) == K.KDA_ERR_SHAPE, (x, y)
+    size["copies"] = 10
+    for x in ("new_table", "new_refs", "copies"):
+        for y in ("table", "refs", "new_table", "new_refs", "copies"):
+            if x != y:
+                assert compact(K, paged(K), **{x: PLACES[y] + 4 * (size[y] - 1)}) == K.KDA_ERR_SHAPE, (x, y)
+                assert compact(K, paged(K), **{x: PLACES[y] - 4 * (size[x] - 1)}) == K.KDA_ERR_SHAPE, (x, y)
+
+
 def test_copy_refusals(K):
     assert copy(K, None) == K.KDA_ERR_NULL
     for kw in (dict(head_dim=96), dict(dtype=5)):

@@ -7,7 +7,7 @@
 // page numbers fetched a group ahead), with the 16 query rows as the rows of mma.sync's tile; the weights enter the
 // second product as a rounded bf16 and the rounded rest, as in kda_paged_attention.
 // Bound by latency: a launch, the chain length - page - keys - scores - join.  One row of 777 tokens, 8 drafted, 8 heads of 4
-// queries: 10.5 us, 17 in the other form.  Blocks of a head read the same keys anew, which counts against it where
+// queries: 9.0 us, 15.6 in the other form.  Blocks of a head read the same keys anew, which counts against it where
 // there are many (see tree_short_cluster).
 #include <cooperative_groups.h>
 
@@ -267,8 +267,8 @@ __global__ void __launch_bounds__(kThreads) kda_paged_tree_short_kernel(const Tr
     }
     __syncthreads();
     // Join the warps, and hand each row's outputs, maximum and sum to the CTA that has the row: what is written to another
-    // SM is not waited for but at the barrier.  (Reading the others' parts behind the barrier, and a second barrier before
-    // leaving, took 5000 cycles in the place of 3000.)
+    // SM is not waited for but at the barrier.  (With the others' parts read behind the barrier, and a second barrier before
+    // leaving, one row of 777 tokens took 10.5 us, now 9.0.)
     const int share = kRows / ctas;                        // rows of a CTA
     cg::cluster_group cluster = cg::this_cluster();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // all CTAs run
@@ -364,8 +364,8 @@ int row_blocks(const PagedTreeArgs &t) { return (t.tokens * (t.p.heads / t.p.kv_
 // CTAs of a cluster, as many as the SMs hold, up to 8.  0: the rows may be longer than a cluster takes in about the time that the
 // two launches of the other form cost, or there are too many of them.
 int tree_short_cluster(const PagedTreeArgs &t, int d) {
-    constexpr int kShortTokens = 512;   // of a CTA (one row, 8 drafted tokens, 8 key/value heads: 4000 tokens 19.5 us, 22.1 in the
-                                        // other form; 8000: 29.4 and 25.0; 4 rows of 2000: 22.3 and 22.8; 8 of 1500: 29.7 and 29.2)
+    constexpr int kShortTokens = 512;   // of a CTA (one row, 8 drafted tokens, 8 key/value heads: 4000 tokens 16.7 us, 18.7 in the
+                                        // other form; 6000: 21.5 and 20.2; 8000: 26.5 and 20.7; 4 rows of 2000: 18.3 and 18.9; 8 of 900: 18.5 and 20.5)
     const int64_t units = (int64_t)t.p.rows * t.p.kv_heads * row_blocks(t);
     const int most = d == 64 ? 4 * kSms : 2 * kSms;   // what the SMs hold at once
     int c = kMaxCluster;

@@ -601,8 +601,8 @@ size_t kda_paged_attention_workspace_bytes(const kda_paged_dims_t *dims);
  * E_i k_i, E_i q_i rounded to 11 bits (2^-11 relative, an eighth of the output's own rounding); fp32 calls split them in
  * two such parts.  A NaN or infinity among a token's inputs reaches the outputs of the tokens that continue
  * it, and no other's.
- * dims: batch = N rows, seqlen = T in [1, KDA_TREE_TOKENS], num_seqs = pool slots.  Errors as in
- * kda_recurrent_step. */
+ * dims: batch = N rows, seqlen = T in [1, KDA_TREE_TOKENS], num_seqs = pool slots; N * H at most (2^31 - 1) / 4, else
+ * KDA_ERR_SHAPE.  Other errors as in kda_recurrent_step. */
 kda_status_t kda_recurrent_tree(const void *q, const void *k, const void *v, const void *g, const void *beta,
                                 const float *state, const int32_t *state_indices, const int32_t *parents,
                                 const int32_t *num_tokens, void *out, const kda_dims_t *dims, cudaStream_t stream);

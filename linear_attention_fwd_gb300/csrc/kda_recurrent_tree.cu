@@ -448,26 +448,29 @@ __global__ void __launch_bounds__(2 * DV, (kFew ? 384 : 256) / DV) kda_recurrent
 
 // Commit.  The path's tokens in order, each as in the decode step: vhat = (Diag(e^g) S)^T k, e = v - vhat,
 // S <- Diag(e^g) S + beta k e^T.  A warp keeps all key channels of 16 value channels in registers (a lane every eighth
-// key channel of four value channels), so that nothing between tokens is wider than a warp.  Bound by
-// reading and writing the state once: 256 rows of 1 to 16 accepted tokens, 64 heads, bf16: 368 us, 2.0 GB, 5.4 TB/s; with three CTAs an
-// SM it spills (461 us).
+// key channel of four value channels), so that nothing between tokens is wider than a warp; a CTA has two
+// warps, since value channels do not meet, and eight CTAs of an SM read, step and write at times of their own.  Bound by reading and
+// writing the state once: 256 rows of 1 to 16 accepted tokens, 64 heads, bf16: 332 us, 2.0 GB, 6.0 TB/s (64 channels a CTA: 337;
+// all 128: 368; those with three CTAs an SM spill: 461).
 constexpr int kStaged = 8;   // tokens whose vectors are staged at once
+constexpr int kCols = 32;    // value channels of a CTA
 
 template <typename Tin, int DK, int DV>
-__global__ void __launch_bounds__(2 * DV) kda_recurrent_tree_commit_kernel(const TreeArgs a) {
-    constexpr int kThreads = 2 * DV, R = DK / 8, kGroups = kThreads / 8;
+__global__ void __launch_bounds__(2 * kCols, 8) kda_recurrent_tree_commit_kernel(const TreeArgs a) {
+    constexpr int kSplit = DV / kCols, kThreads = 2 * kCols, R = DK / 8, kGroups = kThreads / 8;
     __shared__ __align__(16) float2 ska[kStaged][DK];   // key, decay
-    __shared__ __align__(16) float sv[kStaged][DV];
+    __shared__ __align__(16) float sv[kStaged][kCols];
     __shared__ float sb[kStaged];
     __shared__ int up[kTreeMax], path[kTreeMax], s_len;
-    const int n = blockIdx.x / a.heads, h = blockIdx.x - n * a.heads;
+    const int unit = blockIdx.x / kSplit, col0 = (blockIdx.x - unit * kSplit) * kCols;
+    const int n = unit / a.heads, h = unit - n * a.heads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = a.tokens;
     const int slot = a.idx ? __ldg(a.idx + n) : n;
     const int last = __ldg(a.accepted + n);
     if (slot < 0 || slot >= a.slots || last < 0 || last >= tree_count(a.num, T, n)) return;   // uniform across the block
 
     const int r = lane >> 2, c = 16 * warp + 4 * (lane & 3);
-    float *S = a.state + ((int64_t)slot * a.heads + h) * (DK * DV) + r * DV + c;
+    float *S = a.state + ((int64_t)slot * a.heads + h) * (DK * DV) + r * DV + col0 + c;
     float4 s[R];
 #pragma unroll
     for (int x = 0; x < R; ++x) s[x] = __ldcs(reinterpret_cast<const float4 *>(S + 8 * x * DV));
@@ -500,9 +503,9 @@ __global__ void __launch_bounds__(2 * DV) kda_recurrent_tree_commit_kernel(const
             }
             if (l == 0) sb[t] = to_f(static_cast<const Tin *>(a.beta)[row]);
         }
-        for (int x = tid; x < nt * DV; x += kThreads) {
-            const int64_t row = ((int64_t)n * T + path[p0 + x / DV]) * a.heads + h;
-            sv[x / DV][x % DV] = to_f(static_cast<const Tin *>(a.v)[row * DV + x % DV]);
+        for (int x = tid; x < nt * kCols; x += kThreads) {
+            const int64_t row = ((int64_t)n * T + path[p0 + x / kCols]) * a.heads + h;
+            sv[x / kCols][x % kCols] = to_f(static_cast<const Tin *>(a.v)[row * DV + col0 + x % kCols]);
         }
         __syncthreads();
 #pragma unroll 1
@@ -539,7 +542,7 @@ template <typename Tin, int DK, int DV>
 cudaError_t launch(const TreeArgs &a, bool commit, cudaStream_t st) {
     const unsigned grid = (unsigned)a.rows * (unsigned)a.heads;
     if (commit) {
-        kda_recurrent_tree_commit_kernel<Tin, DK, DV><<<grid, 2 * DV, 0, st>>>(a);
+        kda_recurrent_tree_commit_kernel<Tin, DK, DV><<<grid * (DV / kCols), 2 * kCols, 0, st>>>(a);
         return cudaGetLastError();
     }
     const bool few = sizeof(Tin) == 2 && a.tokens <= 16;

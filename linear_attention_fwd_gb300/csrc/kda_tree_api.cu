@@ -36,7 +36,7 @@ kda_status_t check_state_dims(const kda_dims_t *d, const int32_t *state_indices)
     if (!dtype_ok(d->dtype) || !head_size_ok(d->dk) || !head_size_ok(d->dv)) return KDA_ERR_UNSUPPORTED;
     if (d->batch <= 0 || d->heads <= 0 || d->num_seqs <= 0 || !tokens_ok(d->seqlen)) return KDA_ERR_SHAPE;
     if (state_indices == nullptr && d->num_seqs < d->batch) return KDA_ERR_SHAPE;
-    if ((int64_t)d->batch * d->heads > 0x7fffffffLL) return KDA_ERR_SHAPE;
+    if ((int64_t)d->batch * d->heads > 0x7fffffffLL / 4) return KDA_ERR_SHAPE;   // (up to four CTAs each)
     return KDA_OK;
 }
 

@@ -76,6 +76,7 @@ def copy(K, d, kc=FAKE, vc=FAKE, copies=FAKE, count=3):
 @pytest.mark.parametrize("kw,code", [
     (dict(dk=96), 3), (dict(dv=32), 3), (dict(dtype=2), 3), (dict(heads=0), 2), (dict(batch=0), 2), (dict(batch=-1), 2), (dict(seqlen=0), 2),
     (dict(seqlen=65), 2), (dict(num_seqs=0), 2), (dict(num_seqs=1), 2), (dict(batch=1 << 20, num_seqs=1 << 20, heads=1 << 12), 2),
+    (dict(batch=1 << 20, num_seqs=1 << 20, heads=1 << 9), 2),
 ])
 def test_state_dims(K, kw, code):
     for eps in (None, 1e-6):

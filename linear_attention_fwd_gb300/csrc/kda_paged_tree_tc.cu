@@ -26,7 +26,7 @@
 //
 // With 256 query rows bound by the softmax and its hand-overs: 64 keys take 2260 cycles, 1900 of them the softmax warps' work,
 // the products 1536 (the rests are a third); tensor pipe 63 % busy, instruction issue 61 %.  131,071 tokens x 8 heads, 512
-// query rows a head: 298 us, 0.92 PFLOP/s without the rests, 1.38 with them.  With 128 rows or fewer a tile takes 1500 cycles,
+// query rows a head: 298 to 308 us on different GPUs, 0.9 PFLOP/s without the rests, 1.36 with them.  With 128 rows or fewer a tile takes 1500 cycles,
 // 5.9 TB/s of keys and values, and a unit's start and end 20 thousand beside them: 32 rows of 200 to 16,384 tokens, 8
 // heads, 32 to 128 query rows each: 128 us, 4.0 TB/s.
 #include <cuda.h>

@@ -144,6 +144,27 @@ def test_nan_stays_on_its_branch(K, dt):
         assert bool(out[0, 1].isnan().all())
 
 
+@pytest.mark.parametrize("T", [8, 14, 29, 47, 64])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_what_is_not_finite_stays_on_its_branch(K, T, dt):
+    """NaN and infinities in a middle token of a tree of any number of tiles."""
+    c = make(23, 2, T, 2, 128, 128, dt)
+    rows, parents = R.drafts(23, 2, T)
+    at = T // 3
+    below = [{i for i in range(T) if at in R.path(p, i)} for p in rows]
+    clean = K.kda_recurrent_tree(**c, parents=parents)
+    for x, value in (("q", "nan"), ("k", "nan"), ("v", "nan"), ("v", "inf"), ("v", "-inf"), ("beta", "nan")):
+        d = {y: t.clone() for y, t in c.items()}
+        d[x][:, at] = float(value)
+        out = K.kda_recurrent_tree(**d, parents=parents)
+        for n in range(2):
+            for i in range(T):
+                if i not in (below[n] if x != "q" else {at}):
+                    assert torch.equal(out[n, i], clean[n, i]), (x, n, i)
+                else:
+                    assert not out[n, i].isfinite().any(), (x, n, i)
+
+
 def test_magnitudes(K):
     for scale in (2.0 ** -60, 2.0 ** 60):
         c = make(12, 1, 10, 2, 128, 128, BF16)

@@ -688,7 +688,9 @@ kda_status_t kda_paged_tree_commit(void *k_cache, void *v_cache, const int32_t *
  *   - A last page that is only partly filled is kept by the first row n that continues s where page_refs counts
  *     no other reference to it, and copied by the others: they get a free page, and copies[n] = (old page, new
  *     page); else copies[n] = (-1, -1).  kda_paged_copy then copies it in each layer's cache.
- *   - The pages that s holds past len stay with that first row.
+ *   - The pages that s holds past len, room to write to, stay with that first row where page_refs counts no other
+ *     reference to them.  (A row that was set back, its length lowered below pages that others name too, gives those
+ *     up: its entries lose them, and get free pages as below.  Such a row must not be appended to before a fork.)
  *   - Entries below ceil((len + new_tokens[n]) / page_size), at most max_pages, that name no page get a free one.
  * Free pages are those that page_refs counts no reference to on entry (pages that this call frees are
  * available to the next one), lowest first, to the rows in order and within a row to its entries in order.

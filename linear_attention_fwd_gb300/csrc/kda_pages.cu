@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kCommitThreads) kda_paged_tree_commit_kernel(c
 // their bitmaps of free pages with prefix sums over blocks and words through distributed shared memory, so that a
 // call is one launch without a workspace.  Bound by its chains of dependent reads (row, length, page, count) and by the
 // barriers: what a row needs is gathered by a thread each before warps go over its entries.  Fork of 8 rows of 44 pages and
-// the copies of their last pages: 9.0 us; of 256 rows of 100 to 8000 tokens on pages of 16: 20.5 us (16 and 45 where each warp
+// the copies of their last pages: 9.2 us; of 256 rows of 100 to 8000 tokens on pages of 16: 21.0 us (16 and 45 where each warp
 // fetched what its rows need by itself).
 constexpr int kPoolThreads = 1024, kPoolWarps = kPoolThreads / 32, kBlock = 1024;   // pages of a block: 32 words of the bitmap
 constexpr int kMaxCtas = 16, kLocalPages = 1 << 18, kLocalRows = 8192, kBatch = 1024;
@@ -283,9 +283,14 @@ __device__ __forceinline__ NewRow new_row(const ForkArgs &a, const FastDiv &by_p
     }
     return r;
 }
-// Whether entry e keeps the old row's, and what it then is (-1 for none).
-__device__ __forceinline__ bool keeps(const ForkArgs &a, const NewRow &r, int flags, int e) { return r.src >= 0 && ((flags & kHeir) || e < r.full + (row_part(a, r) ? 1 : 0)); }
 __device__ __forceinline__ int valid(const ForkArgs &a, int p) { return p < 0 || p >= a.pages ? -1 : p; }
+// The page that entry e keeps of the old row's, p (-1 for none).  Entries past the length are room to write to: the
+// first row that continues the old one keeps those pages that no other entry names.
+__device__ __forceinline__ int kept(const ForkArgs &a, const NewRow &r, int flags, int e, int p) {
+    p = valid(a, p);
+    if (r.src < 0 || p < 0 || e < r.full + (row_part(a, r) ? 1 : 0)) return r.src < 0 ? -1 : p;
+    return (flags & kHeir) && __ldg(a.refs + p) == 1 ? p : -1;
+}
 // Entries e .. e + 3 of a row of a table, -1 past its end.
 __device__ __forceinline__ int4 load4(const int32_t *row, int e, int end, bool vec) {
     if (vec && e + 4 <= end) return __ldg(reinterpret_cast<const int4 *>(row + e));
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(kPoolThreads) kda_paged_fork_kernel(const Fork
                     const int4 x = load4(a.table + (int64_t)r.src * a.max_pages, e, e1, plan.vec);
                     const int p[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) sum += e + y < e1 && wants(r, fl, e + y, keeps(a, r, fl, e + y) ? valid(a, p[y]) : -1);
+                    for (int y = 0; y < 4; ++y) sum += e + y < e1 && wants(r, fl, e + y, kept(a, r, fl, e + y, p[y]));
                 }
             if constexpr (kNarrow)
                 for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -429,7 +434,9 @@ __global__ void __launch_bounds__(kPoolThreads) kda_paged_fork_kernel(const Fork
                 int want = 0;                                                     // a bit for each entry
 #pragma unroll
                 for (int i2 = 0; i2 < 4; ++i2) {
-                    p[i2] = keeps(a, r, fl, e + i2) ? valid(a, p[i2]) : -1;
+                    const int was = p[i2];
+                    p[i2] = kept(a, r, fl, e + i2, was);
+                    if ((fl & kHeir) && e + i2 < e1 && p[i2] < 0 && valid(a, was) >= 0) atomicSub(a.new_refs + was, 1);   // given up
                     if (e + i2 < e1 && wants(r, fl, e + i2, p[i2])) want |= 1 << i2;
                 }
                 const bool shared = !(fl & kHeir);

@@ -734,7 +734,8 @@ def kda_paged_tree_commit(k_cache, v_cache, block_table, seq_lens, parents, acce
 def kda_paged_fork(block_table, seq_lens, page_refs, sources, new_tokens=None, *, page_size: int, new_table=None,
                    new_lens=None, new_refs=None, copies=None, short_of=None, stream=None):
     """Fork, reorder, end and extend rows: row n of the new table continues row sources[n] of the old one (-1: it
-    is empty), sharing its full pages; a partly filled last page that others hold too is copied.
+    is empty), sharing its full pages; a partly filled last page that others hold too is copied, and pages past the
+    length that others hold too are given up.
 
     block_table: int32 [N, max_pages], -1 where a row has no page; seq_lens, sources: int32 [N]; page_refs: int32
     [pages], how many entries name each page (0: free); new_tokens: int32 [N] or None, the tokens that each row

@@ -160,6 +160,8 @@ def fork(table, lens, refs, sources, new, ps):
             seen.add(s)
             held = W if heir else full + (part > 0)
             row[:held] = [p if ok(p) else -1 for p in table[s][:held]]
+            for e in range(full + (part > 0), held):     # room to write to: the row's own pages alone
+                row[e] = row[e] if row[e] >= 0 and refs[row[e]] == 1 else -1
             need = min(W, -(-(x + max(0, new[n] if new else 0)) // ps))
             for e in range(W):
                 shared = part > 0 and e == full and row[e] >= 0 and not (heir and refs[row[e]] == 1)

@@ -400,9 +400,10 @@ kda_status_t kda_device_status(cudaStream_t stream);
 
 /* kda_debug_checks -- which device-side input checks this build of the library runs before
  * each chunk forward and decode call: a bit mask, 1 = g in [-5, 0], for linear attention
- * g + head_g <= 0 (NaN fails), 2 = packed offsets 0 = cu[0] <= ... <= cu[N] = seqlen; 0 for the release build, which runs none (the
- * precondition is "はじめての自然言語処理 -- Kimi K3", section 3.1: g = -5 sigmoid(x)).  A failed
- * check launches nothing extra and traps nothing: the call still runs, its results are
+ * g + head_g <= 0, for a drafted tree g <= 0 of the tokens that the call uses (NaN fails),
+ * 2 = packed offsets 0 = cu[0] <= ... <= cu[N] = seqlen; 0 for the release build, which runs
+ * none (the precondition is "はじめての自然言語処理 -- Kimi K3", section 3.1: g = -5 sigmoid(x)).
+ * A failed check launches nothing extra and traps nothing: the call still runs, its results are
  * unspecified, and kda_device_status returns KDA_ERR_INPUT.  A host query. */
 int kda_debug_checks(void);
 

@@ -7,6 +7,7 @@
 //     on the strength of it);
 //     For the linear-attention calls: the sum of a token's and its head's log decay is at most 0, of any
 //     magnitude (-infinity included);
+//     For a drafted tree: the log decays of the tokens that the call uses are at most 0, of any magnitude;
 //   - packed offsets satisfy 0 = cu[0] <= cu[1] <= ... <= cu[N] = seqlen.
 // A library built with KDA_DEBUG_CHECKS (build.build(debug=True) -> libkda_debug.so) checks both
 // on the device before a call's kernels run and records a failure as a bit in a device-wide
@@ -15,7 +16,7 @@
 // release library compiles the error word and its reader but launches no check.
 #include <cuda_bf16.h>
 
-#include "kda_lin.h"
+#include "kda_tree.h"
 
 __device__ unsigned int g_kda_input_errors = 0;
 
@@ -46,6 +47,28 @@ __global__ void __launch_bounds__(kCheckThreads) check_lin_decay_kernel(const fl
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
         const float x = (g ? g[i] : 0.f) + (head_g ? head_g[i % heads] : 0.f);
         bad |= !(x <= 0.f);
+    }
+    if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(&g_kda_input_errors, kErrDecay);
+}
+
+// A drafted tree: flags any g above 0 (NaN included) of a token that the call uses: of a row with a slot in the pool, those
+// within its count, and where a path is brought into the state (accepted given) those on it.  A row to a block.
+__global__ void __launch_bounds__(kCheckThreads) check_tree_decay_kernel(const TreeArgs a, int64_t elems, int is_bf16) {
+    const int n = blockIdx.x, slot = a.idx ? a.idx[n] : n, m = tree_count(a.num, a.tokens, n);
+    if (slot < 0 || slot >= a.slots) return;
+    uint64_t used = m > 0 ? ~0ull >> (kTreeMax - m) : 0;
+    if (a.accepted) {
+        used = 0;
+        for (int i = a.accepted[n] < m ? a.accepted[n] : -1; i >= 0; i = tree_parent(a.parents, a.tokens, n, i)) used |= 1ull << i;
+    }
+    bool bad = false;
+    for (int i = 0; i < m; ++i) {
+        if (!((used >> i) & 1)) continue;
+        const int64_t first = ((int64_t)n * a.tokens + i) * elems;
+        for (int64_t x = first + threadIdx.x; x < first + elems; x += blockDim.x) {
+            const float g = is_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.g)[x]) : static_cast<const float *>(a.g)[x];
+            bad |= !(g <= 0.f);
+        }
     }
     if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(&g_kda_input_errors, kErrDecay);
 }
@@ -92,6 +115,16 @@ cudaError_t debug_check_lin_inputs(const float *g, const float *head_g, int64_t 
     return cudaGetLastError();
 #else
     (void)g, (void)head_g, (void)tokens, (void)heads, (void)cu, (void)num_seqs, (void)seqlen, (void)st;
+    return cudaSuccess;
+#endif
+}
+
+cudaError_t debug_check_tree_inputs(const TreeArgs &a, int dk, kda_dtype_t dt, cudaStream_t st) {
+#ifdef KDA_DEBUG_CHECKS
+    check_tree_decay_kernel<<<(unsigned)a.rows, kCheckThreads, 0, st>>>(a, (int64_t)a.heads * dk, dt == KDA_BF16);
+    return cudaGetLastError();
+#else
+    (void)a, (void)dk, (void)dt, (void)st;
     return cudaSuccess;
 #endif
 }

@@ -51,6 +51,8 @@ struct ForkArgs {
 
 cudaError_t launch_recurrent_tree(const TreeArgs &a, int dk, int dv, kda_dtype_t dt, cudaStream_t st);
 cudaError_t launch_recurrent_tree_commit(const TreeArgs &a, int dk, int dv, kda_dtype_t dt, cudaStream_t st);
+// Debug-build check of the log decays (see debug_check_inputs): at most 0, of the tokens that the call uses.
+cudaError_t debug_check_tree_inputs(const TreeArgs &a, int dk, kda_dtype_t dt, cudaStream_t st);
 size_t paged_tree_workspace_bytes(const PagedTreeArgs &a, int d, kda_dtype_t dt);
 // polls: bound on each device wait of the tensor-core kernel (bf16)
 cudaError_t launch_paged_tree(const PagedTreeArgs &a, int d, kda_dtype_t dt, void *workspace, uint32_t polls, cudaStream_t st);

@@ -86,12 +86,9 @@ kda_status_t tree_run(const void *q, const void *k, const void *v, const void *g
     const void *ints[] = {state_indices, parents, num_tokens, accepted};
     for (const void *p : ints)
         if (!aligned(p, 4)) return KDA_ERR_ALIGN;
-    // (what lies behind a row's count may be anything)
-    if (num_tokens == nullptr &&
-        kda::debug_check_inputs(g, (int64_t)d->batch * d->seqlen * d->heads * d->dk, d->dtype, nullptr, 0, 0, stream) != cudaSuccess)
-        return KDA_ERR_CUDA;
     const kda::TreeArgs a{q, k, v, g, beta, state, state_indices, parents, num_tokens, accepted, out,
                           d->batch, d->num_seqs, d->heads, d->seqlen, qk_eps};
+    if (kda::debug_check_tree_inputs(a, d->dk, d->dtype, stream) != cudaSuccess) return KDA_ERR_CUDA;
     const cudaError_t e = commit ? kda::launch_recurrent_tree_commit(a, d->dk, d->dv, d->dtype, stream)
                                  : kda::launch_recurrent_tree(a, d->dk, d->dv, d->dtype, stream);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

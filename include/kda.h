@@ -701,8 +701,8 @@ kda_status_t kda_paged_tree_commit(void *k_cache, void *v_cache, const int32_t *
  *   new_tokens : int32 [rows], or NULL (0; negative values count as 0)
  *   page_refs, new_refs : int32 [pages];  copies : int32 [rows, 2];  short_of : int32 [1]
  * Outputs may not overlap inputs or one another (else KDA_ERR_SHAPE).  dims: rows in
- * [1, 65536], pages at most 2^22, rows * max_pages at most 2^31 - 1 (else KDA_ERR_SHAPE), page_size; the rest is
- * not read. */
+ * [1, 65536], pages at most 2^22, max_pages at most 2^30, rows * max_pages at most 2^31 - 1 (else KDA_ERR_SHAPE),
+ * page_size; the rest is not read. */
 kda_status_t kda_paged_fork(const int32_t *block_table, const int32_t *seq_lens, const int32_t *page_refs,
                             const int32_t *sources, const int32_t *new_tokens, int32_t *new_table, int32_t *new_lens,
                             int32_t *new_refs, int32_t *copies, int32_t *short_of, const kda_paged_dims_t *dims,
@@ -715,7 +715,7 @@ kda_status_t kda_paged_fork(const int32_t *block_table, const int32_t *seq_lens,
  *   copies : int32 [pages / 2, 2], the moves (old page, new page) in order, then (-1, -1); kda_paged_copy carries
  *            them out in each layer's cache.
  * Every entry that the counts stand for has to be in this table.  Other arguments, limits and errors
- * as in kda_paged_fork (rows may be 0). */
+ * as in kda_paged_fork (rows may be 0, and max_pages more than 2^30). */
 kda_status_t kda_paged_compact(const int32_t *block_table, const int32_t *page_refs, int32_t *new_table,
                                int32_t *new_refs, int32_t *copies, const kda_paged_dims_t *dims, cudaStream_t stream);
 

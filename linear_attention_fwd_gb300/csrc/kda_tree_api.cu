@@ -195,7 +195,7 @@ extern "C" kda_status_t kda_paged_fork(const int32_t *block_table, const int32_t
                                        const kda_paged_dims_t *d, cudaStream_t stream) {
     const kda_status_t st = check_pool_dims(d);
     if (st != KDA_OK) return st;
-    if (d->rows == 0) return KDA_ERR_SHAPE;
+    if (d->rows == 0 || d->max_pages > (1 << 30)) return KDA_ERR_SHAPE;   // (entries of a row, and a segment past them, are 32-bit)
     const int64_t rows = d->rows, entries = rows * d->max_pages;
     const Ints in[] = {{block_table, entries}, {seq_lens, rows}, {page_refs, d->pages}, {sources, rows}, {new_tokens, rows}};
     const Ints out[] = {{new_table, entries}, {new_lens, rows}, {new_refs, d->pages}, {copies, 2 * rows}, {short_of, 1}};

@@ -672,8 +672,8 @@ size_t kda_paged_tree_attention_workspace_bytes(int32_t tokens, const kda_paged_
 /* kda_paged_tree_commit -- moves the keys and values of each row's accepted path to the end of the row's cached
  * tokens: the r-th token a_r of the path goes from position len + a_r to len + r, len = seq_lens[n] clamped to
  * [0, max_pages * page_size].  Then new_lens[n] = len + the path's length, at most max_pages * page_size (NULL:
- * not written; it may be seq_lens itself where the cache has one layer: others need the old lengths).  Tokens whose
- * old or new place is past the table or outside the pool are not moved.  No two positions of the rows' drafts may
+ * not written; it may be seq_lens itself where the cache has one layer: others need the old lengths; any other
+ * overlap with an input gives KDA_ERR_SHAPE).  Tokens whose old or new place is past the table or outside the pool are not moved.  No two positions of the rows' drafts may
  * lie in the same place.  Errors as in kda_paged_append; tokens in [1, KDA_TREE_TOKENS]. */
 kda_status_t kda_paged_tree_commit(void *k_cache, void *v_cache, const int32_t *block_table, const int32_t *seq_lens,
                                    const int32_t *parents, const int32_t *num_tokens, const int32_t *accepted,

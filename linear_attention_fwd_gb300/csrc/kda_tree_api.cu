@@ -182,6 +182,11 @@ extern "C" kda_status_t kda_paged_tree_commit(void *k_cache, void *v_cache, cons
     const void *ints[] = {block_table, seq_lens, parents, num_tokens, accepted, new_lens};
     for (const void *p : ints)
         if (!aligned(p, 4)) return KDA_ERR_ALIGN;
+    const int64_t rows = d->rows;
+    const Ints in[] = {{block_table, rows * d->max_pages}, {seq_lens == new_lens ? nullptr : seq_lens, rows}, {parents, rows * tokens},
+                       {num_tokens, rows}, {accepted, rows}};
+    const Ints out[] = {{new_lens, rows}};
+    if (overlap(out, in)) return KDA_ERR_SHAPE;   // (a row's CTA would read what another has written)
     const int64_t vecs = (int64_t)d->kv_heads * d->head_dim * (d->dtype == KDA_F32 ? 4 : 2) / 16;
     if (vecs > 0x7fffffffLL / 64) return KDA_ERR_SHAPE;
     const kda::TreeCommitArgs a{k_cache, v_cache, block_table, seq_lens, parents, num_tokens, accepted, new_lens,

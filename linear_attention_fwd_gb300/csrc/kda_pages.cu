@@ -534,12 +534,20 @@ __global__ void __launch_bounds__(kPoolThreads) kda_paged_compact_kernel(const F
 // vectors at a time.  Bound by DRAM: 6,570 pages of 32 KB of keys and as much of values: 140 us, 6.1 TB/s of reads and writes.
 constexpr int kCopyThreads = 256, kCopyAhead = 4, kCopyVecs = kCopyThreads * kCopyAhead;
 
+// (not by the read-only path: the kernel ahead may write the list while this one is there already.  From the L2 cache alone, 6,570
+// pages take 2 us more: a page's works read the same pair)
+__device__ __forceinline__ int load_fresh(const int32_t *p) {
+    int x;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+    return x;
+}
+
 __global__ void __launch_bounds__(kCopyThreads) kda_paged_copy_kernel(uint4 *kc, uint4 *vc, const int32_t *copies, const int64_t works,
                                                                       const int per_page, const int64_t page_vecs, const int pages) {
     asm volatile("griddepcontrol.wait;" ::: "memory");   // (launched before the kernel ahead of it has ended)
     for (int64_t w = blockIdx.x; w < works; w += gridDim.x) {
         const int64_t i = w / per_page;
-        const int from = __ldg(copies + 2 * i), to = __ldg(copies + 2 * i + 1);
+        const int from = load_fresh(copies + 2 * i), to = load_fresh(copies + 2 * i + 1);
         if (from < 0 || from >= pages || to < 0 || to >= pages) continue;
         const int64_t v0 = (w - i * per_page) * kCopyVecs + threadIdx.x;
         uint4 v[kCopyAhead];

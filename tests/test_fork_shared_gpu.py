@@ -130,3 +130,46 @@ def test_no_row_may_write_where_another_reads(K, N, W, ps):
                     assert copies[n] == ([-1, -1] if own else [was, now])
             if full == held:
                 assert copies[n] == [-1, -1]
+
+
+def test_copies_follow_their_list(K):
+    """A list that a fork writes anew right behind a copy that has read the old one, many times in one graph: every copy goes by
+    the list as its own fork leaves it."""
+    N, W, ps, Hkv, d, rounds = 24, 3, 4, 2, 64, 60
+    pages = 3 * N
+    rng = random.Random(3)
+    table = [[n, -1, -1] for n in range(N)]
+    lens = [rng.randint(1, ps - 1) for _ in range(N)]
+    tables, lengths, refs = i32(table), i32(lens), i32(counts(table, pages))
+    src = [[rng.randrange(N) for _ in range(N)] for _ in range(rounds)]
+    srcs = [i32(x) for x in src]
+    copies = torch.full((N, 2), -1, dtype=torch.int32, device="cuda")
+    outs = [[torch.empty_like(x) for x in (tables, lengths, refs)] for _ in range(rounds)]
+    short = torch.zeros(1, dtype=torch.int32, device="cuda")
+    caches = [torch.randn(pages, ps, Hkv, d, device="cuda") for _ in range(2)]
+    first = [x.clone() for x in caches]
+
+    def run():
+        t, x, r = tables, lengths, refs
+        for i in range(rounds):
+            new = outs[i]
+            K.kda_paged_fork(t, x, r, srcs[i], page_size=ps, new_table=new[0], new_lens=new[1], new_refs=new[2], copies=copies, short_of=short)
+            K.kda_paged_copy(*caches, copies)
+            t, x, r = new
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    row = list(range(N))                                 # the row of the first table whose tokens each one has
+    for s in src:
+        row = [row[n] for n in s]
+    for _ in range(3):
+        for x, y in zip(caches, first):
+            x.copy_(y)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert short.tolist() == [0]
+        last = outs[-1][0].tolist()
+        for n in range(N):
+            for x, y in zip(caches, first):
+                assert torch.equal(x[last[n][0], : lens[row[n]]], y[row[n], : lens[row[n]]]), n

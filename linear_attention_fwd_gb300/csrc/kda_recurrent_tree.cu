@@ -18,7 +18,8 @@
 //  4. (E k; E q) S and C W on tensor cores (mma.sync, tf32), the second added to the first in place, each warp the 16
 //     value channels of which it reads the state straight into B fragments.  bf16 calls round E k, E q and S to 11 bits
 //     (2^-11 relative, an eighth of the outputs' own rounding); C W, and everything in fp32 calls, is three products
-//     of parts of 11 bits.  A W that is not finite is left out of the product and added along the paths.
+//     of parts of 11 bits (in fp32 calls summed outside the tensor cores, see mma_parts: error 1.2e-7 of the outputs' root mean
+//     square, 7e-7 to 9e-7 summed inside; the batch below in fp32 228 us, 215 so).  A W that is not finite is left out of the product and added along the paths.
 // 64 rows of 8 to 32 tokens, 64 heads of 128 x 128, bf16: 145 us, 361 MB, 2.5 TB/s.  Not DRAM but a CTA's chain of short phases bounds
 // it: two CTAs an SM (three do not fit the registers, see below) issue in 45 % of the cycles, and the L1 data path, which the
 // state's sectors and the walks' and tiles' shared-memory reads cross, is busy in 63 %.  Solving for u, channel by
@@ -140,14 +141,21 @@ struct Parts {
         l = tf32(x - __uint_as_float(h));
     }
 };
-__device__ __forceinline__ void mma_parts(float (&c)[2][4], const float (&f)[4], float2 b0, float2 b1) {
+// kApart (fp32 calls): by themselves, the products of the leading parts last, and added to c by ordinary additions.  The tensor
+// cores cut off what falls below their sums' last bit, always towards zero; over 16 steps in c that came to 2^-20 of it.
+template <bool kApart> __device__ __forceinline__ void mma_parts(float (&to)[2][4], const float (&f)[4], float2 b0, float2 b1) {
     const Parts a0(f[0]), a1(f[1]), a2(f[2]), a3(f[3]), x0(b0.x), x1(b1.x), y0(b0.y), y1(b1.y);
+    float apart[2][4] = {};
+    auto &c = kApart ? apart : to;
     mma_1688(c[0], a0.l, a1.l, a2.l, a3.l, x0.h, x1.h);
     mma_1688(c[1], a0.l, a1.l, a2.l, a3.l, y0.h, y1.h);
     mma_1688(c[0], a0.h, a1.h, a2.h, a3.h, x0.l, x1.l);
     mma_1688(c[1], a0.h, a1.h, a2.h, a3.h, y0.l, y1.l);
     mma_1688(c[0], a0.h, a1.h, a2.h, a3.h, x0.h, x1.h);
     mma_1688(c[1], a0.h, a1.h, a2.h, a3.h, y0.h, y1.h);
+    if constexpr (kApart)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[0][e] += apart[0][e], to[1][e] += apart[1][e];
 }
 
 // Four channels as two pairs for packed arithmetic: a walk's time is largely that of issuing its instructions.
@@ -380,7 +388,7 @@ __global__ void __launch_bounds__(2 * DV, (kFew ? 384 : 256) / DV) kda_recurrent
                     const float f[4] = {p ? x.z : x.x, p ? y.z : y.x, p ? x.w : x.y, p ? y.w : y.y};
                     const float2 b0 = b[2 * p], b1 = b[2 * p + 1];
                     if constexpr (kF32) {
-                        mma_parts(c[t], f, b0, b1);
+                        mma_parts<true>(c[t], f, b0, b1);
                     } else {
                         const uint32_t a0 = __float_as_uint(f[0]), a1 = __float_as_uint(f[1]), a2 = __float_as_uint(f[2]), a3 = __float_as_uint(f[3]);
                         mma_1688(c[t][0], a0, a1, a2, a3, __float_as_uint(b0.x), __float_as_uint(b1.x));
@@ -426,7 +434,7 @@ __global__ void __launch_bounds__(2 * DV, (kFew ? 384 : 256) / DV) kda_recurrent
                     x = make_float2(tame(x.x) ? x.x : 0.f, tame(x.y) ? x.y : 0.f);
                     y = make_float2(tame(y.x) ? y.x : 0.f, tame(y.y) ? y.y : 0.f);
                 }
-                mma_parts(c[t], f, x, y);
+                mma_parts<kF32>(c[t], f, x, y);
             }
             if (any_bad) {   // what is not finite reaches the tokens that continue it, and no others
                 auto add = [&](float x, float w, float &to) { to = tame(w) ? to : fmaf(x, w, to); };

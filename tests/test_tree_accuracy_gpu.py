@@ -8,6 +8,8 @@ add along a path of D tokens and do not compound.
    most 16 channels, in which at most three sums of products' leading parts are truncated (2^-24 each on average, all towards zero:
    3 * 2^-24), and rounded additions of those; parts of 11 bits leave 2^-23 of a product, signs at random.  Less than 2^-22 for each
    of D + 1 sums together.
+ - bf16: the output is off by at most 2^-8, the operands of the products with the state by 2^-11 each, signs at random: 2^-8 + 2^-10.
+ - A state: per token the decay (2^-23), one more sum of fp32 and four roundings: 2^-22 for each of D tokens.
 """
 import pytest
 import torch
@@ -54,3 +56,16 @@ def test_fp32(K, T, kind, dk, dv):
     c = make(T, 3, T, 4, dk, dv, F32, -5.0)
     rows, parents = R.drafts(T, 3, T, kind)
     assert outputs(K, c, rows, parents) <= (R.depth(rows) + 1) * 2.0 ** -22
+
+
+@pytest.mark.parametrize("T", [20, 40, 64])
+@pytest.mark.parametrize("dt,least", [(F32, -1e-4), (BF16, -1e-4), (F32, -1.0), (BF16, -1.0)])
+def test_lines_that_hardly_decay(K, T, dt, least):
+    c = make(T, 2, T, 3, 128, 128, dt, least)
+    rows, _ = R.drafts(T, 2, T, "chain")
+    assert outputs(K, c, rows, None) <= (2.0 ** -8 + 2.0 ** -10 if dt == BF16 else (T + 1) * 2.0 ** -22)
+    a = {x: c[x] for x in ("k", "v", "g", "beta")}
+    kept, _, _ = R.recurrent(q=None, **a, state=c["state"], rows=rows)
+    K.kda_recurrent_tree_commit(**a, state=c["state"], parents=None, accepted=torch.tensor([T - 1, T // 2], dtype=torch.int32, device="cuda"))
+    for n, last in enumerate((T - 1, T // 2)):
+        assert relative(c["state"][n], kept[n][last][0]) <= (last + 1) * 2.0 ** -22

@@ -39,7 +39,6 @@ __global__ void __launch_bounds__(kThreads, 2) kda_paged_tree_attention_kernel(c
 
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const PagedArgs &p = a.t.p;
-    if (gridDim.x == 1) tree_clear<float, D, kThreads>(a, 0, 1);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     long long W, G, x, x1, us;
     int n;
@@ -214,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, 2) kda_paged_tree_attention_kernel(c
 // Joins the parts of the units that fell into several shares, kJoinRows query rows a CTA.  Where there are few units, one
 // CTA per unit and rows; else one per boundary between two shares (blockIdx.x + 1 is the share behind it),
 // which takes the unit that the boundary cuts, unless an earlier one cuts it too.  Every CTA waits for the
-// first kernel to end, so that nothing behind this kernel in the stream starts before that.
+// first kernel to end, so that nothing behind this kernel in the stream starts before that.  While they wait they write the outputs
+// of the tokens past their row's count.
 constexpr int kJoinThreads = 256, kJoinRows = 8;
 
 template <typename T, int D, bool kByUnit>
@@ -308,10 +308,10 @@ template <int D> cudaError_t launch_simt(const TreeAtt &a, int ctas, cudaStream_
     if (e != cudaSuccess) return e;
     kda_paged_tree_attention_kernel<D><<<ctas, kThreads, smem, st>>>(a);
     e = cudaGetLastError();
-    return e != cudaSuccess || ctas == 1 ? e : launch_tree_join(a, D, KDA_F32, ctas, st);   // (one CTA: nothing is split)
+    return e != cudaSuccess ? e : launch_tree_join(a, D, KDA_F32, ctas, st);
 }
 
-// CTAs of the kernel: never more than there can be items.
+// CTAs of the kernel: never more than there can be tiles; two at least (a tile of cached tokens, one of drafted ones).
 int simt_ctas(const PagedTreeArgs &t) {
     const int rep = t.p.heads / t.p.kv_heads;
     const int64_t units = (int64_t)t.p.rows * t.p.kv_heads * ((t.tokens * rep + kRb - 1) / kRb);

@@ -190,8 +190,7 @@ __device__ __forceinline__ int64_t tree_place(const TreeAtt &a, int page, int po
     return (int64_t)page * a.t.p.page_size + (pos - (int)a.by_page((uint32_t)pos) * a.t.p.page_size);
 }
 
-// Outputs of the tokens past their row's count: zero and -infinity, by part `part` of `parts`.  (The join does it while it
-// waits; without a join, the kernel itself.)
+// Outputs of the tokens past their row's count: zero and -infinity, by part `part` of `parts`.
 template <typename T, int D, int THREADS> __device__ __forceinline__ void tree_clear(const TreeAtt &a, int part, int parts) {
     if (a.t.num == nullptr) return;
     const PagedArgs &p = a.t.p;

@@ -179,7 +179,6 @@ kda_paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_c
         prefetch_tmap(&tmk);
         prefetch_tmap(&tmv);
     }
-    if (gridDim.x == 1) tree_clear<__nv_bfloat16, D, kThreads>(a, 0, 1);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     long long W, G;
     Walk w;
@@ -801,7 +800,7 @@ bool make_map(CUtensorMap *m, const void *ptr, int64_t tokens, int heads, int d,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// CTAs: one per SM, never more than there can be items.
+// CTAs: one per SM, never more than there can be items (seven at least: a start, a tile of cached tokens and one of drafted ones).
 int tc_ctas(const PagedTreeArgs &t) {
     const int rep = t.p.heads / t.p.kv_heads;
     const int64_t units = (int64_t)t.p.rows * t.p.kv_heads * (((int64_t)t.tokens * rep + kRb - 1) / kRb);
@@ -826,7 +825,7 @@ template <int D> cudaError_t launch_tc(const TreeAtt &a, int ctas, uint32_t poll
     if (e != cudaSuccess) return e;
     kda_paged_tree_tc_kernel<D><<<ctas, kThreads, Tc<D>::BYTES, st>>>(mq, mk, mv, a, qbox, box, polls);
     e = cudaGetLastError();
-    return e != cudaSuccess || ctas == 1 ? e : launch_tree_join(a, D, KDA_BF16, ctas, st);   // (one CTA: nothing is split)
+    return e != cudaSuccess ? e : launch_tree_join(a, D, KDA_BF16, ctas, st);
 }
 
 }  // namespace

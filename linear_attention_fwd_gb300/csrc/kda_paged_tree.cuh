@@ -199,7 +199,8 @@ template <typename T, int D, int THREADS> __device__ __forceinline__ void tree_c
         const int64_t first = ((int64_t)x * a.t.tokens + m) * p.heads;
         const int rows = (a.t.tokens - m) * p.heads;
         uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + first * D);
-        for (int i = threadIdx.x; i < rows * (D * (int)sizeof(T) / 16); i += THREADS) out[i] = make_uint4(0, 0, 0, 0);
+        const int64_t vecs = (int64_t)rows * (D * (int)sizeof(T) / 16);   // (past 32 bits where a row has 2^21 heads)
+        for (int64_t i = threadIdx.x; i < vecs; i += THREADS) out[i] = make_uint4(0, 0, 0, 0);
         if (p.lse)
             for (int i = threadIdx.x; i < rows; i += THREADS) p.lse[first + i] = -INFINITY;
     }

@@ -600,8 +600,8 @@ size_t kda_paged_attention_workspace_bytes(const kda_paged_dims_t *dims);
  * Outputs of tokens past a row's count, and of rows whose slot is outside the pool, are set to zero.
  * g may be any log decay <= 0 (the bound g >= -5 is not needed here).  bf16: the products with S take S and
  * E_i k_i, E_i q_i rounded to 11 bits (2^-11 relative, an eighth of the output's own rounding), where kda_recurrent_steps
- * keeps them in fp32; fp32 calls split them in two such parts and add up in fp32 (errors as of sums in fp32).  A NaN or infinity among a token's inputs reaches the outputs of the tokens that continue
- * it, and no other's.
+ * keeps them in fp32; fp32 calls split them in two such parts and add up in fp32 (errors as of sums in fp32).
+ * A NaN or infinity among a token's inputs reaches the outputs of the tokens that continue it, and no other's.
  * dims: batch = N rows, seqlen = T in [1, KDA_TREE_TOKENS], num_seqs = pool slots; N * H at most (2^31 - 1) / 4, else
  * KDA_ERR_SHAPE.  Other errors as in kda_recurrent_step. */
 kda_status_t kda_recurrent_tree(const void *q, const void *k, const void *v, const void *g, const void *beta,

@@ -364,8 +364,11 @@ int row_blocks(const PagedTreeArgs &t) { return (t.tokens * (t.p.heads / t.p.kv_
 // CTAs of a cluster, as many as the SMs hold, up to 8.  0: the rows may be longer than a cluster takes in about the time that the
 // two launches of the other form cost, or there are too many of them.
 int tree_short_cluster(const PagedTreeArgs &t, int d) {
-    constexpr int kShortTokens = 512;   // of a CTA (one row, 8 drafted tokens, 8 key/value heads: 4000 tokens 16.7 us, 18.7 in the
-                                        // other form; 6000: 21.5 and 20.2; 8000: 26.5 and 20.7; 4 rows of 2000: 18.3 and 18.9; 8 of 900: 18.5 and 20.5)
+    // Of a CTA.  Over 17 shapes (1 to 32 rows, 1 to 64 drafted tokens, 1 to 8 key/value heads, 8 to 64 query heads) this form is faster in 17
+    // at 400 tokens a CTA, in 15 at 512 (at most 6 % slower), in 11 at 640 (at most 16 %), in 6 at 800.  One row, 8 drafted, 8
+    // key/value heads: 4088 tokens 17.3 us, 18.8 in the other form; 6392: 23.1 and 20.5; 64 drafted, 64 query heads: 448 tokens 20.8
+    // and 25.7; 32 rows of 1016 tokens, one key/value head: 19.2 and 19.1.
+    constexpr int kShortTokens = 512;
     const int64_t units = (int64_t)t.p.rows * t.p.kv_heads * row_blocks(t);
     const int most = d == 64 ? 4 * kSms : 2 * kSms;   // what the SMs hold at once
     int c = kMaxCluster;

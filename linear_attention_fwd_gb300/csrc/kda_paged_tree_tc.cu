@@ -25,8 +25,8 @@
 // with bounded waits.
 //
 // With 256 query rows bound by the softmax and its hand-overs: 64 keys take 2260 cycles, 1900 of them the softmax warps' work,
-// the products 1536 (the rests are a third); tensor pipe 63 % busy, instruction issue 61 %.  131,071 tokens x 8 heads, 512
-// query rows a head: 298 to 308 us on different GPUs, 0.9 PFLOP/s without the rests, 1.36 with them.  With 128 rows or fewer a tile takes 1500 cycles,
+// the products 1536 (the rests are a third); tensor pipe 61 % busy, instruction issue 60 %.  131,071 tokens x 8 heads, 512
+// query rows a head: 292 to 311 us on different GPUs, 0.9 PFLOP/s without the rests, 1.36 with them.  With 128 rows or fewer a tile takes 1500 cycles,
 // 5.9 TB/s of keys and values, and a unit's start and end 20 thousand beside them: 32 rows of 200 to 16,384 tokens, 8
 // heads, 32 to 128 query rows each: 128 us, 4.0 TB/s.
 #include <cuda.h>
@@ -44,6 +44,9 @@ namespace {
 
 using namespace ptx;
 
+// kStart: 5 is within 2.5 % of the best of 3, 5, 8 and 13 in each of twelve batches of short, mixed and long rows (3 up to 7 % slower:
+// the batch above 137 us; 8 up to 7 %: 64 rows of 300 to 3000 tokens 95 us for 89; 13 up to 25 %: 102 rows of up to 1285 tokens 81 for 65),
+// although a short row's unit takes as long as more tiles: units of a few tiles are then cut less often, and whole ones are unequal.
 constexpr int kThreads = 640, kRb = 256, kKt = 64, kStart = 5;
 static_assert(kRb == 1 << 8 && kKt == 1 << 6, "their logarithms");
 constexpr float kSlack = 8.f;   // growth of the maximum, in powers of two, that m does not follow

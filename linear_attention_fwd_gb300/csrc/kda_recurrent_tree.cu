@@ -19,12 +19,15 @@
 //     value channels of which it reads the state straight into B fragments.  bf16 calls round E k, E q and S to 11 bits
 //     (2^-11 relative, an eighth of the outputs' own rounding); C W, and everything in fp32 calls, is three products
 //     of parts of 11 bits (in fp32 calls summed outside the tensor cores, see mma_parts: error 1.2e-7 of the outputs' root mean
-//     square, 7e-7 to 9e-7 summed inside; the batch below in fp32 228 us, 215 so).  A W that is not finite is left out of the product and added along the paths.
+//     square, 7e-7 to 9e-7 summed inside; the batch below in fp32 228 us, 215 so).  A W that is not finite is left out of
+//     the product and added along the paths.
 // 64 rows of 8 to 32 tokens, 64 heads of 128 x 128, bf16: 145 us, 361 MB, 2.5 TB/s.  Not DRAM but a CTA's chain of short phases bounds
 // it: two CTAs an SM (three do not fit the registers, see below) issue in 45 % of the cycles, and the L1 data path, which the
 // state's sectors and the walks' and tiles' shared-memory reads cross, is busy in 63 %.  Solving for u, channel by
 // channel, and holding the state in registers from the start took 180 us.  tcgen05 would have to
 // round the state on its way (its tf32 truncates) through 64 KB more of shared memory.
+// These drafts' paths have 2.8 tokens (8 at most).  Deeper ones cost their walks' steps, one after another: 64 rows of 32 tokens, 64
+// heads: 171 us in 5 levels, 182 in 8, 289 as a line (547 step by step); 16 rows of 64: 149, 155 and 320 (280 step by step).
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
@@ -457,8 +460,10 @@ __global__ void __launch_bounds__(2 * DV, (kFew ? 384 : 256) / DV) kda_recurrent
 // S <- Diag(e^g) S + beta k e^T.  A warp keeps all key channels of 16 value channels in registers (a lane every eighth
 // key channel of four value channels), so that nothing between tokens is wider than a warp; a CTA has two
 // warps, since value channels do not meet, and eight CTAs of an SM read, step and write at times of their own.  Bound by reading and
-// writing the state once: 256 rows of 1 to 16 accepted tokens, 64 heads, bf16: 332 us, 2.0 GB, 6.0 TB/s (64 channels a CTA: 337;
-// all 128: 368; those with three CTAs an SM spill: 461).
+// writing the state once where paths are short: 256 rows of 1 to 16 drafted tokens, 0 to 5 of them accepted (1.8 on average), 64 heads,
+// bf16: 332 us, 2.0 GB, 6.0 TB/s (64 channels a CTA: 337; all 128: 368; those with three CTAs an SM spill: 461).  Beyond
+// that by the tokens' chains of product, sum over lanes and update, some 45 us a token: 305 us with 1 accepted in every
+// row, 456 with 4, 623 with 8, 977 with 16.
 constexpr int kStaged = 8;   // tokens whose vectors are staged at once
 constexpr int kCols = 32;    // value channels of a CTA
 
